@@ -311,6 +311,117 @@ ssmvjp_status delta_rule_bwd_stages(const ssmvjp_delta_desc* desc, int32_t stage
                                     float* dq, float* dk, float* dv, float* dg, float* dbeta, float* dS0,
                                     void* workspace, size_t workspace_bytes, void* stream);
 
+/* ------------------------------------------------------------------------ */
+/* delta_chunk_fwd: gated delta rule, one log gate per value head             */
+/* ------------------------------------------------------------------------ */
+
+/* The delta rule above with one gate per value head instead of one per key
+ * channel, over whole sequences:
+ *   S_dec = exp(g_t) S_{t-1};  r = v_t - k_t^T S_dec;  S_t = S_dec + (beta_t k_t) (x) r;
+ *   o_t = (scale q_t)^T S_t.
+ * Sequences: with packed = 0, `batch` sequences of `seqlen` tokens (token
+ * tensors [batch, seqlen, ...]).  With packed = 1, `batch` sequences behind one
+ * another in `seqlen` tokens (token tensors [seqlen, ...]): sequence i owns the
+ * tokens seq_offsets[i] .. seq_offsets[i+1] - 1, seq_offsets in device memory,
+ * ascending.  Borders outside [0, seqlen] are clamped, so that no value there
+ * can lead outside the tensors; an empty sequence's final state is its initial
+ * state; tokens that no sequence owns are neither read nor written. */
+typedef struct {
+  int64_t batch, seqlen, nqk_heads, nv_heads, dk, dv; /* sequences, T, H, HV, K, V */
+  float scale;
+  int32_t dtype;    /* SSMVJP_F32 or SSMVJP_BF16 for q, k, v, o (and their gradients) */
+  int32_t packed;   /* 0 or 1, see above */
+  int32_t reserved; /* must be 0 */
+} ssmvjp_delta_chunk_desc;
+
+/* Forward.
+ *   q, k [.., H, K]   v [.., HV, V] (dtype)   beta, g [.., HV] f32 (g the log gate)
+ *   S0 [batch, HV, K, V] f32 (NULL = zeros)   seq_offsets [batch + 1] int32 (packed; else NULL)
+ * Outputs: o like v;  S_final [batch, HV, K, V] f32 (NULL = not written).
+ * Value head hv reads qk head hv / (HV/H).  bf16 runs the chunked form on the
+ * matrix cores (states to about 1e-5 of their norm), float32 token by token.
+ * g may be -infinity (a reset); the chunked form takes every g below -88 as -88.
+ * Constraints: HV % H == 0 (SSMVJP_EINVAL otherwise); K % 16 == 0, K <= 128,
+ * V % 16 == 0, H*K and HV*V below 2^24 (SSMVJP_EUNSUPPORTED otherwise).  q, k,
+ * v, o, S0, S_final 16-byte aligned. */
+ssmvjp_status delta_chunk_fwd_workspace(const ssmvjp_delta_chunk_desc* desc, size_t* bytes);
+ssmvjp_status delta_chunk_fwd(const ssmvjp_delta_chunk_desc* desc,
+                              const void* q, const void* k, const void* v, const float* beta, const float* g,
+                              const float* S0, const int32_t* seq_offsets, void* o, float* S_final,
+                              void* workspace, size_t workspace_bytes, void* stream);
+
+/* ------------------------------------------------------------------------ */
+/* delta_step: one token per request on a pool of states                      */
+/* ------------------------------------------------------------------------ */
+
+enum { SSMVJP_GATE_PER_HEAD = 0, SSMVJP_GATE_PER_KEY = 1 }; /* g [batch, HV] or [batch, HV, K] */
+
+typedef struct {
+  int64_t batch, nslots, nqk_heads, nv_heads, dk, dv; /* requests, states in the pool, H, HV, K, V */
+  float scale;
+  int32_t dtype;    /* SSMVJP_F32 or SSMVJP_BF16 for q, k, v, o */
+  int32_t gate;     /* SSMVJP_GATE_PER_HEAD (as delta_chunk_fwd) or SSMVJP_GATE_PER_KEY (as delta_rule_bwd) */
+  int32_t reserved; /* must be 0 */
+} ssmvjp_delta_step_desc;
+
+/* One token of the delta rule for every request, the states updated in place.
+ *   q, k [batch, H, K]   v [batch, HV, V] (dtype)   beta [batch, HV] f32   g f32 (see gate)
+ *   state [nslots, HV, K, V] f32, read and written   slots [batch] int32 in device memory
+ *   (NULL: request i uses state i)
+ * Output: o [batch, HV, V].
+ * A request whose slot is outside [0, nslots) (padding of a captured batch) or
+ * was named by an earlier request of the call gets zeros in o and touches no
+ * state.  Constraints and alignment as for delta_chunk_fwd (state 16-byte
+ * aligned; g too with per-key gates). */
+ssmvjp_status delta_step_workspace(const ssmvjp_delta_step_desc* desc, size_t* bytes);
+ssmvjp_status delta_step(const ssmvjp_delta_step_desc* desc,
+                         const void* q, const void* k, const void* v, const float* beta, const float* g,
+                         float* state, const int32_t* slots, void* o,
+                         void* workspace, size_t workspace_bytes, void* stream);
+
+/* ------------------------------------------------------------------------ */
+/* layer_norm_fwd, layer_norm_bwd                                             */
+/* ------------------------------------------------------------------------ */
+
+/* Layer norm of the last axis of x [rows, groups, dim]; the row (t, j) uses
+ * weight[j] and bias[j] (groups = 1: one weight vector; groups = heads: the
+ * norm of every head of a scan's readout, each head with its own):
+ *   mean = sum x / dim;  rstd = 1 / sqrt(sum (x - mean)^2 / dim + eps)
+ *   h = (x - mean) rstd;  y = h weight + bias. */
+typedef struct {
+  int64_t rows, groups, dim;
+  float eps;
+  int32_t dtype; /* SSMVJP_F32 or SSMVJP_BF16 for x, y, dy, dx */
+} ssmvjp_norm_desc;
+
+/* Forward: y like x; mean, rstd [rows, groups] f32 (NULL = not written);
+ * weight, bias [groups, dim] f32 (NULL = ones, zeros).
+ * x8 [rows, groups, dim] int8 and x8_scale [rows, groups, ceil(dim / 64)] f32
+ * (both or neither): the 8-bit form of x that layer_norm_bwd can read in its
+ * place.  For every block of 64 values of a row (the last may be shorter)
+ *   x8_scale = max|x| * (1/127),  x8 = rint(x * (127 * (1/max|x|)))
+ * (each operation rounded to float32, ties to even),
+ * zeros where max|x| < 1e-36: the value kept is off by at most max|x| / 254.
+ * Any dim and any element alignment; 16-byte aligned tensors and a dim that is a
+ * multiple of 8 (bf16) or 4 (f32) are the fast ones. */
+ssmvjp_status layer_norm_fwd_workspace(const ssmvjp_norm_desc* desc, size_t* bytes);
+ssmvjp_status layer_norm_fwd(const ssmvjp_norm_desc* desc,
+                             const void* x, const float* weight, const float* bias, void* y, float* mean, float* rstd,
+                             int8_t* x8, float* x8_scale, void* workspace, size_t workspace_bytes, void* stream);
+
+/* Backward from the upstream gradient dy, the forward's mean and rstd and
+ * either x or (x NULL) x8 and x8_scale, whose values x8 * x8_scale then stand
+ * for x:
+ *   t = dy weight;  dx = rstd (t - sum(t)/dim - h sum(t h)/dim)
+ *   dweight = sum over rows of dy h,  dbias = sum over rows of dy  ([groups, dim] f32,
+ *   each NULL = not computed; zeros when rows = 0).  eps is not used. */
+ssmvjp_status layer_norm_bwd_workspace(const ssmvjp_norm_desc* desc, size_t* bytes);
+ssmvjp_status layer_norm_bwd(const ssmvjp_norm_desc* desc,
+                             const void* dy, const void* x, const int8_t* x8, const float* x8_scale,
+                             const float* mean, const float* rstd, const float* weight,
+                             void* dx, float* dweight, float* dbias,
+                             void* workspace, size_t workspace_bytes, void* stream);
+
 /* Human-readable name of a status code (static storage). */
 const char* ssmvjp_status_str(ssmvjp_status status);
 

@@ -18,12 +18,14 @@ OK, EINVAL, EUNSUPPORTED, EWORKSPACE, EHIP, ENONFINITE = 0, 1, 2, 3, 4, 5
 F32, BF16 = 0, 1
 DECAY_PER_HEAD, DECAY_PER_STATE = 0, 1
 FORM_MAMBA2, FORM_RAW = 0, 1
+GATE_PER_HEAD, GATE_PER_KEY = 0, 1
 DELTA_CKPT, DELTA_BWD, DELTA_REDUCE, DELTA_ALL = 1, 2, 4, 7
 
 _STATUS_FNS = ("ssm_scan_bwd_workspace", "ssm_scan_bwd", "ssm_scan_bwd_dA", "ssd_chunk_bwd_workspace",
                "ssd_chunk_bwd", "ssd_chunk_bwd_dA", "ssd_chunk_bwd_states", "ssd_chunk_bwd_grads", "ssd_chunk_bwd_noalloc",
                "ssd_chunk_fwd_workspace", "ssd_chunk_fwd", "delta_rule_bwd_workspace", "delta_rule_bwd",
-               "delta_rule_bwd_stages")
+               "delta_rule_bwd_stages", "delta_chunk_fwd_workspace", "delta_chunk_fwd", "delta_step_workspace",
+               "delta_step", "layer_norm_fwd_workspace", "layer_norm_fwd", "layer_norm_bwd_workspace", "layer_norm_bwd")
 EXPORTS = _STATUS_FNS + ("ssmvjp_status_str", "ssmvjp_version")
 
 
@@ -45,6 +47,25 @@ class DeltaDesc(ctypes.Structure):
     _fields_ = [("batch", ctypes.c_int64), ("seqlen", ctypes.c_int64), ("nqk_heads", ctypes.c_int64),
                 ("nv_heads", ctypes.c_int64), ("dk", ctypes.c_int64), ("dv", ctypes.c_int64),
                 ("scale", ctypes.c_float), ("reserved", ctypes.c_int32)]
+
+
+class DeltaChunkDesc(ctypes.Structure):
+    _fields_ = [("batch", ctypes.c_int64), ("seqlen", ctypes.c_int64), ("nqk_heads", ctypes.c_int64),
+                ("nv_heads", ctypes.c_int64), ("dk", ctypes.c_int64), ("dv", ctypes.c_int64),
+                ("scale", ctypes.c_float), ("dtype", ctypes.c_int32), ("packed", ctypes.c_int32),
+                ("reserved", ctypes.c_int32)]
+
+
+class DeltaStepDesc(ctypes.Structure):
+    _fields_ = [("batch", ctypes.c_int64), ("nslots", ctypes.c_int64), ("nqk_heads", ctypes.c_int64),
+                ("nv_heads", ctypes.c_int64), ("dk", ctypes.c_int64), ("dv", ctypes.c_int64),
+                ("scale", ctypes.c_float), ("dtype", ctypes.c_int32), ("gate", ctypes.c_int32),
+                ("reserved", ctypes.c_int32)]
+
+
+class NormDesc(ctypes.Structure):
+    _fields_ = [("rows", ctypes.c_int64), ("groups", ctypes.c_int64), ("dim", ctypes.c_int64),
+                ("eps", ctypes.c_float), ("dtype", ctypes.c_int32)]
 
 
 class SsmVjpError(RuntimeError):
@@ -78,6 +99,10 @@ def lib():
         L.delta_rule_bwd_workspace.argtypes = [ctypes.POINTER(DeltaDesc), ctypes.POINTER(sz)]
         L.delta_rule_bwd.argtypes = [ctypes.POINTER(DeltaDesc)] + [vp] * 15 + [sz, vp]
         L.delta_rule_bwd_stages.argtypes = [ctypes.POINTER(DeltaDesc), ctypes.c_int32] + [vp] * 15 + [sz, vp]
+        for name, desc, nptr in (("delta_chunk_fwd", DeltaChunkDesc, 9), ("delta_step", DeltaStepDesc, 8),
+                                 ("layer_norm_fwd", NormDesc, 8), ("layer_norm_bwd", NormDesc, 10)):
+            getattr(L, name + "_workspace").argtypes = [ctypes.POINTER(desc), ctypes.POINTER(sz)]
+            getattr(L, name).argtypes = [ctypes.POINTER(desc)] + [vp] * nptr + [vp, sz, vp]
         for name in _STATUS_FNS:
             getattr(L, name).restype = ctypes.c_int
         L.ssmvjp_status_str.argtypes = [ctypes.c_int]
@@ -526,3 +551,226 @@ class DeltaCall:
 
     def run(self):
         self.stage(DELTA_ALL)
+
+
+# --------------------------------------------------------------------------- #
+def _scope(dev, stream):
+    """Where a call's launches and allocations go: the given stream, or the current
+    stream of the tensors' device (which need not be the current device)."""
+    if dev.type != "cuda":
+        raise ValueError("inputs must be GPU tensors (there is no CPU path)")
+    if stream is not None:
+        if stream.device != dev:
+            raise ValueError(f"the stream is on {stream.device}, the tensors on {dev}")
+        return torch.cuda.stream(stream)
+    return torch.cuda.device(dev)
+
+
+def _required(**tensors):
+    for name, t in tensors.items():
+        if t is None:
+            raise ValueError(f"{name} is required")
+
+
+def _query(name, desc):
+    n = ctypes.c_size_t(0)
+    _check(name, getattr(lib(), name)(ctypes.byref(desc), ctypes.byref(n)))
+    return n.value
+
+
+def _enqueue(name, desc, args, dev, workspace):
+    """Workspace and launch of one of the entry points that end in (workspace, bytes, stream)."""
+    ws, wsb = _workspace(_query(name + "_workspace", desc), dev, workspace)
+    st = getattr(lib(), name)(ctypes.byref(desc), *map(_ptr, args), _ptr(ws), wsb,
+                              ctypes.c_void_p(torch.cuda.current_stream(dev).cuda_stream))
+    _check(name, st)
+
+
+def delta_chunk_desc(q, v, scale, seq_offsets=None):
+    n, T, H, K = q.shape
+    HV, V = v.shape[2], v.shape[3]
+    packed = seq_offsets is not None
+    return DeltaChunkDesc(seq_offsets.shape[0] - 1 if packed else n, T, H, HV, K, V, float(scale), _dtype_code(q),
+                          int(packed), 0)
+
+
+def _delta_chunk_inputs(q, k, v, beta, g, S0, scale, seq_offsets):
+    _required(q=q, k=k, v=v, beta=beta, g=g)
+    if q.dim() != 4 or v.dim() != 4:
+        raise ValueError("q must be [b,T,H,K] and v [b,T,HV,V]")
+    n, T, H, K = q.shape
+    HV, V = v.shape[2], v.shape[3]
+    dev, big, f32 = q.device, q.dtype, torch.float32
+    if seq_offsets is not None:
+        if n != 1:
+            raise ValueError("packed sequences (seq_offsets given) need token tensors [1,T,...]")
+        if seq_offsets.dim() != 1 or seq_offsets.shape[0] < 1:
+            raise ValueError("seq_offsets must be [sequences + 1]")
+        _need(seq_offsets, "seq_offsets", torch.int32, tuple(seq_offsets.shape), dev)
+    desc = delta_chunk_desc(q, v, scale, seq_offsets)
+    _need(q, "q", big, (n, T, H, K), dev)
+    _need(k, "k", big, (n, T, H, K), dev)
+    _need(v, "v", big, (n, T, HV, V), dev)
+    _need(beta, "beta", f32, (n, T, HV), dev)
+    _need(g, "g", f32, (n, T, HV), dev)
+    _need(S0, "S0", f32, (desc.batch, HV, K, V), dev)
+    return desc
+
+
+def delta_chunk_fwd(q, k, v, beta, g, S0=None, *, scale, seq_offsets=None, want_final=True, out=None, workspace=None,
+                    stream=None):
+    """Gated delta rule with one log gate per value head.  Returns dict o (like v) and
+    S_final [b,HV,K,V] float32 (None with want_final=False).
+
+    q, k [b,T,H,K] and v [b,T,HV,V] float32 or bfloat16 (all the same), beta, g [b,T,HV]
+    and S0 [b,HV,K,V] (None = zeros) float32.  With seq_offsets (int32 [n+1] on the GPU,
+    ascending) the token tensors are [1,T,...], sequence i owns the tokens
+    seq_offsets[i] .. seq_offsets[i+1]-1, and the states are [n,HV,K,V]; rows of o that no
+    sequence owns are left as they were.
+    """
+    desc = _delta_chunk_inputs(q, k, v, beta, g, S0, scale, seq_offsets)
+    dev = q.device
+    with _scope(dev, stream):
+        if out is None:
+            shape = (desc.batch, desc.nv_heads, desc.dk, desc.dv)
+            out = {"o": torch.empty_like(v),
+                   "S_final": torch.empty(shape, dtype=torch.float32, device=dev) if want_final else None}
+        if out.get("o") is None:
+            raise ValueError("out is missing 'o'")
+        S_final = out.get("S_final")
+        _need(out["o"], "out['o']", v.dtype, tuple(v.shape), dev)
+        _need(S_final, "out['S_final']", torch.float32, (desc.batch, desc.nv_heads, desc.dk, desc.dv), dev)
+        _on_gpu(dev, q, k, v, beta, g, S0, seq_offsets, out["o"], S_final)
+        _enqueue("delta_chunk_fwd", desc, (q, k, v, beta, g, S0, seq_offsets, out["o"], S_final), dev, workspace)
+    return out
+
+
+def delta_step(q, k, v, beta, g, state, *, scale, slots=None, out=None, workspace=None, stream=None):
+    """One token of the gated delta rule per request; updates ``state`` in place and returns o.
+
+    q, k [b,H,K] and v, o [b,HV,V] float32 or bfloat16 (all the same), beta [b,HV] float32,
+    g float32 [b,HV] (one log gate per head) or [b,HV,K] (per key channel), state
+    [n,HV,K,V] float32.  slots (int32 [b] on the GPU, None = request i uses state i): a
+    request whose slot is outside [0,n) or was named by an earlier request gets zeros and
+    touches no state.
+    """
+    _required(q=q, k=k, v=v, beta=beta, g=g, state=state)
+    if q.dim() != 3 or v.dim() != 3 or state.dim() != 4 or g.dim() not in (2, 3):
+        raise ValueError("q must be [b,H,K], v [b,HV,V], g [b,HV] or [b,HV,K] and state [n,HV,K,V]")
+    b, H, K = q.shape
+    HV, V = v.shape[1], v.shape[2]
+    dev, big, f32 = q.device, q.dtype, torch.float32
+    per_key = g.dim() == 3
+    _need(q, "q", big, (b, H, K), dev)
+    _need(k, "k", big, (b, H, K), dev)
+    _need(v, "v", big, (b, HV, V), dev)
+    _need(beta, "beta", f32, (b, HV), dev)
+    _need(g, "g", f32, (b, HV, K) if per_key else (b, HV), dev)
+    _need(state, "state", f32, (state.shape[0], HV, K, V), dev)
+    _need(slots, "slots", torch.int32, (b,), dev)
+    desc = DeltaStepDesc(b, state.shape[0], H, HV, K, V, float(scale), _dtype_code(q),
+                         GATE_PER_KEY if per_key else GATE_PER_HEAD, 0)
+    with _scope(dev, stream):
+        o = torch.empty_like(v) if out is None else out
+        _need(o, "out", big, (b, HV, V), dev)
+        _on_gpu(dev, q, k, v, beta, g, state, slots, o)
+        _enqueue("delta_step", desc, (q, k, v, beta, g, state, slots, o), dev, workspace)
+    return o
+
+
+# --------------------------------------------------------------------------- #
+def norm_desc(x, weight, eps):
+    """x [..., D] with weight None or [D], or x [..., G, D] with weight [G, D]."""
+    if x.dim() < 1:
+        raise ValueError("x must have at least one axis")
+    D = x.shape[-1]
+    G = 1
+    if weight is not None and weight.dim() == 2:
+        if x.dim() < 2:
+            raise ValueError("a weight [G,D] needs x [...,G,D]")
+        G = x.shape[-2]
+    elif weight is not None and weight.dim() != 1:
+        raise ValueError("weight must be [D] or [G,D]")
+    rows = 1
+    for n in x.shape[:-1]:
+        rows *= n
+    if D == 0 or G == 0:
+        raise ValueError("x has an empty last axis")
+    return NormDesc(rows // G, G, D, float(eps), _dtype_code(x))
+
+
+def _norm_wshape(desc, weight):
+    return (desc.groups, desc.dim) if weight.dim() == 2 else (desc.dim,)
+
+
+def layer_norm_fwd(x, weight=None, bias=None, *, eps=1e-5, want_ckpt8=False, out=None, workspace=None, stream=None):
+    """Layer norm of the last axis.  Returns dict y (like x), mean and rstd (float32, x's shape
+    without the last axis) and, with want_ckpt8=True, x8 (int8, like x) and x8_scale
+    [..., ceil(D/64)]: the 8-bit form of x that layer_norm_bwd can read in its place.
+
+    x [..., D] float32 or bfloat16; weight and bias float32 [D], or [G,D] for x [..., G, D]
+    (every head its own), or None.
+    """
+    _required(x=x)
+    if weight is None and bias is not None:
+        raise ValueError("a bias needs a weight")
+    desc = norm_desc(x, weight, eps)
+    dev, f32 = x.device, torch.float32
+    _need(x, "x", x.dtype, tuple(x.shape), dev)
+    if weight is not None:
+        _need(weight, "weight", f32, _norm_wshape(desc, weight), dev)
+        _need(bias, "bias", f32, _norm_wshape(desc, weight), dev)
+    stat, blocks = tuple(x.shape[:-1]), tuple(x.shape[:-1]) + ((desc.dim + 63) // 64,)
+    with _scope(dev, stream):
+        if out is None:
+            out = {"y": torch.empty_like(x), "mean": torch.empty(stat, dtype=f32, device=dev),
+                   "rstd": torch.empty(stat, dtype=f32, device=dev)}
+            if want_ckpt8:
+                out["x8"] = torch.empty(x.shape, dtype=torch.int8, device=dev)
+                out["x8_scale"] = torch.empty(blocks, dtype=f32, device=dev)
+        spec = {"y": (x.dtype, tuple(x.shape)), "mean": (f32, stat), "rstd": (f32, stat)}
+        if want_ckpt8:
+            spec.update(x8=(torch.int8, tuple(x.shape)), x8_scale=(f32, blocks))
+        _check_out(out, spec, dev)
+        x8, x8s = (out["x8"], out["x8_scale"]) if want_ckpt8 else (None, None)
+        _on_gpu(dev, x, weight, bias, out["y"], out["mean"], out["rstd"], x8, x8s)
+        _enqueue("layer_norm_fwd", desc, (x, weight, bias, out["y"], out["mean"], out["rstd"], x8, x8s), dev, workspace)
+    return out
+
+
+def layer_norm_bwd(dy, x, mean, rstd, weight=None, *, ckpt8=None, out=None, workspace=None, stream=None):
+    """Gradients of layer_norm_fwd.  Returns dict dx (like dy), dweight and dbias (float32, like
+    weight; None without a weight).
+
+    x is the forward's input, or None with ckpt8=(x8, x8_scale) from a forward with
+    want_ckpt8=True; mean and rstd are the forward's.
+    """
+    _required(dy=dy, mean=mean, rstd=rstd)
+    if (x is None) == (ckpt8 is None):
+        raise ValueError("exactly one of x and ckpt8 must be given")
+    desc = norm_desc(dy, weight, 0.0)
+    dev, f32 = dy.device, torch.float32
+    stat = tuple(dy.shape[:-1])
+    _need(dy, "dy", dy.dtype, tuple(dy.shape), dev)
+    _need(x, "x", dy.dtype, tuple(dy.shape), dev)
+    _need(mean, "mean", f32, stat, dev)
+    _need(rstd, "rstd", f32, stat, dev)
+    x8, x8s = (None, None) if ckpt8 is None else ckpt8
+    if ckpt8 is not None:
+        _required(x8=x8, x8_scale=x8s)
+        _need(x8, "x8", torch.int8, tuple(dy.shape), dev)
+        _need(x8s, "x8_scale", f32, stat + ((desc.dim + 63) // 64,), dev)
+    if weight is not None:
+        _need(weight, "weight", f32, _norm_wshape(desc, weight), dev)
+    with _scope(dev, stream):
+        if out is None:
+            out = {"dx": torch.empty_like(dy), "dweight": None if weight is None else torch.empty_like(weight),
+                   "dbias": None if weight is None else torch.empty_like(weight)}
+        spec = {"dx": (dy.dtype, tuple(dy.shape))}
+        if weight is not None:
+            spec.update(dweight=(f32, tuple(weight.shape)), dbias=(f32, tuple(weight.shape)))
+        _check_out(out, spec, dev)
+        dw, db = (out["dweight"], out["dbias"]) if weight is not None else (None, None)
+        _on_gpu(dev, dy, x, x8, x8s, mean, rstd, weight, out["dx"], dw, db)
+        _enqueue("layer_norm_bwd", desc, (dy, x, x8, x8s, mean, rstd, weight, out["dx"], dw, db), dev, workspace)
+    return out

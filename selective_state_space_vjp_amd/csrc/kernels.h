@@ -127,6 +127,50 @@ DeltaPlan delta_plan(const ssmvjp_delta_desc& d);
 hipError_t launch_delta_bwd(const ssmvjp_delta_desc& d, const DeltaPlan& plan, const DeltaPointers& ptr,
                             hipStream_t stream, int stages);
 
+// ------------------- gated delta rule, one gate per head -------------------
+struct DeltaChunkPointers {
+  const void *q, *k, *v;
+  const float *beta, *g, *S0;
+  const int32_t* seq_offsets;  // NULL unless packed
+  void* o;
+  float* S_final;  // NULL: not written
+  void* workspace;
+};
+size_t delta_fwd_workspace_bytes(const ssmvjp_delta_chunk_desc& d);
+hipError_t launch_delta_fwd(const ssmvjp_delta_chunk_desc& d, const DeltaChunkPointers& ptr, hipStream_t stream);
+// the same token by token (delta_step.hip); no workspace
+hipError_t launch_delta_walk(const ssmvjp_delta_chunk_desc& d, const DeltaChunkPointers& ptr, hipStream_t stream);
+
+struct DeltaStepPointers {
+  const void *q, *k, *v;
+  const float *beta, *g;
+  float* state;
+  const int32_t* slots;  // NULL: request i uses state i
+  void* o;
+};
+hipError_t launch_delta_step(const ssmvjp_delta_step_desc& d, const DeltaStepPointers& ptr, hipStream_t stream);
+
+// -------------------------------- layer norm --------------------------------
+struct NormFwdPointers {
+  const void* x;
+  const float *weight, *bias;
+  void* y;
+  float *mean, *rstd;
+  int8_t* x8;  // NULL: no 8-bit form
+  float* x8_scale;
+};
+struct NormBwdPointers {
+  const void *dy, *x;  // x NULL: x8, x8_scale hold the input
+  const int8_t* x8;
+  const float *x8_scale, *mean, *rstd, *weight;
+  void* dx;
+  float *dweight, *dbias;  // NULL: not wanted
+  void* workspace;
+};
+size_t norm_bwd_workspace_bytes(const ssmvjp_norm_desc& d);
+hipError_t launch_norm_fwd(const ssmvjp_norm_desc& d, const NormFwdPointers& ptr, hipStream_t stream);
+hipError_t launch_norm_bwd(const ssmvjp_norm_desc& d, const NormBwdPointers& ptr, hipStream_t stream);
+
 // ---------------------------- debug finiteness -----------------------------
 // flag = 0; then flag = 1 if any of the n elements at p (bf16 or float) is NaN
 // or infinite (finite.hip)
