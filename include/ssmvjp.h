@@ -350,6 +350,24 @@ ssmvjp_status delta_chunk_fwd(const ssmvjp_delta_chunk_desc* desc,
                               const float* S0, const int32_t* seq_offsets, void* o, float* S_final,
                               void* workspace, size_t workspace_bytes, void* stream);
 
+/* Backward: the gradients of J = <d_o, o> + <dS_final, S_final>.
+ *   q, k, v, beta, g, S0, seq_offsets as for delta_chunk_fwd;  d_o like o;
+ *   dS_final [batch, HV, K, V] f32 (NULL = zeros)
+ * Outputs: dq, dk like q (summed over the value heads of each qk head), dv like v,
+ *   dbeta, dg [.., HV] f32, dS0 [batch, HV, K, V] f32 (NULL = not written).
+ * dq, dk and dv are rounded to bf16, dbeta, dg and dS0 come out to about 1e-5
+ * of their norm.  The gradient of a g below -88 is that at -88.
+ * Constraints as for delta_chunk_fwd, and dtype SSMVJP_BF16 (SSMVJP_EUNSUPPORTED
+ * otherwise: delta_rule_bwd has the float32 gradients, with g repeated over the
+ * key channels and dg summed over them).  d_o, dq, dk, dv, dS_final and dS0 are
+ * 16-byte aligned too. */
+ssmvjp_status delta_chunk_bwd_workspace(const ssmvjp_delta_chunk_desc* desc, size_t* bytes);
+ssmvjp_status delta_chunk_bwd(const ssmvjp_delta_chunk_desc* desc,
+                              const void* q, const void* k, const void* v, const float* beta, const float* g,
+                              const float* S0, const void* d_o, const float* dS_final, const int32_t* seq_offsets,
+                              void* dq, void* dk, void* dv, float* dbeta, float* dg, float* dS0,
+                              void* workspace, size_t workspace_bytes, void* stream);
+
 /* ------------------------------------------------------------------------ */
 /* delta_step: one token per request on a pool of states                      */
 /* ------------------------------------------------------------------------ */

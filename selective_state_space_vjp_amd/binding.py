@@ -24,7 +24,8 @@ DELTA_CKPT, DELTA_BWD, DELTA_REDUCE, DELTA_ALL = 1, 2, 4, 7
 _STATUS_FNS = ("ssm_scan_bwd_workspace", "ssm_scan_bwd", "ssm_scan_bwd_dA", "ssd_chunk_bwd_workspace",
                "ssd_chunk_bwd", "ssd_chunk_bwd_dA", "ssd_chunk_bwd_states", "ssd_chunk_bwd_grads", "ssd_chunk_bwd_noalloc",
                "ssd_chunk_fwd_workspace", "ssd_chunk_fwd", "delta_rule_bwd_workspace", "delta_rule_bwd",
-               "delta_rule_bwd_stages", "delta_chunk_fwd_workspace", "delta_chunk_fwd", "delta_step_workspace",
+               "delta_rule_bwd_stages", "delta_chunk_fwd_workspace", "delta_chunk_fwd",
+               "delta_chunk_bwd_workspace", "delta_chunk_bwd", "delta_step_workspace",
                "delta_step", "layer_norm_fwd_workspace", "layer_norm_fwd", "layer_norm_bwd_workspace", "layer_norm_bwd")
 EXPORTS = _STATUS_FNS + ("ssmvjp_status_str", "ssmvjp_version")
 
@@ -99,7 +100,8 @@ def lib():
         L.delta_rule_bwd_workspace.argtypes = [ctypes.POINTER(DeltaDesc), ctypes.POINTER(sz)]
         L.delta_rule_bwd.argtypes = [ctypes.POINTER(DeltaDesc)] + [vp] * 15 + [sz, vp]
         L.delta_rule_bwd_stages.argtypes = [ctypes.POINTER(DeltaDesc), ctypes.c_int32] + [vp] * 15 + [sz, vp]
-        for name, desc, nptr in (("delta_chunk_fwd", DeltaChunkDesc, 9), ("delta_step", DeltaStepDesc, 8),
+        for name, desc, nptr in (("delta_chunk_fwd", DeltaChunkDesc, 9), ("delta_chunk_bwd", DeltaChunkDesc, 15),
+                                 ("delta_step", DeltaStepDesc, 8),
                                  ("layer_norm_fwd", NormDesc, 8), ("layer_norm_bwd", NormDesc, 10)):
             getattr(L, name + "_workspace").argtypes = [ctypes.POINTER(desc), ctypes.POINTER(sz)]
             getattr(L, name).argtypes = [ctypes.POINTER(desc)] + [vp] * nptr + [vp, sz, vp]
@@ -642,6 +644,36 @@ def delta_chunk_fwd(q, k, v, beta, g, S0=None, *, scale, seq_offsets=None, want_
         _need(S_final, "out['S_final']", torch.float32, (desc.batch, desc.nv_heads, desc.dk, desc.dv), dev)
         _on_gpu(dev, q, k, v, beta, g, S0, seq_offsets, out["o"], S_final)
         _enqueue("delta_chunk_fwd", desc, (q, k, v, beta, g, S0, seq_offsets, out["o"], S_final), dev, workspace)
+    return out
+
+
+def delta_chunk_bwd(q, k, v, beta, g, S0, d_o, dS_final=None, *, scale, seq_offsets=None, want_dS0=True, out=None,
+                    workspace=None, stream=None):
+    """Gradients of delta_chunk_fwd (bfloat16 q, k, v, d_o).  Returns dict dq, dk (like q), dv (like v),
+    dbeta, dg (float32) and dS0 [b,HV,K,V] float32 (None with want_dS0=False).
+
+    Arguments as for delta_chunk_fwd; d_o like v, dS_final [b,HV,K,V] float32 (None = zeros).
+    Rows that no sequence of a packed call owns are left as they were.
+    """
+    desc = _delta_chunk_inputs(q, k, v, beta, g, S0, scale, seq_offsets)
+    _required(d_o=d_o)
+    dev, big, f32 = q.device, q.dtype, torch.float32
+    state = (desc.batch, desc.nv_heads, desc.dk, desc.dv)
+    _need(d_o, "d_o", big, tuple(v.shape), dev)
+    _need(dS_final, "dS_final", f32, state, dev)
+    with _scope(dev, stream):
+        if out is None:
+            out = dict(dq=torch.empty_like(q), dk=torch.empty_like(k), dv=torch.empty_like(v),
+                       dbeta=torch.empty_like(beta), dg=torch.empty_like(g),
+                       dS0=torch.empty(state, dtype=f32, device=dev) if want_dS0 else None)
+        _check_out(out, dict(dq=(big, tuple(q.shape)), dk=(big, tuple(q.shape)), dv=(big, tuple(v.shape)),
+                             dbeta=(f32, tuple(beta.shape)), dg=(f32, tuple(g.shape))), dev)
+        dS0 = out.get("dS0")
+        _need(dS0, "out['dS0']", f32, state, dev)
+        args = (q, k, v, beta, g, S0, d_o, dS_final, seq_offsets, out["dq"], out["dk"], out["dv"], out["dbeta"],
+                out["dg"], dS0)
+        _on_gpu(dev, *args)
+        _enqueue("delta_chunk_bwd", desc, args, dev, workspace)
     return out
 
 

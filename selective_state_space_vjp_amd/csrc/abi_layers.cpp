@@ -104,6 +104,46 @@ ssmvjp_status delta_chunk_fwd(const ssmvjp_delta_chunk_desc* desc, const void* q
   return finite_check(workspace, plan, outs, (hipStream_t)stream);
 }
 
+// ------------------------------ delta_chunk_bwd ------------------------------
+
+ssmvjp_status delta_chunk_bwd_workspace(const ssmvjp_delta_chunk_desc* desc, size_t* bytes) {
+  if (!bytes) return SSMVJP_EINVAL;
+  const ssmvjp_status s = delta_chunk_check(desc);
+  if (s != SSMVJP_OK) return s;
+  if (desc->dtype != SSMVJP_BF16) return SSMVJP_EUNSUPPORTED;
+  *bytes = with_flag(delta_bwd_workspace_bytes(*desc));
+  return SSMVJP_OK;
+}
+
+ssmvjp_status delta_chunk_bwd(const ssmvjp_delta_chunk_desc* desc, const void* q, const void* k, const void* v,
+                              const float* beta, const float* g, const float* S0, const void* d_o,
+                              const float* dS_final, const int32_t* seq_offsets, void* dq, void* dk, void* dv,
+                              float* dbeta, float* dg, float* dS0, void* workspace, size_t workspace_bytes,
+                              void* stream) {
+  ssmvjp_status s = delta_chunk_check(desc);
+  if (s != SSMVJP_OK) return s;
+  const ssmvjp_delta_chunk_desc& d = *desc;
+  if (d.dtype != SSMVJP_BF16) return SSMVJP_EUNSUPPORTED;
+  const int64_t tokens = chunk_tokens(d);
+  if (tokens > 0 && (!q || !k || !v || !beta || !g || !d_o || !dq || !dk || !dv || !dbeta || !dg)) return SSMVJP_EINVAL;
+  if ((d.packed != 0) != (seq_offsets != nullptr)) return SSMVJP_EINVAL;
+  const void* p16[] = {q, k, v, d_o, dq, dk, dv, S0, dS_final, dS0};
+  const void* p4[] = {beta, g, seq_offsets, dbeta, dg};
+  if (!all_aligned(p16, 16) || !all_aligned(p4, 4)) return SSMVJP_EINVAL;
+  const size_t plan = delta_bwd_workspace_bytes(d);
+  s = workspace_check(with_flag(plan), workspace, workspace_bytes);
+  if (s != SSMVJP_OK) return s;
+  if (d.batch == 0) return SSMVJP_OK;
+  const DeltaChunkBwdPointers ptr{q, k, v, d_o, beta, g, S0, dS_final, seq_offsets, dq, dk, dv, dbeta, dg, dS0, workspace};
+  s = hip_status(launch_delta_chunk_bwd(d, ptr, (hipStream_t)stream));
+  if (s != SSMVJP_OK || !check_finite_on()) return s;
+  const int64_t n = d.packed ? 0 : tokens;  // packed: rows that no sequence owns are left alone
+  const OutSpan outs[] = {{dq, n * d.nqk_heads * d.dk, true}, {dk, n * d.nqk_heads * d.dk, true},
+                          {dv, n * d.nv_heads * d.dv, true}, {dbeta, n * d.nv_heads, false}, {dg, n * d.nv_heads, false},
+                          {dS0, d.batch * d.nv_heads * d.dk * d.dv, false}};
+  return finite_check(workspace, plan, outs, (hipStream_t)stream);
+}
+
 // -------------------------------- delta_step ---------------------------------
 
 ssmvjp_status delta_step_workspace(const ssmvjp_delta_step_desc* desc, size_t* bytes) {

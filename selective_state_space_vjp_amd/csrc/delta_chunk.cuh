@@ -46,10 +46,11 @@ struct DeltaChunkArgs {
   float* G;   // [64]
   bf16* Tt;   // [6][2][64][8] fragments of T^T                      (backward from here on)
   bf16* Pt;   // [6][2][64][8] fragments of scale P^T
-  bf16 *Sh, *Sl, *dSh;          // [V][K] the state before the chunk (two parts), the state's gradient behind it
-  bf16 *rh, *rl, *muh, *mul;    // [V][64] r and mu = beta lambda (= dv), two parts each
-  float* rowp;                  // [nvt][2][64] per-tile row sums
-  float* endp;                  // [nvt] per-tile e^{G_63} <S0, dS>
+  bf16 *Sh, *Sl, *dSh;          // [nvt][KP/32][64][8] fragments of the state before the chunk (two parts) and of
+                                // the state's gradient behind it
+  bf16 *rh, *rl, *muh, *mul;    // [nvt][2][64][8] fragments of r and mu (two parts each)
+  float* rowp;                  // [nvt][2][64] sums over a tile's columns, see delta_chunk_rev_kernel
+  float* endp;                  // [nvt]
 };
 
 typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
@@ -102,6 +103,61 @@ __device__ __forceinline__ brsrc row_rsrc(const bf16* p, i64 tok0, int rows, i64
   return make_rsrc(p + (tok0 * heads + h) * cols, (unsigned)((((i64)rows - 1) * heads * cols + cols) * 2));
 }
 
+// The rows of a chunk on their way to LDS: registers <- memory (fetch), LDS <-
+// registers (commit), so that the loads of the next chunk are in flight while
+// this one is computed.  NT threads take part.
+template <int KP, int NT>
+struct RowTile {  // [64][KP] of q or k, swizzled rows, columns past K zero
+  static constexpr int N = 64 * KP / 8 / NT;
+  u32x4 r[N];
+  __device__ __forceinline__ void fetch(brsrc rs, int tid, i64 stride, i64 K) {
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+      const int p = tid + NT * i, row = p / (KP / 8), col = p % (KP / 8) * 8;
+      r[i] = bload16(rs, col < K ? (unsigned)((row * stride + col) * 2) : BUF_OOB);
+    }
+  }
+  __device__ __forceinline__ void commit(bf16* lds, int tid) const {
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+      const int p = tid + NT * i;
+      st16_xs(lds, KP, p / (KP / 8), p % (KP / 8) * 8, r[i]);
+    }
+  }
+};
+constexpr int VP = 36;  // row pitch of a staged [64][32] tile: 8-byte rows, shifted by 2 banks each
+template <int NT>
+struct ColTile {  // [64][32] of v or d_o, the columns from v0
+  static constexpr int N = 256 / NT;
+  u32x4 r[N];
+  __device__ __forceinline__ void fetch(brsrc rs, int tid, i64 stride, i64 v0, i64 V) {
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+      const int p = tid + NT * i, row = p / 4;
+      const i64 col = v0 + p % 4 * 8;
+      r[i] = bload16(rs, col < V ? (unsigned)((row * stride + col) * 2) : BUF_OOB);
+    }
+  }
+  __device__ __forceinline__ void commit(bf16* lds, int tid) const {
+    typedef unsigned u32x2 __attribute__((ext_vector_type(2)));
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+      const int p = tid + NT * i;
+      u32x2* d = (u32x2*)(lds + p / 4 * VP + p % 4 * 8);
+      d[0] = u32x2{r[i][0], r[i][1]};
+      d[1] = u32x2{r[i][2], r[i][3]};
+    }
+  }
+};
+// fragment of rows 16m .. 16m+15 of a swizzled row tile, contraction over its columns
+__device__ __forceinline__ Frag8 row_frag(const bf16* t, int KP, int m, int s, int lane) {
+  return {ld_colk_xs(t, KP, 16 * m, 32 * s, lane).v, ld_colk_xs(t, KP, 16 * m, 32 * s + 16, lane).v};
+}
+// fragment of columns 16t .. 16t+15, contraction over its rows
+__device__ __forceinline__ Frag8 col_frag(const bf16* x, int pitch, int t, int s, int lane) {
+  return {ld_rowk_xs(x, pitch, 32 * s, 16 * t, lane).v, ld_rowk_xs(x, pitch, 32 * s + 16, 16 * t, lane).v};
+}
+
 struct ChunkAt {
   DeltaSpan sp;
   i64 seq, tok0;
@@ -128,6 +184,7 @@ __device__ __forceinline__ bool walk_unit(i64 units, i64 nslice, i64& unit, i64&
 }
 inline i64 walk_blocks(i64 units, i64 nslice) { return (units + 7) / 8 * 8 * nslice; }
 
+DeltaChunkArgs delta_chunk_args(const ssmvjp_delta_chunk_desc& d, const int* off);
 hipError_t launch_delta_prep(const DeltaChunkArgs& a, bool backward, hipStream_t stream);
 hipError_t launch_delta_states(const DeltaChunkArgs& a, hipStream_t stream);
 

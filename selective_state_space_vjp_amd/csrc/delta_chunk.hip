@@ -230,14 +230,12 @@ __global__ void __launch_bounds__(256) delta_prep_kernel(DeltaChunkArgs a) {
 // ---------------------------------------------------------------------------
 // walk
 // ---------------------------------------------------------------------------
-constexpr int VP = 36;   // row pitch of the staged V tile (32 columns): 8-byte rows, shifted by 2 banks each
 constexpr int WNT = 128;  // threads of a walk's workgroup
 
 // MODE 0: the forward (o, S_final); 1: the states before every chunk, for the backward
 template <int KP, int MODE>
 __global__ void __launch_bounds__(WNT, 1) delta_chunk_walk_kernel(DeltaChunkArgs a) {
   constexpr int KS = KP / 32, KT = KP / 16;       // 32-steps and 16-tiles of K
-  constexpr int NK = 64 * KP / 8 / WNT;           // 16-byte pieces of K (or Q) per thread
   constexpr bool FWD = MODE == 0;
   __shared__ __attribute__((aligned(16))) bf16 Kb[2][64 * KP];
   __shared__ __attribute__((aligned(16))) bf16 Qb[FWD ? 2 : 1][FWD ? 64 * KP : 8];
@@ -252,47 +250,24 @@ __global__ void __launch_bounds__(WNT, 1) delta_chunk_walk_kernel(DeltaChunkArgs
   const i64 v0 = slice * 32 + w * 16;  // this wave's first column
   const bool act = v0 < a.V;           // V is a multiple of 16: all of a wave's columns or none
 
-  // staging: registers <- memory (chunk ch), LDS buffer <- registers
-  u32x4 sk[NK], sq[FWD ? NK : 1], sv[2];
+  RowTile<KP, WNT> sk, sq;
+  ColTile<WNT> sv;
   float sG = 0.0f, sB = 0.0f;
   auto fetch = [&](i64 ch) {
     const i64 tok0 = sp.start + ch * DCH;
     const int rows = (int)(sp.len - ch * DCH < DCH ? sp.len - ch * DCH : DCH);
-    const brsrc rk = row_rsrc(a.k, tok0, rows, a.H, h, a.K), rq = row_rsrc(a.q, tok0, rows, a.H, h, a.K);
-    const brsrc rv = row_rsrc(a.v, tok0, rows, a.HV, hv, a.V);
-#pragma unroll
-    for (int i = 0; i < NK; ++i) {
-      const int p = tid + WNT * i, row = p / (KP / 8), col = p % (KP / 8) * 8;
-      const unsigned o = col < a.K ? (unsigned)(((i64)row * a.H * a.K + col) * 2) : BUF_OOB;
-      sk[i] = bload16(rk, o);
-      if constexpr (FWD) sq[i] = bload16(rq, o);
-    }
-#pragma unroll
-    for (int i = 0; i < 2; ++i) {
-      const int p = tid + WNT * i, row = p / 4;
-      const i64 col = slice * 32 + p % 4 * 8;
-      sv[i] = bload16(rv, col < a.V ? (unsigned)(((i64)row * a.HV * a.V + col) * 2) : BUF_OOB);
-    }
+    sk.fetch(row_rsrc(a.k, tok0, rows, a.H, h, a.K), tid, a.H * a.K, a.K);
+    if constexpr (FWD) sq.fetch(row_rsrc(a.q, tok0, rows, a.H, h, a.K), tid, a.H * a.K, a.K);
+    sv.fetch(row_rsrc(a.v, tok0, rows, a.HV, hv, a.V), tid, a.HV * a.V, slice * 32, a.V);
     if (w == 0) {
       sG = a.G[((sp.slot0 + ch) * a.HV + hv) * 64 + lane];
       sB = lane < rows ? a.beta[(tok0 + lane) * a.HV + hv] : 0.0f;
     }
   };
   auto commit = [&](int bf) {
-    typedef unsigned u32x2 __attribute__((ext_vector_type(2)));
-#pragma unroll
-    for (int i = 0; i < NK; ++i) {
-      const int p = tid + WNT * i, row = p / (KP / 8), col = p % (KP / 8) * 8;
-      st16_xs(Kb[bf], KP, row, col, sk[i]);
-      if constexpr (FWD) st16_xs(Qb[bf], KP, row, col, sq[i]);
-    }
-#pragma unroll
-    for (int i = 0; i < 2; ++i) {
-      const int p = tid + WNT * i;
-      u32x2* d = (u32x2*)(Vb[bf] + p / 4 * VP + p % 4 * 8);
-      d[0] = u32x2{sv[i][0], sv[i][1]};
-      d[1] = u32x2{sv[i][2], sv[i][3]};
-    }
+    sk.commit(Kb[bf], tid);
+    if constexpr (FWD) sq.commit(Qb[bf], tid);
+    sv.commit(Vb[bf], tid);
     if (w == 0) {
       const float end = __shfl(sG, 63, 64);
       eGs[bf][lane] = exp_hw(sG);
@@ -343,17 +318,17 @@ __global__ void __launch_bounds__(WNT, 1) delta_chunk_walk_kernel(DeltaChunkArgs
         Frag8 hi, lo;
         split8(S[2 * s], S[2 * s + 1], hi, lo);
         if constexpr (!FWD) {
-          const i64 o = (cu * a.V + v0 + c) * a.K + 32 * s + 4 * q;
-          if (32 * s < a.K) *(s16x4*)(a.Sh + o) = hi.a, *(s16x4*)(a.Sl + o) = lo.a;
-          if (32 * s + 16 < a.K) *(s16x4*)(a.Sh + o + 16) = hi.b, *(s16x4*)(a.Sl + o + 16) = lo.b;
+          const i64 o = (((cu * a.nvt + slice * 2 + w) * KS + s) * 64 + lane) * 8;
+          *(u32x4*)(a.Sh + o) = as_u4(hi);
+          *(u32x4*)(a.Sl + o) = as_u4(lo);
         }
 #pragma unroll
         for (int m = 0; m < 4; ++m) {
-          const Frag8 kf = {ld_colk_xs(Kt, KP, 16 * m, 32 * s, lane).v, ld_colk_xs(Kt, KP, 16 * m, 32 * s + 16, lane).v};
+          const Frag8 kf = row_frag(Kt, KP, m, s, lane);
           x[m] = mma32(kf, hi, x[m]);
           x[m] = mma32(kf, lo, x[m]);
           if constexpr (FWD) {
-            const Frag8 qf = {ld_colk_xs(Qt, KP, 16 * m, 32 * s, lane).v, ld_colk_xs(Qt, KP, 16 * m, 32 * s + 16, lane).v};
+            const Frag8 qf = row_frag(Qt, KP, m, s, lane);
             ot[m] = mma32(hi, qf, ot[m]);
           }
         }
@@ -408,7 +383,7 @@ __global__ void __launch_bounds__(WNT, 1) delta_chunk_walk_kernel(DeltaChunkArgs
         S[t] *= eEnd;
 #pragma unroll
         for (int s = 0; s < 2; ++s) {
-          const Frag8 kf = {ld_rowk_xs(Kt, KP, 32 * s, 16 * t, lane).v, ld_rowk_xs(Kt, KP, 32 * s + 16, 16 * t, lane).v};
+          const Frag8 kf = col_frag(Kt, KP, t, s, lane);
           S[t] = mma32(kf, ul[s], S[t]);
           S[t] = mma32(kf, uh[s], S[t]);
         }

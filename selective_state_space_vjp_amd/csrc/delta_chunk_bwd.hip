@@ -1,0 +1,581 @@
+// delta_chunk_bwd.hip -- gradients of the chunked gated delta rule on MFMA.
+//
+// With lambda_i the adjoint of u_i and mu = beta lambda (delta_chunk.cuh has
+// the forward's algebra; dS the gradient of the state behind the chunk, N_ij =
+// mu_i . r_j, M the pair terms):
+//     dU = scale P^T dO + e^{G_63 - G} (K dS)
+//     mu = T^T (beta dU)  = dv
+//     dS0 = e^{G_63} dS + Q^T (scale e^G dO) - K^T (e^G mu)
+//     dD_ij = scale beta_j (dO_i . r_j) Gam_ij  (i >= j),  E_ij = -beta_j N_ij Gam_ij  (i > j)
+//     dq = scale e^G dO S0^T + dD K
+//     dk = -e^G mu S0^T + (e^{G_63 - G} beta r) dS^T + dD^T Q + E K + E^T K
+//     dbeta_j = r_j . dU_j - sum_{i > j} a_ij N_ij
+//     M_ij = dD_ij q_i . k_j + E_ij k_i . k_j
+//     dG_i = scale e^G_i dO_i . (Q S0)_i - e^G_i mu_i . (K S0)_i - su_i + sum_j M_ij - sum_j M_ji
+//     su_i = e^{G_63 - G_i} beta_i r_i . (K dS)_i
+//     dg_t = sum_{i >= t} dG_i + sum_i su_i + e^{G_63} <S0, dS>
+// In the sum over i >= t the pairs with both tokens behind t cancel between the
+// row and the column sums, exactly, since both add the same float32 M_ij; that
+// is why r, mu and the states enter M and the row terms with both bf16 parts,
+// and dg comes out at about 6e-6.  dq and dk are bf16: one part is enough.
+//
+// Four launches: delta_prep_kernel (T, T^T, scale P^T of every chunk),
+// delta_chunk_walk_kernel<., 1> (the state before every chunk),
+// delta_chunk_rev_kernel (the reverse walk, 16 columns per wave as the forward:
+// dv, r, dS, row sums over its columns) and delta_chunk_grads_kernel (all
+// chunks at once: dq, dk summed over the value heads of a qk head, dg, dbeta).
+#include "delta_chunk.cuh"
+
+namespace ssmvjp {
+namespace {
+
+constexpr int WNT = 128;
+
+// ---------------------------------------------------------------------------
+// reverse walk
+// ---------------------------------------------------------------------------
+// rowp[0][i] = this tile's part of dG_i's row terms (all but the M sums),
+// rowp[1][i] = r_i . dU_i,  endp = e^{G_63} <S0, dS> + sum_i su_i
+template <int KP>
+__global__ void __launch_bounds__(WNT, 1) delta_chunk_rev_kernel(DeltaChunkArgs a) {
+  constexpr int KS = KP / 32, KT = KP / 16;
+  __shared__ __attribute__((aligned(16))) bf16 Kb[2][64 * KP];
+  __shared__ __attribute__((aligned(16))) bf16 Qb[2][64 * KP];
+  __shared__ __attribute__((aligned(16))) bf16 Vb[2][64 * VP];
+  __shared__ __attribute__((aligned(16))) bf16 Ob[2][64 * VP];
+  __shared__ __attribute__((aligned(16))) float eGs[2][64], eEs[2][64], Bs[2][64];  // e^G, e^{G_63 - G}, beta
+  const int tid = threadIdx.x, lane = tid & 63, w = tid >> 6, c = lane & 15, q = lane >> 4;
+  i64 unit, slice;
+  if (!walk_unit(a.seq.nseq * a.HV, (a.V + 31) / 32, unit, slice)) return;
+  const i64 n = unit / a.HV, hv = unit % a.HV, h = hv / a.rep;
+  const DeltaSpan sp = a.seq.span(n);
+  const i64 nch = (sp.len + DCH - 1) / DCH;
+  const i64 v0 = slice * 32 + w * 16, vt = slice * 2 + w;
+  const bool act = v0 < a.V;
+
+  RowTile<KP, WNT> sk, sq;
+  ColTile<WNT> sv, so;
+  float sG = 0.0f, sB = 0.0f;
+  auto fetch = [&](i64 ch) {
+    const i64 tok0 = sp.start + ch * DCH;
+    const int rows = (int)(sp.len - ch * DCH < DCH ? sp.len - ch * DCH : DCH);
+    sk.fetch(row_rsrc(a.k, tok0, rows, a.H, h, a.K), tid, a.H * a.K, a.K);
+    sq.fetch(row_rsrc(a.q, tok0, rows, a.H, h, a.K), tid, a.H * a.K, a.K);
+    sv.fetch(row_rsrc(a.v, tok0, rows, a.HV, hv, a.V), tid, a.HV * a.V, slice * 32, a.V);
+    so.fetch(row_rsrc(a.d_o, tok0, rows, a.HV, hv, a.V), tid, a.HV * a.V, slice * 32, a.V);
+    if (w == 0) {
+      sG = a.G[((sp.slot0 + ch) * a.HV + hv) * 64 + lane];
+      sB = lane < rows ? a.beta[(tok0 + lane) * a.HV + hv] : 0.0f;
+    }
+  };
+  auto commit = [&](int bf) {
+    sk.commit(Kb[bf], tid);
+    sq.commit(Qb[bf], tid);
+    sv.commit(Vb[bf], tid);
+    so.commit(Ob[bf], tid);
+    if (w == 0) {
+      const float end = __shfl(sG, 63, 64);
+      eGs[bf][lane] = exp_hw(sG);
+      eEs[bf][lane] = exp_hw(end - sG);
+      Bs[bf][lane] = sB;
+    }
+  };
+
+  f32x4 dS[KT];
+#pragma unroll
+  for (int t = 0; t < KT; ++t) {
+    dS[t] = zero4();
+    if (a.dSf && act) {
+#pragma unroll
+      for (int r = 0; r < 4; ++r) {
+        const int k = 16 * t + 4 * q + r;
+        if (k < a.K) dS[t][r] = a.dSf[(unit * a.K + k) * a.V + v0 + c];
+      }
+    }
+  }
+  if (nch > 0) {
+    fetch(nch - 1);
+    commit((nch - 1) & 1);
+  }
+  __syncthreads();
+  for (i64 ch = nch - 1; ch >= 0; --ch) {
+    const int bf = ch & 1;
+    const i64 cu = (sp.slot0 + ch) * a.HV + hv;
+    if (ch > 0) fetch(ch - 1);
+    if (act) {
+      const bf16 *Kt = Kb[bf], *Qt = Qb[bf];
+      const u32x4* tf = (const u32x4*)(a.Tf + cu * 6 * 2 * 64 * 8) + lane;
+      const u32x4* tt = (const u32x4*)(a.Tt + cu * 6 * 2 * 64 * 8) + lane;
+      const u32x4* pt = (const u32x4*)(a.Pt + cu * 6 * 2 * 64 * 8) + lane;
+      auto at4 = [&](const float* p, int m) { return *(const f32x4*)(p + 16 * m + 4 * q); };
+      // K S0, Q S0 (both parts of S0), K dS (both parts of dS), <S0, dS>
+      f32x4 x[4], y[4], z[4];
+      f32x4 dot = zero4();
+#pragma unroll
+      for (int m = 0; m < 4; ++m) x[m] = zero4(), y[m] = zero4(), z[m] = zero4();
+#pragma unroll
+      for (int s = 0; s < KS; ++s) {
+        const i64 o = (((cu * a.nvt + vt) * KS + s) * 64 + lane) * 8;
+        const Frag8 sh = as_frag(*(const u32x4*)(a.Sh + o)), sl = as_frag(*(const u32x4*)(a.Sl + o));
+        Frag8 dh, dl;
+        split8(dS[2 * s], dS[2 * s + 1], dh, dl);
+        *(u32x4*)(a.dSh + o) = as_u4(dh);
+        dot += (unpack4(sh.a) + unpack4(sl.a)) * dS[2 * s];
+        dot += (unpack4(sh.b) + unpack4(sl.b)) * dS[2 * s + 1];
+#pragma unroll
+        for (int m = 0; m < 4; ++m) {
+          const Frag8 kf = row_frag(Kt, KP, m, s, lane), qf = row_frag(Qt, KP, m, s, lane);
+          x[m] = mma32(kf, sl, x[m]);
+          y[m] = mma32(qf, sl, y[m]);
+          z[m] = mma32(kf, dl, z[m]);
+          x[m] = mma32(kf, sh, x[m]);
+          y[m] = mma32(qf, sh, y[m]);
+          z[m] = mma32(kf, dh, z[m]);
+        }
+      }
+      // r = T (V - e^G K S0)
+      f32x4 r[4];
+      {
+        Frag8 vh[2], vl[2];
+#pragma unroll
+        for (int s = 0; s < 2; ++s) {
+          f32x4 t[2];
+#pragma unroll
+          for (int e = 0; e < 2; ++e) {
+            const int m = 2 * s + e;
+            t[e] = unpack4(ld_rowk(Vb[bf], VP, 16 * m, 16 * w, lane).v) - at4(eGs[bf], m) * x[m];
+          }
+          split8(t[0], t[1], vh[s], vl[s]);
+        }
+#pragma unroll
+        for (int m = 0; m < 4; ++m) {
+          r[m] = zero4();
+#pragma unroll
+          for (int s = 0; s <= m / 2; ++s) {
+            const Frag8 th = as_frag(tf[frag_lo(m, s) * 128]), tl = as_frag(tf[frag_lo(m, s) * 128 + 64]);
+            r[m] = mma32(th, vl[s], r[m]);
+            r[m] = mma32(tl, vh[s], r[m]);
+            r[m] = mma32(th, vh[s], r[m]);
+          }
+        }
+      }
+      // dU = scale P^T dO + e^{G_63 - G} K dS
+      Frag8 of[2];
+#pragma unroll
+      for (int s = 0; s < 2; ++s)
+        of[s] = {ld_rowk(Ob[bf], VP, 32 * s, 16 * w, lane).v, ld_rowk(Ob[bf], VP, 32 * s + 16, 16 * w, lane).v};
+      f32x4 du[4], mu[4];
+#pragma unroll
+      for (int m = 0; m < 4; ++m) {
+        z[m] *= at4(eEs[bf], m);
+        du[m] = z[m];
+#pragma unroll
+        for (int s = m / 2; s < 2; ++s) {
+          du[m] = mma32(as_frag(pt[frag_up(m, s) * 128 + 64]), of[s], du[m]);
+          du[m] = mma32(as_frag(pt[frag_up(m, s) * 128]), of[s], du[m]);
+        }
+      }
+      // mu = T^T (beta dU)
+      {
+        Frag8 bh[2], bl[2];
+#pragma unroll
+        for (int s = 0; s < 2; ++s)
+          split8(at4(Bs[bf], 2 * s) * du[2 * s], at4(Bs[bf], 2 * s + 1) * du[2 * s + 1], bh[s], bl[s]);
+#pragma unroll
+        for (int m = 0; m < 4; ++m) {
+          mu[m] = zero4();
+#pragma unroll
+          for (int s = m / 2; s < 2; ++s) {
+            const Frag8 th = as_frag(tt[frag_up(m, s) * 128]), tl = as_frag(tt[frag_up(m, s) * 128 + 64]);
+            mu[m] = mma32(th, bl[s], mu[m]);
+            mu[m] = mma32(tl, bh[s], mu[m]);
+            mu[m] = mma32(th, bh[s], mu[m]);
+          }
+        }
+      }
+      // r and mu for the gradients kernel
+#pragma unroll
+      for (int s = 0; s < 2; ++s) {
+        const i64 o = (((cu * a.nvt + vt) * 2 + s) * 64 + lane) * 8;
+        Frag8 hi, lo;
+        split8(r[2 * s], r[2 * s + 1], hi, lo);
+        *(u32x4*)(a.rh + o) = as_u4(hi);
+        *(u32x4*)(a.rl + o) = as_u4(lo);
+        split8(mu[2 * s], mu[2 * s + 1], hi, lo);
+        *(u32x4*)(a.muh + o) = as_u4(hi);
+        *(u32x4*)(a.mul + o) = as_u4(lo);
+      }
+      // row terms, summed over this wave's 16 columns
+      const float eEnd = eGs[bf][63];
+      float tail = eEnd * ((dot[0] + dot[1]) + (dot[2] + dot[3]));
+      float* rp = a.rowp + (cu * a.nvt + vt) * 2 * 64;
+#pragma unroll
+      for (int m = 0; m < 4; ++m) {
+        const f32x4 eg = at4(eGs[bf], m), be = at4(Bs[bf], m);
+        const f32x4 o = unpack4(m & 1 ? of[m / 2].b : of[m / 2].a);
+        const f32x4 su = be * r[m] * z[m];
+        const f32x4 t = eg * (a.scale * o * y[m] - mu[m] * x[m]) - su;
+        const f32x4 d = r[m] * du[m];
+        f32x4 ts, ds;
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          tail += su[j];
+          ts[j] = sum16(t[j]);
+          ds[j] = sum16(d[j]);
+        }
+        if (c == 0) {
+          *(f32x4*)(rp + 16 * m + 4 * q) = ts;
+          *(f32x4*)(rp + 64 + 16 * m + 4 * q) = ds;
+        }
+        // the operands of the state's update
+        mu[m] *= -eg;
+        x[m] = a.scale * eg * o;
+      }
+      tail = wave_sum(tail);
+      if (lane == 0) a.endp[cu * a.nvt + vt] = tail;
+      // dS0 = e^{G_63} dS + Q^T (scale e^G dO) - K^T (e^G mu)
+      Frag8 mh[2], ml[2], oh[2], ol[2];
+#pragma unroll
+      for (int s = 0; s < 2; ++s) {
+        split8(mu[2 * s], mu[2 * s + 1], mh[s], ml[s]);
+        split8(x[2 * s], x[2 * s + 1], oh[s], ol[s]);
+      }
+#pragma unroll
+      for (int t = 0; t < KT; ++t) {
+        dS[t] *= eEnd;
+#pragma unroll
+        for (int s = 0; s < 2; ++s) {
+          const Frag8 kf = col_frag(Kt, KP, t, s, lane), qf = col_frag(Qt, KP, t, s, lane);
+          dS[t] = mma32(kf, ml[s], dS[t]);
+          dS[t] = mma32(qf, ol[s], dS[t]);
+          dS[t] = mma32(kf, mh[s], dS[t]);
+          dS[t] = mma32(qf, oh[s], dS[t]);
+        }
+      }
+    }
+    if (ch > 0) commit(bf ^ 1);
+    __syncthreads();
+  }
+  if (a.dS0 && act) {
+#pragma unroll
+    for (int t = 0; t < KT; ++t)
+#pragma unroll
+      for (int r = 0; r < 4; ++r) {
+        const int k = 16 * t + 4 * q + r;
+        if (k < a.K) a.dS0[(unit * a.K + k) * a.V + v0 + c] = dS[t][r];
+      }
+  }
+}
+
+// ---------------------------------------------------------------------------
+// gradients of one chunk of one qk head
+// ---------------------------------------------------------------------------
+// Four waves, wave w owning row tile w of every 64-row result.  The columns of
+// V go by 32 (one contraction step): r, mu (two parts), S0, dS (one part) of
+// the slice are brought to LDS as [v][row] tiles, whose transposed reads are
+// the operands with the contraction over v.
+template <int KP>
+__global__ void __launch_bounds__(256) delta_chunk_grads_kernel(DeltaChunkArgs a) {
+  constexpr int KS = KP / 32, KT = KP / 16;
+  constexpr int NS = 2 * KS * 64 / 256;  // 16-byte pieces per thread of a slice of S0 (or dS)
+  __shared__ __attribute__((aligned(16))) bf16 Kb[64 * KP], Qb[64 * KP];
+  // the slice's tiles; behind the slices the same memory holds dD^T and E^T
+  __shared__ __attribute__((aligned(16))) bf16 buf[4 * 32 * 64 + 2 * 32 * KP];
+  __shared__ __attribute__((aligned(16))) float Gs[64], Bs[64], rowM[64], colM[4][64], colA[4][64];
+  bf16 *rH = buf, *rL = buf + 32 * 64, *mH = buf + 2 * 32 * 64, *mL = buf + 3 * 32 * 64, *sT = buf + 4 * 32 * 64,
+       *dT = sT + 32 * KP;
+  bf16 *Dt = buf, *Et = buf + 64 * 64;
+  const int tid = threadIdx.x, lane = tid & 63, w = tid >> 6, c = lane & 15, q = lane >> 4;
+  const i64 h = blockIdx.x % a.H, slot = blockIdx.x / a.H;
+  const ChunkAt at = chunk_at(a.seq, slot, lane);
+  if (at.rows == 0) return;
+  {
+    RowTile<KP, 256> tk, tq;
+    tk.fetch(row_rsrc(a.k, at.tok0, at.rows, a.H, h, a.K), tid, a.H * a.K, a.K);
+    tq.fetch(row_rsrc(a.q, at.tok0, at.rows, a.H, h, a.K), tid, a.H * a.K, a.K);
+    tk.commit(Kb, tid);
+    tq.commit(Qb, tid);
+  }
+  __syncthreads();
+  // lane: column j = 16 b + c, rows i = 16 w + 4 q + r
+  f32x4 kk[4], qk[4];
+#pragma unroll
+  for (int b = 0; b < 4; ++b) {
+    kk[b] = zero4();
+    qk[b] = zero4();
+    if (b <= w) {
+#pragma unroll
+      for (int s = 0; s < KS; ++s) {
+        const Frag8 y = row_frag(Kb, KP, b, s, lane);
+        kk[b] = mma32(row_frag(Kb, KP, w, s, lane), y, kk[b]);
+        qk[b] = mma32(row_frag(Qb, KP, w, s, lane), y, qk[b]);
+      }
+    }
+  }
+  f32x4 dq[KT], dk[KT];  // rows i = 16 w + 4 q + r, column 16 t + c
+#pragma unroll
+  for (int t = 0; t < KT; ++t) dq[t] = zero4(), dk[t] = zero4();
+
+  const i64 nsl = (a.nvt + 1) / 2;
+  for (i64 rr = 0; rr < a.rep; ++rr) {
+    const i64 hv = h * a.rep + rr, cu = slot * a.HV + hv;
+    u32x4 pr[4], ps[NS], pd[NS];
+    const brsrc ro = row_rsrc(a.d_o, at.tok0, at.rows, a.HV, hv, a.V);
+    typedef unsigned u32x2 __attribute__((ext_vector_type(2)));
+    u32x2 po[2];
+    // piece p of a slice: tile p / (64 n) of the two, step, lane; tiles past V read as zeros
+    auto fetch = [&](i64 sl) {
+      {
+        const i64 t = sl * 2 + (tid >> 7);
+        const i64 o = (((cu * a.nvt + t) * 2 + (w & 1)) * 64 + lane) * 8;
+        const bool in = t < a.nvt;
+        pr[0] = in ? *(const u32x4*)(a.rh + o) : zero_u4();
+        pr[1] = in ? *(const u32x4*)(a.rl + o) : zero_u4();
+        pr[2] = in ? *(const u32x4*)(a.muh + o) : zero_u4();
+        pr[3] = in ? *(const u32x4*)(a.mul + o) : zero_u4();
+      }
+#pragma unroll
+      for (int i = 0; i < NS; ++i) {
+        const int p = tid + 256 * i;
+        const i64 t = sl * 2 + p / (64 * KS);
+        const i64 o = (((cu * a.nvt + t) * KS + p / 64 % KS) * 64 + lane) * 8;
+        const bool in = t < a.nvt;
+        ps[i] = in ? *(const u32x4*)(a.Sh + o) : zero_u4();
+        pd[i] = in ? *(const u32x4*)(a.dSh + o) : zero_u4();
+      }
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        const i64 col = sl * 32 + 16 * e + 4 * q;
+        po[e] = __builtin_bit_cast(u32x2, __builtin_amdgcn_raw_buffer_load_b64(
+            ro, col < a.V ? (int)(((16 * w + c) * a.HV * a.V + col) * 2) : (int)BUF_OOB, 0, 0));
+      }
+    };
+    auto put = [&](bf16* t, int pitch, int row, int s, const u32x4& u) {  // a fragment's two 4-element runs
+      *(u32x2*)(t + row * pitch + xsw_off(row, 32 * s + 4 * q)) = u32x2{u[0], u[1]};
+      *(u32x2*)(t + row * pitch + xsw_off(row, 32 * s + 16 + 4 * q)) = u32x2{u[2], u[3]};
+    };
+    fetch(0);
+    __syncthreads();  // the previous head's readers are done
+    if (w == 0) {
+      Gs[lane] = a.G[cu * 64 + lane];
+      Bs[lane] = lane < at.rows ? a.beta[(at.tok0 + lane) * a.HV + hv] : 0.0f;
+    }
+    f32x4 dp[4], nn[4], x1[KT];
+#pragma unroll
+    for (int b = 0; b < 4; ++b) dp[b] = zero4(), nn[b] = zero4();
+#pragma unroll
+    for (int t = 0; t < KT; ++t) x1[t] = zero4();
+    for (i64 sl = 0; sl < nsl; ++sl) {
+      if (sl) __syncthreads();
+      {
+        const int row = 16 * (tid >> 7) + c;
+        put(rH, 64, row, w & 1, pr[0]);
+        put(rL, 64, row, w & 1, pr[1]);
+        put(mH, 64, row, w & 1, pr[2]);
+        put(mL, 64, row, w & 1, pr[3]);
+#pragma unroll
+        for (int i = 0; i < NS; ++i) {
+          const int p = tid + 256 * i;
+          put(sT, KP, 16 * (p / (64 * KS)) + c, p / 64 % KS, ps[i]);
+          put(dT, KP, 16 * (p / (64 * KS)) + c, p / 64 % KS, pd[i]);
+        }
+      }
+      const Frag8 of = {__builtin_bit_cast(s16x4, po[0]), __builtin_bit_cast(s16x4, po[1])};
+      __syncthreads();
+      if (sl + 1 < nsl) fetch(sl + 1);
+      const float Gi = Gs[16 * w + c], eg = exp_hw(Gi), we = exp_hw(Gs[63] - Gi) * Bs[16 * w + c];
+      const Frag8 mh = col_frag(mH, 64, w, 0, lane), ml = col_frag(mL, 64, w, 0, lane);
+      // dv = mu, rounded: its hi part
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        const i64 col = sl * 32 + 16 * e + 4 * q;
+        if (16 * w + c < at.rows && col < a.V)
+          *(s16x4*)(a.dv + ((at.tok0 + 16 * w + c) * a.HV + hv) * a.V + col) = e ? mh.b : mh.a;
+      }
+#pragma unroll
+      for (int b = 0; b < 4; ++b)
+        if (b <= w) {
+          const Frag8 rh = col_frag(rH, 64, b, 0, lane), rl = col_frag(rL, 64, b, 0, lane);
+          dp[b] = mma32(of, rl, dp[b]);
+          nn[b] = mma32(mh, rl, nn[b]);
+          nn[b] = mma32(ml, rh, nn[b]);
+          dp[b] = mma32(of, rh, dp[b]);
+          nn[b] = mma32(mh, rh, nn[b]);
+        }
+      // -e^G mu and e^{G_63 - G} beta r, rounded once
+      const Frag8 rw = col_frag(rH, 64, w, 0, lane);
+      const Frag8 ms = {pack4(-eg * unpack4(mh.a)), pack4(-eg * unpack4(mh.b))};
+      const Frag8 rs = {pack4(we * unpack4(rw.a)), pack4(we * unpack4(rw.b))};
+#pragma unroll
+      for (int t = 0; t < KT; ++t) {
+        const Frag8 sf = col_frag(sT, KP, t, 0, lane), df = col_frag(dT, KP, t, 0, lane);
+        x1[t] = mma32(of, sf, x1[t]);
+        dk[t] = mma32(ms, sf, dk[t]);
+        dk[t] = mma32(rs, df, dk[t]);
+      }
+    }
+    __syncthreads();  // the slices' tiles are free
+    // pair terms; column j = 16 b + c, rows i = 16 w + 4 q + r
+    const f32x4 Gi = *(const f32x4*)(Gs + 16 * w + 4 * q);
+    f32x4 rm = zero4();
+#pragma unroll
+    for (int b = 0; b < 4; ++b) {
+      f32x4 D = zero4(), E = zero4();
+      float cm = 0.0f, ca = 0.0f;
+      if (b <= w) {
+        const int j = 16 * b + c;
+        const float Gj = Gs[j], bj = Bs[j];
+#pragma unroll
+        for (int r = 0; r < 4; ++r) {
+          const int i = 16 * w + 4 * q + r;
+          const float gam = i >= j ? exp_hw(Gi[r] - Gj) : 0.0f;
+          D[r] = a.scale * bj * dp[b][r] * gam;
+          if (i > j) {
+            E[r] = -bj * nn[b][r] * gam;
+            const float m = D[r] * qk[b][r] + E[r] * kk[b][r];
+            rm[r] += m;
+            cm += m;
+            ca += gam * kk[b][r] * nn[b][r];
+          } else if (i < j) {
+            D[r] = 0.0f;
+          }
+        }
+      }
+      cm = sum4q(cm);
+      ca = sum4q(ca);
+      if (q == 0) colM[w][16 * b + c] = cm, colA[w][16 * b + c] = ca;
+      const int j = 16 * b + c, i0 = 16 * w + 4 * q;
+      *(s16x4*)(Dt + j * 64 + xsw_off(j, i0)) = pack4(D);
+      *(s16x4*)(Et + j * 64 + xsw_off(j, i0)) = pack4(E);
+    }
+#pragma unroll
+    for (int r = 0; r < 4; ++r) rm[r] = sum16(rm[r]);
+    if (c == 0) *(f32x4*)(rowM + 16 * w + 4 * q) = rm;
+    // dq += scale e^G (dO S0^T)
+#pragma unroll
+    for (int t = 0; t < KT; ++t)
+#pragma unroll
+      for (int r = 0; r < 4; ++r) dq[t][r] += a.scale * exp_hw(Gi[r]) * x1[t][r];
+    __syncthreads();
+    // dq += dD K, dk += E K (rows i); dk += dD^T Q + E^T K (rows j)
+    Frag8 dr[2], er[2], dc[2], ec[2];
+#pragma unroll
+    for (int s = 0; s < 2; ++s) {
+      dr[s] = col_frag(Dt, 64, w, s, lane);
+      er[s] = col_frag(Et, 64, w, s, lane);
+      dc[s] = row_frag(Dt, 64, w, s, lane);
+      ec[s] = row_frag(Et, 64, w, s, lane);
+    }
+#pragma unroll
+    for (int t = 0; t < KT; ++t)
+#pragma unroll
+      for (int s = 0; s < 2; ++s) {
+        const Frag8 kf = col_frag(Kb, KP, t, s, lane);
+        if (s <= w >> 1) {
+          dq[t] = mma32(dr[s], kf, dq[t]);
+          dk[t] = mma32(er[s], kf, dk[t]);
+        }
+        if (s >= w >> 1) {
+          dk[t] = mma32(ec[s], kf, dk[t]);
+          dk[t] = mma32(dc[s], col_frag(Qb, KP, t, s, lane), dk[t]);
+        }
+      }
+    // dbeta, dg
+    if (w == 0) {
+      const float* rp = a.rowp + cu * a.nvt * 2 * 64;
+      float dG = 0.0f, db = 0.0f, tail = 0.0f;
+      for (i64 t = 0; t < a.nvt; ++t) {
+        dG += rp[t * 128 + lane];
+        db += rp[t * 128 + 64 + lane];
+        tail += a.endp[cu * a.nvt + t];
+      }
+      dG += rowM[lane] - ((colM[0][lane] + colM[1][lane]) + (colM[2][lane] + colM[3][lane]));
+      db -= (colA[0][lane] + colA[1][lane]) + (colA[2][lane] + colA[3][lane]);
+      const float sum = wave_incl_suffix(dG, lane) + tail;
+      if (lane < at.rows) {
+        const i64 o = (at.tok0 + lane) * a.HV + hv;
+        a.dg[o] = sum;
+        a.dbeta[o] = db;
+      }
+    }
+  }
+  // out: row i, 16 columns at a time
+#pragma unroll
+  for (int t = 0; t < KT; ++t)
+    if (16 * t < a.K) {
+#pragma unroll
+      for (int r = 0; r < 4; ++r) {
+        const int i = 16 * w + 4 * q + r;
+        if (i < at.rows) {
+          const i64 o = ((at.tok0 + i) * a.H + h) * a.K + 16 * t + c;
+          a.dq[o] = (bf16)dq[t][r];
+          a.dk[o] = (bf16)dk[t][r];
+        }
+      }
+    }
+}
+
+struct BwdPlan {
+  i64 off_T, off_Tt, off_Pt, off_G, off_Sh, off_Sl, off_dS, off_rh, off_rl, off_mh, off_ml, off_row, off_end;
+  size_t bytes;
+};
+BwdPlan bwd_plan(const ssmvjp_delta_chunk_desc& d) {
+  const i64 cells = delta_slots(d) * d.nv_heads, nvt = d.dv / 16, KP = d.dk <= 64 ? 64 : 128;
+  BwdPlan p{};
+  i64 off = 0;
+  auto carve = [&](i64 bytes) {
+    const i64 o = off;
+    off += (bytes + 255) / 256 * 256;
+    return o;
+  };
+  const i64 tri = cells * 6 * 2 * 64 * 8 * 2, st = cells * nvt * KP * 16 * 2, rw = cells * nvt * 2 * 64 * 8 * 2;
+  p.off_T = carve(tri);
+  p.off_Tt = carve(tri);
+  p.off_Pt = carve(tri);
+  p.off_G = carve(cells * 64 * 4);
+  p.off_Sh = carve(st);
+  p.off_Sl = carve(st);
+  p.off_dS = carve(st);
+  p.off_rh = carve(rw);
+  p.off_rl = carve(rw);
+  p.off_mh = carve(rw);
+  p.off_ml = carve(rw);
+  p.off_row = carve(cells * nvt * 2 * 64 * 4);
+  p.off_end = carve(cells * nvt * 4);
+  p.bytes = (size_t)off;
+  return p;
+}
+
+}  // namespace
+
+size_t delta_bwd_workspace_bytes(const ssmvjp_delta_chunk_desc& d) { return bwd_plan(d).bytes; }
+
+hipError_t launch_delta_chunk_bwd(const ssmvjp_delta_chunk_desc& d, const DeltaChunkBwdPointers& p, hipStream_t stream) {
+  DeltaChunkArgs a = delta_chunk_args(d, p.seq_offsets);
+  const BwdPlan pl = bwd_plan(d);
+  char* ws = (char*)p.workspace;
+  a.q = (const bf16*)p.q; a.k = (const bf16*)p.k; a.v = (const bf16*)p.v; a.d_o = (const bf16*)p.d_o;
+  a.beta = p.beta; a.g = p.g; a.S0 = p.S0; a.dSf = p.dS_final;
+  a.dq = (bf16*)p.dq; a.dk = (bf16*)p.dk; a.dv = (bf16*)p.dv; a.dbeta = p.dbeta; a.dg = p.dg; a.dS0 = p.dS0;
+  auto b16 = [&](i64 off) { return (bf16*)(ws + off); };
+  a.Tf = b16(pl.off_T); a.Tt = b16(pl.off_Tt); a.Pt = b16(pl.off_Pt); a.G = (float*)(ws + pl.off_G);
+  a.Sh = b16(pl.off_Sh); a.Sl = b16(pl.off_Sl); a.dSh = b16(pl.off_dS);
+  a.rh = b16(pl.off_rh); a.rl = b16(pl.off_rl); a.muh = b16(pl.off_mh); a.mul = b16(pl.off_ml);
+  a.rowp = (float*)(ws + pl.off_row); a.endp = (float*)(ws + pl.off_end);
+  if (a.nslots > 0) {
+    hipError_t e = launch_delta_prep(a, true, stream);
+    if (e == hipSuccess) e = launch_delta_states(a, stream);
+    if (e != hipSuccess) return e;
+  }
+  const dim3 walk((unsigned)walk_blocks(a.seq.nseq * a.HV, (a.V + 31) / 32)), cells((unsigned)(a.nslots * a.H));
+  if (a.K <= 64) {
+    hipLaunchKernelGGL((delta_chunk_rev_kernel<64>), walk, dim3(WNT), 0, stream, a);
+    if (a.nslots > 0) hipLaunchKernelGGL((delta_chunk_grads_kernel<64>), cells, dim3(256), 0, stream, a);
+  } else {
+    hipLaunchKernelGGL((delta_chunk_rev_kernel<128>), walk, dim3(WNT), 0, stream, a);
+    if (a.nslots > 0) hipLaunchKernelGGL((delta_chunk_grads_kernel<128>), cells, dim3(256), 0, stream, a);
+  }
+  return hipGetLastError();
+}
+
+}  // namespace ssmvjp

@@ -141,6 +141,17 @@ hipError_t launch_delta_fwd(const ssmvjp_delta_chunk_desc& d, const DeltaChunkPo
 // the same token by token (delta_step.hip); no workspace
 hipError_t launch_delta_walk(const ssmvjp_delta_chunk_desc& d, const DeltaChunkPointers& ptr, hipStream_t stream);
 
+struct DeltaChunkBwdPointers {
+  const void *q, *k, *v, *d_o;
+  const float *beta, *g, *S0, *dS_final;
+  const int32_t* seq_offsets;
+  void *dq, *dk, *dv;
+  float *dbeta, *dg, *dS0;  // dS0 NULL: not written
+  void* workspace;
+};
+size_t delta_bwd_workspace_bytes(const ssmvjp_delta_chunk_desc& d);
+hipError_t launch_delta_chunk_bwd(const ssmvjp_delta_chunk_desc& d, const DeltaChunkBwdPointers& ptr, hipStream_t stream);
+
 struct DeltaStepPointers {
   const void *q, *k, *v;
   const float *beta, *g;
