@@ -342,8 +342,8 @@ typedef struct {
  * matrix cores (states to about 1e-5 of their norm), float32 token by token.
  * g may be -infinity (a reset); the chunked form takes every g below -88 as -88.
  * Constraints: HV % H == 0 (SSMVJP_EINVAL otherwise); K % 16 == 0, K <= 128,
- * V % 16 == 0, H*K and HV*V below 2^24 (SSMVJP_EUNSUPPORTED otherwise).  q, k,
- * v, o, S0, S_final 16-byte aligned. */
+ * V % 16 == 0, V <= 65536, H*K and HV*V below 2^24 (SSMVJP_EUNSUPPORTED
+ * otherwise).  q, k, v, o, S0, S_final 16-byte aligned. */
 ssmvjp_status delta_chunk_fwd_workspace(const ssmvjp_delta_chunk_desc* desc, size_t* bytes);
 ssmvjp_status delta_chunk_fwd(const ssmvjp_delta_chunk_desc* desc,
                               const void* q, const void* k, const void* v, const float* beta, const float* g,

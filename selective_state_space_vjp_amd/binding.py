@@ -556,6 +556,19 @@ class DeltaCall:
 
 
 # --------------------------------------------------------------------------- #
+class _Here:
+    """The current stream of the current device: nothing to switch."""
+
+    def __enter__(self):
+        return self
+
+    def __exit__(self, *exc):
+        return False
+
+
+_HERE = _Here()
+
+
 def _scope(dev, stream):
     """Where a call's launches and allocations go: the given stream, or the current
     stream of the tensors' device (which need not be the current device)."""
@@ -565,7 +578,7 @@ def _scope(dev, stream):
         if stream.device != dev:
             raise ValueError(f"the stream is on {stream.device}, the tensors on {dev}")
         return torch.cuda.stream(stream)
-    return torch.cuda.device(dev)
+    return _HERE if torch.cuda.current_device() == dev.index else torch.cuda.device(dev)
 
 
 def _required(**tensors):
@@ -574,18 +587,38 @@ def _required(**tensors):
             raise ValueError(f"{name} is required")
 
 
+def _fits(t, dtype, shape):
+    """What _need checks, as a truth value: these calls are made once per token, and a
+    check that passes must cost no more than the comparison."""
+    return t.dtype is dtype and t.shape == shape and t.is_contiguous()
+
+
 def _query(name, desc):
     n = ctypes.c_size_t(0)
     _check(name, getattr(lib(), name)(ctypes.byref(desc), ctypes.byref(n)))
     return n.value
 
 
-def _enqueue(name, desc, args, dev, workspace):
-    """Workspace and launch of one of the entry points that end in (workspace, bytes, stream)."""
-    ws, wsb = _workspace(_query(name + "_workspace", desc), dev, workspace)
-    st = getattr(lib(), name)(ctypes.byref(desc), *map(_ptr, args), _ptr(ws), wsb,
-                              ctypes.c_void_p(torch.cuda.current_stream(dev).cuda_stream))
-    _check(name, st)
+_entry = {}  # entry points by name, looked up once
+
+
+def _enqueue(name, desc, args, dev, workspace, needs=True):
+    """Workspace and launch of one of the entry points that end in (workspace, bytes, stream).
+    needs=False: the call takes a workspace only in the debug finiteness mode, and says so."""
+    fn = _entry.get(name)
+    if fn is None:
+        fn = _entry[name] = getattr(lib(), name)
+    d = ctypes.byref(desc)
+    ptrs = [None if t is None else t.data_ptr() for t in args]
+    stream = torch._C._cuda_getCurrentRawStream(dev.index)
+    st = EWORKSPACE
+    if not needs and workspace is None:
+        st = fn(d, *ptrs, None, 0, stream)
+    if st == EWORKSPACE:
+        ws, wsb = _workspace(_query(name + "_workspace", desc), dev, workspace)
+        st = fn(d, *ptrs, None if ws is None else ws.data_ptr(), wsb, stream)
+    if st != OK:
+        raise SsmVjpError(name, st)
 
 
 def delta_chunk_desc(q, v, scale, seq_offsets=None):
@@ -686,27 +719,30 @@ def delta_step(q, k, v, beta, g, state, *, scale, slots=None, out=None, workspac
     request whose slot is outside [0,n) or was named by an earlier request gets zeros and
     touches no state.
     """
-    _required(q=q, k=k, v=v, beta=beta, g=g, state=state)
+    if q is None or k is None or v is None or beta is None or g is None or state is None:
+        _required(q=q, k=k, v=v, beta=beta, g=g, state=state)
     if q.dim() != 3 or v.dim() != 3 or state.dim() != 4 or g.dim() not in (2, 3):
         raise ValueError("q must be [b,H,K], v [b,HV,V], g [b,HV] or [b,HV,K] and state [n,HV,K,V]")
     b, H, K = q.shape
     HV, V = v.shape[1], v.shape[2]
     dev, big, f32 = q.device, q.dtype, torch.float32
     per_key = g.dim() == 3
-    _need(q, "q", big, (b, H, K), dev)
-    _need(k, "k", big, (b, H, K), dev)
-    _need(v, "v", big, (b, HV, V), dev)
-    _need(beta, "beta", f32, (b, HV), dev)
-    _need(g, "g", f32, (b, HV, K) if per_key else (b, HV), dev)
-    _need(state, "state", f32, (state.shape[0], HV, K, V), dev)
-    _need(slots, "slots", torch.int32, (b,), dev)
+    for name, t, dtype, shape in (("q", q, big, (b, H, K)), ("k", k, big, (b, H, K)), ("v", v, big, (b, HV, V)),
+                                  ("beta", beta, f32, (b, HV)), ("g", g, f32, (b, HV, K) if per_key else (b, HV)),
+                                  ("state", state, f32, (state.shape[0], HV, K, V)), ("slots", slots, torch.int32, (b,))):
+        if t is not None and not _fits(t, dtype, shape):
+            _need(t, name, dtype, shape, dev)
     desc = DeltaStepDesc(b, state.shape[0], H, HV, K, V, float(scale), _dtype_code(q),
                          GATE_PER_KEY if per_key else GATE_PER_HEAD, 0)
     with _scope(dev, stream):
-        o = torch.empty_like(v) if out is None else out
-        _need(o, "out", big, (b, HV, V), dev)
-        _on_gpu(dev, q, k, v, beta, g, state, slots, o)
-        _enqueue("delta_step", desc, (q, k, v, beta, g, state, slots, o), dev, workspace)
+        if out is None:
+            o = torch.empty_like(v)
+        else:
+            o = out
+            _need(o, "out", big, (b, HV, V), dev)
+        args = (q, k, v, beta, g, state, slots, o)
+        _on_gpu(dev, *args)
+        _enqueue("delta_step", desc, args, dev, workspace, needs=False)
     return o
 
 
@@ -748,11 +784,14 @@ def layer_norm_fwd(x, weight=None, bias=None, *, eps=1e-5, want_ckpt8=False, out
         raise ValueError("a bias needs a weight")
     desc = norm_desc(x, weight, eps)
     dev, f32 = x.device, torch.float32
-    _need(x, "x", x.dtype, tuple(x.shape), dev)
+    if not x.is_contiguous():
+        raise ValueError("x must be contiguous")
     if weight is not None:
-        _need(weight, "weight", f32, _norm_wshape(desc, weight), dev)
-        _need(bias, "bias", f32, _norm_wshape(desc, weight), dev)
-    stat, blocks = tuple(x.shape[:-1]), tuple(x.shape[:-1]) + ((desc.dim + 63) // 64,)
+        ws = _norm_wshape(desc, weight)
+        for name, t in (("weight", weight), ("bias", bias)):
+            if t is not None and not _fits(t, f32, ws):
+                _need(t, name, f32, ws, dev)
+    stat, blocks = x.shape[:-1], x.shape[:-1] + ((desc.dim + 63) // 64,)
     with _scope(dev, stream):
         if out is None:
             out = {"y": torch.empty_like(x), "mean": torch.empty(stat, dtype=f32, device=dev),
@@ -760,13 +799,15 @@ def layer_norm_fwd(x, weight=None, bias=None, *, eps=1e-5, want_ckpt8=False, out
             if want_ckpt8:
                 out["x8"] = torch.empty(x.shape, dtype=torch.int8, device=dev)
                 out["x8_scale"] = torch.empty(blocks, dtype=f32, device=dev)
-        spec = {"y": (x.dtype, tuple(x.shape)), "mean": (f32, stat), "rstd": (f32, stat)}
-        if want_ckpt8:
-            spec.update(x8=(torch.int8, tuple(x.shape)), x8_scale=(f32, blocks))
-        _check_out(out, spec, dev)
+        else:
+            spec = {"y": (x.dtype, x.shape), "mean": (f32, stat), "rstd": (f32, stat)}
+            if want_ckpt8:
+                spec.update(x8=(torch.int8, x.shape), x8_scale=(f32, blocks))
+            _check_out(out, spec, dev)
         x8, x8s = (out["x8"], out["x8_scale"]) if want_ckpt8 else (None, None)
-        _on_gpu(dev, x, weight, bias, out["y"], out["mean"], out["rstd"], x8, x8s)
-        _enqueue("layer_norm_fwd", desc, (x, weight, bias, out["y"], out["mean"], out["rstd"], x8, x8s), dev, workspace)
+        args = (x, weight, bias, out["y"], out["mean"], out["rstd"], x8, x8s)
+        _on_gpu(dev, *args)
+        _enqueue("layer_norm_fwd", desc, args, dev, workspace, needs=False)
     return out
 
 
@@ -782,27 +823,27 @@ def layer_norm_bwd(dy, x, mean, rstd, weight=None, *, ckpt8=None, out=None, work
         raise ValueError("exactly one of x and ckpt8 must be given")
     desc = norm_desc(dy, weight, 0.0)
     dev, f32 = dy.device, torch.float32
-    stat = tuple(dy.shape[:-1])
-    _need(dy, "dy", dy.dtype, tuple(dy.shape), dev)
-    _need(x, "x", dy.dtype, tuple(dy.shape), dev)
-    _need(mean, "mean", f32, stat, dev)
-    _need(rstd, "rstd", f32, stat, dev)
+    stat = dy.shape[:-1]
     x8, x8s = (None, None) if ckpt8 is None else ckpt8
     if ckpt8 is not None:
         _required(x8=x8, x8_scale=x8s)
-        _need(x8, "x8", torch.int8, tuple(dy.shape), dev)
-        _need(x8s, "x8_scale", f32, stat + ((desc.dim + 63) // 64,), dev)
-    if weight is not None:
-        _need(weight, "weight", f32, _norm_wshape(desc, weight), dev)
+    ws = None if weight is None else _norm_wshape(desc, weight)
+    for name, t, dtype, shape in (("dy", dy, dy.dtype, dy.shape), ("x", x, dy.dtype, dy.shape), ("mean", mean, f32, stat),
+                                  ("rstd", rstd, f32, stat), ("x8", x8, torch.int8, dy.shape),
+                                  ("x8_scale", x8s, f32, stat + ((desc.dim + 63) // 64,)), ("weight", weight, f32, ws)):
+        if t is not None and not _fits(t, dtype, shape):
+            _need(t, name, dtype, shape, dev)
     with _scope(dev, stream):
         if out is None:
             out = {"dx": torch.empty_like(dy), "dweight": None if weight is None else torch.empty_like(weight),
                    "dbias": None if weight is None else torch.empty_like(weight)}
-        spec = {"dx": (dy.dtype, tuple(dy.shape))}
-        if weight is not None:
-            spec.update(dweight=(f32, tuple(weight.shape)), dbias=(f32, tuple(weight.shape)))
-        _check_out(out, spec, dev)
+        else:
+            spec = {"dx": (dy.dtype, dy.shape)}
+            if weight is not None:
+                spec.update(dweight=(f32, ws), dbias=(f32, ws))
+            _check_out(out, spec, dev)
         dw, db = (out["dweight"], out["dbias"]) if weight is not None else (None, None)
-        _on_gpu(dev, dy, x, x8, x8s, mean, rstd, weight, out["dx"], dw, db)
-        _enqueue("layer_norm_bwd", desc, (dy, x, x8, x8s, mean, rstd, weight, out["dx"], dw, db), dev, workspace)
+        args = (dy, x, x8, x8s, mean, rstd, weight, out["dx"], dw, db)
+        _on_gpu(dev, *args)
+        _enqueue("layer_norm_bwd", desc, args, dev, workspace)
     return out

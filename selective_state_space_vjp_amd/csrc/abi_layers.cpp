@@ -13,9 +13,8 @@ bool fits(double n) { return n <= (double)DIM_MAX; }
 ssmvjp_status delta_dims_check(int64_t H, int64_t HV, int64_t K, int64_t V, int32_t dtype) {
   if (H <= 0 || HV <= 0 || K <= 0 || V <= 0 || HV % H || !valid_dtype(dtype)) return SSMVJP_EINVAL;
   if (K % 16 || K > 128 || V % 16) return SSMVJP_EUNSUPPORTED;
-  // 32-bit byte offsets inside one chunk's rows
-  if (H > (1 << 24) || HV > (1 << 24) || V > (1 << 24) || H * K >= (1 << 24) || HV * V >= (1 << 24))
-    return SSMVJP_EUNSUPPORTED;
+  // 32-bit byte offsets inside one chunk's rows and inside one state
+  if (V > 65536 || H > (1 << 24) || HV > (1 << 24) || H * K >= (1 << 24) || HV * V >= (1 << 24)) return SSMVJP_EUNSUPPORTED;
   return SSMVJP_OK;
 }
 

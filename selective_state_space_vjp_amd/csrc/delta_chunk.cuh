@@ -15,7 +15,8 @@
 // (x = hi + lo up to 2^-16 |x|, about 3e-6 in the mean), and the products keep
 // hi hi, hi lo and lo hi, with float32 accumulation: states and the float32
 // gradients come out at about 5e-6 instead of the 3e-3 of one bf16 part, and
-// an error in the state is carried over thousands of tokens.  What only leads
+// an error in the state is carried over thousands of tokens.  T is applied as
+// I + (T - I), the identity without any rounding.  What only leads
 // to a bf16 output (the readout, dq, dk) takes the hi part alone.
 //
 // Layouts.  D of a 16x16 MFMA tile has lane (c = lane % 16, q = lane / 16) hold
@@ -28,6 +29,7 @@
 #pragma once
 
 #include "delta_seq.cuh"
+#include "lds_dma.cuh"
 #include "ssd_common.cuh"
 
 namespace ssmvjp {
@@ -41,16 +43,20 @@ struct DeltaChunkArgs {
   bf16 *o, *dq, *dk, *dv;
   float *Sf, *dbeta, *dg, *dS0;
   // workspace, all per (slot, value head)
-  bf16* Tf;   // [6][2][64][8] lower fragments of T, hi and lo
+  bf16* Tf;   // [6][2][64][8] lower fragments of T - I, hi and lo
   bf16* Pf;   // [6][64][8] lower fragments of scale P beta
   float* G;   // [64]
-  bf16* Tt;   // [6][2][64][8] fragments of T^T                      (backward from here on)
+  bf16* Tt;   // [6][2][64][8] fragments of T^T - I                  (backward from here on)
   bf16* Pt;   // [6][2][64][8] fragments of scale P^T
-  bf16 *Sh, *Sl, *dSh;          // [nvt][KP/32][64][8] fragments of the state before the chunk (two parts) and of
-                                // the state's gradient behind it
-  bf16 *rh, *rl, *muh, *mul;    // [nvt][2][64][8] fragments of r and mu (two parts each)
-  float* rowp;                  // [nvt][2][64] sums over a tile's columns, see delta_chunk_rev_kernel
-  float* endp;                  // [nvt]
+  // per 16-column tile (cell * nvt + tile):
+  bf16* Sw;     // [2][KP/32][64][8] fragments of the state before the chunk, hi and lo
+  bf16* rw;     // [2][2][64][8] fragments of r, hi and lo
+  float* Xw;    // [4][64][4] tiles of e^G K S0
+  bf16* dSw;    // [KP/32][64][8] fragments of the state's gradient behind the chunk, hi
+  bf16* muw;    // [2][2][64][8] fragments of mu, hi and lo
+  float* rowp;  // [3][64] sums over the tile's columns of scale e^G dO (Q S0), of the rest of dG_i's row terms,
+                // and of r dU
+  float* endp;  // [1] e^{G_63} <S0, dS> + sum_i su_i
 };
 
 typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
@@ -88,6 +94,13 @@ __device__ __forceinline__ void split8(const f32x4& x, const f32x4& y, Frag8& hi
   split4(y, hi.b, lo.b);
 }
 
+// x = hi + mid + lo up to 2^-24 |x|
+__device__ __forceinline__ void split8x3(const f32x4& x, const f32x4& y, Frag8& hi, Frag8& mid, Frag8& lo) {
+  hi.a = pack4(x);
+  hi.b = pack4(y);
+  split8(x - unpack4(hi.a), y - unpack4(hi.b), mid, lo);
+}
+
 // position of the fragment of row tile mt, contraction step s: lower triangular
 // (steps 0 .. mt / 2) and its transpose (steps mt / 2 .. 1)
 __device__ __forceinline__ constexpr int frag_lo(int mt, int s) { return mt < 2 ? mt : 2 * mt - 2 + s; }
@@ -103,59 +116,107 @@ __device__ __forceinline__ brsrc row_rsrc(const bf16* p, i64 tok0, int rows, i64
   return make_rsrc(p + (tok0 * heads + h) * cols, (unsigned)((((i64)rows - 1) * heads * cols + cols) * 2));
 }
 
-// The rows of a chunk on their way to LDS: registers <- memory (fetch), LDS <-
-// registers (commit), so that the loads of the next chunk are in flight while
-// this one is computed.  NT threads take part.
-template <int KP, int NT>
-struct RowTile {  // [64][KP] of q or k, swizzled rows, columns past K zero
-  static constexpr int N = 64 * KP / 8 / NT;
-  u32x4 r[N];
-  __device__ __forceinline__ void fetch(brsrc rs, int tid, i64 stride, i64 K) {
-#pragma unroll
-    for (int i = 0; i < N; ++i) {
-      const int p = tid + NT * i, row = p / (KP / 8), col = p % (KP / 8) * 8;
-      r[i] = bload16(rs, col < K ? (unsigned)((row * stride + col) * 2) : BUF_OOB);
-    }
-  }
-  __device__ __forceinline__ void commit(bf16* lds, int tid) const {
-#pragma unroll
-    for (int i = 0; i < N; ++i) {
-      const int p = tid + NT * i;
-      st16_xs(lds, KP, p / (KP / 8), p % (KP / 8) * 8, r[i]);
-    }
-  }
-};
-constexpr int VP = 36;  // row pitch of a staged [64][32] tile: 8-byte rows, shifted by 2 banks each
-template <int NT>
-struct ColTile {  // [64][32] of v or d_o, the columns from v0
-  static constexpr int N = 256 / NT;
-  u32x4 r[N];
-  __device__ __forceinline__ void fetch(brsrc rs, int tid, i64 stride, i64 v0, i64 V) {
-#pragma unroll
-    for (int i = 0; i < N; ++i) {
-      const int p = tid + NT * i, row = p / 4;
-      const i64 col = v0 + p % 4 * 8;
-      r[i] = bload16(rs, col < V ? (unsigned)((row * stride + col) * 2) : BUF_OOB);
-    }
-  }
-  __device__ __forceinline__ void commit(bf16* lds, int tid) const {
-    typedef unsigned u32x2 __attribute__((ext_vector_type(2)));
-#pragma unroll
-    for (int i = 0; i < N; ++i) {
-      const int p = tid + NT * i;
-      u32x2* d = (u32x2*)(lds + p / 4 * VP + p % 4 * 8);
-      d[0] = u32x2{r[i][0], r[i][1]};
-      d[1] = u32x2{r[i][2], r[i][3]};
-    }
-  }
-};
-// fragment of rows 16m .. 16m+15 of a swizzled row tile, contraction over its columns
-__device__ __forceinline__ Frag8 row_frag(const bf16* t, int KP, int m, int s, int lane) {
-  return {ld_colk_xs(t, KP, 16 * m, 32 * s, lane).v, ld_colk_xs(t, KP, 16 * m, 32 * s + 16, lane).v};
+// ---- row tiles in LDS ----
+// [64][KP] rows of q or k, no padding, columns past K zero.  The 16-byte unit u
+// of a row is stored at u ^ row_swz(row): eight consecutive rows of one unit
+// (a 16-byte fragment read) meet eight different units, four consecutive rows
+// of four units (a transposed read) all eight, twice each.
+__device__ __forceinline__ int row_swz(int row) { return ((row & 1) << 2) | ((row >> 1) & 3); }
+
+// Contraction over K.  A fragment of rows is 16 contiguous bytes: slot e of lane
+// group q <-> column 32s + 8q + e.  The state's tiles match it by their rows:
+// row 4q + r of tile 2s + b is key 32s + 8q + 4b + r.
+__device__ __forceinline__ int state_row(int tile, int q) { return 32 * (tile >> 1) + 8 * q + 4 * (tile & 1); }
+
+// a state [K][V] in memory (NULL, or a wave without columns: zeros): four rows of column v of tile t
+__device__ __forceinline__ brsrc state_rsrc(const float* S, const DeltaChunkArgs& a, i64 unit, bool act) {
+  const float* p = S + unit * a.K * a.V;
+  return make_rsrc(S ? p : S, S && act ? (unsigned)(a.K * a.V * 4) : 0u);
 }
-// fragment of columns 16t .. 16t+15, contraction over its rows
+__device__ __forceinline__ f32x4 load_state4(brsrc rs, const DeltaChunkArgs& a, int t, int q, i64 v) {
+  const int k = state_row(t, q);
+  f32x4 x;
+#pragma unroll
+  for (int r = 0; r < 4; ++r) x[r] = bload_f32(rs, k < a.K ? (unsigned)(((k + r) * a.V + v) * 4) : BUF_OOB);
+  return x;
+}
+
+// rows 16m .. 16m+15, contraction over the columns 32s .. 32s+31
+__device__ __forceinline__ Frag8 row_frag(const bf16* t, int KP, int m, int s, int lane) {
+  const int row = 16 * m + (lane & 15);
+  return as_frag(*(const u32x4*)(t + row * KP + (((4 * s + (lane >> 4)) ^ row_swz(row)) << 3)));
+}
+// the keys of state tile t as rows, contraction over the tokens 32s .. 32s+31 (slot order of the token fragments)
+__device__ __forceinline__ Frag8 key_frag(const bf16* x, int KP, int t, int s, int lane) {
+  const int m = lane & 15, row = 32 * s + 4 * (lane >> 4) + (m >> 2), u = 4 * (t >> 1) + (m & 3);
+  return {lds_tr_b16(x + row * KP + ((u ^ row_swz(row)) << 3) + 4 * (t & 1)).v,
+          lds_tr_b16(x + (row + 16) * KP + ((u ^ row_swz(row + 16)) << 3) + 4 * (t & 1)).v};
+}
+// columns 16t .. 16t+15 of a tile in the 8-byte swizzle, contraction over its rows 32s ..
 __device__ __forceinline__ Frag8 col_frag(const bf16* x, int pitch, int t, int s, int lane) {
   return {ld_rowk_xs(x, pitch, 32 * s, 16 * t, lane).v, ld_rowk_xs(x, pitch, 32 * s + 16, 16 * t, lane).v};
+}
+
+// rows 16m .. of such a tile, contraction over its columns in the token fragments' slot order
+__device__ __forceinline__ Frag8 xs_frag(const bf16* t, int pitch, int m, int s, int lane) {
+  return {ld_colk_xs(t, pitch, 16 * m, 32 * s, lane).v, ld_colk_xs(t, pitch, 16 * m, 32 * s + 16, lane).v};
+}
+
+// LDS-direct loads of one chunk's tiles, shared out over NW waves, 1 KB (64
+// pieces of 16 bytes) an instruction.  A wave's instructions are consecutive,
+// so that the swizzle depends on the lane and the instruction's parity only.
+template <int KP, int NW>
+struct RowDma {
+  static constexpr int N = KP / 8 / NW, VAR = KP == 128 ? 2 : 1;  // instructions a wave; rows 4 or 8 an instruction
+  unsigned off[VAR], step;
+  __device__ __forceinline__ void init(int w, int lane, i64 stride, i64 K) {
+#pragma unroll
+    for (int j = 0; j < VAR; ++j) {
+      const int p = 64 * (N * w + j) + lane, row = p / (KP / 8), col = ((p % (KP / 8)) ^ row_swz(row)) * 8;
+      off[j] = col < K ? (unsigned)((row * stride + col) * 2) : BUF_OOB;
+    }
+    step = (unsigned)(8 * stride * 2);
+  }
+  __device__ __forceinline__ void issue(unsigned lds, int w, u32x4 rs) const {
+#pragma unroll
+    for (int j = 0; j < N; ++j)
+      dma_dwordx4(lds + 1024u * (unsigned)(N * w + j), off[j % VAR] + (unsigned)(j / VAR) * step, rs);
+  }
+};
+// [64][16 NT] of v or d_o, the columns from v0 (zero past V)
+template <int NT, int NW>
+struct ColDma {
+  static constexpr int N = 2 * NT / NW;
+  unsigned off[N];
+  __device__ __forceinline__ void init(int w, int lane, i64 stride, i64 v0, i64 V) {
+#pragma unroll
+    for (int j = 0; j < N; ++j) {
+      const int p = 64 * (N * w + j) + lane, row = p / (2 * NT);
+      const i64 col = p % (2 * NT) * 8;
+      off[j] = v0 + col < V ? (unsigned)((row * stride + col) * 2) : BUF_OOB;
+    }
+  }
+  __device__ __forceinline__ void issue(unsigned lds, int w, u32x4 rs) const {
+#pragma unroll
+    for (int j = 0; j < N; ++j) dma_dwordx4(lds + 1024u * (unsigned)(N * w + j), off[j], rs);
+  }
+};
+// N KB as they are
+template <int N, int NW>
+__device__ __forceinline__ void flat_dma(unsigned lds, int w, int lane, u32x4 rs) {
+#pragma unroll
+  for (int i = 0; i < N; i += NW)
+    if (N % NW == 0 || i + w < N) dma_dwordx4(lds + 1024u * (unsigned)(i + w), (unsigned)((i + w) * 1024 + lane * 16), rs);
+}
+// four values down column 16w + c of a [64][16 NW] tile: rows 16m + 4q ..
+__device__ __forceinline__ s16x4 col4(const bf16* t, int pitch, int m, int w, int lane) {
+  return ld_rowk(t, pitch, 16 * m, 16 * w, lane).v;
+}
+
+// words of a resource over the rows [tok0, tok0 + rows) of head h of a [tokens][heads][cols] tensor, from column
+// col0 (rows past the end read as zeros)
+__device__ __forceinline__ u32x4 row_words(const bf16* p, i64 tok0, int rows, i64 heads, i64 h, i64 cols, i64 col0) {
+  return rsrc_words_u(p + (tok0 * heads + h) * cols + col0, (unsigned)((((i64)rows - 1) * heads * cols + cols - col0) * 2));
 }
 
 struct ChunkAt {

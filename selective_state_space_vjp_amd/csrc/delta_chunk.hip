@@ -14,8 +14,10 @@
 // Walk.  Columns of the state are independent, so a wave owns 16 columns of one
 // head for a whole sequence, with the state in its accumulators, and nothing is
 // exchanged between waves: r, u and the next state come out of the MFMAs in the
-// layout that the following MFMA wants.  Two waves share a workgroup and the
-// K, Q, V rows in LDS, double-buffered: one barrier per chunk.
+// layout that the following MFMA wants.  The waves of a workgroup share the
+// chunk's K, Q, V rows and fragments in LDS.  LDS-direct loads bring the next
+// chunk's while this one is computed (two buffers): one barrier per chunk, no
+// load in the chain that leads from one state to the next.
 #include "delta_chunk.cuh"
 
 namespace ssmvjp {
@@ -195,14 +197,20 @@ __global__ void __launch_bounds__(256) delta_prep_kernel(DeltaChunkArgs a) {
     }
     __syncthreads();
     invert64(As, Ts, w, lane);
-    // T: lane row i = 16 w + c, columns 16 b + 4 q + r; blocks above the diagonal are zero
+    // T - I: lane row i = 16 w + c, columns 16 b + 4 q + r; blocks above the diagonal are zero
+    auto off_diag = [&](f32x4 x, int col) {
+#pragma unroll
+      for (int r = 0; r < 4; ++r)
+        if (col + r == row) x[r] = 0.0f;
+      return x;
+    };
 #pragma unroll
     for (int s = 0; s < 2; ++s)
       if (s <= w >> 1) {
         const f32x4 x = *(const f32x4*)(Ts + row * TP + 32 * s + 4 * q);
         const f32x4 y = 2 * s + 1 <= w ? *(const f32x4*)(Ts + row * TP + 32 * s + 16 + 4 * q) : zero4();
         Frag8 hi, lo;
-        split8(x, y, hi, lo);
+        split8(off_diag(x, 32 * s + 4 * q), off_diag(y, 32 * s + 16 + 4 * q), hi, lo);
         u32x4* f = (u32x4*)(a.Tf + ((unit * 6 + frag_lo(w, s)) * 2 * 64 + lane) * 8);
         f[0] = as_u4(hi);
         f[64] = as_u4(lo);
@@ -218,7 +226,7 @@ __global__ void __launch_bounds__(256) delta_prep_kernel(DeltaChunkArgs a) {
             y[r] = Ts[(32 * s + 16 + 4 * q + r) * TP + row];
           }
           Frag8 hi, lo;
-          split8(x, y, hi, lo);
+          split8(off_diag(x, 32 * s + 4 * q), off_diag(y, 32 * s + 16 + 4 * q), hi, lo);
           u32x4* f = (u32x4*)(a.Tt + ((unit * 6 + frag_up(w, s)) * 2 * 64 + lane) * 8);
           f[0] = as_u4(hi);
           f[64] = as_u4(lo);
@@ -230,177 +238,308 @@ __global__ void __launch_bounds__(256) delta_prep_kernel(DeltaChunkArgs a) {
 // ---------------------------------------------------------------------------
 // walk
 // ---------------------------------------------------------------------------
-constexpr int WNT = 128;  // threads of a walk's workgroup
-
-// MODE 0: the forward (o, S_final); 1: the states before every chunk, for the backward
+// MODE 0: the forward (o, S_final); 1: for the backward, the state before every
+// chunk, r, e^G K S0 and the readout's row sums.
+//
+// Five waves for 32 columns.  Waves 0 and 1 carry the states of 16 columns each
+// and do nothing that the next state does not wait for.  Waves 2 and 3 follow
+// one chunk behind with what is left of the same columns (the readout, or what
+// the backward keeps) from the state's fragments and r, which they get through
+// LDS.  Wave 4 sends for the next chunks' data and prepares the gates.  One wave
+// that does all of it takes 7,600 cycles a chunk at K = 128, 2,000 of them for
+// the readout and 1,100 for issuing the loads.
 template <int KP, int MODE>
-__global__ void __launch_bounds__(WNT, 1) delta_chunk_walk_kernel(DeltaChunkArgs a) {
-  constexpr int KS = KP / 32, KT = KP / 16;       // 32-steps and 16-tiles of K
+struct WalkLds {  // byte offsets
+  static constexpr int K = 0, V = K + 64 * KP * 2, T = V + 4096, ABUF = T + 12 * 1024;        // for waves 0, 1
+  static constexpr int Q = 0, PO = Q + 64 * KP * 2, BBUF = PO + (MODE ? 4096 : 6 * 1024);     // for waves 2, 3
+  static constexpr int B = 2 * ABUF, S = B + 2 * BBUF, SBUF = 2 * KP * 64, R = S + 2 * SBUF;  // S, r: [2 buffers][2 tiles]
+  static constexpr int G = R + 2 * 2 * 4096, TOTAL = G + 3 * 512;                             // gates: [3][e^G, e^{G_63 - G} beta]
+};
+
+// no instruction moves past here: operands that are read ahead stay ahead
+#define SSMVJP_FENCE() __builtin_amdgcn_sched_barrier(0)
+
+constexpr int WALK_NTH = 320;
+
+template <int KP, int MODE>
+__global__ void __launch_bounds__(WALK_NTH) __attribute__((amdgpu_waves_per_eu(2, 2)))
+delta_chunk_walk_kernel(DeltaChunkArgs a) {
+  constexpr int KS = KP / 32, KT = KP / 16;  // 32-steps and 16-tiles of K
   constexpr bool FWD = MODE == 0;
-  __shared__ __attribute__((aligned(16))) bf16 Kb[2][64 * KP];
-  __shared__ __attribute__((aligned(16))) bf16 Qb[FWD ? 2 : 1][FWD ? 64 * KP : 8];
-  __shared__ __attribute__((aligned(16))) bf16 Vb[2][64 * VP];
-  __shared__ __attribute__((aligned(16))) float eGs[2][64], wBs[2][64];  // e^G; e^{G_63 - G} beta
-  const int tid = threadIdx.x, lane = tid & 63, w = tid >> 6, c = lane & 15, q = lane >> 4;
+  typedef WalkLds<KP, MODE> L;
+  extern __shared__ __align__(16) unsigned char smem_raw[];
+  const int lane = threadIdx.x & 63, w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), c = lane & 15, q = lane >> 4;
+  const int t16 = w & 1;  // this wave's column tile of the two
   i64 unit, slice;
   if (!walk_unit(a.seq.nseq * a.HV, (a.V + 31) / 32, unit, slice)) return;
   const i64 n = unit / a.HV, hv = unit % a.HV, h = hv / a.rep;
   const DeltaSpan sp = a.seq.span(n);
-  const i64 nch = (sp.len + DCH - 1) / DCH;
-  const i64 v0 = slice * 32 + w * 16;  // this wave's first column
-  const bool act = v0 < a.V;           // V is a multiple of 16: all of a wave's columns or none
+  const int nch = (int)((sp.len + DCH - 1) / DCH);
+  const i64 v0 = slice * 32 + t16 * 16, vt = slice * 2 + t16;
+  const bool act = v0 < a.V;  // V is a multiple of 16: all of a wave's columns or none
+  const i64 cell0 = sp.slot0 * a.HV + hv;  // chunk ch: cell0 + ch * HV
+  auto gates = [&](int ch) { return (float*)(smem_raw + L::G + ch % 3 * 512); };
+  auto at4 = [&](const float* p, int m) { return *(const f32x4*)(p + 16 * m + 4 * q); };
 
-  RowTile<KP, WNT> sk, sq;
-  ColTile<WNT> sv;
-  float sG = 0.0f, sB = 0.0f;
-  auto fetch = [&](i64 ch) {
-    const i64 tok0 = sp.start + ch * DCH;
-    const int rows = (int)(sp.len - ch * DCH < DCH ? sp.len - ch * DCH : DCH);
-    sk.fetch(row_rsrc(a.k, tok0, rows, a.H, h, a.K), tid, a.H * a.K, a.K);
-    if constexpr (FWD) sq.fetch(row_rsrc(a.q, tok0, rows, a.H, h, a.K), tid, a.H * a.K, a.K);
-    sv.fetch(row_rsrc(a.v, tok0, rows, a.HV, hv, a.V), tid, a.HV * a.V, slice * 32, a.V);
-    if (w == 0) {
-      sG = a.G[((sp.slot0 + ch) * a.HV + hv) * 64 + lane];
-      sB = lane < rows ? a.beta[(tok0 + lane) * a.HV + hv] : 0.0f;
-    }
-  };
-  auto commit = [&](int bf) {
-    sk.commit(Kb[bf], tid);
-    if constexpr (FWD) sq.commit(Qb[bf], tid);
-    sv.commit(Vb[bf], tid);
-    if (w == 0) {
-      const float end = __shfl(sG, 63, 64);
-      eGs[bf][lane] = exp_hw(sG);
-      wBs[bf][lane] = exp_hw(end - sG) * sB;
-    }
-  };
-
-  f32x4 S[KT];
+  if (w < 2) {
+    // ---------------------------------------------------------------- the state
+    f32x4 S[KT];
+    Frag8 sh[KS], sl[KS];  // its two parts
+    const brsrc rs = state_rsrc(a.S0, a, unit, act);
 #pragma unroll
-  for (int t = 0; t < KT; ++t) {
-    S[t] = zero4();
-    if (a.S0 && act) {
+    for (int t = 0; t < KT; ++t) S[t] = load_state4(rs, a, t, q, v0 + c);
 #pragma unroll
-      for (int r = 0; r < 4; ++r) {
-        const int k = 16 * t + 4 * q + r;
-        if (k < a.K) S[t][r] = a.S0[(unit * a.K + k) * a.V + v0 + c];
-      }
-    }
-  }
-  if (nch > 0) {
-    fetch(0);
-    commit(0);
-  }
-  __syncthreads();
-  for (i64 ch = 0; ch < nch; ++ch) {
-    const int bf = ch & 1;
-    const i64 cu = (sp.slot0 + ch) * a.HV + hv;
-    u32x4 tf[6][2], pf[FWD ? 6 : 1];
-    if (act) {
+    for (int s = 0; s < KS; ++s) split8(S[2 * s], S[2 * s + 1], sh[s], sl[s]);
+    __syncthreads();
+    for (int ch = 0; ch < nch; ++ch) {
+      const int bf = ch & 1;
+      if (act) {
+        const unsigned char* const buf = smem_raw + bf * L::ABUF;
+        const bf16 *Kt = (const bf16*)(buf + L::K), *Vt = (const bf16*)(buf + L::V);
+        const u32x4* Tf = (const u32x4*)(buf + L::T) + lane;
+        u32x4* So = (u32x4*)(smem_raw + L::S + bf * L::SBUF + t16 * (L::SBUF / 2)) + lane;
+        f32x4* Ro = (f32x4*)(smem_raw + L::R + (bf * 2 + t16) * 4096) + lane;
+        const float *eG = gates(ch), *wB = eG + 64;
+        // K S0, both parts of S0
+        Frag8 kf[KS][4];
 #pragma unroll
-      for (int i = 0; i < 6; ++i) {
-        const u32x4* f = (const u32x4*)(a.Tf + (cu * 6 + i) * 2 * 64 * 8) + lane;
-        tf[i][0] = f[0];
-        tf[i][1] = f[64];
-        if constexpr (FWD) pf[i] = ((const u32x4*)(a.Pf + (cu * 6 + i) * 64 * 8))[lane];
-      }
-    }
-    if (ch + 1 < nch) fetch(ch + 1);
-    if (act) {
-      const bf16* Kt = Kb[bf];
-      const bf16* Qt = Qb[FWD ? bf : 0];
-      // K S0 (two parts of S0) and (Q S0)^T (one part)
-      f32x4 x[4], ot[4];
+        for (int s = 0; s < 2; ++s)
 #pragma unroll
-      for (int m = 0; m < 4; ++m) x[m] = zero4(), ot[m] = zero4();
+          for (int m = 0; m < 4; ++m) kf[s][m] = row_frag(Kt, KP, m, s, lane);
+        SSMVJP_FENCE();
+        f32x4 x[4], e[4];
+        s16x4 v[4];
 #pragma unroll
-      for (int s = 0; s < KS; ++s) {
-        Frag8 hi, lo;
-        split8(S[2 * s], S[2 * s + 1], hi, lo);
-        if constexpr (!FWD) {
-          const i64 o = (((cu * a.nvt + slice * 2 + w) * KS + s) * 64 + lane) * 8;
-          *(u32x4*)(a.Sh + o) = as_u4(hi);
-          *(u32x4*)(a.Sl + o) = as_u4(lo);
+        for (int m = 0; m < 4; ++m) x[m] = zero4();
+#pragma unroll
+        for (int s = 0; s < KS; ++s) {
+          // under these products: the fragments two steps on, then V and e^G, and the state's parts to the follower
+          if (s + 2 < KS) {
+#pragma unroll
+            for (int m = 0; m < 4; ++m) kf[s + 2][m] = row_frag(Kt, KP, m, s + 2, lane);
+          } else if (s + 2 == KS) {
+#pragma unroll
+            for (int m = 0; m < 4; ++m) v[m] = col4(Vt, 32, m, t16, lane), e[m] = at4(eG, m);
+          }
+          So[s * 64] = as_u4(sh[s]);
+          So[(KS + s) * 64] = as_u4(sl[s]);
+#pragma unroll
+          for (int m = 0; m < 4; ++m) x[m] = mma32(kf[s][m], sl[s], x[m]);
+#pragma unroll
+          for (int m = 0; m < 4; ++m) x[m] = mma32(kf[s][m], sh[s], x[m]);
+          SSMVJP_FENCE();
         }
+        Frag8 th[6], tl[6];
+#pragma unroll
+        for (int i = 0; i < 6; ++i) th[i] = as_frag(Tf[i * 128]), tl[i] = as_frag(Tf[i * 128 + 64]);
+        SSMVJP_FENCE();
+        // V - e^G K S0
+        f32x4* X = (f32x4*)(a.Xw + ((cell0 + ch * a.HV) * a.nvt + vt) * 1024) + lane;
 #pragma unroll
         for (int m = 0; m < 4; ++m) {
-          const Frag8 kf = row_frag(Kt, KP, m, s, lane);
-          x[m] = mma32(kf, hi, x[m]);
-          x[m] = mma32(kf, lo, x[m]);
-          if constexpr (FWD) {
-            const Frag8 qf = row_frag(Qt, KP, m, s, lane);
-            ot[m] = mma32(hi, qf, ot[m]);
+          x[m] *= e[m];
+          if constexpr (!FWD) X[m * 64] = x[m];
+          x[m] = unpack4(v[m]) - x[m];
+        }
+        Frag8 xh[2], xl[2];
+#pragma unroll
+        for (int s = 0; s < 2; ++s) split8(x[2 * s], x[2 * s + 1], xh[s], xl[s]);
+        // r = T (V - e^G K S0), row tiles in turn
+#pragma unroll
+        for (int s = 0; s < 2; ++s) {
+#pragma unroll
+          for (int m = 2 * s; m < 4; ++m) x[m] = mma32(th[frag_lo(m, s)], xl[s], x[m]);
+#pragma unroll
+          for (int m = 2 * s; m < 4; ++m) x[m] = mma32(tl[frag_lo(m, s)], xh[s], x[m]);
+#pragma unroll
+          for (int m = 2 * s; m < 4; ++m) x[m] = mma32(th[frag_lo(m, s)], xh[s], x[m]);
+        }
+        // under those: the keys by column, the decay of the state
+        Frag8 ct[2][KT];
+#pragma unroll
+        for (int t = 0; t < KT; ++t) ct[0][t] = key_frag(Kt, KP, t, 0, lane);
+        f32x4 wb[4];
+#pragma unroll
+        for (int m = 0; m < 4; ++m) wb[m] = at4(wB, m);
+        const float eEnd = eG[63];
+#pragma unroll
+        for (int t = 0; t < KT; ++t) S[t] *= eEnd;
+        SSMVJP_FENCE();
+        // S = e^{G_63} S0 + K^T (e^{G_63 - G} beta r), u in three parts
+#pragma unroll
+        for (int m = 0; m < 4; ++m) Ro[m * 64] = x[m];
+#pragma unroll
+        for (int s = 0; s < 2; ++s) {
+          Frag8 uh, um, ul;
+          split8x3(x[2 * s] * wb[2 * s], x[2 * s + 1] * wb[2 * s + 1], uh, um, ul);
+          if (s == 0) {
+#pragma unroll
+            for (int t = 0; t < KT; ++t) ct[1][t] = key_frag(Kt, KP, t, 1, lane);
+          }
+#pragma unroll
+          for (int t = 0; t < KT; ++t) S[t] = mma32(ct[s][t], ul, S[t]);
+#pragma unroll
+          for (int t = 0; t < KT; ++t) S[t] = mma32(ct[s][t], um, S[t]);
+#pragma unroll
+          for (int t = 0; t < KT; ++t) S[t] = mma32(ct[s][t], uh, S[t]);
+        }
+#pragma unroll
+        for (int s = 0; s < KS; ++s) split8(S[2 * s], S[2 * s + 1], sh[s], sl[s]);
+      }
+      __syncthreads();
+    }
+    __syncthreads();  // the period in which the followers finish the last chunk
+    if (FWD && a.Sf && act) {
+#pragma unroll
+      for (int t = 0; t < KT; ++t)
+#pragma unroll
+        for (int r = 0; r < 4; ++r) {
+          const int k = state_row(t, q) + r;
+          if (k < a.K) a.Sf[(unit * a.K + k) * a.V + v0 + c] = S[t][r];
+        }
+    }
+  } else if (w < 4) {
+    // ------------------------------------------------------------ the followers
+    __syncthreads();
+    for (int p = 0; p <= nch; ++p) {  // chunk p - 1 here, chunk p at the states
+      if (act && p > 0) {
+        const int ch = p - 1, bf = ch & 1;
+        const i64 tile = (cell0 + ch * a.HV) * a.nvt + vt;
+        const unsigned char* const buf = smem_raw + L::B + bf * L::BBUF;
+        const bf16* Qt = (const bf16*)(buf + L::Q);
+        const u32x4* So = (const u32x4*)(smem_raw + L::S + bf * L::SBUF + t16 * (L::SBUF / 2)) + lane;
+        const f32x4* Ro = (const f32x4*)(smem_raw + L::R + (bf * 2 + t16) * 4096) + lane;
+        const float* eG = gates(ch);
+        // Q S0 (the forward: its transpose), both parts of S0
+        u32x4 h4[KS], l4[KS];
+        Frag8 qf[KS][4];
+#pragma unroll
+        for (int s = 0; s < KS; ++s) {
+          h4[s] = So[s * 64];
+          l4[s] = So[(KS + s) * 64];
+#pragma unroll
+          for (int m = 0; m < 4; ++m) qf[s][m] = row_frag(Qt, KP, m, s, lane);
+        }
+        SSMVJP_FENCE();
+        f32x4 y[4];
+#pragma unroll
+        for (int m = 0; m < 4; ++m) y[m] = zero4();
+#pragma unroll
+        for (int s = 0; s < KS; ++s) {
+          const Frag8 hi = as_frag(h4[s]), lo = as_frag(l4[s]);
+#pragma unroll
+          for (int m = 0; m < 4; ++m) y[m] = FWD ? mma32(lo, qf[s][m], y[m]) : mma32(qf[s][m], lo, y[m]);
+#pragma unroll
+          for (int m = 0; m < 4; ++m) y[m] = FWD ? mma32(hi, qf[s][m], y[m]) : mma32(qf[s][m], hi, y[m]);
+          if constexpr (!FWD) {
+            u32x4* o = (u32x4*)(a.Sw + tile * 2 * KS * 512) + s * 64 + lane;
+            o[0] = h4[s];
+            o[KS * 64] = l4[s];
+          }
+        }
+        Frag8 rh[2], rl[2];
+#pragma unroll
+        for (int s = 0; s < 2; ++s) split8(Ro[2 * s * 64], Ro[(2 * s + 1) * 64], rh[s], rl[s]);
+        if constexpr (FWD) {
+          // O^T = scale e^G (Q S0)^T + r^T (scale P beta)^T
+          Frag8 pf[6];
+#pragma unroll
+          for (int i = 0; i < 6; ++i) pf[i] = as_frag(((const u32x4*)(buf + L::PO))[i * 64 + lane]);
+          float e[4];
+#pragma unroll
+          for (int m = 0; m < 4; ++m) e[m] = a.scale * eG[16 * m + c];
+          SSMVJP_FENCE();
+#pragma unroll
+          for (int m = 0; m < 4; ++m) y[m] *= e[m];
+#pragma unroll
+          for (int s = 0; s < 2; ++s) {
+#pragma unroll
+            for (int m = 2 * s; m < 4; ++m) y[m] = mma32(rl[s], pf[frag_lo(m, s)], y[m]);
+#pragma unroll
+            for (int m = 2 * s; m < 4; ++m) y[m] = mma32(rh[s], pf[frag_lo(m, s)], y[m]);
+          }
+          const i64 row0 = (i64)ch * DCH + c;
+          bf16* o = a.o + ((sp.start + row0) * a.HV + hv) * a.V + v0 + 4 * q;
+#pragma unroll
+          for (int m = 0; m < 4; ++m)
+            if (row0 + 16 * m < sp.len) *(s16x4*)(o + 16 * m * a.HV * a.V) = pack4(y[m]);
+        } else {
+          u32x4* o = (u32x4*)(a.rw + tile * 4 * 512) + lane;
+#pragma unroll
+          for (int s = 0; s < 2; ++s) o[s * 64] = as_u4(rh[s]), o[128 + s * 64] = as_u4(rl[s]);
+          const bf16* Ot = (const bf16*)(buf + L::PO);
+          float* rp = a.rowp + tile * 3 * 64;
+#pragma unroll
+          for (int m = 0; m < 4; ++m) {
+            f32x4 t = a.scale * at4(eG, m) * unpack4(col4(Ot, 32, m, t16, lane)) * y[m];
+#pragma unroll
+            for (int r = 0; r < 4; ++r) t[r] = sum16(t[r]);
+            if (c == 0) *(f32x4*)(rp + 16 * m + 4 * q) = t;
           }
         }
       }
-      // V - e^G K S0
-#pragma unroll
-      for (int m = 0; m < 4; ++m) {
-        const f32x4 v = unpack4(ld_rowk(Vb[bf], VP, 16 * m, 16 * w, lane).v);
-        const f32x4 e = *(const f32x4*)(eGs[bf] + 16 * m + 4 * q);
-        x[m] = v - e * x[m];
-      }
-      Frag8 xh[2], xl[2];
-#pragma unroll
-      for (int s = 0; s < 2; ++s) split8(x[2 * s], x[2 * s + 1], xh[s], xl[s]);
-      // r = T (V - e^G K S0)
-      f32x4 r[4];
-#pragma unroll
-      for (int m = 0; m < 4; ++m) {
-        r[m] = zero4();
-#pragma unroll
-        for (int s = 0; s <= m / 2; ++s) {
-          const Frag8 th = as_frag(tf[frag_lo(m, s)][0]), tl = as_frag(tf[frag_lo(m, s)][1]);
-          r[m] = mma32(th, xl[s], r[m]);
-          r[m] = mma32(tl, xh[s], r[m]);
-          r[m] = mma32(th, xh[s], r[m]);
-        }
-      }
-      // O^T = scale e^G (Q S0)^T + r^T (scale P beta)^T
-      if constexpr (FWD) {
-        const i64 tok0 = sp.start + ch * DCH;
-        const i64 left = sp.len - ch * DCH;
-        const Frag8 rf[2] = {{pack4(r[0]), pack4(r[1])}, {pack4(r[2]), pack4(r[3])}};
-#pragma unroll
-        for (int m = 0; m < 4; ++m) {
-          const float e = a.scale * eGs[bf][16 * m + c];
-          ot[m] *= e;
-#pragma unroll
-          for (int s = 0; s <= m / 2; ++s) ot[m] = mma32(rf[s], as_frag(pf[frag_lo(m, s)]), ot[m]);
-          if (16 * m + c < left)
-            *(s16x4*)(a.o + ((tok0 + 16 * m + c) * a.HV + hv) * a.V + v0 + 4 * q) = pack4(ot[m]);
-        }
-      }
-      // S = e^{G_63} S0 + K^T (e^{G_63 - G} beta r)
-      const float eEnd = eGs[bf][63];
-#pragma unroll
-      for (int m = 0; m < 4; ++m) r[m] *= *(const f32x4*)(wBs[bf] + 16 * m + 4 * q);
-      Frag8 uh[2], ul[2];
-#pragma unroll
-      for (int s = 0; s < 2; ++s) split8(r[2 * s], r[2 * s + 1], uh[s], ul[s]);
-#pragma unroll
-      for (int t = 0; t < KT; ++t) {
-        S[t] *= eEnd;
-#pragma unroll
-        for (int s = 0; s < 2; ++s) {
-          const Frag8 kf = col_frag(Kt, KP, t, s, lane);
-          S[t] = mma32(kf, ul[s], S[t]);
-          S[t] = mma32(kf, uh[s], S[t]);
-        }
-      }
+      __syncthreads();
     }
-    if (ch + 1 < nch) commit(bf ^ 1);
+  } else {
+    // --------------------------------------------------------------- the loader
+    const unsigned lds0 = lds_base(smem_raw);
+    RowDma<KP, 1> rows_dma;
+    ColDma<2, 1> cols_dma;
+    rows_dma.init(0, lane, a.H * a.K, a.K);
+    cols_dma.init(0, lane, a.HV * a.V, slice * 32, a.V);
+    auto rows_of = [&](int ch) { return (int)(sp.len - (i64)ch * DCH < DCH ? sp.len - (i64)ch * DCH : DCH); };
+    auto issue_a = [&](int ch) {  // k, v and T of chunk ch
+      const unsigned b = lds0 + (unsigned)((ch & 1) * L::ABUF);
+      const i64 tok0 = sp.start + (i64)ch * DCH;
+      rows_dma.issue(b + L::K, 0, row_words(a.k, tok0, rows_of(ch), a.H, h, a.K, 0));
+      cols_dma.issue(b + L::V, 0, row_words(a.v, tok0, rows_of(ch), a.HV, hv, a.V, slice * 32));
+      flat_dma<12, 1>(b + L::T, 0, lane, rsrc_words_u(a.Tf + (cell0 + ch * a.HV) * 6 * 2 * 512, 12 * 1024));
+    };
+    auto issue_b = [&](int ch) {  // q and P, or q and d_o
+      const unsigned b = lds0 + (unsigned)(L::B + (ch & 1) * L::BBUF);
+      const i64 tok0 = sp.start + (i64)ch * DCH;
+      rows_dma.issue(b + L::Q, 0, row_words(a.q, tok0, rows_of(ch), a.H, h, a.K, 0));
+      if constexpr (FWD) flat_dma<6, 1>(b + L::PO, 0, lane, rsrc_words_u(a.Pf + (cell0 + ch * a.HV) * 6 * 512, 6 * 1024));
+      else cols_dma.issue(b + L::PO, 0, row_words(a.d_o, tok0, rows_of(ch), a.HV, hv, a.V, slice * 32));
+    };
+    float sG = 0.0f, sB = 0.0f;
+    auto fetch_gates = [&](int ch) {
+      sG = a.G[(cell0 + ch * a.HV) * 64 + lane];
+      const i64 t = (i64)ch * DCH + lane;
+      sB = t < sp.len ? a.beta[(sp.start + t) * a.HV + hv] : 0.0f;
+    };
+    auto commit_gates = [&](int ch) {
+      float* g = gates(ch);
+      const float end = __shfl(sG, 63, 64);
+      g[lane] = exp_hw(sG);
+      g[64 + lane] = exp_hw(end - sG) * sB;
+    };
+    if (nch > 0) {
+      fetch_gates(0);
+      issue_a(0);
+      commit_gates(0);
+    }
+    dma_wait();
     __syncthreads();
-  }
-  if (FWD && a.Sf && act) {
-#pragma unroll
-    for (int t = 0; t < KT; ++t)
-#pragma unroll
-      for (int r = 0; r < 4; ++r) {
-        const int k = 16 * t + 4 * q + r;
-        if (k < a.K) a.Sf[(unit * a.K + k) * a.V + v0 + c] = S[t][r];
+    for (int p = 0; p <= nch; ++p) {
+      const bool more = p + 1 < nch;
+      if (more) {
+        fetch_gates(p + 1);
+        issue_a(p + 1);
       }
+      if (p < nch) issue_b(p);
+      if (more) commit_gates(p + 1);
+      dma_wait();
+      __syncthreads();
+    }
   }
+}
+
+template <int MODE>
+void launch_walk(const DeltaChunkArgs& a, hipStream_t s) {
+  const dim3 grid((unsigned)walk_blocks(a.seq.nseq * a.HV, (a.V + 31) / 32)), wg(WALK_NTH);
+  if (a.K <= 64) hipLaunchKernelGGL((delta_chunk_walk_kernel<64, MODE>), grid, wg, (WalkLds<64, MODE>::TOTAL), s, a);
+  else hipLaunchKernelGGL((delta_chunk_walk_kernel<128, MODE>), grid, wg, (WalkLds<128, MODE>::TOTAL), s, a);
 }
 
 // workspace of the forward: T and P fragments and G of every (slot, value head)
@@ -438,9 +577,7 @@ hipError_t launch_delta_prep(const DeltaChunkArgs& a, bool backward, hipStream_t
 }
 
 hipError_t launch_delta_states(const DeltaChunkArgs& a, hipStream_t stream) {
-  const dim3 grid((unsigned)walk_blocks(a.seq.nseq * a.HV, (a.V + 31) / 32)), wg(WNT);
-  if (a.K <= 64) hipLaunchKernelGGL((delta_chunk_walk_kernel<64, 1>), grid, wg, 0, stream, a);
-  else hipLaunchKernelGGL((delta_chunk_walk_kernel<128, 1>), grid, wg, 0, stream, a);
+  launch_walk<1>(a, stream);
   return hipGetLastError();
 }
 
@@ -472,9 +609,7 @@ hipError_t launch_delta_fwd(const ssmvjp_delta_chunk_desc& d, const DeltaChunkPo
     const hipError_t e = launch_delta_prep(a, false, stream);
     if (e != hipSuccess) return e;
   }
-  const dim3 grid((unsigned)walk_blocks(a.seq.nseq * a.HV, (a.V + 31) / 32)), wg(WNT);
-  if (a.K <= 64) hipLaunchKernelGGL((delta_chunk_walk_kernel<64, 0>), grid, wg, 0, stream, a);
-  else hipLaunchKernelGGL((delta_chunk_walk_kernel<128, 0>), grid, wg, 0, stream, a);
+  launch_walk<0>(a, stream);
   return hipGetLastError();
 }
 

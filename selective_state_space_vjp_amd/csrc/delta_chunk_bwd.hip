@@ -20,219 +20,210 @@
 // and dg comes out at about 6e-6.  dq and dk are bf16: one part is enough.
 //
 // Four launches: delta_prep_kernel (T, T^T, scale P^T of every chunk),
-// delta_chunk_walk_kernel<., 1> (the state before every chunk),
+// delta_chunk_walk_kernel<., 1> (the state before every chunk, r),
 // delta_chunk_rev_kernel (the reverse walk, 16 columns per wave as the forward:
-// dv, r, dS, row sums over its columns) and delta_chunk_grads_kernel (all
-// chunks at once: dq, dk summed over the value heads of a qk head, dg, dbeta).
+// mu, dS, row sums over its columns) and delta_chunk_grads_kernel (all chunks at
+// once: dv, dq, dk summed over the value heads of a qk head, dg, dbeta).
 #include "delta_chunk.cuh"
 
 namespace ssmvjp {
 namespace {
 
-constexpr int WNT = 128;
-
 // ---------------------------------------------------------------------------
 // reverse walk
 // ---------------------------------------------------------------------------
-// rowp[0][i] = this tile's part of dG_i's row terms (all but the M sums),
-// rowp[1][i] = r_i . dU_i,  endp = e^{G_63} <S0, dS> + sum_i su_i
-template <int KP>
-__global__ void __launch_bounds__(WNT, 1) delta_chunk_rev_kernel(DeltaChunkArgs a) {
-  constexpr int KS = KP / 32, KT = KP / 16;
-  __shared__ __attribute__((aligned(16))) bf16 Kb[2][64 * KP];
-  __shared__ __attribute__((aligned(16))) bf16 Qb[2][64 * KP];
-  __shared__ __attribute__((aligned(16))) bf16 Vb[2][64 * VP];
-  __shared__ __attribute__((aligned(16))) bf16 Ob[2][64 * VP];
-  __shared__ __attribute__((aligned(16))) float eGs[2][64], eEs[2][64], Bs[2][64];  // e^G, e^{G_63 - G}, beta
-  const int tid = threadIdx.x, lane = tid & 63, w = tid >> 6, c = lane & 15, q = lane >> 4;
+// The chunk's q, k, d_o rows and the fragments of T^T and P^T come as in the
+// forward walk, by LDS-direct loads into the other of two buffers while a chunk
+// is computed.  What belongs to one wave's columns (S0, e^G K S0, r) has one
+// buffer per wave: it is read early in a chunk, and the wave then sends for the
+// next chunk's.
+template <int KP, int NW>
+struct RevLds {
+  static constexpr int KS = KP / 32;
+  static constexpr int K = 0, Q = K + 64 * KP * 2, O = Q + 64 * KP * 2, T = O + 2048 * NW, P = T + 12 * 1024,
+                       BUF = P + 12 * 1024;
+  static constexpr int S = 2 * BUF, X = 2 * KS * 1024, R = X + 4096, OWN = R + 4096;  // per wave: X, R inside it
+  static constexpr int G = S + NW * OWN, TOTAL = G + 6 * 256;
+};
+
+template <int KP, int NW>
+__global__ void __launch_bounds__(64 * NW) __attribute__((amdgpu_waves_per_eu(2, 2))) delta_chunk_rev_kernel(DeltaChunkArgs a) {
+  constexpr int KS = KP / 32, KT = KP / 16, VPITCH = 16 * NW;
+  typedef RevLds<KP, NW> L;
+  extern __shared__ __align__(16) unsigned char smem_raw[];
+  float* const gates = (float*)(smem_raw + L::G);  // [2][e^G, e^{G_63 - G}, beta][64]
+  const int tid = threadIdx.x, lane = tid & 63, w = __builtin_amdgcn_readfirstlane(tid >> 6), c = lane & 15, q = lane >> 4;
   i64 unit, slice;
-  if (!walk_unit(a.seq.nseq * a.HV, (a.V + 31) / 32, unit, slice)) return;
+  if (!walk_unit(a.seq.nseq * a.HV, (a.V + VPITCH - 1) / VPITCH, unit, slice)) return;
   const i64 n = unit / a.HV, hv = unit % a.HV, h = hv / a.rep;
   const DeltaSpan sp = a.seq.span(n);
   const i64 nch = (sp.len + DCH - 1) / DCH;
-  const i64 v0 = slice * 32 + w * 16, vt = slice * 2 + w;
+  const i64 v0 = slice * VPITCH + w * 16, vt = slice * NW + w;
   const bool act = v0 < a.V;
 
-  RowTile<KP, WNT> sk, sq;
-  ColTile<WNT> sv, so;
-  float sG = 0.0f, sB = 0.0f;
-  auto fetch = [&](i64 ch) {
+  const unsigned lds0 = lds_base(smem_raw);
+  RowDma<KP, NW> rows_dma;
+  ColDma<NW, NW> cols_dma;
+  rows_dma.init(w, lane, a.H * a.K, a.K);
+  cols_dma.init(w, lane, a.HV * a.V, slice * VPITCH, a.V);
+  auto issue = [&](i64 ch, int bf) {
     const i64 tok0 = sp.start + ch * DCH;
     const int rows = (int)(sp.len - ch * DCH < DCH ? sp.len - ch * DCH : DCH);
-    sk.fetch(row_rsrc(a.k, tok0, rows, a.H, h, a.K), tid, a.H * a.K, a.K);
-    sq.fetch(row_rsrc(a.q, tok0, rows, a.H, h, a.K), tid, a.H * a.K, a.K);
-    sv.fetch(row_rsrc(a.v, tok0, rows, a.HV, hv, a.V), tid, a.HV * a.V, slice * 32, a.V);
-    so.fetch(row_rsrc(a.d_o, tok0, rows, a.HV, hv, a.V), tid, a.HV * a.V, slice * 32, a.V);
-    if (w == 0) {
-      sG = a.G[((sp.slot0 + ch) * a.HV + hv) * 64 + lane];
-      sB = lane < rows ? a.beta[(tok0 + lane) * a.HV + hv] : 0.0f;
-    }
+    const unsigned b = lds0 + (unsigned)(bf * L::BUF);
+    const i64 cu = (sp.slot0 + ch) * a.HV + hv;
+    rows_dma.issue(b + L::K, w, row_words(a.k, tok0, rows, a.H, h, a.K, 0));
+    rows_dma.issue(b + L::Q, w, row_words(a.q, tok0, rows, a.H, h, a.K, 0));
+    cols_dma.issue(b + L::O, w, row_words(a.d_o, tok0, rows, a.HV, hv, a.V, slice * VPITCH));
+    flat_dma<12, NW>(b + L::T, w, lane, rsrc_words_u(a.Tt + cu * 6 * 2 * 512, 12 * 1024));
+    flat_dma<12, NW>(b + L::P, w, lane, rsrc_words_u(a.Pt + cu * 6 * 2 * 512, 12 * 1024));
   };
-  auto commit = [&](int bf) {
-    sk.commit(Kb[bf], tid);
-    sq.commit(Qb[bf], tid);
-    sv.commit(Vb[bf], tid);
-    so.commit(Ob[bf], tid);
-    if (w == 0) {
-      const float end = __shfl(sG, 63, 64);
-      eGs[bf][lane] = exp_hw(sG);
-      eEs[bf][lane] = exp_hw(end - sG);
-      Bs[bf][lane] = sB;
-    }
+  const unsigned own = (unsigned)(L::S + w * L::OWN);
+  auto issue_own = [&](i64 ch) {
+    const i64 tile = ((sp.slot0 + ch) * a.HV + hv) * a.nvt + vt;
+    flat_dma<2 * KS, 1>(lds0 + own, 0, lane, rsrc_words_u(a.Sw + tile * 2 * KS * 512, 2 * KS * 1024));
+    flat_dma<4, 1>(lds0 + own + L::X, 0, lane, rsrc_words_u(a.Xw + tile * 1024, 4096));
+    flat_dma<4, 1>(lds0 + own + L::R, 0, lane, rsrc_words_u(a.rw + tile * 4 * 512, 4096));
+  };
+  float sG = 0.0f, sB = 0.0f;
+  auto fetch_gates = [&](i64 ch) {
+    const i64 tok0 = sp.start + ch * DCH;
+    sG = a.G[((sp.slot0 + ch) * a.HV + hv) * 64 + lane];
+    sB = ch * DCH + lane < sp.len ? a.beta[(tok0 + lane) * a.HV + hv] : 0.0f;
+  };
+  auto commit_gates = [&](int bf) {
+    const float end = __shfl(sG, 63, 64);
+    float* g = gates + bf * 192 + lane;
+    g[0] = exp_hw(sG);
+    g[64] = exp_hw(end - sG);
+    g[128] = sB;
   };
 
   f32x4 dS[KT];
+  const brsrc rs = state_rsrc(a.dSf, a, unit, act);
 #pragma unroll
-  for (int t = 0; t < KT; ++t) {
-    dS[t] = zero4();
-    if (a.dSf && act) {
-#pragma unroll
-      for (int r = 0; r < 4; ++r) {
-        const int k = 16 * t + 4 * q + r;
-        if (k < a.K) dS[t][r] = a.dSf[(unit * a.K + k) * a.V + v0 + c];
-      }
-    }
-  }
+  for (int t = 0; t < KT; ++t) dS[t] = load_state4(rs, a, t, q, v0 + c);
   if (nch > 0) {
-    fetch(nch - 1);
-    commit((nch - 1) & 1);
+    const int bf = (nch - 1) & 1;
+    if (w == 0) fetch_gates(nch - 1);
+    issue(nch - 1, bf);
+    if (act) issue_own(nch - 1);
+    if (w == 0) commit_gates(bf);
   }
+  dma_wait();
   __syncthreads();
   for (i64 ch = nch - 1; ch >= 0; --ch) {
     const int bf = ch & 1;
-    const i64 cu = (sp.slot0 + ch) * a.HV + hv;
-    if (ch > 0) fetch(ch - 1);
+    const i64 tile = ((sp.slot0 + ch) * a.HV + hv) * a.nvt + vt;
+    if (ch > 0) {
+      if (w == 0) fetch_gates(ch - 1);
+      issue(ch - 1, bf ^ 1);
+    }
     if (act) {
-      const bf16 *Kt = Kb[bf], *Qt = Qb[bf];
-      const u32x4* tf = (const u32x4*)(a.Tf + cu * 6 * 2 * 64 * 8) + lane;
-      const u32x4* tt = (const u32x4*)(a.Tt + cu * 6 * 2 * 64 * 8) + lane;
-      const u32x4* pt = (const u32x4*)(a.Pt + cu * 6 * 2 * 64 * 8) + lane;
+      const unsigned char* const buf = smem_raw + bf * L::BUF;
+      const bf16 *Kt = (const bf16*)(buf + L::K), *Qt = (const bf16*)(buf + L::Q), *Ot = (const bf16*)(buf + L::O);
+      const u32x4 *Tt = (const u32x4*)(buf + L::T) + lane, *Pt = (const u32x4*)(buf + L::P) + lane;
+      const u32x4 *So = (const u32x4*)(smem_raw + own) + lane, *Ro = (const u32x4*)(smem_raw + own + L::R) + lane;
+      const f32x4* Xo = (const f32x4*)(smem_raw + own + L::X) + lane;
+      const float *eG = gates + bf * 192, *eE = eG + 64, *be = eG + 128;
       auto at4 = [&](const float* p, int m) { return *(const f32x4*)(p + 16 * m + 4 * q); };
-      // K S0, Q S0 (both parts of S0), K dS (both parts of dS), <S0, dS>
-      f32x4 x[4], y[4], z[4];
+      // K dS (both parts of dS) and <S0, dS>
+      f32x4 z[4], x[4], r[4];
       f32x4 dot = zero4();
 #pragma unroll
-      for (int m = 0; m < 4; ++m) x[m] = zero4(), y[m] = zero4(), z[m] = zero4();
+      for (int m = 0; m < 4; ++m) z[m] = zero4();
 #pragma unroll
       for (int s = 0; s < KS; ++s) {
-        const i64 o = (((cu * a.nvt + vt) * KS + s) * 64 + lane) * 8;
-        const Frag8 sh = as_frag(*(const u32x4*)(a.Sh + o)), sl = as_frag(*(const u32x4*)(a.Sl + o));
+        const Frag8 sh = as_frag(So[s * 64]), sl = as_frag(So[(KS + s) * 64]);
         Frag8 dh, dl;
         split8(dS[2 * s], dS[2 * s + 1], dh, dl);
-        *(u32x4*)(a.dSh + o) = as_u4(dh);
+        *((u32x4*)(a.dSw + tile * KS * 512) + s * 64 + lane) = as_u4(dh);
         dot += (unpack4(sh.a) + unpack4(sl.a)) * dS[2 * s];
         dot += (unpack4(sh.b) + unpack4(sl.b)) * dS[2 * s + 1];
 #pragma unroll
         for (int m = 0; m < 4; ++m) {
-          const Frag8 kf = row_frag(Kt, KP, m, s, lane), qf = row_frag(Qt, KP, m, s, lane);
-          x[m] = mma32(kf, sl, x[m]);
-          y[m] = mma32(qf, sl, y[m]);
+          const Frag8 kf = row_frag(Kt, KP, m, s, lane);
           z[m] = mma32(kf, dl, z[m]);
-          x[m] = mma32(kf, sh, x[m]);
-          y[m] = mma32(qf, sh, y[m]);
           z[m] = mma32(kf, dh, z[m]);
         }
       }
-      // r = T (V - e^G K S0)
-      f32x4 r[4];
-      {
-        Frag8 vh[2], vl[2];
 #pragma unroll
-        for (int s = 0; s < 2; ++s) {
-          f32x4 t[2];
-#pragma unroll
-          for (int e = 0; e < 2; ++e) {
-            const int m = 2 * s + e;
-            t[e] = unpack4(ld_rowk(Vb[bf], VP, 16 * m, 16 * w, lane).v) - at4(eGs[bf], m) * x[m];
-          }
-          split8(t[0], t[1], vh[s], vl[s]);
-        }
-#pragma unroll
-        for (int m = 0; m < 4; ++m) {
-          r[m] = zero4();
-#pragma unroll
-          for (int s = 0; s <= m / 2; ++s) {
-            const Frag8 th = as_frag(tf[frag_lo(m, s) * 128]), tl = as_frag(tf[frag_lo(m, s) * 128 + 64]);
-            r[m] = mma32(th, vl[s], r[m]);
-            r[m] = mma32(tl, vh[s], r[m]);
-            r[m] = mma32(th, vh[s], r[m]);
-          }
-        }
+      for (int s = 0; s < 2; ++s) {
+        const Frag8 rh = as_frag(Ro[s * 64]), rl = as_frag(Ro[(2 + s) * 64]);
+        r[2 * s] = unpack4(rh.a) + unpack4(rl.a);
+        r[2 * s + 1] = unpack4(rh.b) + unpack4(rl.b);
+        x[2 * s] = Xo[2 * s * 64];
+        x[2 * s + 1] = Xo[(2 * s + 1) * 64];
+      }
+      if (ch > 0) {
+        lds_wait();  // what this wave had of its own is in registers
+        issue_own(ch - 1);
       }
       // dU = scale P^T dO + e^{G_63 - G} K dS
       Frag8 of[2];
 #pragma unroll
-      for (int s = 0; s < 2; ++s)
-        of[s] = {ld_rowk(Ob[bf], VP, 32 * s, 16 * w, lane).v, ld_rowk(Ob[bf], VP, 32 * s + 16, 16 * w, lane).v};
+      for (int s = 0; s < 2; ++s) of[s] = {col4(Ot, VPITCH, 2 * s, w, lane), col4(Ot, VPITCH, 2 * s + 1, w, lane)};
       f32x4 du[4], mu[4];
 #pragma unroll
       for (int m = 0; m < 4; ++m) {
-        z[m] *= at4(eEs[bf], m);
+        z[m] *= at4(eE, m);
         du[m] = z[m];
 #pragma unroll
         for (int s = m / 2; s < 2; ++s) {
-          du[m] = mma32(as_frag(pt[frag_up(m, s) * 128 + 64]), of[s], du[m]);
-          du[m] = mma32(as_frag(pt[frag_up(m, s) * 128]), of[s], du[m]);
+          du[m] = mma32(as_frag(Pt[frag_up(m, s) * 128 + 64]), of[s], du[m]);
+          du[m] = mma32(as_frag(Pt[frag_up(m, s) * 128]), of[s], du[m]);
         }
       }
       // mu = T^T (beta dU)
       {
         Frag8 bh[2], bl[2];
 #pragma unroll
-        for (int s = 0; s < 2; ++s)
-          split8(at4(Bs[bf], 2 * s) * du[2 * s], at4(Bs[bf], 2 * s + 1) * du[2 * s + 1], bh[s], bl[s]);
+        for (int m = 0; m < 4; ++m) mu[m] = at4(be, m) * du[m];
+#pragma unroll
+        for (int s = 0; s < 2; ++s) split8(mu[2 * s], mu[2 * s + 1], bh[s], bl[s]);
 #pragma unroll
         for (int m = 0; m < 4; ++m) {
-          mu[m] = zero4();
 #pragma unroll
           for (int s = m / 2; s < 2; ++s) {
-            const Frag8 th = as_frag(tt[frag_up(m, s) * 128]), tl = as_frag(tt[frag_up(m, s) * 128 + 64]);
+            const Frag8 th = as_frag(Tt[frag_up(m, s) * 128]), tl = as_frag(Tt[frag_up(m, s) * 128 + 64]);
             mu[m] = mma32(th, bl[s], mu[m]);
             mu[m] = mma32(tl, bh[s], mu[m]);
             mu[m] = mma32(th, bh[s], mu[m]);
           }
         }
       }
-      // r and mu for the gradients kernel
+      u32x4* mo = (u32x4*)(a.muw + tile * 4 * 512) + lane;
 #pragma unroll
       for (int s = 0; s < 2; ++s) {
-        const i64 o = (((cu * a.nvt + vt) * 2 + s) * 64 + lane) * 8;
         Frag8 hi, lo;
-        split8(r[2 * s], r[2 * s + 1], hi, lo);
-        *(u32x4*)(a.rh + o) = as_u4(hi);
-        *(u32x4*)(a.rl + o) = as_u4(lo);
         split8(mu[2 * s], mu[2 * s + 1], hi, lo);
-        *(u32x4*)(a.muh + o) = as_u4(hi);
-        *(u32x4*)(a.mul + o) = as_u4(lo);
+        mo[s * 64] = as_u4(hi);
+        mo[128 + s * 64] = as_u4(lo);
       }
-      // row terms, summed over this wave's 16 columns
-      const float eEnd = eGs[bf][63];
+      // row terms, summed over this wave's 16 columns; the operands of the state's update
+      const float eEnd = eG[63];
       float tail = eEnd * ((dot[0] + dot[1]) + (dot[2] + dot[3]));
-      float* rp = a.rowp + (cu * a.nvt + vt) * 2 * 64;
+      float* rp = a.rowp + tile * 3 * 64 + 64;
 #pragma unroll
       for (int m = 0; m < 4; ++m) {
-        const f32x4 eg = at4(eGs[bf], m), be = at4(Bs[bf], m);
+        const f32x4 eg = at4(eG, m);
         const f32x4 o = unpack4(m & 1 ? of[m / 2].b : of[m / 2].a);
-        const f32x4 su = be * r[m] * z[m];
-        const f32x4 t = eg * (a.scale * o * y[m] - mu[m] * x[m]) - su;
-        const f32x4 d = r[m] * du[m];
-        f32x4 ts, ds;
+        const f32x4 su = at4(be, m) * r[m] * z[m];
+        f32x4 t = -mu[m] * x[m] - su, d = r[m] * du[m];
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
           tail += su[j];
-          ts[j] = sum16(t[j]);
-          ds[j] = sum16(d[j]);
+          t[j] = sum16(t[j]);
+          d[j] = sum16(d[j]);
         }
         if (c == 0) {
-          *(f32x4*)(rp + 16 * m + 4 * q) = ts;
-          *(f32x4*)(rp + 64 + 16 * m + 4 * q) = ds;
+          *(f32x4*)(rp + 16 * m + 4 * q) = t;
+          *(f32x4*)(rp + 64 + 16 * m + 4 * q) = d;
         }
-        // the operands of the state's update
         mu[m] *= -eg;
         x[m] = a.scale * eg * o;
       }
       tail = wave_sum(tail);
-      if (lane == 0) a.endp[cu * a.nvt + vt] = tail;
+      if (lane == 0) a.endp[tile] = tail;
       // dS0 = e^{G_63} dS + Q^T (scale e^G dO) - K^T (e^G mu)
       Frag8 mh[2], ml[2], oh[2], ol[2];
 #pragma unroll
@@ -245,7 +236,7 @@ __global__ void __launch_bounds__(WNT, 1) delta_chunk_rev_kernel(DeltaChunkArgs 
         dS[t] *= eEnd;
 #pragma unroll
         for (int s = 0; s < 2; ++s) {
-          const Frag8 kf = col_frag(Kt, KP, t, s, lane), qf = col_frag(Qt, KP, t, s, lane);
+          const Frag8 kf = key_frag(Kt, KP, t, s, lane), qf = key_frag(Qt, KP, t, s, lane);
           dS[t] = mma32(kf, ml[s], dS[t]);
           dS[t] = mma32(qf, ol[s], dS[t]);
           dS[t] = mma32(kf, mh[s], dS[t]);
@@ -253,7 +244,8 @@ __global__ void __launch_bounds__(WNT, 1) delta_chunk_rev_kernel(DeltaChunkArgs 
         }
       }
     }
-    if (ch > 0) commit(bf ^ 1);
+    if (ch > 0 && w == 0) commit_gates(bf ^ 1);
+    dma_wait();
     __syncthreads();
   }
   if (a.dS0 && act) {
@@ -261,7 +253,7 @@ __global__ void __launch_bounds__(WNT, 1) delta_chunk_rev_kernel(DeltaChunkArgs 
     for (int t = 0; t < KT; ++t)
 #pragma unroll
       for (int r = 0; r < 4; ++r) {
-        const int k = 16 * t + 4 * q + r;
+        const int k = state_row(t, q) + r;
         if (k < a.K) a.dS0[(unit * a.K + k) * a.V + v0 + c] = dS[t][r];
       }
   }
@@ -290,11 +282,22 @@ __global__ void __launch_bounds__(256) delta_chunk_grads_kernel(DeltaChunkArgs a
   const ChunkAt at = chunk_at(a.seq, slot, lane);
   if (at.rows == 0) return;
   {
-    RowTile<KP, 256> tk, tq;
-    tk.fetch(row_rsrc(a.k, at.tok0, at.rows, a.H, h, a.K), tid, a.H * a.K, a.K);
-    tq.fetch(row_rsrc(a.q, at.tok0, at.rows, a.H, h, a.K), tid, a.H * a.K, a.K);
-    tk.commit(Kb, tid);
-    tq.commit(Qb, tid);
+    constexpr int N = 64 * KP / 8 / 256;
+    const brsrc rk = row_rsrc(a.k, at.tok0, at.rows, a.H, h, a.K), rq = row_rsrc(a.q, at.tok0, at.rows, a.H, h, a.K);
+    u32x4 tk[N], tq[N];
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+      const int p = tid + 256 * i, row = p / (KP / 8), col = p % (KP / 8) * 8;
+      const unsigned o = col < a.K ? (unsigned)(((i64)row * a.H * a.K + col) * 2) : BUF_OOB;
+      tk[i] = bload16(rk, o);
+      tq[i] = bload16(rq, o);
+    }
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+      const int p = tid + 256 * i;
+      st16_xs(Kb, KP, p / (KP / 8), p % (KP / 8) * 8, tk[i]);
+      st16_xs(Qb, KP, p / (KP / 8), p % (KP / 8) * 8, tq[i]);
+    }
   }
   __syncthreads();
   // lane: column j = 16 b + c, rows i = 16 w + 4 q + r
@@ -306,9 +309,9 @@ __global__ void __launch_bounds__(256) delta_chunk_grads_kernel(DeltaChunkArgs a
     if (b <= w) {
 #pragma unroll
       for (int s = 0; s < KS; ++s) {
-        const Frag8 y = row_frag(Kb, KP, b, s, lane);
-        kk[b] = mma32(row_frag(Kb, KP, w, s, lane), y, kk[b]);
-        qk[b] = mma32(row_frag(Qb, KP, w, s, lane), y, qk[b]);
+        const Frag8 y = xs_frag(Kb, KP, b, s, lane);
+        kk[b] = mma32(xs_frag(Kb, KP, w, s, lane), y, kk[b]);
+        qk[b] = mma32(xs_frag(Qb, KP, w, s, lane), y, qk[b]);
       }
     }
   }
@@ -327,21 +330,21 @@ __global__ void __launch_bounds__(256) delta_chunk_grads_kernel(DeltaChunkArgs a
     auto fetch = [&](i64 sl) {
       {
         const i64 t = sl * 2 + (tid >> 7);
-        const i64 o = (((cu * a.nvt + t) * 2 + (w & 1)) * 64 + lane) * 8;
+        const i64 o = (cu * a.nvt + t) * 256 + (w & 1) * 64 + lane;
         const bool in = t < a.nvt;
-        pr[0] = in ? *(const u32x4*)(a.rh + o) : zero_u4();
-        pr[1] = in ? *(const u32x4*)(a.rl + o) : zero_u4();
-        pr[2] = in ? *(const u32x4*)(a.muh + o) : zero_u4();
-        pr[3] = in ? *(const u32x4*)(a.mul + o) : zero_u4();
+        pr[0] = in ? ((const u32x4*)a.rw)[o] : zero_u4();
+        pr[1] = in ? ((const u32x4*)a.rw)[o + 128] : zero_u4();
+        pr[2] = in ? ((const u32x4*)a.muw)[o] : zero_u4();
+        pr[3] = in ? ((const u32x4*)a.muw)[o + 128] : zero_u4();
       }
 #pragma unroll
       for (int i = 0; i < NS; ++i) {
         const int p = tid + 256 * i;
         const i64 t = sl * 2 + p / (64 * KS);
-        const i64 o = (((cu * a.nvt + t) * KS + p / 64 % KS) * 64 + lane) * 8;
+        const i64 o = p / 64 % KS * 64 + lane;
         const bool in = t < a.nvt;
-        ps[i] = in ? *(const u32x4*)(a.Sh + o) : zero_u4();
-        pd[i] = in ? *(const u32x4*)(a.dSh + o) : zero_u4();
+        ps[i] = in ? ((const u32x4*)a.Sw)[(cu * a.nvt + t) * 2 * KS * 64 + o] : zero_u4();
+        pd[i] = in ? ((const u32x4*)a.dSw)[(cu * a.nvt + t) * KS * 64 + o] : zero_u4();
       }
 #pragma unroll
       for (int e = 0; e < 2; ++e) {
@@ -376,8 +379,9 @@ __global__ void __launch_bounds__(256) delta_chunk_grads_kernel(DeltaChunkArgs a
 #pragma unroll
         for (int i = 0; i < NS; ++i) {
           const int p = tid + 256 * i;
-          put(sT, KP, 16 * (p / (64 * KS)) + c, p / 64 % KS, ps[i]);
-          put(dT, KP, 16 * (p / (64 * KS)) + c, p / 64 % KS, pd[i]);
+          const int row = 16 * (p / (64 * KS)) + c, col = 32 * (p / 64 % KS) + 8 * q;
+          st16_xs(sT, KP, row, col, ps[i]);
+          st16_xs(dT, KP, row, col, pd[i]);
         }
       }
       const Frag8 of = {__builtin_bit_cast(s16x4, po[0]), __builtin_bit_cast(s16x4, po[1])};
@@ -463,8 +467,8 @@ __global__ void __launch_bounds__(256) delta_chunk_grads_kernel(DeltaChunkArgs a
     for (int s = 0; s < 2; ++s) {
       dr[s] = col_frag(Dt, 64, w, s, lane);
       er[s] = col_frag(Et, 64, w, s, lane);
-      dc[s] = row_frag(Dt, 64, w, s, lane);
-      ec[s] = row_frag(Et, 64, w, s, lane);
+      dc[s] = xs_frag(Dt, 64, w, s, lane);
+      ec[s] = xs_frag(Et, 64, w, s, lane);
     }
 #pragma unroll
     for (int t = 0; t < KT; ++t)
@@ -482,11 +486,11 @@ __global__ void __launch_bounds__(256) delta_chunk_grads_kernel(DeltaChunkArgs a
       }
     // dbeta, dg
     if (w == 0) {
-      const float* rp = a.rowp + cu * a.nvt * 2 * 64;
+      const float* rp = a.rowp + cu * a.nvt * 3 * 64;
       float dG = 0.0f, db = 0.0f, tail = 0.0f;
       for (i64 t = 0; t < a.nvt; ++t) {
-        dG += rp[t * 128 + lane];
-        db += rp[t * 128 + 64 + lane];
+        dG += rp[t * 192 + lane] + rp[t * 192 + 64 + lane];
+        db += rp[t * 192 + 128 + lane];
         tail += a.endp[cu * a.nvt + t];
       }
       dG += rowM[lane] - ((colM[0][lane] + colM[1][lane]) + (colM[2][lane] + colM[3][lane]));
@@ -515,12 +519,20 @@ __global__ void __launch_bounds__(256) delta_chunk_grads_kernel(DeltaChunkArgs a
     }
 }
 
+template <int KP>
+void launch_rev_grads(const DeltaChunkArgs& a, hipStream_t s) {
+  const i64 blocks = walk_blocks(a.seq.nseq * a.HV, (a.V + 31) / 32);
+  hipLaunchKernelGGL((delta_chunk_rev_kernel<KP, 2>), dim3((unsigned)blocks), dim3(128), (RevLds<KP, 2>::TOTAL), s, a);
+  if (a.nslots > 0)
+    hipLaunchKernelGGL((delta_chunk_grads_kernel<KP>), dim3((unsigned)(a.nslots * a.H)), dim3(256), 0, s, a);
+}
+
 struct BwdPlan {
-  i64 off_T, off_Tt, off_Pt, off_G, off_Sh, off_Sl, off_dS, off_rh, off_rl, off_mh, off_ml, off_row, off_end;
+  i64 off_T, off_Tt, off_Pt, off_G, off_S, off_dS, off_r, off_X, off_mu, off_row, off_end;
   size_t bytes;
 };
 BwdPlan bwd_plan(const ssmvjp_delta_chunk_desc& d) {
-  const i64 cells = delta_slots(d) * d.nv_heads, nvt = d.dv / 16, KP = d.dk <= 64 ? 64 : 128;
+  const i64 cells = delta_slots(d) * d.nv_heads, tiles = cells * (d.dv / 16), KP = d.dk <= 64 ? 64 : 128;
   BwdPlan p{};
   i64 off = 0;
   auto carve = [&](i64 bytes) {
@@ -528,20 +540,17 @@ BwdPlan bwd_plan(const ssmvjp_delta_chunk_desc& d) {
     off += (bytes + 255) / 256 * 256;
     return o;
   };
-  const i64 tri = cells * 6 * 2 * 64 * 8 * 2, st = cells * nvt * KP * 16 * 2, rw = cells * nvt * 2 * 64 * 8 * 2;
-  p.off_T = carve(tri);
-  p.off_Tt = carve(tri);
-  p.off_Pt = carve(tri);
+  p.off_T = carve(cells * 12 * 1024);
+  p.off_Tt = carve(cells * 12 * 1024);
+  p.off_Pt = carve(cells * 12 * 1024);
   p.off_G = carve(cells * 64 * 4);
-  p.off_Sh = carve(st);
-  p.off_Sl = carve(st);
-  p.off_dS = carve(st);
-  p.off_rh = carve(rw);
-  p.off_rl = carve(rw);
-  p.off_mh = carve(rw);
-  p.off_ml = carve(rw);
-  p.off_row = carve(cells * nvt * 2 * 64 * 4);
-  p.off_end = carve(cells * nvt * 4);
+  p.off_S = carve(tiles * KP * 16 * 2 * 2);
+  p.off_dS = carve(tiles * KP * 16 * 2);
+  p.off_r = carve(tiles * 4 * 1024);
+  p.off_X = carve(tiles * 4 * 1024);
+  p.off_mu = carve(tiles * 4 * 1024);
+  p.off_row = carve(tiles * 3 * 64 * 4);
+  p.off_end = carve(tiles * 4);
   p.bytes = (size_t)off;
   return p;
 }
@@ -559,22 +568,16 @@ hipError_t launch_delta_chunk_bwd(const ssmvjp_delta_chunk_desc& d, const DeltaC
   a.dq = (bf16*)p.dq; a.dk = (bf16*)p.dk; a.dv = (bf16*)p.dv; a.dbeta = p.dbeta; a.dg = p.dg; a.dS0 = p.dS0;
   auto b16 = [&](i64 off) { return (bf16*)(ws + off); };
   a.Tf = b16(pl.off_T); a.Tt = b16(pl.off_Tt); a.Pt = b16(pl.off_Pt); a.G = (float*)(ws + pl.off_G);
-  a.Sh = b16(pl.off_Sh); a.Sl = b16(pl.off_Sl); a.dSh = b16(pl.off_dS);
-  a.rh = b16(pl.off_rh); a.rl = b16(pl.off_rl); a.muh = b16(pl.off_mh); a.mul = b16(pl.off_ml);
+  a.Sw = b16(pl.off_S); a.dSw = b16(pl.off_dS); a.rw = b16(pl.off_r); a.muw = b16(pl.off_mu);
+  a.Xw = (float*)(ws + pl.off_X);
   a.rowp = (float*)(ws + pl.off_row); a.endp = (float*)(ws + pl.off_end);
   if (a.nslots > 0) {
     hipError_t e = launch_delta_prep(a, true, stream);
     if (e == hipSuccess) e = launch_delta_states(a, stream);
     if (e != hipSuccess) return e;
   }
-  const dim3 walk((unsigned)walk_blocks(a.seq.nseq * a.HV, (a.V + 31) / 32)), cells((unsigned)(a.nslots * a.H));
-  if (a.K <= 64) {
-    hipLaunchKernelGGL((delta_chunk_rev_kernel<64>), walk, dim3(WNT), 0, stream, a);
-    if (a.nslots > 0) hipLaunchKernelGGL((delta_chunk_grads_kernel<64>), cells, dim3(256), 0, stream, a);
-  } else {
-    hipLaunchKernelGGL((delta_chunk_rev_kernel<128>), walk, dim3(WNT), 0, stream, a);
-    if (a.nslots > 0) hipLaunchKernelGGL((delta_chunk_grads_kernel<128>), cells, dim3(256), 0, stream, a);
-  }
+  if (a.K <= 64) launch_rev_grads<64>(a, stream);
+  else launch_rev_grads<128>(a, stream);
   return hipGetLastError();
 }
 

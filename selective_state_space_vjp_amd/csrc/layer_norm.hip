@@ -286,6 +286,30 @@ __device__ __forceinline__ void load_x(const NormArgs& a, i64 r, i64 vec, float 
     load_vec<VEC>((const T*)a.x + r * a.D + vec * VEC, o);
 }
 
+// one vector of x (or of its codes, and their scale) and of dy as they are in
+// memory: the next row's are loaded while a row is computed
+template <typename T, int VEC, bool CK>
+struct NormRaw {
+  T dy[VEC], x[CK ? 1 : VEC];
+  int8_t c[CK ? VEC : 1];
+  float s;
+  __device__ __forceinline__ void load(const NormArgs& a, i64 r, i64 vec) {
+    constexpr int B = VEC * (int)sizeof(T), AL = VEC > 1 ? 16 : (int)sizeof(T);
+    const i64 e = r * a.D + vec * VEC;
+    __builtin_memcpy(dy, __builtin_assume_aligned((const T*)a.dy + e, AL), B);
+    if constexpr (CK) {
+      __builtin_memcpy(c, __builtin_assume_aligned(a.x8 + e, VEC), VEC);
+      s = a.x8s[r * a.NB + vec / (64 / VEC)];
+    } else {
+      __builtin_memcpy(x, __builtin_assume_aligned((const T*)a.x + e, AL), B);
+    }
+  }
+  __device__ __forceinline__ float x_at(int k) const {
+    if constexpr (CK) return (float)c[k] * s;
+    else return (float)x[k];
+  }
+};
+
 template <typename T, int VEC, int TPR, int NV, bool CK>
 __global__ void __launch_bounds__(256) norm_bwd_kernel(NormArgs a) {
   constexpr int RPB = 256 / TPR, W = TPR * NV * VEC;  // W: columns a row slot can hold
@@ -302,21 +326,33 @@ __global__ void __launch_bounds__(256) norm_bwd_kernel(NormArgs a) {
     for (int k = 0; k < VEC; ++k) w[n][k] = 1.0f, dw[n][k] = 0.0f, db[n][k] = 0.0f;
     if (a.w && e < a.D) load_vec<VEC>(a.w + g * a.D + e, w[n]);
   }
+  NormRaw<T, VEC, CK> raw[NV];
+  float mean_n = 0.0f, rstd_n = 0.0f;
+  auto fetch = [&](i64 row) {
+    const i64 r = row * a.G + g;
+    mean_n = a.mean[r];
+    rstd_n = a.rstd[r];
+#pragma unroll
+    for (int n = 0; n < NV; ++n)
+      if ((i64)(t + TPR * n) * VEC < a.D) raw[n].load(a, r, t + TPR * n);
+  };
+  i64 row = part * RPB + sub;
+  if (row < a.rows) fetch(row);
   int flip = 0;
-  for (i64 row = part * RPB + sub; row < a.rows; row += a.parts * RPB, flip ^= 1) {
+  for (; row < a.rows; row += a.parts * RPB, flip ^= 1) {
     const i64 r = row * a.G + g;
     float h[NV][VEC], dy[NV][VEC];
-    const float mean = a.mean[r], rstd = a.rstd[r];
+    const float mean = mean_n, rstd = rstd_n;
 #pragma unroll
     for (int n = 0; n < NV; ++n) {
-      const i64 vec = t + TPR * n;
+      const bool live = (i64)(t + TPR * n) * VEC < a.D;
 #pragma unroll
-      for (int k = 0; k < VEC; ++k) h[n][k] = mean, dy[n][k] = 0.0f;
-      if (vec * VEC < a.D) {
-        load_x<T, VEC, CK>(a, r, vec, h[n]);
-        load_vec<VEC>((const T*)a.dy + r * a.D + vec * VEC, dy[n]);
+      for (int k = 0; k < VEC; ++k) {
+        h[n][k] = live ? raw[n].x_at(k) : mean;
+        dy[n][k] = live ? (float)raw[n].dy[k] : 0.0f;
       }
     }
+    if (row + a.parts * RPB < a.rows) fetch(row + a.parts * RPB);
     float s1 = 0.0f, s2 = 0.0f;
 #pragma unroll
     for (int n = 0; n < NV; ++n)
@@ -439,22 +475,27 @@ __global__ void __launch_bounds__(256) norm_cols_kernel(NormArgs a, i64 cblocks)
   a.part[((part * 2 + 1) * a.G + g) * a.D + d] = db;
 }
 
-// dw, db = sums of the workgroups' partial sums: 32 columns x 8 shares per
-// workgroup, each share's parts in ascending order, then the shares in order
-__global__ void __launch_bounds__(256) norm_reduce_kernel(const float* part, i64 parts, i64 GD, float* dw, float* db) {
-  __shared__ float acc[8][32];
+// dw, db = sums of the workgroups' partial sums: 32 columns x 32 shares per
+// workgroup, each share's parts in ascending order, then the shares in a tree
+__global__ void __launch_bounds__(1024) norm_reduce_kernel(const float* part, i64 parts, i64 GD, float* dw, float* db) {
+  __shared__ float acc[32][33];
   const int c = threadIdx.x & 31, sh = threadIdx.x >> 5;
   const i64 col = (i64)blockIdx.x * 32 + c;
   float s = 0.0f;
-  if (col < 2 * GD)
-    for (i64 p = sh; p < parts; p += 8) s += part[p * 2 * GD + col];
+  if (col < 2 * GD) {
+#pragma unroll 8
+    for (i64 p = sh; p < parts; p += 32) s += part[p * 2 * GD + col];
+  }
   acc[sh][c] = s;
   __syncthreads();
-  if (sh == 0 && col < 2 * GD) {
-#pragma unroll
-    for (int i = 1; i < 8; ++i) s += acc[i][c];
-    float* out = col < GD ? dw : db;
-    if (out) out[col < GD ? col : col - GD] = s;
+  // thread (column sh, share c): the sum over the shares lies in one half wave
+  s = acc[c][sh];
+  s = sum16(s);
+  s += __shfl_xor(s, 16, 64);
+  const i64 oc = (i64)blockIdx.x * 32 + sh;
+  if (c == 0 && oc < 2 * GD) {
+    float* out = oc < GD ? dw : db;
+    if (out) out[oc < GD ? oc : oc - GD] = s;
   }
 }
 
@@ -477,10 +518,10 @@ bool vec_ok(const ssmvjp_norm_desc& d, std::initializer_list<const void*> ps) {
   return true;
 }
 
-// workgroups per group: enough to fill the card (about `total` of 4 waves),
-// not more than there are shares of rows
-i64 norm_parts(i64 rows, i64 G, int rpb, i64 total) {
-  const i64 most = (rows + rpb - 1) / rpb, want = (total + G - 1) / G;
+// workgroups per group: enough to fill the card (about `total` of 4 waves), not
+// more than there are shares of `per` rows for each of a workgroup's rpb slots
+i64 norm_parts(i64 rows, i64 G, int rpb, int per, i64 total) {
+  const i64 most = (rows + rpb * per - 1) / (rpb * per), want = (total + G - 1) / G;
   return most < want ? most : want;
 }
 
@@ -494,13 +535,14 @@ int norm_tpr(i64 D, int vec, bool backward) {
 }
 
 constexpr i64 FWD_GROUPS = 2048, BWD_GROUPS = 512;
+constexpr int BWD_ROWS = 2;  // a workgroup's partial dw, db cost as much as a row of dx each
 
 template <typename T, int VEC, bool CK>
 void fwd_vec(const NormArgs& in, hipStream_t s) {
   NormArgs a = in;
   const int tpr = norm_tpr(a.D, VEC, false);
   const i64 n = (a.D + VEC - 1) / VEC;
-  a.parts = norm_parts(a.rows, a.G, tpr ? 256 / tpr : 1, FWD_GROUPS);
+  a.parts = norm_parts(a.rows, a.G, tpr ? 256 / tpr : 1, 1, FWD_GROUPS);
   const dim3 grid((unsigned)(a.parts * a.G)), wg(256);
   if constexpr (VEC > 1) {
     if (tpr == 16) {
@@ -526,7 +568,7 @@ void bwd_vec(const NormArgs& in, hipStream_t s) {
   NormArgs a = in;
   const int tpr = norm_tpr(a.D, VEC, true);
   const i64 n = (a.D + VEC - 1) / VEC;
-  a.parts = norm_parts(a.rows, a.G, tpr ? 256 / tpr : 1, BWD_GROUPS);
+  a.parts = norm_parts(a.rows, a.G, tpr ? 256 / tpr : 1, BWD_ROWS, BWD_GROUPS);
   const dim3 grid((unsigned)(a.parts * a.G)), wg(256);
   if (VEC > 1 && tpr == 16) {
     if constexpr (VEC > 1) {
@@ -558,7 +600,7 @@ NormArgs norm_args(const ssmvjp_norm_desc& d) {
 
 size_t norm_bwd_workspace_bytes(const ssmvjp_norm_desc& d) {
   // the largest number of partial sums over the variants (they differ in the rows per workgroup)
-  return (size_t)(norm_parts(d.rows, d.groups, 1, BWD_GROUPS) * 2 * d.groups * d.dim * 4);
+  return (size_t)(norm_parts(d.rows, d.groups, 1, BWD_ROWS, BWD_GROUPS) * 2 * d.groups * d.dim * 4);
 }
 
 hipError_t launch_norm_fwd(const ssmvjp_norm_desc& d, const NormFwdPointers& p, hipStream_t s) {
@@ -599,8 +641,8 @@ hipError_t launch_norm_bwd(const ssmvjp_norm_desc& d, const NormBwdPointers& p, 
   }
   if (wants) {
     const int tpr = norm_tpr(d.dim, v ? (d.dtype == SSMVJP_BF16 ? 8 : 4) : 1, true);
-    const i64 parts = norm_parts(d.rows, d.groups, tpr ? 256 / tpr : 1, BWD_GROUPS);
-    hipLaunchKernelGGL(norm_reduce_kernel, dim3((unsigned)((2 * GD + 31) / 32)), dim3(256), 0, s, (const float*)p.workspace, parts,
+    const i64 parts = norm_parts(d.rows, d.groups, tpr ? 256 / tpr : 1, BWD_ROWS, BWD_GROUPS);
+    hipLaunchKernelGGL(norm_reduce_kernel, dim3((unsigned)((2 * GD + 31) / 32)), dim3(1024), 0, s, (const float*)p.workspace, parts,
                        GD, p.dweight, p.dbias);
   }
   return hipGetLastError();
