@@ -238,9 +238,9 @@ __device__ __forceinline__ ChunkAt chunk_at(const DeltaSeqs& q, i64 slot, int la
 // and the slices of one head, which read the same q, k and fragments, share one
 // XCD's L2.  unit = sequence * HV + head; false: no work.
 __device__ __forceinline__ bool walk_unit(i64 units, i64 nslice, i64& unit, i64& slice) {
-  const i64 x = blockIdx.x & 7, y = blockIdx.x >> 3;
-  unit = y / nslice * 8 + x;
-  slice = y % nslice;
+  const unsigned x = blockIdx.x & 7, y = blockIdx.x >> 3, ns = (unsigned)nslice;
+  unit = y / ns * 8 + x;
+  slice = y % ns;
   return unit < units;
 }
 inline i64 walk_blocks(i64 units, i64 nslice) { return (units + 7) / 8 * 8 * nslice; }

@@ -49,7 +49,12 @@ __device__ __forceinline__ void invert64(const float* As, float* Ts, int w, int 
     for (int i = 0; i < 16; ++i) {
       float s = i == c ? 1.0f : 0.0f;
 #pragma unroll
-      for (int j = 0; j < i; ++j) s = fmaf(-A[i * TP + j], x[j], s);
+      for (int j = 0; j < i; j += 4) {
+        const f32x4 r = *(const f32x4*)(A + i * TP + j);  // the same for every lane
+#pragma unroll
+        for (int k = 0; k < 4; ++k)
+          if (j + k < i) s = fmaf(-r[k], x[j + k], s);
+      }
       x[i] = s;
     }
     if (q == 0) {
@@ -86,12 +91,13 @@ __device__ __forceinline__ void invert64(const float* As, float* Ts, int w, int 
 }
 
 template <int KP, bool BWD>
-__global__ void __launch_bounds__(256) delta_prep_kernel(DeltaChunkArgs a) {
+__global__ void __launch_bounds__(256, 3) delta_prep_kernel(DeltaChunkArgs a) {
   constexpr int KS = KP / 32;
   __shared__ float As[64 * TP], Ts[64 * TP];
   __shared__ float Gs[64], Bs[64];
-  const int lane = threadIdx.x & 63, w = threadIdx.x >> 6, c = lane & 15, q = lane >> 4;
-  const i64 h = blockIdx.x % a.H, slot = blockIdx.x / a.H;
+  const int lane = threadIdx.x & 63, w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), c = lane & 15, q = lane >> 4;
+  const unsigned H32 = (unsigned)a.H;
+  const i64 h = blockIdx.x % H32, slot = blockIdx.x / H32;
   const ChunkAt at = chunk_at(a.seq, slot, lane);
   if (at.rows == 0) return;
   const brsrc rk = row_rsrc(a.k, at.tok0, at.rows, a.H, h, a.K), rq = row_rsrc(a.q, at.tok0, at.rows, a.H, h, a.K);
@@ -99,9 +105,29 @@ __global__ void __launch_bounds__(256) delta_prep_kernel(DeltaChunkArgs a) {
     const int col = 32 * s + 8 * q;
     return col < a.K ? (unsigned)(((i64)(16 * tile + c) * a.H * a.K + col) * 2) : BUF_OOB;
   };
-  u32x4 kw[KS], qw[KS];
+  // everything this wave needs of k and q is on its way before the first product
+  u32x4 kx[4][KS], qw[KS], qx[BWD ? 4 : 1][KS];
 #pragma unroll
-  for (int s = 0; s < KS; ++s) kw[s] = bload16(rk, off(w, s)), qw[s] = bload16(rq, off(w, s));
+  for (int b = 0; b < 4; ++b)
+    if (b <= w) {
+#pragma unroll
+      for (int s = 0; s < KS; ++s) kx[b][s] = bload16(rk, off(b, s));
+    }
+#pragma unroll
+  for (int s = 0; s < KS; ++s) qw[s] = bload16(rq, off(w, s));
+  if constexpr (BWD) {
+#pragma unroll
+    for (int b = 0; b < 4; ++b)
+      if (b > w) {
+#pragma unroll
+        for (int s = 0; s < KS; ++s) qx[b][s] = bload16(rq, off(b, s));
+      }
+  }
+  const bool in = lane < at.rows;
+  float gn = in ? a.g[(at.tok0 + lane) * a.HV + h * a.rep] : 0.0f, bn = in ? a.beta[(at.tok0 + lane) * a.HV + h * a.rep] : 0.0f;
+  u32x4 kw[KS];
+#pragma unroll
+  for (int s = 0; s < KS; ++s) kw[s] = w == 0 ? kx[0][s] : w == 1 ? kx[1][s] : w == 2 ? kx[2][s] : kx[3][s];
   // lane: row i = 16 w + c, columns j = 16 b + 4 q + r (kt: row j = 16 w + c, columns i)
   f32x4 kk[4], qk[4], kt[BWD ? 4 : 1];
 #pragma unroll
@@ -109,23 +135,17 @@ __global__ void __launch_bounds__(256) delta_prep_kernel(DeltaChunkArgs a) {
     kk[b] = zero4();
     qk[b] = zero4();
     if (b <= w) {
-      u32x4 x[KS];
-#pragma unroll
-      for (int s = 0; s < KS; ++s) x[s] = bload16(rk, off(b, s));
 #pragma unroll
       for (int s = 0; s < KS; ++s) {
-        kk[b] = mma32(x[s], kw[s], kk[b]);
-        qk[b] = mma32(x[s], qw[s], qk[b]);
+        kk[b] = mma32(kx[b][s], kw[s], kk[b]);
+        qk[b] = mma32(kx[b][s], qw[s], qk[b]);
       }
     }
     if constexpr (BWD) {
       kt[b] = zero4();
       if (b >= w) {
-        u32x4 x[KS];
 #pragma unroll
-        for (int s = 0; s < KS; ++s) x[s] = bload16(rq, off(b, s));
-#pragma unroll
-        for (int s = 0; s < KS; ++s) kt[b] = mma32(x[s], kw[s], kt[b]);
+        for (int s = 0; s < KS; ++s) kt[b] = mma32(b == w ? qw[s] : qx[b][s], kw[s], kt[b]);
       }
     }
   }
@@ -133,45 +153,41 @@ __global__ void __launch_bounds__(256) delta_prep_kernel(DeltaChunkArgs a) {
     const i64 hv = h * a.rep + rr, unit = slot * a.HV + hv;
     __syncthreads();  // the previous head's readers are done with LDS
     if (w == 0) {
-      const i64 at1 = (at.tok0 + lane) * a.HV + hv;
-      const bool in = lane < at.rows;
-      const float G = wave_incl_scan(in ? gate_clamp(a.g[at1]) : 0.0f, lane);
+      const float G = wave_incl_scan(gate_clamp(gn), lane);
       Gs[lane] = G;
-      Bs[lane] = in ? a.beta[at1] : 0.0f;
+      Bs[lane] = bn;
       a.G[unit * 64 + lane] = G;
     }
     __syncthreads();
+    if (rr + 1 < a.rep && in) {  // the next head's gates
+      gn = a.g[(at.tok0 + lane) * a.HV + hv + 1];
+      bn = a.beta[(at.tok0 + lane) * a.HV + hv + 1];
+    }
     const int row = 16 * w + c;
     const float Gr = Gs[row];
+    // a beta into LDS and, for the forward, the tiles of scale P beta
+    f32x4 p[4];
 #pragma unroll
     for (int b = 0; b < 4; ++b) {
-      const f32x4 Gc = *(const f32x4*)(Gs + 16 * b + 4 * q), Bc = *(const f32x4*)(Bs + 16 * b + 4 * q);
+      p[b] = zero4();
       if (b <= w) {
+        const f32x4 Gc = *(const f32x4*)(Gs + 16 * b + 4 * q), Bc = *(const f32x4*)(Bs + 16 * b + 4 * q);
         f32x4 x;
 #pragma unroll
         for (int r = 0; r < 4; ++r) {
           const int j = 16 * b + 4 * q + r;
-          x[r] = row > j ? kk[b][r] * exp_hw(Gr - Gc[r]) * Bc[r] : 0.0f;
+          const float gb = exp_hw(row >= j ? Gr - Gc[r] : 0.0f) * Bc[r];
+          x[r] = row > j ? kk[b][r] * gb : 0.0f;
+          if (!BWD && row >= j) p[b][r] = a.scale * qk[b][r] * gb;
         }
         *(f32x4*)(As + row * TP + 16 * b + 4 * q) = x;
       }
     }
-    // fragments of scale P beta (lower) and, for the backward, of scale P^T
-    auto p_tile = [&](int b) {
-      f32x4 x = zero4();
-      if (b <= w) {
-        const f32x4 Gc = *(const f32x4*)(Gs + 16 * b + 4 * q), Bc = *(const f32x4*)(Bs + 16 * b + 4 * q);
-#pragma unroll
-        for (int r = 0; r < 4; ++r)
-          if (row >= 16 * b + 4 * q + r) x[r] = a.scale * qk[b][r] * exp_hw(Gr - Gc[r]) * Bc[r];
-      }
-      return x;
-    };
     if constexpr (!BWD) {
 #pragma unroll
       for (int s = 0; s < 2; ++s)
         if (s <= w >> 1) {
-          const Frag8 f = {pack4(p_tile(2 * s)), pack4(p_tile(2 * s + 1))};
+          const Frag8 f = {pack4(p[2 * s]), pack4(p[2 * s + 1])};
           *(u32x4*)(a.Pf + ((unit * 6 + frag_lo(w, s)) * 64 + lane) * 8) = as_u4(f);
         }
     } else {
@@ -259,6 +275,17 @@ struct WalkLds {  // byte offsets
 // no instruction moves past here: operands that are read ahead stay ahead
 #define SSMVJP_FENCE() __builtin_amdgcn_sched_barrier(0)
 
+// asks the scheduler for N times: an MFMA, VALU vector instructions, LDS reads
+template <int N, int VALU, int READ>
+__device__ __forceinline__ void pipe() {
+#pragma unroll
+  for (int i = 0; i < N; ++i) {
+    __builtin_amdgcn_sched_group_barrier(0x8, 1, 0);
+    if (VALU) __builtin_amdgcn_sched_group_barrier(0x2, VALU, 0);
+    if (READ) __builtin_amdgcn_sched_group_barrier(0x100, READ, 0);
+  }
+}
+
 constexpr int WALK_NTH = 320;
 
 template <int KP, int MODE>
@@ -283,6 +310,7 @@ delta_chunk_walk_kernel(DeltaChunkArgs a) {
 
   if (w < 2) {
     // ---------------------------------------------------------------- the state
+    __builtin_amdgcn_s_setprio(3);  // what every other wave waits for goes first
     f32x4 S[KT];
     Frag8 sh[KS], sl[KS];  // its two parts
     const brsrc rs = state_rsrc(a.S0, a, unit, act);
@@ -300,91 +328,127 @@ delta_chunk_walk_kernel(DeltaChunkArgs a) {
         u32x4* So = (u32x4*)(smem_raw + L::S + bf * L::SBUF + t16 * (L::SBUF / 2)) + lane;
         f32x4* Ro = (f32x4*)(smem_raw + L::R + (bf * 2 + t16) * 4096) + lane;
         const float *eG = gates(ch), *wB = eG + 64;
-        // K S0, both parts of S0
-        Frag8 kf[KS][4];
-#pragma unroll
-        for (int s = 0; s < 2; ++s)
-#pragma unroll
-          for (int m = 0; m < 4; ++m) kf[s][m] = row_frag(Kt, KP, m, s, lane);
-        SSMVJP_FENCE();
-        f32x4 x[4], e[4];
+        // Six stretches of MFMAs, each with the vector and LDS work of its neighbours between them: a 16x16x32
+        // MFMA holds the matrix pipe for 16 cycles, in which three vector instructions issue.
+        // 1: K S0, row tiles 0 and 1, both parts of S0; the state's decay
+        f32x4 x[4], e[4], wb[4];
         s16x4 v[4];
+        Frag8 kf[2][KS];
+#pragma unroll
+        for (int s = 0; s < KS; ++s) kf[0][s] = row_frag(Kt, KP, 0, s, lane), kf[1][s] = row_frag(Kt, KP, 1, s, lane);
+        const float eEnd = eG[63];
+        SSMVJP_FENCE();
 #pragma unroll
         for (int m = 0; m < 4; ++m) x[m] = zero4();
 #pragma unroll
         for (int s = 0; s < KS; ++s) {
-          // under these products: the fragments two steps on, then V and e^G, and the state's parts to the follower
-          if (s + 2 < KS) {
-#pragma unroll
-            for (int m = 0; m < 4; ++m) kf[s + 2][m] = row_frag(Kt, KP, m, s + 2, lane);
-          } else if (s + 2 == KS) {
-#pragma unroll
-            for (int m = 0; m < 4; ++m) v[m] = col4(Vt, 32, m, t16, lane), e[m] = at4(eG, m);
-          }
-          So[s * 64] = as_u4(sh[s]);
-          So[(KS + s) * 64] = as_u4(sl[s]);
-#pragma unroll
-          for (int m = 0; m < 4; ++m) x[m] = mma32(kf[s][m], sl[s], x[m]);
-#pragma unroll
-          for (int m = 0; m < 4; ++m) x[m] = mma32(kf[s][m], sh[s], x[m]);
-          SSMVJP_FENCE();
+          x[0] = mma32(kf[0][s], sl[s], x[0]);
+          x[1] = mma32(kf[1][s], sl[s], x[1]);
+          x[0] = mma32(kf[0][s], sh[s], x[0]);
+          x[1] = mma32(kf[1][s], sh[s], x[1]);
         }
-        Frag8 th[6], tl[6];
+        Frag8 kg[2][KS];
+#pragma unroll
+        for (int s = 0; s < KS; ++s) kg[0][s] = row_frag(Kt, KP, 2, s, lane), kg[1][s] = row_frag(Kt, KP, 3, s, lane);
+#pragma unroll
+        for (int m = 0; m < 4; ++m) v[m] = col4(Vt, 32, m, t16, lane), e[m] = at4(eG, m);
+#pragma unroll
+        for (int t = 0; t < KT; ++t) S[t] *= eEnd;
+        pipe<4 * KS, 2, 1>();
+        SSMVJP_FENCE();
+        // 2: K S0, row tiles 2 and 3; V - e^G K S0 of tiles 0 and 1; the state's parts to the follower
+#pragma unroll
+        for (int s = 0; s < KS; ++s) {
+          x[2] = mma32(kg[0][s], sl[s], x[2]);
+          x[3] = mma32(kg[1][s], sl[s], x[3]);
+          x[2] = mma32(kg[0][s], sh[s], x[2]);
+          x[3] = mma32(kg[1][s], sh[s], x[3]);
+        }
+        f32x4* X = (f32x4*)(a.Xw + ((cell0 + ch * a.HV) * a.nvt + vt) * 1024) + lane;
+        Frag8 xh[2], xl[2], th[6], tl[6];
+        auto residual = [&](int s) {
+#pragma unroll
+          for (int m = 2 * s; m < 2 * s + 2; ++m) {
+            x[m] *= e[m];
+            if constexpr (!FWD) X[m * 64] = x[m];
+            x[m] = unpack4(v[m]) - x[m];
+          }
+          split8(x[2 * s], x[2 * s + 1], xh[s], xl[s]);
+        };
+        residual(0);
 #pragma unroll
         for (int i = 0; i < 6; ++i) th[i] = as_frag(Tf[i * 128]), tl[i] = as_frag(Tf[i * 128 + 64]);
+#pragma unroll
+        for (int s = 0; s < KS; ++s) So[s * 64] = as_u4(sh[s]), So[(KS + s) * 64] = as_u4(sl[s]);
+        pipe<4 * KS, 3, 1>();
         SSMVJP_FENCE();
-        // V - e^G K S0
-        f32x4* X = (f32x4*)(a.Xw + ((cell0 + ch * a.HV) * a.nvt + vt) * 1024) + lane;
+        // 3: r = T (V - e^G K S0), contraction over tiles 0 and 1; the other residual
 #pragma unroll
-        for (int m = 0; m < 4; ++m) {
-          x[m] *= e[m];
-          if constexpr (!FWD) X[m * 64] = x[m];
-          x[m] = unpack4(v[m]) - x[m];
-        }
-        Frag8 xh[2], xl[2];
+        for (int m = 0; m < 4; ++m) x[m] = m < 2 ? mma32(th[frag_lo(m, 0)], xl[0], x[m]) : x[m];
+        f32x4 y[2];  // tiles 2 and 3 get this part later: their own residual is still to be formed
+        y[0] = mma32(th[frag_lo(2, 0)], xl[0], zero4());
+        y[1] = mma32(th[frag_lo(3, 0)], xl[0], zero4());
 #pragma unroll
-        for (int s = 0; s < 2; ++s) split8(x[2 * s], x[2 * s + 1], xh[s], xl[s]);
-        // r = T (V - e^G K S0), row tiles in turn
+        for (int m = 0; m < 2; ++m) x[m] = mma32(tl[frag_lo(m, 0)], xh[0], x[m]);
+        y[0] = mma32(tl[frag_lo(2, 0)], xh[0], y[0]);
+        y[1] = mma32(tl[frag_lo(3, 0)], xh[0], y[1]);
 #pragma unroll
-        for (int s = 0; s < 2; ++s) {
-#pragma unroll
-          for (int m = 2 * s; m < 4; ++m) x[m] = mma32(th[frag_lo(m, s)], xl[s], x[m]);
-#pragma unroll
-          for (int m = 2 * s; m < 4; ++m) x[m] = mma32(tl[frag_lo(m, s)], xh[s], x[m]);
-#pragma unroll
-          for (int m = 2 * s; m < 4; ++m) x[m] = mma32(th[frag_lo(m, s)], xh[s], x[m]);
-        }
-        // under those: the keys by column, the decay of the state
+        for (int m = 0; m < 2; ++m) x[m] = mma32(th[frag_lo(m, 0)], xh[0], x[m]);
+        y[0] = mma32(th[frag_lo(2, 0)], xh[0], y[0]);
+        y[1] = mma32(th[frag_lo(3, 0)], xh[0], y[1]);
+        residual(1);
         Frag8 ct[2][KT];
 #pragma unroll
         for (int t = 0; t < KT; ++t) ct[0][t] = key_frag(Kt, KP, t, 0, lane);
-        f32x4 wb[4];
 #pragma unroll
         for (int m = 0; m < 4; ++m) wb[m] = at4(wB, m);
-        const float eEnd = eG[63];
-#pragma unroll
-        for (int t = 0; t < KT; ++t) S[t] *= eEnd;
+        pipe<12, 4, 2>();
         SSMVJP_FENCE();
-        // S = e^{G_63} S0 + K^T (e^{G_63 - G} beta r), u in three parts
+        // 4: contraction over tiles 2 and 3; u = e^{G_63 - G} beta r of tiles 0 and 1, in three parts
+        y[0] = mma32(th[frag_lo(2, 1)], xl[1], y[0]);
+        y[1] = mma32(th[frag_lo(3, 1)], xl[1], y[1]);
+        y[0] = mma32(tl[frag_lo(2, 1)], xh[1], y[0]);
+        y[1] = mma32(tl[frag_lo(3, 1)], xh[1], y[1]);
+        y[0] = mma32(th[frag_lo(2, 1)], xh[1], y[0]);
+        y[1] = mma32(th[frag_lo(3, 1)], xh[1], y[1]);
+        Frag8 uh[2], um[2], ul[2];
+        split8x3(x[0] * wb[0], x[1] * wb[1], uh[0], um[0], ul[0]);
+        Ro[0] = x[0];
+        Ro[64] = x[1];
+        pipe<6, 8, 0>();
+        SSMVJP_FENCE();
+        // 5: S = e^{G_63} S0 + K^T u, tokens of tiles 0 and 1; u of tiles 2 and 3
 #pragma unroll
-        for (int m = 0; m < 4; ++m) Ro[m * 64] = x[m];
+        for (int t = 0; t < KT; ++t) S[t] = mma32(ct[0][t], ul[0], S[t]);
 #pragma unroll
-        for (int s = 0; s < 2; ++s) {
-          Frag8 uh, um, ul;
-          split8x3(x[2 * s] * wb[2 * s], x[2 * s + 1] * wb[2 * s + 1], uh, um, ul);
-          if (s == 0) {
+        for (int t = 0; t < KT; ++t) S[t] = mma32(ct[0][t], um[0], S[t]);
 #pragma unroll
-            for (int t = 0; t < KT; ++t) ct[1][t] = key_frag(Kt, KP, t, 1, lane);
+        for (int t = 0; t < KT; ++t) S[t] = mma32(ct[0][t], uh[0], S[t]);
+        x[2] += y[0];
+        x[3] += y[1];
+        split8x3(x[2] * wb[2], x[3] * wb[3], uh[1], um[1], ul[1]);
+        Ro[128] = x[2];
+        Ro[192] = x[3];
+#pragma unroll
+        for (int t = 0; t < KT; ++t) ct[1][t] = key_frag(Kt, KP, t, 1, lane);
+        pipe<3 * KT, 3, 1>();
+        SSMVJP_FENCE();
+        // 6: tokens of tiles 2 and 3, two state tiles at a time; the parts of those that are done
+#pragma unroll
+        for (int s = 0; s < KS; ++s) {
+          S[2 * s] = mma32(ct[1][2 * s], ul[1], S[2 * s]);
+          S[2 * s + 1] = mma32(ct[1][2 * s + 1], ul[1], S[2 * s + 1]);
+          S[2 * s] = mma32(ct[1][2 * s], um[1], S[2 * s]);
+          S[2 * s + 1] = mma32(ct[1][2 * s + 1], um[1], S[2 * s + 1]);
+          S[2 * s] = mma32(ct[1][2 * s], uh[1], S[2 * s]);
+          S[2 * s + 1] = mma32(ct[1][2 * s + 1], uh[1], S[2 * s + 1]);
+          if (s > 0) {
+            split8(S[2 * s - 2], S[2 * s - 1], sh[s - 1], sl[s - 1]);
+            pipe<6, 4, 0>();
           }
-#pragma unroll
-          for (int t = 0; t < KT; ++t) S[t] = mma32(ct[s][t], ul, S[t]);
-#pragma unroll
-          for (int t = 0; t < KT; ++t) S[t] = mma32(ct[s][t], um, S[t]);
-#pragma unroll
-          for (int t = 0; t < KT; ++t) S[t] = mma32(ct[s][t], uh, S[t]);
+          SSMVJP_FENCE();
         }
-#pragma unroll
-        for (int s = 0; s < KS; ++s) split8(S[2 * s], S[2 * s + 1], sh[s], sl[s]);
+        split8(S[KT - 2], S[KT - 1], sh[KS - 1], sl[KS - 1]);
       }
       __syncthreads();
     }

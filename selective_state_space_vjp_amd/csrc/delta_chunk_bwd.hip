@@ -262,261 +262,308 @@ __global__ void __launch_bounds__(64 * NW) __attribute__((amdgpu_waves_per_eu(2,
 // ---------------------------------------------------------------------------
 // gradients of one chunk of one qk head
 // ---------------------------------------------------------------------------
-// Four waves, wave w owning row tile w of every 64-row result.  The columns of
-// V go by 32 (one contraction step): r, mu (two parts), S0, dS (one part) of
-// the slice are brought to LDS as [v][row] tiles, whose transposed reads are
-// the operands with the contraction over v.
+// Eight waves: wave (wr = w % 4, half = w / 4) owns row tile wr of every 64-row
+// result and one half of the key columns; of the pair terms, half 0 forms dD
+// and half 1 E.  The columns of V go by 32 (one contraction step): r, mu (two
+// parts), S0, dS (one part) of the slice are brought to LDS as [v][row] tiles,
+// whose transposed reads are the operands with the contraction over v.
+constexpr int GRADS_NTH = 512;
+
+// Row pitches of the tiles: 40 bytes past a multiple of 128.  The 16 rows of a
+// fragment read meet 16 different pairs of banks, the 4 rows of a transposed
+// read overlap in 24 bytes of 128, and, unlike in a swizzled tile, every
+// fragment is the lane's own address plus a constant: swizzled, the addresses
+// alone took more registers than there are.
+constexpr int P64 = 64 + 20;
+__device__ __forceinline__ Frag8 prow(const bf16* t, int pitch, int m, int s, int lane) {
+  return {ld_colk(t, pitch, 16 * m, 32 * s, lane).v, ld_colk(t, pitch, 16 * m, 32 * s + 16, lane).v};
+}
+__device__ __forceinline__ Frag8 pcol(const bf16* t, int pitch, int m, int s, int lane) {
+  return {ld_rowk(t, pitch, 32 * s, 16 * m, lane).v, ld_rowk(t, pitch, 32 * s + 16, 16 * m, lane).v};
+}
+__device__ __forceinline__ void pstore(bf16* t, int pitch, int row, int col, const u32x4& u) {
+  typedef unsigned u32x2 __attribute__((ext_vector_type(2)));
+  u32x2* d = (u32x2*)(t + row * pitch + col);
+  d[0] = u32x2{u[0], u[1]};
+  d[1] = u32x2{u[2], u[3]};
+}
+
 template <int KP>
-__global__ void __launch_bounds__(256) delta_chunk_grads_kernel(DeltaChunkArgs a) {
-  constexpr int KS = KP / 32, KT = KP / 16;
-  constexpr int NS = 2 * KS * 64 / 256;  // 16-byte pieces per thread of a slice of S0 (or dS)
-  __shared__ __attribute__((aligned(16))) bf16 Kb[64 * KP], Qb[64 * KP];
-  // the slice's tiles; behind the slices the same memory holds dD^T and E^T
-  __shared__ __attribute__((aligned(16))) bf16 buf[4 * 32 * 64 + 2 * 32 * KP];
-  __shared__ __attribute__((aligned(16))) float Gs[64], Bs[64], rowM[64], colM[4][64], colA[4][64];
-  bf16 *rH = buf, *rL = buf + 32 * 64, *mH = buf + 2 * 32 * 64, *mL = buf + 3 * 32 * 64, *sT = buf + 4 * 32 * 64,
-       *dT = sT + 32 * KP;
-  bf16 *Dt = buf, *Et = buf + 64 * 64;
-  const int tid = threadIdx.x, lane = tid & 63, w = tid >> 6, c = lane & 15, q = lane >> 4;
-  const i64 h = blockIdx.x % a.H, slot = blockIdx.x / a.H;
+__global__ void __launch_bounds__(GRADS_NTH, 2) delta_chunk_grads_kernel(DeltaChunkArgs a) {
+  constexpr int KS = KP / 32, KT = KP / 16, PK = KP + 20, HT = KT / 2;  // HT: key tiles of a wave
+  constexpr int NP = 4 * KS * 64 / GRADS_NTH;             // 16-byte pieces per thread of a slice of S0 and dS
+  __shared__ __attribute__((aligned(16))) bf16 Kb[64 * PK], Qb[64 * PK];
+  // the slice's tiles; behind the slices the same memory holds dD^T and E^T, two parts each
+  __shared__ __attribute__((aligned(16))) bf16 buf[16 * P64 * 16];
+  __shared__ __attribute__((aligned(16))) float Gs[64], Bs[64], rowM[2][64], colM[2][4][64], colA[4][64];
+  __shared__ float rowG[8][64], rowB[8][64], tails[8];  // the reverse walk's row sums, by wave
+  typedef unsigned u32x2 __attribute__((ext_vector_type(2)));
+  bf16 *rH = buf, *mH = buf + 2 * 32 * P64;  // each followed by its lo part
+  bf16* sT = buf + 4 * 32 * P64;             // [S0, dS][32][KP]
+  const int tid = threadIdx.x, lane = tid & 63, w = __builtin_amdgcn_readfirstlane(tid >> 6), c = lane & 15, q = lane >> 4;
+  const int wr = w & 3, half = w >> 2;
+  const unsigned H32 = (unsigned)a.H;
+  const i64 h = blockIdx.x % H32, slot = blockIdx.x / H32;
   const ChunkAt at = chunk_at(a.seq, slot, lane);
   if (at.rows == 0) return;
   {
-    constexpr int N = 64 * KP / 8 / 256;
+    constexpr int N = 64 * KP / 8 / GRADS_NTH;
     const brsrc rk = row_rsrc(a.k, at.tok0, at.rows, a.H, h, a.K), rq = row_rsrc(a.q, at.tok0, at.rows, a.H, h, a.K);
     u32x4 tk[N], tq[N];
 #pragma unroll
     for (int i = 0; i < N; ++i) {
-      const int p = tid + 256 * i, row = p / (KP / 8), col = p % (KP / 8) * 8;
+      const int p = tid + GRADS_NTH * i, row = p / (KP / 8), col = p % (KP / 8) * 8;
       const unsigned o = col < a.K ? (unsigned)(((i64)row * a.H * a.K + col) * 2) : BUF_OOB;
       tk[i] = bload16(rk, o);
       tq[i] = bload16(rq, o);
     }
 #pragma unroll
     for (int i = 0; i < N; ++i) {
-      const int p = tid + 256 * i;
-      st16_xs(Kb, KP, p / (KP / 8), p % (KP / 8) * 8, tk[i]);
-      st16_xs(Qb, KP, p / (KP / 8), p % (KP / 8) * 8, tq[i]);
+      const int p = tid + GRADS_NTH * i;
+      pstore(Kb, PK, p / (KP / 8), p % (KP / 8) * 8, tk[i]);
+      pstore(Qb, PK, p / (KP / 8), p % (KP / 8) * 8, tq[i]);
     }
   }
-  __syncthreads();
-  // lane: column j = 16 b + c, rows i = 16 w + 4 q + r
-  f32x4 kk[4], qk[4];
+  f32x4 dq[HT], dk[HT];  // rows i = 16 wr + 4 q + r, column 16 (HT half + t) + c
 #pragma unroll
-  for (int b = 0; b < 4; ++b) {
-    kk[b] = zero4();
-    qk[b] = zero4();
-    if (b <= w) {
-#pragma unroll
-      for (int s = 0; s < KS; ++s) {
-        const Frag8 y = xs_frag(Kb, KP, b, s, lane);
-        kk[b] = mma32(xs_frag(Kb, KP, w, s, lane), y, kk[b]);
-        qk[b] = mma32(xs_frag(Qb, KP, w, s, lane), y, qk[b]);
-      }
-    }
-  }
-  f32x4 dq[KT], dk[KT];  // rows i = 16 w + 4 q + r, column 16 t + c
-#pragma unroll
-  for (int t = 0; t < KT; ++t) dq[t] = zero4(), dk[t] = zero4();
+  for (int t = 0; t < HT; ++t) dq[t] = zero4(), dk[t] = zero4();
 
-  const i64 nsl = (a.nvt + 1) / 2;
+  const int nsl = (int)(a.nvt + 1) / 2;
   for (i64 rr = 0; rr < a.rep; ++rr) {
     const i64 hv = h * a.rep + rr, cu = slot * a.HV + hv;
-    u32x4 pr[4], ps[NS], pd[NS];
-    const brsrc ro = row_rsrc(a.d_o, at.tok0, at.rows, a.HV, hv, a.V);
-    typedef unsigned u32x2 __attribute__((ext_vector_type(2)));
+    u32x4 pr[2], ps[NP];
     u32x2 po[2];
-    // piece p of a slice: tile p / (64 n) of the two, step, lane; tiles past V read as zeros
-    auto fetch = [&](i64 sl) {
-      {
-        const i64 t = sl * 2 + (tid >> 7);
-        const i64 o = (cu * a.nvt + t) * 256 + (w & 1) * 64 + lane;
-        const bool in = t < a.nvt;
-        pr[0] = in ? ((const u32x4*)a.rw)[o] : zero_u4();
-        pr[1] = in ? ((const u32x4*)a.rw)[o + 128] : zero_u4();
-        pr[2] = in ? ((const u32x4*)a.muw)[o] : zero_u4();
-        pr[3] = in ? ((const u32x4*)a.muw)[o + 128] : zero_u4();
+    const brsrc ro = row_rsrc(a.d_o, at.tok0, at.rows, a.HV, hv, a.V);
+    // tiles past V lie past the resources: zeros, without a branch
+    const brsrc rm4 = make_rsrc((w < 4 ? a.rw : a.muw) + cu * a.nvt * 2048, (unsigned)(a.nvt * 4096));
+    const brsrc rS = make_rsrc(a.Sw + cu * a.nvt * KS * 1024, (unsigned)(a.nvt * KS * 2048));
+    const brsrc rD = make_rsrc(a.dSw + cu * a.nvt * KS * 512, (unsigned)(a.nvt * KS * 1024));
+    auto fetch = [&](int sl) {
+      {  // waves 0 .. 3: r, the others mu; hi and lo of one fragment
+        const unsigned o = (unsigned)(((sl * 2 + (w >> 1 & 1)) * 256 + (w & 1) * 64 + lane) * 16);
+        pr[0] = bload16(rm4, o);
+        pr[1] = bload16(rm4, o + 2048u);
       }
 #pragma unroll
-      for (int i = 0; i < NS; ++i) {
-        const int p = tid + 256 * i;
-        const i64 t = sl * 2 + p / (64 * KS);
-        const i64 o = p / 64 % KS * 64 + lane;
-        const bool in = t < a.nvt;
-        ps[i] = in ? ((const u32x4*)a.Sw)[(cu * a.nvt + t) * 2 * KS * 64 + o] : zero_u4();
-        pd[i] = in ? ((const u32x4*)a.dSw)[(cu * a.nvt + t) * KS * 64 + o] : zero_u4();
+      for (int i = 0; i < NP; ++i) {
+        const int p = w + GRADS_NTH / 64 * i, t = sl * 2 + p / KS % 2, st = p % KS;
+        if (p < 2 * KS) ps[i] = bload16(rS, (unsigned)(((t * 2 * KS + st) * 64 + lane) * 16));
+        else ps[i] = bload16(rD, (unsigned)(((t * KS + st) * 64 + lane) * 16));
       }
 #pragma unroll
       for (int e = 0; e < 2; ++e) {
-        const i64 col = sl * 32 + 16 * e + 4 * q;
+        const int col = sl * 32 + 16 * e + 4 * q;
         po[e] = __builtin_bit_cast(u32x2, __builtin_amdgcn_raw_buffer_load_b64(
-            ro, col < a.V ? (int)(((16 * w + c) * a.HV * a.V + col) * 2) : (int)BUF_OOB, 0, 0));
+            ro, col < a.V ? (int)(((16 * wr + c) * a.HV * a.V + col) * 2) : (int)BUF_OOB, 0, 0));
       }
     };
-    auto put = [&](bf16* t, int pitch, int row, int s, const u32x4& u) {  // a fragment's two 4-element runs
-      *(u32x2*)(t + row * pitch + xsw_off(row, 32 * s + 4 * q)) = u32x2{u[0], u[1]};
-      *(u32x2*)(t + row * pitch + xsw_off(row, 32 * s + 16 + 4 * q)) = u32x2{u[2], u[3]};
+    auto put = [&](bf16* t, int row, int s, const u32x4& u) {  // a fragment's two 4-element runs
+      *(u32x2*)(t + row * P64 + 32 * s + 4 * q) = u32x2{u[0], u[1]};
+      *(u32x2*)(t + row * P64 + 32 * s + 16 + 4 * q) = u32x2{u[2], u[3]};
     };
     fetch(0);
-    __syncthreads();  // the previous head's readers are done
-    if (w == 0) {
-      Gs[lane] = a.G[cu * 64 + lane];
-      Bs[lane] = lane < at.rows ? a.beta[(at.tok0 + lane) * a.HV + hv] : 0.0f;
+    // this wave's share of the walks' row sums (tiles w, w + 8, ..) and, for wave 0, the gates
+    float dG = 0.0f, db = 0.0f, tail = 0.0f, G0 = 0.0f, b0 = 0.0f;
+    for (int t = w; t < (int)a.nvt; t += 8) {
+      const float* rp = a.rowp + (cu * a.nvt + t) * 192 + lane;
+      dG += rp[0] + rp[64];
+      db += rp[128];
+      tail += a.endp[cu * a.nvt + t];
     }
-    f32x4 dp[4], nn[4], x1[KT];
+    if (w == 0) {
+      G0 = a.G[cu * 64 + lane];
+      b0 = lane < at.rows ? a.beta[(at.tok0 + lane) * a.HV + hv] : 0.0f;
+    }
+    __syncthreads();  // the previous head's readers are done; k and q are in LDS
+    rowG[w][lane] = dG;
+    rowB[w][lane] = db;
+    if (lane == 0) tails[w] = tail;
+    if (w == 0) {
+      Gs[lane] = G0;
+      Bs[lane] = b0;
+    }
+    f32x4 pp[4], x1[HT], y2[HT], y3[HT];  // pp: dO . r (half 0) or mu . r; dO S0^T, mu S0^T, r dS^T
 #pragma unroll
-    for (int b = 0; b < 4; ++b) dp[b] = zero4(), nn[b] = zero4();
+    for (int b = 0; b < 4; ++b) pp[b] = zero4();
 #pragma unroll
-    for (int t = 0; t < KT; ++t) x1[t] = zero4();
-    for (i64 sl = 0; sl < nsl; ++sl) {
+    for (int t = 0; t < HT; ++t) x1[t] = zero4(), y2[t] = zero4(), y3[t] = zero4();
+    for (int sl = 0; sl < nsl; ++sl) {
       if (sl) __syncthreads();
       {
-        const int row = 16 * (tid >> 7) + c;
-        put(rH, 64, row, w & 1, pr[0]);
-        put(rL, 64, row, w & 1, pr[1]);
-        put(mH, 64, row, w & 1, pr[2]);
-        put(mL, 64, row, w & 1, pr[3]);
+        bf16* d = w < 4 ? rH : mH;
+        const int row = 16 * (w >> 1 & 1) + c;
+        put(d, row, w & 1, pr[0]);
+        put(d + 32 * P64, row, w & 1, pr[1]);
 #pragma unroll
-        for (int i = 0; i < NS; ++i) {
-          const int p = tid + 256 * i;
-          const int row = 16 * (p / (64 * KS)) + c, col = 32 * (p / 64 % KS) + 8 * q;
-          st16_xs(sT, KP, row, col, ps[i]);
-          st16_xs(dT, KP, row, col, pd[i]);
+        for (int i = 0; i < NP; ++i) {
+          const int p = w + GRADS_NTH / 64 * i, arr = p / (2 * KS), t2 = p / KS % 2, st = p % KS;
+          pstore(sT + arr * 32 * PK, PK, 16 * t2 + c, 32 * st + 8 * q, ps[i]);
         }
       }
       const Frag8 of = {__builtin_bit_cast(s16x4, po[0]), __builtin_bit_cast(s16x4, po[1])};
       __syncthreads();
       if (sl + 1 < nsl) fetch(sl + 1);
-      const float Gi = Gs[16 * w + c], eg = exp_hw(Gi), we = exp_hw(Gs[63] - Gi) * Bs[16 * w + c];
-      const Frag8 mh = col_frag(mH, 64, w, 0, lane), ml = col_frag(mL, 64, w, 0, lane);
-      // dv = mu, rounded: its hi part
-#pragma unroll
-      for (int e = 0; e < 2; ++e) {
-        const i64 col = sl * 32 + 16 * e + 4 * q;
-        if (16 * w + c < at.rows && col < a.V)
-          *(s16x4*)(a.dv + ((at.tok0 + 16 * w + c) * a.HV + hv) * a.V + col) = e ? mh.b : mh.a;
-      }
+      const Frag8 mh = pcol(mH, P64, wr, 0, lane), ml = pcol(mH + 32 * P64, P64, wr, 0, lane);
+      const Frag8 rh = pcol(rH, P64, wr, 0, lane), rl = pcol(rH + 32 * P64, P64, wr, 0, lane);
 #pragma unroll
       for (int b = 0; b < 4; ++b)
-        if (b <= w) {
-          const Frag8 rh = col_frag(rH, 64, b, 0, lane), rl = col_frag(rL, 64, b, 0, lane);
-          dp[b] = mma32(of, rl, dp[b]);
-          nn[b] = mma32(mh, rl, nn[b]);
-          nn[b] = mma32(ml, rh, nn[b]);
-          dp[b] = mma32(of, rh, dp[b]);
-          nn[b] = mma32(mh, rh, nn[b]);
+        if (b <= wr) {
+          const Frag8 bh = pcol(rH, P64, b, 0, lane), bl = pcol(rH + 32 * P64, P64, b, 0, lane);
+          if (half == 0) {
+            pp[b] = mma32(of, bl, pp[b]);
+            pp[b] = mma32(of, bh, pp[b]);
+          } else {
+            pp[b] = mma32(mh, bl, pp[b]);
+            pp[b] = mma32(ml, bh, pp[b]);
+            pp[b] = mma32(mh, bh, pp[b]);
+          }
         }
-      // -e^G mu and e^{G_63 - G} beta r, rounded once
-      const Frag8 rw = col_frag(rH, 64, w, 0, lane);
-      const Frag8 ms = {pack4(-eg * unpack4(mh.a)), pack4(-eg * unpack4(mh.b))};
-      const Frag8 rs = {pack4(we * unpack4(rw.a)), pack4(we * unpack4(rw.b))};
 #pragma unroll
-      for (int t = 0; t < KT; ++t) {
-        const Frag8 sf = col_frag(sT, KP, t, 0, lane), df = col_frag(dT, KP, t, 0, lane);
+      for (int t = 0; t < HT; ++t) {
+        const Frag8 sf = pcol(sT, PK, HT * half + t, 0, lane), df = pcol(sT + 32 * PK, PK, HT * half + t, 0, lane);
         x1[t] = mma32(of, sf, x1[t]);
-        dk[t] = mma32(ms, sf, dk[t]);
-        dk[t] = mma32(rs, df, dk[t]);
+        y2[t] = mma32(ml, sf, y2[t]);
+        y3[t] = mma32(rl, df, y3[t]);
+        y2[t] = mma32(mh, sf, y2[t]);
+        y3[t] = mma32(rh, df, y3[t]);
+      }
+      // dv = mu, rounded: its hi part
+      if (half == 1) {
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          const int col = sl * 32 + 16 * e + 4 * q;
+          if (16 * wr + c < at.rows && col < a.V)
+            *(s16x4*)(a.dv + ((at.tok0 + 16 * wr + c) * a.HV + hv) * a.V + col) = e ? mh.b : mh.a;
+        }
       }
     }
+    // rows i = 16 wr + 4 q + r
+    const f32x4 Gi = *(const f32x4*)(Gs + 16 * wr + 4 * q), Bi = *(const f32x4*)(Bs + 16 * wr + 4 * q);
+    const float Ge = Gs[63];
+    f32x4 eg, we;
+#pragma unroll
+    for (int r = 0; r < 4; ++r) eg[r] = exp_hw(Gi[r]), we[r] = exp_hw(Ge - Gi[r]) * Bi[r];
+#pragma unroll
+    for (int t = 0; t < HT; ++t) {
+      dq[t] += a.scale * eg * x1[t];
+      dk[t] += we * y3[t] - eg * y2[t];
+    }
     __syncthreads();  // the slices' tiles are free
-    // pair terms; column j = 16 b + c, rows i = 16 w + 4 q + r
-    const f32x4 Gi = *(const f32x4*)(Gs + 16 * w + 4 * q);
+    // pair terms: dD (half 0) or E (half 1); column j = 16 b + c
     f32x4 rm = zero4();
+    bf16* const Pt = buf + half * 2 * 64 * P64;  // [hi, lo][64][64], transposed: row j
+    Frag8 rf[KS];
+#pragma unroll
+    for (int s = 0; s < KS; ++s) rf[s] = prow(half ? Kb : Qb, PK, wr, s, lane);
+    f32x4 kq[4];  // q_i . k_j (half 0) or k_i . k_j
 #pragma unroll
     for (int b = 0; b < 4; ++b) {
-      f32x4 D = zero4(), E = zero4();
+      kq[b] = zero4();
+      if (b <= wr) {
+#pragma unroll
+        for (int s = 0; s < KS; ++s) kq[b] = mma32(rf[s], prow(Kb, PK, b, s, lane), kq[b]);
+      }
+    }
+#pragma unroll
+    for (int b = 0; b < 4; ++b) {
+      f32x4 x = zero4();
       float cm = 0.0f, ca = 0.0f;
-      if (b <= w) {
-        const int j = 16 * b + c;
-        const float Gj = Gs[j], bj = Bs[j];
+      const int j = 16 * b + c;
+      if (b <= wr) {
+        const float Gj = Gs[j], bj = Bs[j] * (half ? -1.0f : a.scale);
 #pragma unroll
         for (int r = 0; r < 4; ++r) {
-          const int i = 16 * w + 4 * q + r;
-          const float gam = i >= j ? exp_hw(Gi[r] - Gj) : 0.0f;
-          D[r] = a.scale * bj * dp[b][r] * gam;
+          const int i = 16 * wr + 4 * q + r;
+          const float gam = exp_hw(i >= j ? Gi[r] - Gj : 0.0f);
+          if (i > j || (half == 0 && i == j)) x[r] = bj * pp[b][r] * gam;
           if (i > j) {
-            E[r] = -bj * nn[b][r] * gam;
-            const float m = D[r] * qk[b][r] + E[r] * kk[b][r];
+            const float m = x[r] * kq[b][r];
             rm[r] += m;
             cm += m;
-            ca += gam * kk[b][r] * nn[b][r];
-          } else if (i < j) {
-            D[r] = 0.0f;
+            ca += gam * kq[b][r] * pp[b][r];
           }
         }
       }
       cm = sum4q(cm);
-      ca = sum4q(ca);
-      if (q == 0) colM[w][16 * b + c] = cm, colA[w][16 * b + c] = ca;
-      const int j = 16 * b + c, i0 = 16 * w + 4 * q;
-      *(s16x4*)(Dt + j * 64 + xsw_off(j, i0)) = pack4(D);
-      *(s16x4*)(Et + j * 64 + xsw_off(j, i0)) = pack4(E);
+      if (half) ca = sum4q(ca);
+      if (q == 0) {
+        colM[half][wr][j] = cm;
+        if (half) colA[wr][j] = ca;
+      }
+      s16x4 hi, lo;
+      split4(x, hi, lo);
+      const int o = j * P64 + 16 * wr + 4 * q;
+      *(s16x4*)(Pt + o) = hi;
+      *(s16x4*)(Pt + 64 * P64 + o) = lo;
     }
 #pragma unroll
     for (int r = 0; r < 4; ++r) rm[r] = sum16(rm[r]);
-    if (c == 0) *(f32x4*)(rowM + 16 * w + 4 * q) = rm;
-    // dq += scale e^G (dO S0^T)
-#pragma unroll
-    for (int t = 0; t < KT; ++t)
-#pragma unroll
-      for (int r = 0; r < 4; ++r) dq[t][r] += a.scale * exp_hw(Gi[r]) * x1[t][r];
+    if (c == 0) *(f32x4*)(rowM[half] + 16 * wr + 4 * q) = rm;
     __syncthreads();
     // dq += dD K, dk += E K (rows i); dk += dD^T Q + E^T K (rows j)
-    Frag8 dr[2], er[2], dc[2], ec[2];
 #pragma unroll
     for (int s = 0; s < 2; ++s) {
-      dr[s] = col_frag(Dt, 64, w, s, lane);
-      er[s] = col_frag(Et, 64, w, s, lane);
-      dc[s] = xs_frag(Dt, 64, w, s, lane);
-      ec[s] = xs_frag(Et, 64, w, s, lane);
-    }
+      const bool lower = s <= wr >> 1, upper = s >= wr >> 1;
+      Frag8 dr[2], er[2], dc[2], ec[2];
 #pragma unroll
-    for (int t = 0; t < KT; ++t)
+      for (int e = 0; e < 2; ++e) {
+        const bf16 *D = buf + e * 64 * P64, *E = buf + (2 + e) * 64 * P64;
+        dr[e] = pcol(D, P64, wr, s, lane);
+        er[e] = pcol(E, P64, wr, s, lane);
+        dc[e] = prow(D, P64, wr, s, lane);
+        ec[e] = prow(E, P64, wr, s, lane);
+      }
 #pragma unroll
-      for (int s = 0; s < 2; ++s) {
-        const Frag8 kf = col_frag(Kb, KP, t, s, lane);
-        if (s <= w >> 1) {
-          dq[t] = mma32(dr[s], kf, dq[t]);
-          dk[t] = mma32(er[s], kf, dk[t]);
+      for (int t = 0; t < HT; ++t) {
+        const Frag8 kf = pcol(Kb, PK, HT * half + t, s, lane);
+        if (lower) {
+          dq[t] = mma32(dr[1], kf, dq[t]);
+          dk[t] = mma32(er[1], kf, dk[t]);
+          dq[t] = mma32(dr[0], kf, dq[t]);
+          dk[t] = mma32(er[0], kf, dk[t]);
         }
-        if (s >= w >> 1) {
-          dk[t] = mma32(ec[s], kf, dk[t]);
-          dk[t] = mma32(dc[s], col_frag(Qb, KP, t, s, lane), dk[t]);
+        if (upper) {
+          const Frag8 qf = pcol(Qb, PK, HT * half + t, s, lane);
+          dk[t] = mma32(ec[1], kf, dk[t]);
+          dk[t] = mma32(dc[1], qf, dk[t]);
+          dk[t] = mma32(ec[0], kf, dk[t]);
+          dk[t] = mma32(dc[0], qf, dk[t]);
         }
       }
+    }
     // dbeta, dg
     if (w == 0) {
-      const float* rp = a.rowp + cu * a.nvt * 3 * 64;
       float dG = 0.0f, db = 0.0f, tail = 0.0f;
-      for (i64 t = 0; t < a.nvt; ++t) {
-        dG += rp[t * 192 + lane] + rp[t * 192 + 64 + lane];
-        db += rp[t * 192 + 128 + lane];
-        tail += a.endp[cu * a.nvt + t];
-      }
-      dG += rowM[lane] - ((colM[0][lane] + colM[1][lane]) + (colM[2][lane] + colM[3][lane]));
-      db -= (colA[0][lane] + colA[1][lane]) + (colA[2][lane] + colA[3][lane]);
+#pragma unroll
+      for (int i = 0; i < 8; ++i) dG += rowG[i][lane], db += rowB[i][lane], tail += tails[i];
+      float col = 0.0f, ca = 0.0f;
+#pragma unroll
+      for (int i = 0; i < 4; ++i) col += colM[0][i][lane] + colM[1][i][lane], ca += colA[i][lane];
+      dG += rowM[0][lane] + rowM[1][lane] - col;
       const float sum = wave_incl_suffix(dG, lane) + tail;
       if (lane < at.rows) {
         const i64 o = (at.tok0 + lane) * a.HV + hv;
         a.dg[o] = sum;
-        a.dbeta[o] = db;
+        a.dbeta[o] = db - ca;
       }
     }
   }
   // out: row i, 16 columns at a time
 #pragma unroll
-  for (int t = 0; t < KT; ++t)
-    if (16 * t < a.K) {
+  for (int t = 0; t < HT; ++t) {
+    const int k0 = 16 * (HT * half + t);
+    if (k0 < a.K) {
 #pragma unroll
       for (int r = 0; r < 4; ++r) {
-        const int i = 16 * w + 4 * q + r;
+        const int i = 16 * wr + 4 * q + r;
         if (i < at.rows) {
-          const i64 o = ((at.tok0 + i) * a.H + h) * a.K + 16 * t + c;
+          const i64 o = ((at.tok0 + i) * a.H + h) * a.K + k0 + c;
           a.dq[o] = (bf16)dq[t][r];
           a.dk[o] = (bf16)dk[t][r];
         }
       }
     }
+  }
 }
 
 template <int KP>
@@ -524,7 +571,7 @@ void launch_rev_grads(const DeltaChunkArgs& a, hipStream_t s) {
   const i64 blocks = walk_blocks(a.seq.nseq * a.HV, (a.V + 31) / 32);
   hipLaunchKernelGGL((delta_chunk_rev_kernel<KP, 2>), dim3((unsigned)blocks), dim3(128), (RevLds<KP, 2>::TOTAL), s, a);
   if (a.nslots > 0)
-    hipLaunchKernelGGL((delta_chunk_grads_kernel<KP>), dim3((unsigned)(a.nslots * a.H)), dim3(256), 0, s, a);
+    hipLaunchKernelGGL((delta_chunk_grads_kernel<KP>), dim3((unsigned)(a.nslots * a.H)), dim3(GRADS_NTH), 0, s, a);
 }
 
 struct BwdPlan {

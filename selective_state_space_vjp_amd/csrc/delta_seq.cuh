@@ -36,7 +36,7 @@ struct DeltaSeqs {
   }
   // the sequence that owns a chunk slot; called by whole waves
   __device__ __forceinline__ i64 of_slot(i64 slot, int lane) const {
-    if (!off) return slot / per;
+    if (!off) return (unsigned)slot / (unsigned)per;
     i64 s = -1;  // the last sequence whose first slot is not behind `slot` (slot 0 is sequence 0's)
     for (i64 s0 = 0; s0 < nseq; s0 += 64) {
       const i64 i = s0 + lane;
