@@ -48,15 +48,11 @@ struct DeltaChunkArgs {
   float* G;   // [64]
   bf16* Tt;   // [6][2][64][8] fragments of T^T - I                  (backward from here on)
   bf16* Pt;   // [6][2][64][8] fragments of scale P^T
-  // per 16-column tile (cell * nvt + tile):
-  bf16* Sw;     // [2][KP/32][64][8] fragments of the state before the chunk, hi and lo
-  bf16* rw;     // [2][2][64][8] fragments of r, hi and lo
-  float* Xw;    // [4][64][4] tiles of e^G K S0
-  bf16* dSw;    // [KP/32][64][8] fragments of the state's gradient behind the chunk, hi
-  bf16* muw;    // [2][2][64][8] fragments of mu, hi and lo
-  float* rowp;  // [3][64] sums over the tile's columns of scale e^G dO (Q S0), of the rest of dG_i's row terms,
-                // and of r dU
-  float* endp;  // [1] e^{G_63} <S0, dS> + sum_i su_i
+  // per 16-column tile (cell * nvt + tile), hi and lo parts:
+  bf16* Sw;   // [2][KP/32][64][8] fragments of the state before the chunk
+  bf16* dSw;  // [2][KP/32][64][8] of the state's gradient behind the chunk
+  bf16* rw;   // [2][2][64][8] fragments of r
+  bf16* muw;  // [2][2][64][8] of mu
 };
 
 typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
@@ -217,6 +213,19 @@ __device__ __forceinline__ s16x4 col4(const bf16* t, int pitch, int m, int w, in
 // col0 (rows past the end read as zeros)
 __device__ __forceinline__ u32x4 row_words(const bf16* p, i64 tok0, int rows, i64 heads, i64 h, i64 cols, i64 col0) {
   return rsrc_words_u(p + (tok0 * heads + h) * cols + col0, (unsigned)((((i64)rows - 1) * heads * cols + cols - col0) * 2));
+}
+
+// no instruction moves past here: operands that are read ahead stay ahead
+#define SSMVJP_FENCE() __builtin_amdgcn_sched_barrier(0)
+// asks the scheduler for N times: an MFMA, VALU vector instructions, READ LDS reads
+template <int N, int VALU, int READ>
+__device__ __forceinline__ void pipe() {
+#pragma unroll
+  for (int i = 0; i < N; ++i) {
+    __builtin_amdgcn_sched_group_barrier(0x8, 1, 0);
+    if (VALU) __builtin_amdgcn_sched_group_barrier(0x2, VALU, 0);
+    if (READ) __builtin_amdgcn_sched_group_barrier(0x100, READ, 0);
+  }
 }
 
 struct ChunkAt {

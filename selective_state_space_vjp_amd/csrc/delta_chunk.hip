@@ -255,41 +255,25 @@ __global__ void __launch_bounds__(256, 3) delta_prep_kernel(DeltaChunkArgs a) {
 // walk
 // ---------------------------------------------------------------------------
 // MODE 0: the forward (o, S_final); 1: for the backward, the state before every
-// chunk, r, e^G K S0 and the readout's row sums.
+// chunk and r.
 //
-// Five waves for 32 columns.  Waves 0 and 1 carry the states of 16 columns each
-// and do nothing that the next state does not wait for.  Waves 2 and 3 follow
-// one chunk behind with what is left of the same columns (the readout, or what
-// the backward keeps) from the state's fragments and r, which they get through
-// LDS.  Wave 4 sends for the next chunks' data and prepares the gates.  One wave
-// that does all of it takes 7,600 cycles a chunk at K = 128, 2,000 of them for
-// the readout and 1,100 for issuing the loads.
+// Waves 0 and 1 carry the states of 16 columns each and do nothing that the next
+// state does not wait for.  Forward only: waves 2 and 3 follow one chunk behind
+// with the readout of the same columns, from the state's fragments and r, which
+// they get through LDS.  The last wave sends for the next chunks' data and
+// prepares the gates.  One wave that does all of it takes 7,600 cycles a chunk
+// at K = 128, 2,000 of them for the readout and 1,100 for issuing the loads.
 template <int KP, int MODE>
 struct WalkLds {  // byte offsets
-  static constexpr int K = 0, V = K + 64 * KP * 2, T = V + 4096, ABUF = T + 12 * 1024;        // for waves 0, 1
-  static constexpr int Q = 0, PO = Q + 64 * KP * 2, BBUF = PO + (MODE ? 4096 : 6 * 1024);     // for waves 2, 3
-  static constexpr int B = 2 * ABUF, S = B + 2 * BBUF, SBUF = 2 * KP * 64, R = S + 2 * SBUF;  // S, r: [2 buffers][2 tiles]
-  static constexpr int G = R + 2 * 2 * 4096, TOTAL = G + 3 * 512;                             // gates: [3][e^G, e^{G_63 - G} beta]
+  static constexpr int K = 0, V = K + 64 * KP * 2, T = V + 4096, ABUF = T + 12 * 1024;  // for waves 0, 1
+  static constexpr int Q = 0, P = Q + 64 * KP * 2, BBUF = MODE ? 0 : P + 6 * 1024;      // for the followers
+  static constexpr int B = 2 * ABUF, S = B + 2 * BBUF, SBUF = MODE ? 0 : 2 * KP * 64, R = S + 2 * SBUF;  // [2 buffers][2 tiles]
+  static constexpr int G = R + (MODE ? 0 : 2 * 2 * 4096), TOTAL = G + 3 * 512;  // gates: [3][e^G, e^{G_63 - G} beta]
 };
-
-// no instruction moves past here: operands that are read ahead stay ahead
-#define SSMVJP_FENCE() __builtin_amdgcn_sched_barrier(0)
-
-// asks the scheduler for N times: an MFMA, VALU vector instructions, LDS reads
-template <int N, int VALU, int READ>
-__device__ __forceinline__ void pipe() {
-#pragma unroll
-  for (int i = 0; i < N; ++i) {
-    __builtin_amdgcn_sched_group_barrier(0x8, 1, 0);
-    if (VALU) __builtin_amdgcn_sched_group_barrier(0x2, VALU, 0);
-    if (READ) __builtin_amdgcn_sched_group_barrier(0x100, READ, 0);
-  }
-}
-
-constexpr int WALK_NTH = 320;
+constexpr int walk_nth(int mode) { return mode ? 192 : 320; }
 
 template <int KP, int MODE>
-__global__ void __launch_bounds__(WALK_NTH) __attribute__((amdgpu_waves_per_eu(2, 2)))
+__global__ void __launch_bounds__(walk_nth(MODE)) __attribute__((amdgpu_waves_per_eu(2, 2)))
 delta_chunk_walk_kernel(DeltaChunkArgs a) {
   constexpr int KS = KP / 32, KT = KP / 16;  // 32-steps and 16-tiles of K
   constexpr bool FWD = MODE == 0;
@@ -325,8 +309,12 @@ delta_chunk_walk_kernel(DeltaChunkArgs a) {
         const unsigned char* const buf = smem_raw + bf * L::ABUF;
         const bf16 *Kt = (const bf16*)(buf + L::K), *Vt = (const bf16*)(buf + L::V);
         const u32x4* Tf = (const u32x4*)(buf + L::T) + lane;
-        u32x4* So = (u32x4*)(smem_raw + L::S + bf * L::SBUF + t16 * (L::SBUF / 2)) + lane;
+        // the state's parts and r: to the follower, or to memory
+        const i64 tile = (cell0 + ch * a.HV) * a.nvt + vt;
+        u32x4* So = FWD ? (u32x4*)(smem_raw + L::S + bf * L::SBUF + t16 * (L::SBUF / 2)) + lane
+                        : (u32x4*)(a.Sw + tile * 2 * KS * 512) + lane;
         f32x4* Ro = (f32x4*)(smem_raw + L::R + (bf * 2 + t16) * 4096) + lane;
+        u32x4* Rw = (u32x4*)(a.rw + tile * 4 * 512) + lane;
         const float *eG = gates(ch), *wB = eG + 64;
         // Six stretches of MFMAs, each with the vector and LDS work of its neighbours between them: a 16x16x32
         // MFMA holds the matrix pipe for 16 cycles, in which three vector instructions issue.
@@ -364,14 +352,11 @@ delta_chunk_walk_kernel(DeltaChunkArgs a) {
           x[2] = mma32(kg[0][s], sh[s], x[2]);
           x[3] = mma32(kg[1][s], sh[s], x[3]);
         }
-        f32x4* X = (f32x4*)(a.Xw + ((cell0 + ch * a.HV) * a.nvt + vt) * 1024) + lane;
         Frag8 xh[2], xl[2], th[6], tl[6];
         auto residual = [&](int s) {
 #pragma unroll
           for (int m = 2 * s; m < 2 * s + 2; ++m) {
-            x[m] *= e[m];
-            if constexpr (!FWD) X[m * 64] = x[m];
-            x[m] = unpack4(v[m]) - x[m];
+            x[m] = unpack4(v[m]) - e[m] * x[m];
           }
           split8(x[2 * s], x[2 * s + 1], xh[s], xl[s]);
         };
@@ -413,8 +398,18 @@ delta_chunk_walk_kernel(DeltaChunkArgs a) {
         y[1] = mma32(th[frag_lo(3, 1)], xh[1], y[1]);
         Frag8 uh[2], um[2], ul[2];
         split8x3(x[0] * wb[0], x[1] * wb[1], uh[0], um[0], ul[0]);
-        Ro[0] = x[0];
-        Ro[64] = x[1];
+        auto keep = [&](int s) {
+          if constexpr (FWD) {
+            Ro[2 * s * 64] = x[2 * s];
+            Ro[(2 * s + 1) * 64] = x[2 * s + 1];
+          } else {
+            Frag8 rh, rl;
+            split8(x[2 * s], x[2 * s + 1], rh, rl);
+            Rw[s * 64] = as_u4(rh);
+            Rw[128 + s * 64] = as_u4(rl);
+          }
+        };
+        keep(0);
         pipe<6, 8, 0>();
         SSMVJP_FENCE();
         // 5: S = e^{G_63} S0 + K^T u, tokens of tiles 0 and 1; u of tiles 2 and 3
@@ -427,8 +422,7 @@ delta_chunk_walk_kernel(DeltaChunkArgs a) {
         x[2] += y[0];
         x[3] += y[1];
         split8x3(x[2] * wb[2], x[3] * wb[3], uh[1], um[1], ul[1]);
-        Ro[128] = x[2];
-        Ro[192] = x[3];
+        keep(1);
 #pragma unroll
         for (int t = 0; t < KT; ++t) ct[1][t] = key_frag(Kt, KP, t, 1, lane);
         pipe<3 * KT, 3, 1>();
@@ -452,7 +446,7 @@ delta_chunk_walk_kernel(DeltaChunkArgs a) {
       }
       __syncthreads();
     }
-    __syncthreads();  // the period in which the followers finish the last chunk
+    if constexpr (FWD) __syncthreads();  // the period in which the followers finish the last chunk
     if (FWD && a.Sf && act) {
 #pragma unroll
       for (int t = 0; t < KT; ++t)
@@ -462,19 +456,18 @@ delta_chunk_walk_kernel(DeltaChunkArgs a) {
           if (k < a.K) a.Sf[(unit * a.K + k) * a.V + v0 + c] = S[t][r];
         }
     }
-  } else if (w < 4) {
+  } else if (FWD && w < 4) {
     // ------------------------------------------------------------ the followers
     __syncthreads();
     for (int p = 0; p <= nch; ++p) {  // chunk p - 1 here, chunk p at the states
       if (act && p > 0) {
         const int ch = p - 1, bf = ch & 1;
-        const i64 tile = (cell0 + ch * a.HV) * a.nvt + vt;
         const unsigned char* const buf = smem_raw + L::B + bf * L::BBUF;
         const bf16* Qt = (const bf16*)(buf + L::Q);
         const u32x4* So = (const u32x4*)(smem_raw + L::S + bf * L::SBUF + t16 * (L::SBUF / 2)) + lane;
         const f32x4* Ro = (const f32x4*)(smem_raw + L::R + (bf * 2 + t16) * 4096) + lane;
         const float* eG = gates(ch);
-        // Q S0 (the forward: its transpose), both parts of S0
+        // (Q S0)^T, both parts of S0
         u32x4 h4[KS], l4[KS];
         Frag8 qf[KS][4];
 #pragma unroll
@@ -492,55 +485,35 @@ delta_chunk_walk_kernel(DeltaChunkArgs a) {
         for (int s = 0; s < KS; ++s) {
           const Frag8 hi = as_frag(h4[s]), lo = as_frag(l4[s]);
 #pragma unroll
-          for (int m = 0; m < 4; ++m) y[m] = FWD ? mma32(lo, qf[s][m], y[m]) : mma32(qf[s][m], lo, y[m]);
+          for (int m = 0; m < 4; ++m) y[m] = mma32(lo, qf[s][m], y[m]);
 #pragma unroll
-          for (int m = 0; m < 4; ++m) y[m] = FWD ? mma32(hi, qf[s][m], y[m]) : mma32(qf[s][m], hi, y[m]);
-          if constexpr (!FWD) {
-            u32x4* o = (u32x4*)(a.Sw + tile * 2 * KS * 512) + s * 64 + lane;
-            o[0] = h4[s];
-            o[KS * 64] = l4[s];
-          }
+          for (int m = 0; m < 4; ++m) y[m] = mma32(hi, qf[s][m], y[m]);
         }
         Frag8 rh[2], rl[2];
 #pragma unroll
         for (int s = 0; s < 2; ++s) split8(Ro[2 * s * 64], Ro[(2 * s + 1) * 64], rh[s], rl[s]);
-        if constexpr (FWD) {
-          // O^T = scale e^G (Q S0)^T + r^T (scale P beta)^T
-          Frag8 pf[6];
+        // O^T = scale e^G (Q S0)^T + r^T (scale P beta)^T
+        Frag8 pf[6];
 #pragma unroll
-          for (int i = 0; i < 6; ++i) pf[i] = as_frag(((const u32x4*)(buf + L::PO))[i * 64 + lane]);
-          float e[4];
+        for (int i = 0; i < 6; ++i) pf[i] = as_frag(((const u32x4*)(buf + L::P))[i * 64 + lane]);
+        float e[4];
 #pragma unroll
-          for (int m = 0; m < 4; ++m) e[m] = a.scale * eG[16 * m + c];
-          SSMVJP_FENCE();
+        for (int m = 0; m < 4; ++m) e[m] = a.scale * eG[16 * m + c];
+        SSMVJP_FENCE();
 #pragma unroll
-          for (int m = 0; m < 4; ++m) y[m] *= e[m];
+        for (int m = 0; m < 4; ++m) y[m] *= e[m];
 #pragma unroll
-          for (int s = 0; s < 2; ++s) {
+        for (int s = 0; s < 2; ++s) {
 #pragma unroll
-            for (int m = 2 * s; m < 4; ++m) y[m] = mma32(rl[s], pf[frag_lo(m, s)], y[m]);
+          for (int m = 2 * s; m < 4; ++m) y[m] = mma32(rl[s], pf[frag_lo(m, s)], y[m]);
 #pragma unroll
-            for (int m = 2 * s; m < 4; ++m) y[m] = mma32(rh[s], pf[frag_lo(m, s)], y[m]);
-          }
-          const i64 row0 = (i64)ch * DCH + c;
-          bf16* o = a.o + ((sp.start + row0) * a.HV + hv) * a.V + v0 + 4 * q;
-#pragma unroll
-          for (int m = 0; m < 4; ++m)
-            if (row0 + 16 * m < sp.len) *(s16x4*)(o + 16 * m * a.HV * a.V) = pack4(y[m]);
-        } else {
-          u32x4* o = (u32x4*)(a.rw + tile * 4 * 512) + lane;
-#pragma unroll
-          for (int s = 0; s < 2; ++s) o[s * 64] = as_u4(rh[s]), o[128 + s * 64] = as_u4(rl[s]);
-          const bf16* Ot = (const bf16*)(buf + L::PO);
-          float* rp = a.rowp + tile * 3 * 64;
-#pragma unroll
-          for (int m = 0; m < 4; ++m) {
-            f32x4 t = a.scale * at4(eG, m) * unpack4(col4(Ot, 32, m, t16, lane)) * y[m];
-#pragma unroll
-            for (int r = 0; r < 4; ++r) t[r] = sum16(t[r]);
-            if (c == 0) *(f32x4*)(rp + 16 * m + 4 * q) = t;
-          }
+          for (int m = 2 * s; m < 4; ++m) y[m] = mma32(rh[s], pf[frag_lo(m, s)], y[m]);
         }
+        const i64 row0 = (i64)ch * DCH + c;
+        bf16* o = a.o + ((sp.start + row0) * a.HV + hv) * a.V + v0 + 4 * q;
+#pragma unroll
+        for (int m = 0; m < 4; ++m)
+          if (row0 + 16 * m < sp.len) *(s16x4*)(o + 16 * m * a.HV * a.V) = pack4(y[m]);
       }
       __syncthreads();
     }
@@ -559,12 +532,11 @@ delta_chunk_walk_kernel(DeltaChunkArgs a) {
       cols_dma.issue(b + L::V, 0, row_words(a.v, tok0, rows_of(ch), a.HV, hv, a.V, slice * 32));
       flat_dma<12, 1>(b + L::T, 0, lane, rsrc_words_u(a.Tf + (cell0 + ch * a.HV) * 6 * 2 * 512, 12 * 1024));
     };
-    auto issue_b = [&](int ch) {  // q and P, or q and d_o
+    auto issue_b = [&](int ch) {  // q and P
       const unsigned b = lds0 + (unsigned)(L::B + (ch & 1) * L::BBUF);
       const i64 tok0 = sp.start + (i64)ch * DCH;
       rows_dma.issue(b + L::Q, 0, row_words(a.q, tok0, rows_of(ch), a.H, h, a.K, 0));
-      if constexpr (FWD) flat_dma<6, 1>(b + L::PO, 0, lane, rsrc_words_u(a.Pf + (cell0 + ch * a.HV) * 6 * 512, 6 * 1024));
-      else cols_dma.issue(b + L::PO, 0, row_words(a.d_o, tok0, rows_of(ch), a.HV, hv, a.V, slice * 32));
+      flat_dma<6, 1>(b + L::P, 0, lane, rsrc_words_u(a.Pf + (cell0 + ch * a.HV) * 6 * 512, 6 * 1024));
     };
     float sG = 0.0f, sB = 0.0f;
     auto fetch_gates = [&](int ch) {
@@ -585,13 +557,13 @@ delta_chunk_walk_kernel(DeltaChunkArgs a) {
     }
     dma_wait();
     __syncthreads();
-    for (int p = 0; p <= nch; ++p) {
+    for (int p = 0; p < nch + (FWD ? 1 : 0); ++p) {
       const bool more = p + 1 < nch;
       if (more) {
         fetch_gates(p + 1);
         issue_a(p + 1);
       }
-      if (p < nch) issue_b(p);
+      if (FWD && p < nch) issue_b(p);
       if (more) commit_gates(p + 1);
       dma_wait();
       __syncthreads();
@@ -601,7 +573,7 @@ delta_chunk_walk_kernel(DeltaChunkArgs a) {
 
 template <int MODE>
 void launch_walk(const DeltaChunkArgs& a, hipStream_t s) {
-  const dim3 grid((unsigned)walk_blocks(a.seq.nseq * a.HV, (a.V + 31) / 32)), wg(WALK_NTH);
+  const dim3 grid((unsigned)walk_blocks(a.seq.nseq * a.HV, (a.V + 31) / 32)), wg(walk_nth(MODE));
   if (a.K <= 64) hipLaunchKernelGGL((delta_chunk_walk_kernel<64, MODE>), grid, wg, (WalkLds<64, MODE>::TOTAL), s, a);
   else hipLaunchKernelGGL((delta_chunk_walk_kernel<128, MODE>), grid, wg, (WalkLds<128, MODE>::TOTAL), s, a);
 }

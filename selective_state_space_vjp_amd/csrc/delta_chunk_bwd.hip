@@ -11,19 +11,23 @@
 //     dk = -e^G mu S0^T + (e^{G_63 - G} beta r) dS^T + dD^T Q + E K + E^T K
 //     dbeta_j = r_j . dU_j - sum_{i > j} a_ij N_ij
 //     M_ij = dD_ij q_i . k_j + E_ij k_i . k_j
-//     dG_i = scale e^G_i dO_i . (Q S0)_i - e^G_i mu_i . (K S0)_i - su_i + sum_j M_ij - sum_j M_ji
-//     su_i = e^{G_63 - G_i} beta_i r_i . (K dS)_i
+//     dG_i = q_i . (scale e^G dO S0^T)_i - k_i . (e^G mu S0^T)_i - su_i + sum_j M_ij - sum_j M_ji
+//     su_i = k_i . ((e^{G_63 - G} beta r) dS^T)_i
 //     dg_t = sum_{i >= t} dG_i + sum_i su_i + e^{G_63} <S0, dS>
-// In the sum over i >= t the pairs with both tokens behind t cancel between the
-// row and the column sums, exactly, since both add the same float32 M_ij; that
-// is why r, mu and the states enter M and the row terms with both bf16 parts,
-// and dg comes out at about 6e-6.  dq and dk are bf16: one part is enough.
+//     r_j . dU_j = scale sum_{i >= j} P_ij (dO_i . r_j) + su_j / beta_j
+// (the last sum is formed without beta.)  In the sum over i >= t the pairs with
+// both tokens behind t cancel between the row and the column sums, exactly,
+// since both add the same float32 M_ij; that is why r, mu and the states enter
+// with both bf16 parts, and dg comes out at about 4e-6.
 //
 // Four launches: delta_prep_kernel (T, T^T, scale P^T of every chunk),
 // delta_chunk_walk_kernel<., 1> (the state before every chunk, r),
 // delta_chunk_rev_kernel (the reverse walk, 16 columns per wave as the forward:
-// mu, dS, row sums over its columns) and delta_chunk_grads_kernel (all chunks at
-// once: dv, dq, dk summed over the value heads of a qk head, dg, dbeta).
+// mu and the state's gradient behind every chunk) and delta_chunk_grads_kernel
+// (all chunks at once: dv, dq, dk summed over the value heads of a qk head, dg,
+// dbeta).  The walks are bound by the chain from one state to the next, so that
+// everything that a chunk can do on its own is left to the last kernel; that one
+// is bound by reading what the walks kept.
 #include "delta_chunk.cuh"
 
 namespace ssmvjp {
@@ -32,230 +36,293 @@ namespace {
 // ---------------------------------------------------------------------------
 // reverse walk
 // ---------------------------------------------------------------------------
-// The chunk's q, k, d_o rows and the fragments of T^T and P^T come as in the
-// forward walk, by LDS-direct loads into the other of two buffers while a chunk
-// is computed.  What belongs to one wave's columns (S0, e^G K S0, r) has one
-// buffer per wave: it is read early in a chunk, and the wave then sends for the
-// next chunk's.
-template <int KP, int NW>
-struct RevLds {
-  static constexpr int KS = KP / 32;
-  static constexpr int K = 0, Q = K + 64 * KP * 2, O = Q + 64 * KP * 2, T = O + 2048 * NW, P = T + 12 * 1024,
-                       BUF = P + 12 * 1024;
-  static constexpr int S = 2 * BUF, X = 2 * KS * 1024, R = X + 4096, OWN = R + 4096;  // per wave: X, R inside it
-  static constexpr int G = S + NW * OWN, TOTAL = G + 6 * 256;
+// As the forward walk: waves 0 and 1 carry the gradients of 16 columns of the
+// state each, waves 2 and 3 work one chunk ahead on the part that does not
+// depend on them, B = Q^T (scale e^G dO), and hand it over through LDS, wave 4
+// loads and prepares the gates.
+template <int KP>
+struct RevLds {  // byte offsets
+  static constexpr int K = 0, T = K + 64 * KP * 2, P = T + 12 * 1024, ABUF = P + 12 * 1024;    // [2] waves 0, 1
+  static constexpr int Q = 2 * ABUF, O = Q + 2 * 64 * KP * 2, B = O + 3 * 4096, BT = KP * 64;  // q [2], d_o [3], B [2][2 tiles]
+  static constexpr int G = B + 4 * BT, TOTAL = G + 3 * 768;  // gates: [3][e^G, e^{G_63 - G}, beta]
 };
+constexpr int REV_NTH = 320;
 
-template <int KP, int NW>
-__global__ void __launch_bounds__(64 * NW) __attribute__((amdgpu_waves_per_eu(2, 2))) delta_chunk_rev_kernel(DeltaChunkArgs a) {
-  constexpr int KS = KP / 32, KT = KP / 16, VPITCH = 16 * NW;
-  typedef RevLds<KP, NW> L;
+template <int KP>
+__global__ void __launch_bounds__(REV_NTH) __attribute__((amdgpu_waves_per_eu(2, 2)))
+delta_chunk_rev_kernel(DeltaChunkArgs a) {
+  constexpr int KS = KP / 32, KT = KP / 16;
+  typedef RevLds<KP> L;
   extern __shared__ __align__(16) unsigned char smem_raw[];
-  float* const gates = (float*)(smem_raw + L::G);  // [2][e^G, e^{G_63 - G}, beta][64]
-  const int tid = threadIdx.x, lane = tid & 63, w = __builtin_amdgcn_readfirstlane(tid >> 6), c = lane & 15, q = lane >> 4;
+  const int lane = threadIdx.x & 63, w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), c = lane & 15, q = lane >> 4;
+  const int t16 = w & 1;
   i64 unit, slice;
-  if (!walk_unit(a.seq.nseq * a.HV, (a.V + VPITCH - 1) / VPITCH, unit, slice)) return;
+  if (!walk_unit(a.seq.nseq * a.HV, (a.V + 31) / 32, unit, slice)) return;
   const i64 n = unit / a.HV, hv = unit % a.HV, h = hv / a.rep;
   const DeltaSpan sp = a.seq.span(n);
-  const i64 nch = (sp.len + DCH - 1) / DCH;
-  const i64 v0 = slice * VPITCH + w * 16, vt = slice * NW + w;
+  const int nch = (int)((sp.len + DCH - 1) / DCH);
+  const i64 v0 = slice * 32 + t16 * 16, vt = slice * 2 + t16;
   const bool act = v0 < a.V;
+  const i64 cell0 = sp.slot0 * a.HV + hv;
+  auto gates = [&](int ch) { return (float*)(smem_raw + L::G + ch % 3 * 768); };
+  auto d_o = [&](int ch) { return (const bf16*)(smem_raw + L::O + ch % 3 * 4096); };
+  auto at4 = [&](const float* p, int m) { return *(const f32x4*)(p + 16 * m + 4 * q); };
+  auto Bof = [&](int ch) { return (f32x4*)(smem_raw + L::B + ((ch & 1) * 2 + t16) * L::BT) + lane; };
 
-  const unsigned lds0 = lds_base(smem_raw);
-  RowDma<KP, NW> rows_dma;
-  ColDma<NW, NW> cols_dma;
-  rows_dma.init(w, lane, a.H * a.K, a.K);
-  cols_dma.init(w, lane, a.HV * a.V, slice * VPITCH, a.V);
-  auto issue = [&](i64 ch, int bf) {
-    const i64 tok0 = sp.start + ch * DCH;
-    const int rows = (int)(sp.len - ch * DCH < DCH ? sp.len - ch * DCH : DCH);
-    const unsigned b = lds0 + (unsigned)(bf * L::BUF);
-    const i64 cu = (sp.slot0 + ch) * a.HV + hv;
-    rows_dma.issue(b + L::K, w, row_words(a.k, tok0, rows, a.H, h, a.K, 0));
-    rows_dma.issue(b + L::Q, w, row_words(a.q, tok0, rows, a.H, h, a.K, 0));
-    cols_dma.issue(b + L::O, w, row_words(a.d_o, tok0, rows, a.HV, hv, a.V, slice * VPITCH));
-    flat_dma<12, NW>(b + L::T, w, lane, rsrc_words_u(a.Tt + cu * 6 * 2 * 512, 12 * 1024));
-    flat_dma<12, NW>(b + L::P, w, lane, rsrc_words_u(a.Pt + cu * 6 * 2 * 512, 12 * 1024));
-  };
-  const unsigned own = (unsigned)(L::S + w * L::OWN);
-  auto issue_own = [&](i64 ch) {
-    const i64 tile = ((sp.slot0 + ch) * a.HV + hv) * a.nvt + vt;
-    flat_dma<2 * KS, 1>(lds0 + own, 0, lane, rsrc_words_u(a.Sw + tile * 2 * KS * 512, 2 * KS * 1024));
-    flat_dma<4, 1>(lds0 + own + L::X, 0, lane, rsrc_words_u(a.Xw + tile * 1024, 4096));
-    flat_dma<4, 1>(lds0 + own + L::R, 0, lane, rsrc_words_u(a.rw + tile * 4 * 512, 4096));
-  };
-  float sG = 0.0f, sB = 0.0f;
-  auto fetch_gates = [&](i64 ch) {
-    const i64 tok0 = sp.start + ch * DCH;
-    sG = a.G[((sp.slot0 + ch) * a.HV + hv) * 64 + lane];
-    sB = ch * DCH + lane < sp.len ? a.beta[(tok0 + lane) * a.HV + hv] : 0.0f;
-  };
-  auto commit_gates = [&](int bf) {
-    const float end = __shfl(sG, 63, 64);
-    float* g = gates + bf * 192 + lane;
-    g[0] = exp_hw(sG);
-    g[64] = exp_hw(end - sG);
-    g[128] = sB;
-  };
-
-  f32x4 dS[KT];
-  const brsrc rs = state_rsrc(a.dSf, a, unit, act);
+  if (w < 2) {
+    // ------------------------------------------------------ the state's gradient
+    __builtin_amdgcn_s_setprio(3);
+    f32x4 dS[KT];
+    Frag8 dh[KS], dl[KS];  // its two parts
+    const brsrc rs = state_rsrc(a.dSf, a, unit, act);
 #pragma unroll
-  for (int t = 0; t < KT; ++t) dS[t] = load_state4(rs, a, t, q, v0 + c);
-  if (nch > 0) {
-    const int bf = (nch - 1) & 1;
-    if (w == 0) fetch_gates(nch - 1);
-    issue(nch - 1, bf);
-    if (act) issue_own(nch - 1);
-    if (w == 0) commit_gates(bf);
-  }
-  dma_wait();
-  __syncthreads();
-  for (i64 ch = nch - 1; ch >= 0; --ch) {
-    const int bf = ch & 1;
-    const i64 tile = ((sp.slot0 + ch) * a.HV + hv) * a.nvt + vt;
-    if (ch > 0) {
-      if (w == 0) fetch_gates(ch - 1);
-      issue(ch - 1, bf ^ 1);
-    }
-    if (act) {
-      const unsigned char* const buf = smem_raw + bf * L::BUF;
-      const bf16 *Kt = (const bf16*)(buf + L::K), *Qt = (const bf16*)(buf + L::Q), *Ot = (const bf16*)(buf + L::O);
-      const u32x4 *Tt = (const u32x4*)(buf + L::T) + lane, *Pt = (const u32x4*)(buf + L::P) + lane;
-      const u32x4 *So = (const u32x4*)(smem_raw + own) + lane, *Ro = (const u32x4*)(smem_raw + own + L::R) + lane;
-      const f32x4* Xo = (const f32x4*)(smem_raw + own + L::X) + lane;
-      const float *eG = gates + bf * 192, *eE = eG + 64, *be = eG + 128;
-      auto at4 = [&](const float* p, int m) { return *(const f32x4*)(p + 16 * m + 4 * q); };
-      // K dS (both parts of dS) and <S0, dS>
-      f32x4 z[4], x[4], r[4];
-      f32x4 dot = zero4();
+    for (int t = 0; t < KT; ++t) dS[t] = load_state4(rs, a, t, q, v0 + c);
 #pragma unroll
-      for (int m = 0; m < 4; ++m) z[m] = zero4();
+    for (int s = 0; s < KS; ++s) split8(dS[2 * s], dS[2 * s + 1], dh[s], dl[s]);
+    __syncthreads();
+    __syncthreads();  // the period in which B of the last chunk is made
+    for (int ch = nch - 1; ch >= 0; --ch) {
+      if (act) {
+        const unsigned char* const buf = smem_raw + (ch & 1) * L::ABUF;
+        const bf16* Kt = (const bf16*)(buf + L::K);
+        const u32x4 *Tt = (const u32x4*)(buf + L::T) + lane, *Pt = (const u32x4*)(buf + L::P) + lane;
+        const bf16* Ot = d_o(ch);
+        const f32x4* B = Bof(ch);
+        const i64 tile = (cell0 + ch * a.HV) * a.nvt + vt;
+        u32x4* Dw = (u32x4*)(a.dSw + tile * 2 * KS * 512) + lane;
+        u32x4* Mw = (u32x4*)(a.muw + tile * 4 * 512) + lane;
+        const float *eG = gates(ch), *eE = eG + 64, *be = eG + 128;
+        // 1: z = K dS, row tiles 2 and 3, both parts of dS
+        f32x4 z[4], du[4], e[4], b[4];
+        Frag8 kf[2][KS], kg[2][KS], of[2], ph[6], pl[6];
 #pragma unroll
-      for (int s = 0; s < KS; ++s) {
-        const Frag8 sh = as_frag(So[s * 64]), sl = as_frag(So[(KS + s) * 64]);
-        Frag8 dh, dl;
-        split8(dS[2 * s], dS[2 * s + 1], dh, dl);
-        *((u32x4*)(a.dSw + tile * KS * 512) + s * 64 + lane) = as_u4(dh);
-        dot += (unpack4(sh.a) + unpack4(sl.a)) * dS[2 * s];
-        dot += (unpack4(sh.b) + unpack4(sl.b)) * dS[2 * s + 1];
+        for (int s = 0; s < KS; ++s) kf[0][s] = row_frag(Kt, KP, 2, s, lane), kf[1][s] = row_frag(Kt, KP, 3, s, lane);
+        SSMVJP_FENCE();
 #pragma unroll
-        for (int m = 0; m < 4; ++m) {
-          const Frag8 kf = row_frag(Kt, KP, m, s, lane);
-          z[m] = mma32(kf, dl, z[m]);
-          z[m] = mma32(kf, dh, z[m]);
+        for (int m = 0; m < 4; ++m) z[m] = zero4(), du[m] = zero4();
+#pragma unroll
+        for (int s = 0; s < KS; ++s) {
+          z[2] = mma32(kf[0][s], dl[s], z[2]);
+          z[3] = mma32(kf[1][s], dl[s], z[3]);
+          z[2] = mma32(kf[0][s], dh[s], z[2]);
+          z[3] = mma32(kf[1][s], dh[s], z[3]);
         }
-      }
 #pragma unroll
-      for (int s = 0; s < 2; ++s) {
-        const Frag8 rh = as_frag(Ro[s * 64]), rl = as_frag(Ro[(2 + s) * 64]);
-        r[2 * s] = unpack4(rh.a) + unpack4(rl.a);
-        r[2 * s + 1] = unpack4(rh.b) + unpack4(rl.b);
-        x[2 * s] = Xo[2 * s * 64];
-        x[2 * s + 1] = Xo[(2 * s + 1) * 64];
-      }
-      if (ch > 0) {
-        lds_wait();  // what this wave had of its own is in registers
-        issue_own(ch - 1);
-      }
-      // dU = scale P^T dO + e^{G_63 - G} K dS
-      Frag8 of[2];
+        for (int i = 0; i < 6; ++i) ph[i] = as_frag(Pt[i * 128]), pl[i] = as_frag(Pt[i * 128 + 64]);
 #pragma unroll
-      for (int s = 0; s < 2; ++s) of[s] = {col4(Ot, VPITCH, 2 * s, w, lane), col4(Ot, VPITCH, 2 * s + 1, w, lane)};
-      f32x4 du[4], mu[4];
+        for (int s = 0; s < 2; ++s) of[s] = {col4(Ot, 32, 2 * s, t16, lane), col4(Ot, 32, 2 * s + 1, t16, lane)};
 #pragma unroll
-      for (int m = 0; m < 4; ++m) {
-        z[m] *= at4(eE, m);
-        du[m] = z[m];
+        for (int s = 0; s < KS; ++s) Dw[s * 64] = as_u4(dh[s]), Dw[(KS + s) * 64] = as_u4(dl[s]);
+        pipe<4 * KS, 2, 1>();
+        SSMVJP_FENCE();
+        // 2: scale P^T dO
 #pragma unroll
-        for (int s = m / 2; s < 2; ++s) {
-          du[m] = mma32(as_frag(Pt[frag_up(m, s) * 128 + 64]), of[s], du[m]);
-          du[m] = mma32(as_frag(Pt[frag_up(m, s) * 128]), of[s], du[m]);
+        for (int s = 1; s >= 0; --s) {
+#pragma unroll
+          for (int m = 0; m < 2 * s + 2; ++m) du[m] = mma32(pl[frag_up(m, s)], of[s], du[m]);
+#pragma unroll
+          for (int m = 0; m < 2 * s + 2; ++m) du[m] = mma32(ph[frag_up(m, s)], of[s], du[m]);
         }
-      }
-      // mu = T^T (beta dU)
-      {
-        Frag8 bh[2], bl[2];
 #pragma unroll
-        for (int m = 0; m < 4; ++m) mu[m] = at4(be, m) * du[m];
+        for (int s = 0; s < KS; ++s) kg[0][s] = row_frag(Kt, KP, 0, s, lane), kg[1][s] = row_frag(Kt, KP, 1, s, lane);
 #pragma unroll
-        for (int s = 0; s < 2; ++s) split8(mu[2 * s], mu[2 * s + 1], bh[s], bl[s]);
+        for (int m = 0; m < 4; ++m) e[m] = at4(eE, m), b[m] = at4(be, m);
+        pipe<12, 2, 2>();
+        SSMVJP_FENCE();
+        // 3: z, row tiles 0 and 1; beta dU of tiles 2 and 3, dU = scale P^T dO + e^{G_63 - G} z
+        Frag8 bh[2], bl[2], th[6], tl[6];
 #pragma unroll
-        for (int m = 0; m < 4; ++m) {
+        for (int s = 0; s < KS; ++s) {
+          z[0] = mma32(kg[0][s], dl[s], z[0]);
+          z[1] = mma32(kg[1][s], dl[s], z[1]);
+          z[0] = mma32(kg[0][s], dh[s], z[0]);
+          z[1] = mma32(kg[1][s], dh[s], z[1]);
+        }
+        f32x4 mu[4];
+        auto bdu = [&](int s) {
 #pragma unroll
-          for (int s = m / 2; s < 2; ++s) {
-            const Frag8 th = as_frag(Tt[frag_up(m, s) * 128]), tl = as_frag(Tt[frag_up(m, s) * 128 + 64]);
-            mu[m] = mma32(th, bl[s], mu[m]);
-            mu[m] = mma32(tl, bh[s], mu[m]);
-            mu[m] = mma32(th, bh[s], mu[m]);
+          for (int m = 2 * s; m < 2 * s + 2; ++m) mu[m] = b[m] * (du[m] + e[m] * z[m]);
+          split8(mu[2 * s], mu[2 * s + 1], bh[s], bl[s]);
+        };
+        bdu(1);
+#pragma unroll
+        for (int i = 0; i < 6; ++i) th[i] = as_frag(Tt[i * 128]), tl[i] = as_frag(Tt[i * 128 + 64]);
+        pipe<4 * KS, 3, 1>();
+        SSMVJP_FENCE();
+        // 4: mu = T^T (beta dU), contraction over tiles 2 and 3; the decay of dS, plus B
+        f32x4 y[2];  // tiles 0 and 1 get this part later
+        y[0] = mma32(th[frag_up(0, 1)], bl[1], zero4());
+        y[1] = mma32(th[frag_up(1, 1)], bl[1], zero4());
+        mu[2] = mma32(th[frag_up(2, 1)], bl[1], mu[2]);
+        mu[3] = mma32(th[frag_up(3, 1)], bl[1], mu[3]);
+        y[0] = mma32(tl[frag_up(0, 1)], bh[1], y[0]);
+        y[1] = mma32(tl[frag_up(1, 1)], bh[1], y[1]);
+        mu[2] = mma32(tl[frag_up(2, 1)], bh[1], mu[2]);
+        mu[3] = mma32(tl[frag_up(3, 1)], bh[1], mu[3]);
+        y[0] = mma32(th[frag_up(0, 1)], bh[1], y[0]);
+        y[1] = mma32(th[frag_up(1, 1)], bh[1], y[1]);
+        mu[2] = mma32(th[frag_up(2, 1)], bh[1], mu[2]);
+        mu[3] = mma32(th[frag_up(3, 1)], bh[1], mu[3]);
+        bdu(0);
+        const float eEnd = eG[63];
+#pragma unroll
+        for (int t = 0; t < KT; ++t) dS[t] = eEnd * dS[t] + B[t * 64];
+        pipe<12, 5, 1>();
+        SSMVJP_FENCE();
+        // 5: contraction over tiles 0 and 1; -e^G mu of tiles 2 and 3
+        y[0] = mma32(th[frag_up(0, 0)], bl[0], y[0]);
+        y[1] = mma32(th[frag_up(1, 0)], bl[0], y[1]);
+        y[0] = mma32(tl[frag_up(0, 0)], bh[0], y[0]);
+        y[1] = mma32(tl[frag_up(1, 0)], bh[0], y[1]);
+        y[0] = mma32(th[frag_up(0, 0)], bh[0], y[0]);
+        y[1] = mma32(th[frag_up(1, 0)], bh[0], y[1]);
+        Frag8 nh[2], nl[2], ct[2][KT];
+        auto turn = [&](int s) {
+          split8(-at4(eG, 2 * s) * mu[2 * s], -at4(eG, 2 * s + 1) * mu[2 * s + 1], nh[s], nl[s]);
+        };
+        auto keep = [&](int s) {
+          Frag8 hi, lo;
+          split8(mu[2 * s], mu[2 * s + 1], hi, lo);
+          Mw[s * 64] = as_u4(hi);
+          Mw[128 + s * 64] = as_u4(lo);
+        };
+        turn(1);
+#pragma unroll
+        for (int t = 0; t < KT; ++t) ct[1][t] = key_frag(Kt, KP, t, 1, lane);
+        pipe<6, 8, 3>();
+        SSMVJP_FENCE();
+        // 6: dS0 = e^{G_63} dS + B - K^T (e^G mu), tokens of tiles 2 and 3
+#pragma unroll
+        for (int t = 0; t < KT; ++t) dS[t] = mma32(ct[1][t], nl[1], dS[t]);
+#pragma unroll
+        for (int t = 0; t < KT; ++t) dS[t] = mma32(ct[1][t], nh[1], dS[t]);
+        mu[0] += y[0];
+        mu[1] += y[1];
+        turn(0);
+        keep(1);
+#pragma unroll
+        for (int t = 0; t < KT; ++t) ct[0][t] = key_frag(Kt, KP, t, 0, lane);
+        pipe<2 * KT, 5, 1>();
+        SSMVJP_FENCE();
+        // 7: tokens of tiles 0 and 1; the parts of the state tiles that are done
+        constexpr int PT = KT < 4 ? KT : 4;  // state tiles at a time
+#pragma unroll
+        for (int g = 0; g < KT; g += PT) {
+#pragma unroll
+          for (int t = g; t < g + PT; ++t) dS[t] = mma32(ct[0][t], nl[0], dS[t]);
+#pragma unroll
+          for (int t = g; t < g + PT; ++t) dS[t] = mma32(ct[0][t], nh[0], dS[t]);
+          if (g == 0) {
+            keep(0);
+          } else {
+#pragma unroll
+            for (int s = (g - PT) / 2; s < g / 2; ++s) split8(dS[2 * s], dS[2 * s + 1], dh[s], dl[s]);
           }
+          pipe<2 * PT, 6, 0>();
+          SSMVJP_FENCE();
         }
+#pragma unroll
+        for (int s = (KT - PT) / 2; s < KS; ++s) split8(dS[2 * s], dS[2 * s + 1], dh[s], dl[s]);
       }
-      u32x4* mo = (u32x4*)(a.muw + tile * 4 * 512) + lane;
+      __syncthreads();
+    }
+    if (a.dS0 && act) {
 #pragma unroll
-      for (int s = 0; s < 2; ++s) {
-        Frag8 hi, lo;
-        split8(mu[2 * s], mu[2 * s + 1], hi, lo);
-        mo[s * 64] = as_u4(hi);
-        mo[128 + s * 64] = as_u4(lo);
-      }
-      // row terms, summed over this wave's 16 columns; the operands of the state's update
-      const float eEnd = eG[63];
-      float tail = eEnd * ((dot[0] + dot[1]) + (dot[2] + dot[3]));
-      float* rp = a.rowp + tile * 3 * 64 + 64;
+      for (int t = 0; t < KT; ++t)
 #pragma unroll
-      for (int m = 0; m < 4; ++m) {
-        const f32x4 eg = at4(eG, m);
-        const f32x4 o = unpack4(m & 1 ? of[m / 2].b : of[m / 2].a);
-        const f32x4 su = at4(be, m) * r[m] * z[m];
-        f32x4 t = -mu[m] * x[m] - su, d = r[m] * du[m];
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          tail += su[j];
-          t[j] = sum16(t[j]);
-          d[j] = sum16(d[j]);
+        for (int r = 0; r < 4; ++r) {
+          const int k = state_row(t, q) + r;
+          if (k < a.K) a.dS0[(unit * a.K + k) * a.V + v0 + c] = dS[t][r];
         }
-        if (c == 0) {
-          *(f32x4*)(rp + 16 * m + 4 * q) = t;
-          *(f32x4*)(rp + 64 + 16 * m + 4 * q) = d;
-        }
-        mu[m] *= -eg;
-        x[m] = a.scale * eg * o;
-      }
-      tail = wave_sum(tail);
-      if (lane == 0) a.endp[tile] = tail;
-      // dS0 = e^{G_63} dS + Q^T (scale e^G dO) - K^T (e^G mu)
-      Frag8 mh[2], ml[2], oh[2], ol[2];
+    }
+  } else if (w < 4) {
+    // ------------------------------------------------- B = Q^T (scale e^G dO) ahead
+    __syncthreads();
+    for (int p = nch; p >= 0; --p) {  // chunk p - 1 here, chunk p at the gradients
+      if (act && p > 0) {
+        const int ch = p - 1;
+        const bf16 *Qt = (const bf16*)(smem_raw + L::Q + (ch & 1) * 64 * KP * 2), *Ot = d_o(ch);
+        const float* eG = gates(ch);
+        f32x4* B = Bof(ch);
+        Frag8 oh[2], ol[2], ct[2][KT];
 #pragma unroll
-      for (int s = 0; s < 2; ++s) {
-        split8(mu[2 * s], mu[2 * s + 1], mh[s], ml[s]);
-        split8(x[2 * s], x[2 * s + 1], oh[s], ol[s]);
-      }
-#pragma unroll
-      for (int t = 0; t < KT; ++t) {
-        dS[t] *= eEnd;
+        for (int t = 0; t < KT; ++t) ct[0][t] = key_frag(Qt, KP, t, 0, lane);
 #pragma unroll
         for (int s = 0; s < 2; ++s) {
-          const Frag8 kf = key_frag(Kt, KP, t, s, lane), qf = key_frag(Qt, KP, t, s, lane);
-          dS[t] = mma32(kf, ml[s], dS[t]);
-          dS[t] = mma32(qf, ol[s], dS[t]);
-          dS[t] = mma32(kf, mh[s], dS[t]);
-          dS[t] = mma32(qf, oh[s], dS[t]);
+          f32x4 o[2];
+#pragma unroll
+          for (int m = 0; m < 2; ++m) o[m] = a.scale * at4(eG, 2 * s + m) * unpack4(col4(Ot, 32, 2 * s + m, t16, lane));
+          split8(o[0], o[1], oh[s], ol[s]);
         }
+        SSMVJP_FENCE();
+        f32x4 x[KT];
+#pragma unroll
+        for (int t = 0; t < KT; ++t) x[t] = mma32(ct[0][t], ol[0], zero4());
+#pragma unroll
+        for (int t = 0; t < KT; ++t) x[t] = mma32(ct[0][t], oh[0], x[t]);
+#pragma unroll
+        for (int t = 0; t < KT; ++t) ct[1][t] = key_frag(Qt, KP, t, 1, lane);
+        SSMVJP_FENCE();
+#pragma unroll
+        for (int t = 0; t < KT; ++t) x[t] = mma32(ct[1][t], ol[1], x[t]);
+#pragma unroll
+        for (int t = 0; t < KT; ++t) x[t] = mma32(ct[1][t], oh[1], x[t]);
+#pragma unroll
+        for (int t = 0; t < KT; ++t) B[t * 64] = x[t];
       }
+      __syncthreads();
     }
-    if (ch > 0 && w == 0) commit_gates(bf ^ 1);
+  } else {
+    // --------------------------------------------------------------- the loader
+    const unsigned lds0 = lds_base(smem_raw);
+    RowDma<KP, 1> rows_dma;
+    ColDma<2, 1> cols_dma;
+    rows_dma.init(0, lane, a.H * a.K, a.K);
+    cols_dma.init(0, lane, a.HV * a.V, slice * 32, a.V);
+    auto rows_of = [&](int ch) { return (int)(sp.len - (i64)ch * DCH < DCH ? sp.len - (i64)ch * DCH : DCH); };
+    auto issue_a = [&](int ch) {  // k, T^T and P^T of chunk ch
+      const unsigned b = lds0 + (unsigned)((ch & 1) * L::ABUF);
+      const i64 cu = cell0 + ch * a.HV;
+      rows_dma.issue(b + L::K, 0, row_words(a.k, sp.start + (i64)ch * DCH, rows_of(ch), a.H, h, a.K, 0));
+      flat_dma<12, 1>(b + L::T, 0, lane, rsrc_words_u(a.Tt + cu * 6 * 2 * 512, 12 * 1024));
+      flat_dma<12, 1>(b + L::P, 0, lane, rsrc_words_u(a.Pt + cu * 6 * 2 * 512, 12 * 1024));
+    };
+    auto issue_b = [&](int ch) {  // q and d_o
+      const i64 tok0 = sp.start + (i64)ch * DCH;
+      rows_dma.issue(lds0 + (unsigned)(L::Q + (ch & 1) * 64 * KP * 2), 0, row_words(a.q, tok0, rows_of(ch), a.H, h, a.K, 0));
+      cols_dma.issue(lds0 + (unsigned)(L::O + ch % 3 * 4096), 0,
+                     row_words(a.d_o, tok0, rows_of(ch), a.HV, hv, a.V, slice * 32));
+    };
+    float sG = 0.0f, sB = 0.0f;
+    auto fetch_gates = [&](int ch) {
+      sG = a.G[(cell0 + ch * a.HV) * 64 + lane];
+      const i64 t = (i64)ch * DCH + lane;
+      sB = t < sp.len ? a.beta[(sp.start + t) * a.HV + hv] : 0.0f;
+    };
+    auto commit_gates = [&](int ch) {
+      float* g = gates(ch) + lane;
+      const float end = __shfl(sG, 63, 64);
+      g[0] = exp_hw(sG);
+      g[64] = exp_hw(end - sG);
+      g[128] = sB;
+    };
+    if (nch > 0) {
+      fetch_gates(nch - 1);
+      issue_b(nch - 1);
+      commit_gates(nch - 1);
+    }
     dma_wait();
     __syncthreads();
-  }
-  if (a.dS0 && act) {
-#pragma unroll
-    for (int t = 0; t < KT; ++t)
-#pragma unroll
-      for (int r = 0; r < 4; ++r) {
-        const int k = state_row(t, q) + r;
-        if (k < a.K) a.dS0[(unit * a.K + k) * a.V + v0 + c] = dS[t][r];
+    for (int p = nch; p >= 0; --p) {
+      if (p > 1) fetch_gates(p - 2);
+      if (p > 0) issue_a(p - 1);
+      if (p > 1) {
+        issue_b(p - 2);
+        commit_gates(p - 2);
       }
+      dma_wait();
+      __syncthreads();
+    }
   }
 }
 
@@ -291,15 +358,15 @@ __device__ __forceinline__ void pstore(bf16* t, int pitch, int row, int col, con
 template <int KP>
 __global__ void __launch_bounds__(GRADS_NTH, 2) delta_chunk_grads_kernel(DeltaChunkArgs a) {
   constexpr int KS = KP / 32, KT = KP / 16, PK = KP + 20, HT = KT / 2;  // HT: key tiles of a wave
-  constexpr int NP = 4 * KS * 64 / GRADS_NTH;             // 16-byte pieces per thread of a slice of S0 and dS
+  static_assert(4 * 64 * P64 <= 4 * 32 * (P64 + PK), "dD and E fit where the slices' tiles were");
   __shared__ __attribute__((aligned(16))) bf16 Kb[64 * PK], Qb[64 * PK];
   // the slice's tiles; behind the slices the same memory holds dD^T and E^T, two parts each
-  __shared__ __attribute__((aligned(16))) bf16 buf[16 * P64 * 16];
-  __shared__ __attribute__((aligned(16))) float Gs[64], Bs[64], rowM[2][64], colM[2][4][64], colA[4][64];
-  __shared__ float rowG[8][64], rowB[8][64], tails[8];  // the reverse walk's row sums, by wave
+  __shared__ __attribute__((aligned(16))) bf16 buf[4 * 32 * (P64 + PK)];
+  __shared__ __attribute__((aligned(16))) float Gs[64], Bs[64], rowM[2][64], colM[2][4][64], colA[2][4][64];
+  __shared__ float rowT[2][64], rowU[2][64], dots[8];  // row terms of dG; su without beta; <S0, dS> by wave
   typedef unsigned u32x2 __attribute__((ext_vector_type(2)));
   bf16 *rH = buf, *mH = buf + 2 * 32 * P64;  // each followed by its lo part
-  bf16* sT = buf + 4 * 32 * P64;             // [S0, dS][32][KP]
+  bf16* sT = buf + 4 * 32 * P64;             // [S0 hi, lo, dS hi, lo][32][PK]
   const int tid = threadIdx.x, lane = tid & 63, w = __builtin_amdgcn_readfirstlane(tid >> 6), c = lane & 15, q = lane >> 4;
   const int wr = w & 3, half = w >> 2;
   const unsigned H32 = (unsigned)a.H;
@@ -331,24 +398,26 @@ __global__ void __launch_bounds__(GRADS_NTH, 2) delta_chunk_grads_kernel(DeltaCh
   const int nsl = (int)(a.nvt + 1) / 2;
   for (i64 rr = 0; rr < a.rep; ++rr) {
     const i64 hv = h * a.rep + rr, cu = slot * a.HV + hv;
-    u32x4 pr[2], ps[NP];
+    u32x4 pr[2], ps[4];
     u32x2 po[2];
     const brsrc ro = row_rsrc(a.d_o, at.tok0, at.rows, a.HV, hv, a.V);
     // tiles past V lie past the resources: zeros, without a branch
     const brsrc rm4 = make_rsrc((w < 4 ? a.rw : a.muw) + cu * a.nvt * 2048, (unsigned)(a.nvt * 4096));
     const brsrc rS = make_rsrc(a.Sw + cu * a.nvt * KS * 1024, (unsigned)(a.nvt * KS * 2048));
-    const brsrc rD = make_rsrc(a.dSw + cu * a.nvt * KS * 512, (unsigned)(a.nvt * KS * 1024));
+    const brsrc rD = make_rsrc(a.dSw + cu * a.nvt * KS * 1024, (unsigned)(a.nvt * KS * 2048));
+    const int pt = w / KS, pst = w % KS;  // waves below 2 KS: the tile and step whose four pieces this thread brings
     auto fetch = [&](int sl) {
       {  // waves 0 .. 3: r, the others mu; hi and lo of one fragment
         const unsigned o = (unsigned)(((sl * 2 + (w >> 1 & 1)) * 256 + (w & 1) * 64 + lane) * 16);
         pr[0] = bload16(rm4, o);
         pr[1] = bload16(rm4, o + 2048u);
       }
-#pragma unroll
-      for (int i = 0; i < NP; ++i) {
-        const int p = w + GRADS_NTH / 64 * i, t = sl * 2 + p / KS % 2, st = p % KS;
-        if (p < 2 * KS) ps[i] = bload16(rS, (unsigned)(((t * 2 * KS + st) * 64 + lane) * 16));
-        else ps[i] = bload16(rD, (unsigned)(((t * KS + st) * 64 + lane) * 16));
+      if (w < 2 * KS) {
+        const unsigned o = (unsigned)((((sl * 2 + pt) * 2 * KS + pst) * 64 + lane) * 16);
+        ps[0] = bload16(rS, o);
+        ps[1] = bload16(rS, o + KS * 1024u);
+        ps[2] = bload16(rD, o);
+        ps[3] = bload16(rD, o + KS * 1024u);
       }
 #pragma unroll
       for (int e = 0; e < 2; ++e) {
@@ -362,22 +431,12 @@ __global__ void __launch_bounds__(GRADS_NTH, 2) delta_chunk_grads_kernel(DeltaCh
       *(u32x2*)(t + row * P64 + 32 * s + 16 + 4 * q) = u32x2{u[2], u[3]};
     };
     fetch(0);
-    // this wave's share of the walks' row sums (tiles w, w + 8, ..) and, for wave 0, the gates
-    float dG = 0.0f, db = 0.0f, tail = 0.0f, G0 = 0.0f, b0 = 0.0f;
-    for (int t = w; t < (int)a.nvt; t += 8) {
-      const float* rp = a.rowp + (cu * a.nvt + t) * 192 + lane;
-      dG += rp[0] + rp[64];
-      db += rp[128];
-      tail += a.endp[cu * a.nvt + t];
-    }
+    float G0 = 0.0f, b0 = 0.0f;
     if (w == 0) {
       G0 = a.G[cu * 64 + lane];
       b0 = lane < at.rows ? a.beta[(at.tok0 + lane) * a.HV + hv] : 0.0f;
     }
     __syncthreads();  // the previous head's readers are done; k and q are in LDS
-    rowG[w][lane] = dG;
-    rowB[w][lane] = db;
-    if (lane == 0) tails[w] = tail;
     if (w == 0) {
       Gs[lane] = G0;
       Bs[lane] = b0;
@@ -387,6 +446,7 @@ __global__ void __launch_bounds__(GRADS_NTH, 2) delta_chunk_grads_kernel(DeltaCh
     for (int b = 0; b < 4; ++b) pp[b] = zero4();
 #pragma unroll
     for (int t = 0; t < HT; ++t) x1[t] = zero4(), y2[t] = zero4(), y3[t] = zero4();
+    f32x4 dot = zero4();
     for (int sl = 0; sl < nsl; ++sl) {
       if (sl) __syncthreads();
       {
@@ -394,10 +454,12 @@ __global__ void __launch_bounds__(GRADS_NTH, 2) delta_chunk_grads_kernel(DeltaCh
         const int row = 16 * (w >> 1 & 1) + c;
         put(d, row, w & 1, pr[0]);
         put(d + 32 * P64, row, w & 1, pr[1]);
+        if (w < 2 * KS) {
 #pragma unroll
-        for (int i = 0; i < NP; ++i) {
-          const int p = w + GRADS_NTH / 64 * i, arr = p / (2 * KS), t2 = p / KS % 2, st = p % KS;
-          pstore(sT + arr * 32 * PK, PK, 16 * t2 + c, 32 * st + 8 * q, ps[i]);
+          for (int i = 0; i < 4; ++i) pstore(sT + i * 32 * PK, PK, 16 * pt + c, 32 * pst + 8 * q, ps[i]);
+          const Frag8 s0 = as_frag(ps[0]), s1 = as_frag(ps[1]), d0 = as_frag(ps[2]), d1 = as_frag(ps[3]);
+          dot += (unpack4(s0.a) + unpack4(s1.a)) * (unpack4(d0.a) + unpack4(d1.a));
+          dot += (unpack4(s0.b) + unpack4(s1.b)) * (unpack4(d0.b) + unpack4(d1.b));
         }
       }
       const Frag8 of = {__builtin_bit_cast(s16x4, po[0]), __builtin_bit_cast(s16x4, po[1])};
@@ -420,12 +482,16 @@ __global__ void __launch_bounds__(GRADS_NTH, 2) delta_chunk_grads_kernel(DeltaCh
         }
 #pragma unroll
       for (int t = 0; t < HT; ++t) {
-        const Frag8 sf = pcol(sT, PK, HT * half + t, 0, lane), df = pcol(sT + 32 * PK, PK, HT * half + t, 0, lane);
-        x1[t] = mma32(of, sf, x1[t]);
-        y2[t] = mma32(ml, sf, y2[t]);
-        y3[t] = mma32(rl, df, y3[t]);
-        y2[t] = mma32(mh, sf, y2[t]);
-        y3[t] = mma32(rh, df, y3[t]);
+        const Frag8 sh = pcol(sT, PK, HT * half + t, 0, lane), sl = pcol(sT + 32 * PK, PK, HT * half + t, 0, lane);
+        const Frag8 dh = pcol(sT + 64 * PK, PK, HT * half + t, 0, lane), dl = pcol(sT + 96 * PK, PK, HT * half + t, 0, lane);
+        x1[t] = mma32(of, sl, x1[t]);
+        y2[t] = mma32(ml, sh, y2[t]);
+        y3[t] = mma32(rl, dh, y3[t]);
+        y2[t] = mma32(mh, sl, y2[t]);
+        y3[t] = mma32(rh, dl, y3[t]);
+        x1[t] = mma32(of, sh, x1[t]);
+        y2[t] = mma32(mh, sh, y2[t]);
+        y3[t] = mma32(rh, dh, y3[t]);
       }
       // dv = mu, rounded: its hi part
       if (half == 1) {
@@ -440,14 +506,30 @@ __global__ void __launch_bounds__(GRADS_NTH, 2) delta_chunk_grads_kernel(DeltaCh
     // rows i = 16 wr + 4 q + r
     const f32x4 Gi = *(const f32x4*)(Gs + 16 * wr + 4 * q), Bi = *(const f32x4*)(Bs + 16 * wr + 4 * q);
     const float Ge = Gs[63];
-    f32x4 eg, we;
+    f32x4 eg, ee, rt = zero4(), ru = zero4();
 #pragma unroll
-    for (int r = 0; r < 4; ++r) eg[r] = exp_hw(Gi[r]), we[r] = exp_hw(Ge - Gi[r]) * Bi[r];
+    for (int r = 0; r < 4; ++r) eg[r] = exp_hw(Gi[r]), ee[r] = exp_hw(Ge - Gi[r]);
 #pragma unroll
     for (int t = 0; t < HT; ++t) {
-      dq[t] += a.scale * eg * x1[t];
-      dk[t] += we * y3[t] - eg * y2[t];
+      const f32x4 q4 = unpack4(ld_rowk(Qb, PK, 16 * wr, 16 * (HT * half + t), lane).v);
+      const f32x4 k4 = unpack4(ld_rowk(Kb, PK, 16 * wr, 16 * (HT * half + t), lane).v);
+      x1[t] *= a.scale * eg;
+      y2[t] *= eg;
+      y3[t] *= ee;
+      dq[t] += x1[t];
+      dk[t] += Bi * y3[t] - y2[t];
+      rt += q4 * x1[t] - k4 * y2[t];
+      ru += k4 * y3[t];
     }
+    rt -= Bi * ru;
+#pragma unroll
+    for (int r = 0; r < 4; ++r) rt[r] = sum16(rt[r]), ru[r] = sum16(ru[r]);
+    if (c == 0) {
+      *(f32x4*)(rowT[half] + 16 * wr + 4 * q) = rt;
+      *(f32x4*)(rowU[half] + 16 * wr + 4 * q) = ru;
+    }
+    const float dsum = wave_sum((dot[0] + dot[1]) + (dot[2] + dot[3]));
+    if (lane == 0) dots[w] = dsum;
     __syncthreads();  // the slices' tiles are free
     // pair terms: dD (half 0) or E (half 1); column j = 16 b + c
     f32x4 rm = zero4();
@@ -476,19 +558,21 @@ __global__ void __launch_bounds__(GRADS_NTH, 2) delta_chunk_grads_kernel(DeltaCh
           const int i = 16 * wr + 4 * q + r;
           const float gam = exp_hw(i >= j ? Gi[r] - Gj : 0.0f);
           if (i > j || (half == 0 && i == j)) x[r] = bj * pp[b][r] * gam;
+          const float g = i >= j ? gam * kq[b][r] * pp[b][r] : 0.0f;
           if (i > j) {
             const float m = x[r] * kq[b][r];
             rm[r] += m;
             cm += m;
-            ca += gam * kq[b][r] * pp[b][r];
+            if (half) ca -= g;  // -a_ij N_ij of dbeta_j
           }
+          if (!half) ca += a.scale * g;  // P_ij (dO_i . r_j)
         }
       }
       cm = sum4q(cm);
-      if (half) ca = sum4q(ca);
+      ca = sum4q(ca);
       if (q == 0) {
         colM[half][wr][j] = cm;
-        if (half) colA[wr][j] = ca;
+        colA[half][wr][j] = ca;
       }
       s16x4 hi, lo;
       split4(x, hi, lo);
@@ -533,18 +617,19 @@ __global__ void __launch_bounds__(GRADS_NTH, 2) delta_chunk_grads_kernel(DeltaCh
     }
     // dbeta, dg
     if (w == 0) {
-      float dG = 0.0f, db = 0.0f, tail = 0.0f;
+      float col = 0.0f, db = 0.0f, dot0 = 0.0f;
 #pragma unroll
-      for (int i = 0; i < 8; ++i) dG += rowG[i][lane], db += rowB[i][lane], tail += tails[i];
-      float col = 0.0f, ca = 0.0f;
+      for (int i = 0; i < 4; ++i) col += colM[0][i][lane] + colM[1][i][lane], db += colA[0][i][lane] + colA[1][i][lane];
 #pragma unroll
-      for (int i = 0; i < 4; ++i) col += colM[0][i][lane] + colM[1][i][lane], ca += colA[i][lane];
-      dG += rowM[0][lane] + rowM[1][lane] - col;
+      for (int i = 0; i < 8; ++i) dot0 += dots[i];
+      const float u = rowU[0][lane] + rowU[1][lane];
+      const float dG = rowT[0][lane] + rowT[1][lane] + rowM[0][lane] + rowM[1][lane] - col;
+      const float tail = exp_hw(Gs[63]) * dot0 + wave_sum(Bs[lane] * u);
       const float sum = wave_incl_suffix(dG, lane) + tail;
       if (lane < at.rows) {
         const i64 o = (at.tok0 + lane) * a.HV + hv;
         a.dg[o] = sum;
-        a.dbeta[o] = db - ca;
+        a.dbeta[o] = db + u;
       }
     }
   }
@@ -569,13 +654,13 @@ __global__ void __launch_bounds__(GRADS_NTH, 2) delta_chunk_grads_kernel(DeltaCh
 template <int KP>
 void launch_rev_grads(const DeltaChunkArgs& a, hipStream_t s) {
   const i64 blocks = walk_blocks(a.seq.nseq * a.HV, (a.V + 31) / 32);
-  hipLaunchKernelGGL((delta_chunk_rev_kernel<KP, 2>), dim3((unsigned)blocks), dim3(128), (RevLds<KP, 2>::TOTAL), s, a);
+  hipLaunchKernelGGL((delta_chunk_rev_kernel<KP>), dim3((unsigned)blocks), dim3(REV_NTH), (RevLds<KP>::TOTAL), s, a);
   if (a.nslots > 0)
     hipLaunchKernelGGL((delta_chunk_grads_kernel<KP>), dim3((unsigned)(a.nslots * a.H)), dim3(GRADS_NTH), 0, s, a);
 }
 
 struct BwdPlan {
-  i64 off_T, off_Tt, off_Pt, off_G, off_S, off_dS, off_r, off_X, off_mu, off_row, off_end;
+  i64 off_T, off_Tt, off_Pt, off_G, off_S, off_dS, off_r, off_mu;
   size_t bytes;
 };
 BwdPlan bwd_plan(const ssmvjp_delta_chunk_desc& d) {
@@ -592,12 +677,9 @@ BwdPlan bwd_plan(const ssmvjp_delta_chunk_desc& d) {
   p.off_Pt = carve(cells * 12 * 1024);
   p.off_G = carve(cells * 64 * 4);
   p.off_S = carve(tiles * KP * 16 * 2 * 2);
-  p.off_dS = carve(tiles * KP * 16 * 2);
+  p.off_dS = carve(tiles * KP * 16 * 2 * 2);
   p.off_r = carve(tiles * 4 * 1024);
-  p.off_X = carve(tiles * 4 * 1024);
   p.off_mu = carve(tiles * 4 * 1024);
-  p.off_row = carve(tiles * 3 * 64 * 4);
-  p.off_end = carve(tiles * 4);
   p.bytes = (size_t)off;
   return p;
 }
@@ -616,8 +698,6 @@ hipError_t launch_delta_chunk_bwd(const ssmvjp_delta_chunk_desc& d, const DeltaC
   auto b16 = [&](i64 off) { return (bf16*)(ws + off); };
   a.Tf = b16(pl.off_T); a.Tt = b16(pl.off_Tt); a.Pt = b16(pl.off_Pt); a.G = (float*)(ws + pl.off_G);
   a.Sw = b16(pl.off_S); a.dSw = b16(pl.off_dS); a.rw = b16(pl.off_r); a.muw = b16(pl.off_mu);
-  a.Xw = (float*)(ws + pl.off_X);
-  a.rowp = (float*)(ws + pl.off_row); a.endp = (float*)(ws + pl.off_end);
   if (a.nslots > 0) {
     hipError_t e = launch_delta_prep(a, true, stream);
     if (e == hipSuccess) e = launch_delta_states(a, stream);
