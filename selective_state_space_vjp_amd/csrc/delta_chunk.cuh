@@ -48,11 +48,12 @@ struct DeltaChunkArgs {
   float* G;   // [64]
   bf16* Tt;   // [6][2][64][8] fragments of T^T - I                  (backward from here on)
   bf16* Pt;   // [6][2][64][8] fragments of scale P^T
-  // per 16-column tile (cell * nvt + tile), hi and lo parts:
-  bf16* Sw;   // [2][KP/32][64][8] fragments of the state before the chunk
-  bf16* dSw;  // [2][KP/32][64][8] of the state's gradient behind the chunk
-  bf16* rw;   // [2][2][64][8] fragments of r
-  bf16* muw;  // [2][2][64][8] of mu
+  // per 16-column tile (cell * nvt + tile), hi and lo parts, in the order in which the gradients kernel reads
+  // them from LDS (state_slot, row_slot):
+  bf16* Sw;   // [2][KP/32][64][8] the state before the chunk
+  bf16* dSw;  // [2][KP/32][64][8] the state's gradient behind the chunk
+  bf16* rw;   // [2][4][64][4] r
+  bf16* muw;  // [2][4][64][4] mu
 };
 
 typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
@@ -123,6 +124,29 @@ __device__ __forceinline__ int row_swz(int row) { return ((row & 1) << 2) | ((ro
 // group q <-> column 32s + 8q + e.  The state's tiles match it by their rows:
 // row 4q + r of tile 2s + b is key 32s + 8q + 4b + r.
 __device__ __forceinline__ int state_row(int tile, int q) { return 32 * (tile >> 1) + 8 * q + 4 * (tile & 1); }
+
+// What the walks keep is read by columns, 4 rows of 4 units of 8 bytes at a time
+// (a transposed read of 16 lanes): these orders put each such group into 128
+// bytes of its own, so that the blocks go to LDS as they are.
+// The 8-key pieces of a state's fragment, lane (c, q): 16-byte slots.
+__device__ __forceinline__ int state_slot(int lane) {
+  const int c = lane & 15, q = lane >> 4;
+  return (c >> 2) * 16 + q * 4 + (c & 3);
+}
+// The four rows 4q .. of one row tile, lane (c, q): 8-byte slots.
+__device__ __forceinline__ int row_slot(int lane) {
+  const int c = lane & 15, q = lane >> 4;
+  return (c >> 2) * 16 + (c & 3) * 4 + q;
+}
+// column tile b of r or mu, contraction over 32 columns of V: t0, t1 are the blocks [4][64][4] of two tiles
+__device__ __forceinline__ Frag8 kept_rows(const bf16* t0, const bf16* t1, int b, int lane) {
+  return {lds_tr_b16(t0 + b * 256 + lane * 4).v, lds_tr_b16(t1 + b * 256 + lane * 4).v};
+}
+// keys 16t .. of a state, contraction over 32 columns of V: t0, t1 are the blocks [KP/32][64][8] of two tiles
+__device__ __forceinline__ Frag8 kept_keys(const bf16* t0, const bf16* t1, int t, int lane) {
+  const int m = lane & 15, o = (t >> 1) * 512 + ((lane >> 4) * 16 + ((t & 1) * 2 + ((m >> 1) & 1)) * 4 + (m >> 2)) * 8 + (m & 1) * 4;
+  return {lds_tr_b16(t0 + o).v, lds_tr_b16(t1 + o).v};
+}
 
 // a state [K][V] in memory (NULL, or a wave without columns: zeros): four rows of column v of tile t
 __device__ __forceinline__ brsrc state_rsrc(const float* S, const DeltaChunkArgs& a, i64 unit, bool act) {

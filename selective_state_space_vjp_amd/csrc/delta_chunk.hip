@@ -312,9 +312,9 @@ delta_chunk_walk_kernel(DeltaChunkArgs a) {
         // the state's parts and r: to the follower, or to memory
         const i64 tile = (cell0 + ch * a.HV) * a.nvt + vt;
         u32x4* So = FWD ? (u32x4*)(smem_raw + L::S + bf * L::SBUF + t16 * (L::SBUF / 2)) + lane
-                        : (u32x4*)(a.Sw + tile * 2 * KS * 512) + lane;
+                        : (u32x4*)(a.Sw + tile * 2 * KS * 512) + state_slot(lane);
         f32x4* Ro = (f32x4*)(smem_raw + L::R + (bf * 2 + t16) * 4096) + lane;
-        u32x4* Rw = (u32x4*)(a.rw + tile * 4 * 512) + lane;
+        s16x4* Rw = (s16x4*)(a.rw + tile * 4 * 512) + row_slot(lane);
         const float *eG = gates(ch), *wB = eG + 64;
         // Six stretches of MFMAs, each with the vector and LDS work of its neighbours between them: a 16x16x32
         // MFMA holds the matrix pipe for 16 cycles, in which three vector instructions issue.
@@ -405,8 +405,10 @@ delta_chunk_walk_kernel(DeltaChunkArgs a) {
           } else {
             Frag8 rh, rl;
             split8(x[2 * s], x[2 * s + 1], rh, rl);
-            Rw[s * 64] = as_u4(rh);
-            Rw[128 + s * 64] = as_u4(rl);
+            Rw[2 * s * 64] = rh.a;
+            Rw[(2 * s + 1) * 64] = rh.b;
+            Rw[256 + 2 * s * 64] = rl.a;
+            Rw[256 + (2 * s + 1) * 64] = rl.b;
           }
         };
         keep(0);

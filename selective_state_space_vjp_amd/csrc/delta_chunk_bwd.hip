@@ -89,8 +89,8 @@ delta_chunk_rev_kernel(DeltaChunkArgs a) {
         const bf16* Ot = d_o(ch);
         const f32x4* B = Bof(ch);
         const i64 tile = (cell0 + ch * a.HV) * a.nvt + vt;
-        u32x4* Dw = (u32x4*)(a.dSw + tile * 2 * KS * 512) + lane;
-        u32x4* Mw = (u32x4*)(a.muw + tile * 4 * 512) + lane;
+        u32x4* Dw = (u32x4*)(a.dSw + tile * 2 * KS * 512) + state_slot(lane);
+        s16x4* Mw = (s16x4*)(a.muw + tile * 4 * 512) + row_slot(lane);
         const float *eG = gates(ch), *eE = eG + 64, *be = eG + 128;
         // 1: z = K dS, row tiles 2 and 3, both parts of dS
         f32x4 z[4], du[4], e[4], b[4];
@@ -183,8 +183,10 @@ delta_chunk_rev_kernel(DeltaChunkArgs a) {
         auto keep = [&](int s) {
           Frag8 hi, lo;
           split8(mu[2 * s], mu[2 * s + 1], hi, lo);
-          Mw[s * 64] = as_u4(hi);
-          Mw[128 + s * 64] = as_u4(lo);
+          Mw[2 * s * 64] = hi.a;
+          Mw[(2 * s + 1) * 64] = hi.b;
+          Mw[256 + 2 * s * 64] = lo.a;
+          Mw[256 + (2 * s + 1) * 64] = lo.b;
         };
         turn(1);
 #pragma unroll
@@ -331,13 +333,17 @@ delta_chunk_rev_kernel(DeltaChunkArgs a) {
 // ---------------------------------------------------------------------------
 // Eight waves: wave (wr = w % 4, half = w / 4) owns row tile wr of every 64-row
 // result and one half of the key columns; of the pair terms, half 0 forms dD
-// and half 1 E.  The columns of V go by 32 (one contraction step): r, mu (two
-// parts), S0, dS (one part) of the slice are brought to LDS as [v][row] tiles,
-// whose transposed reads are the operands with the contraction over v.
+// and half 1 E.  The columns of V go by 32 (one contraction step): r, mu, S0 and
+// dS of the slice, both parts, come to LDS by LDS-direct loads, one slice ahead
+// and over the border between two value heads (two buffers), and are read
+// transposed, the contraction running over v.  dD and E then take the place of
+// the last slice.
+//
+// Bound by what the walks kept: 208 KB of a chunk and head at K = V = 128.
 constexpr int GRADS_NTH = 512;
 
-// Row pitches of the tiles: 40 bytes past a multiple of 128.  The 16 rows of a
-// fragment read meet 16 different pairs of banks, the 4 rows of a transposed
+// Row pitches of the padded tiles: 40 bytes past a multiple of 128.  The 16 rows
+// of a fragment read meet 16 different pairs of banks, the 4 rows of a transposed
 // read overlap in 24 bytes of 128, and, unlike in a swizzled tile, every
 // fragment is the lane's own address plus a constant: swizzled, the addresses
 // alone took more registers than there are.
@@ -356,23 +362,49 @@ __device__ __forceinline__ void pstore(bf16* t, int pitch, int row, int col, con
 }
 
 template <int KP>
+struct GradsLds {  // byte offsets
+  static constexpr int KS = KP / 32, PK = KP + 20;
+  static constexpr int R = 0, MU = 8 * 1024, S = 16 * 1024, DS = S + 4 * KS * 1024, SLICE = DS + 4 * KS * 1024;
+  static constexpr int PAIRS = 4 * 64 * P64 * 2;  // dD^T, E^T, two parts each
+  static constexpr int BUF = SLICE > PAIRS ? SLICE : PAIRS;
+  static constexpr int K = 2 * BUF, Q = K + 64 * PK * 2, F = Q + 64 * PK * 2, TOTAL = F + 4 * (2 * 64 + 3 * 2 * 64 + 2 * 2 * 4 * 64 + 8);
+};
+
+template <int KP>
 __global__ void __launch_bounds__(GRADS_NTH, 2) delta_chunk_grads_kernel(DeltaChunkArgs a) {
   constexpr int KS = KP / 32, KT = KP / 16, PK = KP + 20, HT = KT / 2;  // HT: key tiles of a wave
-  static_assert(4 * 64 * P64 <= 4 * 32 * (P64 + PK), "dD and E fit where the slices' tiles were");
-  __shared__ __attribute__((aligned(16))) bf16 Kb[64 * PK], Qb[64 * PK];
-  // the slice's tiles; behind the slices the same memory holds dD^T and E^T, two parts each
-  __shared__ __attribute__((aligned(16))) bf16 buf[4 * 32 * (P64 + PK)];
-  __shared__ __attribute__((aligned(16))) float Gs[64], Bs[64], rowM[2][64], colM[2][4][64], colA[2][4][64];
-  __shared__ float rowT[2][64], rowU[2][64], dots[8];  // row terms of dG; su without beta; <S0, dS> by wave
+  typedef GradsLds<KP> L;
+  extern __shared__ __align__(16) unsigned char smem_raw[];
+  bf16 *const Kb = (bf16*)(smem_raw + L::K), *const Qb = (bf16*)(smem_raw + L::Q);
+  float *const Gs = (float*)(smem_raw + L::F), *const Bs = Gs + 64;
+  // row terms of dG, su without beta, row sums of M (by half); column sums of M and of dbeta's pairs; <S0, dS> by wave
+  float(*const rowT)[64] = (float(*)[64])(Gs + 128), (*const rowU)[64] = rowT + 2, (*const rowM)[64] = rowT + 4;
+  float(*const colM)[4][64] = (float(*)[4][64])(Gs + 512), (*const colA)[4][64] = colM + 2;
+  float* const dots = Gs + 512 + 1024;
   typedef unsigned u32x2 __attribute__((ext_vector_type(2)));
-  bf16 *rH = buf, *mH = buf + 2 * 32 * P64;  // each followed by its lo part
-  bf16* sT = buf + 4 * 32 * P64;             // [S0 hi, lo, dS hi, lo][32][PK]
   const int tid = threadIdx.x, lane = tid & 63, w = __builtin_amdgcn_readfirstlane(tid >> 6), c = lane & 15, q = lane >> 4;
   const int wr = w & 3, half = w >> 2;
   const unsigned H32 = (unsigned)a.H;
   const i64 h = blockIdx.x % H32, slot = blockIdx.x / H32;
   const ChunkAt at = chunk_at(a.seq, slot, lane);
   if (at.rows == 0) return;
+  const int nsl = (int)(a.nvt + 1) / 2, nvt = (int)a.nvt;
+  const unsigned lds0 = lds_base(smem_raw);
+  // slice sl of value head hv into buffer bf, in three parts (r and mu, S0, dS), tiles past V as zeros
+  auto issue = [&](int part, i64 hv, int sl, int bf) {
+    const i64 tile = (slot * a.HV + hv) * nvt + 2 * sl;
+    const unsigned b = lds0 + (unsigned)(bf * L::BUF), left = nvt - 2 * sl > 1 ? 2u : 1u;
+    if (part == 0) {
+      flat_dma<8, 8>(b + L::R, w, lane, rsrc_words_u(a.rw + tile * 2048, left * 4096u));
+      flat_dma<8, 8>(b + L::MU, w, lane, rsrc_words_u(a.muw + tile * 2048, left * 4096u));
+    } else if (part == 1) {
+      flat_dma<4 * KS, 8>(b + L::S, w, lane, rsrc_words_u(a.Sw + tile * KS * 1024, left * KS * 2048u));
+    } else {
+      flat_dma<4 * KS, 8>(b + L::DS, w, lane, rsrc_words_u(a.dSw + tile * KS * 1024, left * KS * 2048u));
+    }
+  };
+#pragma unroll
+  for (int i = 0; i < 3; ++i) issue(i, h * a.rep, 0, 0);
   {
     constexpr int N = 64 * KP / 8 / GRADS_NTH;
     const brsrc rk = row_rsrc(a.k, at.tok0, at.rows, a.H, h, a.K), rq = row_rsrc(a.q, at.tok0, at.rows, a.H, h, a.K);
@@ -395,30 +427,12 @@ __global__ void __launch_bounds__(GRADS_NTH, 2) delta_chunk_grads_kernel(DeltaCh
 #pragma unroll
   for (int t = 0; t < HT; ++t) dq[t] = zero4(), dk[t] = zero4();
 
-  const int nsl = (int)(a.nvt + 1) / 2;
+  int bf = 0;  // the buffer of the slice at hand
   for (i64 rr = 0; rr < a.rep; ++rr) {
     const i64 hv = h * a.rep + rr, cu = slot * a.HV + hv;
-    u32x4 pr[2], ps[4];
     u32x2 po[2];
     const brsrc ro = row_rsrc(a.d_o, at.tok0, at.rows, a.HV, hv, a.V);
-    // tiles past V lie past the resources: zeros, without a branch
-    const brsrc rm4 = make_rsrc((w < 4 ? a.rw : a.muw) + cu * a.nvt * 2048, (unsigned)(a.nvt * 4096));
-    const brsrc rS = make_rsrc(a.Sw + cu * a.nvt * KS * 1024, (unsigned)(a.nvt * KS * 2048));
-    const brsrc rD = make_rsrc(a.dSw + cu * a.nvt * KS * 1024, (unsigned)(a.nvt * KS * 2048));
-    const int pt = w / KS, pst = w % KS;  // waves below 2 KS: the tile and step whose four pieces this thread brings
-    auto fetch = [&](int sl) {
-      {  // waves 0 .. 3: r, the others mu; hi and lo of one fragment
-        const unsigned o = (unsigned)(((sl * 2 + (w >> 1 & 1)) * 256 + (w & 1) * 64 + lane) * 16);
-        pr[0] = bload16(rm4, o);
-        pr[1] = bload16(rm4, o + 2048u);
-      }
-      if (w < 2 * KS) {
-        const unsigned o = (unsigned)((((sl * 2 + pt) * 2 * KS + pst) * 64 + lane) * 16);
-        ps[0] = bload16(rS, o);
-        ps[1] = bload16(rS, o + KS * 1024u);
-        ps[2] = bload16(rD, o);
-        ps[3] = bload16(rD, o + KS * 1024u);
-      }
+    auto fetch_o = [&](int sl) {
 #pragma unroll
       for (int e = 0; e < 2; ++e) {
         const int col = sl * 32 + 16 * e + 4 * q;
@@ -426,19 +440,10 @@ __global__ void __launch_bounds__(GRADS_NTH, 2) delta_chunk_grads_kernel(DeltaCh
             ro, col < a.V ? (int)(((16 * wr + c) * a.HV * a.V + col) * 2) : (int)BUF_OOB, 0, 0));
       }
     };
-    auto put = [&](bf16* t, int row, int s, const u32x4& u) {  // a fragment's two 4-element runs
-      *(u32x2*)(t + row * P64 + 32 * s + 4 * q) = u32x2{u[0], u[1]};
-      *(u32x2*)(t + row * P64 + 32 * s + 16 + 4 * q) = u32x2{u[2], u[3]};
-    };
-    fetch(0);
-    float G0 = 0.0f, b0 = 0.0f;
+    fetch_o(0);
     if (w == 0) {
-      G0 = a.G[cu * 64 + lane];
-      b0 = lane < at.rows ? a.beta[(at.tok0 + lane) * a.HV + hv] : 0.0f;
-    }
-    __syncthreads();  // the previous head's readers are done; k and q are in LDS
-    if (w == 0) {
-      Gs[lane] = G0;
+      const float G0 = a.G[cu * 64 + lane], b0 = lane < at.rows ? a.beta[(at.tok0 + lane) * a.HV + hv] : 0.0f;
+      Gs[lane] = G0;  // the previous head's readers of these are past the barrier behind its last sums
       Bs[lane] = b0;
     }
     f32x4 pp[4], x1[HT], y2[HT], y3[HT];  // pp: dO . r (half 0) or mu . r; dO S0^T, mu S0^T, r dS^T
@@ -447,51 +452,54 @@ __global__ void __launch_bounds__(GRADS_NTH, 2) delta_chunk_grads_kernel(DeltaCh
 #pragma unroll
     for (int t = 0; t < HT; ++t) x1[t] = zero4(), y2[t] = zero4(), y3[t] = zero4();
     f32x4 dot = zero4();
+    dma_wait();
+    __syncthreads();  // the first slice has landed; k and q are in LDS
     for (int sl = 0; sl < nsl; ++sl) {
-      if (sl) __syncthreads();
-      {
-        bf16* d = w < 4 ? rH : mH;
-        const int row = 16 * (w >> 1 & 1) + c;
-        put(d, row, w & 1, pr[0]);
-        put(d + 32 * P64, row, w & 1, pr[1]);
-        if (w < 2 * KS) {
-#pragma unroll
-          for (int i = 0; i < 4; ++i) pstore(sT + i * 32 * PK, PK, 16 * pt + c, 32 * pst + 8 * q, ps[i]);
-          const Frag8 s0 = as_frag(ps[0]), s1 = as_frag(ps[1]), d0 = as_frag(ps[2]), d1 = as_frag(ps[3]);
-          dot += (unpack4(s0.a) + unpack4(s1.a)) * (unpack4(d0.a) + unpack4(d1.a));
-          dot += (unpack4(s0.b) + unpack4(s1.b)) * (unpack4(d0.b) + unpack4(d1.b));
-        }
-      }
+      const bool last = sl + 1 == nsl;
+      // the next slice's loads, spread over this one's products: all at once they block for 2,000 cycles
+      const bool ahead = !last || rr + 1 < a.rep;
+      const i64 nhv = last ? hv + 1 : hv;
+      const int nxt = last ? 0 : sl + 1;
+      if (ahead) issue(0, nhv, nxt, bf ^ 1);
       const Frag8 of = {__builtin_bit_cast(s16x4, po[0]), __builtin_bit_cast(s16x4, po[1])};
-      __syncthreads();
-      if (sl + 1 < nsl) fetch(sl + 1);
-      const Frag8 mh = pcol(mH, P64, wr, 0, lane), ml = pcol(mH + 32 * P64, P64, wr, 0, lane);
-      const Frag8 rh = pcol(rH, P64, wr, 0, lane), rl = pcol(rH + 32 * P64, P64, wr, 0, lane);
-#pragma unroll
-      for (int b = 0; b < 4; ++b)
-        if (b <= wr) {
-          const Frag8 bh = pcol(rH, P64, b, 0, lane), bl = pcol(rH + 32 * P64, P64, b, 0, lane);
-          if (half == 0) {
-            pp[b] = mma32(of, bl, pp[b]);
-            pp[b] = mma32(of, bh, pp[b]);
-          } else {
-            pp[b] = mma32(mh, bl, pp[b]);
-            pp[b] = mma32(ml, bh, pp[b]);
-            pp[b] = mma32(mh, bh, pp[b]);
-          }
-        }
+      if (!last) fetch_o(sl + 1);
+      const unsigned char* const buf = smem_raw + bf * L::BUF;
+      const bf16 *R = (const bf16*)(buf + L::R), *MU = (const bf16*)(buf + L::MU), *S = (const bf16*)(buf + L::S),
+                 *DS = (const bf16*)(buf + L::DS);
+      // [tile][hi, lo]: 1024 values each of r and mu, 512 KS of the states
+      const Frag8 mh = kept_rows(MU, MU + 2048, wr, lane), ml = kept_rows(MU + 1024, MU + 3072, wr, lane);
+      const Frag8 rh = kept_rows(R, R + 2048, wr, lane), rl = kept_rows(R + 1024, R + 3072, wr, lane);
 #pragma unroll
       for (int t = 0; t < HT; ++t) {
-        const Frag8 sh = pcol(sT, PK, HT * half + t, 0, lane), sl = pcol(sT + 32 * PK, PK, HT * half + t, 0, lane);
-        const Frag8 dh = pcol(sT + 64 * PK, PK, HT * half + t, 0, lane), dl = pcol(sT + 96 * PK, PK, HT * half + t, 0, lane);
-        x1[t] = mma32(of, sl, x1[t]);
+        const int k = HT * half + t;
+        const Frag8 sh = kept_keys(S, S + 1024 * KS, k, lane), sl2 = kept_keys(S + 512 * KS, S + 1536 * KS, k, lane);
+        const Frag8 dh = kept_keys(DS, DS + 1024 * KS, k, lane), dl = kept_keys(DS + 512 * KS, DS + 1536 * KS, k, lane);
+        x1[t] = mma32(of, sl2, x1[t]);
         y2[t] = mma32(ml, sh, y2[t]);
         y3[t] = mma32(rl, dh, y3[t]);
-        y2[t] = mma32(mh, sl, y2[t]);
+        y2[t] = mma32(mh, sl2, y2[t]);
         y3[t] = mma32(rh, dl, y3[t]);
         x1[t] = mma32(of, sh, x1[t]);
         y2[t] = mma32(mh, sh, y2[t]);
         y3[t] = mma32(rh, dh, y3[t]);
+      }
+      if (ahead) issue(1, nhv, nxt, bf ^ 1);
+      // all four column tiles: what lies above the diagonal is dropped later, and straight code is read ahead
+      const Frag8 none = as_frag(zero_u4()), ph = half ? mh : of, pl = half ? ml : none;
+#pragma unroll
+      for (int b = 0; b < 4; ++b) {
+        const Frag8 bh = kept_rows(R, R + 2048, b, lane), bl = kept_rows(R + 1024, R + 3072, b, lane);
+        pp[b] = mma32(ph, bl, pp[b]);
+        pp[b] = mma32(pl, bh, pp[b]);
+        pp[b] = mma32(ph, bh, pp[b]);
+      }
+      if (ahead) issue(2, nhv, nxt, bf ^ 1);
+      if (w < 2 * KS) {  // this wave's 64 pieces of each array
+        const int o = (w / KS) * 1024 * KS + (w % KS) * 512 + lane * 8;
+        const Frag8 s0 = as_frag(*(const u32x4*)(S + o)), s1 = as_frag(*(const u32x4*)(S + o + 512 * KS));
+        const Frag8 d0 = as_frag(*(const u32x4*)(DS + o)), d1 = as_frag(*(const u32x4*)(DS + o + 512 * KS));
+        dot += (unpack4(s0.a) + unpack4(s1.a)) * (unpack4(d0.a) + unpack4(d1.a));
+        dot += (unpack4(s0.b) + unpack4(s1.b)) * (unpack4(d0.b) + unpack4(d1.b));
       }
       // dv = mu, rounded: its hi part
       if (half == 1) {
@@ -501,6 +509,11 @@ __global__ void __launch_bounds__(GRADS_NTH, 2) delta_chunk_grads_kernel(DeltaCh
           if (16 * wr + c < at.rows && col < a.V)
             *(s16x4*)(a.dv + ((at.tok0 + 16 * wr + c) * a.HV + hv) * a.V + col) = e ? mh.b : mh.a;
         }
+      }
+      if (!last) {
+        dma_wait();
+        __syncthreads();
+        bf ^= 1;
       }
     }
     // rows i = 16 wr + 4 q + r
@@ -530,10 +543,12 @@ __global__ void __launch_bounds__(GRADS_NTH, 2) delta_chunk_grads_kernel(DeltaCh
     }
     const float dsum = wave_sum((dot[0] + dot[1]) + (dot[2] + dot[3]));
     if (lane == 0) dots[w] = dsum;
-    __syncthreads();  // the slices' tiles are free
+    __syncthreads();  // the last slice's readers are done
     // pair terms: dD (half 0) or E (half 1); column j = 16 b + c
     f32x4 rm = zero4();
-    bf16* const Pt = buf + half * 2 * 64 * P64;  // [hi, lo][64][64], transposed: row j
+    bf16* const pairs = (bf16*)(smem_raw + bf * L::BUF);  // dD hi, lo, E hi, lo
+    bf16* const Pt = pairs + half * 2 * 64 * P64;         // [hi, lo][64][64], transposed: row j
+    bf ^= 1;
     Frag8 rf[KS];
 #pragma unroll
     for (int s = 0; s < KS; ++s) rf[s] = prow(half ? Kb : Qb, PK, wr, s, lane);
@@ -591,7 +606,7 @@ __global__ void __launch_bounds__(GRADS_NTH, 2) delta_chunk_grads_kernel(DeltaCh
       Frag8 dr[2], er[2], dc[2], ec[2];
 #pragma unroll
       for (int e = 0; e < 2; ++e) {
-        const bf16 *D = buf + e * 64 * P64, *E = buf + (2 + e) * 64 * P64;
+        const bf16 *D = pairs + e * 64 * P64, *E = pairs + (2 + e) * 64 * P64;
         dr[e] = pcol(D, P64, wr, s, lane);
         er[e] = pcol(E, P64, wr, s, lane);
         dc[e] = prow(D, P64, wr, s, lane);
@@ -656,7 +671,8 @@ void launch_rev_grads(const DeltaChunkArgs& a, hipStream_t s) {
   const i64 blocks = walk_blocks(a.seq.nseq * a.HV, (a.V + 31) / 32);
   hipLaunchKernelGGL((delta_chunk_rev_kernel<KP>), dim3((unsigned)blocks), dim3(REV_NTH), (RevLds<KP>::TOTAL), s, a);
   if (a.nslots > 0)
-    hipLaunchKernelGGL((delta_chunk_grads_kernel<KP>), dim3((unsigned)(a.nslots * a.H)), dim3(GRADS_NTH), 0, s, a);
+    hipLaunchKernelGGL((delta_chunk_grads_kernel<KP>), dim3((unsigned)(a.nslots * a.H)), dim3(GRADS_NTH),
+                       (GradsLds<KP>::TOTAL), s, a);
 }
 
 struct BwdPlan {
