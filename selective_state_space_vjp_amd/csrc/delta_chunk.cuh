@@ -125,6 +125,13 @@ __device__ __forceinline__ int row_swz(int row) { return ((row & 1) << 2) | ((ro
 // row 4q + r of tile 2s + b is key 32s + 8q + 4b + r.
 __device__ __forceinline__ int state_row(int tile, int q) { return 32 * (tile >> 1) + 8 * q + 4 * (tile & 1); }
 
+// a store that the L2 need not keep: the walks write more than it holds, and what it holds (k, q, fragments) is
+// read by the other slices of the head
+template <typename T>
+__device__ __forceinline__ void stream_store(T* p, const T& v) {
+  __builtin_nontemporal_store(v, p);
+}
+
 // What the walks keep is read by columns, 4 rows of 4 units of 8 bytes at a time
 // (a transposed read of 16 lanes): these orders put each such group into 128
 // bytes of its own, so that the blocks go to LDS as they are.

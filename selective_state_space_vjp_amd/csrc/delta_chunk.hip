@@ -311,8 +311,8 @@ delta_chunk_walk_kernel(DeltaChunkArgs a) {
         const u32x4* Tf = (const u32x4*)(buf + L::T) + lane;
         // the state's parts and r: to the follower, or to memory
         const i64 tile = (cell0 + ch * a.HV) * a.nvt + vt;
-        u32x4* So = FWD ? (u32x4*)(smem_raw + L::S + bf * L::SBUF + t16 * (L::SBUF / 2)) + lane
-                        : (u32x4*)(a.Sw + tile * 2 * KS * 512) + state_slot(lane);
+        u32x4* So = (u32x4*)(smem_raw + L::S + bf * L::SBUF + t16 * (L::SBUF / 2)) + lane;
+        u32x4* Sw = (u32x4*)(a.Sw + tile * 2 * KS * 512) + state_slot(lane);
         f32x4* Ro = (f32x4*)(smem_raw + L::R + (bf * 2 + t16) * 4096) + lane;
         s16x4* Rw = (s16x4*)(a.rw + tile * 4 * 512) + row_slot(lane);
         const float *eG = gates(ch), *wB = eG + 64;
@@ -364,7 +364,15 @@ delta_chunk_walk_kernel(DeltaChunkArgs a) {
 #pragma unroll
         for (int i = 0; i < 6; ++i) th[i] = as_frag(Tf[i * 128]), tl[i] = as_frag(Tf[i * 128 + 64]);
 #pragma unroll
-        for (int s = 0; s < KS; ++s) So[s * 64] = as_u4(sh[s]), So[(KS + s) * 64] = as_u4(sl[s]);
+        for (int s = 0; s < KS; ++s) {
+          if constexpr (FWD) {
+            So[s * 64] = as_u4(sh[s]);
+            So[(KS + s) * 64] = as_u4(sl[s]);
+          } else {
+            stream_store(Sw + s * 64, as_u4(sh[s]));
+            stream_store(Sw + (KS + s) * 64, as_u4(sl[s]));
+          }
+        }
         pipe<4 * KS, 3, 1>();
         SSMVJP_FENCE();
         // 3: r = T (V - e^G K S0), contraction over tiles 0 and 1; the other residual
@@ -405,10 +413,10 @@ delta_chunk_walk_kernel(DeltaChunkArgs a) {
           } else {
             Frag8 rh, rl;
             split8(x[2 * s], x[2 * s + 1], rh, rl);
-            Rw[2 * s * 64] = rh.a;
-            Rw[(2 * s + 1) * 64] = rh.b;
-            Rw[256 + 2 * s * 64] = rl.a;
-            Rw[256 + (2 * s + 1) * 64] = rl.b;
+            stream_store(Rw + 2 * s * 64, rh.a);
+            stream_store(Rw + (2 * s + 1) * 64, rh.b);
+            stream_store(Rw + 256 + 2 * s * 64, rl.a);
+            stream_store(Rw + 256 + (2 * s + 1) * 64, rl.b);
           }
         };
         keep(0);

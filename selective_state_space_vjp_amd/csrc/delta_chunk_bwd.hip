@@ -112,7 +112,7 @@ delta_chunk_rev_kernel(DeltaChunkArgs a) {
 #pragma unroll
         for (int s = 0; s < 2; ++s) of[s] = {col4(Ot, 32, 2 * s, t16, lane), col4(Ot, 32, 2 * s + 1, t16, lane)};
 #pragma unroll
-        for (int s = 0; s < KS; ++s) Dw[s * 64] = as_u4(dh[s]), Dw[(KS + s) * 64] = as_u4(dl[s]);
+        for (int s = 0; s < KS; ++s) stream_store(Dw + s * 64, as_u4(dh[s])), stream_store(Dw + (KS + s) * 64, as_u4(dl[s]));
         pipe<4 * KS, 2, 1>();
         SSMVJP_FENCE();
         // 2: scale P^T dO
@@ -183,10 +183,10 @@ delta_chunk_rev_kernel(DeltaChunkArgs a) {
         auto keep = [&](int s) {
           Frag8 hi, lo;
           split8(mu[2 * s], mu[2 * s + 1], hi, lo);
-          Mw[2 * s * 64] = hi.a;
-          Mw[(2 * s + 1) * 64] = hi.b;
-          Mw[256 + 2 * s * 64] = lo.a;
-          Mw[256 + (2 * s + 1) * 64] = lo.b;
+          stream_store(Mw + 2 * s * 64, hi.a);
+          stream_store(Mw + (2 * s + 1) * 64, hi.b);
+          stream_store(Mw + 256 + 2 * s * 64, lo.a);
+          stream_store(Mw + 256 + (2 * s + 1) * 64, lo.b);
         };
         turn(1);
 #pragma unroll
