@@ -179,16 +179,6 @@ __device__ __forceinline__ Frag8 key_frag(const bf16* x, int KP, int t, int s, i
   return {lds_tr_b16(x + row * KP + ((u ^ row_swz(row)) << 3) + 4 * (t & 1)).v,
           lds_tr_b16(x + (row + 16) * KP + ((u ^ row_swz(row + 16)) << 3) + 4 * (t & 1)).v};
 }
-// columns 16t .. 16t+15 of a tile in the 8-byte swizzle, contraction over its rows 32s ..
-__device__ __forceinline__ Frag8 col_frag(const bf16* x, int pitch, int t, int s, int lane) {
-  return {ld_rowk_xs(x, pitch, 32 * s, 16 * t, lane).v, ld_rowk_xs(x, pitch, 32 * s + 16, 16 * t, lane).v};
-}
-
-// rows 16m .. of such a tile, contraction over its columns in the token fragments' slot order
-__device__ __forceinline__ Frag8 xs_frag(const bf16* t, int pitch, int m, int s, int lane) {
-  return {ld_colk_xs(t, pitch, 16 * m, 32 * s, lane).v, ld_colk_xs(t, pitch, 16 * m, 32 * s + 16, lane).v};
-}
-
 // LDS-direct loads of one chunk's tiles, shared out over NW waves, 1 KB (64
 // pieces of 16 bytes) an instruction.  A wave's instructions are consecutive,
 // so that the swizzle depends on the lane and the instruction's parity only.

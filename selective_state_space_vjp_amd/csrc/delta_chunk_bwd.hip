@@ -11,11 +11,12 @@
 //     dk = -e^G mu S0^T + (e^{G_63 - G} beta r) dS^T + dD^T Q + E K + E^T K
 //     dbeta_j = r_j . dU_j - sum_{i > j} a_ij N_ij
 //     M_ij = dD_ij q_i . k_j + E_ij k_i . k_j
-//     dG_i = q_i . (scale e^G dO S0^T)_i - k_i . (e^G mu S0^T)_i - su_i + sum_j M_ij - sum_j M_ji
+//     dG_i = q_i . (scale e^G dO S0^T)_i - k_i . (e^G mu S0^T)_i + sum_{j < i} M_ij - sum_{j > i} M_ji
 //     su_i = k_i . ((e^{G_63 - G} beta r) dS^T)_i
-//     dg_t = sum_{i >= t} dG_i + sum_i su_i + e^{G_63} <S0, dS>
+//     dg_t = sum_{i >= t} dG_i + sum_{i < t} su_i + e^{G_63} <S0, dS>
 //     r_j . dU_j = scale sum_{i >= j} P_ij (dO_i . r_j) + su_j / beta_j
-// (the last sum is formed without beta.)  In the sum over i >= t the pairs with
+// (dG_i without -su_i, which the gate of the chunk's end cancels for i >= t; the
+// last sum is formed without beta.)  In the sum over i >= t the pairs with
 // both tokens behind t cancel between the row and the column sums, exactly,
 // since both add the same float32 M_ij; that is why r, mu and the states enter
 // with both bf16 parts, and dg comes out at about 4e-6.
@@ -534,7 +535,6 @@ __global__ void __launch_bounds__(GRADS_NTH, 2) delta_chunk_grads_kernel(DeltaCh
       rt += q4 * x1[t] - k4 * y2[t];
       ru += k4 * y3[t];
     }
-    rt -= Bi * ru;
 #pragma unroll
     for (int r = 0; r < 4; ++r) rt[r] = sum16(rt[r]), ru[r] = sum16(ru[r]);
     if (c == 0) {
@@ -639,8 +639,10 @@ __global__ void __launch_bounds__(GRADS_NTH, 2) delta_chunk_grads_kernel(DeltaCh
       for (int i = 0; i < 8; ++i) dot0 += dots[i];
       const float u = rowU[0][lane] + rowU[1][lane];
       const float dG = rowT[0][lane] + rowT[1][lane] + rowM[0][lane] + rowM[1][lane] - col;
-      const float tail = exp_hw(Gs[63]) * dot0 + wave_sum(Bs[lane] * u);
-      const float sum = wave_incl_suffix(dG, lane) + tail;
+      // true one-sided sums: under strong gates a result is far smaller than the sum over the whole chunk
+      const float after = __shfl(wave_incl_scan(__shfl(dG, 63 - lane, 64), lane), 63 - lane, 64);
+      const float su = __shfl_up(Bs[lane] * u, 1, 64), before = wave_incl_scan(lane ? su : 0.0f, lane);
+      const float sum = after + before + exp_hw(Gs[63]) * dot0;
       if (lane < at.rows) {
         const i64 o = (at.tok0 + lane) * a.HV + hv;
         a.dg[o] = sum;

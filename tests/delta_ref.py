@@ -127,10 +127,11 @@ def reference(d, grads=True):
     return {n: torch.from_numpy(v) for n, v in out.items()}
 
 
-def check(got, ref, tols, where=""):
+def check(got, ref, tols, where="", floors={}):
     """got[n] against ref[n] for n in tols: the 2-norm as a whole, and every value within
     8 tol of the larger of itself and the root mean square (five standard deviations of the
-    operands' errors and one whole rounding of the largest values)."""
+    operands' errors and one whole rounding of the largest values).  floors[n] is an absolute
+    error that every value of n may have besides."""
     errs = {}
     for n, tol in tols.items():
         a, e = got[n].detach().double().cpu(), ref[n].double()
@@ -138,13 +139,14 @@ def check(got, ref, tols, where=""):
         if not e.numel():
             continue
         assert torch.isfinite(a).all(), (where, n)
+        err = ((a - e).abs() - floors.get(n, 0.0)).clamp(min=0.0)
         norm = max(float(e.norm()), float(ref["scale of " + n].norm()) if "scale of " + n in ref else 0.0)
         if norm == 0:
             assert float(a.abs().max()) == 0, (where, n)
             continue
         rms = norm / math.sqrt(e.numel())
-        rel = float((a - e).norm()) / norm
-        big = float(((a - e).abs() / e.abs().clamp(min=rms)).max())
+        rel = float(err.norm()) / norm
+        big = float((err / e.abs().clamp(min=rms)).max())
         errs[n] = (rel, big, tol)
     print(where, {n: f"{r:.1e}/{b:.1e}" for n, (r, b, _) in errs.items()}, flush=True)
     bad = {n: v for n, v in errs.items() if v[0] > v[2] or v[1] > 8 * v[2]}
