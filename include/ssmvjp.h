@@ -341,6 +341,10 @@ typedef struct {
  * Value head hv reads qk head hv / (HV/H).  bf16 runs the chunked form on the
  * matrix cores (states to about 1e-5 of their norm), float32 token by token.
  * g may be -infinity (a reset); the chunked form takes every g below -88 as -88.
+ * There the decay between two tokens is the exponential of a difference of sums
+ * of g over their chunk of 64 tokens, relatively off by up to 2^-24 of the larger
+ * sum's size (1e-5 after two resets, 6e-5 after twelve in one chunk).
+ * S_final may be S0.
  * Constraints: HV % H == 0 (SSMVJP_EINVAL otherwise); K % 16 == 0, K <= 128,
  * V % 16 == 0, V <= 65536, H*K and HV*V below 2^24 (SSMVJP_EUNSUPPORTED
  * otherwise).  q, k, v, o, S0, S_final 16-byte aligned. */
@@ -357,6 +361,7 @@ ssmvjp_status delta_chunk_fwd(const ssmvjp_delta_chunk_desc* desc,
  *   dbeta, dg [.., HV] f32, dS0 [batch, HV, K, V] f32 (NULL = not written).
  * dq, dk and dv are rounded to bf16, dbeta, dg and dS0 come out to about 1e-5
  * of their norm.  The gradient of a g below -88 is that at -88.
+ * dS0 may be dS_final or S0.
  * Constraints as for delta_chunk_fwd, and dtype SSMVJP_BF16 (SSMVJP_EUNSUPPORTED
  * otherwise: delta_rule_bwd has the float32 gradients, with g repeated over the
  * key channels and dg summed over them).  d_o, dq, dk, dv, dS_final and dS0 are
