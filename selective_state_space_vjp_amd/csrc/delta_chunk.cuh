@@ -44,7 +44,7 @@ struct DeltaChunkArgs {
   float *Sf, *dbeta, *dg, *dS0;
   // workspace, all per (slot, value head)
   bf16* Tf;   // [6][2][64][8] lower fragments of T - I, hi and lo
-  bf16* Pf;   // [6][64][8] lower fragments of scale P beta
+  bf16* Pf;   // [6][2][64][8] lower fragments of scale P beta
   float* G;   // [64]
   bf16* Tt;   // [6][2][64][8] fragments of T^T - I                  (backward from here on)
   bf16* Pt;   // [6][2][64][8] fragments of scale P^T

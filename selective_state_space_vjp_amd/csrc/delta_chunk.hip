@@ -187,8 +187,11 @@ __global__ void __launch_bounds__(256, 3) delta_prep_kernel(DeltaChunkArgs a) {
 #pragma unroll
       for (int s = 0; s < 2; ++s)
         if (s <= w >> 1) {
-          const Frag8 f = {pack4(p[2 * s]), pack4(p[2 * s + 1])};
-          *(u32x4*)(a.Pf + ((unit * 6 + frag_lo(w, s)) * 64 + lane) * 8) = as_u4(f);
+          Frag8 hi, lo;
+          split8(p[2 * s], p[2 * s + 1], hi, lo);
+          u32x4* f = (u32x4*)(a.Pf + ((unit * 6 + frag_lo(w, s)) * 2 * 64 + lane) * 8);
+          f[0] = as_u4(hi);
+          f[64] = as_u4(lo);
         }
     } else {
       auto pt_tile = [&](int b) {
@@ -266,7 +269,7 @@ __global__ void __launch_bounds__(256, 3) delta_prep_kernel(DeltaChunkArgs a) {
 template <int KP, int MODE>
 struct WalkLds {  // byte offsets
   static constexpr int K = 0, V = K + 64 * KP * 2, T = V + 4096, ABUF = T + 12 * 1024;  // for waves 0, 1
-  static constexpr int Q = 0, P = Q + 64 * KP * 2, BBUF = MODE ? 0 : P + 6 * 1024;      // for the followers
+  static constexpr int Q = 0, BBUF = MODE ? 0 : 64 * KP * 2;  // for the followers
   static constexpr int B = 2 * ABUF, S = B + 2 * BBUF, SBUF = MODE ? 0 : 2 * KP * 64, R = S + 2 * SBUF;  // [2 buffers][2 tiles]
   static constexpr int G = R + (MODE ? 0 : 2 * 2 * 4096), TOTAL = G + 3 * 512;  // gates: [3][e^G, e^{G_63 - G} beta]
 };
@@ -468,6 +471,14 @@ delta_chunk_walk_kernel(DeltaChunkArgs a) {
     }
   } else if (FWD && w < 4) {
     // ------------------------------------------------------------ the followers
+    // P comes straight from memory, a period ahead: both parts would not fit into LDS beside the rest
+    u32x4 pf[12];
+    auto fetch_p = [&](int ch) {
+      const u32x4* f = (const u32x4*)(a.Pf + (cell0 + ch * a.HV) * 6 * 2 * 512) + lane;
+#pragma unroll
+      for (int i = 0; i < 12; ++i) pf[i] = f[i * 64];
+    };
+    if (nch > 0) fetch_p(0);
     __syncthreads();
     for (int p = 0; p <= nch; ++p) {  // chunk p - 1 here, chunk p at the states
       if (act && p > 0) {
@@ -503,9 +514,6 @@ delta_chunk_walk_kernel(DeltaChunkArgs a) {
 #pragma unroll
         for (int s = 0; s < 2; ++s) split8(Ro[2 * s * 64], Ro[(2 * s + 1) * 64], rh[s], rl[s]);
         // O^T = scale e^G (Q S0)^T + r^T (scale P beta)^T
-        Frag8 pf[6];
-#pragma unroll
-        for (int i = 0; i < 6; ++i) pf[i] = as_frag(((const u32x4*)(buf + L::P))[i * 64 + lane]);
         float e[4];
 #pragma unroll
         for (int m = 0; m < 4; ++m) e[m] = a.scale * eG[16 * m + c];
@@ -515,10 +523,13 @@ delta_chunk_walk_kernel(DeltaChunkArgs a) {
 #pragma unroll
         for (int s = 0; s < 2; ++s) {
 #pragma unroll
-          for (int m = 2 * s; m < 4; ++m) y[m] = mma32(rl[s], pf[frag_lo(m, s)], y[m]);
+          for (int m = 2 * s; m < 4; ++m) y[m] = mma32(rl[s], as_frag(pf[2 * frag_lo(m, s)]), y[m]);
 #pragma unroll
-          for (int m = 2 * s; m < 4; ++m) y[m] = mma32(rh[s], pf[frag_lo(m, s)], y[m]);
+          for (int m = 2 * s; m < 4; ++m) y[m] = mma32(rh[s], as_frag(pf[2 * frag_lo(m, s) + 1]), y[m]);
+#pragma unroll
+          for (int m = 2 * s; m < 4; ++m) y[m] = mma32(rh[s], as_frag(pf[2 * frag_lo(m, s)]), y[m]);
         }
+        if (p < nch) fetch_p(p);
         const i64 row0 = (i64)ch * DCH + c;
         bf16* o = a.o + ((sp.start + row0) * a.HV + hv) * a.V + v0 + 4 * q;
 #pragma unroll
@@ -542,11 +553,10 @@ delta_chunk_walk_kernel(DeltaChunkArgs a) {
       cols_dma.issue(b + L::V, 0, row_words(a.v, tok0, rows_of(ch), a.HV, hv, a.V, slice * 32));
       flat_dma<12, 1>(b + L::T, 0, lane, rsrc_words_u(a.Tf + (cell0 + ch * a.HV) * 6 * 2 * 512, 12 * 1024));
     };
-    auto issue_b = [&](int ch) {  // q and P
+    auto issue_b = [&](int ch) {  // q
       const unsigned b = lds0 + (unsigned)(L::B + (ch & 1) * L::BBUF);
       const i64 tok0 = sp.start + (i64)ch * DCH;
       rows_dma.issue(b + L::Q, 0, row_words(a.q, tok0, rows_of(ch), a.H, h, a.K, 0));
-      flat_dma<6, 1>(b + L::P, 0, lane, rsrc_words_u(a.Pf + (cell0 + ch * a.HV) * 6 * 512, 6 * 1024));
     };
     float sG = 0.0f, sB = 0.0f;
     auto fetch_gates = [&](int ch) {
@@ -602,7 +612,7 @@ FwdPlan fwd_plan(i64 cells) {
     return o;
   };
   p.off_T = carve(cells * 6 * 2 * 64 * 8 * 2);
-  p.off_P = carve(cells * 6 * 64 * 8 * 2);
+  p.off_P = carve(cells * 6 * 2 * 64 * 8 * 2);
   p.off_G = carve(cells * 64 * 4);
   p.bytes = (size_t)off;
   return p;
