@@ -365,10 +365,10 @@ __device__ __forceinline__ void pstore(bf16* t, int pitch, int row, int col, con
 template <int KP>
 struct GradsLds {  // byte offsets
   static constexpr int KS = KP / 32, PK = KP + 20;
-  static constexpr int R = 0, MU = 8 * 1024, S = 16 * 1024, DS = S + 4 * KS * 1024, SLICE = DS + 4 * KS * 1024;
+  static constexpr int R = 0, MU = 8 * 1024, S = 16 * 1024, DS = S + 4 * KS * 1024, DO = DS + 4 * KS * 1024, SLICE = DO + 4096;
   static constexpr int PAIRS = 4 * 64 * P64 * 2;  // dD^T, E^T, two parts each
   static constexpr int BUF = SLICE > PAIRS ? SLICE : PAIRS;
-  static constexpr int K = 2 * BUF, Q = K + 64 * PK * 2, F = Q + 64 * PK * 2, TOTAL = F + 4 * (2 * 64 + 3 * 2 * 64 + 2 * 2 * 4 * 64 + 8);
+  static constexpr int K = 2 * BUF, Q = K + 64 * PK * 2, F = Q + 64 * PK * 2, TOTAL = F + 4 * (2 * 2 * 64 + 3 * 2 * 64 + 2 * 2 * 4 * 64 + 8);
 };
 
 template <int KP>
@@ -377,12 +377,11 @@ __global__ void __launch_bounds__(GRADS_NTH, 2) delta_chunk_grads_kernel(DeltaCh
   typedef GradsLds<KP> L;
   extern __shared__ __align__(16) unsigned char smem_raw[];
   bf16 *const Kb = (bf16*)(smem_raw + L::K), *const Qb = (bf16*)(smem_raw + L::Q);
-  float *const Gs = (float*)(smem_raw + L::F), *const Bs = Gs + 64;
+  float* const gates = (float*)(smem_raw + L::F);  // [2 heads][G, beta]
   // row terms of dG, su without beta, row sums of M (by half); column sums of M and of dbeta's pairs; <S0, dS> by wave
-  float(*const rowT)[64] = (float(*)[64])(Gs + 128), (*const rowU)[64] = rowT + 2, (*const rowM)[64] = rowT + 4;
-  float(*const colM)[4][64] = (float(*)[4][64])(Gs + 512), (*const colA)[4][64] = colM + 2;
-  float* const dots = Gs + 512 + 1024;
-  typedef unsigned u32x2 __attribute__((ext_vector_type(2)));
+  float(*const rowT)[64] = (float(*)[64])(gates + 256), (*const rowU)[64] = rowT + 2, (*const rowM)[64] = rowT + 4;
+  float(*const colM)[4][64] = (float(*)[4][64])(gates + 640), (*const colA)[4][64] = colM + 2;
+  float* const dots = gates + 640 + 1024;
   const int tid = threadIdx.x, lane = tid & 63, w = __builtin_amdgcn_readfirstlane(tid >> 6), c = lane & 15, q = lane >> 4;
   const int wr = w & 3, half = w >> 2;
   const unsigned H32 = (unsigned)a.H;
@@ -391,13 +390,18 @@ __global__ void __launch_bounds__(GRADS_NTH, 2) delta_chunk_grads_kernel(DeltaCh
   if (at.rows == 0) return;
   const int nsl = (int)(a.nvt + 1) / 2, nvt = (int)a.nvt;
   const unsigned lds0 = lds_base(smem_raw);
-  // slice sl of value head hv into buffer bf, in three parts (r and mu, S0, dS), tiles past V as zeros
+  const int orow = 16 * wr + (lane >> 2), ocol = (lane & 3) * 8;  // this lane's piece of d_o
+  const unsigned ooff = (unsigned)((orow * a.HV * a.V + ocol) * 2);
+  // slice sl of value head hv into buffer bf, in three parts (r, mu and d_o; S0; dS), tiles past V as zeros
   auto issue = [&](int part, i64 hv, int sl, int bf) {
     const i64 tile = (slot * a.HV + hv) * nvt + 2 * sl;
     const unsigned b = lds0 + (unsigned)(bf * L::BUF), left = nvt - 2 * sl > 1 ? 2u : 1u;
     if (part == 0) {
       flat_dma<8, 8>(b + L::R, w, lane, rsrc_words_u(a.rw + tile * 2048, left * 4096u));
       flat_dma<8, 8>(b + L::MU, w, lane, rsrc_words_u(a.muw + tile * 2048, left * 4096u));
+      if (half == 0)
+        dma_dwordx4(b + L::DO + 1024u * (unsigned)wr, sl * 32 + ocol < a.V ? ooff : BUF_OOB,
+                    row_words(a.d_o, at.tok0, at.rows, a.HV, hv, a.V, sl * 32));
     } else if (part == 1) {
       flat_dma<4 * KS, 8>(b + L::S, w, lane, rsrc_words_u(a.Sw + tile * KS * 1024, left * KS * 2048u));
     } else {
@@ -424,29 +428,36 @@ __global__ void __launch_bounds__(GRADS_NTH, 2) delta_chunk_grads_kernel(DeltaCh
       pstore(Qb, PK, p / (KP / 8), p % (KP / 8) * 8, tq[i]);
     }
   }
+  auto load_gates = [&](i64 hv, float& G, float& b) {
+    G = a.G[(slot * a.HV + hv) * 64 + lane];
+    b = lane < at.rows ? a.beta[(at.tok0 + lane) * a.HV + hv] : 0.0f;
+  };
+  if (w == 0) load_gates(h * a.rep, gates[lane], gates[64 + lane]);
+  __syncthreads();
+  f32x4 kq[4];  // q_i . k_j (half 0) or k_i . k_j, for every value head
+  {
+    Frag8 rf[KS];
+#pragma unroll
+    for (int s = 0; s < KS; ++s) rf[s] = prow(half ? Kb : Qb, PK, wr, s, lane);
+#pragma unroll
+    for (int b = 0; b < 4; ++b) {
+      kq[b] = zero4();
+      if (b <= wr) {
+#pragma unroll
+        for (int s = 0; s < KS; ++s) kq[b] = mma32(rf[s], prow(Kb, PK, b, s, lane), kq[b]);
+      }
+    }
+  }
   f32x4 dq[HT], dk[HT];  // rows i = 16 wr + 4 q + r, column 16 (HT half + t) + c
 #pragma unroll
   for (int t = 0; t < HT; ++t) dq[t] = zero4(), dk[t] = zero4();
 
   int bf = 0;  // the buffer of the slice at hand
   for (i64 rr = 0; rr < a.rep; ++rr) {
-    const i64 hv = h * a.rep + rr, cu = slot * a.HV + hv;
-    u32x2 po[2];
-    const brsrc ro = row_rsrc(a.d_o, at.tok0, at.rows, a.HV, hv, a.V);
-    auto fetch_o = [&](int sl) {
-#pragma unroll
-      for (int e = 0; e < 2; ++e) {
-        const int col = sl * 32 + 16 * e + 4 * q;
-        po[e] = __builtin_bit_cast(u32x2, __builtin_amdgcn_raw_buffer_load_b64(
-            ro, col < a.V ? (int)(((16 * wr + c) * a.HV * a.V + col) * 2) : (int)BUF_OOB, 0, 0));
-      }
-    };
-    fetch_o(0);
-    if (w == 0) {
-      const float G0 = a.G[cu * 64 + lane], b0 = lane < at.rows ? a.beta[(at.tok0 + lane) * a.HV + hv] : 0.0f;
-      Gs[lane] = G0;  // the previous head's readers of these are past the barrier behind its last sums
-      Bs[lane] = b0;
-    }
+    const i64 hv = h * a.rep + rr;
+    const float *const Gs = gates + (rr & 1) * 128, *const Bs = Gs + 64;
+    float G1 = 0.0f, b1 = 0.0f;  // the next head's
+    if (w == 0 && rr + 1 < a.rep) load_gates(hv + 1, G1, b1);
     f32x4 pp[4], x1[HT], y2[HT], y3[HT];  // pp: dO . r (half 0) or mu . r; dO S0^T, mu S0^T, r dS^T
 #pragma unroll
     for (int b = 0; b < 4; ++b) pp[b] = zero4();
@@ -454,7 +465,12 @@ __global__ void __launch_bounds__(GRADS_NTH, 2) delta_chunk_grads_kernel(DeltaCh
     for (int t = 0; t < HT; ++t) x1[t] = zero4(), y2[t] = zero4(), y3[t] = zero4();
     f32x4 dot = zero4();
     dma_wait();
-    __syncthreads();  // the first slice has landed; k and q are in LDS
+    __syncthreads();  // the first slice has landed
+    if (w == 0) {
+      float* const g = gates + ((rr + 1) & 1) * 128 + lane;  // the previous head's: its readers are past a barrier
+      g[0] = G1;
+      g[64] = b1;
+    }
     for (int sl = 0; sl < nsl; ++sl) {
       const bool last = sl + 1 == nsl;
       // the next slice's loads, spread over this one's products: all at once they block for 2,000 cycles
@@ -462,11 +478,11 @@ __global__ void __launch_bounds__(GRADS_NTH, 2) delta_chunk_grads_kernel(DeltaCh
       const i64 nhv = last ? hv + 1 : hv;
       const int nxt = last ? 0 : sl + 1;
       if (ahead) issue(0, nhv, nxt, bf ^ 1);
-      const Frag8 of = {__builtin_bit_cast(s16x4, po[0]), __builtin_bit_cast(s16x4, po[1])};
-      if (!last) fetch_o(sl + 1);
       const unsigned char* const buf = smem_raw + bf * L::BUF;
       const bf16 *R = (const bf16*)(buf + L::R), *MU = (const bf16*)(buf + L::MU), *S = (const bf16*)(buf + L::S),
                  *DS = (const bf16*)(buf + L::DS);
+      const s16x4* const orp = (const s16x4*)(buf + L::DO) + (16 * wr + c) * 8 + q;  // rows of 32 columns
+      const Frag8 of = {orp[0], orp[4]};
       // [tile][hi, lo]: 1024 values each of r and mu, 512 KS of the states
       const Frag8 mh = kept_rows(MU, MU + 2048, wr, lane), ml = kept_rows(MU + 1024, MU + 3072, wr, lane);
       const Frag8 rh = kept_rows(R, R + 2048, wr, lane), rl = kept_rows(R + 1024, R + 3072, wr, lane);
@@ -549,18 +565,6 @@ __global__ void __launch_bounds__(GRADS_NTH, 2) delta_chunk_grads_kernel(DeltaCh
     bf16* const pairs = (bf16*)(smem_raw + bf * L::BUF);  // dD hi, lo, E hi, lo
     bf16* const Pt = pairs + half * 2 * 64 * P64;         // [hi, lo][64][64], transposed: row j
     bf ^= 1;
-    Frag8 rf[KS];
-#pragma unroll
-    for (int s = 0; s < KS; ++s) rf[s] = prow(half ? Kb : Qb, PK, wr, s, lane);
-    f32x4 kq[4];  // q_i . k_j (half 0) or k_i . k_j
-#pragma unroll
-    for (int b = 0; b < 4; ++b) {
-      kq[b] = zero4();
-      if (b <= wr) {
-#pragma unroll
-        for (int s = 0; s < KS; ++s) kq[b] = mma32(rf[s], prow(Kb, PK, b, s, lane), kq[b]);
-      }
-    }
 #pragma unroll
     for (int b = 0; b < 4; ++b) {
       f32x4 x = zero4();
@@ -650,20 +654,26 @@ __global__ void __launch_bounds__(GRADS_NTH, 2) delta_chunk_grads_kernel(DeltaCh
       }
     }
   }
-  // out: row i, 16 columns at a time
+  // out, through LDS: 16-byte stores of whole rows in place of two bytes of sixteen columns
+  __syncthreads();  // the last pair terms' readers are done
+  constexpr int PO = KP + 8;
+  bf16 *const dqb = (bf16*)smem_raw, *const dkb = dqb + 64 * PO;
 #pragma unroll
-  for (int t = 0; t < HT; ++t) {
-    const int k0 = 16 * (HT * half + t);
-    if (k0 < a.K) {
+  for (int t = 0; t < HT; ++t)
 #pragma unroll
-      for (int r = 0; r < 4; ++r) {
-        const int i = 16 * wr + 4 * q + r;
-        if (i < at.rows) {
-          const i64 o = ((at.tok0 + i) * a.H + h) * a.K + k0 + c;
-          a.dq[o] = (bf16)dq[t][r];
-          a.dk[o] = (bf16)dk[t][r];
-        }
-      }
+    for (int r = 0; r < 4; ++r) {
+      const int o = (16 * wr + 4 * q + r) * PO + 16 * (HT * half + t) + c;
+      dqb[o] = (bf16)dq[t][r];
+      dkb[o] = (bf16)dk[t][r];
+    }
+  __syncthreads();
+#pragma unroll
+  for (int i = 0; i < 64 * KP / 8 / GRADS_NTH; ++i) {
+    const int p = tid + GRADS_NTH * i, row = p / (KP / 8), col = p % (KP / 8) * 8;
+    if (row < at.rows && col < a.K) {
+      const i64 o = ((at.tok0 + row) * a.H + h) * a.K + col;
+      *(u32x4*)(a.dq + o) = *(const u32x4*)(dqb + row * PO + col);
+      *(u32x4*)(a.dk + o) = *(const u32x4*)(dkb + row * PO + col);
     }
   }
 }
