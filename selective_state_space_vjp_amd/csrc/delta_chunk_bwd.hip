@@ -309,20 +309,21 @@ delta_chunk_rev_kernel(DeltaChunkArgs a) {
       g[64] = exp_hw(end - sG);
       g[128] = sB;
     };
+    // gates are fetched a period before they are prepared: a wait for them among the loads would be one for all
     if (nch > 0) {
       fetch_gates(nch - 1);
       issue_b(nch - 1);
       commit_gates(nch - 1);
+      if (nch > 1) fetch_gates(nch - 2);
     }
     dma_wait();
     __syncthreads();
     for (int p = nch; p >= 0; --p) {
-      if (p > 1) fetch_gates(p - 2);
+      if (p > 1) commit_gates(p - 2);
+      SSMVJP_FENCE();
+      if (p > 2) fetch_gates(p - 3);
       if (p > 0) issue_a(p - 1);
-      if (p > 1) {
-        issue_b(p - 2);
-        commit_gates(p - 2);
-      }
+      if (p > 1) issue_b(p - 2);
       dma_wait();
       __syncthreads();
     }
