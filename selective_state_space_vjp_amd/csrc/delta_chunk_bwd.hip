@@ -334,9 +334,9 @@ delta_chunk_rev_kernel(DeltaChunkArgs a) {
 // gradients of one chunk of one qk head
 // ---------------------------------------------------------------------------
 // Eight waves: wave (wr = w % 4, half = w / 4) owns row tile wr of every 64-row
-// result and one half of the key columns; of the pair terms, half 0 forms dD
-// and half 1 E.  The columns of V go by 32 (one contraction step): r, mu, S0 and
-// dS of the slice, both parts, come to LDS by LDS-direct loads, one slice ahead
+// result and one half of its columns (of the keys, or of the pairs' tokens j).
+// The columns of V go by 32 (one contraction step): r, mu, S0 and dS of the
+// slice, both parts, and d_o come to LDS by LDS-direct loads, one slice ahead
 // and over the border between two value heads (two buffers), and are read
 // transposed, the contraction running over v.  dD and E then take the place of
 // the last slice.
@@ -369,7 +369,7 @@ struct GradsLds {  // byte offsets
   static constexpr int R = 0, MU = 8 * 1024, S = 16 * 1024, DS = S + 4 * KS * 1024, DO = DS + 4 * KS * 1024, SLICE = DO + 4096;
   static constexpr int PAIRS = 4 * 64 * P64 * 2;  // dD^T, E^T, two parts each
   static constexpr int BUF = SLICE > PAIRS ? SLICE : PAIRS;
-  static constexpr int K = 2 * BUF, Q = K + 64 * PK * 2, F = Q + 64 * PK * 2, TOTAL = F + 4 * (2 * 2 * 64 + 3 * 2 * 64 + 2 * 2 * 4 * 64 + 8);
+  static constexpr int K = 2 * BUF, Q = K + 64 * PK * 2, F = Q + 64 * PK * 2, TOTAL = F + 4 * (2 * 2 * 64 + 3 * 2 * 64 + 2 * 4 * 64 + 8);
 };
 
 template <int KP>
@@ -379,10 +379,11 @@ __global__ void __launch_bounds__(GRADS_NTH, 2) delta_chunk_grads_kernel(DeltaCh
   extern __shared__ __align__(16) unsigned char smem_raw[];
   bf16 *const Kb = (bf16*)(smem_raw + L::K), *const Qb = (bf16*)(smem_raw + L::Q);
   float* const gates = (float*)(smem_raw + L::F);  // [2 heads][G, beta]
-  // row terms of dG, su without beta, row sums of M (by half); column sums of M and of dbeta's pairs; <S0, dS> by wave
+  // row terms of dG, su without beta, row sums of M (by half); column sums of M and of dbeta's pairs (by row tile);
+  // <S0, dS> by wave
   float(*const rowT)[64] = (float(*)[64])(gates + 256), (*const rowU)[64] = rowT + 2, (*const rowM)[64] = rowT + 4;
-  float(*const colM)[4][64] = (float(*)[4][64])(gates + 640), (*const colA)[4][64] = colM + 2;
-  float* const dots = gates + 640 + 1024;
+  float(*const colM)[64] = (float(*)[64])(gates + 640), (*const colA)[64] = colM + 4;
+  float* const dots = gates + 640 + 512;
   const int tid = threadIdx.x, lane = tid & 63, w = __builtin_amdgcn_readfirstlane(tid >> 6), c = lane & 15, q = lane >> 4;
   const int wr = w & 3, half = w >> 2;
   const unsigned H32 = (unsigned)a.H;
@@ -435,17 +436,21 @@ __global__ void __launch_bounds__(GRADS_NTH, 2) delta_chunk_grads_kernel(DeltaCh
   };
   if (w == 0) load_gates(h * a.rep, gates[lane], gates[64 + lane]);
   __syncthreads();
-  f32x4 kq[4];  // q_i . k_j (half 0) or k_i . k_j, for every value head
+  f32x4 qk[2], kk[2];  // q_i . k_j and k_i . k_j of column tiles 2 half and 2 half + 1, for every value head
   {
-    Frag8 rf[KS];
+    Frag8 fq[KS], fk[KS];
 #pragma unroll
-    for (int s = 0; s < KS; ++s) rf[s] = prow(half ? Kb : Qb, PK, wr, s, lane);
+    for (int s = 0; s < KS; ++s) fq[s] = prow(Qb, PK, wr, s, lane), fk[s] = prow(Kb, PK, wr, s, lane);
 #pragma unroll
-    for (int b = 0; b < 4; ++b) {
-      kq[b] = zero4();
-      if (b <= wr) {
+    for (int e = 0; e < 2; ++e) {
+      qk[e] = kk[e] = zero4();
+      if (2 * half + e <= wr) {
 #pragma unroll
-        for (int s = 0; s < KS; ++s) kq[b] = mma32(rf[s], prow(Kb, PK, b, s, lane), kq[b]);
+        for (int s = 0; s < KS; ++s) {
+          const Frag8 f = prow(Kb, PK, 2 * half + e, s, lane);
+          qk[e] = mma32(fq[s], f, qk[e]);
+          kk[e] = mma32(fk[s], f, kk[e]);
+        }
       }
     }
   }
@@ -459,9 +464,9 @@ __global__ void __launch_bounds__(GRADS_NTH, 2) delta_chunk_grads_kernel(DeltaCh
     const float *const Gs = gates + (rr & 1) * 128, *const Bs = Gs + 64;
     float G1 = 0.0f, b1 = 0.0f;  // the next head's
     if (w == 0 && rr + 1 < a.rep) load_gates(hv + 1, G1, b1);
-    f32x4 pp[4], x1[HT], y2[HT], y3[HT];  // pp: dO . r (half 0) or mu . r; dO S0^T, mu S0^T, r dS^T
+    f32x4 po[2], pm[2], x1[HT], y2[HT], y3[HT];  // dO . r, mu . r; dO S0^T, mu S0^T, r dS^T
 #pragma unroll
-    for (int b = 0; b < 4; ++b) pp[b] = zero4();
+    for (int e = 0; e < 2; ++e) po[e] = zero4(), pm[e] = zero4();
 #pragma unroll
     for (int t = 0; t < HT; ++t) x1[t] = zero4(), y2[t] = zero4(), y3[t] = zero4();
     f32x4 dot = zero4();
@@ -502,14 +507,15 @@ __global__ void __launch_bounds__(GRADS_NTH, 2) delta_chunk_grads_kernel(DeltaCh
         y3[t] = mma32(rh, dh, y3[t]);
       }
       if (ahead) issue(1, nhv, nxt, bf ^ 1);
-      // all four column tiles: what lies above the diagonal is dropped later, and straight code is read ahead
-      const Frag8 none = as_frag(zero_u4()), ph = half ? mh : of, pl = half ? ml : none;
+      // also where all of a tile lies above the diagonal and is dropped later: straight code is read ahead
 #pragma unroll
-      for (int b = 0; b < 4; ++b) {
-        const Frag8 bh = kept_rows(R, R + 2048, b, lane), bl = kept_rows(R + 1024, R + 3072, b, lane);
-        pp[b] = mma32(ph, bl, pp[b]);
-        pp[b] = mma32(pl, bh, pp[b]);
-        pp[b] = mma32(ph, bh, pp[b]);
+      for (int e = 0; e < 2; ++e) {
+        const Frag8 bh = kept_rows(R, R + 2048, 2 * half + e, lane), bl = kept_rows(R + 1024, R + 3072, 2 * half + e, lane);
+        po[e] = mma32(of, bl, po[e]);
+        pm[e] = mma32(mh, bl, pm[e]);
+        po[e] = mma32(of, bh, po[e]);
+        pm[e] = mma32(ml, bh, pm[e]);
+        pm[e] = mma32(mh, bh, pm[e]);
       }
       if (ahead) issue(2, nhv, nxt, bf ^ 1);
       if (w < 2 * KS) {  // this wave's 64 pieces of each array
@@ -561,44 +567,44 @@ __global__ void __launch_bounds__(GRADS_NTH, 2) delta_chunk_grads_kernel(DeltaCh
     const float dsum = wave_sum((dot[0] + dot[1]) + (dot[2] + dot[3]));
     if (lane == 0) dots[w] = dsum;
     __syncthreads();  // the last slice's readers are done
-    // pair terms: dD (half 0) or E (half 1); column j = 16 b + c
+    // pair terms; column j = 16 b + c
     f32x4 rm = zero4();
-    bf16* const pairs = (bf16*)(smem_raw + bf * L::BUF);  // dD hi, lo, E hi, lo
-    bf16* const Pt = pairs + half * 2 * 64 * P64;         // [hi, lo][64][64], transposed: row j
+    bf16* const pairs = (bf16*)(smem_raw + bf * L::BUF);  // dD hi, lo, E hi, lo: [64][64], transposed: row j
     bf ^= 1;
 #pragma unroll
-    for (int b = 0; b < 4; ++b) {
-      f32x4 x = zero4();
+    for (int e = 0; e < 2; ++e) {
+      f32x4 xd = zero4(), xe = zero4();
       float cm = 0.0f, ca = 0.0f;
-      const int j = 16 * b + c;
+      const int b = 2 * half + e, j = 16 * b + c;
       if (b <= wr) {
-        const float Gj = Gs[j], bj = Bs[j] * (half ? -1.0f : a.scale);
+        const float Gj = Gs[j], bj = Bs[j];
 #pragma unroll
         for (int r = 0; r < 4; ++r) {
           const int i = 16 * wr + 4 * q + r;
           const float gam = exp_hw(i >= j ? Gi[r] - Gj : 0.0f);
-          if (i > j || (half == 0 && i == j)) x[r] = bj * pp[b][r] * gam;
-          const float g = i >= j ? gam * kq[b][r] * pp[b][r] : 0.0f;
-          if (i > j) {
-            const float m = x[r] * kq[b][r];
-            rm[r] += m;
-            cm += m;
-            if (half) ca -= g;  // -a_ij N_ij of dbeta_j
-          }
-          if (!half) ca += a.scale * g;  // P_ij (dO_i . r_j)
+          const float d = i >= j ? a.scale * gam * po[e][r] : 0.0f, m = i > j ? gam * pm[e][r] : 0.0f;
+          xd[r] = bj * d;
+          xe[r] = -bj * m;
+          ca += d * qk[e][r] - m * kk[e][r];  // P_ij (dO_i . r_j) - a_ij N_ij
+          const float t = (i > j ? xd[r] * qk[e][r] : 0.0f) + xe[r] * kk[e][r];
+          rm[r] += t;
+          cm += t;
         }
       }
       cm = sum4q(cm);
       ca = sum4q(ca);
       if (q == 0) {
-        colM[half][wr][j] = cm;
-        colA[half][wr][j] = ca;
+        colM[wr][j] = cm;
+        colA[wr][j] = ca;
       }
+      bf16* const o = pairs + j * P64 + 16 * wr + 4 * q;
       s16x4 hi, lo;
-      split4(x, hi, lo);
-      const int o = j * P64 + 16 * wr + 4 * q;
-      *(s16x4*)(Pt + o) = hi;
-      *(s16x4*)(Pt + 64 * P64 + o) = lo;
+      split4(xd, hi, lo);
+      *(s16x4*)o = hi;
+      *(s16x4*)(o + 64 * P64) = lo;
+      split4(xe, hi, lo);
+      *(s16x4*)(o + 2 * 64 * P64) = hi;
+      *(s16x4*)(o + 3 * 64 * P64) = lo;
     }
 #pragma unroll
     for (int r = 0; r < 4; ++r) rm[r] = sum16(rm[r]);
@@ -639,7 +645,7 @@ __global__ void __launch_bounds__(GRADS_NTH, 2) delta_chunk_grads_kernel(DeltaCh
     if (w == 0) {
       float col = 0.0f, db = 0.0f, dot0 = 0.0f;
 #pragma unroll
-      for (int i = 0; i < 4; ++i) col += colM[0][i][lane] + colM[1][i][lane], db += colA[0][i][lane] + colA[1][i][lane];
+      for (int i = 0; i < 4; ++i) col += colM[i][lane], db += colA[i][lane];
 #pragma unroll
       for (int i = 0; i < 8; ++i) dot0 += dots[i];
       const float u = rowU[0][lane] + rowU[1][lane];
