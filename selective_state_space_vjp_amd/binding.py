@@ -133,9 +133,10 @@ def _stream(stream):
 
 
 def _dtype_code(t):
-    if t.dtype == torch.float32:
+    dtype = t.dtype
+    if dtype is torch.float32:
         return F32
-    if t.dtype == torch.bfloat16:
+    if dtype is torch.bfloat16:
         return BF16
     raise TypeError(f"unsupported dtype {t.dtype}; big tensors are float32 or bfloat16")
 
@@ -727,10 +728,11 @@ def delta_step(q, k, v, beta, g, state, *, scale, slots=None, out=None, workspac
     HV, V = v.shape[1], v.shape[2]
     dev, big, f32 = q.device, q.dtype, torch.float32
     per_key = g.dim() == 3
-    for name, t, dtype, shape in (("q", q, big, (b, H, K)), ("k", k, big, (b, H, K)), ("v", v, big, (b, HV, V)),
-                                  ("beta", beta, f32, (b, HV)), ("g", g, f32, (b, HV, K) if per_key else (b, HV)),
-                                  ("state", state, f32, (state.shape[0], HV, K, V)), ("slots", slots, torch.int32, (b,))):
-        if t is not None and not _fits(t, dtype, shape):
+    qs, hs, gs, ss = (b, H, K), (b, HV), ((b, HV, K) if per_key else (b, HV)), (state.shape[0], HV, K, V)
+    if not (_fits(q, big, qs) and _fits(k, big, qs) and _fits(v, big, (b, HV, V)) and _fits(beta, f32, hs)
+            and _fits(g, f32, gs) and _fits(state, f32, ss) and (slots is None or _fits(slots, torch.int32, (b,)))):
+        for name, t, dtype, shape in (("q", q, big, qs), ("k", k, big, qs), ("v", v, big, (b, HV, V)), ("beta", beta, f32, hs),
+                                      ("g", g, f32, gs), ("state", state, f32, ss), ("slots", slots, torch.int32, (b,))):
             _need(t, name, dtype, shape, dev)
     desc = DeltaStepDesc(b, state.shape[0], H, HV, K, V, float(scale), _dtype_code(q),
                          GATE_PER_KEY if per_key else GATE_PER_HEAD, 0)
@@ -749,22 +751,22 @@ def delta_step(q, k, v, beta, g, state, *, scale, slots=None, out=None, workspac
 # --------------------------------------------------------------------------- #
 def norm_desc(x, weight, eps):
     """x [..., D] with weight None or [D], or x [..., G, D] with weight [G, D]."""
-    if x.dim() < 1:
+    shape = x.shape
+    if len(shape) < 1:
         raise ValueError("x must have at least one axis")
-    D = x.shape[-1]
+    D = shape[-1]
     G = 1
-    if weight is not None and weight.dim() == 2:
-        if x.dim() < 2:
-            raise ValueError("a weight [G,D] needs x [...,G,D]")
-        G = x.shape[-2]
-    elif weight is not None and weight.dim() != 1:
-        raise ValueError("weight must be [D] or [G,D]")
-    rows = 1
-    for n in x.shape[:-1]:
-        rows *= n
+    if weight is not None:
+        wdim = weight.dim()
+        if wdim == 2:
+            if len(shape) < 2:
+                raise ValueError("a weight [G,D] needs x [...,G,D]")
+            G = shape[-2]
+        elif wdim != 1:
+            raise ValueError("weight must be [D] or [G,D]")
     if D == 0 or G == 0:
         raise ValueError("x has an empty last axis")
-    return NormDesc(rows // G, G, D, float(eps), _dtype_code(x))
+    return NormDesc(x.numel() // (G * D), G, D, eps, _dtype_code(x))
 
 
 def _norm_wshape(desc, weight):
@@ -779,7 +781,8 @@ def layer_norm_fwd(x, weight=None, bias=None, *, eps=1e-5, want_ckpt8=False, out
     x [..., D] float32 or bfloat16; weight and bias float32 [D], or [G,D] for x [..., G, D]
     (every head its own), or None.
     """
-    _required(x=x)
+    if x is None:
+        _required(x=x)
     if weight is None and bias is not None:
         raise ValueError("a bias needs a weight")
     desc = norm_desc(x, weight, eps)
@@ -791,18 +794,18 @@ def layer_norm_fwd(x, weight=None, bias=None, *, eps=1e-5, want_ckpt8=False, out
         for name, t in (("weight", weight), ("bias", bias)):
             if t is not None and not _fits(t, f32, ws):
                 _need(t, name, f32, ws, dev)
-    stat, blocks = x.shape[:-1], x.shape[:-1] + ((desc.dim + 63) // 64,)
+    stat = x.shape[:-1]
     with _scope(dev, stream):
         if out is None:
-            out = {"y": torch.empty_like(x), "mean": torch.empty(stat, dtype=f32, device=dev),
-                   "rstd": torch.empty(stat, dtype=f32, device=dev)}
+            mean = x.new_empty(stat, dtype=f32)
+            out = {"y": torch.empty_like(x), "mean": mean, "rstd": torch.empty_like(mean)}
             if want_ckpt8:
-                out["x8"] = torch.empty(x.shape, dtype=torch.int8, device=dev)
-                out["x8_scale"] = torch.empty(blocks, dtype=f32, device=dev)
+                out["x8"] = x.new_empty(x.shape, dtype=torch.int8)
+                out["x8_scale"] = x.new_empty(stat + ((desc.dim + 63) // 64,), dtype=f32)
         else:
             spec = {"y": (x.dtype, x.shape), "mean": (f32, stat), "rstd": (f32, stat)}
             if want_ckpt8:
-                spec.update(x8=(torch.int8, x.shape), x8_scale=(f32, blocks))
+                spec.update(x8=(torch.int8, x.shape), x8_scale=(f32, stat + ((desc.dim + 63) // 64,)))
             _check_out(out, spec, dev)
         x8, x8s = (out["x8"], out["x8_scale"]) if want_ckpt8 else (None, None)
         args = (x, weight, bias, out["y"], out["mean"], out["rstd"], x8, x8s)
@@ -818,7 +821,8 @@ def layer_norm_bwd(dy, x, mean, rstd, weight=None, *, ckpt8=None, out=None, work
     x is the forward's input, or None with ckpt8=(x8, x8_scale) from a forward with
     want_ckpt8=True; mean and rstd are the forward's.
     """
-    _required(dy=dy, mean=mean, rstd=rstd)
+    if dy is None or mean is None or rstd is None:
+        _required(dy=dy, mean=mean, rstd=rstd)
     if (x is None) == (ckpt8 is None):
         raise ValueError("exactly one of x and ckpt8 must be given")
     desc = norm_desc(dy, weight, 0.0)
@@ -828,11 +832,14 @@ def layer_norm_bwd(dy, x, mean, rstd, weight=None, *, ckpt8=None, out=None, work
     if ckpt8 is not None:
         _required(x8=x8, x8_scale=x8s)
     ws = None if weight is None else _norm_wshape(desc, weight)
-    for name, t, dtype, shape in (("dy", dy, dy.dtype, dy.shape), ("x", x, dy.dtype, dy.shape), ("mean", mean, f32, stat),
-                                  ("rstd", rstd, f32, stat), ("x8", x8, torch.int8, dy.shape),
-                                  ("x8_scale", x8s, f32, stat + ((desc.dim + 63) // 64,)), ("weight", weight, f32, ws)):
-        if t is not None and not _fits(t, dtype, shape):
-            _need(t, name, dtype, shape, dev)
+    shape, blocks = dy.shape, None if x8 is None else stat + ((desc.dim + 63) // 64,)
+    if not (_fits(dy, dy.dtype, shape) and _fits(mean, f32, stat) and _fits(rstd, f32, stat)
+            and (x is None or _fits(x, dy.dtype, shape)) and (weight is None or _fits(weight, f32, ws))
+            and (x8 is None or (_fits(x8, torch.int8, shape) and _fits(x8s, f32, blocks)))):
+        for name, t, dtype, want in (("dy", dy, dy.dtype, shape), ("x", x, dy.dtype, shape), ("mean", mean, f32, stat),
+                                     ("rstd", rstd, f32, stat), ("x8", x8, torch.int8, shape),
+                                     ("x8_scale", x8s, f32, blocks), ("weight", weight, f32, ws)):
+            _need(t, name, dtype, want, dev)
     with _scope(dev, stream):
         if out is None:
             out = {"dx": torch.empty_like(dy), "dweight": None if weight is None else torch.empty_like(weight),
