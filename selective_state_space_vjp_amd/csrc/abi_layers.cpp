@@ -25,7 +25,7 @@ ssmvjp_status delta_chunk_check(const ssmvjp_delta_chunk_desc* d) {
   // grids and workspace cells: 31-bit counts
   const double slots = d->packed ? (double)d->seqlen / 64 + (double)d->batch : (double)d->batch * ((double)d->seqlen / 64 + 1);
   if (!fits((double)d->batch) || !fits((double)d->seqlen) || !fits(slots * (double)d->nv_heads) ||
-      !fits(((double)d->batch * (double)d->nv_heads + 8) * ((double)d->dv / 32 + 1)))
+      !fits(2 * ((double)d->batch * (double)d->nv_heads + 8) * ((double)d->dv / 32 + 1)))
     return SSMVJP_EUNSUPPORTED;
   return SSMVJP_OK;
 }

@@ -37,7 +37,6 @@ namespace ssmvjp {
 struct DeltaChunkArgs {
   DeltaSeqs seq;
   i64 nslots, H, HV, K, V, rep, nvt;  // nvt: 16-column tiles of V
-  float scale;
   const bf16 *q, *k, *v, *d_o;
   const float *beta, *g, *S0, *dSf;
   bf16 *o, *dq, *dk, *dv;
@@ -54,6 +53,7 @@ struct DeltaChunkArgs {
   bf16* dSw;  // [2][KP/32][64][8] the state's gradient behind the chunk
   bf16* rw;   // [2][4][64][4] r
   bf16* muw;  // [2][4][64][4] mu
+  float scale;
 };
 
 typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
@@ -203,19 +203,16 @@ struct RowDma {
 // [64][16 NT] of v or d_o, the columns from v0 (zero past V)
 template <int NT, int NW>
 struct ColDma {
-  static constexpr int N = 2 * NT / NW;
-  unsigned off[N];
+  static constexpr int N = 2 * NT / NW, ROWS = 32 / NT;  // instructions a wave; rows an instruction
+  unsigned off, step;
   __device__ __forceinline__ void init(int w, int lane, i64 stride, i64 v0, i64 V) {
-#pragma unroll
-    for (int j = 0; j < N; ++j) {
-      const int p = 64 * (N * w + j) + lane, row = p / (2 * NT);
-      const i64 col = p % (2 * NT) * 8;
-      off[j] = v0 + col < V ? (unsigned)((row * stride + col) * 2) : BUF_OOB;
-    }
+    const int row = N * w * ROWS + lane / (2 * NT), col = lane % (2 * NT) * 8;
+    off = v0 + col < V ? (unsigned)((row * stride + col) * 2) : BUF_OOB;
+    step = (unsigned)(ROWS * stride * 2);
   }
   __device__ __forceinline__ void issue(unsigned lds, int w, u32x4 rs) const {
 #pragma unroll
-    for (int j = 0; j < N; ++j) dma_dwordx4(lds + 1024u * (unsigned)(N * w + j), off[j], rs);
+    for (int j = 0; j < N; ++j) dma_dwordx4(lds + 1024u * (unsigned)(N * w + j), off + (unsigned)j * step, rs);
   }
 };
 // N KB as they are
@@ -266,17 +263,17 @@ __device__ __forceinline__ ChunkAt chunk_at(const DeltaSeqs& q, i64 slot, int la
 
 // (sequence, value head, slice) of a walk's workgroup: ids go round the 8 XCDs,
 // and the slices of one head, which read the same q, k and fragments, share one
-// XCD's L2.  unit = sequence * HV + head; false: no work.
-__device__ __forceinline__ bool walk_unit(i64 units, i64 nslice, i64& unit, i64& slice) {
-  const unsigned x = blockIdx.x & 7, y = blockIdx.x >> 3, ns = (unsigned)nslice;
-  unit = y / ns * 8 + x;
-  slice = y % ns;
-  return unit < units;
+// XCD's L2.  unit = sequence * HV + head, past the last one: no work.
+struct WalkUnit {
+  i64 unit, slice;
+};
+__device__ __forceinline__ WalkUnit walk_unit(unsigned block, i64 nslice) {
+  const unsigned x = block & 7, y = block >> 3, ns = (unsigned)nslice;
+  return {(i64)(y / ns * 8 + x), (i64)(y % ns)};
 }
 inline i64 walk_blocks(i64 units, i64 nslice) { return (units + 7) / 8 * 8 * nslice; }
 
 DeltaChunkArgs delta_chunk_args(const ssmvjp_delta_chunk_desc& d, const int* off);
 hipError_t launch_delta_prep(const DeltaChunkArgs& a, bool backward, hipStream_t stream);
-hipError_t launch_delta_states(const DeltaChunkArgs& a, hipStream_t stream);
 
 }  // namespace ssmvjp

@@ -21,15 +21,14 @@
 // since both add the same float32 M_ij; that is why r, mu and the states enter
 // with both bf16 parts, and dg comes out at about 4e-6.
 //
-// Four launches: delta_prep_kernel (T, T^T, scale P^T of every chunk),
-// delta_chunk_walk_kernel<., 1> (the state before every chunk, r),
-// delta_chunk_rev_kernel (the reverse walk, 16 columns per wave as the forward:
-// mu and the state's gradient behind every chunk) and delta_chunk_grads_kernel
-// (all chunks at once: dv, dq, dk summed over the value heads of a qk head, dg,
-// dbeta).  The walks are bound by the chain from one state to the next, so that
-// everything that a chunk can do on its own is left to the last kernel; that one
-// is bound by reading what the walks kept.
-#include "delta_chunk.cuh"
+// delta_prep_kernel (T, T^T, scale P^T of every chunk), then the two walks:
+// delta_chunk_walk<., 1> (the state before every chunk, r) and delta_chunk_rev
+// (mu and the state's gradient behind every chunk, 16 columns per wave as the
+// forward), then delta_chunk_grads_kernel (all chunks at once: dv, dq, dk summed
+// over the value heads of a qk head, dg, dbeta).  The
+// walks are bound by the chain from one state to the next, so that everything
+// that a chunk can do on its own is left to the last kernel.
+#include "delta_walk.cuh"
 
 namespace ssmvjp {
 namespace {
@@ -50,15 +49,15 @@ struct RevLds {  // byte offsets
 constexpr int REV_NTH = 320;
 
 template <int KP>
-__global__ void __launch_bounds__(REV_NTH) __attribute__((amdgpu_waves_per_eu(2, 2)))
-delta_chunk_rev_kernel(DeltaChunkArgs a) {
+__device__ __forceinline__ void delta_chunk_rev(const DeltaChunkArgs& a, unsigned block) {
   constexpr int KS = KP / 32, KT = KP / 16;
   typedef RevLds<KP> L;
   extern __shared__ __align__(16) unsigned char smem_raw[];
   const int lane = threadIdx.x & 63, w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), c = lane & 15, q = lane >> 4;
   const int t16 = w & 1;
-  i64 unit, slice;
-  if (!walk_unit(a.seq.nseq * a.HV, (a.V + 31) / 32, unit, slice)) return;
+  const WalkUnit wu = walk_unit(block, (a.V + 31) / 32);
+  const i64 unit = wu.unit, slice = wu.slice;
+  if (unit >= a.seq.nseq * a.HV) return;
   const i64 n = unit / a.HV, hv = unit % a.HV, h = hv / a.rep;
   const DeltaSpan sp = a.seq.span(n);
   const int nch = (int)((sp.len + DCH - 1) / DCH);
@@ -328,6 +327,20 @@ delta_chunk_rev_kernel(DeltaChunkArgs a) {
       __syncthreads();
     }
   }
+}
+
+// The two walks need nothing of each other: with BOTH, blocks below `half` are
+// reverse walks (they take longer and go first), the others forward walks.
+template <int KP, bool BOTH>
+__global__ void __launch_bounds__(REV_NTH) __attribute__((amdgpu_waves_per_eu(2, 2)))
+delta_chunk_rev_kernel(DeltaChunkArgs a, unsigned half) {
+  if (!BOTH || blockIdx.x < half) delta_chunk_rev<KP>(a, blockIdx.x);
+  else if (threadIdx.x < walk_nth(1)) delta_chunk_walk<KP, 1>(a, blockIdx.x - half);  // two waves end here
+}
+template <int KP>
+__global__ void __launch_bounds__(walk_nth(1)) __attribute__((amdgpu_waves_per_eu(2, 2)))
+delta_chunk_states_kernel(DeltaChunkArgs a) {
+  delta_chunk_walk<KP, 1>(a, blockIdx.x);
 }
 
 // ---------------------------------------------------------------------------
@@ -686,9 +699,20 @@ __global__ void __launch_bounds__(GRADS_NTH, 2) delta_chunk_grads_kernel(DeltaCh
 }
 
 template <int KP>
-void launch_rev_grads(const DeltaChunkArgs& a, hipStream_t s) {
-  const i64 blocks = walk_blocks(a.seq.nseq * a.HV, (a.V + 31) / 32);
-  hipLaunchKernelGGL((delta_chunk_rev_kernel<KP>), dim3((unsigned)blocks), dim3(REV_NTH), (RevLds<KP>::TOTAL), s, a);
+void launch_walks_grads(const DeltaChunkArgs& a, hipStream_t s) {
+  static_assert(RevLds<KP>::TOTAL >= WalkLds<KP, 1>::TOTAL, "one launch for both walks");
+  const unsigned half = (unsigned)walk_blocks(a.seq.nseq * a.HV, (a.V + 31) / 32);
+  // A workgroup takes a CU, so that the walks run in rounds of 256 workgroups.  Where a walk's last round is not
+  // full, one launch of both lets the other fill it: 123 us against 177 us for the whole backward at 64 workgroups
+  // per walk (b=1 T=2048 HV=16, K = V = 128), 279 against 292 at 192, 267 against 285 at 384.  Full rounds gain
+  // nothing, and the walks' inputs push each other out of the caches: 686 against 675 us at 256 (b=2 T=4096 HV=32),
+  // 352 against 348 at 512 and 785 against 719 at 1024 (T=1024).
+  if (half % 256 != 0 && half < 512) {
+    hipLaunchKernelGGL((delta_chunk_rev_kernel<KP, true>), dim3(2 * half), dim3(REV_NTH), (RevLds<KP>::TOTAL), s, a, half);
+  } else {
+    hipLaunchKernelGGL((delta_chunk_states_kernel<KP>), dim3(half), dim3(walk_nth(1)), (WalkLds<KP, 1>::TOTAL), s, a);
+    hipLaunchKernelGGL((delta_chunk_rev_kernel<KP, false>), dim3(half), dim3(REV_NTH), (RevLds<KP>::TOTAL), s, a, half);
+  }
   if (a.nslots > 0)
     hipLaunchKernelGGL((delta_chunk_grads_kernel<KP>), dim3((unsigned)(a.nslots * a.H)), dim3(GRADS_NTH),
                        (GradsLds<KP>::TOTAL), s, a);
@@ -734,12 +758,11 @@ hipError_t launch_delta_chunk_bwd(const ssmvjp_delta_chunk_desc& d, const DeltaC
   a.Tf = b16(pl.off_T); a.Tt = b16(pl.off_Tt); a.Pt = b16(pl.off_Pt); a.G = (float*)(ws + pl.off_G);
   a.Sw = b16(pl.off_S); a.dSw = b16(pl.off_dS); a.rw = b16(pl.off_r); a.muw = b16(pl.off_mu);
   if (a.nslots > 0) {
-    hipError_t e = launch_delta_prep(a, true, stream);
-    if (e == hipSuccess) e = launch_delta_states(a, stream);
+    const hipError_t e = launch_delta_prep(a, true, stream);
     if (e != hipSuccess) return e;
   }
-  if (a.K <= 64) launch_rev_grads<64>(a, stream);
-  else launch_rev_grads<128>(a, stream);
+  if (a.K <= 64) launch_walks_grads<64>(a, stream);
+  else launch_walks_grads<128>(a, stream);
   return hipGetLastError();
 }
 
