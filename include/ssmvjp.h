@@ -339,7 +339,8 @@ typedef struct {
  *   S0 [batch, HV, K, V] f32 (NULL = zeros)   seq_offsets [batch + 1] int32 (packed; else NULL)
  * Outputs: o like v;  S_final [batch, HV, K, V] f32 (NULL = not written).
  * Value head hv reads qk head hv / (HV/H).  bf16 runs the chunked form on the
- * matrix cores (states to about 1e-5 of their norm), float32 token by token.
+ * matrix cores (states to about 1e-5 of their norm), float32 and calls of up to
+ * 16 tokens (seqlen) run token by token.
  * g may be -infinity (a reset); the chunked form takes every g below -88 as -88.
  * There the decay between two tokens is the exponential of a difference of sums
  * of g over their chunk of 64 tokens, relatively off by up to 2^-24 of the larger

@@ -286,8 +286,12 @@ hipError_t launch_delta_prep(const DeltaChunkArgs& a, bool backward, hipStream_t
   return hipGetLastError();
 }
 
-// Chunked MFMA kernels or the token walk.  float32 inputs take the walk.
-bool delta_fwd_walks(const ssmvjp_delta_chunk_desc& d) { return d.dtype == SSMVJP_F32; }
+// Chunked MFMA kernels or the token walk: float32 inputs take the walk (the chunked form's operands are bf16), and
+// so do up to 16 tokens, since a chunk costs the same whether it is full or not while the walk grows with its
+// tokens.  Chunked against walk at K = V = 128, HV = 32: 17 against 9 us for 8 tokens, 17 against 14 for 16, 18
+// against 25 for 32 (1 sequence); 40 against 24 for 16, 40 against 33 for 24, 40 against 42 for 32 (8); 115 against
+// 69 for 16, 117 against 122 for 32 (32).  At 24 tokens one sequence takes 18 against 20.
+bool delta_fwd_walks(const ssmvjp_delta_chunk_desc& d) { return d.dtype == SSMVJP_F32 || d.seqlen <= 16; }
 
 size_t delta_fwd_workspace_bytes(const ssmvjp_delta_chunk_desc& d) {
   return delta_fwd_walks(d) ? 0 : fwd_plan(delta_slots(d) * d.nv_heads).bytes;

@@ -1,6 +1,6 @@
 // delta_step.hip -- the gated delta rule token by token: one token per request
 // on a pool of states (serving), and whole sequences where the chunked kernels
-// do not apply (float32, few tokens).
+// do not apply or not pay (float32, up to 16 tokens).
 //
 //   S_dec = a_t S_{t-1} (a_t = exp(g_t): one per value head, or one per key
 //   channel);  r = v_t - k_t^T S_dec;  u = beta_t r;  S_t = S_dec + k_t (x) u
