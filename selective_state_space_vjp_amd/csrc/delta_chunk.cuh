@@ -115,10 +115,14 @@ __device__ __forceinline__ brsrc row_rsrc(const bf16* p, i64 tok0, int rows, i64
 
 // ---- row tiles in LDS ----
 // [64][KP] rows of q or k, no padding, columns past K zero.  The 16-byte unit u
-// of a row is stored at u ^ row_swz(row): eight consecutive rows of one unit
-// (a 16-byte fragment read) meet eight different units, four consecutive rows
-// of four units (a transposed read) all eight, twice each.
-__device__ __forceinline__ int row_swz(int row) { return ((row & 1) << 2) | ((row >> 1) & 3); }
+// of a row is stored at u ^ row_swz(KP, row).  LDS takes 16 lanes of 16 bytes or 32
+// of 8 at a time over 256 bytes (a row of KP = 128, two of KP = 64): the 16 rows
+// of one unit that a fragment read takes meet 16 different places; the 8 rows of
+// four half units that a transposed read takes fill every place twice, the least
+// that half units allow.
+__device__ __forceinline__ int row_swz(int KP, int row) {
+  return KP == 128 ? ((row & 3) << 2) | ((row >> 2) & 3) : ((row & 2) << 1) | ((row >> 2) & 3);
+}
 
 // Contraction over K.  A fragment of rows is 16 contiguous bytes: slot e of lane
 // group q <-> column 32s + 8q + e.  The state's tiles match it by their rows:
@@ -171,28 +175,28 @@ __device__ __forceinline__ f32x4 load_state4(brsrc rs, const DeltaChunkArgs& a, 
 // rows 16m .. 16m+15, contraction over the columns 32s .. 32s+31
 __device__ __forceinline__ Frag8 row_frag(const bf16* t, int KP, int m, int s, int lane) {
   const int row = 16 * m + (lane & 15);
-  return as_frag(*(const u32x4*)(t + row * KP + (((4 * s + (lane >> 4)) ^ row_swz(row)) << 3)));
+  return as_frag(*(const u32x4*)(t + row * KP + (((4 * s + (lane >> 4)) ^ row_swz(KP, row)) << 3)));
 }
 // the keys of state tile t as rows, contraction over the tokens 32s .. 32s+31 (slot order of the token fragments)
 __device__ __forceinline__ Frag8 key_frag(const bf16* x, int KP, int t, int s, int lane) {
   const int m = lane & 15, row = 32 * s + 4 * (lane >> 4) + (m >> 2), u = 4 * (t >> 1) + (m & 3);
-  return {lds_tr_b16(x + row * KP + ((u ^ row_swz(row)) << 3) + 4 * (t & 1)).v,
-          lds_tr_b16(x + (row + 16) * KP + ((u ^ row_swz(row + 16)) << 3) + 4 * (t & 1)).v};
+  return {lds_tr_b16(x + row * KP + ((u ^ row_swz(KP, row)) << 3) + 4 * (t & 1)).v,
+          lds_tr_b16(x + (row + 16) * KP + ((u ^ row_swz(KP, row + 16)) << 3) + 4 * (t & 1)).v};
 }
 // LDS-direct loads of one chunk's tiles, shared out over NW waves, 1 KB (64
-// pieces of 16 bytes) an instruction.  A wave's instructions are consecutive,
-// so that the swizzle depends on the lane and the instruction's parity only.
+// pieces of 16 bytes) an instruction.  A wave's instructions are consecutive; the
+// swizzle repeats every 16 rows, VAR instructions.
 template <int KP, int NW>
 struct RowDma {
-  static constexpr int N = KP / 8 / NW, VAR = KP == 128 ? 2 : 1;  // instructions a wave; rows 4 or 8 an instruction
+  static constexpr int N = KP / 8 / NW, VAR = KP == 128 ? 4 : 2;  // instructions a wave; rows 4 or 8 an instruction
   unsigned off[VAR], step;
   __device__ __forceinline__ void init(int w, int lane, i64 stride, i64 K) {
 #pragma unroll
     for (int j = 0; j < VAR; ++j) {
-      const int p = 64 * (N * w + j) + lane, row = p / (KP / 8), col = ((p % (KP / 8)) ^ row_swz(row)) * 8;
+      const int p = 64 * (N * w + j) + lane, row = p / (KP / 8), col = ((p % (KP / 8)) ^ row_swz(KP, row)) * 8;
       off[j] = col < K ? (unsigned)((row * stride + col) * 2) : BUF_OOB;
     }
-    step = (unsigned)(8 * stride * 2);
+    step = (unsigned)(16 * stride * 2);
   }
   __device__ __forceinline__ void issue(unsigned lds, int w, u32x4 rs) const {
 #pragma unroll
