@@ -9,6 +9,8 @@ namespace {
 constexpr int64_t DIM_MAX = 0x7fffffff;
 
 bool fits(double n) { return n <= (double)DIM_MAX; }
+// a launch has fewer than 2^32 threads
+bool launches(double groups, int threads) { return groups * threads < 4294967296.0; }
 
 ssmvjp_status delta_dims_check(int64_t H, int64_t HV, int64_t K, int64_t V, int32_t dtype) {
   if (H <= 0 || HV <= 0 || K <= 0 || V <= 0 || HV % H || !valid_dtype(dtype)) return SSMVJP_EINVAL;
@@ -25,7 +27,8 @@ ssmvjp_status delta_chunk_check(const ssmvjp_delta_chunk_desc* d) {
   // grids and workspace cells: 31-bit counts
   const double slots = d->packed ? (double)d->seqlen / 64 + (double)d->batch : (double)d->batch * ((double)d->seqlen / 64 + 1);
   if (!fits((double)d->batch) || !fits((double)d->seqlen) || !fits(slots * (double)d->nv_heads) ||
-      !fits(2 * ((double)d->batch * (double)d->nv_heads + 8) * ((double)d->dv / 32 + 1)))
+      !launches(slots * (double)d->nqk_heads, 512) ||
+      !launches(2 * ((double)d->batch * (double)d->nv_heads + 8) * ((double)d->dv / 32 + 1), 320))
     return SSMVJP_EUNSUPPORTED;
   return SSMVJP_OK;
 }
@@ -37,7 +40,7 @@ ssmvjp_status delta_step_check(const ssmvjp_delta_step_desc* d) {
   if (d->gate != SSMVJP_GATE_PER_HEAD && d->gate != SSMVJP_GATE_PER_KEY) return SSMVJP_EINVAL;
   const ssmvjp_status s = delta_dims_check(d->nqk_heads, d->nv_heads, d->dk, d->dv, d->dtype);
   if (s != SSMVJP_OK) return s;
-  if (!fits((double)d->batch * (double)d->nv_heads * ((double)d->dv / 64 + 1)) || !fits((double)d->nslots))
+  if (!launches((double)d->batch * (double)d->nv_heads * ((double)d->dv / 64 + 1), 256) || !fits((double)d->nslots))
     return SSMVJP_EUNSUPPORTED;
   return SSMVJP_OK;
 }
@@ -47,8 +50,8 @@ ssmvjp_status norm_check(const ssmvjp_norm_desc* d) {
   if (!(d->eps >= 0.0f)) return SSMVJP_EINVAL;  // also NaN
   const double parts = 4096.0 / (double)d->groups + 1, rows = (double)d->rows * (double)d->groups;
   if (rows * (double)d->dim * 4 > 9e18) return SSMVJP_EUNSUPPORTED;  // 64-bit byte offsets
-  if (!fits(rows) || !fits((double)d->groups * (double)d->dim / 16) ||
-      !fits(parts * (double)d->groups * ((double)d->dim / 256 + 1)))
+  if (!fits(rows) || !launches((double)d->groups * (double)d->dim / 16 + 1, 1024) ||
+      !launches(parts * (double)d->groups * ((double)d->dim / 256 + 1), 256))
     return SSMVJP_EUNSUPPORTED;
   return SSMVJP_OK;
 }

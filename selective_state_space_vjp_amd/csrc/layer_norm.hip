@@ -26,6 +26,8 @@
 // Rows that are too long for the registers, or whose length or pointers do not
 // allow 16-byte accesses at that length, are walked in passes over memory
 // (the second and third pass mostly hit L2).
+#include <algorithm>
+
 #include "common.cuh"
 #include "kernels.h"
 
@@ -229,48 +231,50 @@ __global__ void __launch_bounds__(256) norm_fwd_kernel(NormArgs a) {
   }
 }
 
-// forward, one row per workgroup in three passes over memory
+// forward, a row per workgroup at a time in three passes over memory
 template <typename T, int VEC, bool CK>
 __global__ void __launch_bounds__(256) norm_fwd_long_kernel(NormArgs a) {
   __shared__ float red[2][4];
-  const i64 r = blockIdx.x, g = r % a.G;
-  const T* x = (const T*)a.x + r * a.D;
-  T* y = (T*)a.out + r * a.D;
-  const float invD = 1.0f / (float)a.D;
-  const i64 nv = (a.D + VEC - 1) / VEC;
-  float s = 0.0f, v[VEC];
-  for (i64 i = threadIdx.x; i < nv; i += 256) {
-    load_vec<VEC>(x + i * VEC, v);
+  for (i64 r = blockIdx.x; r < a.rows * a.G; r += gridDim.x) {
+    const i64 g = r % a.G;
+    const T* x = (const T*)a.x + r * a.D;
+    T* y = (T*)a.out + r * a.D;
+    const float invD = 1.0f / (float)a.D;
+    const i64 nv = (a.D + VEC - 1) / VEC;
+    float s = 0.0f, v[VEC];
+    for (i64 i = threadIdx.x; i < nv; i += 256) {
+      load_vec<VEC>(x + i * VEC, v);
 #pragma unroll
-    for (int k = 0; k < VEC; ++k) s += v[k];
-  }
-  const float mean = row_sum<256>(s, red[0]) * invD;
-  float q = 0.0f;
-  for (i64 i = threadIdx.x; i < nv; i += 256) {
-    load_vec<VEC>(x + i * VEC, v);
-#pragma unroll
-    for (int k = 0; k < VEC; ++k) q += (v[k] - mean) * (v[k] - mean);
-  }
-  const float rstd = 1.0f / sqrtf(row_sum<256>(q, red[1]) * invD + a.eps);
-  const i64 nround = (nv + 255) / 256 * 256;  // whole waves: every lane of a block takes part in its maximum
-  for (i64 i = threadIdx.x; i < nround; i += 256) {
-    const bool live = i < nv;
-    if (live) load_vec<VEC>(x + i * VEC, v);
-    if constexpr (CK) store_codes<VEC>(a, r, i, v, live);
-    if (live) {
-      float w[VEC], b[VEC], o[VEC];
-#pragma unroll
-      for (int k = 0; k < VEC; ++k) w[k] = 1.0f, b[k] = 0.0f;
-      if (a.w) load_vec<VEC>(a.w + g * a.D + i * VEC, w);
-      if (a.b) load_vec<VEC>(a.b + g * a.D + i * VEC, b);
-#pragma unroll
-      for (int k = 0; k < VEC; ++k) o[k] = (v[k] - mean) * rstd * w[k] + b[k];
-      store_vec<VEC>(y + i * VEC, o);
+      for (int k = 0; k < VEC; ++k) s += v[k];
     }
-  }
-  if (threadIdx.x == 0) {
-    if (a.mean) a.mean[r] = mean;
-    if (a.rstd) a.rstd[r] = rstd;
+    const float mean = row_sum<256>(s, red[0]) * invD;
+    float q = 0.0f;
+    for (i64 i = threadIdx.x; i < nv; i += 256) {
+      load_vec<VEC>(x + i * VEC, v);
+#pragma unroll
+      for (int k = 0; k < VEC; ++k) q += (v[k] - mean) * (v[k] - mean);
+    }
+    const float rstd = 1.0f / sqrtf(row_sum<256>(q, red[1]) * invD + a.eps);
+    const i64 nround = (nv + 255) / 256 * 256;  // whole waves: every lane of a block takes part in its maximum
+    for (i64 i = threadIdx.x; i < nround; i += 256) {
+      const bool live = i < nv;
+      if (live) load_vec<VEC>(x + i * VEC, v);
+      if constexpr (CK) store_codes<VEC>(a, r, i, v, live);
+      if (live) {
+        float w[VEC], b[VEC], o[VEC];
+#pragma unroll
+        for (int k = 0; k < VEC; ++k) w[k] = 1.0f, b[k] = 0.0f;
+        if (a.w) load_vec<VEC>(a.w + g * a.D + i * VEC, w);
+        if (a.b) load_vec<VEC>(a.b + g * a.D + i * VEC, b);
+#pragma unroll
+        for (int k = 0; k < VEC; ++k) o[k] = (v[k] - mean) * rstd * w[k] + b[k];
+        store_vec<VEC>(y + i * VEC, o);
+      }
+    }
+    if (threadIdx.x == 0) {
+      if (a.mean) a.mean[r] = mean;
+      if (a.rstd) a.rstd[r] = rstd;
+    }
   }
 }
 
@@ -421,38 +425,40 @@ __global__ void __launch_bounds__(256) norm_bwd_kernel(NormArgs a) {
   }
 }
 
-// backward, one row per workgroup in two passes over memory (dx only)
+// backward, a row per workgroup at a time in two passes over memory (dx only)
 template <typename T, int VEC, bool CK>
 __global__ void __launch_bounds__(256) norm_bwd_long_kernel(NormArgs a) {
   __shared__ float red[2][4];
-  const i64 r = blockIdx.x, g = r % a.G;
-  const float invD = 1.0f / (float)a.D, mean = a.mean[r], rstd = a.rstd[r];
-  const i64 nv = (a.D + VEC - 1) / VEC;
-  const T* dyp = (const T*)a.dy + r * a.D;
-  const float* wp = a.w ? a.w + g * a.D : nullptr;
-  float h[VEC], dy[VEC], w[VEC], s1 = 0.0f, s2 = 0.0f;
+  for (i64 r = blockIdx.x; r < a.rows * a.G; r += gridDim.x) {
+    const i64 g = r % a.G;
+    const float invD = 1.0f / (float)a.D, mean = a.mean[r], rstd = a.rstd[r];
+    const i64 nv = (a.D + VEC - 1) / VEC;
+    const T* dyp = (const T*)a.dy + r * a.D;
+    const float* wp = a.w ? a.w + g * a.D : nullptr;
+    float h[VEC], dy[VEC], w[VEC], s1 = 0.0f, s2 = 0.0f;
 #pragma unroll
-  for (int k = 0; k < VEC; ++k) w[k] = 1.0f;
-  for (i64 i = threadIdx.x; i < nv; i += 256) {
-    load_x<T, VEC, CK>(a, r, i, h);
-    load_vec<VEC>(dyp + i * VEC, dy);
-    if (wp) load_vec<VEC>(wp + i * VEC, w);
+    for (int k = 0; k < VEC; ++k) w[k] = 1.0f;
+    for (i64 i = threadIdx.x; i < nv; i += 256) {
+      load_x<T, VEC, CK>(a, r, i, h);
+      load_vec<VEC>(dyp + i * VEC, dy);
+      if (wp) load_vec<VEC>(wp + i * VEC, w);
 #pragma unroll
-    for (int k = 0; k < VEC; ++k) {
-      s1 += dy[k] * w[k];
-      s2 += dy[k] * w[k] * ((h[k] - mean) * rstd);
+      for (int k = 0; k < VEC; ++k) {
+        s1 += dy[k] * w[k];
+        s2 += dy[k] * w[k] * ((h[k] - mean) * rstd);
+      }
     }
-  }
-  const float c1 = row_sum<256>(s1, red[0]) * invD, c2 = row_sum<256>(s2, red[1]) * invD;
-  T* dx = (T*)a.out + r * a.D;
-  for (i64 i = threadIdx.x; i < nv; i += 256) {
-    load_x<T, VEC, CK>(a, r, i, h);
-    load_vec<VEC>(dyp + i * VEC, dy);
-    if (wp) load_vec<VEC>(wp + i * VEC, w);
-    float o[VEC];
+    const float c1 = row_sum<256>(s1, red[0]) * invD, c2 = row_sum<256>(s2, red[1]) * invD;
+    T* dx = (T*)a.out + r * a.D;
+    for (i64 i = threadIdx.x; i < nv; i += 256) {
+      load_x<T, VEC, CK>(a, r, i, h);
+      load_vec<VEC>(dyp + i * VEC, dy);
+      if (wp) load_vec<VEC>(wp + i * VEC, w);
+      float o[VEC];
 #pragma unroll
-    for (int k = 0; k < VEC; ++k) o[k] = rstd * (dy[k] * w[k] - c1 - (h[k] - mean) * rstd * c2);
-    store_vec<VEC>(dx + i * VEC, o);
+      for (int k = 0; k < VEC; ++k) o[k] = rstd * (dy[k] * w[k] - c1 - (h[k] - mean) * rstd * c2);
+      store_vec<VEC>(dx + i * VEC, o);
+    }
   }
 }
 
@@ -534,6 +540,9 @@ int norm_tpr(i64 D, int vec, bool backward) {
   return 0;
 }
 
+// a launch has fewer than 2^32 threads
+unsigned long_grid(const NormArgs& a) { return (unsigned)std::min<i64>(a.rows * a.G, 1 << 20); }
+
 constexpr i64 FWD_GROUPS = 2048, BWD_GROUPS = 512;
 constexpr int BWD_ROWS = 2;  // a workgroup's partial dw, db cost as much as a row of dx each
 
@@ -559,7 +568,7 @@ void fwd_vec(const NormArgs& in, hipStream_t s) {
     else if (n <= 1024) hipLaunchKernelGGL((norm_fwd_kernel<T, VEC, 256, 4, CK>), grid, wg, 0, s, a);
     else hipLaunchKernelGGL((norm_fwd_kernel<T, VEC, 256, 8, CK>), grid, wg, 0, s, a);
   } else {
-    hipLaunchKernelGGL((norm_fwd_long_kernel<T, VEC, CK>), dim3((unsigned)(a.rows * a.G)), wg, 0, s, a);
+    hipLaunchKernelGGL((norm_fwd_long_kernel<T, VEC, CK>), dim3(long_grid(a)), wg, 0, s, a);
   }
 }
 
@@ -582,7 +591,7 @@ void bwd_vec(const NormArgs& in, hipStream_t s) {
     if (n <= 512) hipLaunchKernelGGL((norm_bwd_kernel<T, VEC, 256, 2, CK>), grid, wg, 0, s, a);
     else hipLaunchKernelGGL((norm_bwd_kernel<T, VEC, 256, 4, CK>), grid, wg, 0, s, a);
   } else {
-    hipLaunchKernelGGL((norm_bwd_long_kernel<T, VEC, CK>), dim3((unsigned)(a.rows * a.G)), wg, 0, s, a);
+    hipLaunchKernelGGL((norm_bwd_long_kernel<T, VEC, CK>), dim3(long_grid(a)), wg, 0, s, a);
     if (a.part) {
       const i64 cb = (a.D + 255) / 256;
       hipLaunchKernelGGL((norm_cols_kernel<T, CK>), dim3((unsigned)(cb * a.G * a.parts)), wg, 0, s, a, cb);

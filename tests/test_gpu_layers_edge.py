@@ -172,3 +172,23 @@ def test_strided_tensors_are_refused_not_copied():
     with pytest.raises(bd.SsmVjpError) as e:
         fwd(dict(t, v=flat.view(1, 20, 2, 32)))
     assert e.value.status == bd.EINVAL
+
+
+def test_more_long_rows_than_one_grid():
+    """Rows past the registers' length, more than 2^20 of them: the last rows as in a small call."""
+    announce("norm many long rows")
+    n = (1 << 20) + 3
+    gen = torch.Generator(DEV).manual_seed(2)
+    x = torch.randn(n, 2049, generator=gen, device=DEV, dtype=BF)
+    f = bd.layer_norm_fwd(x)
+    few = torch.cat([x[:2], x[-4:]])
+    want = bd.layer_norm_fwd(few)
+    for name in want:
+        assert torch.equal(torch.cat([f[name][:2], f[name][-4:]]), want[name]), name
+    x = x.view(-1)[:n * 1025].view(n, 1025)
+    st = bd.layer_norm_fwd(x)
+    dy = f["y"].view(-1)[:n * 1025].view(n, 1025)
+    b = bd.layer_norm_bwd(dy, x, st["mean"], st["rstd"])
+    pick = torch.tensor([0, 1, n - 4, n - 3, n - 2, n - 1], device=DEV)
+    want = bd.layer_norm_bwd(dy[pick], x[pick], st["mean"][pick], st["rstd"][pick])
+    assert torch.equal(b["dx"][pick], want["dx"])
