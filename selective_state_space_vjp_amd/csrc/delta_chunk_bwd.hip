@@ -39,7 +39,9 @@ namespace {
 // As the forward walk: waves 0 and 1 carry the gradients of 16 columns of the
 // state each, waves 2 and 3 work one chunk ahead on the part that does not
 // depend on them, B = Q^T (scale e^G dO), and hand it over through LDS, wave 4
-// loads and prepares the gates.
+// loads and prepares the gates.  195 us for b=2 T=4096 HV=32 K=V=128 (64 chunks
+// in a row, 393 MB stored), 150 of them without the stores of mu and dS; a second
+// loading wave made it 211, the gates waited for among the loads 225.
 template <int KP>
 struct RevLds {  // byte offsets
   static constexpr int K = 0, T = K + 64 * KP * 2, P = T + 12 * 1024, ABUF = P + 12 * 1024;    // [2] waves 0, 1
@@ -354,7 +356,11 @@ delta_chunk_states_kernel(DeltaChunkArgs a) {
 // transposed, the contraction running over v.  dD and E then take the place of
 // the last slice.
 //
-// Bound by what the walks kept: 208 KB of a chunk and head at K = V = 128.
+// A workgroup takes a CU, and what it waits for (its first slice, the barriers
+// between the steps of a head) nobody fills: b=2 T=4096 H=16 HV=32 K=V=128 takes
+// 298 us for 4096 chunks of a head, 208 KB each (2.9 TB/s; 60 us less if they came
+// from the L2), the matrix cores 39 % and the LDS 33 % busy.  Two workgroups per CU
+// would need half the registers (1024 threads spilled and were slower).
 constexpr int GRADS_NTH = 512;
 
 // Row pitches of the padded tiles: 40 bytes past a multiple of 128.  The 16 rows

@@ -15,6 +15,8 @@
 // column quad lane % 4) holds K/16 consecutive rows of four columns in
 // registers, the row sums are two DPP rotations and two permlane swaps, and
 // there is no LDS and no barrier.
+// 256 requests of HV=32 K=V=128: 221 us, 1.08 GB at 4.9 TB/s (a device copy moves
+// 5.2); one request: 4.4 us, a launch and one round trip to memory.
 //
 // Whole sequences: the same with the state kept in registers from the first
 // token to the last; the inputs of the next four tokens are in flight while
