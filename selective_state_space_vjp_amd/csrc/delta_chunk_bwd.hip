@@ -28,6 +28,8 @@
 // over the value heads of a qk head, dg, dbeta).  The
 // walks are bound by the chain from one state to the next, so that everything
 // that a chunk can do on its own is left to the last kernel.
+#include <algorithm>
+
 #include "delta_walk.cuh"
 
 namespace ssmvjp {
@@ -356,11 +358,13 @@ delta_chunk_states_kernel(DeltaChunkArgs a) {
 // transposed, the contraction running over v.  dD and E then take the place of
 // the last slice.
 //
-// A workgroup takes a CU, and what it waits for (its first slice, the barriers
-// between the steps of a head) nobody fills: b=2 T=4096 H=16 HV=32 K=V=128 takes
-// 298 us for 4096 chunks of a head, 208 KB each (2.9 TB/s; 60 us less if they came
-// from the L2), the matrix cores 39 % and the LDS 33 % busy.  Two workgroups per CU
-// would need half the registers (1024 threads spilled and were slower).
+// A workgroup takes a CU, and what it waits for (the barriers between the steps of
+// a head, loads) nobody fills, so that it goes from unit to unit with the next
+// one's first slice, k, q and gates on their way: b=2 T=4096 H=16 HV=32 K=V=128
+// takes 285 us for 4096 chunks of a head, 208 KB each (3.0 TB/s; a workgroup per
+// unit: 295; 60 us less if the blocks came from the L2), the matrix cores 40 % and
+// the LDS 33 % busy.  Two workgroups per CU would need half the registers (1024
+// threads spilled and were slower).
 constexpr int GRADS_NTH = 512;
 
 // Row pitches of the padded tiles: 40 bytes past a multiple of 128.  The 16 rows
@@ -406,15 +410,25 @@ __global__ void __launch_bounds__(GRADS_NTH, 2) delta_chunk_grads_kernel(DeltaCh
   const int tid = threadIdx.x, lane = tid & 63, w = __builtin_amdgcn_readfirstlane(tid >> 6), c = lane & 15, q = lane >> 4;
   const int wr = w & 3, half = w >> 2;
   const unsigned H32 = (unsigned)a.H;
-  const i64 h = blockIdx.x % H32, slot = blockIdx.x / H32;
-  const ChunkAt at = chunk_at(a.seq, slot, lane);
-  if (at.rows == 0) return;
+  // the workgroup's units (slot, qk head): from one to the next that has tokens
+  const unsigned units = (unsigned)(a.nslots * a.H);
+  unsigned un = blockIdx.x;
+  i64 tok0 = 0;
+  int rows = 0;
+  for (; un < units; un += gridDim.x) {
+    const ChunkAt x = chunk_at(a.seq, un / H32, lane);
+    tok0 = x.tok0;
+    rows = x.rows;
+    if (rows) break;
+  }
+  if (un >= units) return;
+  i64 h = un % H32, slot = un / H32;
   const int nsl = (int)(a.nvt + 1) / 2, nvt = (int)a.nvt;
   const unsigned lds0 = lds_base(smem_raw);
   const int orow = 16 * wr + (lane >> 2), ocol = (lane & 3) * 8;  // this lane's piece of d_o
   const unsigned ooff = (unsigned)((orow * a.HV * a.V + ocol) * 2);
   // slice sl of value head hv into buffer bf, in three parts (r, mu and d_o; S0; dS), tiles past V as zeros
-  auto issue = [&](int part, i64 hv, int sl, int bf) {
+  auto issue = [&](int part, i64 tok0, int rows, i64 slot, i64 hv, int sl, int bf) {
     const i64 tile = (slot * a.HV + hv) * nvt + 2 * sl;
     const unsigned b = lds0 + (unsigned)(bf * L::BUF), left = nvt - 2 * sl > 1 ? 2u : 1u;
     if (part == 0) {
@@ -422,7 +436,7 @@ __global__ void __launch_bounds__(GRADS_NTH, 2) delta_chunk_grads_kernel(DeltaCh
       flat_dma<8, 8>(b + L::MU, w, lane, rsrc_words_u(a.muw + tile * 2048, left * 4096u));
       if (half == 0)
         dma_dwordx4(b + L::DO + 1024u * (unsigned)wr, sl * 32 + ocol < a.V ? ooff : BUF_OOB,
-                    row_words(a.d_o, at.tok0, at.rows, a.HV, hv, a.V, sl * 32));
+                    row_words(a.d_o, tok0, rows, a.HV, hv, a.V, sl * 32));
     } else if (part == 1) {
       flat_dma<4 * KS, 8>(b + L::S, w, lane, rsrc_words_u(a.Sw + tile * KS * 1024, left * KS * 2048u));
     } else {
@@ -430,11 +444,21 @@ __global__ void __launch_bounds__(GRADS_NTH, 2) delta_chunk_grads_kernel(DeltaCh
     }
   };
 #pragma unroll
-  for (int i = 0; i < 3; ++i) issue(i, h * a.rep, 0, 0);
-  {
-    constexpr int N = 64 * KP / 8 / GRADS_NTH;
-    const brsrc rk = row_rsrc(a.k, at.tok0, at.rows, a.H, h, a.K), rq = row_rsrc(a.q, at.tok0, at.rows, a.H, h, a.K);
-    u32x4 tk[N], tq[N];
+  for (int i = 0; i < 3; ++i) issue(i, tok0, rows, slot, h * a.rep, 0, 0);
+  int bf = 0;  // the buffer of the slice at hand
+  // k and q of a unit, a value head's gates: loaded ahead
+  constexpr int N = 64 * KP / 8 / GRADS_NTH;
+  u32x4 tk[N], tq[N];
+  float G1 = 0.0f, b1 = 0.0f;
+  // the thread's number, anew: addresses made from it are not kept in registers from unit to unit
+  auto thread = [&] {
+    int t = tid;
+    asm volatile("" : "+v"(t));
+    return t;
+  };
+  auto load_kq = [&](i64 tok0, int rows, i64 h) {
+    const int tid = thread();
+    const brsrc rk = row_rsrc(a.k, tok0, rows, a.H, h, a.K), rq = row_rsrc(a.q, tok0, rows, a.H, h, a.K);
 #pragma unroll
     for (int i = 0; i < N; ++i) {
       const int p = tid + GRADS_NTH * i, row = p / (KP / 8), col = p % (KP / 8) * 8;
@@ -442,265 +466,294 @@ __global__ void __launch_bounds__(GRADS_NTH, 2) delta_chunk_grads_kernel(DeltaCh
       tk[i] = bload16(rk, o);
       tq[i] = bload16(rq, o);
     }
+  };
+  auto load_gates = [&](i64 tok0, int rows, i64 slot, i64 hv) {
+    G1 = a.G[(slot * a.HV + hv) * 64 + lane];
+    b1 = lane < rows ? a.beta[(tok0 + lane) * a.HV + hv] : 0.0f;
+  };
+  load_kq(tok0, rows, h);
+  if (w == 0) load_gates(tok0, rows, slot, h * a.rep);
+  for (;;) {
+    un += gridDim.x;
+    i64 ntok0 = 0;  // the next unit
+    int nrows = 0;
+    for (; un < units; un += gridDim.x) {
+      const ChunkAt x = chunk_at(a.seq, un / H32, lane);
+      ntok0 = x.tok0;
+      nrows = x.rows;
+      if (nrows) break;
+    }
+    const i64 nslot = un / H32, nh = un % H32;
+    const bool next = un < units;
+    const int tn = thread();
 #pragma unroll
     for (int i = 0; i < N; ++i) {
-      const int p = tid + GRADS_NTH * i;
+      const int p = tn + GRADS_NTH * i;
       pstore(Kb, PK, p / (KP / 8), p % (KP / 8) * 8, tk[i]);
       pstore(Qb, PK, p / (KP / 8), p % (KP / 8) * 8, tq[i]);
     }
-  }
-  auto load_gates = [&](i64 hv, float& G, float& b) {
-    G = a.G[(slot * a.HV + hv) * 64 + lane];
-    b = lane < at.rows ? a.beta[(at.tok0 + lane) * a.HV + hv] : 0.0f;
-  };
-  if (w == 0) load_gates(h * a.rep, gates[lane], gates[64 + lane]);
-  __syncthreads();
-  f32x4 qk[2], kk[2];  // q_i . k_j and k_i . k_j of column tiles 2 half and 2 half + 1, for every value head
-  {
-    Frag8 fq[KS], fk[KS];
+    if (w == 0) {
+      gates[lane] = G1;
+      gates[64 + lane] = b1;
+    }
+    __syncthreads();
+    f32x4 qk[2], kk[2];  // q_i . k_j and k_i . k_j of column tiles 2 half and 2 half + 1, for every value head
+    {
+      Frag8 fq[KS], fk[KS];
 #pragma unroll
-    for (int s = 0; s < KS; ++s) fq[s] = prow(Qb, PK, wr, s, lane), fk[s] = prow(Kb, PK, wr, s, lane);
+      for (int s = 0; s < KS; ++s) fq[s] = prow(Qb, PK, wr, s, lane), fk[s] = prow(Kb, PK, wr, s, lane);
 #pragma unroll
-    for (int e = 0; e < 2; ++e) {
-      qk[e] = kk[e] = zero4();
-      if (2 * half + e <= wr) {
+      for (int e = 0; e < 2; ++e) {
+        qk[e] = kk[e] = zero4();
+        if (2 * half + e <= wr) {
 #pragma unroll
-        for (int s = 0; s < KS; ++s) {
-          const Frag8 f = prow(Kb, PK, 2 * half + e, s, lane);
-          qk[e] = mma32(fq[s], f, qk[e]);
-          kk[e] = mma32(fk[s], f, kk[e]);
+          for (int s = 0; s < KS; ++s) {
+            const Frag8 f = prow(Kb, PK, 2 * half + e, s, lane);
+            qk[e] = mma32(fq[s], f, qk[e]);
+            kk[e] = mma32(fk[s], f, kk[e]);
+          }
         }
       }
     }
-  }
-  f32x4 dq[HT], dk[HT];  // rows i = 16 wr + 4 q + r, column 16 (HT half + t) + c
+    f32x4 dq[HT], dk[HT];  // rows i = 16 wr + 4 q + r, column 16 (HT half + t) + c
 #pragma unroll
-  for (int t = 0; t < HT; ++t) dq[t] = zero4(), dk[t] = zero4();
+    for (int t = 0; t < HT; ++t) dq[t] = zero4(), dk[t] = zero4();
 
-  int bf = 0;  // the buffer of the slice at hand
-  for (i64 rr = 0; rr < a.rep; ++rr) {
-    const i64 hv = h * a.rep + rr;
-    const float *const Gs = gates + (rr & 1) * 128, *const Bs = Gs + 64;
-    float G1 = 0.0f, b1 = 0.0f;  // the next head's
-    if (w == 0 && rr + 1 < a.rep) load_gates(hv + 1, G1, b1);
-    f32x4 po[2], pm[2], x1[HT], y2[HT], y3[HT];  // dO . r, mu . r; dO S0^T, mu S0^T, r dS^T
+    for (i64 rr = 0; rr < a.rep; ++rr) {
+      const i64 hv = h * a.rep + rr;
+      const float *const Gs = gates + (rr & 1) * 128, *const Bs = Gs + 64;
+      if (w == 0 && rr + 1 < a.rep) load_gates(tok0, rows, slot, hv + 1);
+      f32x4 po[2], pm[2], x1[HT], y2[HT], y3[HT];  // dO . r, mu . r; dO S0^T, mu S0^T, r dS^T
 #pragma unroll
-    for (int e = 0; e < 2; ++e) po[e] = zero4(), pm[e] = zero4();
+      for (int e = 0; e < 2; ++e) po[e] = zero4(), pm[e] = zero4();
 #pragma unroll
-    for (int t = 0; t < HT; ++t) x1[t] = zero4(), y2[t] = zero4(), y3[t] = zero4();
-    f32x4 dot = zero4();
-    dma_wait();
-    __syncthreads();  // the first slice has landed
-    if (w == 0) {
-      float* const g = gates + ((rr + 1) & 1) * 128 + lane;  // the previous head's: its readers are past a barrier
-      g[0] = G1;
-      g[64] = b1;
-    }
-    for (int sl = 0; sl < nsl; ++sl) {
-      const bool last = sl + 1 == nsl;
-      // the next slice's loads, spread over this one's products: all at once they block for 2,000 cycles
-      const bool ahead = !last || rr + 1 < a.rep;
-      const i64 nhv = last ? hv + 1 : hv;
-      const int nxt = last ? 0 : sl + 1;
-      if (ahead) issue(0, nhv, nxt, bf ^ 1);
-      const unsigned char* const buf = smem_raw + bf * L::BUF;
-      const bf16 *R = (const bf16*)(buf + L::R), *MU = (const bf16*)(buf + L::MU), *S = (const bf16*)(buf + L::S),
-                 *DS = (const bf16*)(buf + L::DS);
-      const s16x4* const orp = (const s16x4*)(buf + L::DO) + (16 * wr + c) * 8 + q;  // rows of 32 columns
-      const Frag8 of = {orp[0], orp[4]};
-      // [tile][hi, lo]: 1024 values each of r and mu, 512 KS of the states
-      const Frag8 mh = kept_rows(MU, MU + 2048, wr, lane), ml = kept_rows(MU + 1024, MU + 3072, wr, lane);
-      const Frag8 rh = kept_rows(R, R + 2048, wr, lane), rl = kept_rows(R + 1024, R + 3072, wr, lane);
-#pragma unroll
-      for (int t = 0; t < HT; ++t) {
-        const int k = HT * half + t;
-        const Frag8 sh = kept_keys(S, S + 1024 * KS, k, lane), sl2 = kept_keys(S + 512 * KS, S + 1536 * KS, k, lane);
-        const Frag8 dh = kept_keys(DS, DS + 1024 * KS, k, lane), dl = kept_keys(DS + 512 * KS, DS + 1536 * KS, k, lane);
-        x1[t] = mma32(of, sl2, x1[t]);
-        y2[t] = mma32(ml, sh, y2[t]);
-        y3[t] = mma32(rl, dh, y3[t]);
-        y2[t] = mma32(mh, sl2, y2[t]);
-        y3[t] = mma32(rh, dl, y3[t]);
-        x1[t] = mma32(of, sh, x1[t]);
-        y2[t] = mma32(mh, sh, y2[t]);
-        y3[t] = mma32(rh, dh, y3[t]);
+      for (int t = 0; t < HT; ++t) x1[t] = zero4(), y2[t] = zero4(), y3[t] = zero4();
+      f32x4 dot = zero4();
+      dma_wait();
+      __syncthreads();  // the first slice has landed
+      if (w == 0) {
+        float* const g = gates + ((rr + 1) & 1) * 128 + lane;  // the previous head's: its readers are past a barrier
+        g[0] = G1;
+        g[64] = b1;
       }
-      if (ahead) issue(1, nhv, nxt, bf ^ 1);
-      // also where all of a tile lies above the diagonal and is dropped later: straight code is read ahead
+      for (int sl = 0; sl < nsl; ++sl) {
+        const bool last = sl + 1 == nsl;
+        // the next slice's loads, spread over this one's products: all at once they block for 2,000 cycles
+        const bool over = last && rr + 1 == a.rep, ahead = !over || next;
+        const i64 nhv = over ? nh * a.rep : last ? hv + 1 : hv, nsl2 = over ? nslot : slot;
+        const i64 tok2 = over ? ntok0 : tok0;
+        const int rows2 = over ? nrows : rows;
+        const int nxt = last ? 0 : sl + 1;
+        if (ahead) issue(0, tok2, rows2, nsl2, nhv, nxt, bf ^ 1);
+        const unsigned char* const buf = smem_raw + bf * L::BUF;
+        const bf16 *R = (const bf16*)(buf + L::R), *MU = (const bf16*)(buf + L::MU), *S = (const bf16*)(buf + L::S),
+                   *DS = (const bf16*)(buf + L::DS);
+        const s16x4* const orp = (const s16x4*)(buf + L::DO) + (16 * wr + c) * 8 + q;  // rows of 32 columns
+        const Frag8 of = {orp[0], orp[4]};
+        // [tile][hi, lo]: 1024 values each of r and mu, 512 KS of the states
+        const Frag8 mh = kept_rows(MU, MU + 2048, wr, lane), ml = kept_rows(MU + 1024, MU + 3072, wr, lane);
+        const Frag8 rh = kept_rows(R, R + 2048, wr, lane), rl = kept_rows(R + 1024, R + 3072, wr, lane);
 #pragma unroll
-      for (int e = 0; e < 2; ++e) {
-        const Frag8 bh = kept_rows(R, R + 2048, 2 * half + e, lane), bl = kept_rows(R + 1024, R + 3072, 2 * half + e, lane);
-        po[e] = mma32(of, bl, po[e]);
-        pm[e] = mma32(mh, bl, pm[e]);
-        po[e] = mma32(of, bh, po[e]);
-        pm[e] = mma32(ml, bh, pm[e]);
-        pm[e] = mma32(mh, bh, pm[e]);
-      }
-      if (ahead) issue(2, nhv, nxt, bf ^ 1);
-      if (w < 2 * KS) {  // this wave's 64 pieces of each array
-        const int o = (w / KS) * 1024 * KS + (w % KS) * 512 + lane * 8;
-        const Frag8 s0 = as_frag(*(const u32x4*)(S + o)), s1 = as_frag(*(const u32x4*)(S + o + 512 * KS));
-        const Frag8 d0 = as_frag(*(const u32x4*)(DS + o)), d1 = as_frag(*(const u32x4*)(DS + o + 512 * KS));
-        dot += (unpack4(s0.a) + unpack4(s1.a)) * (unpack4(d0.a) + unpack4(d1.a));
-        dot += (unpack4(s0.b) + unpack4(s1.b)) * (unpack4(d0.b) + unpack4(d1.b));
-      }
-      // dv = mu, rounded: its hi part
-      if (half == 1) {
+        for (int t = 0; t < HT; ++t) {
+          const int k = HT * half + t;
+          const Frag8 sh = kept_keys(S, S + 1024 * KS, k, lane), sl2 = kept_keys(S + 512 * KS, S + 1536 * KS, k, lane);
+          const Frag8 dh = kept_keys(DS, DS + 1024 * KS, k, lane), dl = kept_keys(DS + 512 * KS, DS + 1536 * KS, k, lane);
+          x1[t] = mma32(of, sl2, x1[t]);
+          y2[t] = mma32(ml, sh, y2[t]);
+          y3[t] = mma32(rl, dh, y3[t]);
+          y2[t] = mma32(mh, sl2, y2[t]);
+          y3[t] = mma32(rh, dl, y3[t]);
+          x1[t] = mma32(of, sh, x1[t]);
+          y2[t] = mma32(mh, sh, y2[t]);
+          y3[t] = mma32(rh, dh, y3[t]);
+        }
+        if (ahead) issue(1, tok2, rows2, nsl2, nhv, nxt, bf ^ 1);
+        // also where all of a tile lies above the diagonal and is dropped later: straight code is read ahead
 #pragma unroll
         for (int e = 0; e < 2; ++e) {
-          const int col = sl * 32 + 16 * e + 4 * q;
-          if (16 * wr + c < at.rows && col < a.V)
-            *(s16x4*)(a.dv + ((at.tok0 + 16 * wr + c) * a.HV + hv) * a.V + col) = e ? mh.b : mh.a;
+          const Frag8 bh = kept_rows(R, R + 2048, 2 * half + e, lane), bl = kept_rows(R + 1024, R + 3072, 2 * half + e, lane);
+          po[e] = mma32(of, bl, po[e]);
+          pm[e] = mma32(mh, bl, pm[e]);
+          po[e] = mma32(of, bh, po[e]);
+          pm[e] = mma32(ml, bh, pm[e]);
+          pm[e] = mma32(mh, bh, pm[e]);
+        }
+        if (ahead) issue(2, tok2, rows2, nsl2, nhv, nxt, bf ^ 1);
+        if (w < 2 * KS) {  // this wave's 64 pieces of each array
+          const int o = (w / KS) * 1024 * KS + (w % KS) * 512 + lane * 8;
+          const Frag8 s0 = as_frag(*(const u32x4*)(S + o)), s1 = as_frag(*(const u32x4*)(S + o + 512 * KS));
+          const Frag8 d0 = as_frag(*(const u32x4*)(DS + o)), d1 = as_frag(*(const u32x4*)(DS + o + 512 * KS));
+          dot += (unpack4(s0.a) + unpack4(s1.a)) * (unpack4(d0.a) + unpack4(d1.a));
+          dot += (unpack4(s0.b) + unpack4(s1.b)) * (unpack4(d0.b) + unpack4(d1.b));
+        }
+        // dv = mu, rounded: its hi part
+        if (half == 1) {
+#pragma unroll
+          for (int e = 0; e < 2; ++e) {
+            const int col = sl * 32 + 16 * e + 4 * q;
+            if (16 * wr + c < rows && col < a.V)
+              *(s16x4*)(a.dv + ((tok0 + 16 * wr + c) * a.HV + hv) * a.V + col) = e ? mh.b : mh.a;
+          }
+        }
+        if (!last) {
+          dma_wait();
+          __syncthreads();
+          bf ^= 1;
         }
       }
-      if (!last) {
-        dma_wait();
-        __syncthreads();
-        bf ^= 1;
-      }
-    }
-    // rows i = 16 wr + 4 q + r
-    const f32x4 Gi = *(const f32x4*)(Gs + 16 * wr + 4 * q), Bi = *(const f32x4*)(Bs + 16 * wr + 4 * q);
-    const float Ge = Gs[63];
-    f32x4 eg, ee, rt = zero4(), ru = zero4();
+      // rows i = 16 wr + 4 q + r
+      const f32x4 Gi = *(const f32x4*)(Gs + 16 * wr + 4 * q), Bi = *(const f32x4*)(Bs + 16 * wr + 4 * q);
+      const float Ge = Gs[63];
+      f32x4 eg, ee, rt = zero4(), ru = zero4();
 #pragma unroll
-    for (int r = 0; r < 4; ++r) eg[r] = exp_hw(Gi[r]), ee[r] = exp_hw(Ge - Gi[r]);
-#pragma unroll
-    for (int t = 0; t < HT; ++t) {
-      const f32x4 q4 = unpack4(ld_rowk(Qb, PK, 16 * wr, 16 * (HT * half + t), lane).v);
-      const f32x4 k4 = unpack4(ld_rowk(Kb, PK, 16 * wr, 16 * (HT * half + t), lane).v);
-      x1[t] *= a.scale * eg;
-      y2[t] *= eg;
-      y3[t] *= ee;
-      dq[t] += x1[t];
-      dk[t] += Bi * y3[t] - y2[t];
-      rt += q4 * x1[t] - k4 * y2[t];
-      ru += k4 * y3[t];
-    }
-#pragma unroll
-    for (int r = 0; r < 4; ++r) rt[r] = sum16(rt[r]), ru[r] = sum16(ru[r]);
-    if (c == 0) {
-      *(f32x4*)(rowT[half] + 16 * wr + 4 * q) = rt;
-      *(f32x4*)(rowU[half] + 16 * wr + 4 * q) = ru;
-    }
-    const float dsum = wave_sum((dot[0] + dot[1]) + (dot[2] + dot[3]));
-    if (lane == 0) dots[w] = dsum;
-    __syncthreads();  // the last slice's readers are done
-    // pair terms; column j = 16 b + c
-    f32x4 rm = zero4();
-    bf16* const pairs = (bf16*)(smem_raw + bf * L::BUF);  // dD hi, lo, E hi, lo: [64][64], transposed: row j
-    bf ^= 1;
-#pragma unroll
-    for (int e = 0; e < 2; ++e) {
-      f32x4 xd = zero4(), xe = zero4();
-      float cm = 0.0f, ca = 0.0f;
-      const int b = 2 * half + e, j = 16 * b + c;
-      if (b <= wr) {
-        const float Gj = Gs[j], bj = Bs[j];
-#pragma unroll
-        for (int r = 0; r < 4; ++r) {
-          const int i = 16 * wr + 4 * q + r;
-          const float gam = exp_hw(i >= j ? Gi[r] - Gj : 0.0f);
-          const float d = i >= j ? a.scale * gam * po[e][r] : 0.0f, m = i > j ? gam * pm[e][r] : 0.0f;
-          xd[r] = bj * d;
-          xe[r] = -bj * m;
-          ca += d * qk[e][r] - m * kk[e][r];  // P_ij (dO_i . r_j) - a_ij N_ij
-          const float t = (i > j ? xd[r] * qk[e][r] : 0.0f) + xe[r] * kk[e][r];
-          rm[r] += t;
-          cm += t;
-        }
-      }
-      cm = sum4q(cm);
-      ca = sum4q(ca);
-      if (q == 0) {
-        colM[wr][j] = cm;
-        colA[wr][j] = ca;
-      }
-      bf16* const o = pairs + j * P64 + 16 * wr + 4 * q;
-      s16x4 hi, lo;
-      split4(xd, hi, lo);
-      *(s16x4*)o = hi;
-      *(s16x4*)(o + 64 * P64) = lo;
-      split4(xe, hi, lo);
-      *(s16x4*)(o + 2 * 64 * P64) = hi;
-      *(s16x4*)(o + 3 * 64 * P64) = lo;
-    }
-#pragma unroll
-    for (int r = 0; r < 4; ++r) rm[r] = sum16(rm[r]);
-    if (c == 0) *(f32x4*)(rowM[half] + 16 * wr + 4 * q) = rm;
-    __syncthreads();
-    // dq += dD K, dk += E K (rows i); dk += dD^T Q + E^T K (rows j)
-#pragma unroll
-    for (int s = 0; s < 2; ++s) {
-      const bool lower = s <= wr >> 1, upper = s >= wr >> 1;
-      Frag8 dr[2], er[2], dc[2], ec[2];
-#pragma unroll
-      for (int e = 0; e < 2; ++e) {
-        const bf16 *D = pairs + e * 64 * P64, *E = pairs + (2 + e) * 64 * P64;
-        dr[e] = pcol(D, P64, wr, s, lane);
-        er[e] = pcol(E, P64, wr, s, lane);
-        dc[e] = prow(D, P64, wr, s, lane);
-        ec[e] = prow(E, P64, wr, s, lane);
-      }
+      for (int r = 0; r < 4; ++r) eg[r] = exp_hw(Gi[r]), ee[r] = exp_hw(Ge - Gi[r]);
 #pragma unroll
       for (int t = 0; t < HT; ++t) {
-        const Frag8 kf = pcol(Kb, PK, HT * half + t, s, lane);
-        if (lower) {
-          dq[t] = mma32(dr[1], kf, dq[t]);
-          dk[t] = mma32(er[1], kf, dk[t]);
-          dq[t] = mma32(dr[0], kf, dq[t]);
-          dk[t] = mma32(er[0], kf, dk[t]);
+        const f32x4 q4 = unpack4(ld_rowk(Qb, PK, 16 * wr, 16 * (HT * half + t), lane).v);
+        const f32x4 k4 = unpack4(ld_rowk(Kb, PK, 16 * wr, 16 * (HT * half + t), lane).v);
+        x1[t] *= a.scale * eg;
+        y2[t] *= eg;
+        y3[t] *= ee;
+        dq[t] += x1[t];
+        dk[t] += Bi * y3[t] - y2[t];
+        rt += q4 * x1[t] - k4 * y2[t];
+        ru += k4 * y3[t];
+      }
+#pragma unroll
+      for (int r = 0; r < 4; ++r) rt[r] = sum16(rt[r]), ru[r] = sum16(ru[r]);
+      if (c == 0) {
+        *(f32x4*)(rowT[half] + 16 * wr + 4 * q) = rt;
+        *(f32x4*)(rowU[half] + 16 * wr + 4 * q) = ru;
+      }
+      const float dsum = wave_sum((dot[0] + dot[1]) + (dot[2] + dot[3]));
+      if (lane == 0) dots[w] = dsum;
+      __syncthreads();  // the last slice's readers are done
+      // pair terms; column j = 16 b + c
+      f32x4 rm = zero4();
+      bf16* const pairs = (bf16*)(smem_raw + bf * L::BUF);  // dD hi, lo, E hi, lo: [64][64], transposed: row j
+      bf ^= 1;
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        f32x4 xd = zero4(), xe = zero4();
+        float cm = 0.0f, ca = 0.0f;
+        const int b = 2 * half + e, j = 16 * b + c;
+        if (b <= wr) {
+          const float Gj = Gs[j], bj = Bs[j];
+#pragma unroll
+          for (int r = 0; r < 4; ++r) {
+            const int i = 16 * wr + 4 * q + r;
+            const float gam = exp_hw(i >= j ? Gi[r] - Gj : 0.0f);
+            const float d = i >= j ? a.scale * gam * po[e][r] : 0.0f, m = i > j ? gam * pm[e][r] : 0.0f;
+            xd[r] = bj * d;
+            xe[r] = -bj * m;
+            ca += d * qk[e][r] - m * kk[e][r];  // P_ij (dO_i . r_j) - a_ij N_ij
+            const float t = (i > j ? xd[r] * qk[e][r] : 0.0f) + xe[r] * kk[e][r];
+            rm[r] += t;
+            cm += t;
+          }
         }
-        if (upper) {
-          const Frag8 qf = pcol(Qb, PK, HT * half + t, s, lane);
-          dk[t] = mma32(ec[1], kf, dk[t]);
-          dk[t] = mma32(dc[1], qf, dk[t]);
-          dk[t] = mma32(ec[0], kf, dk[t]);
-          dk[t] = mma32(dc[0], qf, dk[t]);
+        cm = sum4q(cm);
+        ca = sum4q(ca);
+        if (q == 0) {
+          colM[wr][j] = cm;
+          colA[wr][j] = ca;
+        }
+        bf16* const o = pairs + j * P64 + 16 * wr + 4 * q;
+        s16x4 hi, lo;
+        split4(xd, hi, lo);
+        *(s16x4*)o = hi;
+        *(s16x4*)(o + 64 * P64) = lo;
+        split4(xe, hi, lo);
+        *(s16x4*)(o + 2 * 64 * P64) = hi;
+        *(s16x4*)(o + 3 * 64 * P64) = lo;
+      }
+#pragma unroll
+      for (int r = 0; r < 4; ++r) rm[r] = sum16(rm[r]);
+      if (c == 0) *(f32x4*)(rowM[half] + 16 * wr + 4 * q) = rm;
+      __syncthreads();
+      // dq += dD K, dk += E K (rows i); dk += dD^T Q + E^T K (rows j)
+#pragma unroll
+      for (int s = 0; s < 2; ++s) {
+        const bool lower = s <= wr >> 1, upper = s >= wr >> 1;
+        Frag8 dr[2], er[2], dc[2], ec[2];
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          const bf16 *D = pairs + e * 64 * P64, *E = pairs + (2 + e) * 64 * P64;
+          dr[e] = pcol(D, P64, wr, s, lane);
+          er[e] = pcol(E, P64, wr, s, lane);
+          dc[e] = prow(D, P64, wr, s, lane);
+          ec[e] = prow(E, P64, wr, s, lane);
+        }
+#pragma unroll
+        for (int t = 0; t < HT; ++t) {
+          const Frag8 kf = pcol(Kb, PK, HT * half + t, s, lane);
+          if (lower) {
+            dq[t] = mma32(dr[1], kf, dq[t]);
+            dk[t] = mma32(er[1], kf, dk[t]);
+            dq[t] = mma32(dr[0], kf, dq[t]);
+            dk[t] = mma32(er[0], kf, dk[t]);
+          }
+          if (upper) {
+            const Frag8 qf = pcol(Qb, PK, HT * half + t, s, lane);
+            dk[t] = mma32(ec[1], kf, dk[t]);
+            dk[t] = mma32(dc[1], qf, dk[t]);
+            dk[t] = mma32(ec[0], kf, dk[t]);
+            dk[t] = mma32(dc[0], qf, dk[t]);
+          }
+        }
+      }
+      // dbeta, dg
+      if (w == 0) {
+        float col = 0.0f, db = 0.0f, dot0 = 0.0f;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) col += colM[i][lane], db += colA[i][lane];
+#pragma unroll
+        for (int i = 0; i < 8; ++i) dot0 += dots[i];
+        const float u = rowU[0][lane] + rowU[1][lane];
+        const float dG = rowT[0][lane] + rowT[1][lane] + rowM[0][lane] + rowM[1][lane] - col;
+        // true one-sided sums: under strong gates a result is far smaller than the sum over the whole chunk
+        const float after = __shfl(wave_incl_scan(__shfl(dG, 63 - lane, 64), lane), 63 - lane, 64);
+        const float su = __shfl_up(Bs[lane] * u, 1, 64), before = wave_incl_scan(lane ? su : 0.0f, lane);
+        const float sum = after + before + exp_hw(Gs[63]) * dot0;
+        if (lane < rows) {
+          const i64 o = (tok0 + lane) * a.HV + hv;
+          a.dg[o] = sum;
+          a.dbeta[o] = db + u;
         }
       }
     }
-    // dbeta, dg
-    if (w == 0) {
-      float col = 0.0f, db = 0.0f, dot0 = 0.0f;
+    if (next) {
+      load_kq(ntok0, nrows, nh);
+      if (w == 0) load_gates(ntok0, nrows, nslot, nh * a.rep);
+    }
+    // out, through LDS: 16-byte stores of whole rows in place of two bytes of sixteen columns
+    __syncthreads();  // the last pair terms' readers are done
+    constexpr int PO = KP + 8;
+    const int to = thread(), lo = to & 63, row0 = 16 * wr + 4 * (lo >> 4), col0 = 16 * HT * half + (lo & 15);
+    bf16 *const dqb = (bf16*)(smem_raw + (bf ^ 1) * L::BUF), *const dkb = dqb + 64 * PO;
 #pragma unroll
-      for (int i = 0; i < 4; ++i) col += colM[i][lane], db += colA[i][lane];
+    for (int t = 0; t < HT; ++t)
 #pragma unroll
-      for (int i = 0; i < 8; ++i) dot0 += dots[i];
-      const float u = rowU[0][lane] + rowU[1][lane];
-      const float dG = rowT[0][lane] + rowT[1][lane] + rowM[0][lane] + rowM[1][lane] - col;
-      // true one-sided sums: under strong gates a result is far smaller than the sum over the whole chunk
-      const float after = __shfl(wave_incl_scan(__shfl(dG, 63 - lane, 64), lane), 63 - lane, 64);
-      const float su = __shfl_up(Bs[lane] * u, 1, 64), before = wave_incl_scan(lane ? su : 0.0f, lane);
-      const float sum = after + before + exp_hw(Gs[63]) * dot0;
-      if (lane < at.rows) {
-        const i64 o = (at.tok0 + lane) * a.HV + hv;
-        a.dg[o] = sum;
-        a.dbeta[o] = db + u;
+      for (int r = 0; r < 4; ++r) {
+        const int o = (row0 + r) * PO + col0 + 16 * t;
+        dqb[o] = (bf16)dq[t][r];
+        dkb[o] = (bf16)dk[t][r];
+      }
+    __syncthreads();
+#pragma unroll
+    for (int i = 0; i < 64 * KP / 8 / GRADS_NTH; ++i) {
+      const int p = to + GRADS_NTH * i, row = p / (KP / 8), col = p % (KP / 8) * 8;
+      if (row < rows && col < a.K) {
+        const i64 o = ((tok0 + row) * a.H + h) * a.K + col;
+        *(u32x4*)(a.dq + o) = *(const u32x4*)(dqb + row * PO + col);
+        *(u32x4*)(a.dk + o) = *(const u32x4*)(dkb + row * PO + col);
       }
     }
-  }
-  // out, through LDS: 16-byte stores of whole rows in place of two bytes of sixteen columns
-  __syncthreads();  // the last pair terms' readers are done
-  constexpr int PO = KP + 8;
-  bf16 *const dqb = (bf16*)smem_raw, *const dkb = dqb + 64 * PO;
-#pragma unroll
-  for (int t = 0; t < HT; ++t)
-#pragma unroll
-    for (int r = 0; r < 4; ++r) {
-      const int o = (16 * wr + 4 * q + r) * PO + 16 * (HT * half + t) + c;
-      dqb[o] = (bf16)dq[t][r];
-      dkb[o] = (bf16)dk[t][r];
-    }
-  __syncthreads();
-#pragma unroll
-  for (int i = 0; i < 64 * KP / 8 / GRADS_NTH; ++i) {
-    const int p = tid + GRADS_NTH * i, row = p / (KP / 8), col = p % (KP / 8) * 8;
-    if (row < at.rows && col < a.K) {
-      const i64 o = ((at.tok0 + row) * a.H + h) * a.K + col;
-      *(u32x4*)(a.dq + o) = *(const u32x4*)(dqb + row * PO + col);
-      *(u32x4*)(a.dk + o) = *(const u32x4*)(dkb + row * PO + col);
-    }
+    if (!next) return;
+    tok0 = ntok0;
+    rows = nrows;
+    h = nh;
+    slot = nslot;
   }
 }
 
@@ -720,7 +773,7 @@ void launch_walks_grads(const DeltaChunkArgs& a, hipStream_t s) {
     hipLaunchKernelGGL((delta_chunk_rev_kernel<KP, false>), dim3(half), dim3(REV_NTH), (RevLds<KP>::TOTAL), s, a, half);
   }
   if (a.nslots > 0)
-    hipLaunchKernelGGL((delta_chunk_grads_kernel<KP>), dim3((unsigned)(a.nslots * a.H)), dim3(GRADS_NTH),
+    hipLaunchKernelGGL((delta_chunk_grads_kernel<KP>), dim3((unsigned)std::min<i64>(a.nslots * a.H, 256)), dim3(GRADS_NTH),
                        (GradsLds<KP>::TOTAL), s, a);
 }
 
