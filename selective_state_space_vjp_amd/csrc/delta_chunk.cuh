@@ -55,6 +55,9 @@ struct DeltaChunkArgs {
   bf16* dSw;  // [2][KP/32][64][8] the state's gradient behind the chunk
   bf16* rw;   // [2][4][64][4] r
   bf16* muw;  // [2][4][64][4] mu
+  // few cells only (NULL otherwise): the states before and the gradients behind every chunk [K][V] and r [64][V] in
+  // float32, and what comes of them: r . (K dS) e^{G_63 - G} per token [64], <S0, dS>
+  float *S32, *dS32, *r32, *su, *dot;
   float scale;
 };
 
@@ -250,6 +253,22 @@ __device__ __forceinline__ void pipe() {
     if (VALU) __builtin_amdgcn_sched_group_barrier(0x2, VALU, 0);
     if (READ) __builtin_amdgcn_sched_group_barrier(0x100, READ, 0);
   }
+}
+
+// a wave's 16 columns of a state into the float32 matrix m [K][V] (col: the lane's)
+template <int KT>
+__device__ __forceinline__ void store_state32(float* m, const f32x4 (&S)[KT], i64 K, i64 V, int q, i64 col) {
+  const brsrc rs = make_rsrc(m, (unsigned)(K * V * 4));
+  unsigned o = (unsigned)((8 * q * V + col) * 4);
+  asm volatile("" : "+v"(o));  // anew for every chunk: 32 addresses kept over the loop would not fit
+#pragma unroll
+  for (int t = 0; t < KT; ++t)
+#pragma unroll
+    for (int r = 0; r < 4; ++r) {
+      const float x = S[t][r];
+      const unsigned at = state_row(t, q) + r < K ? o + (unsigned)((state_row(t, 0) + r) * V * 4) : BUF_OOB;
+      __builtin_amdgcn_raw_buffer_store_b32(__builtin_bit_cast(unsigned, x), rs, (int)at, 0, 0);
+    }
 }
 
 struct ChunkAt {

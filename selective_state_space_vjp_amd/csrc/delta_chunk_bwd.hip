@@ -52,7 +52,7 @@ struct RevLds {  // byte offsets
 };
 constexpr int REV_NTH = 320;
 
-template <int KP>
+template <int KP, bool X32>
 __device__ __forceinline__ void delta_chunk_rev(const DeltaChunkArgs& a, unsigned block) {
   constexpr int KS = KP / 32, KT = KP / 16;
   typedef RevLds<KP> L;
@@ -87,6 +87,7 @@ __device__ __forceinline__ void delta_chunk_rev(const DeltaChunkArgs& a, unsigne
     __syncthreads();  // the period in which B of the last chunk is made
     for (int ch = nch - 1; ch >= 0; --ch) {
       if (act) {
+        if constexpr (X32) store_state32(a.dS32 + (cell0 + ch * a.HV) * a.K * a.V, dS, a.K, a.V, q, v0 + c);
         const unsigned char* const buf = smem_raw + (ch & 1) * L::ABUF;
         const bf16* Kt = (const bf16*)(buf + L::K);
         const u32x4 *Tt = (const u32x4*)(buf + L::T) + lane, *Pt = (const u32x4*)(buf + L::P) + lane;
@@ -334,17 +335,95 @@ __device__ __forceinline__ void delta_chunk_rev(const DeltaChunkArgs& a, unsigne
 }
 
 // The two walks need nothing of each other: with BOTH, blocks below `half` are
-// reverse walks (they take longer and go first), the others forward walks.
-template <int KP, bool BOTH>
+// reverse walks (they take longer and go first), the others forward walks.  X32:
+// both keep what they keep in float32 too.
+template <int KP, bool BOTH, bool X32>
 __global__ void __launch_bounds__(REV_NTH) __attribute__((amdgpu_waves_per_eu(2, 2)))
 delta_chunk_rev_kernel(DeltaChunkArgs a, unsigned half) {
-  if (!BOTH || blockIdx.x < half) delta_chunk_rev<KP>(a, blockIdx.x);
-  else if (threadIdx.x < walk_nth(1)) delta_chunk_walk<KP, 1>(a, blockIdx.x - half);  // two waves end here
+  if (!BOTH || blockIdx.x < half) delta_chunk_rev<KP, X32>(a, blockIdx.x);
+  else if (threadIdx.x < walk_nth(1)) delta_chunk_walk<KP, X32 ? 2 : 1>(a, blockIdx.x - half);  // two waves end here
 }
 template <int KP>
 __global__ void __launch_bounds__(walk_nth(1)) __attribute__((amdgpu_waves_per_eu(2, 2)))
 delta_chunk_states_kernel(DeltaChunkArgs a) {
   delta_chunk_walk<KP, 1>(a, blockIdx.x);
+}
+
+// su_i = e^{G_63 - G_i} r_i . (K dS)_i and <S0, dS> of one cell from float32 r, S0
+// and dS (K dS in three parts of dS), for few cells.  dg is a sum of a few such
+// terms of either sign, and with r and dS in two bf16 parts (2e-6 of each value)
+// it comes out at 5e-6 of its norm where many cells make up the norm, but at 1e-5
+// and more for a short sequence of a few heads (1.4e-5 for 30 tokens of 2).
+// Eight waves, each every eighth tile of 16 columns.
+template <int KP>
+__global__ void __launch_bounds__(512) delta_su_kernel(DeltaChunkArgs a) {
+  constexpr int KS = KP / 32;
+  __shared__ float red[8][64], dots[8];
+  const int lane = threadIdx.x & 63, w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), c = lane & 15, q = lane >> 4;
+  const i64 cell = blockIdx.x, slot = cell / a.HV, hv = cell % a.HV, h = hv / a.rep;
+  const ChunkAt at = chunk_at(a.seq, slot, lane);
+  if (at.rows == 0) return;
+  const brsrc rd = state_rsrc(a.dS32, a, cell, true), rs = state_rsrc(a.S32, a, cell, true);
+  const brsrc rk = row_rsrc(a.k, at.tok0, at.rows, a.H, h, a.K);
+  u32x4 kf[4][KS];
+#pragma unroll
+  for (int m = 0; m < 4; ++m)
+#pragma unroll
+    for (int s = 0; s < KS; ++s) {
+      const int col = 32 * s + 8 * q;
+      kf[m][s] = bload16(rk, col < a.K ? (unsigned)(((16 * m + c) * a.H * a.K + col) * 2) : BUF_OOB);
+    }
+  f32x4 su[4];
+#pragma unroll
+  for (int m = 0; m < 4; ++m) su[m] = zero4();
+  float dot = 0.0f;
+  for (i64 vt = w; vt < a.nvt; vt += 8) {
+    const i64 v = 16 * vt + c;
+    f32x4 z[4], x[2 * KS];
+#pragma unroll
+    for (int m = 0; m < 4; ++m) z[m] = zero4();
+#pragma unroll
+    for (int t = 0; t < 2 * KS; ++t) x[t] = load_state4(rd, a, t, q, v);  // rows 32s + 8q + 4 (t & 1) ..
+#pragma unroll
+    for (int t = 0; t < 2 * KS; ++t) {
+      const f32x4 s0 = load_state4(rs, a, t, q, v);
+#pragma unroll
+      for (int r = 0; r < 4; ++r) dot = fmaf(s0[r], x[t][r], dot);
+    }
+#pragma unroll
+    for (int s = 0; s < KS; ++s) {
+      Frag8 hi, mid, lo;
+      split8x3(x[2 * s], x[2 * s + 1], hi, mid, lo);
+#pragma unroll
+      for (int m = 0; m < 4; ++m) z[m] = mma32(kf[m][s], as_u4(lo), z[m]);
+#pragma unroll
+      for (int m = 0; m < 4; ++m) z[m] = mma32(kf[m][s], as_u4(mid), z[m]);
+#pragma unroll
+      for (int m = 0; m < 4; ++m) z[m] = mma32(kf[m][s], as_u4(hi), z[m]);
+    }
+#pragma unroll
+    for (int m = 0; m < 4; ++m)
+#pragma unroll
+      for (int r = 0; r < 4; ++r) su[m][r] = fmaf(z[m][r], a.r32[(cell * 64 + 16 * m + 4 * q + r) * a.V + v], su[m][r]);
+  }
+#pragma unroll
+  for (int m = 0; m < 4; ++m)
+#pragma unroll
+    for (int r = 0; r < 4; ++r) {
+      const float x = sum16(su[m][r]);
+      if (c == 0) red[w][16 * m + 4 * q + r] = x;
+    }
+  dot = wave_sum(dot);
+  if (lane == 0) dots[w] = dot;
+  __syncthreads();
+  if (w == 0) {
+    const float G = a.G[cell * 64 + lane], end = __shfl(G, 63, 64);
+    float s = 0.0f, t = 0.0f;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) s += red[i][lane], t += dots[i];
+    a.su[cell * 64 + lane] = exp_hw(end - G) * s;
+    if (lane == 0) a.dot[cell] = t;
+  }
 }
 
 // ---------------------------------------------------------------------------
@@ -709,7 +788,11 @@ __global__ void __launch_bounds__(GRADS_NTH, 2) delta_chunk_grads_kernel(DeltaCh
         for (int i = 0; i < 4; ++i) col += colM[i][lane], db += colA[i][lane];
 #pragma unroll
         for (int i = 0; i < 8; ++i) dot0 += dots[i];
-        const float u = rowU[0][lane] + rowU[1][lane];
+        float u = rowU[0][lane] + rowU[1][lane];
+        if (a.su) {
+          u = a.su[(slot * a.HV + hv) * 64 + lane];
+          dot0 = a.dot[slot * a.HV + hv];
+        }
         const float dG = rowT[0][lane] + rowT[1][lane] + rowM[0][lane] + rowM[1][lane] - col;
         // true one-sided sums: under strong gates a result is far smaller than the sum over the whole chunk
         const float after = __shfl(wave_incl_scan(__shfl(dG, 63 - lane, 64), lane), 63 - lane, 64);
@@ -760,17 +843,22 @@ __global__ void __launch_bounds__(GRADS_NTH, 2) delta_chunk_grads_kernel(DeltaCh
 template <int KP>
 void launch_walks_grads(const DeltaChunkArgs& a, hipStream_t s) {
   static_assert(RevLds<KP>::TOTAL >= WalkLds<KP, 1>::TOTAL, "one launch for both walks");
+  const size_t lds = RevLds<KP>::TOTAL;
   const unsigned half = (unsigned)walk_blocks(a.seq.nseq * a.HV, (a.V + 31) / 32);
   // A workgroup takes a CU, so that the walks run in rounds of 256 workgroups.  Where a walk's last round is not
   // full, one launch of both lets the other fill it: 123 us against 177 us for the whole backward at 64 workgroups
   // per walk (b=1 T=2048 HV=16, K = V = 128), 279 against 292 at 192, 267 against 285 at 384.  Full rounds gain
   // nothing, and the walks' inputs push each other out of the caches: 686 against 675 us at 256 (b=2 T=4096 HV=32),
   // 352 against 348 at 512 and 785 against 719 at 1024 (T=1024).
-  if (half % 256 != 0 && half < 512) {
-    hipLaunchKernelGGL((delta_chunk_rev_kernel<KP, true>), dim3(2 * half), dim3(REV_NTH), (RevLds<KP>::TOTAL), s, a, half);
+  if (a.su) {  // few cells
+    hipLaunchKernelGGL((delta_chunk_rev_kernel<KP, true, true>), dim3(2 * half), dim3(REV_NTH), lds, s, a, half);
+    if (a.nslots > 0)
+      hipLaunchKernelGGL((delta_su_kernel<KP>), dim3((unsigned)(a.nslots * a.HV)), dim3(512), 0, s, a);
+  } else if (half % 256 != 0 && half < 512) {
+    hipLaunchKernelGGL((delta_chunk_rev_kernel<KP, true, false>), dim3(2 * half), dim3(REV_NTH), lds, s, a, half);
   } else {
     hipLaunchKernelGGL((delta_chunk_states_kernel<KP>), dim3(half), dim3(walk_nth(1)), (WalkLds<KP, 1>::TOTAL), s, a);
-    hipLaunchKernelGGL((delta_chunk_rev_kernel<KP, false>), dim3(half), dim3(REV_NTH), (RevLds<KP>::TOTAL), s, a, half);
+    hipLaunchKernelGGL((delta_chunk_rev_kernel<KP, false, false>), dim3(half), dim3(REV_NTH), lds, s, a, half);
   }
   if (a.nslots > 0)
     hipLaunchKernelGGL((delta_chunk_grads_kernel<KP>), dim3((unsigned)std::min<i64>(a.nslots * a.H, 256)), dim3(GRADS_NTH),
@@ -779,6 +867,8 @@ void launch_walks_grads(const DeltaChunkArgs& a, hipStream_t s) {
 
 struct BwdPlan {
   i64 off_T, off_Tt, off_Pt, off_G, off_S, off_dS, off_r, off_mu;
+  i64 off_S32, off_dS32, off_r32, off_su, off_dot;  // few cells only
+  bool few;
   size_t bytes;
 };
 BwdPlan bwd_plan(const ssmvjp_delta_chunk_desc& d) {
@@ -798,6 +888,16 @@ BwdPlan bwd_plan(const ssmvjp_delta_chunk_desc& d) {
   p.off_dS = carve(tiles * KP * 16 * 2 * 2);
   p.off_r = carve(tiles * 4 * 1024);
   p.off_mu = carve(tiles * 4 * 1024);
+  // few: dg's norm is made up of few sums (delta_su_kernel).  Not for more: at 48 cells dg is within 8e-6 without,
+  // and the call takes longer, 105 against 67 us at 128 cells (b=1 T=512 HV=16).  At most 20 MB of workspace.
+  p.few = cells <= 32 && cells * d.dv <= 1 << 14;
+  if (p.few) {
+    p.off_S32 = carve(cells * d.dk * d.dv * 4);
+    p.off_dS32 = carve(cells * d.dk * d.dv * 4);
+    p.off_r32 = carve(cells * 64 * d.dv * 4);
+    p.off_su = carve(cells * 64 * 4);
+    p.off_dot = carve(cells * 4);
+  }
   p.bytes = (size_t)off;
   return p;
 }
@@ -816,6 +916,11 @@ hipError_t launch_delta_chunk_bwd(const ssmvjp_delta_chunk_desc& d, const DeltaC
   auto b16 = [&](i64 off) { return (bf16*)(ws + off); };
   a.Tf = b16(pl.off_T); a.Tt = b16(pl.off_Tt); a.Pt = b16(pl.off_Pt); a.G = (float*)(ws + pl.off_G);
   a.Sw = b16(pl.off_S); a.dSw = b16(pl.off_dS); a.rw = b16(pl.off_r); a.muw = b16(pl.off_mu);
+  if (pl.few) {
+    auto f32 = [&](i64 off) { return (float*)(ws + off); };
+    a.S32 = f32(pl.off_S32); a.dS32 = f32(pl.off_dS32); a.r32 = f32(pl.off_r32); a.su = f32(pl.off_su);
+    a.dot = f32(pl.off_dot);
+  }
   if (a.nslots > 0) {
     const hipError_t e = launch_delta_prep(a, true, stream);
     if (e != hipSuccess) return e;

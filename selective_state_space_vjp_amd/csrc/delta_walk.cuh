@@ -9,7 +9,7 @@
 // load in the chain that leads from one state to the next.
 //
 // MODE 0: the forward (o, S_final); 1: for the backward, the state before every
-// chunk and r.
+// chunk and r; 2: those in float32 too.
 //
 // Waves 0 and 1 carry the states of 16 columns each and do nothing that the next
 // state does not wait for.  Forward only: waves 2 and 3 follow one chunk behind
@@ -43,7 +43,7 @@ constexpr int walk_nth(int mode) { return mode ? 192 : 320; }
 template <int KP, int MODE>
 __device__ __forceinline__ void delta_chunk_walk(const DeltaChunkArgs& a, unsigned block) {
   constexpr int KS = KP / 32, KT = KP / 16;  // 32-steps and 16-tiles of K
-  constexpr bool FWD = MODE == 0;
+  constexpr bool FWD = MODE == 0, X32 = MODE == 2;
   typedef WalkLds<KP, MODE> L;
   extern __shared__ __align__(16) unsigned char smem_raw[];
   const int lane = threadIdx.x & 63, w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), c = lane & 15, q = lane >> 4;
@@ -84,6 +84,7 @@ __device__ __forceinline__ void delta_chunk_walk(const DeltaChunkArgs& a, unsign
         f32x4* Ro = (f32x4*)(smem_raw + L::R + (bf * 2 + t16) * 4096) + lane;
         s16x4* Rw = (s16x4*)(a.rw + tile * 4 * 512) + row_slot(lane);
         const float *eG = gates(ch), *wB = eG + 64;
+        if constexpr (X32) store_state32(a.S32 + (cell0 + ch * a.HV) * a.K * a.V, S, a.K, a.V, q, v0 + c);
         // Six stretches of MFMAs, each with the vector and LDS work of its neighbours between them: a 16x16x32
         // MFMA holds the matrix pipe for 16 cycles, in which three vector instructions issue.
         // 1: K S0, row tiles 0 and 1, both parts of S0; the state's decay
@@ -179,6 +180,11 @@ __device__ __forceinline__ void delta_chunk_walk(const DeltaChunkArgs& a, unsign
             Ro[2 * s * 64] = x[2 * s];
             Ro[(2 * s + 1) * 64] = x[2 * s + 1];
           } else {
+            if constexpr (X32) {
+              float* p = a.r32 + ((cell0 + ch * a.HV) * 64 + 32 * s + 4 * q) * a.V + v0 + c;
+#pragma unroll
+              for (int i = 0; i < 8; ++i) p[(16 * (i >> 2) + (i & 3)) * a.V] = x[2 * s + (i >> 2)][i & 3];
+            }
             Frag8 rh, rl;
             split8(x[2 * s], x[2 * s + 1], rh, rl);
             stream_store(Rw + 2 * s * 64, rh.a);
