@@ -630,8 +630,8 @@ __global__ void __launch_bounds__(GRADS_NTH, 2) delta_chunk_grads_kernel(DeltaCh
         const s16x4* const orp = (const s16x4*)(buf + L::DO) + (16 * wr + c) * 8 + q;  // rows of 32 columns
         const Frag8 of = {orp[0], orp[4]};
         // [tile][hi, lo]: 1024 values each of r and mu, 512 KS of the states
-        const Frag8 mh = kept_rows(MU, MU + 2048, wr, lane), ml = kept_rows(MU + 1024, MU + 3072, wr, lane);
-        const Frag8 rh = kept_rows(R, R + 2048, wr, lane), rl = kept_rows(R + 1024, R + 3072, wr, lane);
+        const Frag8 mh = kept_rows(MU, MU + 2048, wr, lane), ml = kept_rows(MU + 1024, MU + 2048 + 1024, wr, lane);
+        const Frag8 rh = kept_rows(R, R + 2048, wr, lane), rl = kept_rows(R + 1024, R + 2048 + 1024, wr, lane);
 #pragma unroll
         for (int t = 0; t < HT; ++t) {
           const int k = HT * half + t;
@@ -650,7 +650,7 @@ __global__ void __launch_bounds__(GRADS_NTH, 2) delta_chunk_grads_kernel(DeltaCh
         // also where all of a tile lies above the diagonal and is dropped later: straight code is read ahead
 #pragma unroll
         for (int e = 0; e < 2; ++e) {
-          const Frag8 bh = kept_rows(R, R + 2048, 2 * half + e, lane), bl = kept_rows(R + 1024, R + 3072, 2 * half + e, lane);
+          const Frag8 bh = kept_rows(R, R + 2048, 2 * half + e, lane), bl = kept_rows(R + 1024, R + 2048 + 1024, 2 * half + e, lane);
           po[e] = mma32(of, bl, po[e]);
           pm[e] = mma32(mh, bl, pm[e]);
           po[e] = mma32(of, bh, po[e]);

@@ -44,8 +44,6 @@ __device__ __forceinline__ void dma_dwordx4(unsigned lds_addr, unsigned off, u32
 
 // the wave's LDS-direct loads (and its other memory operations) are complete
 __device__ __forceinline__ void dma_wait() { asm volatile("s_waitcnt vmcnt(0)" ::: "memory"); }
-// the wave's LDS reads are complete: what it read may be overwritten
-__device__ __forceinline__ void lds_wait() { asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory"); }
 
 __device__ __forceinline__ unsigned lds_base(const void* smem) {
   return (unsigned)__builtin_amdgcn_readfirstlane((int)(unsigned)(unsigned long long)(lds_char*)smem);
