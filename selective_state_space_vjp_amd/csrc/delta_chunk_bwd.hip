@@ -888,9 +888,11 @@ BwdPlan bwd_plan(const ssmvjp_delta_chunk_desc& d) {
   p.off_dS = carve(tiles * KP * 16 * 2 * 2);
   p.off_r = carve(tiles * 4 * 1024);
   p.off_mu = carve(tiles * 4 * 1024);
-  // few: dg's norm is made up of few sums (delta_su_kernel).  Not for more: at 48 cells dg is within 8e-6 without,
-  // and the call takes longer, 105 against 67 us at 128 cells (b=1 T=512 HV=16).  At most 20 MB of workspace.
-  p.few = cells <= 32 && cells * d.dv <= 1 << 14;
+  // few: dg's norm is made up of few sums (delta_su_kernel): 16 cells of K = V = 128, where 48 come out within 8e-6
+  // without and the call takes longer (105 against 67 us at 128 cells, b=1 T=512 HV=16).  Narrow keys come out worse
+  // (K = 16, V = 48: 9.8e-6 at 140 cells, 8.3e-6 with) and cost less (152 against 129 us at 256 cells).  At most 6 MB
+  // of workspace.
+  p.few = cells * d.dk * d.dv <= 1 << 18;
   if (p.few) {
     p.off_S32 = carve(cells * d.dk * d.dv * 4);
     p.off_dS32 = carve(cells * d.dk * d.dv * 4);
