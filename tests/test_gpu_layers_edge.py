@@ -192,3 +192,43 @@ def test_more_long_rows_than_one_grid():
     pick = torch.tensor([0, 1, n - 4, n - 3, n - 2, n - 1], device=DEV)
     want = bd.layer_norm_bwd(dy[pick], x[pick], st["mean"][pick], st["rstd"][pick])
     assert torch.equal(b["dx"][pick], want["dx"])
+
+
+@pytest.mark.parametrize("shape", [
+    (3, 130, 4, 8, 64, 64),     # both walks in one launch, K <= 64
+    (3, 130, 4, 8, 128, 48),    # the same, K > 64
+    (8, 70, 4, 32, 64, 32),     # a full round of 256 workgroups: two launches, K <= 64
+    (8, 70, 4, 32, 80, 32),     # the same, K > 64
+    (5, 3, 2, 6, 16, 32),       # few cells: float32 terms of dg, K <= 64
+    (1, 65, 1, 3, 112, 48),     # the same, K > 64
+], ids=str)
+def test_every_form_of_the_backward(shape):
+    announce(f"delta backward form {shape}")
+    b, T, H, HV, K, V = shape
+    d = inputs(b, T, H, HV, K, V, BF, True, None, seed=T + K)
+    tol = dict(dq=TOL_BF16, dk=TOL_BF16, dv=TOL_BF16, dbeta=TOL_SPLIT, dg=TOL_SPLIT, dS0=TOL_SPLIT)
+    t = dev(d)
+    got = bwd(t)
+    check(got, reference(d), tol, str(shape))
+    for n, x in bwd(t).items():
+        assert torch.equal(x, got[n]), n
+
+
+def test_more_units_than_the_gradients_grid():
+    """More (chunk, qk head) units than workgroups of the gradients kernel, some of them without tokens: the same
+    bits as sequence by sequence."""
+    announce("delta gradients units")
+    lens = [130, 0, 1, 64, 65, 200, 0, 63] * 2
+    d = inputs(1, sum(lens), 24, 24, 64, 32, BF, True, lens, seed=12)
+    t = dev(d)
+    got = bwd(t)
+    at = 0
+    for i, n in enumerate(lens):
+        if n:
+            one = {k: (t[k][:, at:at + n].contiguous() if k in ("q", "k", "v", "beta", "g", "d_o") else t[k]) for k in t}
+            one.update(S0=t["S0"][i:i + 1], dS=t["dS"][i:i + 1], offsets=None)
+            w = bwd(one)
+            for k in ("dq", "dk", "dv"):
+                assert torch.equal(got[k][:, at:at + n], w[k]), (i, k)
+            assert torch.equal(got["dS0"][i], w["dS0"][0]), i
+        at += n
