@@ -365,7 +365,8 @@ ssmvjp_status delta_chunk_fwd(const ssmvjp_delta_chunk_desc* desc,
  *   dbeta, dg [.., HV] f32, dS0 [batch, HV, K, V] f32 (NULL = not written).
  * dq, dk and dv are rounded to bf16, dbeta, dg and dS0 come out to about 1e-5
  * of their norm.  The gradient of a g below -88 is that at -88.
- * dS0 may be dS_final or S0.
+ * dS0 may be dS_final or S0 (over S0 the two state walks run one behind the
+ * other where they would share a launch).
  * Constraints as for delta_chunk_fwd, and dtype SSMVJP_BF16 (SSMVJP_EUNSUPPORTED
  * otherwise: delta_rule_bwd has the float32 gradients, with g repeated over the
  * key channels and dg summed over them).  d_o, dq, dk, dv, dS_final and dS0 are

@@ -334,19 +334,19 @@ __device__ __forceinline__ void delta_chunk_rev(const DeltaChunkArgs& a, unsigne
   }
 }
 
-// The two walks need nothing of each other: with BOTH, blocks below `half` are
-// reverse walks (they take longer and go first), the others forward walks.  X32:
-// both keep what they keep in float32 too.
+// The two walks need nothing of each other unless dS0 is written over S0: with
+// BOTH, blocks below `half` are reverse walks (they take longer and go first),
+// the others forward walks.  X32: both keep what they keep in float32 too.
 template <int KP, bool BOTH, bool X32>
 __global__ void __launch_bounds__(REV_NTH) __attribute__((amdgpu_waves_per_eu(2, 2)))
 delta_chunk_rev_kernel(DeltaChunkArgs a, unsigned half) {
   if (!BOTH || blockIdx.x < half) delta_chunk_rev<KP, X32>(a, blockIdx.x);
   else if (threadIdx.x < walk_nth(1)) delta_chunk_walk<KP, X32 ? 2 : 1>(a, blockIdx.x - half);  // two waves end here
 }
-template <int KP>
+template <int KP, bool X32>
 __global__ void __launch_bounds__(walk_nth(1)) __attribute__((amdgpu_waves_per_eu(2, 2)))
 delta_chunk_states_kernel(DeltaChunkArgs a) {
-  delta_chunk_walk<KP, 1>(a, blockIdx.x);
+  delta_chunk_walk<KP, X32 ? 2 : 1>(a, blockIdx.x);
 }
 
 // su_i = e^{G_63 - G_i} r_i . (K dS)_i and <S0, dS> of one cell from float32 r, S0
@@ -840,25 +840,40 @@ __global__ void __launch_bounds__(GRADS_NTH, 2) delta_chunk_grads_kernel(DeltaCh
   }
 }
 
+template <int KP, bool X32>
+void launch_walks(const DeltaChunkArgs& a, unsigned half, bool together, hipStream_t s) {
+  static_assert(RevLds<KP>::TOTAL >= WalkLds<KP, 1>::TOTAL && walk_nth(1) == walk_nth(2) &&
+                    WalkLds<KP, 1>::TOTAL == WalkLds<KP, 2>::TOTAL, "one launch for both walks");
+  const size_t lds = RevLds<KP>::TOTAL;
+  if (together) {
+    hipLaunchKernelGGL((delta_chunk_rev_kernel<KP, true, X32>), dim3(2 * half), dim3(REV_NTH), lds, s, a, half);
+  } else {
+    hipLaunchKernelGGL((delta_chunk_states_kernel<KP, X32>), dim3(half), dim3(walk_nth(1)), (WalkLds<KP, 1>::TOTAL), s, a);
+    hipLaunchKernelGGL((delta_chunk_rev_kernel<KP, false, X32>), dim3(half), dim3(REV_NTH), lds, s, a, half);
+  }
+}
+
+// dS0 lies over S0: the reverse walk writes what the forward walk reads, and blocks of one launch have no order
+bool writes_over_s0(const DeltaChunkArgs& a) {
+  const uintptr_t bytes = (uintptr_t)(a.seq.nseq * a.HV * a.K * a.V * 4), r = (uintptr_t)a.S0, w = (uintptr_t)a.dS0;
+  return a.S0 && a.dS0 && r < w + bytes && w < r + bytes;
+}
+
 template <int KP>
 void launch_walks_grads(const DeltaChunkArgs& a, hipStream_t s) {
-  static_assert(RevLds<KP>::TOTAL >= WalkLds<KP, 1>::TOTAL, "one launch for both walks");
-  const size_t lds = RevLds<KP>::TOTAL;
   const unsigned half = (unsigned)walk_blocks(a.seq.nseq * a.HV, (a.V + 31) / 32);
+  const bool apart = writes_over_s0(a);
   // A workgroup takes a CU, so that the walks run in rounds of 256 workgroups.  Where a walk's last round is not
   // full, one launch of both lets the other fill it: 123 us against 177 us for the whole backward at 64 workgroups
   // per walk (b=1 T=2048 HV=16, K = V = 128), 279 against 292 at 192, 267 against 285 at 384.  Full rounds gain
   // nothing, and the walks' inputs push each other out of the caches: 686 against 675 us at 256 (b=2 T=4096 HV=32),
   // 352 against 348 at 512 and 785 against 719 at 1024 (T=1024).
   if (a.su) {  // few cells
-    hipLaunchKernelGGL((delta_chunk_rev_kernel<KP, true, true>), dim3(2 * half), dim3(REV_NTH), lds, s, a, half);
+    launch_walks<KP, true>(a, half, !apart, s);
     if (a.nslots > 0)
       hipLaunchKernelGGL((delta_su_kernel<KP>), dim3((unsigned)(a.nslots * a.HV)), dim3(512), 0, s, a);
-  } else if (half % 256 != 0 && half < 512) {
-    hipLaunchKernelGGL((delta_chunk_rev_kernel<KP, true, false>), dim3(2 * half), dim3(REV_NTH), lds, s, a, half);
   } else {
-    hipLaunchKernelGGL((delta_chunk_states_kernel<KP>), dim3(half), dim3(walk_nth(1)), (WalkLds<KP, 1>::TOTAL), s, a);
-    hipLaunchKernelGGL((delta_chunk_rev_kernel<KP, false, false>), dim3(half), dim3(REV_NTH), lds, s, a, half);
+    launch_walks<KP, false>(a, half, !apart && half % 256 != 0 && half < 512, s);
   }
   if (a.nslots > 0)
     hipLaunchKernelGGL((delta_chunk_grads_kernel<KP>), dim3((unsigned)std::min<i64>(a.nslots * a.H, 256)), dim3(GRADS_NTH),
