@@ -41,17 +41,23 @@ struct OutSpan {
   bool bf16;
 };
 
-// After the launches: clear the flag, scan every output, read the flag back
-// (this synchronises the stream) and turn a raised flag into ENONFINITE.
-template <size_t K>
-ssmvjp_status finite_check(void* workspace, size_t plan_bytes, const OutSpan (&outs)[K], hipStream_t stream) {
+// After the launches: clear the flag, scan every output (`more`: those that the
+// call writes in part), read the flag back (this synchronises the stream) and
+// turn a raised flag into ENONFINITE.
+template <size_t K, typename More>
+ssmvjp_status finite_check(void* workspace, size_t plan_bytes, const OutSpan (&outs)[K], hipStream_t stream, More more) {
   unsigned* flag = (unsigned*)((char*)workspace + round256(plan_bytes));
   launch_flag_clear(flag, stream);
   for (const OutSpan& o : outs) launch_nonfinite_check(o.p, o.n, o.bf16, flag, stream);
+  more(flag);
   unsigned host = 0;
   if (hipMemcpyAsync(&host, flag, sizeof(host), hipMemcpyDeviceToHost, stream) != hipSuccess) return SSMVJP_EHIP;
   if (hipStreamSynchronize(stream) != hipSuccess) return SSMVJP_EHIP;
   return host ? SSMVJP_ENONFINITE : SSMVJP_OK;
+}
+template <size_t K>
+ssmvjp_status finite_check(void* workspace, size_t plan_bytes, const OutSpan (&outs)[K], hipStream_t stream) {
+  return finite_check(workspace, plan_bytes, outs, stream, [](unsigned*) {});
 }
 
 }  // namespace

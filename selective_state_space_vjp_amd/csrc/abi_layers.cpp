@@ -35,6 +35,18 @@ ssmvjp_status delta_chunk_check(const ssmvjp_delta_chunk_desc* d) {
 
 int64_t chunk_tokens(const ssmvjp_delta_chunk_desc& d) { return d.packed ? d.seqlen : d.batch * d.seqlen; }
 
+// finite_check of a call's token tensors (`rows`, by the elements of one token) beside `outs`: with packed
+// sequences only the tokens that one owns, since the call leaves the others alone
+template <size_t K, size_t R>
+ssmvjp_status finite_check_tokens(const ssmvjp_delta_chunk_desc& d, const int32_t* seq_offsets, void* workspace,
+                                  size_t plan_bytes, const OutSpan (&outs)[K], const OutSpan (&rows)[R], hipStream_t stream) {
+  return finite_check(workspace, plan_bytes, outs, stream, [&](unsigned* flag) {
+    for (const OutSpan& r : rows)
+      if (d.packed) launch_nonfinite_check_rows(r.p, r.n, r.bf16, seq_offsets, d.batch, d.seqlen, flag, stream);
+      else launch_nonfinite_check(r.p, r.n * chunk_tokens(d), r.bf16, flag, stream);
+  });
+}
+
 ssmvjp_status delta_step_check(const ssmvjp_delta_step_desc* d) {
   if (!d || d->batch < 0 || d->nslots < 0 || d->reserved != 0) return SSMVJP_EINVAL;
   if (d->gate != SSMVJP_GATE_PER_HEAD && d->gate != SSMVJP_GATE_PER_KEY) return SSMVJP_EINVAL;
@@ -101,10 +113,9 @@ ssmvjp_status delta_chunk_fwd(const ssmvjp_delta_chunk_desc* desc, const void* q
   const DeltaChunkPointers ptr{q, k, v, beta, g, S0, seq_offsets, o, S_final, workspace};
   s = hip_status(launch_delta_fwd(d, ptr, (hipStream_t)stream));
   if (s != SSMVJP_OK || !check_finite_on()) return s;
-  // with packed sequences o may hold rows that no sequence owns and that the call leaves alone
-  const OutSpan outs[] = {{d.packed ? nullptr : o, tokens * d.nv_heads * d.dv, d.dtype == SSMVJP_BF16},
-                          {S_final, d.batch * d.nv_heads * d.dk * d.dv, false}};
-  return finite_check(workspace, plan, outs, (hipStream_t)stream);
+  const OutSpan outs[] = {{S_final, d.batch * d.nv_heads * d.dk * d.dv, false}};
+  const OutSpan rows[] = {{o, d.nv_heads * d.dv, d.dtype == SSMVJP_BF16}};
+  return finite_check_tokens(d, seq_offsets, workspace, plan, outs, rows, (hipStream_t)stream);
 }
 
 // ------------------------------ delta_chunk_bwd ------------------------------
@@ -140,11 +151,10 @@ ssmvjp_status delta_chunk_bwd(const ssmvjp_delta_chunk_desc* desc, const void* q
   const DeltaChunkBwdPointers ptr{q, k, v, d_o, beta, g, S0, dS_final, seq_offsets, dq, dk, dv, dbeta, dg, dS0, workspace};
   s = hip_status(launch_delta_chunk_bwd(d, ptr, (hipStream_t)stream));
   if (s != SSMVJP_OK || !check_finite_on()) return s;
-  const int64_t n = d.packed ? 0 : tokens;  // packed: rows that no sequence owns are left alone
-  const OutSpan outs[] = {{dq, n * d.nqk_heads * d.dk, true}, {dk, n * d.nqk_heads * d.dk, true},
-                          {dv, n * d.nv_heads * d.dv, true}, {dbeta, n * d.nv_heads, false}, {dg, n * d.nv_heads, false},
-                          {dS0, d.batch * d.nv_heads * d.dk * d.dv, false}};
-  return finite_check(workspace, plan, outs, (hipStream_t)stream);
+  const OutSpan outs[] = {{dS0, d.batch * d.nv_heads * d.dk * d.dv, false}};
+  const OutSpan rows[] = {{dq, d.nqk_heads * d.dk, true}, {dk, d.nqk_heads * d.dk, true}, {dv, d.nv_heads * d.dv, true},
+                          {dbeta, d.nv_heads, false}, {dg, d.nv_heads, false}};
+  return finite_check_tokens(d, seq_offsets, workspace, plan, outs, rows, (hipStream_t)stream);
 }
 
 // -------------------------------- delta_step ---------------------------------
@@ -175,8 +185,11 @@ ssmvjp_status delta_step(const ssmvjp_delta_step_desc* desc, const void* q, cons
   const DeltaStepPointers ptr{q, k, v, beta, g, state, slots, o};
   s = hip_status(launch_delta_step(d, ptr, (hipStream_t)stream));
   if (s != SSMVJP_OK || !check_finite_on()) return s;
-  const OutSpan outs[] = {{o, d.batch * d.nv_heads * d.dv, d.dtype == SSMVJP_BF16}};
-  return finite_check(workspace, 0, outs, (hipStream_t)stream);
+  const int64_t n = d.nv_heads * d.dk * d.dv;
+  const OutSpan outs[] = {{o, d.batch * d.nv_heads * d.dv, d.dtype == SSMVJP_BF16}, {slots ? nullptr : state, d.batch * n, false}};
+  return finite_check(workspace, 0, outs, (hipStream_t)stream, [&](unsigned* flag) {
+    if (slots) launch_nonfinite_check_states(state, n, slots, d.batch, d.nslots, flag, (hipStream_t)stream);
+  });
 }
 
 // -------------------------------- layer_norm ---------------------------------

@@ -187,5 +187,11 @@ hipError_t launch_norm_bwd(const ssmvjp_norm_desc& d, const NormBwdPointers& ptr
 // or infinite (finite.hip)
 void launch_flag_clear(unsigned* flag, hipStream_t stream);
 void launch_nonfinite_check(const void* p, int64_t n, bool is_bf16, unsigned* flag, hipStream_t stream);
+// the same for a token tensor of packed sequences, n elements a row: only the rows that a sequence owns
+void launch_nonfinite_check_rows(const void* p, int64_t n, bool is_bf16, const int32_t* seq_offsets, int64_t nseq,
+                                 int64_t tokens, unsigned* flag, hipStream_t stream);
+// and for the states, n elements each, that the requests of a one-token call name
+void launch_nonfinite_check_states(const float* p, int64_t n, const int32_t* slots, int64_t batch, int64_t nslots,
+                                   unsigned* flag, hipStream_t stream);
 
 }  // namespace ssmvjp
