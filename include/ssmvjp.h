@@ -430,8 +430,10 @@ typedef struct {
  *   x8_scale = max|x| * (1/127),  x8 = rint(x * (127 * (1/max|x|)))
  * (each operation rounded to float32, ties to even),
  * zeros where max|x| < 1e-36: the value kept is off by at most max|x| / 254.
- * Any dim and any element alignment (groups * dim below 2^26); 16-byte aligned tensors and a dim that is a
- * multiple of 8 (bf16) or 4 (f32) are the fast ones. */
+ * Any dim and any element alignment (groups * dim below 2^26 - 16, groups below
+ * 2^24 - 2048, rows * groups below 2^31: SSMVJP_EUNSUPPORTED otherwise); 16-byte
+ * aligned tensors and a dim that is a multiple of 8 (bf16) or 4 (f32) are the
+ * fast ones. */
 ssmvjp_status layer_norm_fwd_workspace(const ssmvjp_norm_desc* desc, size_t* bytes);
 ssmvjp_status layer_norm_fwd(const ssmvjp_norm_desc* desc,
                              const void* x, const float* weight, const float* bias, void* y, float* mean, float* rstd,

@@ -60,10 +60,11 @@ ssmvjp_status delta_step_check(const ssmvjp_delta_step_desc* d) {
 ssmvjp_status norm_check(const ssmvjp_norm_desc* d) {
   if (!d || d->rows < 0 || d->groups <= 0 || d->dim <= 0 || !valid_dtype(d->dtype)) return SSMVJP_EINVAL;
   if (!(d->eps >= 0.0f)) return SSMVJP_EINVAL;  // also NaN
-  const double parts = 4096.0 / (double)d->groups + 1, rows = (double)d->rows * (double)d->groups;
+  const double rows = (double)d->rows * (double)d->groups;
   if (rows * (double)d->dim * 4 > 9e18) return SSMVJP_EUNSUPPORTED;  // 64-bit byte offsets
-  if (!fits(rows) || !launches((double)d->groups * (double)d->dim / 16 + 1, 1024) ||
-      !launches(parts * (double)d->groups * ((double)d->dim / 256 + 1), 256))
+  // the sums over the workgroups (32 of 2 groups dim columns each) and the kernels with one or more workgroups per
+  // group, 2048 more than groups at most
+  if (!fits(rows) || !launches((double)d->groups * (double)d->dim / 16 + 1, 1024) || !launches((double)d->groups + 2048, 256))
     return SSMVJP_EUNSUPPORTED;
   return SSMVJP_OK;
 }

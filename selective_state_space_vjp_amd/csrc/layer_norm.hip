@@ -551,6 +551,15 @@ unsigned long_grid(const NormArgs& a) { return (unsigned)std::min<i64>(a.rows * 
 
 constexpr i64 FWD_GROUPS = 2048, BWD_GROUPS = 512;
 constexpr int BWD_ROWS = 2;  // a workgroup's partial dw, db cost as much as a row of dx each
+constexpr i64 COLS_GROUPS = (1 << 24) - 1;  // norm_cols_kernel: a launch has fewer than 2^32 threads
+
+i64 col_blocks(i64 D) { return (D + 255) / 256; }
+
+// partial dw, db of a group: one for each of its workgroups, or (tpr = 0) of its shares of the rows in norm_cols_kernel
+i64 bwd_parts(i64 rows, i64 G, i64 D, int tpr) {
+  const i64 p = norm_parts(rows, G, tpr ? 256 / tpr : 1, BWD_ROWS, BWD_GROUPS);
+  return tpr ? p : std::min(p, COLS_GROUPS / (col_blocks(D) * G));
+}
 
 template <typename T, int VEC, bool CK>
 void fwd_vec(const NormArgs& in, hipStream_t s) {
@@ -583,7 +592,7 @@ void bwd_vec(const NormArgs& in, hipStream_t s) {
   NormArgs a = in;
   const int tpr = norm_tpr(a.D, VEC, true);
   const i64 n = (a.D + VEC - 1) / VEC;
-  a.parts = norm_parts(a.rows, a.G, tpr ? 256 / tpr : 1, BWD_ROWS, BWD_GROUPS);
+  a.parts = bwd_parts(a.rows, a.G, a.D, tpr);
   const dim3 grid((unsigned)(a.parts * a.G)), wg(256);
   if (VEC > 1 && tpr == 16) {
     if constexpr (VEC > 1) {
@@ -599,7 +608,7 @@ void bwd_vec(const NormArgs& in, hipStream_t s) {
   } else {
     hipLaunchKernelGGL((norm_bwd_long_kernel<T, VEC, CK>), dim3(long_grid(a)), wg, 0, s, a);
     if (a.part) {
-      const i64 cb = (a.D + 255) / 256;
+      const i64 cb = col_blocks(a.D);
       hipLaunchKernelGGL((norm_cols_kernel<T, CK>), dim3((unsigned)(cb * a.G * a.parts)), wg, 0, s, a, cb);
     }
   }
@@ -614,8 +623,10 @@ NormArgs norm_args(const ssmvjp_norm_desc& d) {
 }  // namespace
 
 size_t norm_bwd_workspace_bytes(const ssmvjp_norm_desc& d) {
-  // the largest number of partial sums over the variants (they differ in the rows per workgroup)
-  return (size_t)(norm_parts(d.rows, d.groups, 1, BWD_ROWS, BWD_GROUPS) * 2 * d.groups * d.dim * 4);
+  // the largest number of partial sums over the variants: one row a workgroup, and no cap by norm_cols_kernel's grid
+  // unless every variant walks the row in passes
+  const int tpr = norm_tpr(d.dim, d.dtype == SSMVJP_BF16 ? 8 : 4, true) ? 256 : 0;
+  return (size_t)(bwd_parts(d.rows, d.groups, d.dim, tpr) * 2 * d.groups * d.dim * 4);
 }
 
 hipError_t launch_norm_fwd(const ssmvjp_norm_desc& d, const NormFwdPointers& p, hipStream_t s) {
@@ -656,7 +667,7 @@ hipError_t launch_norm_bwd(const ssmvjp_norm_desc& d, const NormBwdPointers& p, 
   }
   if (wants) {
     const int tpr = norm_tpr(d.dim, v ? (d.dtype == SSMVJP_BF16 ? 8 : 4) : 1, true);
-    const i64 parts = norm_parts(d.rows, d.groups, tpr ? 256 / tpr : 1, BWD_ROWS, BWD_GROUPS);
+    const i64 parts = bwd_parts(d.rows, d.groups, d.dim, tpr);
     hipLaunchKernelGGL(norm_reduce_kernel, dim3((unsigned)((2 * GD + 31) / 32)), dim3(1024), 0, s, (const float*)p.workspace, parts,
                        GD, p.dweight, p.dbias);
   }
