@@ -60,11 +60,11 @@ def algorithmic_bytes(w, elem=2, state_elem=2):
 
 _CSRC = "selective_state_space_vjp_amd/csrc/"
 _COMMON = (_CSRC + "ssd_common.cuh", _CSRC + "common.cuh")
-# the sources each profiled kernel is built from (a counter summary is valid
-# for the kernel as long as these files are unchanged)
+# the sources each profiled kernel is built from, its own file first (a counter
+# summary is valid for the kernel as long as these files and the compiler's
+# options are unchanged)
 KERNEL_SOURCES = {
-    # (the build script too: it sets this file's scheduling strategy)
-    "ssd_chunk16_kernel": (_CSRC + "ssd_chunk16.hip",) + _COMMON + ("selective_state_space_vjp_amd/_build.py",),
+    "ssd_chunk16_kernel": (_CSRC + "ssd_chunk16.hip", _CSRC + "lds_dma.cuh") + _COMMON,
     "ssd_chunk_bwd_kernel": (_CSRC + "ssd_chunk.hip",) + _COMMON,
     "ssd_state_scan_kernel": (_CSRC + "ssd_chunk.hip",) + _COMMON,
     "ssd_blocked_bwd_kernel": (_CSRC + "ssd_blocked.hip",) + _COMMON,
@@ -72,10 +72,15 @@ KERNEL_SOURCES = {
 
 
 def sources_sha256(kernel_name):
-    """sha256 over a kernel's sources, in order (identifies the kernel a counter run measured)."""
+    """sha256 over a kernel's sources, in order, and the options its file is compiled with (identifies the
+    kernel a counter run measured; what else the library is built from does not matter to it)."""
+    from selective_state_space_vjp_amd import _build
+
     h = hashlib.sha256()
     for f in KERNEL_SOURCES[kernel_name]:
         h.update(open(os.path.join(ROOT, f), "rb").read())
+    flags = _build.FLAGS + _build.EXTRA.get(os.path.basename(KERNEL_SOURCES[kernel_name][0]), [])
+    h.update("\0".join(f for f in flags if not os.path.isabs(f)).encode())  # not where the checkout lies
     return h.hexdigest()
 
 
