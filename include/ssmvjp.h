@@ -33,7 +33,7 @@
  *  - `stream` is a hipStream_t (NULL = the null stream).  Work is enqueued
  *    asynchronously; the caller synchronises.
  *  - Outputs are overwritten, never accumulated into.  Inputs, outputs and the
- *    workspace must not overlap.
+ *    workspace must not overlap, unless the entry point says that they may.
  *  - Validation errors (SSMVJP_EINVAL, SSMVJP_EUNSUPPORTED, SSMVJP_EWORKSPACE)
  *    are returned before anything is enqueued.  SSMVJP_EHIP means a launch
  *    failed; outputs are then undefined.
@@ -340,7 +340,9 @@ typedef struct {
  * Outputs: o like v;  S_final [batch, HV, K, V] f32 (NULL = not written).
  * Value head hv reads qk head hv / (HV/H).  bf16 runs the chunked form on the
  * matrix cores (states to about 1e-5 of their norm), float32 and calls of up to
- * 16 tokens (seqlen) run token by token.
+ * 16 tokens (seqlen: of all sequences of a packed call together) run token by
+ * token in float32 throughout.  bf16 values given as float32 therefore leave the
+ * states at float32's accuracy, at 0.7 us a token of the longest sequence.
  * g may be -infinity (a reset); the chunked form takes every g below -88 as -88.
  * There the decay between two tokens is the exponential of a difference of sums
  * of g over their chunk of 64 tokens, relatively off by up to 2^-24 of the larger
@@ -368,9 +370,12 @@ ssmvjp_status delta_chunk_fwd(const ssmvjp_delta_chunk_desc* desc,
  * dS0 may be dS_final or S0 (over S0 the two state walks run one behind the
  * other where they would share a launch).
  * Constraints as for delta_chunk_fwd, and dtype SSMVJP_BF16 (SSMVJP_EUNSUPPORTED
- * otherwise: delta_rule_bwd has the float32 gradients, with g repeated over the
- * key channels and dg summed over them).  d_o, dq, dk, dv, dS_final and dS0 are
- * 16-byte aligned too. */
+ * otherwise).  d_o, dq, dk, dv, dS_final and dS0 are 16-byte aligned too.
+ * There is no float32 form.  delta_rule_bwd computes the same gradients in
+ * float32, with g repeated over the key channels and dg summed over them, but
+ * takes only K = 128, V a multiple of 32 and equal sequences: narrower heads have
+ * to be padded with zeros (q, k, S0 and dS_final to 128 keys; v, d_o, S0 and
+ * dS_final to a multiple of 32 columns), packed sequences called one by one. */
 ssmvjp_status delta_chunk_bwd_workspace(const ssmvjp_delta_chunk_desc* desc, size_t* bytes);
 ssmvjp_status delta_chunk_bwd(const ssmvjp_delta_chunk_desc* desc,
                               const void* q, const void* k, const void* v, const float* beta, const float* g,

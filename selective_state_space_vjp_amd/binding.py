@@ -688,6 +688,8 @@ def delta_chunk_bwd(q, k, v, beta, g, S0, d_o, dS_final=None, *, scale, seq_offs
 
     Arguments as for delta_chunk_fwd; d_o like v, dS_final [b,HV,K,V] float32 (None = zeros).
     Rows that no sequence of a packed call owns are left as they were.
+    There is no float32 form (EUNSUPPORTED): delta_rule_bwd has it for equal sequences, K = 128
+    and V a multiple of 32, with g repeated over the key channels and dg summed over them.
     """
     desc = _delta_chunk_inputs(q, k, v, beta, g, S0, scale, seq_offsets)
     _required(d_o=d_o)
