@@ -291,11 +291,15 @@ hipError_t launch_delta_prep(const DeltaChunkArgs& a, bool backward, hipStream_t
   return hipGetLastError();
 }
 
-// Chunked MFMA kernels or the token walk: float32 inputs take the walk (the chunked form's operands are bf16), and
-// so do up to 16 tokens, since a chunk costs the same whether it is full or not while the walk grows with its
-// tokens.  Chunked against walk at K = V = 128, HV = 32: 17 against 9 us for 8 tokens, 17 against 14 for 16, 18
-// against 25 for 32 (1 sequence); 40 against 24 for 16, 40 against 33 for 24, 40 against 42 for 32 (8); 115 against
-// 69 for 16, 117 against 122 for 32 (32).  At 24 tokens one sequence takes 18 against 20.
+// Chunked MFMA kernels or the token walk: float32 inputs take the walk at any length, since the chunked kernels read
+// bf16 operands and keep what they compute in two bf16 parts, short of float32 results.  It is slow where sequences
+// are long, 0.7 us a token: b=2 HV=32 K=V=128 takes 45 us for T=64, 174 for 256, 2,770 for 4096 (bf16, chunked: 22,
+// 28, 175).  Up to 16 tokens take it in bf16 too, since a chunk costs the same whether it is full or not while the
+// walk grows with its tokens.  Chunked against walk at K = V = 128, HV = 32: 17 against 9 us for 8 tokens, 17 against
+// 14 for 16, 18 against 25 for 32 (1 sequence); 40 against 24 for 16, 40 against 33 for 24, 40 against 42 for 32 (8);
+// 115 against 69 for 16, 117 against 122 for 32 (32).  At 24 tokens one sequence takes 18 against 20.  A packed call
+// goes by all its tokens together, since the lengths are in device memory: many short sequences take the chunked
+// kernels there (32 of 16 tokens: 119 us packed, 65 as a batch), and one long one among them never takes the walk.
 bool delta_fwd_walks(const ssmvjp_delta_chunk_desc& d) { return d.dtype == SSMVJP_F32 || d.seqlen <= 16; }
 
 size_t delta_fwd_workspace_bytes(const ssmvjp_delta_chunk_desc& d) {

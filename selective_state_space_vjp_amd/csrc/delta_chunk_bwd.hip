@@ -441,9 +441,10 @@ __global__ void __launch_bounds__(512) delta_su_kernel(DeltaChunkArgs a) {
 // a head, loads) nobody fills, so that it goes from unit to unit with the next
 // one's first slice, k, q and gates on their way: b=2 T=4096 H=16 HV=32 K=V=128
 // takes 285 us for 4096 chunks of a head, 208 KB each (3.0 TB/s; a workgroup per
-// unit: 295; 60 us less if the blocks came from the L2), the matrix cores 41 % and
-// the LDS 33 % busy.  Two workgroups per CU would need half the registers (1024
-// threads spilled and were slower).
+// unit: 295; 60 us less if the blocks came from the L2), the matrix cores 20 % busy
+// (442 MFMAs of 16 cycles a wave and unit) and the LDS 34 %, 43 % of that bank
+// conflicts (the pitches below): most of the time the waves wait.  Two workgroups
+// per CU would need half the registers (1024 threads spilled and were slower).
 constexpr int GRADS_NTH = 512;
 
 // Row pitches of the padded tiles: 40 bytes past a multiple of 128.  The 16 rows

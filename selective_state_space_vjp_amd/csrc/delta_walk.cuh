@@ -18,11 +18,16 @@
 // prepares the gates.  One wave that does all of it takes 7,600 cycles a chunk
 // at K = 128, 2,000 of them for the readout and 1,100 for issuing the loads.
 //
-// Bound by the chain from one state to the next, 2.1 us a chunk at K = 128 (100
-// MFMAs of 16 cycles in a row, the splits of r, u and S between them, one
-// barrier): 136 us for b=2 T=4096 HV=32 V=128, 256 workgroups for 256 CUs.  MODE 1
-// takes 155 us there, 85 of them without its stores (393 MB, 2.5 TB/s); stored
-// through the L2 it took 193, and loads two chunks ahead made it 176 to 181.
+// Bound by the chain from one state to the next: 136 us for b=2 T=4096 HV=32
+// K=V=128, 256 workgroups for 256 CUs, 2.1 us or 4,330 cycles a chunk.  The 98
+// MFMAs of a state wave issue in 1,570 of them.  By the clock the six stretches
+// take K S0 and the residual 943 + 710 cycles (32 MFMAs), T 539 + 394 (18), K^T u
+// 891 + 788 (48), the barrier 69: each begins with what the one before it ends
+// with (the last MFMAs' results, their split into parts) and with its LDS reads,
+// and there is one such wave on a SIMD to fill the time.  The matrix cores are 27 %
+// busy over all SIMDs.  MODE 1 takes 155 us there, 85 of them without its stores
+// (393 MB, 2.5 TB/s); stored through the L2 it took 193, and loads two chunks ahead
+// made it 176 to 181.
 #pragma once
 
 #include "delta_chunk.cuh"

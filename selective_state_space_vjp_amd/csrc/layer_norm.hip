@@ -31,7 +31,10 @@
 // of a device copy; backward of 8192 x 4096 in 40.9 us (4.9 TB/s) and 4.6 us for the
 // second launch; with the 8-bit form 42.1 and 40.2 us.  The two launches of the
 // backward took 69 us a call before a row was loaded ahead and 32 partial sums were
-// summed at a time, 50 since.
+// summed at a time, 50 since.  Widths that are no multiple of a vector go value by
+// value: 8192 x 1001 takes 14.5 us forward and 20.5 backward in registers (8192 x
+// 1000: 13.2 and 18.4), 8192 x 4097 in passes 64 and 107 us a call (8192 x 4096: 25
+// and 45), 4096 x 5001 45 and 70.
 #include <algorithm>
 
 #include "common.cuh"
