@@ -352,8 +352,10 @@ typedef struct {
  * sequence, and dq and dk of its qk head), and nothing else.
  * S_final may be S0.
  * Constraints: HV % H == 0 (SSMVJP_EINVAL otherwise); K % 16 == 0, K <= 128,
- * V % 16 == 0, V <= 65536, H*K and HV*V below 2^24 (SSMVJP_EUNSUPPORTED
- * otherwise).  q, k, v, o, S0, S_final 16-byte aligned. */
+ * V % 16 == 0, V <= 65536, H*K and HV*V below 2^24, and launches of fewer than
+ * 2^32 threads: chunks * H below 2^23 with seqlen/64 + 1 chunks a sequence (packed:
+ * seqlen/64 + batch of all) and (batch*HV + 8) * (V/32 + 1) at most 6,710,886
+ * (SSMVJP_EUNSUPPORTED otherwise).  q, k, v, o, S0, S_final 16-byte aligned. */
 ssmvjp_status delta_chunk_fwd_workspace(const ssmvjp_delta_chunk_desc* desc, size_t* bytes);
 ssmvjp_status delta_chunk_fwd(const ssmvjp_delta_chunk_desc* desc,
                               const void* q, const void* k, const void* v, const float* beta, const float* g,
@@ -404,8 +406,9 @@ typedef struct {
  * Output: o [batch, HV, V].
  * A request whose slot is outside [0, nslots) (padding of a captured batch) or
  * was named by an earlier request of the call gets zeros in o and touches no
- * state.  Constraints and alignment as for delta_chunk_fwd (state 16-byte
- * aligned; g too with per-key gates). */
+ * state.  Constraints on the heads and alignment as for delta_chunk_fwd (state
+ * 16-byte aligned; g too with per-key gates); batch * HV * (V/64 + 1) below 2^24
+ * (SSMVJP_EUNSUPPORTED otherwise). */
 ssmvjp_status delta_step_workspace(const ssmvjp_delta_step_desc* desc, size_t* bytes);
 ssmvjp_status delta_step(const ssmvjp_delta_step_desc* desc,
                          const void* q, const void* k, const void* v, const float* beta, const float* g,
@@ -434,7 +437,8 @@ typedef struct {
  * place.  For every block of 64 values of a row (the last may be shorter)
  *   x8_scale = max|x| * (1/127),  x8 = rint(x * (127 * (1/max|x|)))
  * (each operation rounded to float32, ties to even),
- * zeros where max|x| < 1e-36: the value kept is off by at most max|x| / 254.
+ * zeros where max|x| < 1e-36: the value kept is off by max|x| / 254, half a code, and
+ * the float32 roundings at most.
  * Any dim and any element alignment (groups * dim below 2^26 - 16, groups below
  * 2^24 - 2048, rows * groups below 2^31: SSMVJP_EUNSUPPORTED otherwise); 16-byte
  * aligned tensors and a dim that is a multiple of 8 (bf16) or 4 (f32) are the
