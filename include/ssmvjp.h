@@ -347,9 +347,11 @@ typedef struct {
  * There the decay between two tokens is the exponential of a difference of sums
  * of g over their chunk of 64 tokens, relatively off by up to 2^-24 of the larger
  * sum's size (1e-5 after two resets, 6e-5 after twelve in one chunk).
- * A NaN or an infinity in a token of one value head reaches every token of its
- * chunk of 64 and all behind them in that head (in the backward, its whole
- * sequence, and dq and dk of its qk head), and nothing else.
+ * A NaN or an infinity in a token of one value head reaches that token and those
+ * behind it in that head, as in the definition: garbage in the padding behind the
+ * end of a sequence leaves the tokens before it alone (its final state not).  In
+ * the backward it reaches the head's whole sequence, and dq and dk of its qk head;
+ * in both, nothing else.
  * S_final may be S0.
  * Constraints: HV % H == 0 (SSMVJP_EINVAL otherwise); K % 16 == 0, K <= 128,
  * V % 16 == 0, V <= 65536, H*K and HV*V below 2^24, and launches of fewer than

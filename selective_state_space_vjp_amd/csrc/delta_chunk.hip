@@ -92,6 +92,7 @@ __global__ void __launch_bounds__(256, 3) delta_prep_kernel(DeltaChunkArgs a) {
   constexpr int KS = KP / 32;
   __shared__ float As[64 * TP], Ts[64 * TP];
   __shared__ float Gs[64], Bs[64];
+  __shared__ int lost;  // forward: the first row of a beta with a value that is not finite (64: none)
   const int lane = threadIdx.x & 63, w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), c = lane & 15, q = lane >> 4;
   const unsigned H32 = (unsigned)a.H;
   const i64 h = blockIdx.x % H32, slot = blockIdx.x / H32;
@@ -154,6 +155,7 @@ __global__ void __launch_bounds__(256, 3) delta_prep_kernel(DeltaChunkArgs a) {
       Gs[lane] = G;
       Bs[lane] = bn;
       a.G[unit * 64 + lane] = G;
+      if (!BWD && lane == 0) lost = 64;
     }
     __syncthreads();
     if (rr + 1 < a.rep && in) {  // the next head's gates
@@ -163,7 +165,7 @@ __global__ void __launch_bounds__(256, 3) delta_prep_kernel(DeltaChunkArgs a) {
     const int row = 16 * w + c;
     const float Gr = Gs[row];
     // a beta into LDS and, for the forward, the tiles of scale P beta
-    f32x4 p[4];
+    f32x4 p[4], az = zero4();
 #pragma unroll
     for (int b = 0; b < 4; ++b) {
       p[b] = zero4();
@@ -178,9 +180,18 @@ __global__ void __launch_bounds__(256, 3) delta_prep_kernel(DeltaChunkArgs a) {
           if (!BWD && row >= j) p[b][r] = a.scale * qk[b][r] * gb;
         }
         *(f32x4*)(As + row * TP + 16 * b + 4 * q) = x;
+        az += 0.0f * x;
       }
     }
     if constexpr (!BWD) {
+      // T is formed without the rows that hold such values and gets NaN from the first of them on: its products run
+      // over the zeros above the diagonal and would carry them to rows before
+      if (__builtin_expect(!(az[0] + az[1] + az[2] + az[3] == 0.0f), 0)) {
+        atomicMin(&lost, row);
+#pragma unroll
+        for (int b = 0; b < 4; ++b)
+          if (b <= w) *(f32x4*)(As + row * TP + 16 * b + 4 * q) = zero4();
+      }
 #pragma unroll
       for (int s = 0; s < 2; ++s)
         if (s <= w >> 1) {
@@ -214,10 +225,13 @@ __global__ void __launch_bounds__(256, 3) delta_prep_kernel(DeltaChunkArgs a) {
     __syncthreads();
     invert64(As, Ts, w, lane);
     // T - I: lane row i = 16 w + c, columns 16 b + 4 q + r; blocks above the diagonal are zero
+    const bool gone = !BWD && row >= lost;
     auto off_diag = [&](f32x4 x, int col) {
 #pragma unroll
-      for (int r = 0; r < 4; ++r)
+      for (int r = 0; r < 4; ++r) {
         if (col + r == row) x[r] = 0.0f;
+        if (gone) x[r] = __builtin_nanf("");
+      }
       return x;
     };
 #pragma unroll

@@ -49,6 +49,9 @@ struct DeltaSeqs {
   }
 };
 
+// NaN or an infinity
+__device__ __forceinline__ bool nonfinite(float v) { return !(fabsf(v) <= 3.402823466e38f); }
+
 inline i64 delta_slots(const ssmvjp_delta_chunk_desc& d) {
   return d.packed ? d.seqlen / DCH + d.batch : d.batch * ((d.seqlen + DCH - 1) / DCH);
 }

@@ -44,6 +44,84 @@ struct WalkLds {  // byte offsets
 };
 constexpr int walk_nth(int mode) { return mode ? 192 : 320; }
 
+// ---- values that are not finite ----
+// A product over a chunk's tokens multiplies a later token's NaN or infinity by
+// the zeros of T and P above the diagonal and so carries it to earlier tokens.
+// The state is not harmed by that: a column that meets such a value is lost from
+// there on.  Where r comes out with one, the follower forms r and the readout once
+// more, with zeros in place of the column's rows from the first such value on, and
+// puts NaN there afterwards.  To look for them costs it 16 multiply-adds a chunk, no
+// time of the walk; the same look and path in the state wave cost 4 us of 136.
+
+// the first of the column's 64 rows that is not finite (64: none); zeros from there on.  x: rows 16m + 4q ..
+__device__ __forceinline__ int drop_from_first_nonfinite(f32x4 (&x)[4], int q) {
+  int first = 64;
+#pragma unroll
+  for (int m = 3; m >= 0; --m)
+#pragma unroll
+    for (int r = 3; r >= 0; --r)
+      if (nonfinite(x[m][r])) first = 16 * m + 4 * q + r;
+  first = min(first, __shfl_xor(first, 16, 64));
+  first = min(first, __shfl_xor(first, 32, 64));
+#pragma unroll
+  for (int m = 0; m < 4; ++m)
+#pragma unroll
+    for (int r = 0; r < 4; ++r)
+      if (16 * m + 4 * q + r >= first) x[m][r] = 0.0f;
+  return first;
+}
+
+// r of a chunk from memory and the state's parts before it (So), in the order of the walk's own products: rows before
+// the column's first value that is not finite come out as if it were not there.  Columns without one keep theirs.
+template <int KP>
+__device__ __forceinline__ void causal_residual(const DeltaChunkArgs& a, i64 tok0, int rows, i64 h, i64 hv, i64 cell,
+                                                i64 col, const u32x4* So, const float* eG, f32x4 (&r)[4], int lane) {
+  constexpr int KS = KP / 32;
+  const int c = lane & 15, q = lane >> 4;
+  const brsrc rk = row_rsrc(a.k, tok0, rows, a.H, h, a.K);
+  const u32x4* Tf = (const u32x4*)(a.Tf + cell * 6 * 2 * 512) + lane;
+  f32x4 x[4], y[4];
+#pragma unroll
+  for (int m = 0; m < 4; ++m) {
+    x[m] = y[m] = zero4();
+#pragma unroll
+    for (int s = 0; s < KS; ++s) {
+      const int kc = 32 * s + 8 * q;
+      const Frag8 k = as_frag(bload16(rk, kc < a.K ? (unsigned)(((i64)(16 * m + c) * a.H * a.K + kc) * 2) : BUF_OOB));
+      x[m] = mma32(k, as_frag(So[(KS + s) * 64]), x[m]);
+      x[m] = mma32(k, as_frag(So[s * 64]), x[m]);
+    }
+    const f32x4 e = *(const f32x4*)(eG + 16 * m + 4 * q);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const int row = 16 * m + 4 * q + i;
+      x[m][i] = (row < rows ? (float)a.v[((tok0 + row) * a.HV + hv) * a.V + col] : 0.0f) - e[i] * x[m][i];
+    }
+  }
+  const int first = drop_from_first_nonfinite(x, q);
+  y[0] = x[0];
+  y[1] = x[1];
+#pragma unroll
+  for (int s = 0; s < 2; ++s) {
+    Frag8 xh, xl;
+    split8(x[2 * s], x[2 * s + 1], xh, xl);
+#pragma unroll
+    for (int m = 2 * s; m < 4; ++m) {
+      const Frag8 th = as_frag(Tf[frag_lo(m, s) * 128]), tl = as_frag(Tf[frag_lo(m, s) * 128 + 64]);
+      y[m] = mma32(th, xl, y[m]);
+      y[m] = mma32(tl, xh, y[m]);
+      y[m] = mma32(th, xh, y[m]);
+    }
+  }
+  y[2] += x[2];
+  y[3] += x[3];
+  if (first == 64) return;
+#pragma unroll
+  for (int m = 0; m < 4; ++m)
+#pragma unroll
+    for (int i = 0; i < 4; ++i) r[m][i] = 16 * m + 4 * q + i >= first ? __builtin_nanf("") : y[m][i];
+}
+
 // block `block` of walk_blocks
 template <int KP, int MODE>
 __device__ __forceinline__ void delta_chunk_walk(const DeltaChunkArgs& a, unsigned block) {
@@ -287,8 +365,19 @@ __device__ __forceinline__ void delta_chunk_walk(const DeltaChunkArgs& a, unsign
           for (int m = 0; m < 4; ++m) y[m] = mma32(hi, qf[s][m], y[m]);
         }
         Frag8 rh[2], rl[2];
+        f32x4 r[4], rz = zero4();
 #pragma unroll
-        for (int s = 0; s < 2; ++s) split8(Ro[2 * s * 64], Ro[(2 * s + 1) * 64], rh[s], rl[s]);
+        for (int m = 0; m < 4; ++m) r[m] = Ro[m * 64], rz += 0.0f * r[m];
+        const bool bad = __any(!(rz[0] + rz[1] + rz[2] + rz[3] == 0.0f));  // see above
+        int first = 64;
+        if (__builtin_expect(bad, 0)) {
+          const i64 left = sp.len - (i64)ch * DCH;
+          causal_residual<KP>(a, sp.start + (i64)ch * DCH, (int)(left < DCH ? left : DCH), h, hv, cell0 + ch * a.HV, v0 + c,
+                              So, eG, r, lane);
+          first = drop_from_first_nonfinite(r, q);
+        }
+#pragma unroll
+        for (int s = 0; s < 2; ++s) split8(r[2 * s], r[2 * s + 1], rh[s], rl[s]);
         // O^T = scale e^G (Q S0)^T + r^T (scale P beta)^T
         float e[4];
 #pragma unroll
@@ -304,6 +393,15 @@ __device__ __forceinline__ void delta_chunk_walk(const DeltaChunkArgs& a, unsign
           for (int m = 2 * s; m < 4; ++m) y[m] = mma32(rh[s], as_frag(pf[2 * frag_lo(m, s) + 1]), y[m]);
 #pragma unroll
           for (int m = 2 * s; m < 4; ++m) y[m] = mma32(rh[s], as_frag(pf[2 * frag_lo(m, s)]), y[m]);
+        }
+        if (__builtin_expect(bad, 0)) {
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            const int from = __shfl(first, 4 * q + j, 64);
+#pragma unroll
+            for (int m = 0; m < 4; ++m)
+              if (16 * m + c >= from) y[m][j] = __builtin_nanf("");
+          }
         }
         if (p < nch) fetch_p(p);
         const i64 row0 = (i64)ch * DCH + c;

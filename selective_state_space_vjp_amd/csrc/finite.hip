@@ -13,8 +13,6 @@ __global__ void __launch_bounds__(256) flag_clear_kernel(unsigned* flag) {
   if (threadIdx.x == 0) *flag = 0u;
 }
 
-__device__ __forceinline__ bool nonfinite(float v) { return !(fabsf(v) <= 3.402823466e38f); }  // NaN or +-inf
-
 template <typename T>
 __global__ void __launch_bounds__(256) nonfinite_scan_kernel(const T* p, i64 n, unsigned* flag) {
   bool bad = false;
