@@ -463,6 +463,154 @@ ssmvjp_status layer_norm_bwd(const ssmvjp_norm_desc* desc,
                              void* dx, float* dweight, float* dbias,
                              void* workspace, size_t workspace_bytes, void* stream);
 
+/* ------------------------------------------------------------------------ */
+/* linear_scan_fwd, linear_scan_bwd, linear_scan_step                         */
+/* ------------------------------------------------------------------------ */
+
+/* A recurrence with one state value per channel, h_t in R^dim:
+ *   SSMVJP_SCAN_LOG:    h_t = exp(gate_t) h_{t-1} + x_t        (gate the log decay, float32)
+ *   SSMVJP_SCAN_GATED:  L_t = c softplus(decay) sigmoid(gate_t);  a_t = exp(-L_t);
+ *                       h_t = a_t h_{t-1} + sqrt(1 - a_t^2) sigmoid(input_gate_t) x_t
+ * with h_{-1} = h0.  Sequences as for delta_chunk_fwd: packed = 0, `batch` sequences of
+ * `seqlen` tokens (token tensors [batch, seqlen, dim]); packed = 1, `batch` sequences
+ * behind one another in `seqlen` tokens ([seqlen, dim]) with their borders in seq_offsets,
+ * clamped to [0, seqlen]; tokens that no sequence owns are neither read nor written. */
+enum { SSMVJP_SCAN_LOG = 0, SSMVJP_SCAN_GATED = 1 };
+typedef struct {
+  int64_t batch, seqlen, dim;
+  float c;          /* SSMVJP_SCAN_GATED: finite and > 0; else not used */
+  int32_t form;     /* SSMVJP_SCAN_LOG or SSMVJP_SCAN_GATED */
+  int32_t dtype;    /* SSMVJP_F32 or SSMVJP_BF16 for x, input_gate, h, dh, dx, dinput_gate, and for gate and dgate
+                       of SSMVJP_SCAN_GATED */
+  int32_t packed;   /* 0 or 1 */
+} ssmvjp_linear_scan_desc;
+
+/* Forward.
+ *   x [.., dim] (dtype)   gate [.., dim] (f32 in the log form, dtype in the gated one)
+ *   input_gate [.., dim] (dtype), decay [dim] f32: gated form (NULL in the log form)
+ *   h0 [batch, dim] f32 (NULL = zeros)   seq_offsets [batch + 1] int32 (packed; else NULL)
+ * Outputs: h like x;  h_final [batch, dim] f32 (NULL = not written; an empty sequence's is
+ *   its h0);  ckpt f32 (NULL = not written): the state before every 64th token of a
+ *   sequence, [batch, ceil(seqlen/64), dim], packed [seqlen/64 + batch, dim], where the
+ *   token 64 j of sequence s, which starts at token o, has row o/64 + s + j, and rows that
+ *   no token has are zeros.  linear_scan_bwd reads it in place of a second forward pass.
+ * The state and every sum are float32.  gate = -infinity (log form) is a reset.  A NaN or
+ * an infinity reaches the tokens behind it in its channel, and nothing else.
+ * Constraints: dim below 2^28, and launches of fewer than 2^32 threads:
+ * (tokens/64 + batch + 1) * (dim/64 + 1) below 2^23 (SSMVJP_EUNSUPPORTED otherwise).
+ * Pointers aligned to their elements; even dims on tensors aligned to two elements are the
+ * fast ones.  h_final must not be h0 (SSMVJP_EINVAL). */
+ssmvjp_status linear_scan_fwd_workspace(const ssmvjp_linear_scan_desc* desc, size_t* bytes);
+ssmvjp_status linear_scan_fwd(const ssmvjp_linear_scan_desc* desc,
+                              const void* x, const void* gate, const void* input_gate, const float* decay,
+                              const float* h0, const int32_t* seq_offsets, void* h, float* h_final, float* ckpt,
+                              void* workspace, size_t workspace_bytes, void* stream);
+
+/* Backward: the gradients of J = <dh, h> + <dh_final, h_final>.
+ *   x, gate, input_gate, decay, h0, seq_offsets as for linear_scan_fwd;  ckpt from it, or
+ *   NULL: the states are then formed again first;  dh like h;  dh_final [batch, dim] f32
+ *   (NULL = zeros)
+ * Outputs: dx like x, dgate like gate, dinput_gate like input_gate (gated form),
+ *   ddecay [dim] f32 (gated form; summed over all tokens in a fixed order; zeros where there
+ *   are none), dh0 [batch, dim] f32 (NULL = not written).
+ * Constraints as for linear_scan_fwd.  dh0 must not be dh_final (SSMVJP_EINVAL). */
+ssmvjp_status linear_scan_bwd_workspace(const ssmvjp_linear_scan_desc* desc, size_t* bytes);
+ssmvjp_status linear_scan_bwd(const ssmvjp_linear_scan_desc* desc,
+                              const void* x, const void* gate, const void* input_gate, const float* decay,
+                              const float* h0, const float* ckpt, const void* dh, const float* dh_final,
+                              const int32_t* seq_offsets,
+                              void* dx, void* dgate, void* dinput_gate, float* ddecay, float* dh0,
+                              void* workspace, size_t workspace_bytes, void* stream);
+
+typedef struct {
+  int64_t batch, nslots, dim;
+  float c;
+  int32_t form, dtype; /* as in ssmvjp_linear_scan_desc */
+  int32_t reserved;    /* must be 0 */
+} ssmvjp_linear_step_desc;
+
+/* One token of the recurrence for every request, the states updated in place.
+ *   x, gate, input_gate [batch, dim], decay [dim] as above;  state [nslots, dim] f32, read
+ *   and written;  slots [batch] int32 in device memory (NULL: request i uses state i)
+ * Output: h [batch, dim] (dtype).
+ * A request whose slot is outside [0, nslots) or was named by an earlier request of the
+ * call gets zeros in h and touches no state.  dim below 2^28, batch * (dim/256 + 1) below
+ * 2^24 (SSMVJP_EUNSUPPORTED otherwise). */
+ssmvjp_status linear_scan_step_workspace(const ssmvjp_linear_step_desc* desc, size_t* bytes);
+ssmvjp_status linear_scan_step(const ssmvjp_linear_step_desc* desc,
+                               const void* x, const void* gate, const void* input_gate, const float* decay,
+                               float* state, const int32_t* slots, void* h,
+                               void* workspace, size_t workspace_bytes, void* stream);
+
+/* ------------------------------------------------------------------------ */
+/* gated_ffn_fwd, gated_ffn_bwd                                               */
+/* ------------------------------------------------------------------------ */
+
+/* The first half of a gated feed-forward block (the product with the output
+ * projection is a plain one):
+ *   gate = x w_gate^T;  up = x w_up^T;  h = act(gate) up
+ * with act(z) = z sigmoid(z) or z (1 + tanh(sqrt(2/pi) (z + 0.044715 z^3))) / 2. */
+enum { SSMVJP_ACT_SILU = 0, SSMVJP_ACT_GELU = 1 };
+typedef struct {
+  int64_t rows, dim, hidden;
+  int32_t act;    /* SSMVJP_ACT_SILU or SSMVJP_ACT_GELU */
+  int32_t dtype;  /* SSMVJP_F32 or SSMVJP_BF16 for every tensor */
+} ssmvjp_ffn_desc;
+
+/* Forward: x [rows, dim], w_gate, w_up [hidden, dim];  h [rows, hidden];  gate, up
+ * [rows, hidden] (both or neither NULL = not written): what gated_ffn_bwd can read in
+ * place of forming them again.  Sums are float32; h is formed from the sums, not from
+ * the rounded gate and up.
+ * Constraints: dim and hidden multiples of 8 below 2^20 and launches of fewer than 2^32
+ * threads: (rows/32 + 1) * (max(dim, hidden)/32 + 1) below 2^24 (SSMVJP_EUNSUPPORTED
+ * otherwise); every tensor 16-byte aligned (SSMVJP_EINVAL otherwise). */
+ssmvjp_status gated_ffn_fwd_workspace(const ssmvjp_ffn_desc* desc, size_t* bytes);
+ssmvjp_status gated_ffn_fwd(const ssmvjp_ffn_desc* desc, const void* x, const void* w_gate, const void* w_up,
+                            void* h, void* gate, void* up, void* workspace, size_t workspace_bytes, void* stream);
+
+/* Backward from dh [rows, hidden] and either the forward's gate and up or (both NULL) x
+ * and the weights, from which they are formed again, in float32:
+ *   dgate = dh up act'(gate);  dup = dh act(gate);
+ *   dx = dgate w_gate + dup w_up;  dw_gate = dgate^T x;  dw_up = dup^T x
+ * Outputs like their inputs, each NULL = not computed; zeros when rows = 0.  dgate and dup
+ * are kept in `dtype` between the products.  Constraints as for gated_ffn_fwd. */
+ssmvjp_status gated_ffn_bwd_workspace(const ssmvjp_ffn_desc* desc, size_t* bytes);
+ssmvjp_status gated_ffn_bwd(const ssmvjp_ffn_desc* desc, const void* dh, const void* x, const void* w_gate,
+                            const void* w_up, const void* gate, const void* up, void* dx, void* dw_gate, void* dw_up,
+                            void* workspace, size_t workspace_bytes, void* stream);
+
+/* ------------------------------------------------------------------------ */
+/* dropout_fwd, dropout_bwd                                                   */
+/* ------------------------------------------------------------------------ */
+
+/* Dropout whose mask is drawn, never stored.  rng [2] int64 in device memory holds a seed
+ * and an offset (a captured call reads what they are at each replay).  Element e of the n
+ * takes the 16-bit half e % 8 (low half of the first word first) of the four words of the
+ * Philox 4x32-10 generator (Salmon, Moraes, Dror and Shaw, "Parallel random numbers: as
+ * easy as 1, 2, 3", 2011) with the seed's two 32-bit words as key and the counter
+ * (low, high word of e / 8, low, high word of the offset).  It is kept where that draw is
+ * at least t = rint(65536 p); kept values are multiplied by 65536 / (65536 - t), so that
+ * the mean is that of x exactly at every p; dropped ones give 0, whatever they hold. */
+typedef struct {
+  int64_t n;
+  double p;         /* in [0, 1] */
+  int32_t dtype;    /* SSMVJP_F32 or SSMVJP_BF16 for x, residual, y, dy, dx */
+  int32_t reserved; /* must be 0 */
+} ssmvjp_dropout_desc;
+
+/* Forward: y = residual + kept x 65536 / (65536 - t) (residual NULL = zeros), one rounding
+ * to dtype.  y may be x or residual.  Any element alignment; 16-byte aligned tensors are
+ * the fast ones.  n below 2^60 (SSMVJP_EUNSUPPORTED otherwise). */
+ssmvjp_status dropout_fwd_workspace(const ssmvjp_dropout_desc* desc, size_t* bytes);
+ssmvjp_status dropout_fwd(const ssmvjp_dropout_desc* desc, const void* x, const void* residual, const int64_t* rng,
+                          void* y, void* workspace, size_t workspace_bytes, void* stream);
+
+/* Backward: dx = kept dy 65536 / (65536 - t), the mask of the forward with the same rng
+ * (the residual's gradient is dy itself).  dx may be dy. */
+ssmvjp_status dropout_bwd_workspace(const ssmvjp_dropout_desc* desc, size_t* bytes);
+ssmvjp_status dropout_bwd(const ssmvjp_dropout_desc* desc, const void* dy, const int64_t* rng, void* dx,
+                          void* workspace, size_t workspace_bytes, void* stream);
+
 /* Human-readable name of a status code (static storage). */
 const char* ssmvjp_status_str(ssmvjp_status status);
 

@@ -19,7 +19,8 @@ BUILD = ROOT / "_build"
 LIB = PKG / "libssmvjp.so"
 SOURCES = ["abi.cpp", "scan_seq.hip", "ssd_chunk.hip", "ssd_chunk16.hip", "ssd_blocked.hip", "ssd_fwd.hip", "delta_rule.hip",
            "noalloc.hip", "finite.hip",
-           "ssd_pad.hip", "abi_layers.cpp", "delta_step.hip", "delta_chunk.hip", "delta_chunk_bwd.hip", "layer_norm.hip"]
+           "ssd_pad.hip", "abi_layers.cpp", "delta_step.hip", "delta_chunk.hip", "delta_chunk_bwd.hip", "layer_norm.hip",
+           "abi_block.cpp", "linear_scan.hip", "gated_ffn.hip", "dropout.hip"]
 # per-file extra flags: the per-chunk kernel is scheduled with LLVM's
 # max-memory-clause strategy (its LDS and buffer loads grouped into clauses;
 # 1-2 % faster in A/B against the default strategy, identical results)

@@ -20,13 +20,19 @@ DECAY_PER_HEAD, DECAY_PER_STATE = 0, 1
 FORM_MAMBA2, FORM_RAW = 0, 1
 GATE_PER_HEAD, GATE_PER_KEY = 0, 1
 DELTA_CKPT, DELTA_BWD, DELTA_REDUCE, DELTA_ALL = 1, 2, 4, 7
+SCAN_LOG, SCAN_GATED = 0, 1
+ACT_SILU, ACT_GELU = 0, 1
 
 _STATUS_FNS = ("ssm_scan_bwd_workspace", "ssm_scan_bwd", "ssm_scan_bwd_dA", "ssd_chunk_bwd_workspace",
                "ssd_chunk_bwd", "ssd_chunk_bwd_dA", "ssd_chunk_bwd_states", "ssd_chunk_bwd_grads", "ssd_chunk_bwd_noalloc",
                "ssd_chunk_fwd_workspace", "ssd_chunk_fwd", "delta_rule_bwd_workspace", "delta_rule_bwd",
                "delta_rule_bwd_stages", "delta_chunk_fwd_workspace", "delta_chunk_fwd",
                "delta_chunk_bwd_workspace", "delta_chunk_bwd", "delta_step_workspace",
-               "delta_step", "layer_norm_fwd_workspace", "layer_norm_fwd", "layer_norm_bwd_workspace", "layer_norm_bwd")
+               "delta_step", "layer_norm_fwd_workspace", "layer_norm_fwd", "layer_norm_bwd_workspace", "layer_norm_bwd",
+               "linear_scan_fwd_workspace", "linear_scan_fwd", "linear_scan_bwd_workspace", "linear_scan_bwd",
+               "linear_scan_step_workspace", "linear_scan_step", "gated_ffn_fwd_workspace", "gated_ffn_fwd",
+               "gated_ffn_bwd_workspace", "gated_ffn_bwd", "dropout_fwd_workspace", "dropout_fwd",
+               "dropout_bwd_workspace", "dropout_bwd")
 EXPORTS = _STATUS_FNS + ("ssmvjp_status_str", "ssmvjp_version")
 
 
@@ -69,6 +75,25 @@ class NormDesc(ctypes.Structure):
                 ("eps", ctypes.c_float), ("dtype", ctypes.c_int32)]
 
 
+class LinearScanDesc(ctypes.Structure):
+    _fields_ = [("batch", ctypes.c_int64), ("seqlen", ctypes.c_int64), ("dim", ctypes.c_int64),
+                ("c", ctypes.c_float), ("form", ctypes.c_int32), ("dtype", ctypes.c_int32), ("packed", ctypes.c_int32)]
+
+
+class LinearStepDesc(ctypes.Structure):
+    _fields_ = [("batch", ctypes.c_int64), ("nslots", ctypes.c_int64), ("dim", ctypes.c_int64),
+                ("c", ctypes.c_float), ("form", ctypes.c_int32), ("dtype", ctypes.c_int32), ("reserved", ctypes.c_int32)]
+
+
+class FfnDesc(ctypes.Structure):
+    _fields_ = [("rows", ctypes.c_int64), ("dim", ctypes.c_int64), ("hidden", ctypes.c_int64),
+                ("act", ctypes.c_int32), ("dtype", ctypes.c_int32)]
+
+
+class DropoutDesc(ctypes.Structure):
+    _fields_ = [("n", ctypes.c_int64), ("p", ctypes.c_double), ("dtype", ctypes.c_int32), ("reserved", ctypes.c_int32)]
+
+
 class SsmVjpError(RuntimeError):
     def __init__(self, fn, status):
         self.status = status
@@ -102,7 +127,11 @@ def lib():
         L.delta_rule_bwd_stages.argtypes = [ctypes.POINTER(DeltaDesc), ctypes.c_int32] + [vp] * 15 + [sz, vp]
         for name, desc, nptr in (("delta_chunk_fwd", DeltaChunkDesc, 9), ("delta_chunk_bwd", DeltaChunkDesc, 15),
                                  ("delta_step", DeltaStepDesc, 8),
-                                 ("layer_norm_fwd", NormDesc, 8), ("layer_norm_bwd", NormDesc, 10)):
+                                 ("layer_norm_fwd", NormDesc, 8), ("layer_norm_bwd", NormDesc, 10),
+                                 ("linear_scan_fwd", LinearScanDesc, 9), ("linear_scan_bwd", LinearScanDesc, 14),
+                                 ("linear_scan_step", LinearStepDesc, 7), ("gated_ffn_fwd", FfnDesc, 6),
+                                 ("gated_ffn_bwd", FfnDesc, 9), ("dropout_fwd", DropoutDesc, 4),
+                                 ("dropout_bwd", DropoutDesc, 3)):
             getattr(L, name + "_workspace").argtypes = [ctypes.POINTER(desc), ctypes.POINTER(sz)]
             getattr(L, name).argtypes = [ctypes.POINTER(desc)] + [vp] * nptr + [vp, sz, vp]
         for name in _STATUS_FNS:
@@ -856,3 +885,257 @@ def layer_norm_bwd(dy, x, mean, rstd, weight=None, *, ckpt8=None, out=None, work
         _on_gpu(dev, *args)
         _enqueue("layer_norm_bwd", desc, args, dev, workspace)
     return out
+
+
+# --------------------------------------------------------------------------- #
+def _needs(dev, *checks):
+    """_need of every (name, tensor, dtype, shape), the passing comparison first."""
+    for name, t, dtype, shape in checks:
+        if t is not None and not _fits(t, dtype, shape):
+            _need(t, name, dtype, shape, dev)
+
+
+def _scan_form(x, gate, input_gate, decay):
+    """The form of a linear recurrence's arguments and its gate's type."""
+    _required(x=x, gate=gate)
+    if (input_gate is None) != (decay is None):
+        raise ValueError("input_gate and decay belong together (the gated form), or neither is given (the log form)")
+    return (SCAN_LOG, torch.float32) if decay is None else (SCAN_GATED, x.dtype)
+
+
+def _linear_scan_inputs(x, gate, h0, input_gate, decay, c, seq_offsets):
+    form, gtype = _scan_form(x, gate, input_gate, decay)
+    if x.dim() != 3:
+        raise ValueError("x must be [b,T,D]")
+    n, T, D = x.shape
+    dev, f32 = x.device, torch.float32
+    if seq_offsets is not None:
+        if n != 1:
+            raise ValueError("packed sequences (seq_offsets given) need token tensors [1,T,D]")
+        if seq_offsets.dim() != 1 or seq_offsets.shape[0] < 1:
+            raise ValueError("seq_offsets must be [sequences + 1]")
+    b = n if seq_offsets is None else seq_offsets.shape[0] - 1
+    desc = LinearScanDesc(b, T, D, float(c), form, _dtype_code(x), int(seq_offsets is not None))
+    _needs(dev, ("x", x, x.dtype, (n, T, D)), ("gate", gate, gtype, (n, T, D)), ("input_gate", input_gate, x.dtype, (n, T, D)),
+           ("decay", decay, f32, (D,)), ("h0", h0, f32, (b, D)), ("seq_offsets", seq_offsets, torch.int32, (b + 1,)))
+    return desc
+
+
+def linear_scan_ckpt_shape(desc):
+    """Shape of the kept states of a linear recurrence: one row for every 64 tokens of a sequence
+    ([b, ceil(T/64), D]; packed [T//64 + b, D])."""
+    rows = (desc.seqlen // 64 + desc.batch,) if desc.packed else (desc.batch, (desc.seqlen + 63) // 64)
+    return rows + (desc.dim,)
+
+
+def linear_scan_fwd(x, gate, h0=None, *, input_gate=None, decay=None, c=8.0, seq_offsets=None, want_final=True,
+                    want_ckpt=False, out=None, workspace=None, stream=None):
+    """A recurrence with one state value per channel.  Returns dict h (like x), h_final [b,D] float32
+    (None with want_final=False) and ckpt (float32, what linear_scan_bwd reads in place of a
+    second forward pass; None unless want_ckpt=True).
+
+    Log form (input_gate and decay None): h_t = exp(gate_t) h_{t-1} + x_t, gate [b,T,D] float32.
+    Gated form: a_t = exp(-c softplus(decay) sigmoid(gate_t)),
+    h_t = a_t h_{t-1} + sqrt(1 - a_t^2) sigmoid(input_gate_t) x_t, gate and input_gate like x,
+    decay [D] float32.
+
+    x [b,T,D] float32 or bfloat16, h0 [b,D] float32 (None = zeros).  With seq_offsets (int32 [n+1]
+    on the GPU, ascending) the token tensors are [1,T,D] and sequence i owns the tokens
+    seq_offsets[i] .. seq_offsets[i+1]-1; rows of h that no sequence owns are left as they were.
+    h_final must not be h0.
+    """
+    desc = _linear_scan_inputs(x, gate, h0, input_gate, decay, c, seq_offsets)
+    dev, f32 = x.device, torch.float32
+    final, kept = (desc.batch, desc.dim), linear_scan_ckpt_shape(desc)
+    with _scope(dev, stream):
+        if out is None:
+            out = {"h": torch.empty_like(x), "h_final": x.new_empty(final, dtype=f32) if want_final else None,
+                   "ckpt": x.new_empty(kept, dtype=f32) if want_ckpt else None}
+        else:
+            if out.get("h") is None:
+                raise ValueError("out is missing 'h'")
+            _needs(dev, ("out['h']", out["h"], x.dtype, x.shape), ("out['h_final']", out.get("h_final"), f32, final),
+                   ("out['ckpt']", out.get("ckpt"), f32, kept))
+        args = (x, gate, input_gate, decay, h0, seq_offsets, out["h"], out.get("h_final"), out.get("ckpt"))
+        _on_gpu(dev, *args)
+        _enqueue("linear_scan_fwd", desc, args, dev, workspace)
+    return out
+
+
+def linear_scan_bwd(x, gate, dh, h0=None, dh_final=None, *, input_gate=None, decay=None, c=8.0, ckpt=None,
+                    seq_offsets=None, want_dh0=True, out=None, workspace=None, stream=None):
+    """Gradients of linear_scan_fwd.  Returns dict dx (like x), dgate (like gate), dinput_gate (like
+    input_gate) and ddecay [D] float32 (both None in the log form) and dh0 [b,D] float32 (None with
+    want_dh0=False).
+
+    Arguments as for linear_scan_fwd; dh like x, dh_final [b,D] float32 (None = zeros); ckpt from a
+    forward with want_ckpt=True, or None: the states are then formed again first.  Rows that no
+    sequence of a packed call owns are left as they were.  dh0 must not be dh_final.
+    """
+    desc = _linear_scan_inputs(x, gate, h0, input_gate, decay, c, seq_offsets)
+    _required(dh=dh)
+    dev, f32 = x.device, torch.float32
+    gated, final = decay is not None, (desc.batch, desc.dim)
+    _needs(dev, ("dh", dh, x.dtype, x.shape), ("dh_final", dh_final, f32, final),
+           ("ckpt", ckpt, f32, linear_scan_ckpt_shape(desc)))
+    with _scope(dev, stream):
+        if out is None:
+            out = {"dx": torch.empty_like(x), "dgate": torch.empty_like(gate),
+                   "dinput_gate": torch.empty_like(input_gate) if gated else None,
+                   "ddecay": torch.empty_like(decay) if gated else None,
+                   "dh0": x.new_empty(final, dtype=f32) if want_dh0 else None}
+        else:
+            spec = {"dx": (x.dtype, x.shape), "dgate": (gate.dtype, x.shape)}
+            if gated:
+                spec.update(dinput_gate=(x.dtype, x.shape), ddecay=(f32, decay.shape))
+            _check_out(out, spec, dev)
+            _need(out.get("dh0"), "out['dh0']", f32, final, dev)
+        args = (x, gate, input_gate, decay, h0, ckpt, dh, dh_final, seq_offsets, out["dx"], out["dgate"],
+                out.get("dinput_gate") if gated else None, out.get("ddecay") if gated else None, out.get("dh0"))
+        _on_gpu(dev, *args)
+        _enqueue("linear_scan_bwd", desc, args, dev, workspace)
+    return out
+
+
+def linear_scan_step(x, gate, state, *, input_gate=None, decay=None, c=8.0, slots=None, out=None, workspace=None,
+                     stream=None):
+    """One token of the linear recurrence per request; updates ``state`` in place and returns h.
+
+    x and h [b,D] float32 or bfloat16, gate (and input_gate, decay) as for linear_scan_fwd without
+    the time axis, state [n,D] float32.  slots (int32 [b] on the GPU, None = request i uses state
+    i): a request whose slot is outside [0,n) or was named by an earlier request gets zeros and
+    touches no state.
+    """
+    form, gtype = _scan_form(x, gate, input_gate, decay)
+    _required(state=state)
+    if x.dim() != 2 or state.dim() != 2:
+        raise ValueError("x must be [b,D] and state [n,D]")
+    b, D = x.shape
+    dev, f32 = x.device, torch.float32
+    desc = LinearStepDesc(b, state.shape[0], D, float(c), form, _dtype_code(x), 0)
+    _needs(dev, ("x", x, x.dtype, (b, D)), ("gate", gate, gtype, (b, D)), ("input_gate", input_gate, x.dtype, (b, D)),
+           ("decay", decay, f32, (D,)), ("state", state, f32, (state.shape[0], D)), ("slots", slots, torch.int32, (b,)),
+           ("out", out, x.dtype, (b, D)))
+    with _scope(dev, stream):
+        h = torch.empty_like(x) if out is None else out
+        args = (x, gate, input_gate, decay, state, slots, h)
+        _on_gpu(dev, *args)
+        _enqueue("linear_scan_step", desc, args, dev, workspace, needs=False)
+    return h
+
+
+# --------------------------------------------------------------------------- #
+_ACTS = {"silu": ACT_SILU, "gelu": ACT_GELU}
+
+
+def _ffn_inputs(x, w_gate, w_up, act):
+    _required(x=x, w_gate=w_gate, w_up=w_up)
+    if act not in _ACTS:
+        raise ValueError(f"act must be one of {', '.join(_ACTS)}")
+    if x.dim() < 1 or w_gate.dim() != 2:
+        raise ValueError("x must be [..., D] and w_gate [F,D]")
+    F, D = w_gate.shape
+    if D == 0 or F == 0:
+        raise ValueError("w_gate has an empty axis")
+    dtype = x.dtype
+    desc = FfnDesc(x.numel() // D, D, F, _ACTS[act], _dtype_code(x))
+    lead = x.shape[:-1]
+    _needs(x.device, ("x", x, dtype, lead + (D,)), ("w_gate", w_gate, dtype, (F, D)), ("w_up", w_up, dtype, (F, D)))
+    return desc, lead + (F,)
+
+
+def gated_ffn_fwd(x, w_gate, w_up, *, act="silu", want_saved=False, out=None, workspace=None, stream=None):
+    """First half of a gated feed-forward block, h = act(x w_gate^T) * (x w_up^T).  Returns dict h
+    [..., F] and, with want_saved=True, gate and up [..., F]: what gated_ffn_bwd can read in place
+    of forming them again (None otherwise).
+
+    x [..., D], w_gate and w_up [F,D] float32 or bfloat16 (all the same), D and F multiples of 8;
+    act "silu" or "gelu" (its tanh form).
+    """
+    desc, shape = _ffn_inputs(x, w_gate, w_up, act)
+    dev, dtype = x.device, x.dtype
+    with _scope(dev, stream):
+        if out is None:
+            h = x.new_empty(shape)
+            out = {"h": h, "gate": torch.empty_like(h) if want_saved else None, "up": torch.empty_like(h) if want_saved else None}
+        else:
+            _check_out(out, {n: (dtype, shape) for n in (("h", "gate", "up") if want_saved else ("h",))}, dev)
+        gate, up = (out["gate"], out["up"]) if want_saved else (None, None)
+        args = (x, w_gate, w_up, out["h"], gate, up)
+        _on_gpu(dev, *args)
+        _enqueue("gated_ffn_fwd", desc, args, dev, workspace, needs=False)
+    return out
+
+
+def gated_ffn_bwd(dh, x, w_gate, w_up, *, act="silu", saved=None, want_dx=True, want_dw=True, out=None, workspace=None,
+                  stream=None):
+    """Gradients of gated_ffn_fwd.  Returns dict dx (like x), dw_gate and dw_up (like the weights); None
+    for what want_dx=False or want_dw=False leaves out.
+
+    dh [..., F]; saved=(gate, up) from a forward with want_saved=True, or None: they are then formed
+    again, in float32.
+    """
+    desc, shape = _ffn_inputs(x, w_gate, w_up, act)
+    _required(dh=dh)
+    dev, dtype = x.device, x.dtype
+    gate, up = (None, None) if saved is None else saved
+    if saved is not None:
+        _required(gate=gate, up=up)
+    _needs(dev, ("dh", dh, dtype, shape), ("gate", gate, dtype, shape), ("up", up, dtype, shape))
+    with _scope(dev, stream):
+        if out is None:
+            out = {"dx": torch.empty_like(x) if want_dx else None, "dw_gate": torch.empty_like(w_gate) if want_dw else None,
+                   "dw_up": torch.empty_like(w_up) if want_dw else None}
+        else:
+            spec = {"dx": (dtype, x.shape)} if want_dx else {}
+            if want_dw:
+                spec.update(dw_gate=(dtype, w_gate.shape), dw_up=(dtype, w_up.shape))
+            _check_out(out, spec, dev)
+        args = (dh, x, w_gate, w_up, gate, up, out["dx"] if want_dx else None, out["dw_gate"] if want_dw else None,
+                out["dw_up"] if want_dw else None)
+        _on_gpu(dev, *args)
+        _enqueue("gated_ffn_bwd", desc, args, dev, workspace)
+    return out
+
+
+# --------------------------------------------------------------------------- #
+def _dropout_inputs(x, rng, p):
+    _required(x=x, rng=rng)
+    if not 0.0 <= p <= 1.0:
+        raise ValueError(f"p must be in [0, 1], not {p}")
+    if not x.is_contiguous():
+        raise ValueError("x must be contiguous")
+    _needs(x.device, ("rng", rng, torch.int64, (2,)))
+    return DropoutDesc(x.numel(), p, _dtype_code(x), 0)
+
+
+def dropout_fwd(x, rng, residual=None, *, p, out=None, workspace=None, stream=None):
+    """residual + dropout(x) (residual None = zeros), one rounding.  Returns y, like x.
+
+    x and residual float32 or bfloat16, any shape; rng (int64 [2] on the GPU) holds the seed and the
+    offset of the counter-based generator that draws the mask: the same two give the same mask,
+    another offset (or seed) another one.  out may be x or residual.
+    """
+    desc = _dropout_inputs(x, rng, p)
+    dev = x.device
+    _needs(dev, ("residual", residual, x.dtype, x.shape), ("out", out, x.dtype, x.shape))
+    with _scope(dev, stream):
+        y = torch.empty_like(x) if out is None else out
+        args = (x, residual, rng, y)
+        _on_gpu(dev, *args)
+        _enqueue("dropout_fwd", desc, args, dev, workspace, needs=False)
+    return y
+
+
+def dropout_bwd(dy, rng, *, p, out=None, workspace=None, stream=None):
+    """Gradient of dropout_fwd to its x, the mask drawn again from the forward's rng (the residual's
+    gradient is dy itself).  Returns dx, like dy; out may be dy."""
+    desc = _dropout_inputs(dy, rng, p)
+    dev = dy.device
+    _needs(dev, ("out", out, dy.dtype, dy.shape))
+    with _scope(dev, stream):
+        dx = torch.empty_like(dy) if out is None else out
+        args = (dy, rng, dx)
+        _on_gpu(dev, *args)
+        _enqueue("dropout_bwd", desc, args, dev, workspace, needs=False)
+    return dx

@@ -182,6 +182,60 @@ size_t norm_bwd_workspace_bytes(const ssmvjp_norm_desc& d);
 hipError_t launch_norm_fwd(const ssmvjp_norm_desc& d, const NormFwdPointers& ptr, hipStream_t stream);
 hipError_t launch_norm_bwd(const ssmvjp_norm_desc& d, const NormBwdPointers& ptr, hipStream_t stream);
 
+// ------------------------------ linear recurrence ----------------------------
+struct LinearScanPointers {
+  const void *x, *gate, *input_gate;
+  const float *decay, *h0;
+  const int32_t* seq_offsets;  // NULL unless packed
+  void* h;                     // NULL: not written (the backward's own pass for the states)
+  float *h_final, *ckpt;       // NULL: not written
+  void* workspace;
+};
+struct LinearScanBwdPointers {
+  const void *x, *gate, *input_gate;
+  const float *decay, *h0, *ckpt;  // ckpt NULL: formed here
+  const void* dh;
+  const float* dh_final;
+  const int32_t* seq_offsets;
+  void *dx, *dgate, *dinput_gate;
+  float *ddecay, *dh0;  // dh0 NULL: not written
+  void* workspace;
+};
+struct LinearStepPointers {
+  const void *x, *gate, *input_gate;
+  const float* decay;
+  float* state;
+  const int32_t* slots;  // NULL: request i uses state i
+  void* h;
+};
+int64_t linear_scan_ckpt_rows(const ssmvjp_linear_scan_desc& d);
+size_t linear_scan_fwd_workspace_bytes(const ssmvjp_linear_scan_desc& d);
+size_t linear_scan_bwd_workspace_bytes(const ssmvjp_linear_scan_desc& d);
+hipError_t launch_linear_scan_fwd(const ssmvjp_linear_scan_desc& d, const LinearScanPointers& ptr, hipStream_t stream);
+hipError_t launch_linear_scan_bwd(const ssmvjp_linear_scan_desc& d, const LinearScanBwdPointers& ptr, hipStream_t stream);
+hipError_t launch_linear_step(const ssmvjp_linear_step_desc& d, const LinearStepPointers& ptr, hipStream_t stream);
+
+// --------------------------- gated feed-forward -----------------------------
+struct FfnFwdPointers {
+  const void *x, *w_gate, *w_up;
+  void *h, *gate, *up;  // gate, up NULL: not kept
+  void* workspace;
+};
+struct FfnBwdPointers {
+  const void *dh, *x, *w_gate, *w_up, *gate, *up;  // gate, up NULL: formed again
+  void *dx, *dw_gate, *dw_up;                      // NULL: not wanted
+  void* workspace;
+};
+size_t ffn_fwd_workspace_bytes(const ssmvjp_ffn_desc& d);
+size_t ffn_bwd_workspace_bytes(const ssmvjp_ffn_desc& d);
+hipError_t launch_ffn_fwd(const ssmvjp_ffn_desc& d, const FfnFwdPointers& ptr, hipStream_t stream);
+hipError_t launch_ffn_bwd(const ssmvjp_ffn_desc& d, const FfnBwdPointers& ptr, hipStream_t stream);
+
+// --------------------------------- dropout ----------------------------------
+// out = residual + kept in * 65536 / (65536 - t); residual NULL: zeros
+hipError_t launch_dropout(int64_t n, double p, int32_t dtype, const void* in, const void* residual, const int64_t* rng,
+                          void* out, hipStream_t stream);
+
 // ---------------------------- debug finiteness -----------------------------
 // flag = 0; then flag = 1 if any of the n elements at p (bf16 or float) is NaN
 // or infinite (finite.hip)
