@@ -55,7 +55,7 @@ __device__ __forceinline__ Token gated_token(float x, float r, float i, float ra
   const float y = 2.0f * t.L;
   const float series = y * fmaf(y, fmaf(y, fmaf(y, fmaf(y, fmaf(y, -1.0f / 720, 1.0f / 120), -1.0f / 24), 1.0f / 6), -0.5f), 1.0f);
   const float m2 = y < 0.25f ? series : fmaf(-t.a, t.a, 1.0f);
-  t.rm = m2 > 0.0f ? __builtin_amdgcn_rsqf(m2) : 0.0f;
+  t.rm = m2 >= 1.17549435e-38f ? __builtin_amdgcn_rsqf(m2) : 0.0f;  // the instruction takes denormals as zeros
   t.m = m2 * t.rm;
   t.u = t.m * t.w * x;
   return t;

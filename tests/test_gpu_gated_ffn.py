@@ -1,0 +1,143 @@
+"""GPU parity of gated_ffn_fwd and gated_ffn_bwd against float64, from one row to many, at sizes that no tile divides."""
+import math
+
+import pytest
+import torch
+
+from block_ref import BF, F32, check, ffn_reference
+from gpu_common import announce
+from selective_state_space_vjp_amd import binding as bd
+
+pytestmark = pytest.mark.gpu
+DEV = "cuda:0"
+
+
+def inputs(M, D, F, dtype, seed):
+    gen = torch.Generator().manual_seed(seed)
+    rn = lambda *s: torch.randn(s, generator=gen)  # noqa: E731
+    return [t.to(dtype) for t in (rn(M, D), rn(F, D) * D**-0.5, rn(F, D) * D**-0.5, rn(M, F))]
+
+
+SIZES = [(1, 8, 8), (1, 256, 520), (2, 64, 16), (5, 136, 72), (16, 128, 128), (17, 104, 264), (33, 72, 136), (64, 64, 64),
+         (65, 200, 96), (100, 512, 144), (129, 88, 328), (257, 264, 136), (300, 136, 512), (520, 128, 264)]
+
+
+@pytest.mark.parametrize("M,D,F", SIZES)
+@pytest.mark.parametrize("act", ["silu", "gelu"])
+@pytest.mark.parametrize("dtype", [F32, BF], ids=["f32", "bf16"])
+def test_forward_and_gradients(M, D, F, act, dtype):
+    announce(f"gated ffn {act} {dtype} M={M} D={D} F={F}")
+    x, wg, wu, dh = inputs(M, D, F, dtype, M + D + F)
+    ref = ffn_reference(x, wg, wu, dh, act, dtype=dtype)
+    t = [v.to(DEV) for v in (x, wg, wu, dh)]
+    out = bd.gated_ffn_fwd(*t[:3], act=act, want_saved=True)
+    for k in ("h", "gate", "up"):
+        check(out[k], *ref[k], k)
+    lean = bd.gated_ffn_fwd(*t[:3], act=act)
+    assert torch.equal(lean["h"], out["h"]) and lean["gate"] is None
+    got = bd.gated_ffn_bwd(t[3], *t[:3], act=act)
+    for k in ("dx", "dw_gate", "dw_up"):
+        check(got[k], *ref[k], k + " formed again")
+    saved = (out["gate"], out["up"])
+    ref = ffn_reference(x, wg, wu, dh, act, saved=[s.cpu() for s in saved], dtype=dtype)
+    got = bd.gated_ffn_bwd(t[3], *t[:3], act=act, saved=saved)
+    for k in ("dx", "dw_gate", "dw_up"):
+        check(got[k], *ref[k], k + " kept")
+
+
+def near(got, want, tol, where):
+    err = float((got.double() - want).norm() / want.norm())
+    print(where, f"{err:.1e} of {tol:.1e}", flush=True)
+    assert err <= tol, (where, err, tol)
+
+
+@pytest.mark.parametrize("M,D,F", [(777, 1000, 2712), (1030, 1544, 1032), (2048, 512, 2560)])
+def test_large_tiles(M, D, F):
+    """Norms of the errors: a rounding of bf16 leaves at most 2^-8 of the norm, dgate's and dup's roundings 2^-8 of
+    independent terms more, float32 sums far less."""
+    announce(f"gated ffn large {M} {D} {F}")
+    x, wg, wu, dh = (v.to(DEV) for v in inputs(M, D, F, BF, 5))
+    out = bd.gated_ffn_fwd(x, wg, wu, want_saved=True)
+    X, G, Uw, H = (v.double() for v in (x, wg, wu, dh))
+    gate, up = torch.mm(X, G.T), torch.mm(X, Uw.T)
+    near(out["gate"], gate, 2.0**-8, "gate")
+    near(out["up"], up, 2.0**-8, "up")
+    near(out["h"], gate * torch.sigmoid(gate) * up, 2.0**-8, "h")
+    for saved in (None, (out["gate"], out["up"])):
+        if saved:
+            gate, up = (v.double() for v in saved)
+        s = torch.sigmoid(gate)
+        dg, du = H * up * (s + gate * s * (1 - s)), H * gate * s
+        got = bd.gated_ffn_bwd(dh, x, wg, wu, saved=saved)
+        near(got["dx"], torch.mm(dg, G) + torch.mm(du, Uw), 2.0**-7, "dx")
+        near(got["dw_gate"], torch.mm(dg.T, X), 2.0**-7, "dw_gate")
+        near(got["dw_up"], torch.mm(du.T, X), 2.0**-7, "dw_up")
+
+
+@pytest.mark.parametrize("dtype", [F32, BF], ids=["f32", "bf16"])
+def test_rows_are_independent(dtype):
+    """A row's result does not depend on which rows stand beside it where the same kernel runs, a NaN row harms no other,
+    and the zeros that fill a tile never meet it."""
+    announce(f"gated ffn rows {dtype}")
+    for M in (3, 70, 300):
+        x, wg, wu, dh = (v.to(DEV) for v in inputs(M, 136, 264, dtype, 3))
+        clean = bd.gated_ffn_fwd(x, wg, wu, want_saved=True)
+        x2 = x.clone()
+        x2[M // 2] = math.nan
+        got = bd.gated_ffn_fwd(x2, wg, wu, want_saved=True)
+        rest = torch.ones(M, dtype=torch.bool)
+        rest[M // 2] = False
+        for k in clean:
+            assert torch.equal(got[k][rest], clean[k][rest]) and torch.isnan(got[k][M // 2]).all()
+        g = bd.gated_ffn_bwd(dh, x, wg, wu, saved=(clean["gate"], clean["up"]))
+        d2 = dh.clone()
+        d2[M // 2] = math.inf
+        g2 = bd.gated_ffn_bwd(d2, x, wg, wu, saved=(clean["gate"], clean["up"]))
+        assert torch.equal(g2["dx"][rest], g["dx"][rest])
+
+
+def test_extreme_projections():
+    """act and its derivative far out: finite where the formula is."""
+    announce("gated ffn extremes")
+    for act in ("silu", "gelu"):
+        x = torch.tensor([[-300.0, 0, 0, 0, 0, 0, 0, 0], [300.0, 0, 0, 0, 0, 0, 0, 0], [0.0] * 8], device=DEV)
+        w = torch.eye(8, device=DEV)
+        out = bd.gated_ffn_fwd(x, w, torch.ones(8, 8, device=DEV), act=act)
+        assert torch.isfinite(out["h"]).all()
+        assert out["h"][0, 0] == 0 and float(out["h"][1, 0]) == 300.0 * 300.0 and out["h"][2, 0] == 0
+        g = bd.gated_ffn_bwd(torch.ones(3, 8, device=DEV), x, w, torch.ones(8, 8, device=DEV), act=act)
+        assert all(torch.isfinite(v).all() for v in g.values())
+
+
+def test_optional_outputs_empty_batches_and_streams():
+    announce("gated ffn options")
+    x, wg, wu, dh = (v.to(DEV) for v in inputs(40, 64, 96, BF, 7))
+    full = bd.gated_ffn_bwd(dh, x, wg, wu)
+    only = bd.gated_ffn_bwd(dh, x, wg, wu, want_dw=False)
+    assert torch.equal(only["dx"], full["dx"]) and only["dw_gate"] is None and only["dw_up"] is None
+    only = bd.gated_ffn_bwd(dh, x, wg, wu, want_dx=False)
+    assert torch.equal(only["dw_up"], full["dw_up"]) and torch.equal(only["dw_gate"], full["dw_gate"]) and only["dx"] is None
+    e = bd.gated_ffn_fwd(x[:0], wg, wu, want_saved=True)
+    assert e["h"].shape == (0, 96)
+    g = bd.gated_ffn_bwd(dh[:0], x[:0], wg, wu)
+    assert (g["dw_gate"] == 0).all() and (g["dw_up"] == 0).all() and g["dx"].shape == (0, 64)
+    # leading axes, another stream, a graph replayed on other values
+    other = torch.cuda.Stream()
+    other.wait_stream(torch.cuda.current_stream())
+    h = bd.gated_ffn_fwd(x.view(4, 10, 64), wg, wu, stream=other)["h"]
+    other.synchronize()
+    assert h.shape == (4, 10, 96) and torch.equal(h.view(40, 96), bd.gated_ffn_fwd(x, wg, wu)["h"])
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        f = bd.gated_ffn_fwd(x, wg, wu, want_saved=True)
+        b = bd.gated_ffn_bwd(dh, x, wg, wu, saved=(f["gate"], f["up"]))
+        b2 = bd.gated_ffn_bwd(dh, x, wg, wu)
+    for _ in range(3):
+        x.copy_(torch.randn(40, 64, device=DEV))
+        g.replay()
+        torch.cuda.synchronize()
+        wf = bd.gated_ffn_fwd(x, wg, wu, want_saved=True)
+        wb, wb2 = bd.gated_ffn_bwd(dh, x, wg, wu, saved=(wf["gate"], wf["up"])), bd.gated_ffn_bwd(dh, x, wg, wu)
+        for got, want in ((f, wf), (b, wb), (b2, wb2)):
+            for k in want:
+                assert torch.equal(got[k], want[k]), k
