@@ -11,6 +11,24 @@
 //                E = L dJ/dL = l (w x a^2 (L/m) - L a h_{t-1}),
 //                dr = E (1 - sigmoid(r)), ddecay = sigmoid(decay)/softplus(decay) sum E
 // E is formed with L/m, which stays finite (sqrt(L/2)) where L and m go to zero.
+//
+// Both directions go over the data once.  A workgroup takes a tile of tokens of
+// 64 or 128 channels; its eight waves hold consecutive rows of it in registers.
+// A run of tokens acts on the state before it as h -> A h + H (A the product of
+// its a), and such pairs combine in order; what a tile needs of the tiles before
+// it in its sequence it takes from the pairs that they publish:
+//   - every tile publishes its pair as soon as it has it, before it waits;
+//   - the last tile of each group of GROUP tiles publishes the state behind it;
+//   - a tile combines the state behind the group before its own with the pairs
+//     of the tiles before it in its group, always these and in this order, so
+//     that results do not depend on which tile ran when.
+// Pairs and states are published as single 64- and 32-bit words past the L2s
+// (device-scope atomics) over a filling that no published value has, so a value
+// that is there is whole and no fence is needed.  Tiles are handed out by a
+// counter in the order of the sequence: what a tile waits for was handed out
+// before it, to a workgroup that is running.
+#include <type_traits>
+
 #include "common.cuh"
 #include "delta_seq.cuh"
 #include "kernels.h"
@@ -18,9 +36,23 @@
 namespace ssmvjp {
 namespace {
 
+constexpr int NW = 8;         // waves of a workgroup
+constexpr int FWD_ROWS = 16;  // rows of a wave: tiles of 128 tokens forward ...
+constexpr int BWD_ROWS = 8;   // ... and of 64 backward, which holds more of each
+constexpr int GROUP = 16;     // tiles between published states
+
+typedef unsigned long long u64;
+constexpr u64 NO_PAIR = ~0ull;
+constexpr unsigned NO_STATE = ~0u;
+// Polls before a wave gives up and goes on with NaN: seconds, where a wait lasts microseconds.
+constexpr int POLLS = 1 << 22;
+
 struct ScanArgs {
-  DeltaSeqs seq;
-  i64 D;
+  const int* off;         // borders of packed sequences, or NULL
+  i64 nseq, T, per, D;    // per: tiles of one sequence (off == NULL)
+  i64 ntiles;             // tile slots
+  int nslab;              // channel slabs
+  bool chain;             // a sequence may have more than one tile
   float c;
   const void *x, *gate, *igate;
   const float *decay, *h0;
@@ -32,7 +64,69 @@ struct ScanArgs {
   const float* dh_final;
   void *dx, *dgate, *digate;
   float *part, *dh0;
+  // what tiles tell each other
+  u64* pairs;        // [ntiles][D]
+  unsigned* states;  // [ntiles / GROUP + 1][D]
+  unsigned* ticket;
 };
+
+// Tile slots of N tokens each: a packed sequence s owns those from start / N + s, which never meet the next one's
+// (see delta_seq.cuh).
+template <int N>
+struct Tiles {
+  const ScanArgs& a;
+  __device__ __forceinline__ i64 border(i64 s) const {
+    const i64 o = a.off[s];
+    return o < 0 ? 0 : o > a.T ? a.T : o;
+  }
+  // the sequence of a packed slot; called by whole waves
+  __device__ __forceinline__ i64 of_slot(i64 slot, int lane) const {
+    i64 s = -1;
+    for (i64 s0 = 0; s0 < a.nseq; s0 += 64) {
+      const i64 i = s0 + lane;
+      const int n = __popcll(__ballot(i < a.nseq && border(i) / N + i <= slot));
+      s += n;
+      if (n < 64) break;
+    }
+    return s < 0 ? 0 : s;
+  }
+};
+
+struct Tile {
+  i64 seq, start, len;  // the sequence
+  i64 slot0, slot, j, n;  // its first slot, this one, tile j of n
+};
+
+__device__ __forceinline__ i64 uniform(i64 v) {
+  return (i64)(((u64)(unsigned)__builtin_amdgcn_readfirstlane((int)(v >> 32)) << 32) |
+               (unsigned)__builtin_amdgcn_readfirstlane((int)v));
+}
+
+// tile number `o` in the order of hand-out (REV: from the ends of the sequences); false: a slot without tokens
+template <int N, bool REV>
+__device__ __forceinline__ bool find_tile(const ScanArgs& a, i64 o, int lane, Tile& t) {
+  if (!a.off) {
+    const i64 j = o / a.nseq;
+    t.seq = o - j * a.nseq;
+    t.j = REV ? a.per - 1 - j : j;
+    t.n = a.per;
+    t.start = t.seq * a.T;
+    t.len = a.T;
+    t.slot0 = t.seq * a.per;
+    t.slot = t.slot0 + t.j;
+    return true;
+  }
+  const Tiles<N> seqs{a};
+  t.slot = REV ? a.ntiles - 1 - o : o;
+  t.seq = uniform(seqs.of_slot(t.slot, lane));
+  const i64 o0 = uniform(seqs.border(t.seq)), o1 = uniform(seqs.border(t.seq + 1));
+  t.start = o0;
+  t.len = o1 > o0 ? o1 - o0 : 0;
+  t.slot0 = o0 / N + t.seq;
+  t.j = t.slot - t.slot0;
+  t.n = (t.len + N - 1) / N;
+  return t.j >= 0 && t.j < t.n;
+}
 
 __device__ __forceinline__ float sigmoid_hw(float z) { return __builtin_amdgcn_rcpf(1.0f + exp_hw(-z)); }
 
@@ -61,82 +155,443 @@ __device__ __forceinline__ Token gated_token(float x, float r, float i, float ra
   return t;
 }
 
-template <typename T, bool GATED>
-__device__ __forceinline__ Token load_token(const ScanArgs& a, i64 e, float rate, float& x) {
-  x = ld((const T*)a.x, e);
-  if constexpr (GATED) return gated_token(x, ld((const T*)a.gate, e), ld((const T*)a.igate, e), rate);
-  Token t{};
-  t.a = exp_hw(((const float*)a.gate)[e]);
-  t.u = x;
-  return t;
+
+// A h + u; a state of zero stays out of a product that has overflowed
+__device__ __forceinline__ float apply(float A, float h, float u) { return h == 0.0f ? u : fmaf(A, h, u); }
+
+// ---------------------------------------------------------------------------
+// rows of V channels per lane
+// ---------------------------------------------------------------------------
+template <typename T, int V>
+struct Raw {
+  T v[V];
+};
+template <typename T, int V>
+__device__ __forceinline__ Raw<T, V> load_raw(const T* row, unsigned off) {
+  Raw<T, V> r;
+  __builtin_memcpy(&r, __builtin_assume_aligned(row + off, V * sizeof(T)), V * sizeof(T));
+  return r;
+}
+template <int V>
+__device__ __forceinline__ void store_raw(bf16* row, unsigned off, const float (&v)[V]) {
+  if constexpr (V == 2) *(unsigned*)(row + off) = pk_bf16(v[0], v[1]);
+  else row[off] = (bf16)v[0];
+}
+template <int V>
+__device__ __forceinline__ void store_raw(float* row, unsigned off, const float (&v)[V]) {
+  if constexpr (V == 2) *(float2*)(row + off) = make_float2(v[0], v[1]);
+  else row[off] = v[0];
 }
 
-template <typename T, bool GATED>
-__global__ void __launch_bounds__(64) scan_fwd_kernel(ScanArgs a) {
-  const i64 ch = (i64)blockIdx.x * 64 + threadIdx.x, s = blockIdx.y;
-  if (ch >= a.D) return;
-  const DeltaSpan sp = a.seq.span(s);
-  const float rate = GATED ? decay_rate(a.c, a.decay[ch]) : 0.0f;
-  float h = a.h0 ? a.h0[s * a.D + ch] : 0.0f;
-  for (i64 t = 0; t < sp.len; ++t) {
-    if (a.ckpt && t % DCH == 0) a.ckpt[(sp.slot0 + t / DCH) * a.D + ch] = h;
-    const i64 e = (sp.start + t) * a.D + ch;
-    float x;
-    const Token k = load_token<T, GATED>(a, e, rate, x);
-    h = fmaf(k.a, h, k.u);
-    if (a.h) st((T*)a.h, e, h);
+// ---------------------------------------------------------------------------
+// what tiles publish
+// ---------------------------------------------------------------------------
+__device__ __forceinline__ float plain_nan(float v) { return v == v ? v : __uint_as_float(0x7fc00000u); }
+
+__device__ __forceinline__ void put_pair(u64* p, float A, float H) {
+  const u64 v = (u64)__float_as_uint(plain_nan(A)) | ((u64)__float_as_uint(plain_nan(H)) << 32);
+  __hip_atomic_store(p, v, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+}
+__device__ __forceinline__ void put_state(unsigned* p, float h) {
+  __hip_atomic_store(p, __float_as_uint(plain_nan(h)), __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+}
+template <typename W, W NONE>
+__device__ __forceinline__ W await(const W* p) {
+  W v = __hip_atomic_load(p, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+  for (int n = 0; v == NONE && n < POLLS; ++n) {
+    __builtin_amdgcn_s_sleep(1);
+    v = __hip_atomic_load(p, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
   }
-  if (a.h_final) a.h_final[s * a.D + ch] = h;
+  return v;  // NONE is a NaN
 }
 
-template <typename T, bool GATED>
-__global__ void __launch_bounds__(64) scan_bwd_kernel(ScanArgs a) {
-  const i64 ch = (i64)blockIdx.x * 64 + threadIdx.x, s = blockIdx.y;
-  if (ch >= a.D) return;
-  const DeltaSpan sp = a.seq.span(s);
-  const float rate = GATED ? decay_rate(a.c, a.decay[ch]) : 0.0f;
-  float carry = a.dh_final ? a.dh_final[s * a.D + ch] : 0.0f, sum = 0.0f;
-  for (i64 j = (sp.len + DCH - 1) / DCH - 1; j >= 0; --j) {
-    const int n = (int)(sp.len - j * DCH < DCH ? sp.len - j * DCH : DCH);
-    float prev[DCH], x;
-    float h = a.kept[(sp.slot0 + j) * a.D + ch];
-    for (int t = 0; t < n; ++t) {
-      prev[t] = h;
-      const Token k = load_token<T, GATED>(a, (sp.start + j * DCH + t) * a.D + ch, rate, x);
-      h = fmaf(k.a, h, k.u);
+struct Pair {
+  float A, H;
+};
+
+// Everything between a workgroup's segments and its sequence's other tiles.  Waves are numbered `w` in the order of
+// the recurrence (REV: the last rows first), tiles `k` likewise.
+template <int V>
+struct Chain {
+  Pair (*seg)[V][64];   // [NW]: the waves' segments
+  Pair (*look)[V][64];  // [NW]: what the waves found of the tiles before
+  float (*base)[64];    // the state behind the group before
+
+  // the state before this wave's rows.  first: the state before the sequence.  total: the state behind this tile (the
+  // last wave's only)
+  __device__ __forceinline__ void enter(const ScanArgs& a, i64 slot, int step, i64 k, i64 n, int w, int lane, i64 ch0,
+                                        unsigned coff, bool mine, const float (&first)[V], float (&h)[V]) {
+    // (1) this tile's pair; the last tile's is not needed, and a group's last one publishes a state instead
+    const int back = (int)(k % GROUP);
+    if (w == 0 && k + 1 < n && back != GROUP - 1) {
+#pragma unroll
+      for (int v = 0; v < V; ++v) {
+        Pair t = seg[0][v][lane];
+#pragma unroll
+        for (int i = 1; i < NW; ++i) {
+          const Pair s = seg[i][v][lane];
+          t.H = apply(s.A, t.H, s.H);
+          t.A *= s.A;
+        }
+        if (mine) put_pair(a.pairs + slot * a.D + ch0 + coff + v, t.A, t.H);
+      }
     }
-    for (int t = n - 1; t >= 0; --t) {
-      const i64 e = (sp.start + j * DCH + t) * a.D + ch;
-      const Token k = load_token<T, GATED>(a, e, rate, x);
-      const float l = ld((const T*)a.dh, e) + carry;
-      carry = k.a * l;
+    // (2) the tiles before it in its group, two per wave; and the state behind the group before
+    if (k > 0) {
+      Pair f[V];
+#pragma unroll
+      for (int v = 0; v < V; ++v) f[v] = {1.0f, 0.0f};
+      constexpr int EACH = GROUP / NW;
+#pragma unroll
+      for (int i = 0; i < EACH; ++i) {
+        const int b = w * EACH + i;
+        if (b < back) {
+          const u64* p = a.pairs + (slot - (i64)step * (back - b)) * a.D + ch0 + coff;
+#pragma unroll
+          for (int v = 0; v < V; ++v) {
+            const u64 q = await<u64, NO_PAIR>(p + v);
+            const float A = __uint_as_float((unsigned)q);
+            f[v].H = apply(A, f[v].H, __uint_as_float((unsigned)(q >> 32)));
+            f[v].A *= A;
+          }
+        }
+      }
+#pragma unroll
+      for (int v = 0; v < V; ++v) look[w][v][lane] = f[v];
+      if (w == NW - 1 && k >= GROUP) {
+        const unsigned* p = a.states + (slot - (i64)step * (back + 1)) / GROUP * a.D + ch0 + coff;
+#pragma unroll
+        for (int v = 0; v < V; ++v) base[v][lane] = __uint_as_float(await<unsigned, NO_STATE>(p + v));
+      }
+      __syncthreads();
+    }
+    // (3) in order
+#pragma unroll
+    for (int v = 0; v < V; ++v) {
+      h[v] = k >= GROUP ? base[v][lane] : first[v];
+      if (k > 0)
+        for (int i = 0; i < NW; ++i) h[v] = apply(look[i][v][lane].A, h[v], look[i][v][lane].H);
+      for (int i = 0; i < w; ++i) h[v] = apply(seg[i][v][lane].A, h[v], seg[i][v][lane].H);
+    }
+  }
+  // the state behind the last wave's rows, where a group ends
+  __device__ __forceinline__ void leave(const ScanArgs& a, i64 slot, i64 k, i64 n, int w, i64 ch0, unsigned coff, bool mine,
+                                        const float (&h)[V]) {
+    if (w == NW - 1 && k + 1 < n && k % GROUP == GROUP - 1 && mine)
+#pragma unroll
+      for (int v = 0; v < V; ++v) put_state(a.states + slot / GROUP * a.D + ch0 + coff + v, h[v]);
+  }
+};
+
+template <int N, bool REV>
+__device__ __forceinline__ bool take_tile(const ScanArgs& a, int lane, unsigned* shared, Tile& t, int& slab) {
+  unsigned o = blockIdx.x;
+  if (a.chain) {
+    if (threadIdx.x == 0) *shared = __hip_atomic_fetch_add(a.ticket, 1u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+    __syncthreads();
+    o = (unsigned)__builtin_amdgcn_readfirstlane((int)*shared);
+  }
+  const unsigned i = o / (unsigned)a.nslab;
+  slab = (int)(o - i * (unsigned)a.nslab);
+  return find_tile<N, REV>(a, i, lane, t);
+}
+
+template <typename T, bool GATED, int V>
+__global__ void __launch_bounds__(64 * NW) scan_fwd_kernel(ScanArgs a) {
+  constexpr int R = FWD_ROWS, N = R * NW;
+  __shared__ Pair seg[NW][V][64], look[NW][V][64];
+  __shared__ float base[V][64];
+  __shared__ unsigned number;
+  const int lane = threadIdx.x & 63, w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  Tile t;
+  int slab;
+  if (!take_tile<N, false>(a, lane, &number, t, slab)) return;
+  const i64 ch0 = (i64)slab * 64 * V, t0 = t.j * N + w * R;
+  const bool mine = ch0 + lane * V < a.D;
+  const unsigned coff = mine ? lane * V : 0;
+  const int rows = t0 >= t.len ? 0 : t.len - t0 < R ? (int)(t.len - t0) : R;
+  const i64 at = (t.start + t0) * a.D + ch0;
+
+  float A[R][V], U[R][V];  // per row: products of a and states from the segment's start on
+  typedef Raw<T, V> raw;
+  typedef Raw<float, V> rawf;
+  float first[V], rate[V];
+#pragma unroll
+  for (int v = 0; v < V; ++v) {
+    first[v] = a.h0 ? a.h0[t.seq * a.D + ch0 + coff + v] : 0.0f;
+    if constexpr (GATED) rate[v] = a.decay[ch0 + coff + v];
+  }
+  auto scan = [&](auto full) {
+    raw x[R], r[GATED ? R : 1], ig[GATED ? R : 1];
+    rawf g[GATED ? 1 : R];
+#pragma unroll
+    for (int i = 0; i < R; ++i) {
+      const i64 e = at + (i64)(full || i < rows ? i : rows - 1) * a.D;
       if constexpr (GATED) {
-        const float lm = l * k.m * k.w, E = l * (k.w * x * k.a * k.a * (k.L * k.rm) - k.L * k.a * prev[t]);
-        st((T*)a.dx, e, lm);
-        st((T*)a.digate, e, lm * x * (1.0f - k.w));
-        st((T*)a.dgate, e, E * (1.0f - k.sr));
-        sum += E;
+        r[i] = load_raw<T, V>((const T*)a.gate + e, coff);
+        ig[i] = load_raw<T, V>((const T*)a.igate + e, coff);
       } else {
-        st((T*)a.dx, e, l);
-        ((float*)a.dgate)[e] = carry * prev[t];
+        g[i] = load_raw<float, V>((const float*)a.gate + e, coff);
+      }
+      x[i] = load_raw<T, V>((const T*)a.x + e, coff);
+    }
+    if constexpr (GATED)
+#pragma unroll
+      for (int v = 0; v < V; ++v) rate[v] = decay_rate(a.c, rate[v]);
+#pragma unroll
+    for (int i = 0; i < R; ++i)
+#pragma unroll
+      for (int v = 0; v < V; ++v) {
+        float ai, u;
+        if constexpr (GATED) {
+          const Token k = gated_token((float)x[i].v[v], (float)r[i].v[v], (float)ig[i].v[v], rate[v]);
+          ai = k.a;
+          u = k.u;
+        } else {
+          ai = exp_hw(g[i].v[v]);
+          u = (float)x[i].v[v];
+        }
+        if (!full && i >= rows) ai = 1.0f, u = 0.0f;
+        A[i][v] = i ? A[i - 1][v] * ai : ai;
+        U[i][v] = fmaf(ai, i ? U[i - 1][v] : 0.0f, u);
+      }
+  };
+  if (rows == R) {
+    scan(std::true_type{});
+  } else if (rows > 0) {
+    scan(std::false_type{});
+  } else {
+#pragma unroll
+    for (int i = 0; i < R; ++i)
+#pragma unroll
+      for (int v = 0; v < V; ++v) A[i][v] = 1.0f, U[i][v] = 0.0f;
+  }
+#pragma unroll
+  for (int v = 0; v < V; ++v) seg[w][v][lane] = {A[R - 1][v], U[R - 1][v]};
+  __syncthreads();
+  float h[V], last[V];
+  Chain<V> chain{seg, look, base};
+  chain.enter(a, t.slot, 1, t.j, t.n, w, lane, ch0, coff, mine, first, h);
+#pragma unroll
+  for (int v = 0; v < V; ++v) last[v] = apply(A[R - 1][v], h[v], U[R - 1][v]);
+  chain.leave(a, t.slot, t.j, t.n, w, ch0, coff, mine, last);
+  if (!mine) return;
+  if (a.h)
+#pragma unroll
+    for (int i = 0; i < R; ++i)
+      if (i < rows) {
+        float o[V];
+#pragma unroll
+        for (int v = 0; v < V; ++v) o[v] = apply(A[i][v], h[v], U[i][v]);
+        store_raw((T*)a.h + at + (i64)i * a.D, coff, o);
+      }
+  if (a.ckpt && rows > 0 && w * R % DCH == 0) {
+    const i64 row = (a.off ? t.start / DCH + t.seq : t.seq * ((a.T + DCH - 1) / DCH)) + t0 / DCH;
+#pragma unroll
+    for (int v = 0; v < V; ++v) a.ckpt[row * a.D + ch0 + coff + v] = h[v];
+  }
+  if (a.h_final && w == NW - 1 && t.j == t.n - 1)
+#pragma unroll
+    for (int v = 0; v < V; ++v) a.h_final[t.seq * a.D + ch0 + coff + v] = last[v];
+}
+
+// A wave's rows: forward from the state before the tile (kept by the forward pass), backward from the gradient of the
+// state behind it.  b_t = a_t l_t, the gradient that reaches h_{t-1}, obeys b_t = a_t b_{t+1} + a_t dh_t.
+template <typename T, bool GATED, int V>
+__global__ void __launch_bounds__(64 * NW) scan_bwd_kernel(ScanArgs a) {
+  constexpr int R = BWD_ROWS, N = R * NW;
+  static_assert(N == DCH, "a tile of the backward starts at a kept state");
+  __shared__ Pair seg[NW][V][64], look[NW][V][64], fseg[NW][V][64];
+  __shared__ float base[V][64];
+  __shared__ unsigned number;
+  const int lane = threadIdx.x & 63, w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  Tile t;
+  int slab;
+  if (!take_tile<N, true>(a, lane, &number, t, slab)) {
+    // a slot without tokens has no part in the sum over the tokens
+    const i64 ch = (i64)slab * 64 * V + threadIdx.x;
+    if (GATED && threadIdx.x < 64 * V && ch < a.D) a.part[t.slot * a.D + ch] = 0.0f;
+    return;
+  }
+  const i64 ch0 = (i64)slab * 64 * V, t0 = t.j * N + w * R;
+  const bool mine = ch0 + lane * V < a.D;
+  const unsigned coff = mine ? lane * V : 0;
+  const int rows = t0 >= t.len ? 0 : t.len - t0 < R ? (int)(t.len - t0) : R;
+  const i64 at = (t.start + t0) * a.D + ch0;
+  typedef Raw<T, V> raw;
+  raw x[R], dh[R];
+  float ai[R][V], u[R][V];                                                            // h = ai h + u
+  float sr[GATED ? R : 1][V], wi[GATED ? R : 1][V], m[GATED ? R : 1][V], rm[GATED ? R : 1][V];
+  float first[V], rate[V], hin[V];
+#pragma unroll
+  for (int v = 0; v < V; ++v) {
+    first[v] = a.dh_final ? a.dh_final[t.seq * a.D + ch0 + coff + v] : 0.0f;
+    hin[v] = a.kept[t.slot * a.D + ch0 + coff + v];
+    if constexpr (GATED) rate[v] = a.decay[ch0 + coff + v];
+  }
+  auto load = [&](auto full) {
+    raw r[GATED ? R : 1], ig[GATED ? R : 1];
+    Raw<float, V> g[GATED ? 1 : R];
+#pragma unroll
+    for (int i = 0; i < R; ++i) {
+      const i64 e = at + (i64)(full || i < rows ? i : rows - 1) * a.D;
+      if constexpr (GATED) {
+        r[i] = load_raw<T, V>((const T*)a.gate + e, coff);
+        ig[i] = load_raw<T, V>((const T*)a.igate + e, coff);
+      } else {
+        g[i] = load_raw<float, V>((const float*)a.gate + e, coff);
+      }
+      x[i] = load_raw<T, V>((const T*)a.x + e, coff);
+      dh[i] = load_raw<T, V>((const T*)a.dh + e, coff);
+    }
+    if constexpr (GATED)
+#pragma unroll
+      for (int v = 0; v < V; ++v) rate[v] = decay_rate(a.c, rate[v]);
+#pragma unroll
+    for (int i = 0; i < R; ++i)
+#pragma unroll
+      for (int v = 0; v < V; ++v) {
+        if constexpr (GATED) {
+          const Token k = gated_token((float)x[i].v[v], (float)r[i].v[v], (float)ig[i].v[v], rate[v]);
+          ai[i][v] = k.a; u[i][v] = k.u; sr[i][v] = k.sr; wi[i][v] = k.w; m[i][v] = k.m; rm[i][v] = k.rm;
+        } else {
+          ai[i][v] = exp_hw(g[i].v[v]);
+          u[i][v] = (float)x[i].v[v];
+        }
+        if (!full && i >= rows) ai[i][v] = 1.0f, u[i][v] = 0.0f, dh[i].v[v] = (T)0.0f;
+      }
+  };
+  if (rows == R) {
+    load(std::true_type{});
+  } else if (rows > 0) {
+    load(std::false_type{});
+  } else {
+#pragma unroll
+    for (int i = 0; i < R; ++i)
+#pragma unroll
+      for (int v = 0; v < V; ++v) {
+        ai[i][v] = 1.0f; u[i][v] = 0.0f; x[i].v[v] = dh[i].v[v] = (T)0.0f;
+        if constexpr (GATED) sr[i][v] = wi[i][v] = m[i][v] = rm[i][v] = 0.0f;
+      }
+  }
+  const int wr = NW - 1 - w;  // the waves in the order of the adjoint
+#pragma unroll
+  for (int v = 0; v < V; ++v) {
+    float A = 1.0f, H = 0.0f, B = 0.0f;
+#pragma unroll
+    for (int i = 0; i < R; ++i) {
+      A *= ai[i][v];
+      H = fmaf(ai[i][v], H, u[i][v]);
+    }
+#pragma unroll
+    for (int i = R - 1; i >= 0; --i) B = ai[i][v] * (B + (float)dh[i].v[v]);
+    fseg[w][v][lane] = {A, H};
+    seg[wr][v][lane] = {A, B};
+  }
+  __syncthreads();
+  float b[V];
+  Chain<V> chain{seg, look, base};
+  const i64 k = t.n - 1 - t.j;
+  chain.enter(a, t.slot, -1, k, t.n, wr, lane, ch0, coff, mine, first, b);
+  float sum[V];
+#pragma unroll
+  for (int v = 0; v < V; ++v) {
+    float h = hin[v];
+    for (int i = 0; i < w; ++i) h = apply(fseg[i][v][lane].A, h, fseg[i][v][lane].H);
+    // u becomes h_{t-1}
+#pragma unroll
+    for (int i = 0; i < R; ++i) {
+      const float n = fmaf(ai[i][v], h, u[i][v]);
+      u[i][v] = h;
+      h = n;
+    }
+    sum[v] = 0.0f;
+  }
+#pragma unroll
+  for (int i = R - 1; i >= 0; --i) {
+    float ox[V], og[V], oi[V];
+#pragma unroll
+    for (int v = 0; v < V; ++v) {
+      const float l = (float)dh[i].v[v] + b[v], prev = u[i][v];
+      b[v] = ai[i][v] * l;
+      if constexpr (GATED) {
+        const float L = rate[v] * sr[i][v], xv = (float)x[i].v[v], lm = l * m[i][v] * wi[i][v];
+        const float E = l * (wi[i][v] * xv * ai[i][v] * ai[i][v] * (L * rm[i][v]) - L * ai[i][v] * prev);
+        ox[v] = lm;
+        oi[v] = lm * xv * (1.0f - wi[i][v]);
+        og[v] = E * (1.0f - sr[i][v]);
+        if (i < rows) sum[v] += E;
+      } else {
+        ox[v] = l;
+        og[v] = b[v] * prev;
+      }
+    }
+    if (i < rows && mine) {
+      const i64 e = at + (i64)i * a.D;
+      store_raw((T*)a.dx + e, coff, ox);
+      if constexpr (GATED) {
+        store_raw((T*)a.dgate + e, coff, og);
+        store_raw((T*)a.digate + e, coff, oi);
+      } else {
+        store_raw((float*)a.dgate + e, coff, og);
       }
     }
   }
-  if (GATED) a.part[s * a.D + ch] = sum;
-  if (a.dh0) a.dh0[s * a.D + ch] = carry;
+  chain.leave(a, t.slot, k, t.n, wr, ch0, coff, mine, b);
+  if (a.dh0 && w == 0 && t.j == 0 && mine)
+#pragma unroll
+    for (int v = 0; v < V; ++v) a.dh0[t.seq * a.D + ch0 + coff + v] = b[v];
+  if constexpr (GATED) {
+    // fseg and look are read no more behind this barrier
+    __syncthreads();
+    float(*sums)[V][64] = (float(*)[V][64])fseg;
+#pragma unroll
+    for (int v = 0; v < V; ++v) sums[w][v][lane] = sum[v];
+    __syncthreads();
+    if (w == 0 && mine)
+#pragma unroll
+      for (int v = 0; v < V; ++v) {
+        float s = sums[0][v][lane];
+#pragma unroll
+        for (int i = 1; i < NW; ++i) s += sums[i][v][lane];
+        a.part[t.slot * a.D + ch0 + coff + v] = s;
+      }
+  }
 }
 
-__global__ void __launch_bounds__(64) decay_sum_kernel(const float* part, i64 n, i64 D, const float* decay, float* out) {
-  const i64 ch = (i64)blockIdx.x * 64 + threadIdx.x;
-  if (ch >= D) return;
+// Before a call whose tiles wait for each other: the filling of what they publish, and the counter.  Sequences without
+// tokens, which have no tile: their final state (`to`) is their first (`from`).  Rows of ckpt that no token has: zeros.
+__global__ void __launch_bounds__(256) scan_init_kernel(u64* pairs, i64 words, unsigned* ticket, const int* off, i64 nseq,
+                                                        i64 T, i64 D, const float* from, float* to, float* clear, i64 nclear) {
+  const i64 i0 = (i64)blockIdx.x * 256 + threadIdx.x, step = (i64)gridDim.x * 256;
+  if (ticket && i0 == 0) *ticket = 0u;
+  for (i64 i = i0; i < words; i += step) pairs[i] = NO_PAIR;
+  for (i64 i = i0; i < nclear; i += step) clear[i] = 0.0f;
+  if (!to) return;
+  for (i64 i = i0; i < nseq * D; i += step) {
+    const i64 s = i / D;
+    bool empty = T == 0;
+    if (off) {
+      const i64 o0 = off[s] < 0 ? 0 : off[s] > T ? T : off[s], o1 = off[s + 1] < 0 ? 0 : off[s + 1] > T ? T : off[s + 1];
+      empty = o1 <= o0;
+    }
+    if (empty) to[i] = from ? from[i] : 0.0f;
+  }
+}
+
+// ddecay = slope * sum over the tiles: 16 runs of tiles per channel, each in order, then the runs in order
+__global__ void __launch_bounds__(1024) decay_sum_kernel(const float* part, i64 n, i64 D, const float* decay, float* out) {
+  __shared__ float runs[16][64];
+  const i64 ch = (i64)blockIdx.x * 64 + (threadIdx.x & 63), each = (n + 15) / 16;
+  const int run = threadIdx.x >> 6;
   float sum = 0.0f;
-  for (i64 i = 0; i < n; ++i) sum += part[i * D + ch];
+  if (ch < D)
+    for (i64 i = run * each; i < n && i < (run + 1) * each; ++i) sum += part[i * D + ch];
+  runs[run][threadIdx.x & 63] = sum;
+  __syncthreads();
+  if (run || ch >= D) return;
+  for (int i = 1; i < 16; ++i) sum += runs[i][threadIdx.x];
   out[ch] = n > 0 ? sum * decay_slope(decay[ch]) : 0.0f;
-}
-
-// rows of ckpt that no token has
-__global__ void __launch_bounds__(64) ckpt_clear_kernel(float* ckpt, i64 n) {
-  for (i64 i = (i64)blockIdx.x * 64 + threadIdx.x; i < n; i += (i64)gridDim.x * 64) ckpt[i] = 0.0f;
 }
 
 struct StepArgs {
@@ -180,66 +635,127 @@ __global__ void __launch_bounds__(256) scan_step_kernel(StepArgs a) {
   st((T*)a.h, e, h);
 }
 
-DeltaSeqs scan_seqs(const ssmvjp_linear_scan_desc& d, const int* off) {
-  return {d.packed ? off : nullptr, d.batch, d.seqlen, (d.seqlen + DCH - 1) / DCH};
+// ---------------------------------------------------------------------------
+// host
+// ---------------------------------------------------------------------------
+i64 tile_slots(const ssmvjp_linear_scan_desc& d, int n) {
+  return d.packed ? d.seqlen / n + d.batch : d.batch * ((d.seqlen + n - 1) / n);
+}
+// a sequence may have more than one tile
+bool chained(const ssmvjp_linear_scan_desc& d, int n) { return d.seqlen > n; }
+
+i64 round64(i64 n) { return (n + 63) / 64 * 64; }
+// words of 8 bytes: the pairs, the states, the counter
+i64 chain_words(const ssmvjp_linear_scan_desc& d, int n) {
+  if (!chained(d, n)) return 0;
+  const i64 slots = tile_slots(d, n);
+  return slots * d.dim + ((slots / GROUP + 1) * d.dim + 1) / 2 + 32;
+}
+
+void set_chain(const ssmvjp_linear_scan_desc& d, int n, void* workspace, ScanArgs& a) {
+  a.ntiles = tile_slots(d, n);
+  a.per = (d.seqlen + n - 1) / n;
+  a.chain = chained(d, n);
+  if (!a.chain) return;
+  a.pairs = (u64*)workspace;
+  a.states = (unsigned*)(a.pairs + a.ntiles * d.dim);
+  a.ticket = (unsigned*)(a.pairs + chain_words(d, n) - 1);
+}
+
+void launch_init(const ScanArgs& a, i64 words, const float* from, float* to, float* clear, i64 nclear, hipStream_t s) {
+  if (words <= 0 && !to && nclear <= 0) return;
+  i64 most = words > nclear ? words : nclear;
+  if (to && a.nseq * a.D > most) most = a.nseq * a.D;
+  const i64 blocks = (most + 1023) / 1024 < 2048 ? (most + 1023) / 1024 : 2048;
+  hipLaunchKernelGGL(scan_init_kernel, dim3((unsigned)(blocks > 0 ? blocks : 1)), dim3(256), 0, s, a.pairs, words > 0 ? words - 1 : 0,
+                     a.ticket, a.off, a.nseq, a.T, a.D, from, to, clear, nclear);
+}
+
+template <typename T, bool GATED, int V, bool BWD>
+void launch_tiles(ScanArgs& a, hipStream_t s) {
+  a.nslab = (int)((a.D + 64 * V - 1) / (64 * V));
+  const dim3 grid((unsigned)(a.ntiles * a.nslab));
+  if constexpr (BWD) hipLaunchKernelGGL((scan_bwd_kernel<T, GATED, V>), grid, dim3(64 * NW), 0, s, a);
+  else hipLaunchKernelGGL((scan_fwd_kernel<T, GATED, V>), grid, dim3(64 * NW), 0, s, a);
+}
+
+// Two channels per lane where every row starts at a multiple of two elements: 4 bytes of bf16 a load.
+template <typename T, bool GATED, bool BWD>
+void launch_wide(ScanArgs& a, hipStream_t s) {
+  const void* big[] = {a.x, a.igate, a.h, a.dh, a.dx, a.digate};
+  const void* gates[] = {a.gate, a.dgate};
+  bool two = a.D % 2 == 0;
+  for (const void* p : big) two &= (uintptr_t)p % (2 * sizeof(T)) == 0;
+  for (const void* p : gates) two &= (uintptr_t)p % (2 * (GATED ? sizeof(T) : 4)) == 0;
+  if (two) launch_tiles<T, GATED, 2, BWD>(a, s);
+  else launch_tiles<T, GATED, 1, BWD>(a, s);
+}
+
+template <bool BWD>
+void launch_scan(const ssmvjp_linear_scan_desc& d, ScanArgs& a, hipStream_t s) {
+  if (a.ntiles == 0 || d.seqlen == 0) return;
+  const bool gated = d.form == SSMVJP_SCAN_GATED;
+  if (d.dtype == SSMVJP_BF16) gated ? launch_wide<bf16, true, BWD>(a, s) : launch_wide<bf16, false, BWD>(a, s);
+  else gated ? launch_wide<float, true, BWD>(a, s) : launch_wide<float, false, BWD>(a, s);
+}
+
+ScanArgs scan_args(const ssmvjp_linear_scan_desc& d, const int* off) {
+  ScanArgs a{};
+  a.off = d.packed ? off : nullptr;
+  a.nseq = d.batch; a.T = d.seqlen; a.D = d.dim; a.c = d.c;
+  return a;
 }
 
 }  // namespace
 
-int64_t linear_scan_ckpt_rows(const ssmvjp_linear_scan_desc& d) {
-  return d.packed ? d.seqlen / DCH + d.batch : d.batch * ((d.seqlen + DCH - 1) / DCH);
+int64_t linear_scan_ckpt_rows(const ssmvjp_linear_scan_desc& d) { return tile_slots(d, DCH); }
+
+size_t linear_scan_fwd_workspace_bytes(const ssmvjp_linear_scan_desc& d) {
+  return (size_t)(8 * round64(chain_words(d, FWD_ROWS * NW)));
 }
 
-size_t linear_scan_fwd_workspace_bytes(const ssmvjp_linear_scan_desc&) { return 0; }
-
+// the tiles' words (those of the forward pass for the states, then the backward's), partial sums of ddecay, states
 size_t linear_scan_bwd_workspace_bytes(const ssmvjp_linear_scan_desc& d) {
-  return (size_t)(4 * (linear_scan_ckpt_rows(d) + d.batch) * d.dim);
+  const i64 f = chain_words(d, FWD_ROWS * NW), b = chain_words(d, BWD_ROWS * NW);
+  return (size_t)(8 * round64(f > b ? f : b) + 8 * linear_scan_ckpt_rows(d) * d.dim);
 }
 
 hipError_t launch_linear_scan_fwd(const ssmvjp_linear_scan_desc& d, const LinearScanPointers& p, hipStream_t stream) {
-  ScanArgs a{};
-  a.seq = scan_seqs(d, p.seq_offsets);
-  a.D = d.dim; a.c = d.c; a.x = p.x; a.gate = p.gate; a.igate = p.input_gate; a.decay = p.decay; a.h0 = p.h0;
+  constexpr int N = FWD_ROWS * NW;
+  ScanArgs a = scan_args(d, p.seq_offsets);
+  a.x = p.x; a.gate = p.gate; a.igate = p.input_gate; a.decay = p.decay; a.h0 = p.h0;
   a.h = p.h; a.h_final = p.h_final; a.ckpt = p.ckpt;
-  if (p.ckpt && linear_scan_ckpt_rows(d) > 0) hipLaunchKernelGGL(ckpt_clear_kernel, dim3(1024), dim3(64), 0, stream, p.ckpt, linear_scan_ckpt_rows(d) * d.dim);
-  const dim3 grid((unsigned)((d.dim + 63) / 64), (unsigned)d.batch);
-  const bool gated = d.form == SSMVJP_SCAN_GATED;
-  if (d.dtype == SSMVJP_BF16) {
-    if (gated) hipLaunchKernelGGL((scan_fwd_kernel<bf16, true>), grid, dim3(64), 0, stream, a);
-    else hipLaunchKernelGGL((scan_fwd_kernel<bf16, false>), grid, dim3(64), 0, stream, a);
-  } else {
-    if (gated) hipLaunchKernelGGL((scan_fwd_kernel<float, true>), grid, dim3(64), 0, stream, a);
-    else hipLaunchKernelGGL((scan_fwd_kernel<float, false>), grid, dim3(64), 0, stream, a);
-  }
+  set_chain(d, N, p.workspace, a);
+  const bool gaps = d.packed || d.seqlen == 0;  // sequences without tokens, rows of ckpt without one
+  launch_init(a, chain_words(d, N), p.h0, gaps ? p.h_final : nullptr, d.packed ? p.ckpt : nullptr,
+              d.packed && p.ckpt ? linear_scan_ckpt_rows(d) * d.dim : 0, stream);
+  launch_scan<false>(d, a, stream);
   return hipGetLastError();
 }
 
 hipError_t launch_linear_scan_bwd(const ssmvjp_linear_scan_desc& d, const LinearScanBwdPointers& p, hipStream_t stream) {
-  float* states = (float*)p.workspace;
-  float* part = states + linear_scan_ckpt_rows(d) * d.dim;
+  constexpr int N = BWD_ROWS * NW;
+  const i64 f = chain_words(d, FWD_ROWS * NW), b = chain_words(d, N), rows = linear_scan_ckpt_rows(d);
+  float* part = (float*)((u64*)p.workspace + round64(f > b ? f : b));
+  float* states = part + rows * d.dim;
   const bool gated = d.form == SSMVJP_SCAN_GATED;
   if (d.batch > 0) {
-    if (!p.ckpt) {
-      const LinearScanPointers f{p.x, p.gate, p.input_gate, p.decay, p.h0, p.seq_offsets, nullptr, nullptr, states, nullptr};
-      const hipError_t e = launch_linear_scan_fwd(d, f, stream);
+    if (!p.ckpt && d.seqlen > 0) {
+      const LinearScanPointers fwd{p.x, p.gate, p.input_gate, p.decay, p.h0, p.seq_offsets, nullptr, nullptr, states, p.workspace};
+      const hipError_t e = launch_linear_scan_fwd(d, fwd, stream);
       if (e != hipSuccess) return e;
     }
-    ScanArgs a{};
-    a.seq = scan_seqs(d, p.seq_offsets);
-    a.D = d.dim; a.c = d.c; a.x = p.x; a.gate = p.gate; a.igate = p.input_gate; a.decay = p.decay; a.h0 = p.h0;
+    ScanArgs a = scan_args(d, p.seq_offsets);
+    a.x = p.x; a.gate = p.gate; a.igate = p.input_gate; a.decay = p.decay; a.h0 = p.h0;
     a.kept = p.ckpt ? p.ckpt : states; a.dh = p.dh; a.dh_final = p.dh_final;
     a.dx = p.dx; a.dgate = p.dgate; a.digate = p.dinput_gate; a.part = part; a.dh0 = p.dh0;
-    const dim3 grid((unsigned)((d.dim + 63) / 64), (unsigned)d.batch);
-    if (d.dtype == SSMVJP_BF16) {
-      if (gated) hipLaunchKernelGGL((scan_bwd_kernel<bf16, true>), grid, dim3(64), 0, stream, a);
-      else hipLaunchKernelGGL((scan_bwd_kernel<bf16, false>), grid, dim3(64), 0, stream, a);
-    } else {
-      if (gated) hipLaunchKernelGGL((scan_bwd_kernel<float, true>), grid, dim3(64), 0, stream, a);
-      else hipLaunchKernelGGL((scan_bwd_kernel<float, false>), grid, dim3(64), 0, stream, a);
-    }
+    set_chain(d, N, p.workspace, a);
+    launch_init(a, b, p.dh_final, d.packed || d.seqlen == 0 ? p.dh0 : nullptr, nullptr, 0, stream);
+    launch_scan<true>(d, a, stream);
   }
   if (gated)
-    hipLaunchKernelGGL(decay_sum_kernel, dim3((unsigned)((d.dim + 63) / 64)), dim3(64), 0, stream, part, d.batch, d.dim, p.decay, p.ddecay);
+    hipLaunchKernelGGL(decay_sum_kernel, dim3((unsigned)((d.dim + 63) / 64)), dim3(1024), 0, stream, part, d.batch > 0 && d.seqlen > 0 ? rows : 0,
+                       d.dim, p.decay, p.ddecay);
   return hipGetLastError();
 }
 
