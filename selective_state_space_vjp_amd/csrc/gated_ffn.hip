@@ -9,6 +9,7 @@
 // k runs along the rows of an operand in memory (KC) or down its columns.
 #include "common.cuh"
 #include "kernels.h"
+#include "lds_dma.cuh"
 
 namespace ssmvjp {
 namespace {
@@ -51,91 +52,252 @@ __device__ __forceinline__ float act_of(float z) {
   return f;
 }
 
-constexpr int TM = 64, TN = 64, TK = 32;
+// ---------------------------------------------------------------------------
+// Tiles.  A workgroup forms BM x BN values of C; every step of its loop brings
+// 128 bytes of k (64 values of bf16, 32 of float32) of both operands into one
+// of two buffers in LDS by LDS-direct loads while the other is multiplied.
+//
+// In LDS a tile lies as in memory, in 16-byte chunks: rows of 8 chunks (KC: a
+// row is one m or n), or rows of BM or BN values (a row is one k).  Chunk p of
+// row r holds the row's chunk p ^ swizzle(r), which spreads the rows that one
+// read touches over the banks; the loads write LDS in order, so it is the
+// addresses in memory that are permuted.
+//
+// The products run with the roles of A and B exchanged, which leaves a lane
+// with four consecutive n of one m.
+// ---------------------------------------------------------------------------
+typedef bf16 bf16x8 __attribute__((ext_vector_type(8)));
+constexpr int ROWB = 128;  // bytes of k per step
 
-// TMN x TK values of an operand into LDS, [mn][k] (KC) or [k][mn]; zeros outside
+template <typename T>
+struct Fragment;  // 16 values of m or n, half a step of k
+template <>
+struct Fragment<bf16> {
+  bf16x8 v;
+};
+template <>
+struct Fragment<float> {
+  f32x4 v;
+};
+
+__device__ __forceinline__ void multiply(f32x4& d, const Fragment<bf16>& a, const Fragment<bf16>& b) {
+  d = __builtin_amdgcn_mfma_f32_16x16x32_bf16(a.v, b.v, d, 0, 0, 0);
+}
+__device__ __forceinline__ void multiply(f32x4& d, const Fragment<float>& a, const Fragment<float>& b) {
+#pragma unroll
+  for (int j = 0; j < 4; ++j) d = __builtin_amdgcn_mfma_f32_16x16x4f32(a.v[j], b.v[j], d, 0, 0, 0);
+}
+
+template <typename T, bool KC, int MN>
+struct TileOf {
+  static constexpr int CPR = KC ? ROWB / 16 : MN * (int)sizeof(T) / 16;  // chunks of a row
+  static constexpr int ROWS = KC ? MN : ROWB / (int)sizeof(T);
+  static constexpr int BYTES = MN * ROWB;
+  static __device__ __forceinline__ int swizzle(int r) {
+    if constexpr (KC) return r & 7;
+    else if constexpr (sizeof(T) == 2) return (((r & 3) | ((r >> 3) & 3) << 2) << 1) & (CPR - 1);
+    else return ((r >> 2) & 3) << 2;
+  }
+  // the byte in memory, from the tile's first, that chunk i of LDS holds
+  static __device__ __forceinline__ unsigned source(int i, unsigned ldb) {
+    const int r = i / CPR, p = i % CPR;
+    return r * ldb + ((p ^ swizzle(r)) << 4);
+  }
+  // the k (in values from the step's first) of that chunk's first value
+  static __device__ __forceinline__ int source_k(int i) {
+    const int r = i / CPR, p = i % CPR;
+    return KC ? (p ^ swizzle(r)) * (16 / (int)sizeof(T)) : r;
+  }
+  // values mn .. mn + 15, half `kk` of the step
+  static __device__ __forceinline__ Fragment<T> fragment(const char* lds, int mn, int kk, int lane) {
+    const int q = lane >> 4, c = lane & 15;
+    Fragment<T> f;
+    if constexpr (KC) {
+      const int r = mn + c;
+      f.v = *(const decltype(f.v)*)(lds + r * ROWB + (((q + 4 * kk) ^ swizzle(r)) << 4));
+    } else if constexpr (sizeof(T) == 2) {
+      // two transposing reads of 4 k x 16 values
+      typedef short s16x8 __attribute__((ext_vector_type(8)));
+      s16x4 h[2];
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        const int r = kk * 32 + 8 * q + 4 * i + (c >> 2);
+        const int chunk = ((mn >> 3) + ((c & 3) >> 1)) ^ swizzle(r);
+        h[i] = lds_tr_b16((const bf16*)(lds + r * (CPR * 16) + chunk * 16 + (c & 1) * 8)).v;
+      }
+      f.v = __builtin_bit_cast(bf16x8, (s16x8)__builtin_shufflevector(h[0], h[1], 0, 1, 2, 3, 4, 5, 6, 7));
+    } else {
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const int r = kk * 16 + 4 * q + j;
+        const int chunk = ((mn >> 2) + (c >> 2)) ^ swizzle(r);
+        f.v[j] = *(const float*)(lds + r * (CPR * 16) + chunk * 16 + (c & 3) * 4);
+      }
+    }
+    return f;
+  }
+};
+
+// Where the tile mn0 .. of an operand begins at step k0, and how many bytes behind that may be read: rows of KC past
+// the last m or n, and rows of k past the last, come back as zeros.  Columns past the last m or n reach C there only.
 template <typename T, bool KC>
-__device__ __forceinline__ void stage(T* lds, const Operand& o, i64 mn0, i64 MN, i64 k0, i64 K, int tid) {
-  constexpr int W = 16 / sizeof(T), cols = KC ? TK : TM, rows = KC ? TM : TK, pitch = cols + W;
-  for (int i = tid; i < rows * cols / W; i += 256) {
-    const int r = i / (cols / W), c = i % (cols / W) * W;
-    const i64 gr = (KC ? mn0 : k0) + r, gc = (KC ? k0 : mn0) + c;
-    uint4 v = {0u, 0u, 0u, 0u};
-    if (gr < (KC ? MN : K) && gc < (KC ? K : MN)) v = *(const uint4*)((const T*)o.p + gr * o.ld + gc);
-    *(uint4*)(lds + r * pitch + c) = v;
+__device__ __forceinline__ u32x4 tile_rsrc(const Operand& o, i64 mn0, i64 MN, i64 k0, i64 K, int tile) {
+  constexpr int KB = ROWB / (int)sizeof(T);
+  const i64 r0 = KC ? mn0 : k0, c0 = KC ? k0 : mn0, all = KC ? MN : K;
+  const i64 rows = all - r0 < (KC ? tile : KB) ? all - r0 : (KC ? tile : KB);
+  return rsrc_words_u((const T*)o.p + r0 * o.ld + c0, (unsigned)((rows * o.ld - c0) * (i64)sizeof(T)));
+}
+
+// Tile number -> (m, n).  Workgroups go round the eight XCDs, each with an L2 of its own: an XCD gets a contiguous run
+// of tiles, in bands of 8 tiles of m, so that those it works on at one time share rows of A and of B.
+__device__ __forceinline__ void place(unsigned id, unsigned nm, unsigned nn, unsigned& m, unsigned& n) {
+  const unsigned total = nm * nn, each = total / 8, rest = total % 8, xcd = id % 8;
+  const unsigned t = xcd * each + (xcd < rest ? xcd : rest) + id / 8;
+  const unsigned band = t / (8 * nn), m0 = band * 8, h = nm - m0 < 8 ? nm - m0 : 8, in = t - band * 8 * nn;
+  m = m0 + in % h;
+  n = in / h;
+}
+
+// act(gate) up and what the backward makes of it, four n of one m
+template <typename T>
+__device__ __forceinline__ void store4(void* p, i64 e, const float (&v)[4]) {
+  if constexpr (sizeof(T) == 2) *(uint2*)((bf16*)p + e) = make_uint2(pk_bf16(v[0], v[1]), pk_bf16(v[2], v[3]));
+  else *(float4*)((float*)p + e) = make_float4(v[0], v[1], v[2], v[3]);
+}
+template <typename T>
+__device__ __forceinline__ void fetch4(const void* p, i64 e, float (&v)[4]) {
+  if constexpr (sizeof(T) == 2) {
+    const uint2 u = *(const uint2*)((const bf16*)p + e);
+    v[0] = __uint_as_float(u.x << 16); v[1] = __uint_as_float(u.x & 0xffff0000u);
+    v[2] = __uint_as_float(u.y << 16); v[3] = __uint_as_float(u.y & 0xffff0000u);
+  } else {
+    const float4 u = *(const float4*)((const float*)p + e);
+    v[0] = u.x; v[1] = u.y; v[2] = u.z; v[3] = u.w;
   }
 }
 
-template <typename T, bool KC>
-__device__ __forceinline__ Frag<T> frag_of(const T* lds, int mn, int k, int lane) {
-  constexpr int W = 16 / sizeof(T);
-  if constexpr (KC) return ld_colk(lds, TK + W, mn, k, lane);
-  else return ld_rowk(lds, TM + W, k, mn, lane);
-}
-
-template <typename T, bool AKC, bool BKC, int EPI, int ACT>
-__global__ void __launch_bounds__(256) ffn_gemm_kernel(FfnArgs a) {
+// WM x WN waves.  PAIR: the tile's BN columns are BN/2 of each of two products, side by side in every wave.
+template <typename T, bool AKC, bool BKC, int EPI, int ACT, int BM, int BN, int WM, int WN>
+__global__ void __launch_bounds__(64 * WM * WN) ffn_gemm_kernel(FfnArgs a) {
   constexpr bool PAIR = EPI != EPI_PLAIN;
-  constexpr int LDSN = 64 * 40 > 32 * 72 ? 64 * 40 : 32 * 72;
-  __shared__ __align__(16) T sA[LDSN], sB[PAIR ? 2 : 1][LDSN];
-  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
-  const i64 m0 = (i64)blockIdx.y * TM, n0 = (i64)blockIdx.x * TN;
-  const int wm = (wave & 1) * 32, wn = (wave >> 1) * 32;
-  f32x4 acc[PAIR ? 2 : 1][2][2];
+  constexpr int W = WM * WN, KB = ROWB / (int)sizeof(T), NOUT = PAIR ? BN / 2 : BN;
+  constexpr int FM = BM / WM / 16, FN = BN / WN / 16;
+  typedef TileOf<T, AKC, BM> TA;
+  typedef TileOf<T, BKC, NOUT> TB;
+  constexpr int IA = TA::BYTES / 1024 / W, IB = TB::BYTES / 1024 / W;  // loads of a wave, each product's B by itself
+  constexpr int BUF = TA::BYTES + (PAIR ? 2 : 1) * TB::BYTES;
+  static_assert(IA * 1024 * W == TA::BYTES && IB * 1024 * W == TB::BYTES, "");
+  extern __shared__ __align__(1024) char lds[];
+  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int wm = wave / WN * (BM / WM), wn = wave % WN * (NOUT / WN);
+  unsigned tm, tn;
+  place(blockIdx.x, (unsigned)((a.M + BM - 1) / BM), (unsigned)((a.N + NOUT - 1) / NOUT), tm, tn);
+  const i64 m0 = (i64)tm * BM, n0 = (i64)tn * NOUT;
+  const int steps1 = (int)((a.K + KB - 1) / KB), steps = (PAIR ? 1 : a.segs) * steps1;
+  const unsigned base = lds_base(lds);
+
+  unsigned offA[IA], offB[IB];
 #pragma unroll
-  for (int p = 0; p < (PAIR ? 2 : 1); ++p)
+  for (int i = 0; i < IA; ++i) offA[i] = TA::source((wave * IA + i) * 64 + lane, (unsigned)(a.A[0].ld * sizeof(T)));
 #pragma unroll
-    for (int i = 0; i < 4; ++i) acc[p][i >> 1][i & 1] = zero4();
-  for (int s = 0; s < (PAIR ? 1 : a.segs); ++s)
-    for (i64 k0 = 0; k0 < a.K; k0 += TK) {
-      stage<T, AKC>(sA, a.A[s], m0, a.M, k0, a.K, tid);
-      stage<T, BKC>(sB[0], a.B[s], n0, a.N, k0, a.K, tid);
-      if constexpr (PAIR) stage<T, BKC>(sB[1], a.B[1], n0, a.N, k0, a.K, tid);
-      __syncthreads();
+  for (int i = 0; i < IB; ++i) offB[i] = TB::source((wave * IB + i) * 64 + lane, (unsigned)(a.B[0].ld * sizeof(T)));
+
+  auto load = [&](int step, int buf) {
+    const int s = !PAIR && step >= steps1;
+    const i64 k0 = (i64)(step - s * steps1) * KB;
+    const bool part = k0 + KB > a.K;  // KC: chunks past the last k would be the next row's
+    const unsigned to = base + buf * BUF;
+    const u32x4 ra = tile_rsrc<T, AKC>(a.A[s], m0, a.M, k0, a.K, BM);
 #pragma unroll
-      for (int k = 0; k < TK; k += 16) {
-        Frag<T> fa[2], fb[PAIR ? 2 : 1][2];
-#pragma unroll
-        for (int i = 0; i < 2; ++i) fa[i] = frag_of<T, AKC>(sA, wm + 16 * i, k, lane);
-#pragma unroll
-        for (int p = 0; p < (PAIR ? 2 : 1); ++p)
-#pragma unroll
-          for (int j = 0; j < 2; ++j) fb[p][j] = frag_of<T, BKC>(sB[p], wn + 16 * j, k, lane);
-#pragma unroll
-        for (int p = 0; p < (PAIR ? 2 : 1); ++p)
-#pragma unroll
-          for (int i = 0; i < 2; ++i)
-#pragma unroll
-            for (int j = 0; j < 2; ++j) mma(acc[p][i][j], fa[i], fb[p][j]);
-      }
-      __syncthreads();
+    for (int i = 0; i < IA; ++i) {
+      unsigned off = offA[i];
+      if (AKC && part && k0 + TA::source_k((wave * IA + i) * 64 + lane) >= a.K) off = BUF_OOB;
+      dma_dwordx4(to + (wave * IA + i) * 1024, off, ra);
     }
 #pragma unroll
-  for (int i = 0; i < 2; ++i)
+    for (int p = 0; p < (PAIR ? 2 : 1); ++p) {
+      const u32x4 rb = tile_rsrc<T, BKC>(a.B[PAIR ? p : s], n0, a.N, k0, a.K, NOUT);
 #pragma unroll
-    for (int j = 0; j < 2; ++j)
-#pragma unroll
-      for (int r = 0; r < 4; ++r) {
-        const i64 m = m0 + wm + 16 * i + 4 * (lane >> 4) + r, n = n0 + wn + 16 * j + (lane & 15);
-        if (m >= a.M || n >= a.N) continue;
-        const i64 e = m * a.ldc + n;
-        if constexpr (EPI == EPI_PLAIN) {
-          st((T*)a.C[0], e, acc[0][i][j][r]);
-        } else if constexpr (EPI == EPI_GLU) {
-          const float g = acc[0][i][j][r], u = acc[1][i][j][r];
-          st((T*)a.C[0], e, act_of<ACT>(g) * u);
-          if (a.C[1]) {
-            st((T*)a.C[1], e, g);
-            st((T*)a.C[2], e, u);
-          }
-        } else {
-          float f, df;
-          act_pair<ACT>(acc[0][i][j][r], f, df);
-          const float dh = ld((const T*)a.dh, e);
-          st((T*)a.C[0], e, dh * acc[1][i][j][r] * df);
-          st((T*)a.C[1], e, dh * f);
-        }
+      for (int i = 0; i < IB; ++i) {
+        unsigned off = offB[i];
+        if (BKC && part && k0 + TB::source_k((wave * IB + i) * 64 + lane) >= a.K) off = BUF_OOB;
+        dma_dwordx4(to + TA::BYTES + p * TB::BYTES + (wave * IB + i) * 1024, off, rb);
       }
+    }
+  };
+
+  f32x4 acc[FM][FN];
+#pragma unroll
+  for (int i = 0; i < FM; ++i)
+#pragma unroll
+    for (int j = 0; j < FN; ++j) acc[i][j] = zero4();
+
+  if (steps > 0) load(0, 0);
+  dma_wait();
+  __syncthreads();
+  for (int step = 0; step < steps; ++step) {
+    const char* buf = lds + (step & 1) * BUF;
+    if (step + 1 < steps) load(step + 1, (step + 1) & 1);
+#pragma unroll
+    for (int kk = 0; kk < 2; ++kk) {
+      Fragment<T> fa[FM], fb[FN];
+#pragma unroll
+      for (int j = 0; j < FN; ++j) {
+        constexpr int half = PAIR ? FN / 2 : FN;
+        const int p = j / half;
+        fb[j] = TB::fragment(buf + TA::BYTES + p * TB::BYTES, wn + 16 * (j - p * half), kk, lane);
+      }
+#pragma unroll
+      for (int i = 0; i < FM; ++i) fa[i] = TA::fragment(buf, wm + 16 * i, kk, lane);
+#pragma unroll
+      for (int i = 0; i < FM; ++i)
+#pragma unroll
+        for (int j = 0; j < FN; ++j) multiply(acc[i][j], fb[j], fa[i]);
+    }
+    dma_wait();
+    __syncthreads();
+  }
+
+#pragma unroll
+  for (int i = 0; i < FM; ++i) {
+    const i64 m = m0 + wm + 16 * i + (lane & 15);
+    if (m >= a.M) continue;
+#pragma unroll
+    for (int j = 0; j < (PAIR ? FN / 2 : FN); ++j) {
+      const i64 n = n0 + wn + 16 * j + 4 * (lane >> 4);
+      if (n >= a.N) continue;
+      const i64 e = m * a.ldc + n;
+      float v[3][4];
+      if constexpr (EPI == EPI_PLAIN) {
+#pragma unroll
+        for (int r = 0; r < 4; ++r) v[0][r] = acc[i][j][r];
+        store4<T>(a.C[0], e, v[0]);
+      } else if constexpr (EPI == EPI_GLU) {
+#pragma unroll
+        for (int r = 0; r < 4; ++r) {
+          v[1][r] = acc[i][j][r];
+          v[2][r] = acc[i][j + FN / 2][r];
+          v[0][r] = act_of<ACT>(v[1][r]) * v[2][r];
+        }
+        store4<T>(a.C[0], e, v[0]);
+        if (a.C[1]) {
+          store4<T>(a.C[1], e, v[1]);
+          store4<T>(a.C[2], e, v[2]);
+        }
+      } else {
+        fetch4<T>(a.dh, e, v[2]);
+#pragma unroll
+        for (int r = 0; r < 4; ++r) {
+          float f, df;
+          act_pair<ACT>(acc[i][j][r], f, df);
+          v[0][r] = v[2][r] * acc[i][j + FN / 2][r] * df;
+          v[1][r] = v[2][r] * f;
+        }
+        store4<T>(a.C[0], e, v[0]);
+        store4<T>(a.C[1], e, v[1]);
+      }
+    }
+  }
 }
 
 // dgate, dup from the kept gate and up
@@ -150,10 +312,20 @@ __global__ void __launch_bounds__(256) ffn_grad_kernel(const T* dh, const T* gat
   }
 }
 
+template <typename T, bool AKC, bool BKC, int EPI, int ACT, int BM, int BN, int WM, int WN>
+void launch_tile(const FfnArgs& a, hipStream_t s) {
+  constexpr int NOUT = EPI != EPI_PLAIN ? BN / 2 : BN;
+  const dim3 grid((unsigned)(((a.N + NOUT - 1) / NOUT) * ((a.M + BM - 1) / BM)));
+  hipLaunchKernelGGL((ffn_gemm_kernel<T, AKC, BKC, EPI, ACT, BM, BN, WM, WN>), grid, dim3(64 * WM * WN), 2 * (BM + BN) * ROWB, s, a);
+}
+
 template <typename T, bool AKC, bool BKC, int EPI, int ACT>
 void launch_gemm(const FfnArgs& a, hipStream_t s) {
-  const dim3 grid((unsigned)((a.N + TN - 1) / TN), (unsigned)((a.M + TM - 1) / TM));
-  hipLaunchKernelGGL((ffn_gemm_kernel<T, AKC, BKC, EPI, ACT>), grid, dim3(256), 0, s, a);
+  constexpr int pair = EPI != EPI_PLAIN ? 2 : 1;
+  // the large tile where it fills the 256 CUs
+  const i64 large = ((a.M + 255) / 256) * ((a.N * pair + 255) / 256);
+  if (large >= 256) launch_tile<T, AKC, BKC, EPI, ACT, 256, 256, 2, 4>(a, s);
+  else launch_tile<T, AKC, BKC, EPI, ACT, 128, 128, 2, 2>(a, s);
 }
 
 template <typename T, int ACT>
