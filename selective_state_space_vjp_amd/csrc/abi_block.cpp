@@ -77,7 +77,9 @@ ssmvjp_status ffn_check(const ssmvjp_ffn_desc* d) {
   if (d->act != SSMVJP_ACT_SILU && d->act != SSMVJP_ACT_GELU) return SSMVJP_EINVAL;
   if (d->dim % 8 || d->hidden % 8 || d->dim >= (1 << 20) || d->hidden >= (1 << 20)) return SSMVJP_EUNSUPPORTED;
   const double wide = (double)(d->dim > d->hidden ? d->dim : d->hidden);
-  if ((double)d->rows > DIM_MAX || !launches(((double)d->rows / 32 + 1) * (wide / 32 + 1), 256)) return SSMVJP_EUNSUPPORTED;
+  if ((double)d->rows > DIM_MAX || !launches(((double)d->rows / 32 + 1) * (wide / 32 + 1), 256) ||
+      !launches(((double)d->hidden / 128 + 1) * ((double)d->dim / 128 + 1), 256))
+    return SSMVJP_EUNSUPPORTED;
   return SSMVJP_OK;
 }
 

@@ -26,6 +26,8 @@ struct FfnArgs {
   i64 ldc;
   void* C[3];           // h, gate, up | dgate, dup | C
   const void *dh;       // BACK: [M, N]
+  int split;            // parts of k, each a workgroup's; more than one: sums to part
+  float* part;          // [split][PAIR ? 2 : 1][M][N]
 };
 
 enum { EPI_PLAIN, EPI_GLU, EPI_GLU_BACK };
@@ -176,24 +178,61 @@ __device__ __forceinline__ void fetch4(const void* p, i64 e, float (&v)[4]) {
   }
 }
 
-// WM x WN waves.  PAIR: the tile's BN columns are BN/2 of each of two products, side by side in every wave.
-template <typename T, bool AKC, bool BKC, int EPI, int ACT, int BM, int BN, int WM, int WN>
+// all but the last N loads have come, and every read of LDS has its data: behind a barrier the buffer read last is free
+template <int N>
+__device__ __forceinline__ void step_wait() {
+  asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)" ::"i"(N) : "memory");
+}
+
+// the four values at e of what the sums v[0] (and v[1], PAIR) become
+template <typename T, int EPI, int ACT>
+__device__ __forceinline__ void finish4(const FfnArgs& a, i64 e, float (&v)[3][4]) {
+  if constexpr (EPI == EPI_PLAIN) {
+    store4<T>(a.C[0], e, v[0]);
+  } else if constexpr (EPI == EPI_GLU) {
+#pragma unroll
+    for (int r = 0; r < 4; ++r) v[2][r] = act_of<ACT>(v[0][r]) * v[1][r];
+    store4<T>(a.C[0], e, v[2]);
+    if (a.C[1]) {
+      store4<T>(a.C[1], e, v[0]);
+      store4<T>(a.C[2], e, v[1]);
+    }
+  } else {
+    fetch4<T>(a.dh, e, v[2]);
+#pragma unroll
+    for (int r = 0; r < 4; ++r) {
+      float f, df;
+      act_pair<ACT>(v[0][r], f, df);
+      v[0][r] = v[2][r] * v[1][r] * df;
+      v[1][r] = v[2][r] * f;
+    }
+    store4<T>(a.C[0], e, v[0]);
+    store4<T>(a.C[1], e, v[1]);
+  }
+}
+
+// WM x WN waves, NB buffers.  PAIR: the tile's BN columns are BN/2 of each of two products, side by side in every wave.
+template <typename T, bool AKC, bool BKC, int EPI, int ACT, int BM, int BN, int WM, int WN, int NB>
 __global__ void __launch_bounds__(64 * WM * WN) ffn_gemm_kernel(FfnArgs a) {
   constexpr bool PAIR = EPI != EPI_PLAIN;
   constexpr int W = WM * WN, KB = ROWB / (int)sizeof(T), NOUT = PAIR ? BN / 2 : BN;
   constexpr int FM = BM / WM / 16, FN = BN / WN / 16;
   typedef TileOf<T, AKC, BM> TA;
   typedef TileOf<T, BKC, NOUT> TB;
+  static_assert(BM >= 32 && FM > 0 && FN > 0, "");
   constexpr int IA = TA::BYTES / 1024 / W, IB = TB::BYTES / 1024 / W;  // loads of a wave, each product's B by itself
   constexpr int BUF = TA::BYTES + (PAIR ? 2 : 1) * TB::BYTES;
   static_assert(IA * 1024 * W == TA::BYTES && IB * 1024 * W == TB::BYTES, "");
   extern __shared__ __align__(1024) char lds[];
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int wm = wave / WN * (BM / WM), wn = wave % WN * (NOUT / WN);
+  const unsigned nm = (unsigned)((a.M + BM - 1) / BM), nn = (unsigned)((a.N + NOUT - 1) / NOUT);
   unsigned tm, tn;
-  place(blockIdx.x, (unsigned)((a.M + BM - 1) / BM), (unsigned)((a.N + NOUT - 1) / NOUT), tm, tn);
+  place(blockIdx.x % (nm * nn), nm, nn, tm, tn);
   const i64 m0 = (i64)tm * BM, n0 = (i64)tn * NOUT;
-  const int steps1 = (int)((a.K + KB - 1) / KB), steps = (PAIR ? 1 : a.segs) * steps1;
+  const int steps1 = (int)((a.K + KB - 1) / KB), all = (PAIR ? 1 : a.segs) * steps1;
+  const int share = blockIdx.x / (nm * nn);
+  const int first = (int)((i64)all * share / a.split), steps = (int)((i64)all * (share + 1) / a.split) - first;
   const unsigned base = lds_base(lds);
 
   unsigned offA[IA], offB[IB];
@@ -202,8 +241,8 @@ __global__ void __launch_bounds__(64 * WM * WN) ffn_gemm_kernel(FfnArgs a) {
 #pragma unroll
   for (int i = 0; i < IB; ++i) offB[i] = TB::source((wave * IB + i) * 64 + lane, (unsigned)(a.B[0].ld * sizeof(T)));
 
-  auto load = [&](int step, int buf) {
-    const int s = !PAIR && step >= steps1;
+  auto load = [&](int at, int buf) {
+    const int step = first + at, s = !PAIR && step >= steps1;
     const i64 k0 = (i64)(step - s * steps1) * KB;
     const bool part = k0 + KB > a.K;  // KC: chunks past the last k would be the next row's
     const unsigned to = base + buf * BUF;
@@ -232,12 +271,20 @@ __global__ void __launch_bounds__(64 * WM * WN) ffn_gemm_kernel(FfnArgs a) {
 #pragma unroll
     for (int j = 0; j < FN; ++j) acc[i][j] = zero4();
 
-  if (steps > 0) load(0, 0);
-  dma_wait();
-  __syncthreads();
+  // the next NB - 1 steps are on their way while one is multiplied
+  constexpr int LOADS = IA + (PAIR ? 2 : 1) * IB;
+#pragma unroll
+  for (int i = 0; i < NB - 1; ++i)
+    if (i < steps) load(i, i);
+  int at = 0;
   for (int step = 0; step < steps; ++step) {
-    const char* buf = lds + (step & 1) * BUF;
-    if (step + 1 < steps) load(step + 1, (step + 1) & 1);
+    if (step + NB - 1 <= steps) step_wait<(NB - 2) * LOADS>();
+    else step_wait<0>();
+    __builtin_amdgcn_s_barrier();
+    asm volatile("" ::: "memory");
+    const char* buf = lds + at * BUF;
+    if (step + NB - 1 < steps) load(step + NB - 1, at == 0 ? NB - 1 : at - 1);
+    at = at + 1 == NB ? 0 : at + 1;
 #pragma unroll
     for (int kk = 0; kk < 2; ++kk) {
       Fragment<T> fa[FM], fb[FN];
@@ -254,8 +301,6 @@ __global__ void __launch_bounds__(64 * WM * WN) ffn_gemm_kernel(FfnArgs a) {
 #pragma unroll
         for (int j = 0; j < FN; ++j) multiply(acc[i][j], fb[j], fa[i]);
     }
-    dma_wait();
-    __syncthreads();
   }
 
 #pragma unroll
@@ -266,37 +311,42 @@ __global__ void __launch_bounds__(64 * WM * WN) ffn_gemm_kernel(FfnArgs a) {
     for (int j = 0; j < (PAIR ? FN / 2 : FN); ++j) {
       const i64 n = n0 + wn + 16 * j + 4 * (lane >> 4);
       if (n >= a.N) continue;
-      const i64 e = m * a.ldc + n;
       float v[3][4];
-      if constexpr (EPI == EPI_PLAIN) {
 #pragma unroll
-        for (int r = 0; r < 4; ++r) v[0][r] = acc[i][j][r];
-        store4<T>(a.C[0], e, v[0]);
-      } else if constexpr (EPI == EPI_GLU) {
-#pragma unroll
-        for (int r = 0; r < 4; ++r) {
-          v[1][r] = acc[i][j][r];
-          v[2][r] = acc[i][j + FN / 2][r];
-          v[0][r] = act_of<ACT>(v[1][r]) * v[2][r];
-        }
-        store4<T>(a.C[0], e, v[0]);
-        if (a.C[1]) {
-          store4<T>(a.C[1], e, v[1]);
-          store4<T>(a.C[2], e, v[2]);
-        }
+      for (int r = 0; r < 4; ++r) {
+        v[0][r] = acc[i][j][r];
+        if constexpr (PAIR) v[1][r] = acc[i][j + FN / 2][r];
+      }
+      if (a.split > 1) {
+        const i64 each = a.M * a.N;
+        float* p = a.part + (PAIR ? 2 : 1) * each * share + m * a.N + n;
+        store4<float>(p, 0, v[0]);
+        if constexpr (PAIR) store4<float>(p, each, v[1]);
       } else {
-        fetch4<T>(a.dh, e, v[2]);
-#pragma unroll
-        for (int r = 0; r < 4; ++r) {
-          float f, df;
-          act_pair<ACT>(acc[i][j][r], f, df);
-          v[0][r] = v[2][r] * acc[i][j + FN / 2][r] * df;
-          v[1][r] = v[2][r] * f;
-        }
-        store4<T>(a.C[0], e, v[0]);
-        store4<T>(a.C[1], e, v[1]);
+        finish4<T, EPI, ACT>(a, m * a.ldc + n, v);
       }
     }
+  }
+}
+
+// the parts' sums in order, and what becomes of them
+template <typename T, int EPI, int ACT>
+__global__ void __launch_bounds__(256) ffn_join_kernel(FfnArgs a) {
+  constexpr bool PAIR = EPI != EPI_PLAIN;
+  const i64 each = a.M * a.N;
+  for (i64 e = ((i64)blockIdx.x * 256 + threadIdx.x) * 4; e < each; e += (i64)gridDim.x * 1024) {
+    float v[3][4];
+#pragma unroll
+    for (int p = 0; p < (PAIR ? 2 : 1); ++p) {
+      fetch4<float>(a.part, p * each + e, v[p]);
+      for (int s = 1; s < a.split; ++s) {
+        float w[4];
+        fetch4<float>(a.part, ((PAIR ? 2 : 1) * s + p) * each + e, w);
+#pragma unroll
+        for (int r = 0; r < 4; ++r) v[p][r] += w[r];
+      }
+    }
+    finish4<T, EPI, ACT>(a, e / a.N * a.ldc + e % a.N, v);
   }
 }
 
@@ -312,59 +362,106 @@ __global__ void __launch_bounds__(256) ffn_grad_kernel(const T* dh, const T* gat
   }
 }
 
-template <typename T, bool AKC, bool BKC, int EPI, int ACT, int BM, int BN, int WM, int WN>
+// ---------------------------------------------------------------------------
+// host
+// ---------------------------------------------------------------------------
+enum { TILE_LARGE, TILE_MID, TILE_FEW };  // 256 x 256, 128 x 128, 32 x 64
+
+struct GemmPlan {
+  int tile, split;
+};
+
+GemmPlan gemm_plan(i64 M, i64 N, i64 K, int segs, bool pair, bool few, size_t elem) {
+  const int p = pair ? 2 : 1;
+  const i64 steps = segs * ((K * (i64)elem + ROWB - 1) / ROWB);
+  const auto tiles = [&](i64 bm, i64 bn) { return ((M + bm - 1) / bm) * ((N * p + bn - 1) / bn); };
+  GemmPlan g{few && M <= 32 ? TILE_FEW : tiles(256, 256) >= 256 ? TILE_LARGE : TILE_MID, 1};
+  const i64 n = g.tile == TILE_FEW ? tiles(32, 64) : tiles(128, 128);
+  if (g.tile != TILE_LARGE && n > 0 && n < 256) {
+    const i64 most = steps / 8 < 512 / n ? steps / 8 : 512 / n;
+    if (most > 1) g.split = (int)most;
+  }
+  return g;
+}
+
+size_t part_bytes(const GemmPlan& g, i64 M, i64 N, bool pair) {
+  return g.split > 1 ? (size_t)(g.split * M * N * (pair ? 8 : 4)) : 0;
+}
+
+template <typename T, bool AKC, bool BKC, int EPI, int ACT, int BM, int BN, int WM, int WN, int NB>
 void launch_tile(const FfnArgs& a, hipStream_t s) {
   constexpr int NOUT = EPI != EPI_PLAIN ? BN / 2 : BN;
-  const dim3 grid((unsigned)(((a.N + NOUT - 1) / NOUT) * ((a.M + BM - 1) / BM)));
-  hipLaunchKernelGGL((ffn_gemm_kernel<T, AKC, BKC, EPI, ACT, BM, BN, WM, WN>), grid, dim3(64 * WM * WN), 2 * (BM + BN) * ROWB, s, a);
+  const dim3 grid((unsigned)(((a.N + NOUT - 1) / NOUT) * ((a.M + BM - 1) / BM) * a.split));
+  hipLaunchKernelGGL((ffn_gemm_kernel<T, AKC, BKC, EPI, ACT, BM, BN, WM, WN, NB>), grid, dim3(64 * WM * WN),
+                     NB * (BM + BN) * ROWB, s, a);
 }
 
 template <typename T, bool AKC, bool BKC, int EPI, int ACT>
-void launch_gemm(const FfnArgs& a, hipStream_t s) {
-  constexpr int pair = EPI != EPI_PLAIN ? 2 : 1;
-  // the large tile where it fills the 256 CUs
-  const i64 large = ((a.M + 255) / 256) * ((a.N * pair + 255) / 256);
-  if (large >= 256) launch_tile<T, AKC, BKC, EPI, ACT, 256, 256, 2, 4>(a, s);
-  else launch_tile<T, AKC, BKC, EPI, ACT, 128, 128, 2, 2>(a, s);
+void launch_gemm(FfnArgs a, float* part, hipStream_t s) {
+  const GemmPlan g = gemm_plan(a.M, a.N, a.K, a.segs, EPI != EPI_PLAIN, AKC, sizeof(T));
+  a.split = g.split;
+  a.part = part;
+  if (g.tile == TILE_LARGE) launch_tile<T, AKC, BKC, EPI, ACT, 256, 256, 2, 4, 2>(a, s);
+  else if (g.tile == TILE_MID) launch_tile<T, AKC, BKC, EPI, ACT, 128, 128, 2, 2, 2>(a, s);
+  else if constexpr (AKC) launch_tile<T, AKC, BKC, EPI, ACT, 32, 64, 2, 2, 6>(a, s);
+  if (g.split > 1) {
+    const i64 blocks = (a.M * a.N + 1023) / 1024;
+    hipLaunchKernelGGL((ffn_join_kernel<T, EPI, ACT>), dim3((unsigned)(blocks < 4096 ? blocks : 4096)), dim3(256), 0, s, a);
+  }
 }
 
 template <typename T, int ACT>
 void ffn_fwd(const ssmvjp_ffn_desc& d, const FfnFwdPointers& p, hipStream_t s) {
-  FfnArgs a{d.rows, d.hidden, d.dim, {{p.x, d.dim}}, {{p.w_gate, d.dim}, {p.w_up, d.dim}}, 1, d.hidden, {p.h, p.gate, p.up}, nullptr};
-  launch_gemm<T, true, true, EPI_GLU, ACT>(a, s);
+  FfnArgs a{d.rows, d.hidden, d.dim, {{p.x, d.dim}}, {{p.w_gate, d.dim}, {p.w_up, d.dim}}, 1, d.hidden, {p.h, p.gate, p.up}, nullptr, 1, nullptr};
+  launch_gemm<T, true, true, EPI_GLU, ACT>(a, (float*)p.workspace, s);
+}
+
+// dgate and dup
+size_t grads_bytes(const ssmvjp_ffn_desc& d) {
+  return (size_t)((2 * d.rows * d.hidden * (d.dtype == SSMVJP_BF16 ? 2 : 4) + 255) / 256 * 256);
 }
 
 template <typename T, int ACT>
 void ffn_bwd(const ssmvjp_ffn_desc& d, const FfnBwdPointers& p, hipStream_t s) {
   const i64 n = d.rows * d.hidden;
   T *dgate = (T*)p.workspace, *dup = dgate + n;
+  float* part = (float*)((char*)p.workspace + grads_bytes(d));
   if (n > 0) {
     if (p.gate) {
       const i64 blocks = (n + 255) / 256 < 65536 ? (n + 255) / 256 : 65536;
       hipLaunchKernelGGL((ffn_grad_kernel<T, ACT>), dim3((unsigned)blocks), dim3(256), 0, s, (const T*)p.dh, (const T*)p.gate,
                          (const T*)p.up, dgate, dup, n);
     } else {
-      FfnArgs a{d.rows, d.hidden, d.dim, {{p.x, d.dim}}, {{p.w_gate, d.dim}, {p.w_up, d.dim}}, 1, d.hidden, {dgate, dup}, p.dh};
-      launch_gemm<T, true, true, EPI_GLU_BACK, ACT>(a, s);
+      FfnArgs a{d.rows, d.hidden, d.dim, {{p.x, d.dim}}, {{p.w_gate, d.dim}, {p.w_up, d.dim}}, 1, d.hidden, {dgate, dup}, p.dh, 1, nullptr};
+      launch_gemm<T, true, true, EPI_GLU_BACK, ACT>(a, part, s);
     }
     if (p.dx) {
-      FfnArgs a{d.rows, d.dim, d.hidden, {{dgate, d.hidden}, {dup, d.hidden}}, {{p.w_gate, d.dim}, {p.w_up, d.dim}}, 2, d.dim, {p.dx}, nullptr};
-      launch_gemm<T, true, false, EPI_PLAIN, 0>(a, s);
+      FfnArgs a{d.rows, d.dim, d.hidden, {{dgate, d.hidden}, {dup, d.hidden}}, {{p.w_gate, d.dim}, {p.w_up, d.dim}}, 2, d.dim, {p.dx}, nullptr, 1, nullptr};
+      launch_gemm<T, true, false, EPI_PLAIN, 0>(a, part, s);
     }
   }
   for (int w = 0; w < 2; ++w) {
     void* out = w ? p.dw_up : p.dw_gate;
     if (!out) continue;
-    FfnArgs a{d.hidden, d.dim, d.rows, {{w ? dup : dgate, d.hidden}}, {{p.x, d.dim}}, 1, d.dim, {out}, nullptr};
-    launch_gemm<T, false, false, EPI_PLAIN, 0>(a, s);
+    FfnArgs a{d.hidden, d.dim, d.rows, {{w ? dup : dgate, d.hidden}}, {{p.x, d.dim}}, 1, d.dim, {out}, nullptr, 1, nullptr};
+    launch_gemm<T, false, false, EPI_PLAIN, 0>(a, part, s);
   }
 }
 
 }  // namespace
 
-size_t ffn_fwd_workspace_bytes(const ssmvjp_ffn_desc&) { return 0; }
+size_t ffn_fwd_workspace_bytes(const ssmvjp_ffn_desc& d) {
+  return part_bytes(gemm_plan(d.rows, d.hidden, d.dim, 1, true, true, d.dtype == SSMVJP_BF16 ? 2 : 4), d.rows, d.hidden, true);
+}
+
+// dgate and dup, then the largest of the products' parts
 size_t ffn_bwd_workspace_bytes(const ssmvjp_ffn_desc& d) {
-  return (size_t)(2 * d.rows * d.hidden * (d.dtype == SSMVJP_BF16 ? 2 : 4));
+  const size_t elem = d.dtype == SSMVJP_BF16 ? 2 : 4;
+  size_t part = ffn_fwd_workspace_bytes(d);
+  const size_t dx = part_bytes(gemm_plan(d.rows, d.dim, d.hidden, 2, false, true, elem), d.rows, d.dim, false);
+  const size_t dw = part_bytes(gemm_plan(d.hidden, d.dim, d.rows, 1, false, false, elem), d.hidden, d.dim, false);
+  part = part > dx ? part : dx;
+  return grads_bytes(d) + (part > dw ? part : dw);
 }
 
 hipError_t launch_ffn_fwd(const ssmvjp_ffn_desc& d, const FfnFwdPointers& p, hipStream_t stream) {
