@@ -562,8 +562,8 @@ typedef struct {
  * place of forming them again.  Sums are float32; h is formed from the sums, not from
  * the rounded gate and up.
  * Constraints: dim and hidden multiples of 8 below 2^20 and launches of fewer than 2^32
- * threads: (rows/32 + 1) * (max(dim, hidden)/32 + 1) and (hidden/128 + 1) * (dim/128 + 1)
- * below 2^24 (SSMVJP_EUNSUPPORTED otherwise); every tensor 16-byte aligned (SSMVJP_EINVAL otherwise). */
+ * threads: (rows/32 + 1) * (max(dim, hidden)/32 + 1) below 2^24, (hidden/128 + 1) * (dim/128 + 1)
+ * below 2^23 (SSMVJP_EUNSUPPORTED otherwise); every tensor 16-byte aligned (SSMVJP_EINVAL otherwise). */
 ssmvjp_status gated_ffn_fwd_workspace(const ssmvjp_ffn_desc* desc, size_t* bytes);
 ssmvjp_status gated_ffn_fwd(const ssmvjp_ffn_desc* desc, const void* x, const void* w_gate, const void* w_up,
                             void* h, void* gate, void* up, void* workspace, size_t workspace_bytes, void* stream);

@@ -78,7 +78,7 @@ ssmvjp_status ffn_check(const ssmvjp_ffn_desc* d) {
   if (d->dim % 8 || d->hidden % 8 || d->dim >= (1 << 20) || d->hidden >= (1 << 20)) return SSMVJP_EUNSUPPORTED;
   const double wide = (double)(d->dim > d->hidden ? d->dim : d->hidden);
   if ((double)d->rows > DIM_MAX || !launches(((double)d->rows / 32 + 1) * (wide / 32 + 1), 256) ||
-      !launches(((double)d->hidden / 128 + 1) * ((double)d->dim / 128 + 1), 256))
+      !launches(((double)d->hidden / 128 + 1) * ((double)d->dim / 128 + 1), 512))
     return SSMVJP_EUNSUPPORTED;
   return SSMVJP_OK;
 }

@@ -46,20 +46,71 @@ __device__ __forceinline__ bool keep(const Words& w, int j, unsigned t) {
   return ((j & 1) ? w.w[j >> 1] >> 16 : w.w[j >> 1] & 0xffffu) >= t;
 }
 
-template <typename T, bool RES>
+// eight elements of a 16-byte aligned tensor
+struct Eight {
+  float v[8];
+};
+__device__ __forceinline__ Eight load8(const bf16* p) {
+  const uint4 u = *(const uint4*)p;
+  const unsigned d[4] = {u.x, u.y, u.z, u.w};
+  Eight e;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    e.v[2 * i] = __uint_as_float(d[i] << 16);
+    e.v[2 * i + 1] = __uint_as_float(d[i] & 0xffff0000u);
+  }
+  return e;
+}
+__device__ __forceinline__ Eight load8(const float* p) {
+  const float4 a = *(const float4*)p, b = *(const float4*)(p + 4);
+  return {{a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w}};
+}
+__device__ __forceinline__ void store8(bf16* p, const Eight& e) {
+  *(uint4*)p = make_uint4(pk_bf16(e.v[0], e.v[1]), pk_bf16(e.v[2], e.v[3]), pk_bf16(e.v[4], e.v[5]), pk_bf16(e.v[6], e.v[7]));
+}
+__device__ __forceinline__ void store8(float* p, const Eight& e) {
+  *(float4*)p = make_float4(e.v[0], e.v[1], e.v[2], e.v[3]);
+  *(float4*)(p + 4) = make_float4(e.v[4], e.v[5], e.v[6], e.v[7]);
+}
+
+// A thread takes one counter's eight elements at a time.  WIDE: 16-byte aligned tensors.
+template <typename T, bool RES, bool WIDE>
 __global__ void __launch_bounds__(256) dropout_kernel(DropArgs a) {
   const unsigned long long seed = (unsigned long long)a.rng[0], offset = (unsigned long long)a.rng[1];
+  const T *x = (const T*)a.x, *res = (const T*)a.res;
+  T* y = (T*)a.y;
   const i64 blocks = (a.n + 7) / 8;
   for (i64 b = (i64)blockIdx.x * 256 + threadIdx.x; b < blocks; b += (i64)gridDim.x * 256) {
-    const Words w = philox((unsigned long long)b, offset, seed);
+    const i64 e = 8 * b;
+    if (WIDE && e + 8 <= a.n) {
+      Eight v = load8(x + e), r;
+      if (RES) r = load8(res + e);
+      const Words w = philox((unsigned long long)b, offset, seed);
 #pragma unroll
-    for (int j = 0; j < 8; ++j) {
-      const i64 e = 8 * b + j;
-      if (e >= a.n) break;
-      const float v = keep(w, j, a.t) ? ld((const T*)a.x, e) * a.scale : 0.0f;
-      st((T*)a.y, e, RES ? ld((const T*)a.res, e) + v : v);
+      for (int j = 0; j < 8; ++j) {
+        v.v[j] = keep(w, j, a.t) ? v.v[j] * a.scale : 0.0f;
+        if (RES) v.v[j] += r.v[j];
+      }
+      store8(y + e, v);
+    } else {
+      const Words w = philox((unsigned long long)b, offset, seed);
+#pragma unroll
+      for (int j = 0; j < 8; ++j)
+        if (e + j < a.n) {
+          const float v = keep(w, j, a.t) ? ld(x, e + j) * a.scale : 0.0f;
+          st(y, e + j, RES ? ld(res, e + j) + v : v);
+        }
     }
   }
+}
+
+template <typename T, bool RES>
+void launch_wide(const DropArgs& a, hipStream_t s) {
+  const i64 blocks = ((a.n + 7) / 8 + 255) / 256;
+  const dim3 grid((unsigned)(blocks < (1 << 22) ? blocks : 1 << 22));
+  const bool wide = (uintptr_t)a.x % 16 == 0 && (uintptr_t)a.res % 16 == 0 && (uintptr_t)a.y % 16 == 0;
+  if (wide) hipLaunchKernelGGL((dropout_kernel<T, RES, true>), grid, dim3(256), 0, s, a);
+  else hipLaunchKernelGGL((dropout_kernel<T, RES, false>), grid, dim3(256), 0, s, a);
 }
 
 }  // namespace
@@ -68,15 +119,8 @@ hipError_t launch_dropout(int64_t n, double p, int32_t dtype, const void* in, co
                           void* out, hipStream_t stream) {
   const unsigned t = (unsigned)__builtin_rint(65536.0 * p);
   const DropArgs a{n, t, t < 65536u ? (float)(65536.0 / (65536.0 - t)) : 0.0f, in, residual, rng, out};
-  const i64 blocks = ((n + 7) / 8 + 255) / 256;
-  const dim3 grid((unsigned)(blocks < 65536 ? blocks : 65536));
-  if (dtype == SSMVJP_BF16) {
-    if (residual) hipLaunchKernelGGL((dropout_kernel<bf16, true>), grid, dim3(256), 0, stream, a);
-    else hipLaunchKernelGGL((dropout_kernel<bf16, false>), grid, dim3(256), 0, stream, a);
-  } else {
-    if (residual) hipLaunchKernelGGL((dropout_kernel<float, true>), grid, dim3(256), 0, stream, a);
-    else hipLaunchKernelGGL((dropout_kernel<float, false>), grid, dim3(256), 0, stream, a);
-  }
+  if (dtype == SSMVJP_BF16) residual ? launch_wide<bf16, true>(a, stream) : launch_wide<bf16, false>(a, stream);
+  else residual ? launch_wide<float, true>(a, stream) : launch_wide<float, false>(a, stream);
   return hipGetLastError();
 }
 

@@ -26,8 +26,9 @@ struct FfnArgs {
   i64 ldc;
   void* C[3];           // h, gate, up | dgate, dup | C
   const void *dh;       // BACK: [M, N]
+  int items;            // products of one shape in one launch: A[i], C[i] (EPI_PLAIN, segs = 1)
   int split;            // parts of k, each a workgroup's; more than one: sums to part
-  float* part;          // [split][PAIR ? 2 : 1][M][N]
+  float* part;          // [items][split][PAIR ? 2 : 1][M][N]
 };
 
 enum { EPI_PLAIN, EPI_GLU, EPI_GLU_BACK };
@@ -186,9 +187,9 @@ __device__ __forceinline__ void step_wait() {
 
 // the four values at e of what the sums v[0] (and v[1], PAIR) become
 template <typename T, int EPI, int ACT>
-__device__ __forceinline__ void finish4(const FfnArgs& a, i64 e, float (&v)[3][4]) {
+__device__ __forceinline__ void finish4(const FfnArgs& a, int item, i64 e, float (&v)[3][4]) {
   if constexpr (EPI == EPI_PLAIN) {
-    store4<T>(a.C[0], e, v[0]);
+    store4<T>(a.C[item], e, v[0]);
   } else if constexpr (EPI == EPI_GLU) {
 #pragma unroll
     for (int r = 0; r < 4; ++r) v[2][r] = act_of<ACT>(v[0][r]) * v[1][r];
@@ -231,7 +232,7 @@ __global__ void __launch_bounds__(64 * WM * WN) ffn_gemm_kernel(FfnArgs a) {
   place(blockIdx.x % (nm * nn), nm, nn, tm, tn);
   const i64 m0 = (i64)tm * BM, n0 = (i64)tn * NOUT;
   const int steps1 = (int)((a.K + KB - 1) / KB), all = (PAIR ? 1 : a.segs) * steps1;
-  const int share = blockIdx.x / (nm * nn);
+  const int which = blockIdx.x / (nm * nn), item = PAIR ? 0 : which / a.split, share = which - item * a.split;
   const int first = (int)((i64)all * share / a.split), steps = (int)((i64)all * (share + 1) / a.split) - first;
   const unsigned base = lds_base(lds);
 
@@ -246,7 +247,7 @@ __global__ void __launch_bounds__(64 * WM * WN) ffn_gemm_kernel(FfnArgs a) {
     const i64 k0 = (i64)(step - s * steps1) * KB;
     const bool part = k0 + KB > a.K;  // KC: chunks past the last k would be the next row's
     const unsigned to = base + buf * BUF;
-    const u32x4 ra = tile_rsrc<T, AKC>(a.A[s], m0, a.M, k0, a.K, BM);
+    const u32x4 ra = tile_rsrc<T, AKC>(a.A[s + item], m0, a.M, k0, a.K, BM);
 #pragma unroll
     for (int i = 0; i < IA; ++i) {
       unsigned off = offA[i];
@@ -319,11 +320,11 @@ __global__ void __launch_bounds__(64 * WM * WN) ffn_gemm_kernel(FfnArgs a) {
       }
       if (a.split > 1) {
         const i64 each = a.M * a.N;
-        float* p = a.part + (PAIR ? 2 : 1) * each * share + m * a.N + n;
+        float* p = a.part + (PAIR ? 2 : 1) * each * which + m * a.N + n;
         store4<float>(p, 0, v[0]);
         if constexpr (PAIR) store4<float>(p, each, v[1]);
       } else {
-        finish4<T, EPI, ACT>(a, m * a.ldc + n, v);
+        finish4<T, EPI, ACT>(a, item, m * a.ldc + n, v);
       }
     }
   }
@@ -334,31 +335,46 @@ template <typename T, int EPI, int ACT>
 __global__ void __launch_bounds__(256) ffn_join_kernel(FfnArgs a) {
   constexpr bool PAIR = EPI != EPI_PLAIN;
   const i64 each = a.M * a.N;
-  for (i64 e = ((i64)blockIdx.x * 256 + threadIdx.x) * 4; e < each; e += (i64)gridDim.x * 1024) {
+  for (i64 i = ((i64)blockIdx.x * 256 + threadIdx.x) * 4; i < each * a.items; i += (i64)gridDim.x * 1024) {
+    const int item = (int)(i / each);
+    const i64 e = i - item * each;
     float v[3][4];
 #pragma unroll
     for (int p = 0; p < (PAIR ? 2 : 1); ++p) {
-      fetch4<float>(a.part, p * each + e, v[p]);
+      const float* part = a.part + ((PAIR ? 2 : 1) * (i64)item * a.split + p) * each + e;
+      fetch4<float>(part, 0, v[p]);
       for (int s = 1; s < a.split; ++s) {
         float w[4];
-        fetch4<float>(a.part, ((PAIR ? 2 : 1) * s + p) * each + e, w);
+        fetch4<float>(part, (PAIR ? 2 : 1) * s * each, w);
 #pragma unroll
         for (int r = 0; r < 4; ++r) v[p][r] += w[r];
       }
     }
-    finish4<T, EPI, ACT>(a, e / a.N * a.ldc + e % a.N, v);
+    finish4<T, EPI, ACT>(a, item, e / a.N * a.ldc + e % a.N, v);
   }
 }
 
-// dgate, dup from the kept gate and up
+// dgate, dup from the kept gate and up; n a multiple of 8
 template <typename T, int ACT>
 __global__ void __launch_bounds__(256) ffn_grad_kernel(const T* dh, const T* gate, const T* up, T* dgate, T* dup, i64 n) {
-  for (i64 e = (i64)blockIdx.x * 256 + threadIdx.x; e < n; e += (i64)gridDim.x * 256) {
-    float f, df;
-    act_pair<ACT>(ld(gate, e), f, df);
-    const float d = ld(dh, e);
-    st(dgate, e, d * ld(up, e) * df);
-    st(dup, e, d * f);
+  constexpr int W = 16 / sizeof(T);
+  for (i64 e = ((i64)blockIdx.x * 256 + threadIdx.x) * W; e < n; e += (i64)gridDim.x * 256 * W) {
+#pragma unroll
+    for (int i = 0; i < W; i += 4) {
+      float d[4], g[4], u[4], og[4], ou[4];
+      fetch4<T>(dh, e + i, d);
+      fetch4<T>(gate, e + i, g);
+      fetch4<T>(up, e + i, u);
+#pragma unroll
+      for (int r = 0; r < 4; ++r) {
+        float f, df;
+        act_pair<ACT>(g[r], f, df);
+        og[r] = d[r] * u[r] * df;
+        ou[r] = d[r] * f;
+      }
+      store4<T>(dgate, e + i, og);
+      store4<T>(dup, e + i, ou);
+    }
   }
 }
 
@@ -371,10 +387,10 @@ struct GemmPlan {
   int tile, split;
 };
 
-GemmPlan gemm_plan(i64 M, i64 N, i64 K, int segs, bool pair, bool few, size_t elem) {
+GemmPlan gemm_plan(i64 M, i64 N, i64 K, int segs, int items, bool pair, bool few, size_t elem) {
   const int p = pair ? 2 : 1;
   const i64 steps = segs * ((K * (i64)elem + ROWB - 1) / ROWB);
-  const auto tiles = [&](i64 bm, i64 bn) { return ((M + bm - 1) / bm) * ((N * p + bn - 1) / bn); };
+  const auto tiles = [&](i64 bm, i64 bn) { return items * ((M + bm - 1) / bm) * ((N * p + bn - 1) / bn); };
   GemmPlan g{few && M <= 32 ? TILE_FEW : tiles(256, 256) >= 256 ? TILE_LARGE : TILE_MID, 1};
   const i64 n = g.tile == TILE_FEW ? tiles(32, 64) : tiles(128, 128);
   if (g.tile != TILE_LARGE && n > 0 && n < 256) {
@@ -384,35 +400,35 @@ GemmPlan gemm_plan(i64 M, i64 N, i64 K, int segs, bool pair, bool few, size_t el
   return g;
 }
 
-size_t part_bytes(const GemmPlan& g, i64 M, i64 N, bool pair) {
-  return g.split > 1 ? (size_t)(g.split * M * N * (pair ? 8 : 4)) : 0;
+size_t part_bytes(const GemmPlan& g, i64 M, i64 N, int items, bool pair) {
+  return g.split > 1 ? (size_t)(items * g.split * M * N * (pair ? 8 : 4)) : 0;
 }
 
 template <typename T, bool AKC, bool BKC, int EPI, int ACT, int BM, int BN, int WM, int WN, int NB>
 void launch_tile(const FfnArgs& a, hipStream_t s) {
   constexpr int NOUT = EPI != EPI_PLAIN ? BN / 2 : BN;
-  const dim3 grid((unsigned)(((a.N + NOUT - 1) / NOUT) * ((a.M + BM - 1) / BM) * a.split));
+  const dim3 grid((unsigned)(((a.N + NOUT - 1) / NOUT) * ((a.M + BM - 1) / BM) * a.items * a.split));
   hipLaunchKernelGGL((ffn_gemm_kernel<T, AKC, BKC, EPI, ACT, BM, BN, WM, WN, NB>), grid, dim3(64 * WM * WN),
                      NB * (BM + BN) * ROWB, s, a);
 }
 
 template <typename T, bool AKC, bool BKC, int EPI, int ACT>
 void launch_gemm(FfnArgs a, float* part, hipStream_t s) {
-  const GemmPlan g = gemm_plan(a.M, a.N, a.K, a.segs, EPI != EPI_PLAIN, AKC, sizeof(T));
+  const GemmPlan g = gemm_plan(a.M, a.N, a.K, a.segs, a.items, EPI != EPI_PLAIN, AKC, sizeof(T));
   a.split = g.split;
   a.part = part;
   if (g.tile == TILE_LARGE) launch_tile<T, AKC, BKC, EPI, ACT, 256, 256, 2, 4, 2>(a, s);
   else if (g.tile == TILE_MID) launch_tile<T, AKC, BKC, EPI, ACT, 128, 128, 2, 2, 2>(a, s);
   else if constexpr (AKC) launch_tile<T, AKC, BKC, EPI, ACT, 32, 64, 2, 2, 6>(a, s);
   if (g.split > 1) {
-    const i64 blocks = (a.M * a.N + 1023) / 1024;
+    const i64 blocks = (a.items * a.M * a.N + 1023) / 1024;
     hipLaunchKernelGGL((ffn_join_kernel<T, EPI, ACT>), dim3((unsigned)(blocks < 4096 ? blocks : 4096)), dim3(256), 0, s, a);
   }
 }
 
 template <typename T, int ACT>
 void ffn_fwd(const ssmvjp_ffn_desc& d, const FfnFwdPointers& p, hipStream_t s) {
-  FfnArgs a{d.rows, d.hidden, d.dim, {{p.x, d.dim}}, {{p.w_gate, d.dim}, {p.w_up, d.dim}}, 1, d.hidden, {p.h, p.gate, p.up}, nullptr, 1, nullptr};
+  FfnArgs a{d.rows, d.hidden, d.dim, {{p.x, d.dim}}, {{p.w_gate, d.dim}, {p.w_up, d.dim}}, 1, d.hidden, {p.h, p.gate, p.up}, nullptr, 1, 1, nullptr};
   launch_gemm<T, true, true, EPI_GLU, ACT>(a, (float*)p.workspace, s);
 }
 
@@ -428,40 +444,42 @@ void ffn_bwd(const ssmvjp_ffn_desc& d, const FfnBwdPointers& p, hipStream_t s) {
   float* part = (float*)((char*)p.workspace + grads_bytes(d));
   if (n > 0) {
     if (p.gate) {
-      const i64 blocks = (n + 255) / 256 < 65536 ? (n + 255) / 256 : 65536;
+      const i64 need = (n * (i64)sizeof(T) + 4095) / 4096, blocks = need < (1 << 22) ? need : 1 << 22;
       hipLaunchKernelGGL((ffn_grad_kernel<T, ACT>), dim3((unsigned)blocks), dim3(256), 0, s, (const T*)p.dh, (const T*)p.gate,
                          (const T*)p.up, dgate, dup, n);
     } else {
-      FfnArgs a{d.rows, d.hidden, d.dim, {{p.x, d.dim}}, {{p.w_gate, d.dim}, {p.w_up, d.dim}}, 1, d.hidden, {dgate, dup}, p.dh, 1, nullptr};
+      FfnArgs a{d.rows, d.hidden, d.dim, {{p.x, d.dim}}, {{p.w_gate, d.dim}, {p.w_up, d.dim}}, 1, d.hidden, {dgate, dup}, p.dh, 1, 1, nullptr};
       launch_gemm<T, true, true, EPI_GLU_BACK, ACT>(a, part, s);
     }
     if (p.dx) {
-      FfnArgs a{d.rows, d.dim, d.hidden, {{dgate, d.hidden}, {dup, d.hidden}}, {{p.w_gate, d.dim}, {p.w_up, d.dim}}, 2, d.dim, {p.dx}, nullptr, 1, nullptr};
+      FfnArgs a{d.rows, d.dim, d.hidden, {{dgate, d.hidden}, {dup, d.hidden}}, {{p.w_gate, d.dim}, {p.w_up, d.dim}}, 2, d.dim, {p.dx}, nullptr, 1, 1, nullptr};
       launch_gemm<T, true, false, EPI_PLAIN, 0>(a, part, s);
     }
   }
-  for (int w = 0; w < 2; ++w) {
-    void* out = w ? p.dw_up : p.dw_gate;
-    if (!out) continue;
-    FfnArgs a{d.hidden, d.dim, d.rows, {{w ? dup : dgate, d.hidden}}, {{p.x, d.dim}}, 1, d.dim, {out}, nullptr, 1, nullptr};
-    launch_gemm<T, false, false, EPI_PLAIN, 0>(a, part, s);
-  }
+  // both weights' gradients in one launch
+  FfnArgs a{d.hidden, d.dim, d.rows, {}, {{p.x, d.dim}}, 1, d.dim, {}, nullptr, 0, 1, nullptr};
+  if (p.dw_gate) a.A[a.items] = {dgate, d.hidden}, a.C[a.items++] = p.dw_gate;
+  if (p.dw_up) a.A[a.items] = {dup, d.hidden}, a.C[a.items++] = p.dw_up;
+  if (a.items) launch_gemm<T, false, false, EPI_PLAIN, 0>(a, part, s);
 }
 
 }  // namespace
 
 size_t ffn_fwd_workspace_bytes(const ssmvjp_ffn_desc& d) {
-  return part_bytes(gemm_plan(d.rows, d.hidden, d.dim, 1, true, true, d.dtype == SSMVJP_BF16 ? 2 : 4), d.rows, d.hidden, true);
+  return part_bytes(gemm_plan(d.rows, d.hidden, d.dim, 1, 1, true, true, d.dtype == SSMVJP_BF16 ? 2 : 4), d.rows, d.hidden, 1, true);
 }
 
 // dgate and dup, then the largest of the products' parts
 size_t ffn_bwd_workspace_bytes(const ssmvjp_ffn_desc& d) {
   const size_t elem = d.dtype == SSMVJP_BF16 ? 2 : 4;
   size_t part = ffn_fwd_workspace_bytes(d);
-  const size_t dx = part_bytes(gemm_plan(d.rows, d.dim, d.hidden, 2, false, true, elem), d.rows, d.dim, false);
-  const size_t dw = part_bytes(gemm_plan(d.hidden, d.dim, d.rows, 1, false, false, elem), d.hidden, d.dim, false);
-  part = part > dx ? part : dx;
-  return grads_bytes(d) + (part > dw ? part : dw);
+  const size_t dx = part_bytes(gemm_plan(d.rows, d.dim, d.hidden, 2, 1, false, true, elem), d.rows, d.dim, 1, false);
+  // one weight's gradient may be asked for without the other
+  for (int items = 1; items <= 2; ++items) {
+    const size_t dw = part_bytes(gemm_plan(d.hidden, d.dim, d.rows, 1, items, false, false, elem), d.hidden, d.dim, items, false);
+    part = part > dw ? part : dw;
+  }
+  return grads_bytes(d) + (part > dx ? part : dx);
 }
 
 hipError_t launch_ffn_fwd(const ssmvjp_ffn_desc& d, const FfnFwdPointers& p, hipStream_t stream) {
