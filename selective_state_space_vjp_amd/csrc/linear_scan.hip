@@ -134,37 +134,58 @@ __device__ __forceinline__ float sigmoid_hw(float z) { return __builtin_amdgcn_r
 __device__ __forceinline__ float decay_rate(float c, float z) { return c * softplus_f(z); }
 __device__ __forceinline__ float decay_slope(float z) { return z < -16.0f ? 1.0f : sigmoid_f(z) / softplus_f(z); }
 
+constexpr float MIN_NORMAL = 1.17549435e-38f;  // the reciprocals take denormals as zeros
+
 struct Token {
   float a, u;              // h = a h + u
-  float L, m, sr, w, rm;   // gated form; rm = 1/m, 0 where m = 0
+  float lc, sr, w, mw;     // gated form: log2(e) L, sigmoid(r), w, m w
 };
 
-// 1 - exp(-y) loses what a has rounded away where y is small: there its series
-__device__ __forceinline__ Token gated_token(float x, float r, float i, float rate) {
+// rate2: log2(e) c softplus(decay).  m^2 = 1 - a^2 loses what a has rounded away where y = 2 L is small: there the
+// series of 1 - exp(-y), off by 5e-8 of it at most.  m is m^2 / sqrt(m^2) with the root taken of a normal number.
+__device__ __forceinline__ Token gated_token(float x, float r, float i, float rate2) {
+  constexpr float Y = 1.3862943611198906f;  // y = Y lc
   Token t;
   t.sr = sigmoid_hw(r);
   t.w = sigmoid_hw(i);
-  t.L = rate * t.sr;
-  t.a = exp_hw(-t.L);
-  const float y = 2.0f * t.L;
+  t.lc = rate2 * t.sr;
+  t.a = __builtin_amdgcn_exp2f(-t.lc);
+  const float y = Y * t.lc;
   const float series = y * fmaf(y, fmaf(y, fmaf(y, fmaf(y, fmaf(y, -1.0f / 720, 1.0f / 120), -1.0f / 24), 1.0f / 6), -0.5f), 1.0f);
   const float m2 = y < 0.25f ? series : fmaf(-t.a, t.a, 1.0f);
-  t.rm = m2 >= 1.17549435e-38f ? __builtin_amdgcn_rsqf(m2) : 0.0f;  // the instruction takes denormals as zeros
-  t.m = m2 * t.rm;
-  t.u = t.m * t.w * x;
+  t.mw = m2 * __builtin_amdgcn_rsqf(fmaxf(m2, MIN_NORMAL)) * t.w;
+  t.u = t.mw * x;
   return t;
 }
+constexpr float LOG2E = 1.4426950408889634f, LN2 = 0.6931471805599453f;
 
-
-// A h + u; a state of zero stays out of a product that has overflowed
-__device__ __forceinline__ float apply(float A, float h, float u) { return h == 0.0f ? u : fmaf(A, h, u); }
+// A h + u.  GROWS: A may have overflowed (log gates above 0); a state of zero stays out of that.
+template <bool GROWS>
+__device__ __forceinline__ float apply(float A, float h, float u) {
+  return GROWS && h == 0.0f ? u : fmaf(A, h, u);
+}
 
 // ---------------------------------------------------------------------------
 // rows of V channels per lane
 // ---------------------------------------------------------------------------
+// a lane's values of one row as they lie in memory (two of bf16 in one register)
 template <typename T, int V>
 struct Raw {
   T v[V];
+  __device__ __forceinline__ float get(int i) const { return (float)v[i]; }
+  __device__ __forceinline__ void clear() {
+#pragma unroll
+    for (int i = 0; i < V; ++i) v[i] = (T)0.0f;
+  }
+  __device__ __forceinline__ void pin() {}
+};
+template <>
+struct Raw<bf16, 2> {
+  unsigned v;
+  __device__ __forceinline__ float get(int i) const { return __uint_as_float(i ? v & 0xffff0000u : v << 16); }
+  __device__ __forceinline__ void clear() { v = 0u; }
+  // from here on the values are taken out of the word again: they are not kept beside it
+  __device__ __forceinline__ void pin() { asm volatile("" : "+v"(v)); }
 };
 template <typename T, int V>
 __device__ __forceinline__ Raw<T, V> load_raw(const T* row, unsigned off) {
@@ -211,7 +232,7 @@ struct Pair {
 
 // Everything between a workgroup's segments and its sequence's other tiles.  Waves are numbered `w` in the order of
 // the recurrence (REV: the last rows first), tiles `k` likewise.
-template <int V>
+template <int V, bool GROWS>
 struct Chain {
   Pair (*seg)[V][64];   // [NW]: the waves' segments
   Pair (*look)[V][64];  // [NW]: what the waves found of the tiles before
@@ -230,7 +251,7 @@ struct Chain {
 #pragma unroll
         for (int i = 1; i < NW; ++i) {
           const Pair s = seg[i][v][lane];
-          t.H = apply(s.A, t.H, s.H);
+          t.H = apply<GROWS>(s.A, t.H, s.H);
           t.A *= s.A;
         }
         if (mine) put_pair(a.pairs + slot * a.D + ch0 + coff + v, t.A, t.H);
@@ -251,7 +272,7 @@ struct Chain {
           for (int v = 0; v < V; ++v) {
             const u64 q = await<u64, NO_PAIR>(p + v);
             const float A = __uint_as_float((unsigned)q);
-            f[v].H = apply(A, f[v].H, __uint_as_float((unsigned)(q >> 32)));
+            f[v].H = apply<GROWS>(A, f[v].H, __uint_as_float((unsigned)(q >> 32)));
             f[v].A *= A;
           }
         }
@@ -270,8 +291,8 @@ struct Chain {
     for (int v = 0; v < V; ++v) {
       h[v] = k >= GROUP ? base[v][lane] : first[v];
       if (k > 0)
-        for (int i = 0; i < NW; ++i) h[v] = apply(look[i][v][lane].A, h[v], look[i][v][lane].H);
-      for (int i = 0; i < w; ++i) h[v] = apply(seg[i][v][lane].A, h[v], seg[i][v][lane].H);
+        for (int i = 0; i < NW; ++i) h[v] = apply<GROWS>(look[i][v][lane].A, h[v], look[i][v][lane].H);
+      for (int i = 0; i < w; ++i) h[v] = apply<GROWS>(seg[i][v][lane].A, h[v], seg[i][v][lane].H);
     }
   }
   // the state behind the last wave's rows, where a group ends
@@ -337,19 +358,19 @@ __global__ void __launch_bounds__(64 * NW) scan_fwd_kernel(ScanArgs a) {
     }
     if constexpr (GATED)
 #pragma unroll
-      for (int v = 0; v < V; ++v) rate[v] = decay_rate(a.c, rate[v]);
+      for (int v = 0; v < V; ++v) rate[v] = LOG2E * decay_rate(a.c, rate[v]);
 #pragma unroll
     for (int i = 0; i < R; ++i)
 #pragma unroll
       for (int v = 0; v < V; ++v) {
         float ai, u;
         if constexpr (GATED) {
-          const Token k = gated_token((float)x[i].v[v], (float)r[i].v[v], (float)ig[i].v[v], rate[v]);
+          const Token k = gated_token(x[i].get(v), r[i].get(v), ig[i].get(v), rate[v]);
           ai = k.a;
           u = k.u;
         } else {
           ai = exp_hw(g[i].v[v]);
-          u = (float)x[i].v[v];
+          u = x[i].get(v);
         }
         if (!full && i >= rows) ai = 1.0f, u = 0.0f;
         A[i][v] = i ? A[i - 1][v] * ai : ai;
@@ -370,10 +391,10 @@ __global__ void __launch_bounds__(64 * NW) scan_fwd_kernel(ScanArgs a) {
   for (int v = 0; v < V; ++v) seg[w][v][lane] = {A[R - 1][v], U[R - 1][v]};
   __syncthreads();
   float h[V], last[V];
-  Chain<V> chain{seg, look, base};
+  Chain<V, !GATED> chain{seg, look, base};
   chain.enter(a, t.slot, 1, t.j, t.n, w, lane, ch0, coff, mine, first, h);
 #pragma unroll
-  for (int v = 0; v < V; ++v) last[v] = apply(A[R - 1][v], h[v], U[R - 1][v]);
+  for (int v = 0; v < V; ++v) last[v] = apply<!GATED>(A[R - 1][v], h[v], U[R - 1][v]);
   chain.leave(a, t.slot, t.j, t.n, w, ch0, coff, mine, last);
   if (!mine) return;
   if (a.h)
@@ -382,7 +403,7 @@ __global__ void __launch_bounds__(64 * NW) scan_fwd_kernel(ScanArgs a) {
       if (i < rows) {
         float o[V];
 #pragma unroll
-        for (int v = 0; v < V; ++v) o[v] = apply(A[i][v], h[v], U[i][v]);
+        for (int v = 0; v < V; ++v) o[v] = apply<!GATED>(A[i][v], h[v], U[i][v]);
         store_raw((T*)a.h + at + (i64)i * a.D, coff, o);
       }
   if (a.ckpt && rows > 0 && w * R % DCH == 0) {
@@ -420,14 +441,16 @@ __global__ void __launch_bounds__(64 * NW) scan_bwd_kernel(ScanArgs a) {
   const i64 at = (t.start + t0) * a.D + ch0;
   typedef Raw<T, V> raw;
   raw x[R], dh[R];
-  float ai[R][V], u[R][V];                                                            // h = ai h + u
-  float sr[GATED ? R : 1][V], wi[GATED ? R : 1][V], m[GATED ? R : 1][V], rm[GATED ? R : 1][V];
+  float ai[R][V];                                                                    // h = ai h + u
+  float sr[GATED ? R : 1][V], wi[GATED ? R : 1][V], mw[GATED ? R : 1][V];
   float first[V], rate[V], hin[V];
+  Pair f[V];
 #pragma unroll
   for (int v = 0; v < V; ++v) {
     first[v] = a.dh_final ? a.dh_final[t.seq * a.D + ch0 + coff + v] : 0.0f;
     hin[v] = a.kept[t.slot * a.D + ch0 + coff + v];
     if constexpr (GATED) rate[v] = a.decay[ch0 + coff + v];
+    f[v] = {1.0f, 0.0f};
   }
   auto load = [&](auto full) {
     raw r[GATED ? R : 1], ig[GATED ? R : 1];
@@ -446,20 +469,26 @@ __global__ void __launch_bounds__(64 * NW) scan_bwd_kernel(ScanArgs a) {
     }
     if constexpr (GATED)
 #pragma unroll
-      for (int v = 0; v < V; ++v) rate[v] = decay_rate(a.c, rate[v]);
+      for (int v = 0; v < V; ++v) rate[v] = LOG2E * decay_rate(a.c, rate[v]);
 #pragma unroll
-    for (int i = 0; i < R; ++i)
+    for (int i = 0; i < R; ++i) {
 #pragma unroll
       for (int v = 0; v < V; ++v) {
+        float u;
         if constexpr (GATED) {
-          const Token k = gated_token((float)x[i].v[v], (float)r[i].v[v], (float)ig[i].v[v], rate[v]);
-          ai[i][v] = k.a; u[i][v] = k.u; sr[i][v] = k.sr; wi[i][v] = k.w; m[i][v] = k.m; rm[i][v] = k.rm;
+          const Token k = gated_token(x[i].get(v), r[i].get(v), ig[i].get(v), rate[v]);
+          ai[i][v] = k.a; u = k.u; sr[i][v] = k.sr; wi[i][v] = k.w; mw[i][v] = k.mw;
         } else {
           ai[i][v] = exp_hw(g[i].v[v]);
-          u[i][v] = (float)x[i].v[v];
+          u = x[i].get(v);
         }
-        if (!full && i >= rows) ai[i][v] = 1.0f, u[i][v] = 0.0f, dh[i].v[v] = (T)0.0f;
+        if (!full && i >= rows) ai[i][v] = 1.0f, u = 0.0f;
+        f[v].A *= ai[i][v];
+        f[v].H = fmaf(ai[i][v], f[v].H, u);
       }
+      if (!full && i >= rows) dh[i].clear();
+      x[i].pin();
+    }
   };
   if (rows == R) {
     load(std::true_type{});
@@ -467,43 +496,41 @@ __global__ void __launch_bounds__(64 * NW) scan_bwd_kernel(ScanArgs a) {
     load(std::false_type{});
   } else {
 #pragma unroll
-    for (int i = 0; i < R; ++i)
+    for (int i = 0; i < R; ++i) {
+      x[i].clear();
+      dh[i].clear();
 #pragma unroll
       for (int v = 0; v < V; ++v) {
-        ai[i][v] = 1.0f; u[i][v] = 0.0f; x[i].v[v] = dh[i].v[v] = (T)0.0f;
-        if constexpr (GATED) sr[i][v] = wi[i][v] = m[i][v] = rm[i][v] = 0.0f;
+        ai[i][v] = 1.0f;
+        if constexpr (GATED) sr[i][v] = wi[i][v] = mw[i][v] = 0.0f;
       }
+    }
   }
   const int wr = NW - 1 - w;  // the waves in the order of the adjoint
 #pragma unroll
   for (int v = 0; v < V; ++v) {
-    float A = 1.0f, H = 0.0f, B = 0.0f;
+    float B = 0.0f;
 #pragma unroll
-    for (int i = 0; i < R; ++i) {
-      A *= ai[i][v];
-      H = fmaf(ai[i][v], H, u[i][v]);
-    }
-#pragma unroll
-    for (int i = R - 1; i >= 0; --i) B = ai[i][v] * (B + (float)dh[i].v[v]);
-    fseg[w][v][lane] = {A, H};
-    seg[wr][v][lane] = {A, B};
+    for (int i = R - 1; i >= 0; --i) B = ai[i][v] * (B + dh[i].get(v));
+    fseg[w][v][lane] = f[v];
+    seg[wr][v][lane] = {f[v].A, B};
   }
+#pragma unroll
+  for (int i = 0; i < R; ++i) dh[i].pin();
   __syncthreads();
   float b[V];
-  Chain<V> chain{seg, look, base};
+  Chain<V, !GATED> chain{seg, look, base};
   const i64 k = t.n - 1 - t.j;
   chain.enter(a, t.slot, -1, k, t.n, wr, lane, ch0, coff, mine, first, b);
-  float sum[V];
+  float sum[V], prev[R][V];  // h_{t-1}
 #pragma unroll
   for (int v = 0; v < V; ++v) {
     float h = hin[v];
-    for (int i = 0; i < w; ++i) h = apply(fseg[i][v][lane].A, h, fseg[i][v][lane].H);
-    // u becomes h_{t-1}
+    for (int i = 0; i < w; ++i) h = apply<!GATED>(fseg[i][v][lane].A, h, fseg[i][v][lane].H);
 #pragma unroll
     for (int i = 0; i < R; ++i) {
-      const float n = fmaf(ai[i][v], h, u[i][v]);
-      u[i][v] = h;
-      h = n;
+      prev[i][v] = h;
+      h = fmaf(ai[i][v], h, GATED ? mw[GATED ? i : 0][v] * x[i].get(v) : x[i].get(v));
     }
     sum[v] = 0.0f;
   }
@@ -512,18 +539,19 @@ __global__ void __launch_bounds__(64 * NW) scan_bwd_kernel(ScanArgs a) {
     float ox[V], og[V], oi[V];
 #pragma unroll
     for (int v = 0; v < V; ++v) {
-      const float l = (float)dh[i].v[v] + b[v], prev = u[i][v];
+      const float l = dh[i].get(v) + b[v], hp = prev[i][v];
       b[v] = ai[i][v] * l;
       if constexpr (GATED) {
-        const float L = rate[v] * sr[i][v], xv = (float)x[i].v[v], lm = l * m[i][v] * wi[i][v];
-        const float E = l * (wi[i][v] * xv * ai[i][v] * ai[i][v] * (L * rm[i][v]) - L * ai[i][v] * prev);
+        const float La = LN2 * rate[v] * sr[i][v] * ai[i][v], wx = wi[i][v] * x[i].get(v), lm = l * mw[i][v];
+        const float w_m = wi[i][v] * (wi[i][v] * __builtin_amdgcn_rcpf(fmaxf(mw[i][v], MIN_NORMAL)));  // w / m, finite
+        const float E = l * fmaf(La * w_m, ai[i][v] * x[i].get(v), -La * hp);
         ox[v] = lm;
-        oi[v] = lm * xv * (1.0f - wi[i][v]);
+        oi[v] = lm * (x[i].get(v) - wx);
         og[v] = E * (1.0f - sr[i][v]);
         if (i < rows) sum[v] += E;
       } else {
         ox[v] = l;
-        og[v] = b[v] * prev;
+        og[v] = b[v] * hp;
       }
     }
     if (i < rows && mine) {
@@ -604,35 +632,50 @@ struct StepArgs {
   void* h;
 };
 
-template <typename T, bool GATED>
+// V channels per thread.  The state of the named slot is on its way while the wave looks through the earlier requests.
+template <typename T, bool GATED, int V>
 __global__ void __launch_bounds__(256) scan_step_kernel(StepArgs a) {
-  const i64 req = blockIdx.x / a.nblk, ch = (blockIdx.x % a.nblk) * 256 + threadIdx.x;
-  i64 slot = req;
-  if (a.slots) {
-    // every wave looks through the earlier requests for the same slot
-    slot = a.slots[req];
-    bool taken = slot < 0 || slot >= a.nslots;
-    for (i64 j = threadIdx.x & 63; j < req; j += 64) taken |= a.slots[j] == (int)slot;
-    if (__any(taken)) slot = -1;
-  }
-  if (ch >= a.D) return;
-  const i64 e = req * a.D + ch;
-  if (slot < 0) {
-    st((T*)a.h, e, 0.0f);
-    return;
-  }
-  const float x = ld((const T*)a.x, e);
-  Token k{};
+  const i64 req = blockIdx.x / a.nblk, ch = ((blockIdx.x % a.nblk) * 256 + threadIdx.x) * V;
+  const bool mine = ch < a.D;
+  const unsigned coff = mine ? (unsigned)ch : 0;
+  const i64 e = req * a.D;
+  i64 slot = a.slots ? a.slots[req] : req;
+  const bool in = slot >= 0 && slot < a.nslots;
+  float* p = a.state + (in ? slot : 0) * a.D + coff;
+  Raw<T, V> x = load_raw<T, V>((const T*)a.x + e, coff), r, ig;
+  Raw<float, V> g;
   if constexpr (GATED) {
-    k = gated_token(x, ld((const T*)a.gate, e), ld((const T*)a.igate, e), decay_rate(a.c, a.decay[ch]));
+    r = load_raw<T, V>((const T*)a.gate + e, coff);
+    ig = load_raw<T, V>((const T*)a.igate + e, coff);
   } else {
-    k.a = exp_hw(((const float*)a.gate)[e]);
-    k.u = x;
+    g = load_raw<float, V>((const float*)a.gate + e, coff);
   }
-  float* p = a.state + slot * a.D + ch;
-  const float h = fmaf(k.a, *p, k.u);
-  *p = h;
-  st((T*)a.h, e, h);
+  float s[V], o[V];
+#pragma unroll
+  for (int v = 0; v < V; ++v) s[v] = a.nslots > 0 ? p[v] : 0.0f;
+  bool dead = !in;
+  if (a.slots && in) {
+    bool taken = false;
+#pragma unroll 4
+    for (i64 j = threadIdx.x & 63; j < req; j += 64) taken |= a.slots[j] == (int)slot;
+    dead = __any(taken);
+  }
+  if (!mine) return;
+#pragma unroll
+  for (int v = 0; v < V; ++v) {
+    float ai, u;
+    if constexpr (GATED) {
+      const Token k = gated_token(x.get(v), r.get(v), ig.get(v), LOG2E * decay_rate(a.c, a.decay[coff + v]));
+      ai = k.a;
+      u = k.u;
+    } else {
+      ai = exp_hw(g.v[v]);
+      u = x.get(v);
+    }
+    o[v] = dead ? 0.0f : fmaf(ai, s[v], u);
+    if (!dead) p[v] = o[v];
+  }
+  store_raw((T*)a.h + e, coff, o);
 }
 
 // ---------------------------------------------------------------------------
@@ -689,6 +732,19 @@ void launch_wide(ScanArgs& a, hipStream_t s) {
   for (const void* p : gates) two &= (uintptr_t)p % (2 * (GATED ? sizeof(T) : 4)) == 0;
   if (two) launch_tiles<T, GATED, 2, BWD>(a, s);
   else launch_tiles<T, GATED, 1, BWD>(a, s);
+}
+
+template <typename T, bool GATED, int V>
+void launch_step_v(StepArgs& a, i64 batch, hipStream_t s) {
+  a.nblk = (a.D + 256 * V - 1) / (256 * V);
+  hipLaunchKernelGGL((scan_step_kernel<T, GATED, V>), dim3((unsigned)(batch * a.nblk)), dim3(256), 0, s, a);
+}
+template <typename T, bool GATED>
+void launch_step(StepArgs& a, i64 batch, hipStream_t s) {
+  const bool two = a.D % 2 == 0 && (uintptr_t)a.x % (2 * sizeof(T)) == 0 && (uintptr_t)a.h % (2 * sizeof(T)) == 0 &&
+                   (uintptr_t)a.igate % (2 * sizeof(T)) == 0 && (uintptr_t)a.gate % (2 * (GATED ? sizeof(T) : 4)) == 0;
+  if (two) launch_step_v<T, GATED, 2>(a, batch, s);
+  else launch_step_v<T, GATED, 1>(a, batch, s);
 }
 
 template <bool BWD>
@@ -760,16 +816,10 @@ hipError_t launch_linear_scan_bwd(const ssmvjp_linear_scan_desc& d, const Linear
 }
 
 hipError_t launch_linear_step(const ssmvjp_linear_step_desc& d, const LinearStepPointers& p, hipStream_t stream) {
-  const StepArgs a{d.nslots, d.dim, (d.dim + 255) / 256, d.c, p.x, p.gate, p.input_gate, p.decay, p.state, p.slots, p.h};
-  const dim3 grid((unsigned)(d.batch * a.nblk));
+  StepArgs a{d.nslots, d.dim, 0, d.c, p.x, p.gate, p.input_gate, p.decay, p.state, p.slots, p.h};
   const bool gated = d.form == SSMVJP_SCAN_GATED;
-  if (d.dtype == SSMVJP_BF16) {
-    if (gated) hipLaunchKernelGGL((scan_step_kernel<bf16, true>), grid, dim3(256), 0, stream, a);
-    else hipLaunchKernelGGL((scan_step_kernel<bf16, false>), grid, dim3(256), 0, stream, a);
-  } else {
-    if (gated) hipLaunchKernelGGL((scan_step_kernel<float, true>), grid, dim3(256), 0, stream, a);
-    else hipLaunchKernelGGL((scan_step_kernel<float, false>), grid, dim3(256), 0, stream, a);
-  }
+  if (d.dtype == SSMVJP_BF16) gated ? launch_step<bf16, true>(a, d.batch, stream) : launch_step<bf16, false>(a, d.batch, stream);
+  else gated ? launch_step<float, true>(a, d.batch, stream) : launch_step<float, false>(a, d.batch, stream);
   return hipGetLastError();
 }
 
