@@ -496,7 +496,7 @@ typedef struct {
  *   no token has are zeros.  linear_scan_bwd reads it in place of a second forward pass.
  * The state and every sum are float32.  gate = -infinity (log form) is a reset.  A NaN or
  * an infinity reaches the tokens behind it in its channel, and nothing else.
- * Constraints: dim below 2^28, and launches of fewer than 2^32 threads:
+ * Constraints: dim below 2^24, and launches of fewer than 2^32 threads:
  * (tokens/64 + batch + 1) * (dim/64 + 1) below 2^23 (SSMVJP_EUNSUPPORTED otherwise).
  * Pointers aligned to their elements; even dims on tensors aligned to two elements are the
  * fast ones.  h_final must not be h0 (SSMVJP_EINVAL). */
@@ -534,7 +534,7 @@ typedef struct {
  *   and written;  slots [batch] int32 in device memory (NULL: request i uses state i)
  * Output: h [batch, dim] (dtype).
  * A request whose slot is outside [0, nslots) or was named by an earlier request of the
- * call gets zeros in h and touches no state.  dim below 2^28, batch * (dim/256 + 1) below
+ * call gets zeros in h and touches no state.  dim below 2^24, batch * (dim/256 + 1) below
  * 2^24 (SSMVJP_EUNSUPPORTED otherwise). */
 ssmvjp_status linear_scan_step_workspace(const ssmvjp_linear_step_desc* desc, size_t* bytes);
 ssmvjp_status linear_scan_step(const ssmvjp_linear_step_desc* desc,

@@ -26,7 +26,7 @@ ssmvjp_status workspace_check(size_t need, const void* workspace, size_t workspa
 ssmvjp_status scan_form_check(int32_t form, int32_t dtype, float c, int64_t dim) {
   if (dim <= 0 || !valid_dtype(dtype) || (form != SSMVJP_SCAN_LOG && form != SSMVJP_SCAN_GATED)) return SSMVJP_EINVAL;
   if (form == SSMVJP_SCAN_GATED && !(c > 0.0f && c <= 3.402823466e38f)) return SSMVJP_EINVAL;  // also NaN
-  return dim >= (1 << 28) ? SSMVJP_EUNSUPPORTED : SSMVJP_OK;  // 32-bit byte offsets inside a token
+  return dim >= (1 << 24) ? SSMVJP_EUNSUPPORTED : SSMVJP_OK;  // 32-bit byte offsets inside a wave's 16 tokens
 }
 
 ssmvjp_status linear_scan_check(const ssmvjp_linear_scan_desc* d) {

@@ -131,29 +131,35 @@ __device__ __forceinline__ bool find_tile(const ScanArgs& a, i64 o, int lane, Ti
 __device__ __forceinline__ float sigmoid_hw(float z) { return __builtin_amdgcn_rcpf(1.0f + exp_hw(-z)); }
 
 // per channel: c softplus(decay), and sigmoid(decay) / softplus(decay) (1 where both go to exp(decay))
-__device__ __forceinline__ float decay_rate(float c, float z) { return c * softplus_f(z); }
+__device__ __forceinline__ float decay_rate(float c, float z) { return c * softplus_hw(z); }
 __device__ __forceinline__ float decay_slope(float z) { return z < -16.0f ? 1.0f : sigmoid_f(z) / softplus_f(z); }
 
 constexpr float MIN_NORMAL = 1.17549435e-38f;  // the reciprocals take denormals as zeros
 
 struct Token {
-  float a, u;              // h = a h + u
-  float lc, sr, w, mw;     // gated form: log2(e) L, sigmoid(r), w, m w
+  float a, u;       // h = a h + u
+  float sr, w, mw;  // gated form: sigmoid(r), w, m w
 };
 
-// rate2: log2(e) c softplus(decay).  m^2 = 1 - a^2 loses what a has rounded away where y = 2 L is small: there the
-// series of 1 - exp(-y), off by 5e-8 of it at most.  m is m^2 / sqrt(m^2) with the root taken of a normal number.
-__device__ __forceinline__ Token gated_token(float x, float r, float i, float rate2) {
-  constexpr float Y = 1.3862943611198906f;  // y = Y lc
+// rate2: log2(e) c softplus(decay).  m^2 = 1 - a^2 loses what a has rounded away where y = 2 L = Y lc is small: there the
+// series of 1 - exp(-y) in lc, off by 5e-8 of it at most.
+// top: the series' last coefficient, in a register that the caller keeps.
+constexpr float Y = 1.3862943611198906f;
+__device__ __forceinline__ float series_top() {
+  float c6 = -Y * Y * Y * Y * Y * Y / 720;
+  asm volatile("" : "+v"(c6));
+  return c6;
+}
+__device__ __forceinline__ Token gated_token(float x, float r, float i, float rate2, float top) {
   Token t;
   t.sr = sigmoid_hw(r);
   t.w = sigmoid_hw(i);
-  t.lc = rate2 * t.sr;
-  t.a = __builtin_amdgcn_exp2f(-t.lc);
-  const float y = Y * t.lc;
-  const float series = y * fmaf(y, fmaf(y, fmaf(y, fmaf(y, fmaf(y, -1.0f / 720, 1.0f / 120), -1.0f / 24), 1.0f / 6), -0.5f), 1.0f);
-  const float m2 = y < 0.25f ? series : fmaf(-t.a, t.a, 1.0f);
-  t.mw = m2 * __builtin_amdgcn_rsqf(fmaxf(m2, MIN_NORMAL)) * t.w;
+  const float lc = rate2 * t.sr;
+  t.a = __builtin_amdgcn_exp2f(-lc);
+  constexpr float c2 = -Y * Y / 2, c3 = Y * Y * Y / 6, c4 = -Y * Y * Y * Y / 24, c5 = Y * Y * Y * Y * Y / 120;
+  const float series = lc * fmaf(lc, fmaf(lc, fmaf(lc, fmaf(lc, fmaf(lc, top, c5), c4), c3), c2), Y);
+  const float m2 = lc < 0.25f / Y ? series : fmaf(-t.a, t.a, 1.0f);
+  t.mw = __builtin_amdgcn_sqrtf(m2) * t.w;
   t.u = t.mw * x;
   return t;
 }
@@ -190,18 +196,42 @@ struct Raw<bf16, 2> {
 template <typename T, int V>
 __device__ __forceinline__ Raw<T, V> load_raw(const T* row, unsigned off) {
   Raw<T, V> r;
-  __builtin_memcpy(&r, __builtin_assume_aligned(row + off, V * sizeof(T)), V * sizeof(T));
+  __builtin_memcpy(&r, __builtin_assume_aligned((const char*)row + off * (unsigned)sizeof(T), V * sizeof(T)), V * sizeof(T));
   return r;
+}
+// the same from row `row` of a workgroup's rows: the row's offset in a scalar register, nothing to add per lane
+template <typename T, int V>
+__device__ __forceinline__ Raw<T, V> load_row(brsrc rs, unsigned off, unsigned row) {
+  constexpr int B = V * (int)sizeof(T);
+  Raw<T, V> r;
+  if constexpr (B == 2) {
+    const unsigned short w = __builtin_amdgcn_raw_buffer_load_b16(rs, (int)(off * sizeof(T)), (int)row, 0);
+    __builtin_memcpy(&r, &w, B);
+  } else if constexpr (B == 4) {
+    const unsigned w = __builtin_amdgcn_raw_buffer_load_b32(rs, (int)(off * sizeof(T)), (int)row, 0);
+    __builtin_memcpy(&r, &w, B);
+  } else {
+    const auto w = __builtin_amdgcn_raw_buffer_load_b64(rs, (int)(off * sizeof(T)), (int)row, 0);
+    __builtin_memcpy(&r, &w, B);
+  }
+  return r;
+}
+// rows of T from element e on; what is read there is the caller's to keep inside
+template <typename T>
+__device__ __forceinline__ brsrc rows_at(const void* p, i64 e) {
+  return make_rsrc((const T*)p + e, 0x7fffffffu);
 }
 template <int V>
 __device__ __forceinline__ void store_raw(bf16* row, unsigned off, const float (&v)[V]) {
-  if constexpr (V == 2) *(unsigned*)(row + off) = pk_bf16(v[0], v[1]);
-  else row[off] = (bf16)v[0];
+  char* p = (char*)row + off * 2u;
+  if constexpr (V == 2) *(unsigned*)p = pk_bf16(v[0], v[1]);
+  else *(bf16*)p = (bf16)v[0];
 }
 template <int V>
 __device__ __forceinline__ void store_raw(float* row, unsigned off, const float (&v)[V]) {
-  if constexpr (V == 2) *(float2*)(row + off) = make_float2(v[0], v[1]);
-  else row[off] = v[0];
+  char* p = (char*)row + off * 4u;
+  if constexpr (V == 2) *(float2*)p = make_float2(v[0], v[1]);
+  else *(float*)p = v[0];
 }
 
 // ---------------------------------------------------------------------------
@@ -345,17 +375,20 @@ __global__ void __launch_bounds__(64 * NW) scan_fwd_kernel(ScanArgs a) {
   auto scan = [&](auto full) {
     raw x[R], r[GATED ? R : 1], ig[GATED ? R : 1];
     rawf g[GATED ? 1 : R];
+    const brsrc bx = rows_at<T>(a.x, at), bg = GATED ? rows_at<T>(a.gate, at) : rows_at<float>(a.gate, at);
+    const brsrc bi = rows_at<T>(GATED ? a.igate : a.x, at);
 #pragma unroll
     for (int i = 0; i < R; ++i) {
-      const i64 e = at + (i64)(full || i < rows ? i : rows - 1) * a.D;
+      const unsigned row = (unsigned)(full || i < rows ? i : rows - 1) * (unsigned)a.D, o = row * (unsigned)sizeof(T);
       if constexpr (GATED) {
-        r[i] = load_raw<T, V>((const T*)a.gate + e, coff);
-        ig[i] = load_raw<T, V>((const T*)a.igate + e, coff);
+        r[i] = load_row<T, V>(bg, coff, o);
+        ig[i] = load_row<T, V>(bi, coff, o);
       } else {
-        g[i] = load_raw<float, V>((const float*)a.gate + e, coff);
+        g[i] = load_row<float, V>(bg, coff, row * 4u);
       }
-      x[i] = load_raw<T, V>((const T*)a.x + e, coff);
+      x[i] = load_row<T, V>(bx, coff, o);
     }
+    const float top = GATED ? series_top() : 0.0f;
     if constexpr (GATED)
 #pragma unroll
       for (int v = 0; v < V; ++v) rate[v] = LOG2E * decay_rate(a.c, rate[v]);
@@ -365,7 +398,7 @@ __global__ void __launch_bounds__(64 * NW) scan_fwd_kernel(ScanArgs a) {
       for (int v = 0; v < V; ++v) {
         float ai, u;
         if constexpr (GATED) {
-          const Token k = gated_token(x[i].get(v), r[i].get(v), ig[i].get(v), rate[v]);
+          const Token k = gated_token(x[i].get(v), r[i].get(v), ig[i].get(v), rate[v], top);
           ai = k.a;
           u = k.u;
         } else {
@@ -455,18 +488,21 @@ __global__ void __launch_bounds__(64 * NW) scan_bwd_kernel(ScanArgs a) {
   auto load = [&](auto full) {
     raw r[GATED ? R : 1], ig[GATED ? R : 1];
     Raw<float, V> g[GATED ? 1 : R];
+    const brsrc bx = rows_at<T>(a.x, at), bg = GATED ? rows_at<T>(a.gate, at) : rows_at<float>(a.gate, at);
+    const brsrc bi = rows_at<T>(GATED ? a.igate : a.x, at), bd = rows_at<T>(a.dh, at);
 #pragma unroll
     for (int i = 0; i < R; ++i) {
-      const i64 e = at + (i64)(full || i < rows ? i : rows - 1) * a.D;
+      const unsigned row = (unsigned)(full || i < rows ? i : rows - 1) * (unsigned)a.D, o = row * (unsigned)sizeof(T);
       if constexpr (GATED) {
-        r[i] = load_raw<T, V>((const T*)a.gate + e, coff);
-        ig[i] = load_raw<T, V>((const T*)a.igate + e, coff);
+        r[i] = load_row<T, V>(bg, coff, o);
+        ig[i] = load_row<T, V>(bi, coff, o);
       } else {
-        g[i] = load_raw<float, V>((const float*)a.gate + e, coff);
+        g[i] = load_row<float, V>(bg, coff, row * 4u);
       }
-      x[i] = load_raw<T, V>((const T*)a.x + e, coff);
-      dh[i] = load_raw<T, V>((const T*)a.dh + e, coff);
+      x[i] = load_row<T, V>(bx, coff, o);
+      dh[i] = load_row<T, V>(bd, coff, o);
     }
+    const float top = GATED ? series_top() : 0.0f;
     if constexpr (GATED)
 #pragma unroll
       for (int v = 0; v < V; ++v) rate[v] = LOG2E * decay_rate(a.c, rate[v]);
@@ -476,7 +512,7 @@ __global__ void __launch_bounds__(64 * NW) scan_bwd_kernel(ScanArgs a) {
       for (int v = 0; v < V; ++v) {
         float u;
         if constexpr (GATED) {
-          const Token k = gated_token(x[i].get(v), r[i].get(v), ig[i].get(v), rate[v]);
+          const Token k = gated_token(x[i].get(v), r[i].get(v), ig[i].get(v), rate[v], top);
           ai[i][v] = k.a; u = k.u; sr[i][v] = k.sr; wi[i][v] = k.w; mw[i][v] = k.mw;
         } else {
           ai[i][v] = exp_hw(g[i].v[v]);
@@ -665,7 +701,7 @@ __global__ void __launch_bounds__(256) scan_step_kernel(StepArgs a) {
   for (int v = 0; v < V; ++v) {
     float ai, u;
     if constexpr (GATED) {
-      const Token k = gated_token(x.get(v), r.get(v), ig.get(v), LOG2E * decay_rate(a.c, a.decay[coff + v]));
+      const Token k = gated_token(x.get(v), r.get(v), ig.get(v), LOG2E * decay_rate(a.c, a.decay[coff + v]), series_top());
       ai = k.a;
       u = k.u;
     } else {
