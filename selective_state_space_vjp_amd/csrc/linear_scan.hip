@@ -24,9 +24,11 @@
 //     that results do not depend on which tile ran when.
 // Pairs and states are published as single 64- and 32-bit words past the L2s
 // (device-scope atomics) over a filling that no published value has, so a value
-// that is there is whole and no fence is needed.  Tiles are handed out by a
-// counter in the order of the sequence: what a tile waits for was handed out
-// before it, to a workgroup that is running.
+// that is there is whole and no fence is needed.  The tiles of a channel slab
+// are handed out by a counter in the order of the sequence: what a tile waits
+// for was handed out before it, to a workgroup that is running.  A counter for
+// every slab, since additions to one address take 11.5 ns each: one counter for
+// all cost 47 of 118 us of the backward at b=2 T=4096 D=4096.
 #include <type_traits>
 
 #include "common.cuh"
@@ -67,8 +69,10 @@ struct ScanArgs {
   // what tiles tell each other
   u64* pairs;        // [ntiles][D]
   unsigned* states;  // [ntiles / GROUP + 1][D]
-  unsigned* ticket;
+  unsigned* tickets; // one every TICKET words
 };
+
+constexpr int TICKET = 32;
 
 // Tile slots of N tokens each: a packed sequence s owns those from start / N + s, which never meet the next one's
 // (see delta_seq.cuh).
@@ -199,19 +203,20 @@ __device__ __forceinline__ Raw<T, V> load_raw(const T* row, unsigned off) {
   __builtin_memcpy(&r, __builtin_assume_aligned((const char*)row + off * (unsigned)sizeof(T), V * sizeof(T)), V * sizeof(T));
   return r;
 }
-// the same from row `row` of a workgroup's rows: the row's offset in a scalar register, nothing to add per lane
-template <typename T, int V>
+// the same from row `row` of a workgroup's rows: the row's offset in a scalar register, nothing to add per lane.
+// STREAM: past the caches' normal order, for what is read once
+template <typename T, int V, bool STREAM>
 __device__ __forceinline__ Raw<T, V> load_row(brsrc rs, unsigned off, unsigned row) {
-  constexpr int B = V * (int)sizeof(T);
+  constexpr int B = V * (int)sizeof(T), AUX = STREAM ? 2 : 0;  // nt
   Raw<T, V> r;
   if constexpr (B == 2) {
-    const unsigned short w = __builtin_amdgcn_raw_buffer_load_b16(rs, (int)(off * sizeof(T)), (int)row, 0);
+    const unsigned short w = __builtin_amdgcn_raw_buffer_load_b16(rs, (int)(off * sizeof(T)), (int)row, AUX);
     __builtin_memcpy(&r, &w, B);
   } else if constexpr (B == 4) {
-    const unsigned w = __builtin_amdgcn_raw_buffer_load_b32(rs, (int)(off * sizeof(T)), (int)row, 0);
+    const unsigned w = __builtin_amdgcn_raw_buffer_load_b32(rs, (int)(off * sizeof(T)), (int)row, AUX);
     __builtin_memcpy(&r, &w, B);
   } else {
-    const auto w = __builtin_amdgcn_raw_buffer_load_b64(rs, (int)(off * sizeof(T)), (int)row, 0);
+    const auto w = __builtin_amdgcn_raw_buffer_load_b64(rs, (int)(off * sizeof(T)), (int)row, AUX);
     __builtin_memcpy(&r, &w, B);
   }
   return r;
@@ -336,18 +341,19 @@ struct Chain {
 
 template <int N, bool REV>
 __device__ __forceinline__ bool take_tile(const ScanArgs& a, int lane, unsigned* shared, Tile& t, int& slab) {
-  unsigned o = blockIdx.x;
+  unsigned i = blockIdx.x / (unsigned)a.nslab;
+  slab = (int)(blockIdx.x - i * (unsigned)a.nslab);
   if (a.chain) {
-    if (threadIdx.x == 0) *shared = __hip_atomic_fetch_add(a.ticket, 1u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+    // from the filling, ~0, on
+    if (threadIdx.x == 0)
+      *shared = __hip_atomic_fetch_add(a.tickets + (i64)slab * TICKET, 1u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT) + 1u;
     __syncthreads();
-    o = (unsigned)__builtin_amdgcn_readfirstlane((int)*shared);
+    i = (unsigned)__builtin_amdgcn_readfirstlane((int)*shared);
   }
-  const unsigned i = o / (unsigned)a.nslab;
-  slab = (int)(o - i * (unsigned)a.nslab);
   return find_tile<N, REV>(a, i, lane, t);
 }
 
-template <typename T, bool GATED, int V>
+template <typename T, bool GATED, int V, bool STREAM>
 __global__ void __launch_bounds__(64 * NW) scan_fwd_kernel(ScanArgs a) {
   constexpr int R = FWD_ROWS, N = R * NW;
   __shared__ Pair seg[NW][V][64], look[NW][V][64];
@@ -363,82 +369,71 @@ __global__ void __launch_bounds__(64 * NW) scan_fwd_kernel(ScanArgs a) {
   const int rows = t0 >= t.len ? 0 : t.len - t0 < R ? (int)(t.len - t0) : R;
   const i64 at = (t.start + t0) * a.D + ch0;
 
-  float A[R][V], U[R][V];  // per row: products of a and states from the segment's start on
   typedef Raw<T, V> raw;
-  typedef Raw<float, V> rawf;
+  raw x[R];
+  float ai[R][V], ui[GATED ? R : 1][V];  // h = ai h + ui (log form: ui is x)
   float first[V], rate[V];
+  Pair f[V];
 #pragma unroll
   for (int v = 0; v < V; ++v) {
     first[v] = a.h0 ? a.h0[t.seq * a.D + ch0 + coff + v] : 0.0f;
     if constexpr (GATED) rate[v] = a.decay[ch0 + coff + v];
+    f[v] = {1.0f, 0.0f};
   }
   auto scan = [&](auto full) {
-    raw x[R], r[GATED ? R : 1], ig[GATED ? R : 1];
-    rawf g[GATED ? 1 : R];
+    raw r[GATED ? R : 1], ig[GATED ? R : 1];
+    Raw<float, V> g[GATED ? 1 : R];
     const brsrc bx = rows_at<T>(a.x, at), bg = GATED ? rows_at<T>(a.gate, at) : rows_at<float>(a.gate, at);
     const brsrc bi = rows_at<T>(GATED ? a.igate : a.x, at);
 #pragma unroll
     for (int i = 0; i < R; ++i) {
       const unsigned row = (unsigned)(full || i < rows ? i : rows - 1) * (unsigned)a.D, o = row * (unsigned)sizeof(T);
       if constexpr (GATED) {
-        r[i] = load_row<T, V>(bg, coff, o);
-        ig[i] = load_row<T, V>(bi, coff, o);
+        r[i] = load_row<T, V, STREAM>(bg, coff, o);
+        ig[i] = load_row<T, V, STREAM>(bi, coff, o);
       } else {
-        g[i] = load_row<float, V>(bg, coff, row * 4u);
+        g[i] = load_row<float, V, STREAM>(bg, coff, row * 4u);
       }
-      x[i] = load_row<T, V>(bx, coff, o);
+      x[i] = load_row<T, V, STREAM>(bx, coff, o);
     }
     const float top = GATED ? series_top() : 0.0f;
     if constexpr (GATED)
 #pragma unroll
       for (int v = 0; v < V; ++v) rate[v] = LOG2E * decay_rate(a.c, rate[v]);
 #pragma unroll
-    for (int i = 0; i < R; ++i)
+    for (int i = 0; i < R; ++i) {
 #pragma unroll
       for (int v = 0; v < V; ++v) {
-        float ai, u;
+        float u;
         if constexpr (GATED) {
           const Token k = gated_token(x[i].get(v), r[i].get(v), ig[i].get(v), rate[v], top);
-          ai = k.a;
-          u = k.u;
+          ai[i][v] = k.a;
+          ui[i][v] = u = k.u;
         } else {
-          ai = exp_hw(g[i].v[v]);
+          ai[i][v] = exp_hw(g[i].v[v]);
           u = x[i].get(v);
         }
-        if (!full && i >= rows) ai = 1.0f, u = 0.0f;
-        A[i][v] = i ? A[i - 1][v] * ai : ai;
-        U[i][v] = fmaf(ai, i ? U[i - 1][v] : 0.0f, u);
+        if (full || i < rows) {
+          f[v].A *= ai[i][v];
+          f[v].H = fmaf(ai[i][v], f[v].H, u);
+        }
       }
+      x[i].pin();
+    }
   };
-  if (rows == R) {
-    scan(std::true_type{});
-  } else if (rows > 0) {
-    scan(std::false_type{});
-  } else {
+  if (rows == R) scan(std::true_type{});
+  else if (rows > 0) scan(std::false_type{});
 #pragma unroll
-    for (int i = 0; i < R; ++i)
-#pragma unroll
-      for (int v = 0; v < V; ++v) A[i][v] = 1.0f, U[i][v] = 0.0f;
-  }
-#pragma unroll
-  for (int v = 0; v < V; ++v) seg[w][v][lane] = {A[R - 1][v], U[R - 1][v]};
+  for (int v = 0; v < V; ++v) seg[w][v][lane] = f[v];
   __syncthreads();
   float h[V], last[V];
   Chain<V, !GATED> chain{seg, look, base};
   chain.enter(a, t.slot, 1, t.j, t.n, w, lane, ch0, coff, mine, first, h);
+  // the state behind the tile first: the next group waits for it
 #pragma unroll
-  for (int v = 0; v < V; ++v) last[v] = apply<!GATED>(A[R - 1][v], h[v], U[R - 1][v]);
+  for (int v = 0; v < V; ++v) last[v] = apply<!GATED>(f[v].A, h[v], f[v].H);
   chain.leave(a, t.slot, t.j, t.n, w, ch0, coff, mine, last);
   if (!mine) return;
-  if (a.h)
-#pragma unroll
-    for (int i = 0; i < R; ++i)
-      if (i < rows) {
-        float o[V];
-#pragma unroll
-        for (int v = 0; v < V; ++v) o[v] = apply<!GATED>(A[i][v], h[v], U[i][v]);
-        store_raw((T*)a.h + at + (i64)i * a.D, coff, o);
-      }
   if (a.ckpt && rows > 0 && w * R % DCH == 0) {
     const i64 row = (a.off ? t.start / DCH + t.seq : t.seq * ((a.T + DCH - 1) / DCH)) + t0 / DCH;
 #pragma unroll
@@ -447,11 +442,19 @@ __global__ void __launch_bounds__(64 * NW) scan_fwd_kernel(ScanArgs a) {
   if (a.h_final && w == NW - 1 && t.j == t.n - 1)
 #pragma unroll
     for (int v = 0; v < V; ++v) a.h_final[t.seq * a.D + ch0 + coff + v] = last[v];
+  if (!a.h) return;
+#pragma unroll
+  for (int i = 0; i < R; ++i)
+    if (i < rows) {
+#pragma unroll
+      for (int v = 0; v < V; ++v) h[v] = fmaf(ai[i][v], h[v], GATED ? ui[GATED ? i : 0][v] : x[i].get(v));
+      store_raw((T*)a.h + at + (i64)i * a.D, coff, h);
+    }
 }
 
 // A wave's rows: forward from the state before the tile (kept by the forward pass), backward from the gradient of the
 // state behind it.  b_t = a_t l_t, the gradient that reaches h_{t-1}, obeys b_t = a_t b_{t+1} + a_t dh_t.
-template <typename T, bool GATED, int V>
+template <typename T, bool GATED, int V, bool STREAM>
 __global__ void __launch_bounds__(64 * NW) scan_bwd_kernel(ScanArgs a) {
   constexpr int R = BWD_ROWS, N = R * NW;
   static_assert(N == DCH, "a tile of the backward starts at a kept state");
@@ -494,13 +497,13 @@ __global__ void __launch_bounds__(64 * NW) scan_bwd_kernel(ScanArgs a) {
     for (int i = 0; i < R; ++i) {
       const unsigned row = (unsigned)(full || i < rows ? i : rows - 1) * (unsigned)a.D, o = row * (unsigned)sizeof(T);
       if constexpr (GATED) {
-        r[i] = load_row<T, V>(bg, coff, o);
-        ig[i] = load_row<T, V>(bi, coff, o);
+        r[i] = load_row<T, V, STREAM>(bg, coff, o);
+        ig[i] = load_row<T, V, STREAM>(bi, coff, o);
       } else {
-        g[i] = load_row<float, V>(bg, coff, row * 4u);
+        g[i] = load_row<float, V, STREAM>(bg, coff, row * 4u);
       }
-      x[i] = load_row<T, V>(bx, coff, o);
-      dh[i] = load_row<T, V>(bd, coff, o);
+      x[i] = load_row<T, V, STREAM>(bx, coff, o);
+      dh[i] = load_row<T, V, STREAM>(bd, coff, o);
     }
     const float top = GATED ? series_top() : 0.0f;
     if constexpr (GATED)
@@ -625,10 +628,9 @@ __global__ void __launch_bounds__(64 * NW) scan_bwd_kernel(ScanArgs a) {
 
 // Before a call whose tiles wait for each other: the filling of what they publish, and the counter.  Sequences without
 // tokens, which have no tile: their final state (`to`) is their first (`from`).  Rows of ckpt that no token has: zeros.
-__global__ void __launch_bounds__(256) scan_init_kernel(u64* pairs, i64 words, unsigned* ticket, const int* off, i64 nseq,
-                                                        i64 T, i64 D, const float* from, float* to, float* clear, i64 nclear) {
+__global__ void __launch_bounds__(256) scan_init_kernel(u64* pairs, i64 words, const int* off, i64 nseq, i64 T, i64 D,
+                                                        const float* from, float* to, float* clear, i64 nclear) {
   const i64 i0 = (i64)blockIdx.x * 256 + threadIdx.x, step = (i64)gridDim.x * 256;
-  if (ticket && i0 == 0) *ticket = 0u;
   for (i64 i = i0; i < words; i += step) pairs[i] = NO_PAIR;
   for (i64 i = i0; i < nclear; i += step) clear[i] = 0.0f;
   if (!to) return;
@@ -650,6 +652,7 @@ __global__ void __launch_bounds__(1024) decay_sum_kernel(const float* part, i64 
   const int run = threadIdx.x >> 6;
   float sum = 0.0f;
   if (ch < D)
+#pragma unroll 8
     for (i64 i = run * each; i < n && i < (run + 1) * each; ++i) sum += part[i * D + ch];
   runs[run][threadIdx.x & 63] = sum;
   __syncthreads();
@@ -724,11 +727,11 @@ i64 tile_slots(const ssmvjp_linear_scan_desc& d, int n) {
 bool chained(const ssmvjp_linear_scan_desc& d, int n) { return d.seqlen > n; }
 
 i64 round64(i64 n) { return (n + 63) / 64 * 64; }
-// words of 8 bytes: the pairs, the states, the counter
+// words of 8 bytes: the pairs, the states, the counters
 i64 chain_words(const ssmvjp_linear_scan_desc& d, int n) {
   if (!chained(d, n)) return 0;
   const i64 slots = tile_slots(d, n);
-  return slots * d.dim + ((slots / GROUP + 1) * d.dim + 1) / 2 + 32;
+  return slots * d.dim + ((slots / GROUP + 1) * d.dim + 1) / 2 + (d.dim + 63) / 64 * (TICKET / 2);
 }
 
 void set_chain(const ssmvjp_linear_scan_desc& d, int n, void* workspace, ScanArgs& a) {
@@ -738,7 +741,7 @@ void set_chain(const ssmvjp_linear_scan_desc& d, int n, void* workspace, ScanArg
   if (!a.chain) return;
   a.pairs = (u64*)workspace;
   a.states = (unsigned*)(a.pairs + a.ntiles * d.dim);
-  a.ticket = (unsigned*)(a.pairs + chain_words(d, n) - 1);
+  a.tickets = (unsigned*)(a.pairs + chain_words(d, n) - (d.dim + 63) / 64 * (TICKET / 2));
 }
 
 void launch_init(const ScanArgs& a, i64 words, const float* from, float* to, float* clear, i64 nclear, hipStream_t s) {
@@ -746,17 +749,21 @@ void launch_init(const ScanArgs& a, i64 words, const float* from, float* to, flo
   i64 most = words > nclear ? words : nclear;
   if (to && a.nseq * a.D > most) most = a.nseq * a.D;
   const i64 blocks = (most + 1023) / 1024 < 2048 ? (most + 1023) / 1024 : 2048;
-  hipLaunchKernelGGL(scan_init_kernel, dim3((unsigned)(blocks > 0 ? blocks : 1)), dim3(256), 0, s, a.pairs, words > 0 ? words - 1 : 0,
-                     a.ticket, a.off, a.nseq, a.T, a.D, from, to, clear, nclear);
+  hipLaunchKernelGGL(scan_init_kernel, dim3((unsigned)(blocks > 0 ? blocks : 1)), dim3(256), 0, s, a.pairs, words, a.off, a.nseq, a.T, a.D, from, to, clear, nclear);
 }
 
-template <typename T, bool GATED, int V, bool BWD>
+template <typename T, bool GATED, int V, bool BWD, bool STREAM>
 void launch_tiles(ScanArgs& a, hipStream_t s) {
   a.nslab = (int)((a.D + 64 * V - 1) / (64 * V));
   const dim3 grid((unsigned)(a.ntiles * a.nslab));
-  if constexpr (BWD) hipLaunchKernelGGL((scan_bwd_kernel<T, GATED, V>), grid, dim3(64 * NW), 0, s, a);
-  else hipLaunchKernelGGL((scan_fwd_kernel<T, GATED, V>), grid, dim3(64 * NW), 0, s, a);
+  if constexpr (BWD) hipLaunchKernelGGL((scan_bwd_kernel<T, GATED, V, STREAM>), grid, dim3(64 * NW), 0, s, a);
+  else hipLaunchKernelGGL((scan_fwd_kernel<T, GATED, V, STREAM>), grid, dim3(64 * NW), 0, s, a);
 }
+
+// Inputs of more than this are read with the streaming hint: what was written just before is then out of the caches
+// anyway (one sequence of D=4096 gated, backward: 240 -> 228 us for 512 MB read; 63.8 -> 64.5 for 128 MB, 74.1 -> 77.0
+// for 93 MB where the states are formed again first and the second pass finds the inputs in the caches).
+constexpr i64 STREAM_BYTES = 128 << 20;
 
 // Two channels per lane where every row starts at a multiple of two elements: 4 bytes of bf16 a load.
 template <typename T, bool GATED, bool BWD>
@@ -766,8 +773,11 @@ void launch_wide(ScanArgs& a, hipStream_t s) {
   bool two = a.D % 2 == 0;
   for (const void* p : big) two &= (uintptr_t)p % (2 * sizeof(T)) == 0;
   for (const void* p : gates) two &= (uintptr_t)p % (2 * (GATED ? sizeof(T) : 4)) == 0;
-  if (two) launch_tiles<T, GATED, 2, BWD>(a, s);
-  else launch_tiles<T, GATED, 1, BWD>(a, s);
+  const i64 read = (a.off ? a.T : a.nseq * a.T) * a.D * (i64)((GATED ? 3 * sizeof(T) : sizeof(T) + 4) + (BWD ? sizeof(T) : 0));
+  const bool stream = read > STREAM_BYTES;
+  if (!two) launch_tiles<T, GATED, 1, BWD, false>(a, s);
+  else if (stream) launch_tiles<T, GATED, 2, BWD, true>(a, s);
+  else launch_tiles<T, GATED, 2, BWD, false>(a, s);
 }
 
 template <typename T, bool GATED, int V>
