@@ -446,17 +446,23 @@ struct GemmPlan {
   int tile, split;
 };
 
+// Which tile, and into how many parts k is cut.  The large one where it fills the 256 CUs by itself (4096 x 2048 -> 8192
+// dw: 278 us, 327 with 128 x 128) or with k cut into long parts (dx of the same: 317, uncut 446, 128 x 128 347; of 1024 x
+// 4096 -> 12288: 215, 552, 270).  Else 128 x 128, of which a CU holds two, cut until there are 512, in parts of at least
+// 16 steps: a second launch adds them (2048 x 2048 -> 8192 dx: 176 us in two, 209 uncut; 100 x 1024 -> 2048 forward, 16
+// steps: 18.5 in two, 14.9 uncut).  Up to 32 rows are one tile of the small kind.
 GemmPlan gemm_plan(i64 M, i64 N, i64 K, int segs, int items, bool pair, bool few, size_t elem) {
-  const int p = pair ? 2 : 1;
   const i64 steps = segs * ((K * (i64)elem + ROWB - 1) / ROWB);
-  const auto tiles = [&](i64 bm, i64 bn) { return items * ((M + bm - 1) / bm) * ((N * p + bn - 1) / bn); };
-  GemmPlan g{few && M <= 32 ? TILE_FEW : tiles(256, 256) >= 256 ? TILE_LARGE : TILE_MID, 1};
-  const i64 n = g.tile == TILE_FEW ? tiles(32, 64) : tiles(128, 128);
-  if (g.tile != TILE_LARGE && n > 0 && n < 256) {
-    const i64 most = steps / 8 < 512 / n ? steps / 8 : 512 / n;
-    if (most > 1) g.split = (int)most;
-  }
-  return g;
+  const auto tiles = [&](i64 bm, i64 bn) { return items * ((M + bm - 1) / bm) * ((N * (pair ? 2 : 1) + bn - 1) / bn); };
+  const i64 large = tiles(256, 256);
+  if (large >= 256) return {TILE_LARGE, 1};
+  const bool small = few && M <= 32;
+  const i64 n = small ? tiles(32, 64) : tiles(128, 128);
+  if (n == 0) return {TILE_MID, 1};
+  const i64 cut = 256 / large;
+  if (!small && cut * large >= 232 && steps >= 96 * cut) return {TILE_LARGE, (int)cut};
+  const i64 most = steps / 16 < 512 / n ? steps / 16 : 512 / n;
+  return {small ? TILE_FEW : TILE_MID, most > 1 ? (int)most : 1};
 }
 
 size_t part_bytes(const GemmPlan& g, i64 M, i64 N, int items, bool pair) {
