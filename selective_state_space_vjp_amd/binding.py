@@ -947,15 +947,15 @@ def linear_scan_fwd(x, gate, h0=None, *, input_gate=None, decay=None, c=8.0, seq
     desc = _linear_scan_inputs(x, gate, h0, input_gate, decay, c, seq_offsets)
     dev, f32 = x.device, torch.float32
     final, kept = (desc.batch, desc.dim), linear_scan_ckpt_shape(desc)
+    if out is not None:
+        if out.get("h") is None:
+            raise ValueError("out is missing 'h'")
+        _needs(dev, ("out['h']", out["h"], x.dtype, x.shape), ("out['h_final']", out.get("h_final"), f32, final),
+               ("out['ckpt']", out.get("ckpt"), f32, kept))
     with _scope(dev, stream):
         if out is None:
             out = {"h": torch.empty_like(x), "h_final": x.new_empty(final, dtype=f32) if want_final else None,
                    "ckpt": x.new_empty(kept, dtype=f32) if want_ckpt else None}
-        else:
-            if out.get("h") is None:
-                raise ValueError("out is missing 'h'")
-            _needs(dev, ("out['h']", out["h"], x.dtype, x.shape), ("out['h_final']", out.get("h_final"), f32, final),
-                   ("out['ckpt']", out.get("ckpt"), f32, kept))
         args = (x, gate, input_gate, decay, h0, seq_offsets, out["h"], out.get("h_final"), out.get("ckpt"))
         _on_gpu(dev, *args)
         _enqueue("linear_scan_fwd", desc, args, dev, workspace)
@@ -978,18 +978,18 @@ def linear_scan_bwd(x, gate, dh, h0=None, dh_final=None, *, input_gate=None, dec
     gated, final = decay is not None, (desc.batch, desc.dim)
     _needs(dev, ("dh", dh, x.dtype, x.shape), ("dh_final", dh_final, f32, final),
            ("ckpt", ckpt, f32, linear_scan_ckpt_shape(desc)))
+    if out is not None:
+        spec = {"dx": (x.dtype, x.shape), "dgate": (gate.dtype, x.shape)}
+        if gated:
+            spec.update(dinput_gate=(x.dtype, x.shape), ddecay=(f32, decay.shape))
+        _check_out(out, spec, dev)
+        _need(out.get("dh0"), "out['dh0']", f32, final, dev)
     with _scope(dev, stream):
         if out is None:
             out = {"dx": torch.empty_like(x), "dgate": torch.empty_like(gate),
                    "dinput_gate": torch.empty_like(input_gate) if gated else None,
                    "ddecay": torch.empty_like(decay) if gated else None,
                    "dh0": x.new_empty(final, dtype=f32) if want_dh0 else None}
-        else:
-            spec = {"dx": (x.dtype, x.shape), "dgate": (gate.dtype, x.shape)}
-            if gated:
-                spec.update(dinput_gate=(x.dtype, x.shape), ddecay=(f32, decay.shape))
-            _check_out(out, spec, dev)
-            _need(out.get("dh0"), "out['dh0']", f32, final, dev)
         args = (x, gate, input_gate, decay, h0, ckpt, dh, dh_final, seq_offsets, out["dx"], out["dgate"],
                 out.get("dinput_gate") if gated else None, out.get("ddecay") if gated else None, out.get("dh0"))
         _on_gpu(dev, *args)
@@ -1006,16 +1006,22 @@ def linear_scan_step(x, gate, state, *, input_gate=None, decay=None, c=8.0, slot
     i): a request whose slot is outside [0,n) or was named by an earlier request gets zeros and
     touches no state.
     """
-    form, gtype = _scan_form(x, gate, input_gate, decay)
-    _required(state=state)
+    if x is None or gate is None or state is None or (input_gate is None) != (decay is None):
+        _required(x=x, gate=gate, state=state)
+        _scan_form(x, gate, input_gate, decay)
     if x.dim() != 2 or state.dim() != 2:
         raise ValueError("x must be [b,D] and state [n,D]")
-    b, D = x.shape
-    dev, f32 = x.device, torch.float32
-    desc = LinearStepDesc(b, state.shape[0], D, float(c), form, _dtype_code(x), 0)
-    _needs(dev, ("x", x, x.dtype, (b, D)), ("gate", gate, gtype, (b, D)), ("input_gate", input_gate, x.dtype, (b, D)),
-           ("decay", decay, f32, (D,)), ("state", state, f32, (state.shape[0], D)), ("slots", slots, torch.int32, (b,)),
-           ("out", out, x.dtype, (b, D)))
+    xs, n, dtype = x.shape, state.shape[0], x.dtype
+    b, D = xs
+    dev, f32, gated = x.device, torch.float32, decay is not None
+    ds, ss, gtype = (D,), (n, D), dtype if gated else f32
+    # one comparison after the other, as in delta_step: a call is made once per token
+    if not (_fits(x, dtype, xs) and _fits(gate, gtype, xs) and _fits(state, f32, ss)
+            and (not gated or (_fits(input_gate, dtype, xs) and _fits(decay, f32, ds)))
+            and (slots is None or _fits(slots, torch.int32, (b,))) and (out is None or _fits(out, dtype, xs))):
+        _needs(dev, ("x", x, dtype, xs), ("gate", gate, gtype, xs), ("input_gate", input_gate, dtype, xs),
+               ("decay", decay, f32, ds), ("state", state, f32, ss), ("slots", slots, torch.int32, (b,)), ("out", out, dtype, xs))
+    desc = LinearStepDesc(b, n, D, c, SCAN_GATED if gated else SCAN_LOG, _dtype_code(x), 0)
     with _scope(dev, stream):
         h = torch.empty_like(x) if out is None else out
         args = (x, gate, input_gate, decay, state, slots, h)
@@ -1054,12 +1060,12 @@ def gated_ffn_fwd(x, w_gate, w_up, *, act="silu", want_saved=False, out=None, wo
     """
     desc, shape = _ffn_inputs(x, w_gate, w_up, act)
     dev, dtype = x.device, x.dtype
+    if out is not None:
+        _check_out(out, {n: (dtype, shape) for n in (("h", "gate", "up") if want_saved else ("h",))}, dev)
     with _scope(dev, stream):
         if out is None:
             h = x.new_empty(shape)
             out = {"h": h, "gate": torch.empty_like(h) if want_saved else None, "up": torch.empty_like(h) if want_saved else None}
-        else:
-            _check_out(out, {n: (dtype, shape) for n in (("h", "gate", "up") if want_saved else ("h",))}, dev)
         gate, up = (out["gate"], out["up"]) if want_saved else (None, None)
         args = (x, w_gate, w_up, out["h"], gate, up)
         _on_gpu(dev, *args)
@@ -1082,15 +1088,15 @@ def gated_ffn_bwd(dh, x, w_gate, w_up, *, act="silu", saved=None, want_dx=True, 
     if saved is not None:
         _required(gate=gate, up=up)
     _needs(dev, ("dh", dh, dtype, shape), ("gate", gate, dtype, shape), ("up", up, dtype, shape))
+    if out is not None:
+        spec = {"dx": (dtype, x.shape)} if want_dx else {}
+        if want_dw:
+            spec.update(dw_gate=(dtype, w_gate.shape), dw_up=(dtype, w_up.shape))
+        _check_out(out, spec, dev)
     with _scope(dev, stream):
         if out is None:
             out = {"dx": torch.empty_like(x) if want_dx else None, "dw_gate": torch.empty_like(w_gate) if want_dw else None,
                    "dw_up": torch.empty_like(w_up) if want_dw else None}
-        else:
-            spec = {"dx": (dtype, x.shape)} if want_dx else {}
-            if want_dw:
-                spec.update(dw_gate=(dtype, w_gate.shape), dw_up=(dtype, w_up.shape))
-            _check_out(out, spec, dev)
         args = (dh, x, w_gate, w_up, gate, up, out["dx"] if want_dx else None, out["dw_gate"] if want_dw else None,
                 out["dw_up"] if want_dw else None)
         _on_gpu(dev, *args)
