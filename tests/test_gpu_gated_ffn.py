@@ -51,7 +51,9 @@ def near(got, want, tol, where):
     assert err <= tol, (where, err, tol)
 
 
-@pytest.mark.parametrize("M,D,F", [(777, 1000, 2712), (1030, 1544, 1032), (2048, 512, 2560)])
+# 128 x 128 with k in parts; whole; 256 x 256 of the forward, of dx, of the weights' gradients, and of dx with k in parts
+@pytest.mark.parametrize("M,D,F", [(777, 1000, 2712), (1030, 1544, 1032), (2048, 512, 2560), (2100, 72, 4104), (4104, 4104, 72),
+                                   (264, 2056, 4360), (2056, 2048, 12296)])
 def test_large_tiles(M, D, F):
     """Norms of the errors: a rounding of bf16 leaves at most 2^-8 of the norm, dgate's and dup's roundings 2^-8 of
     independent terms more, float32 sums far less."""
