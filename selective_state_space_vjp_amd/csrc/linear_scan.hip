@@ -744,12 +744,13 @@ void set_chain(const ssmvjp_linear_scan_desc& d, int n, void* workspace, ScanArg
   a.tickets = (unsigned*)(a.pairs + chain_words(d, n) - (d.dim + 63) / 64 * (TICKET / 2));
 }
 
-void launch_init(const ScanArgs& a, i64 words, const float* from, float* to, float* clear, i64 nclear, hipStream_t s) {
+void launch_init(const ScanArgs& a, void* base, i64 words, const float* from, float* to, float* clear, i64 nclear, hipStream_t s) {
   if (words <= 0 && !to && nclear <= 0) return;
   i64 most = words > nclear ? words : nclear;
   if (to && a.nseq * a.D > most) most = a.nseq * a.D;
   const i64 blocks = (most + 1023) / 1024 < 2048 ? (most + 1023) / 1024 : 2048;
-  hipLaunchKernelGGL(scan_init_kernel, dim3((unsigned)(blocks > 0 ? blocks : 1)), dim3(256), 0, s, a.pairs, words, a.off, a.nseq, a.T, a.D, from, to, clear, nclear);
+  hipLaunchKernelGGL(scan_init_kernel, dim3((unsigned)(blocks > 0 ? blocks : 1)), dim3(256), 0, s, (u64*)base, words, a.off, a.nseq,
+                     a.T, a.D, from, to, clear, nclear);
 }
 
 template <typename T, bool GATED, int V, bool BWD, bool STREAM>
@@ -816,10 +817,10 @@ size_t linear_scan_fwd_workspace_bytes(const ssmvjp_linear_scan_desc& d) {
   return (size_t)(8 * round64(chain_words(d, FWD_ROWS * NW)));
 }
 
-// the tiles' words (those of the forward pass for the states, then the backward's), partial sums of ddecay, states
+// the tiles' words of the forward pass for the states and of the backward, partial sums of ddecay, states
 size_t linear_scan_bwd_workspace_bytes(const ssmvjp_linear_scan_desc& d) {
-  const i64 f = chain_words(d, FWD_ROWS * NW), b = chain_words(d, BWD_ROWS * NW);
-  return (size_t)(8 * round64(f > b ? f : b) + 8 * linear_scan_ckpt_rows(d) * d.dim);
+  return (size_t)(8 * (round64(chain_words(d, FWD_ROWS * NW)) + round64(chain_words(d, BWD_ROWS * NW))) +
+                  8 * linear_scan_ckpt_rows(d) * d.dim);
 }
 
 hipError_t launch_linear_scan_fwd(const ssmvjp_linear_scan_desc& d, const LinearScanPointers& p, hipStream_t stream) {
@@ -829,35 +830,39 @@ hipError_t launch_linear_scan_fwd(const ssmvjp_linear_scan_desc& d, const Linear
   a.h = p.h; a.h_final = p.h_final; a.ckpt = p.ckpt;
   set_chain(d, N, p.workspace, a);
   const bool gaps = d.packed || d.seqlen == 0;  // sequences without tokens, rows of ckpt without one
-  launch_init(a, chain_words(d, N), p.h0, gaps ? p.h_final : nullptr, d.packed ? p.ckpt : nullptr,
+  launch_init(a, p.workspace, chain_words(d, N), p.h0, gaps ? p.h_final : nullptr, d.packed ? p.ckpt : nullptr,
               d.packed && p.ckpt ? linear_scan_ckpt_rows(d) * d.dim : 0, stream);
   launch_scan<false>(d, a, stream);
   return hipGetLastError();
 }
 
 hipError_t launch_linear_scan_bwd(const ssmvjp_linear_scan_desc& d, const LinearScanBwdPointers& p, hipStream_t stream) {
-  constexpr int N = BWD_ROWS * NW;
-  const i64 f = chain_words(d, FWD_ROWS * NW), b = chain_words(d, N), rows = linear_scan_ckpt_rows(d);
-  float* part = (float*)((u64*)p.workspace + round64(f > b ? f : b));
+  constexpr int NF = FWD_ROWS * NW, NB = BWD_ROWS * NW;
+  const i64 f = round64(chain_words(d, NF)), b = chain_words(d, NB), rows = linear_scan_ckpt_rows(d);
+  u64* words = (u64*)p.workspace;
+  float* part = (float*)(words + f + round64(b));
   float* states = part + rows * d.dim;
   const bool gated = d.form == SSMVJP_SCAN_GATED;
   if (d.batch > 0) {
-    if (!p.ckpt && d.seqlen > 0) {
-      const LinearScanPointers fwd{p.x, p.gate, p.input_gate, p.decay, p.h0, p.seq_offsets, nullptr, nullptr, states, p.workspace};
-      const hipError_t e = launch_linear_scan_fwd(d, fwd, stream);
-      if (e != hipSuccess) return e;
-    }
     ScanArgs a = scan_args(d, p.seq_offsets);
     a.x = p.x; a.gate = p.gate; a.igate = p.input_gate; a.decay = p.decay; a.h0 = p.h0;
+    ScanArgs fwd = a;
     a.kept = p.ckpt ? p.ckpt : states; a.dh = p.dh; a.dh_final = p.dh_final;
     a.dx = p.dx; a.dgate = p.dgate; a.digate = p.dinput_gate; a.part = part; a.dh0 = p.dh0;
-    set_chain(d, N, p.workspace, a);
-    launch_init(a, b, p.dh_final, d.packed || d.seqlen == 0 ? p.dh0 : nullptr, nullptr, 0, stream);
+    set_chain(d, NB, words + f, a);
+    // one launch for what both passes wait on
+    launch_init(a, p.ckpt ? words + f : words, p.ckpt ? b : f + b, p.dh_final, d.packed || d.seqlen == 0 ? p.dh0 : nullptr, nullptr, 0,
+                stream);
+    if (!p.ckpt) {
+      fwd.ckpt = states;
+      set_chain(d, NF, words, fwd);
+      launch_scan<false>(d, fwd, stream);
+    }
     launch_scan<true>(d, a, stream);
   }
   if (gated)
-    hipLaunchKernelGGL(decay_sum_kernel, dim3((unsigned)((d.dim + 63) / 64)), dim3(1024), 0, stream, part, d.batch > 0 && d.seqlen > 0 ? rows : 0,
-                       d.dim, p.decay, p.ddecay);
+    hipLaunchKernelGGL(decay_sum_kernel, dim3((unsigned)((d.dim + 63) / 64)), dim3(1024), 0, stream, part,
+                       d.batch > 0 && d.seqlen > 0 ? rows : 0, d.dim, p.decay, p.ddecay);
   return hipGetLastError();
 }
 
