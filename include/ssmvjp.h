@@ -474,7 +474,8 @@ ssmvjp_status layer_norm_bwd(const ssmvjp_norm_desc* desc,
  * with h_{-1} = h0.  Sequences as for delta_chunk_fwd: packed = 0, `batch` sequences of
  * `seqlen` tokens (token tensors [batch, seqlen, dim]); packed = 1, `batch` sequences
  * behind one another in `seqlen` tokens ([seqlen, dim]) with their borders in seq_offsets,
- * clamped to [0, seqlen]; tokens that no sequence owns are neither read nor written. */
+ * clamped to [0, seqlen] (a border below one before it counts as that one); tokens that
+ * no sequence owns are neither read nor written. */
 enum { SSMVJP_SCAN_LOG = 0, SSMVJP_SCAN_GATED = 1 };
 typedef struct {
   int64_t batch, seqlen, dim;
@@ -494,8 +495,10 @@ typedef struct {
  *   sequence, [batch, ceil(seqlen/64), dim], packed [seqlen/64 + batch, dim], where the
  *   token 64 j of sequence s, which starts at token o, has row o/64 + s + j, and rows that
  *   no token has are zeros.  linear_scan_bwd reads it in place of a second forward pass.
- * The state and every sum are float32.  gate = -infinity (log form) is a reset.  A NaN or
- * an infinity reaches the tokens behind it in its channel, and nothing else.
+ * The state and every sum are float32.  gate = -infinity (log form) is a reset; gates above
+ * 0 grow the state, and where the product of the decays of up to 256 tokens of a sequence
+ * passes float32's largest, states that are not zero become infinite or NaN.  A NaN or an
+ * infinity reaches the tokens behind it in its channel, and nothing else.
  * Constraints: dim below 2^24, and launches of fewer than 2^32 threads:
  * (tokens/64 + batch + 1) * (dim/64 + 1) below 2^23 (SSMVJP_EUNSUPPORTED otherwise).
  * Pointers aligned to their elements; even dims on tensors aligned to two elements are the

@@ -154,11 +154,11 @@ __device__ __forceinline__ u32x4 tile_rsrc(const Operand& o, i64 mn0, i64 MN, i6
 }
 
 // Tile number -> (m, n).  Workgroups go round the eight XCDs, each with an L2 of its own: an XCD gets a contiguous run
-// of tiles, in bands of 8 tiles of m, so that those it works on at one time share rows of A and of B.
+// of tiles, in bands of 4 tiles of m, so that those it works on at one time share rows of A and of B.
 __device__ __forceinline__ void place(unsigned id, unsigned nm, unsigned nn, unsigned& m, unsigned& n) {
   const unsigned total = nm * nn, each = total / 8, rest = total % 8, xcd = id % 8;
   const unsigned t = xcd * each + (xcd < rest ? xcd : rest) + id / 8;
-  const unsigned band = t / (8 * nn), m0 = band * 8, h = nm - m0 < 8 ? nm - m0 : 8, in = t - band * 8 * nn;
+  const unsigned band = t / (4 * nn), m0 = band * 4, h = nm - m0 < 4 ? nm - m0 : 4, in = t - band * 4 * nn;
   m = m0 + in % h;
   n = in / h;
 }

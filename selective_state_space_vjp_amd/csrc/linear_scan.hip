@@ -75,26 +75,33 @@ struct ScanArgs {
 constexpr int TICKET = 32;
 
 // Tile slots of N tokens each: a packed sequence s owns those from start / N + s, which never meet the next one's
-// (see delta_seq.cuh).
-template <int N>
-struct Tiles {
-  const ScanArgs& a;
-  __device__ __forceinline__ i64 border(i64 s) const {
-    const i64 o = a.off[s];
-    return o < 0 ? 0 : o > a.T ? a.T : o;
-  }
-  // the sequence of a packed slot; called by whole waves
-  __device__ __forceinline__ i64 of_slot(i64 slot, int lane) const {
-    i64 s = -1;
-    for (i64 s0 = 0; s0 < a.nseq; s0 += 64) {
-      const i64 i = s0 + lane;
-      const int n = __popcll(__ballot(i < a.nseq && border(i) / N + i <= slot));
-      s += n;
-      if (n < 64) break;
-    }
-    return s < 0 ? 0 : s;
-  }
+// (see delta_seq.cuh).  Every border counts as the largest up to it: a tile waits for others, so that each slot has to
+// belong to one sequence whatever the borders hold.
+struct Span {
+  i64 seq, start, end;
 };
+// the sequence of a packed slot (-1: it lies before all); called by whole waves
+template <int N>
+__device__ __forceinline__ Span of_slot(const ScanArgs& a, i64 slot, int lane) {
+  const auto at = [](int v, int l) { return __builtin_amdgcn_readlane(v, l); };
+  int most = 0;  // of the borders before this round's
+  for (i64 s0 = 0;; s0 += 64) {
+    const i64 i = s0 + lane;
+    i64 o = i <= a.nseq ? a.off[i] : 0;
+    o = o < 0 ? 0 : o > a.T ? a.T : o;
+    int e = (int)o;
+#pragma unroll
+    for (int d = 1; d < 64; d *= 2) {
+      const int up = __shfl_up(e, d);
+      e = lane >= d && up > e ? up : e;
+    }
+    e = e > most ? e : most;
+    // those whose first slot is not behind `slot`; border nseq is none's
+    const int n = __popcll(__ballot(i < a.nseq && (i64)e / N + i <= slot));
+    if (n < 64) return {s0 + n - 1, n > 0 ? at(e, n > 0 ? n - 1 : 0) : most, at(e, n)};
+    most = at(e, 63);
+  }
+}
 
 struct Tile {
   i64 seq, start, len;  // the sequence
@@ -120,13 +127,13 @@ __device__ __forceinline__ bool find_tile(const ScanArgs& a, i64 o, int lane, Ti
     t.slot = t.slot0 + t.j;
     return true;
   }
-  const Tiles<N> seqs{a};
   t.slot = REV ? a.ntiles - 1 - o : o;
-  t.seq = uniform(seqs.of_slot(t.slot, lane));
-  const i64 o0 = uniform(seqs.border(t.seq)), o1 = uniform(seqs.border(t.seq + 1));
-  t.start = o0;
-  t.len = o1 > o0 ? o1 - o0 : 0;
-  t.slot0 = o0 / N + t.seq;
+  const Span sp = of_slot<N>(a, t.slot, lane);
+  t.seq = uniform(sp.seq);
+  if (t.seq < 0) return false;
+  t.start = uniform(sp.start);
+  t.len = uniform(sp.end) - t.start;
+  t.slot0 = t.start / N + t.seq;
   t.j = t.slot - t.slot0;
   t.n = (t.len + N - 1) / N;
   return t.j >= 0 && t.j < t.n;

@@ -161,6 +161,53 @@ def test_borders_outside_the_tokens_are_clamped():
     assert torch.equal(got["h"], want["h"]) and torch.equal(got["h_final"], want["h_final"])
 
 
+def test_borders_that_go_back_count_as_the_largest_before():
+    """Tiles wait for each other: no borders may leave one waiting."""
+    announce("linear scan borders out of order")
+    d = make_scan("gated", 1, 0, 16, F32, lens=[300, 0, 500, 100], seed=9)
+    t = dev(d)
+    want, wg = fwd(t, want_ckpt=True), bwd(t)
+    t["seq_offsets"] = torch.tensor([0, 300, 7, 800, 900], dtype=torch.int32, device=DEV)
+    got, gg = fwd(t, want_ckpt=True), bwd(t)
+    torch.cuda.synchronize()
+    assert torch.equal(got["h"], want["h"]) and torch.equal(got["ckpt"], want["ckpt"])
+    for k in ("dx", "dgate", "dinput_gate", "ddecay"):
+        assert torch.equal(gg[k], wg[k])
+
+
+def test_more_sequences_than_a_wave():
+    """The slot of a tile among hundreds of sequences, most of them empty."""
+    announce("linear scan many sequences")
+    lens = [0] * 70 + [130] + [0] * 63 + [1, 64, 65] + [0] * 128 + [200, 0]
+    compare(make_scan("log", 1, 0, 3, F32, lens=lens, seed=19, first=5, tail=70), "many")
+    compare(make_scan("gated", 1, 0, 2, F32, lens=[0] * 200, seed=20, tail=130), "all empty")
+
+
+@pytest.mark.parametrize("form", ["log", "gated"])
+def test_whole_tiles_that_no_sequence_owns(form):
+    """Tiles of tokens before the first sequence and behind the last."""
+    announce(f"linear scan unowned tiles {form}")
+    d = make_scan(form, 1, 0, 10, BF, lens=[40, 150], seed=21, first=700, tail=600)
+    own = owned(d)[0]
+    for k in ("x", "gate", "input_gate", "dh"):
+        if d[k] is not None:
+            d[k][0, ~own] = math.nan
+    t = dev(d)
+    out = {"h": torch.full_like(t["x"], 7.0), "h_final": torch.empty(2, 10, device=DEV), "ckpt": None}
+    fwd(t, out=out)
+    g = {"dx": torch.full_like(t["x"], 7.0), "dgate": torch.full_like(t["gate"], 7.0), "dh0": torch.empty(2, 10, device=DEV)}
+    if form == "gated":
+        g.update(dinput_gate=torch.full_like(t["x"], 7.0), ddecay=torch.empty(10, device=DEV))
+    bwd(t, out=g)
+    for k, v in {"h": out["h"], **{k: g[k] for k in ("dx", "dgate", "dinput_gate") if k in g}}.items():
+        assert (v[0, ~own] == 7.0).all() and torch.isfinite(v).all(), k
+    assert all(torch.isfinite(v).all() for v in (out["h_final"], g["dh0"], g.get("ddecay", out["h_final"])))
+    for k in ("x", "gate", "input_gate", "dh"):
+        if d[k] is not None:
+            d[k][0, ~own] = 0
+    compare(d, "unowned tiles")
+
+
 @pytest.mark.parametrize("form", ["log", "gated"])
 def test_values_that_are_not_numbers_stay_causal(form):
     announce(f"linear scan nan {form}")
