@@ -413,27 +413,23 @@ __global__ void __launch_bounds__(256) ffn_join_kernel(FfnArgs a) {
   }
 }
 
-// dgate, dup from the kept gate and up; n a multiple of 8
+// dgate, dup from the kept gate and up, 16 bytes a lane; n a multiple of 8
 template <typename T, int ACT>
 __global__ void __launch_bounds__(256) ffn_grad_kernel(const T* dh, const T* gate, const T* up, T* dgate, T* dup, i64 n) {
   constexpr int W = 16 / sizeof(T);
+  typedef T vec __attribute__((ext_vector_type(W)));
   for (i64 e = ((i64)blockIdx.x * 256 + threadIdx.x) * W; e < n; e += (i64)gridDim.x * 256 * W) {
+    const vec d = *(const vec*)(dh + e), g = *(const vec*)(gate + e), u = *(const vec*)(up + e);
+    vec og, ou;
 #pragma unroll
-    for (int i = 0; i < W; i += 4) {
-      float d[4], g[4], u[4], og[4], ou[4];
-      fetch4<T>(dh, e + i, d);
-      fetch4<T>(gate, e + i, g);
-      fetch4<T>(up, e + i, u);
-#pragma unroll
-      for (int r = 0; r < 4; ++r) {
-        float f, df;
-        act_pair<ACT>(g[r], f, df);
-        og[r] = d[r] * u[r] * df;
-        ou[r] = d[r] * f;
-      }
-      store4<T>(dgate, e + i, og);
-      store4<T>(dup, e + i, ou);
+    for (int r = 0; r < W; ++r) {
+      float f, df;
+      act_pair<ACT>((float)g[r], f, df);
+      og[r] = (T)((float)d[r] * (float)u[r] * df);
+      ou[r] = (T)((float)d[r] * f);
     }
+    *(vec*)(dgate + e) = og;
+    *(vec*)(dup + e) = ou;
   }
 }
 
@@ -449,8 +445,9 @@ struct GemmPlan {
 // Which tile, and into how many parts k is cut.  The large one where it fills the 256 CUs by itself (4096 x 2048 -> 8192
 // dw: 278 us, 327 with 128 x 128) or with k cut into long parts (dx of the same: 317, uncut 446, 128 x 128 347; of 1024 x
 // 4096 -> 12288: 215, 552, 270).  Else 128 x 128, of which a CU holds two, cut until there are 512, in parts of at least
-// 16 steps: a second launch adds them (2048 x 2048 -> 8192 dx: 176 us in two, 209 uncut; 100 x 1024 -> 2048 forward, 16
-// steps: 18.5 in two, 14.9 uncut).  Up to 32 rows are one tile of the small kind.
+// 16 steps (8 of float32): a second launch adds them (2048 x 2048 -> 8192 dx: 176 us in two, 209 uncut; 100 x 1024 ->
+// 2048 forward, 16 steps: 18.5 in two, 14.9 uncut; 200 x 512 -> 1024 in float32, 16 steps: 26 in two, 41 uncut).  Up to
+// 32 rows are one tile of the small kind.
 GemmPlan gemm_plan(i64 M, i64 N, i64 K, int segs, int items, bool pair, bool few, size_t elem) {
   const i64 steps = segs * ((K * (i64)elem + ROWB - 1) / ROWB);
   const auto tiles = [&](i64 bm, i64 bn) { return items * ((M + bm - 1) / bm) * ((N * (pair ? 2 : 1) + bn - 1) / bn); };
@@ -461,7 +458,7 @@ GemmPlan gemm_plan(i64 M, i64 N, i64 K, int segs, int items, bool pair, bool few
   if (n == 0) return {TILE_MID, 1};
   const i64 cut = 256 / large;
   if (!small && cut * large >= 232 && steps >= 96 * cut) return {TILE_LARGE, (int)cut};
-  const i64 most = steps / 16 < 512 / n ? steps / 16 : 512 / n;
+  const i64 least = elem == 2 ? 16 : 8, most = steps / least < 512 / n ? steps / least : 512 / n;
   return {small ? TILE_FEW : TILE_MID, most > 1 ? (int)most : 1};
 }
 
