@@ -5,7 +5,9 @@
 // numbers: as easy as 1, 2, 3", 2011): ten rounds of two 32 x 32 -> 64-bit
 // products on a 128-bit counter.  One counter gives eight 16-bit draws, which is
 // one 16-byte vector of bf16: the probability is a multiple of 2^-16 then, and
-// the scale is the exact one for it.
+// the scale is the exact one for it.  So the generator hides behind the memory
+// (32-bit draws would need twice its products): 8192 x 4096 bf16 with a residual,
+// 201 MB, takes 36 us (5.6 TB/s), 29 where the memory-side cache holds a part.
 #include "common.cuh"
 #include "kernels.h"
 

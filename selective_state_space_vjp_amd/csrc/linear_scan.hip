@@ -29,6 +29,15 @@
 // for was handed out before it, to a workgroup that is running.  A counter for
 // every slab, since additions to one address take 11.5 ns each: one counter for
 // all cost 47 of 118 us of the backward at b=2 T=4096 D=4096.
+//
+// The bytes are the bound, and in the gated form the coefficients beside them:
+// six (backward seven) of an element's instructions are transcendental, each as
+// long as four others.  Gated bf16 b=2 T=4096 D=4096: forward 60 us for 271 MB
+// (vector units busy 39 us), backward 110 us for 472 MB (busy 67 us), where a
+// copy at 5.2 TB/s takes 52 and 91.  Log form, 32771 packed tokens of 2560
+// channels: 138 us for 671 MB; 123 where no tile waits, of 256 sequences of 128
+// tokens 108.  Tiles of half as many tokens: 170 us, groups of 32 tiles: 150;
+// three workgroups per CU of the gated form (80 registers) spill: 93 us.
 #include <type_traits>
 
 #include "common.cuh"
@@ -145,6 +154,7 @@ __device__ __forceinline__ float sigmoid_hw(float z) { return __builtin_amdgcn_r
 __device__ __forceinline__ float decay_rate(float c, float z) { return c * softplus_hw(z); }
 __device__ __forceinline__ float decay_slope(float z) { return z < -16.0f ? 1.0f : sigmoid_f(z) / softplus_f(z); }
 
+constexpr float LOG2E = 1.4426950408889634f, LN2 = 0.6931471805599453f;
 constexpr float MIN_NORMAL = 1.17549435e-38f;  // the reciprocals take denormals as zeros
 
 struct Token {
@@ -174,7 +184,6 @@ __device__ __forceinline__ Token gated_token(float x, float r, float i, float ra
   t.u = t.mw * x;
   return t;
 }
-constexpr float LOG2E = 1.4426950408889634f, LN2 = 0.6931471805599453f;
 
 // A h + u.  GROWS: A may have overflowed (log gates above 0); a state of zero stays out of that.
 template <bool GROWS>
@@ -280,8 +289,7 @@ struct Chain {
   Pair (*look)[V][64];  // [NW]: what the waves found of the tiles before
   float (*base)[64];    // the state behind the group before
 
-  // the state before this wave's rows.  first: the state before the sequence.  total: the state behind this tile (the
-  // last wave's only)
+  // the state before this wave's rows.  first: the state before the sequence
   __device__ __forceinline__ void enter(const ScanArgs& a, i64 slot, int step, i64 k, i64 n, int w, int lane, i64 ch0,
                                         unsigned coff, bool mine, const float (&first)[V], float (&h)[V]) {
     // (1) this tile's pair; the last tile's is not needed, and a group's last one publishes a state instead
@@ -679,6 +687,7 @@ struct StepArgs {
 };
 
 // V channels per thread.  The state of the named slot is on its way while the wave looks through the earlier requests.
+// Two trips to memory and the launch are what it takes: 2.8 us for one request of 4096 channels, 6.1 for 256 (17 MB).
 template <typename T, bool GATED, int V>
 __global__ void __launch_bounds__(256) scan_step_kernel(StepArgs a) {
   const i64 req = blockIdx.x / a.nblk, ch = ((blockIdx.x % a.nblk) * 256 + threadIdx.x) * V;
