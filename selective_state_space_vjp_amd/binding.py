@@ -635,9 +635,10 @@ _entry = {}  # entry points by name, looked up once
 def _enqueue(name, desc, args, dev, workspace, needs=True):
     """Workspace and launch of one of the entry points that end in (workspace, bytes, stream).
     needs=False: the call takes a workspace only in the debug finiteness mode, and says so."""
-    fn = _entry.get(name)
-    if fn is None:
-        fn = _entry[name] = getattr(lib(), name)
+    entry = _entry.get(name)
+    if entry is None:
+        entry = _entry[name] = getattr(lib(), name), getattr(lib(), name + "_workspace")
+    fn, size = entry
     d = ctypes.byref(desc)
     ptrs = [None if t is None else t.data_ptr() for t in args]
     stream = torch._C._cuda_getCurrentRawStream(dev.index)
@@ -645,7 +646,11 @@ def _enqueue(name, desc, args, dev, workspace, needs=True):
     if not needs and workspace is None:
         st = fn(d, *ptrs, None, 0, stream)
     if st == EWORKSPACE:
-        ws, wsb = _workspace(_query(name + "_workspace", desc), dev, workspace)
+        n = ctypes.c_size_t()
+        st = size(d, ctypes.byref(n))
+        if st != OK:
+            raise SsmVjpError(name + "_workspace", st)
+        ws, wsb = _workspace(n.value, dev, workspace)
         st = fn(d, *ptrs, None if ws is None else ws.data_ptr(), wsb, stream)
     if st != OK:
         raise SsmVjpError(name, st)
@@ -896,29 +901,32 @@ def _needs(dev, *checks):
 
 
 def _scan_form(x, gate, input_gate, decay):
-    """The form of a linear recurrence's arguments and its gate's type."""
     _required(x=x, gate=gate)
     if (input_gate is None) != (decay is None):
         raise ValueError("input_gate and decay belong together (the gated form), or neither is given (the log form)")
-    return (SCAN_LOG, torch.float32) if decay is None else (SCAN_GATED, x.dtype)
 
 
 def _linear_scan_inputs(x, gate, h0, input_gate, decay, c, seq_offsets):
-    form, gtype = _scan_form(x, gate, input_gate, decay)
-    if x.dim() != 3:
+    gated = decay is not None
+    if x is None or gate is None or (input_gate is not None) != gated:
+        _scan_form(x, gate, input_gate, decay)
+    xs, dtype, dev, f32 = x.shape, x.dtype, x.device, torch.float32
+    if len(xs) != 3:
         raise ValueError("x must be [b,T,D]")
-    n, T, D = x.shape
-    dev, f32 = x.device, torch.float32
+    n, T, D = xs
     if seq_offsets is not None:
         if n != 1:
             raise ValueError("packed sequences (seq_offsets given) need token tensors [1,T,D]")
         if seq_offsets.dim() != 1 or seq_offsets.shape[0] < 1:
             raise ValueError("seq_offsets must be [sequences + 1]")
     b = n if seq_offsets is None else seq_offsets.shape[0] - 1
-    desc = LinearScanDesc(b, T, D, float(c), form, _dtype_code(x), int(seq_offsets is not None))
-    _needs(dev, ("x", x, x.dtype, (n, T, D)), ("gate", gate, gtype, (n, T, D)), ("input_gate", input_gate, x.dtype, (n, T, D)),
-           ("decay", decay, f32, (D,)), ("h0", h0, f32, (b, D)), ("seq_offsets", seq_offsets, torch.int32, (b + 1,)))
-    return desc
+    gtype, ds, hs = dtype if gated else f32, (D,), (b, D)
+    if not (_fits(x, dtype, xs) and _fits(gate, gtype, xs)
+            and (not gated or (_fits(input_gate, dtype, xs) and _fits(decay, f32, ds)))
+            and (h0 is None or _fits(h0, f32, hs)) and (seq_offsets is None or _fits(seq_offsets, torch.int32, (b + 1,)))):
+        _needs(dev, ("x", x, dtype, xs), ("gate", gate, gtype, xs), ("input_gate", input_gate, dtype, xs),
+               ("decay", decay, f32, ds), ("h0", h0, f32, hs), ("seq_offsets", seq_offsets, torch.int32, (b + 1,)))
+    return LinearScanDesc(b, T, D, c, SCAN_GATED if gated else SCAN_LOG, _dtype_code(x), seq_offsets is not None)
 
 
 def linear_scan_ckpt_shape(desc):
@@ -1035,19 +1043,20 @@ _ACTS = {"silu": ACT_SILU, "gelu": ACT_GELU}
 
 
 def _ffn_inputs(x, w_gate, w_up, act):
-    _required(x=x, w_gate=w_gate, w_up=w_up)
+    if x is None or w_gate is None or w_up is None:
+        _required(x=x, w_gate=w_gate, w_up=w_up)
     if act not in _ACTS:
         raise ValueError(f"act must be one of {', '.join(_ACTS)}")
-    if x.dim() < 1 or w_gate.dim() != 2:
+    xs, ws, dtype = x.shape, w_gate.shape, x.dtype
+    if len(xs) < 1 or len(ws) != 2:
         raise ValueError("x must be [..., D] and w_gate [F,D]")
-    F, D = w_gate.shape
+    F, D = ws
     if D == 0 or F == 0:
         raise ValueError("w_gate has an empty axis")
-    dtype = x.dtype
-    desc = FfnDesc(x.numel() // D, D, F, _ACTS[act], _dtype_code(x))
-    lead = x.shape[:-1]
-    _needs(x.device, ("x", x, dtype, lead + (D,)), ("w_gate", w_gate, dtype, (F, D)), ("w_up", w_up, dtype, (F, D)))
-    return desc, lead + (F,)
+    lead = xs[:-1]
+    if not (xs[-1] == D and _fits(x, dtype, xs) and _fits(w_gate, dtype, ws) and _fits(w_up, dtype, ws)):
+        _needs(x.device, ("x", x, dtype, lead + (D,)), ("w_gate", w_gate, dtype, ws), ("w_up", w_up, dtype, ws))
+    return FfnDesc(x.numel() // D, D, F, _ACTS[act], _dtype_code(x)), lead + (F,)
 
 
 def gated_ffn_fwd(x, w_gate, w_up, *, act="silu", want_saved=False, out=None, workspace=None, stream=None):
