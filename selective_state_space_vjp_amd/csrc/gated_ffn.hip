@@ -89,6 +89,7 @@ __device__ __forceinline__ float act_of(float z) {
 // ---------------------------------------------------------------------------
 typedef bf16 bf16x8 __attribute__((ext_vector_type(8)));
 constexpr int ROWB = 128;  // bytes of k per step
+constexpr int LDS_BYTES = 160 * 1024;
 constexpr int SCHED_MFMA = 0x008, SCHED_LDS_READ = 0x100;  // kinds of instructions of sched_group_barrier
 
 template <typename T>
@@ -236,6 +237,15 @@ __device__ __forceinline__ int outputs(const FfnArgs& a) {
   return EPI == EPI_PLAIN ? 1 : EPI == EPI_GLU_BACK ? 2 : a.C[1] ? 3 : 1;
 }
 
+// The outputs on their way through LDS: ROWS of a wave's FM rows of 16 at a time, the most that fit, in 1, 2, 4 .. parts.
+template <typename T, bool PAIR, int BM, int NOUT, int FM>
+struct StoreOf {
+  static constexpr int PITCH = NOUT * (int)sizeof(T) + 16, ALL = (PAIR ? 3 : 1) * BM * PITCH;
+  static constexpr int PARTS = FM > 2 && ALL / 2 > LDS_BYTES ? 4 : FM > 1 ? 2 : 1;
+  static constexpr int ROWS = FM / PARTS, BYTES = ALL / PARTS;
+  static_assert(FM % PARTS == 0 && BYTES <= LDS_BYTES, "");
+};
+
 // WM x WN waves, NB buffers.  PAIR: the tile's BN columns are BN/2 of each of two products, side by side in every wave.
 template <typename T, bool AKC, bool BKC, int EPI, int ACT, int BM, int BN, int WM, int WN, int NB>
 __global__ void __launch_bounds__(64 * WM * WN) ffn_gemm_kernel(FfnArgs a) {
@@ -358,30 +368,31 @@ __global__ void __launch_bounds__(64 * WM * WN) ffn_gemm_kernel(FfnArgs a) {
     }
     return;
   }
-  // Through LDS, so that whole rows of the tile are stored by 16 bytes a lane: half of every wave's rows at a time, all
+  // Through LDS, so that whole rows of the tile are stored by 16 bytes a lane: a part of every wave's rows at a time, all
   // outputs side by side (8192 x 4096 -> 12288 with gate and up: 1350 us; 1440 with stores of 32 bytes of a row from the
   // registers).
-  constexpr int HALF = FM > 1 ? FM / 2 : 1, ER = WM * 16 * HALF, PITCH = NOUT * (int)sizeof(T) + 16, CHUNKS = NOUT * (int)sizeof(T) / 16;
+  typedef StoreOf<T, PAIR, BM, NOUT, FM> SO;
+  constexpr int ROWS = SO::ROWS, ER = WM * 16 * ROWS, PITCH = SO::PITCH, CHUNKS = NOUT * (int)sizeof(T) / 16;
   const int nout = outputs<EPI>(a);
 #pragma unroll
-  for (int h = 0; h < FM / HALF; ++h) {
+  for (int h = 0; h < FM / ROWS; ++h) {
     step_wait<0>();
     step_barrier();
 #pragma unroll
-    for (int i = 0; i < HALF; ++i)
+    for (int i = 0; i < ROWS; ++i)
 #pragma unroll
       for (int j = 0; j < (PAIR ? FN / 2 : FN); ++j) {
         const int col = wn + 16 * j + 4 * (lane >> 4);
-        const i64 m = m0 + wm + 16 * (h * HALF + i) + (lane & 15), n = n0 + col;
+        const i64 m = m0 + wm + 16 * (h * ROWS + i) + (lane & 15), n = n0 + col;
         const bool in = m < a.M && n < a.N;
         float v[3][4];
 #pragma unroll
         for (int r = 0; r < 4; ++r) {
-          v[0][r] = acc[h * HALF + i][j][r];
-          if constexpr (PAIR) v[1][r] = acc[h * HALF + i][j + FN / 2][r];
+          v[0][r] = acc[h * ROWS + i][j][r];
+          if constexpr (PAIR) v[1][r] = acc[h * ROWS + i][j + FN / 2][r];
         }
         finish4<T, EPI, ACT>(a, in ? m * a.ldc + n : 0, v);
-        char* to = lds + ((wave / WN) * 16 * HALF + 16 * i + (lane & 15)) * PITCH + col * (int)sizeof(T);
+        char* to = lds + ((wave / WN) * 16 * ROWS + 16 * i + (lane & 15)) * PITCH + col * (int)sizeof(T);
         store4<T>(to, 0, v[0]);
         if constexpr (PAIR)
           if (nout > 1) {
@@ -393,7 +404,7 @@ __global__ void __launch_bounds__(64 * WM * WN) ffn_gemm_kernel(FfnArgs a) {
     step_barrier();
     for (int i = threadIdx.x; i < nout * ER * CHUNKS; i += 64 * W) {
       const int o = i / (ER * CHUNKS), r = i / CHUNKS % ER, c = i % CHUNKS;
-      const i64 m = m0 + r / (16 * HALF) * (BM / WM) + h * 16 * HALF + r % (16 * HALF), n = n0 + c * (16 / (int)sizeof(T));
+      const i64 m = m0 + r / (16 * ROWS) * (BM / WM) + h * 16 * ROWS + r % (16 * ROWS), n = n0 + c * (16 / (int)sizeof(T));
       if (m < a.M && n < a.N)
         *(uint4*)((T*)a.C[EPI == EPI_PLAIN ? item : o] + m * a.ldc + n) = *(const uint4*)(lds + (o * ER + r) * PITCH + c * 16);
     }
@@ -487,8 +498,8 @@ size_t part_bytes(const GemmPlan& g, i64 M, i64 N, int items, bool pair) {
 template <typename T, bool AKC, bool BKC, int EPI, int ACT, int BM, int BN, int WM, int WN, int NB>
 void launch_tile(const FfnArgs& a, hipStream_t s) {
   constexpr int NOUT = EPI != EPI_PLAIN ? BN / 2 : BN, FM = BM / WM / 16;
-  // the buffers, or the outputs of half the rows (all of them where a wave has 16)
-  constexpr int loop = NB * (BM + BN) * ROWB, rows = BM / (FM > 1 ? 2 : 1) * (NOUT * (int)sizeof(T) + 16) * (EPI == EPI_PLAIN ? 1 : 3);
+  constexpr int loop = NB * (BM + BN) * ROWB, rows = StoreOf<T, EPI != EPI_PLAIN, BM, NOUT, FM>::BYTES;
+  static_assert(loop <= LDS_BYTES, "");
   const dim3 grid((unsigned)(((a.N + NOUT - 1) / NOUT) * ((a.M + BM - 1) / BM) * a.items * a.split));
   hipLaunchKernelGGL((ffn_gemm_kernel<T, AKC, BKC, EPI, ACT, BM, BN, WM, WN, NB>), grid, dim3(64 * WM * WN),
                      loop > rows ? loop : rows, s, a);

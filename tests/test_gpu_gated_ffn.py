@@ -51,7 +51,7 @@ def near(got, want, tol, where):
     assert err <= tol, (where, err, tol)
 
 
-# 128 x 128 with k in parts; whole; 256 x 256 of the forward, of dx, of the weights' gradients, and of dx with k in parts
+# 128 x 128 with k in parts; whole; 256 x 256 of the forward, of dx, of the weights' gradients, of all but dx
 @pytest.mark.parametrize("M,D,F", [(777, 1000, 2712), (1030, 1544, 1032), (2048, 512, 2560), (2100, 72, 4104), (4104, 4104, 72),
                                    (264, 2056, 4360), (2056, 2048, 12296)])
 def test_large_tiles(M, D, F):
@@ -74,6 +74,34 @@ def test_large_tiles(M, D, F):
         near(got["dx"], torch.mm(dg, G) + torch.mm(du, Uw), 2.0**-7, "dx")
         near(got["dw_gate"], torch.mm(dg.T, X), 2.0**-7, "dw_gate")
         near(got["dw_up"], torch.mm(du.T, X), 2.0**-7, "dw_up")
+
+
+# 256 x 256 of the forward and of what it forms again; of dx; of the weights' gradients; of dx with k in parts
+@pytest.mark.parametrize("M,D,F,dtype", [(2100, 72, 4104, F32), (4104, 4104, 72, F32), (264, 2056, 4360, F32),
+                                         (1024, 2048, 12296, F32), (1000, 4096, 12288, BF)])
+def test_large_tiles_of_both_types(M, D, F, dtype):
+    """Norms of the errors: bf16 as above.  float32: a sum of k products wanders off by about 2^-24 sqrt(k / 6) of its
+    norm, what the activation adds is a few roundings, and the second product passes the first one's on."""
+    announce(f"gated ffn large {M} {D} {F} {dtype}")
+    x, wg, wu, dh = (v.to(DEV) for v in inputs(M, D, F, dtype, 6))
+    out = bd.gated_ffn_fwd(x, wg, wu, want_saved=True)
+    first, rows, cols = ((2.0**-8, 2.0**-7, 2.0**-7) if dtype is BF else
+                         [2.0**-24 * (16 + math.sqrt(D) + math.sqrt(k)) for k in (0, 2 * F, M)])
+    X, G, Uw, H = (v.double() for v in (x, wg, wu, dh))
+    gate, up = torch.mm(X, G.T), torch.mm(X, Uw.T)
+    near(out["gate"], gate, first, "gate")
+    near(out["up"], up, first, "up")
+    near(out["h"], gate * torch.sigmoid(gate) * up, first, "h")
+    assert torch.equal(bd.gated_ffn_fwd(x, wg, wu)["h"], out["h"])
+    for saved in (None, (out["gate"], out["up"])):
+        if saved:
+            gate, up = (v.double() for v in saved)
+        s = torch.sigmoid(gate)
+        dg, du = H * up * (s + gate * s * (1 - s)), H * gate * s
+        got = bd.gated_ffn_bwd(dh, x, wg, wu, saved=saved)
+        near(got["dx"], torch.mm(dg, G) + torch.mm(du, Uw), rows, "dx")
+        near(got["dw_gate"], torch.mm(dg.T, X), cols, "dw_gate")
+        near(got["dw_up"], torch.mm(du.T, X), cols, "dw_up")
 
 
 @pytest.mark.parametrize("dtype", [F32, BF], ids=["f32", "bf16"])
