@@ -25,6 +25,8 @@
 // gradients, and only with the accumulators pinned by hand), streaming stores.
 // Few rows are bound by the weights: 5 rows of 4096 -> 12288 take 41 us (201 MB,
 // 4.9 TB/s), 33 where the memory-side cache still holds them.
+#include <cmath>
+
 #include "common.cuh"
 #include "kernels.h"
 #include "lds_dma.cuh"
@@ -465,30 +467,52 @@ __global__ void __launch_bounds__(256) ffn_grad_kernel(const T* dh, const T* gat
 // ---------------------------------------------------------------------------
 // host
 // ---------------------------------------------------------------------------
-enum { TILE_LARGE, TILE_MID, TILE_FEW };  // 256 x 256, 128 x 128, 32 x 64
+enum { TILE_LARGE, TILE_MID, TILE_NARROW, TILE_FEW };  // 256 x 256, 128 x 128, 128 x 64, 32 x 64
 
 struct GemmPlan {
   int tile, split;
 };
 
-// Which tile, and into how many parts k is cut.  The large one where it fills the 256 CUs by itself (4096 x 2048 -> 8192
-// dw: 278 us, 327 with 128 x 128) or with k cut into long parts (dx of the same: 317, uncut 446, 128 x 128 347; of 1024 x
-// 4096 -> 12288: 215, 552, 270).  Else 128 x 128, of which a CU holds two, cut until there are 512, in parts of at least
-// 16 steps (8 of float32): a second launch adds them (2048 x 2048 -> 8192 dx: 176 us in two, 209 uncut; 100 x 1024 ->
-// 2048 forward, 16 steps: 18.5 in two, 14.9 uncut; 200 x 512 -> 1024 in float32, 16 steps: 26 in two, 41 uncut).  Up to
-// 32 rows are one tile of the small kind.
+// Which tile, and into how many parts k is cut (a second launch adds the parts).  The large one where it fills the 256 CUs
+// by itself (4096 x 2048 -> 8192 dw: 278 us, 327 with 128 x 128) or with k cut into long parts (dx of the same: 317, uncut
+// 446, 128 x 128 347; of 1024 x 4096 -> 12288: 215, 552, 270).  Up to 32 rows are one tile of the small kind, cut into
+// parts of 16 steps (8 of float32) until there are 512.
+//
+// Between them 128 x 128 and 128 x 64, by the time of the busiest CU in steps of the former.  A step of 128 x 64 takes 0.7
+// of it (0.6 in float32).  bf16 waits for its loads, so that two workgroups of a CU take 1.2 of the time of one; float32
+// keeps the matrix cores busy, and two take 2.  The sum of parts: a launch, 4 steps (2), and the parts' bytes, 1 MB a step
+// (8 MB).  These come from a sweep of both tiles in 1 to 16 parts over 61 products of 40 to 2500 rows; the choice is
+// 1.5 % (0.8) above the fastest on average, 128 x 128 alone in parts of 16 steps (8) 10 % (25).  Forward at 100 x 1024 ->
+// 2048: 9.9 us with 128 x 64, 12.7 with 128 x 128; at 777 x 1000 -> 2712: 22.8, 19.4, in float32 109, 131; dx of 512 x
+// 1024 -> 4096 in 8 parts: 28, 31.
 GemmPlan gemm_plan(i64 M, i64 N, i64 K, int segs, int items, bool pair, bool few, size_t elem) {
   const i64 steps = segs * ((K * (i64)elem + ROWB - 1) / ROWB);
   const auto tiles = [&](i64 bm, i64 bn) { return items * ((M + bm - 1) / bm) * ((N * (pair ? 2 : 1) + bn - 1) / bn); };
   const i64 large = tiles(256, 256);
   if (large >= 256) return {TILE_LARGE, 1};
-  const bool small = few && M <= 32;
-  const i64 n = small ? tiles(32, 64) : tiles(128, 128);
-  if (n == 0) return {TILE_MID, 1};
+  if (large == 0) return {TILE_MID, 1};
+  if (few && M <= 32) {
+    const i64 n = tiles(32, 64), least = elem == 2 ? 16 : 8, most = steps / least < 512 / n ? steps / least : 512 / n;
+    return {TILE_FEW, most > 1 ? (int)most : 1};
+  }
   const i64 cut = 256 / large;
-  if (!small && cut * large >= 232 && steps >= 96 * cut) return {TILE_LARGE, (int)cut};
-  const i64 least = elem == 2 ? 16 : 8, most = steps / least < 512 / n ? steps / least : 512 / n;
-  return {small ? TILE_FEW : TILE_MID, most > 1 ? (int)most : 1};
+  if (cut * large >= 232 && steps >= 96 * cut) return {TILE_LARGE, (int)cut};
+  const bool two = elem == 2;
+  GemmPlan best{TILE_MID, 1};
+  float least = INFINITY;
+  for (int tile : {TILE_MID, TILE_NARROW})
+    for (int split = 1; split <= 16; ++split) {
+      const i64 n = split * tiles(128, tile == TILE_MID ? 128 : 64), per_cu = (n + 255) / 256;
+      if (split > 1 && (steps < 4 * split || n > 512)) break;
+      float time = (float)((steps + split - 1) / split) * (tile == TILE_MID ? 1.0f : two ? 0.7f : 0.6f);
+      time *= per_cu == 1 ? 1.0f : (two ? 0.6f : 1.0f) * (float)per_cu;
+      if (split > 1) time += (two ? 4.0f : 2.0f) + (float)(split * items * M * N * (pair ? 8 : 4)) / (two ? 1e6f : 8e6f);
+      if (time < least) {
+        least = time;
+        best = {tile, split};
+      }
+    }
+  return best;
 }
 
 size_t part_bytes(const GemmPlan& g, i64 M, i64 N, int items, bool pair) {
@@ -512,6 +536,7 @@ void launch_gemm(FfnArgs a, float* part, hipStream_t s) {
   a.part = part;
   if (g.tile == TILE_LARGE) launch_tile<T, AKC, BKC, EPI, ACT, 256, 256, 2, 4, 2>(a, s);
   else if (g.tile == TILE_MID) launch_tile<T, AKC, BKC, EPI, ACT, 128, 128, 2, 2, 2>(a, s);
+  else if (g.tile == TILE_NARROW) launch_tile<T, AKC, BKC, EPI, ACT, 128, 64, 2, 2, 3>(a, s);
   else if constexpr (AKC) launch_tile<T, AKC, BKC, EPI, ACT, 32, 64, 2, 2, 6>(a, s);
   if (g.split > 1) {
     const i64 blocks = (a.items * a.M * a.N + 1023) / 1024;
