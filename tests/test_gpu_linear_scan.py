@@ -104,6 +104,32 @@ def test_long_sequences(form):
     compare(make_scan(form, 1, 0, 4, BF, lens=[4200, 1, 8300], seed=4, first=7, tail=60), f"{form} 4200,1,8300")
 
 
+@pytest.mark.parametrize("form", ["log", "gated"])
+def test_states_kept_over_thousands_of_tokens(form):
+    """Norms of the errors of the final states and of dh0, float32, a within 0.0005 to 0.002 of one.  A state adds up the
+    last tau = 1 / (1 - a) <= 2000 tokens; each has met tau roundings of half a step, 2^-25, in a, in the products of a
+    and in the sums: three walks of sqrt(tau) 2^-25 = 1.3e-6, 4e-6 if all go one way.  The plain bound of a state, which
+    takes every a to be off by its worst to one side, is hundreds of times that."""
+    T, D, b = 12000, 64, 2
+    d = make_scan(form, b, T, D, F32, seed=11)
+    rate = torch.exp(torch.linspace(math.log(0.0005), math.log(0.002), D))
+    if form == "log":
+        d["gate"] = -rate * torch.rand(b, T, D, generator=torch.Generator().manual_seed(1)).add(0.5)
+    else:  # sigmoid(gate) is 1/2 in the middle
+        d["decay"] = torch.log(torch.expm1((2 * rate / C).double())).float()
+    t = dev(d)
+    a, u = coefficients(d)
+    h, l = d["h0"].double(), d["dh_final"].double()
+    for i in range(T):
+        h = a[:, i] * h + u[:, i]
+        l = a[:, T - 1 - i] * (l + d["dh"][:, T - 1 - i].double())
+    out, got = fwd(t), bwd(t)
+    for where, have, want in (("h_final", out["h_final"], h), ("dh0", got["dh0"], l)):
+        err = float((have.double().cpu() - want).norm() / want.norm())
+        print(form, where, f"{err:.1e}", flush=True)
+        assert err <= 3 * math.sqrt(2000) * 2.0**-25, (where, err)
+
+
 def test_states_that_span_every_channel_tile():
     announce("linear scan wide")
     compare(make_scan("gated", 1, 140, 5000, BF, seed=6), "wide")
