@@ -33,9 +33,9 @@
 // The bytes are the bound, and in the gated form the coefficients beside them:
 // six (backward seven) of an element's instructions are transcendental, each as
 // long as four others.  Gated bf16 b=2 T=4096 D=4096: forward 60 us for 271 MB
-// (vector units busy 39 us), backward 110 us for 472 MB (busy 67 us), where a
-// copy at 5.2 TB/s takes 52 and 91.  Log form, 32771 packed tokens of 2560
-// channels: 138 us for 671 MB; 123 where no tile waits, of 256 sequences of 128
+// (vector units busy 0.59 of it), backward 108 us for 472 MB (0.63), where a copy
+// at 5.2 TB/s takes 52 and 91.  Log form, 32771 packed tokens of 2560
+// channels: 142 us for 671 MB; 123 where no tile waits, of 256 sequences of 128
 // tokens 108.  Tiles of half as many tokens: 170 us, groups of 32 tiles: 150;
 // three workgroups per CU of the gated form (80 registers) spill: 93 us.
 #include <type_traits>
