@@ -61,8 +61,8 @@ __device__ __forceinline__ void act_pair(float z, float& f, float& df) {
     f = z * s;
     df = fmaf(f, 1.0f - s, s);
   } else {
-    // (1 + tanh(v)) / 2 = sigmoid(2 v)
-    const float k = 1.5957691216057308f, z2 = z * z;
+    // (1 + tanh(v)) / 2 = sigmoid(2 v); a z^2 that overflows would meet the 0 of f (1 - s)
+    const float k = 1.5957691216057308f, z2 = fminf(z * z, 1e30f);
     const float s = __builtin_amdgcn_rcpf(1.0f + exp_hw(-k * z * fmaf(0.044715f, z2, 1.0f)));
     f = z * s;
     df = fmaf(f * (1.0f - s), k * fmaf(0.134145f, z2, 1.0f), s);

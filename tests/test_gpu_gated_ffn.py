@@ -139,6 +139,24 @@ def test_extreme_projections():
         assert all(torch.isfinite(v).all() for v in g.values())
 
 
+@pytest.mark.parametrize("act", ["silu", "gelu"])
+def test_projections_whose_square_overflows(act):
+    """act'(z) is 1 above and 0 below, act(z) is z and 0, in the epilogue that forms gate again and from the kept one."""
+    announce(f"gated ffn far {act}")
+    x = torch.zeros(2, 8, device=DEV)
+    x[0, 0], x[1, 0] = 1e20, -1e20
+    w, one = torch.eye(8, device=DEV), torch.zeros(8, 8, device=DEV)
+    one[:, 1] = 1.0
+    x[:, 1] = 1.0  # up = 1
+    out = bd.gated_ffn_fwd(x, w, one, act=act, want_saved=True)
+    assert float(out["h"][0, 0]) == float(x[0, 0]) and float(out["h"][1, 0]) == 0.0
+    for saved in (None, (out["gate"], out["up"])):
+        g = bd.gated_ffn_bwd(torch.ones(2, 8, device=DEV), x, w, one, act=act, saved=saved)
+        # dw_up[0, 0] = act(1e20) 1e20 is past float32's largest
+        assert torch.isfinite(g["dx"]).all() and torch.isfinite(g["dw_gate"]).all() and float(g["dw_up"][0, 0]) == math.inf
+        assert float(g["dx"][0, 0]) == 1.0 and float(g["dx"][1, 0]) == 0.0
+
+
 def test_optional_outputs_empty_batches_and_streams():
     announce("gated ffn options")
     x, wg, wu, dh = (v.to(DEV) for v in inputs(40, 64, 96, BF, 7))
