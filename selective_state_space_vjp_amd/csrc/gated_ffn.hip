@@ -475,43 +475,50 @@ struct GemmPlan {
 
 // Which tile, and into how many parts k is cut (a second launch adds the parts).  The large one where it fills the 256 CUs
 // by itself (4096 x 2048 -> 8192 dw: 278 us, 327 with 128 x 128) or with k cut into long parts (dx of the same: 317, uncut
-// 446, 128 x 128 347; of 1024 x 4096 -> 12288: 215, 552, 270).  Up to 32 rows are one tile of the small kind, cut into
-// parts of 16 steps (8 of float32) until there are 512.
+// 446, 128 x 128 347; of 1024 x 4096 -> 12288: 215, 552, 270).
 //
-// Between them 128 x 128 and 128 x 64, by the time of the busiest CU in steps of the former.  A step of 128 x 64 takes 0.7
-// of it (0.6 in float32).  bf16 waits for its loads, so that two workgroups of a CU take 1.2 of the time of one; float32
-// keeps the matrix cores busy, and two take 2.  The sum of parts: a launch, 4 steps (2), and the parts' bytes, 1 MB a step
-// (8 MB).  These come from a sweep of both tiles in 1 to 16 parts over 61 products of 40 to 2500 rows; the choice is
-// 1.5 % (0.8) above the fastest on average, 128 x 128 alone in parts of 16 steps (8) 10 % (25).  Forward at 100 x 1024 ->
-// 2048: 9.9 us with 128 x 64, 12.7 with 128 x 128; at 777 x 1000 -> 2712: 22.8, 19.4, in float32 109, 131; dx of 512 x
-// 1024 -> 4096 in 8 parts: 28, 31.
-GemmPlan gemm_plan(i64 M, i64 N, i64 K, int segs, int items, bool pair, bool few, size_t elem) {
+// Else the tile and parts of at least 4 steps (together at most 512 workgroups) by the time of the busiest CU in steps of
+// 128 x 128: a step of 128 x 64 takes 0.7 of one (0.6 in float32), of 32 x 64, which is for operands with k along the
+// rows, 0.35 (0.15).  bf16 waits for its loads, so that two workgroups of a CU take 1.2 of the time of one; with the small
+// tile and in float32 they take 2.  The sum of parts: a launch, 4 steps (1.5), and the parts' bytes, 2 MB a step (8 MB).
+// These come from a sweep of the tiles in 1 to 16 parts over 125 products of 1 to 8000 rows: the choice is 1.4 % above the
+// fastest on average.  Forward at 100 x 1024 -> 2048: 6.9 us with 32 x 64, 9.8 with 128 x 64, 12.7 with 128 x 128; at
+// 777 x 1000 -> 2712: 22.8 with 128 x 64, 19 with 128 x 128; dx of 512 x 1024 -> 4096 in 8 parts: 28, 31.  Up to 32 rows are
+// one tile of the small kind.
+GemmPlan gemm_plan(i64 M, i64 N, i64 K, int segs, int items, bool pair, bool kc, size_t elem) {
+  struct Kind {
+    int tile;
+    i64 bm, bn;
+    float step, crowd;  // bf16
+    float step32;
+  };
+  constexpr Kind kinds[] = {{TILE_MID, 128, 128, 1.0f, 0.6f, 1.0f}, {TILE_NARROW, 128, 64, 0.7f, 0.6f, 0.6f}, {TILE_FEW, 32, 64, 0.35f, 1.0f, 0.15f}};
   const i64 steps = segs * ((K * (i64)elem + ROWB - 1) / ROWB);
   const auto tiles = [&](i64 bm, i64 bn) { return items * ((M + bm - 1) / bm) * ((N * (pair ? 2 : 1) + bn - 1) / bn); };
+  const bool one = kc && M <= 32, two = elem == 2;
   const i64 large = tiles(256, 256);
-  if (large >= 256) return {TILE_LARGE, 1};
   if (large == 0) return {TILE_MID, 1};
-  if (few && M <= 32) {
-    const i64 n = tiles(32, 64), least = elem == 2 ? 16 : 8, most = steps / least < 512 / n ? steps / least : 512 / n;
-    return {TILE_FEW, most > 1 ? (int)most : 1};
+  if (!one) {
+    if (large >= 256) return {TILE_LARGE, 1};
+    const i64 cut = 256 / large;
+    if (cut * large >= 232 && steps >= 96 * cut) return {TILE_LARGE, (int)cut};
   }
-  const i64 cut = 256 / large;
-  if (cut * large >= 232 && steps >= 96 * cut) return {TILE_LARGE, (int)cut};
-  const bool two = elem == 2;
-  GemmPlan best{TILE_MID, 1};
+  GemmPlan best{one ? TILE_FEW : TILE_MID, 1};
   float least = INFINITY;
-  for (int tile : {TILE_MID, TILE_NARROW})
+  for (const Kind& k : kinds) {
+    if (k.tile == TILE_FEW ? !kc : one) continue;
     for (int split = 1; split <= 16; ++split) {
-      const i64 n = split * tiles(128, tile == TILE_MID ? 128 : 64), per_cu = (n + 255) / 256;
+      const i64 n = split * tiles(k.bm, k.bn), per_cu = (n + 255) / 256;
       if (split > 1 && (steps < 4 * split || n > 512)) break;
-      float time = (float)((steps + split - 1) / split) * (tile == TILE_MID ? 1.0f : two ? 0.7f : 0.6f);
-      time *= per_cu == 1 ? 1.0f : (two ? 0.6f : 1.0f) * (float)per_cu;
-      if (split > 1) time += (two ? 4.0f : 2.0f) + (float)(split * items * M * N * (pair ? 8 : 4)) / (two ? 1e6f : 8e6f);
+      float time = (float)((steps + split - 1) / split) * (two ? k.step : k.step32);
+      if (per_cu > 1) time *= (two ? k.crowd : 1.0f) * (float)per_cu;
+      if (split > 1) time += (two ? 4.0f : 1.5f) + (float)(split * items * M * N * (pair ? 8 : 4)) / (two ? 2e6f : 8e6f);
       if (time < least) {
         least = time;
-        best = {tile, split};
+        best = {k.tile, split};
       }
     }
+  }
   return best;
 }
 
