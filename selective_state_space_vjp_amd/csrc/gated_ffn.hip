@@ -249,8 +249,9 @@ struct StoreOf {
 };
 
 // WM x WN waves, NB buffers.  PAIR: the tile's BN columns are BN/2 of each of two products, side by side in every wave.
+// block: the workgroup's number among those of this product.
 template <typename T, bool AKC, bool BKC, int EPI, int ACT, int BM, int BN, int WM, int WN, int NB>
-__global__ void __launch_bounds__(64 * WM * WN) ffn_gemm_kernel(FfnArgs a) {
+__device__ __forceinline__ void gemm_tile(const FfnArgs& a, const unsigned block, char* lds) {
   constexpr bool PAIR = EPI != EPI_PLAIN;
   constexpr int W = WM * WN, KB = ROWB / (int)sizeof(T), NOUT = PAIR ? BN / 2 : BN;
   constexpr int FM = BM / WM / 16, FN = BN / WN / 16;
@@ -260,15 +261,14 @@ __global__ void __launch_bounds__(64 * WM * WN) ffn_gemm_kernel(FfnArgs a) {
   constexpr int IA = TA::BYTES / 1024 / W, IB = TB::BYTES / 1024 / W;  // loads of a wave, each product's B by itself
   constexpr int BUF = TA::BYTES + (PAIR ? 2 : 1) * TB::BYTES;
   static_assert(IA * 1024 * W == TA::BYTES && IB * 1024 * W == TB::BYTES, "");
-  extern __shared__ __align__(1024) char lds[];
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int wm = wave / WN * (BM / WM), wn = wave % WN * (NOUT / WN);
   const unsigned nm = (unsigned)((a.M + BM - 1) / BM), nn = (unsigned)((a.N + NOUT - 1) / NOUT);
   unsigned tm, tn;
-  place(blockIdx.x % (nm * nn), nm, nn, tm, tn);
+  place(block % (nm * nn), nm, nn, tm, tn);
   const i64 m0 = (i64)tm * BM, n0 = (i64)tn * NOUT;
   const int steps1 = (int)((a.K + KB - 1) / KB), all = (PAIR ? 1 : a.segs) * steps1;
-  const int which = blockIdx.x / (nm * nn), item = PAIR ? 0 : which / a.split, share = which - item * a.split;
+  const int which = block / (nm * nn), item = PAIR ? 0 : which / a.split, share = which - item * a.split;
   const int first = (int)((i64)all * share / a.split), steps = (int)((i64)all * (share + 1) / a.split) - first;
   const unsigned base = lds_base(lds);
 
@@ -413,12 +413,27 @@ __global__ void __launch_bounds__(64 * WM * WN) ffn_gemm_kernel(FfnArgs a) {
   }
 }
 
-// the parts' sums in order, and what becomes of them
+template <typename T, bool AKC, bool BKC, int EPI, int ACT, int BM, int BN, int WM, int WN, int NB>
+__global__ void __launch_bounds__(64 * WM * WN) ffn_gemm_kernel(FfnArgs a) {
+  extern __shared__ __align__(1024) char lds[];
+  gemm_tile<T, AKC, BKC, EPI, ACT, BM, BN, WM, WN, NB>(a, blockIdx.x, lds);
+}
+
+// dx by the first workgroups, the weights' gradients by the others, which need nothing of each other: a launch less (the
+// backward of 20 x 512 -> 1024 takes 13.3 us, 16.2 with two; of 777 x 1000 -> 2712 65, 68).
+template <typename T, int BMX, int BNX, int WX, int NBX, int BNW, int NBW>
+__global__ void __launch_bounds__(256) ffn_grads_kernel(FfnArgs dx, FfnArgs dw, unsigned blocks) {
+  extern __shared__ __align__(1024) char lds[];
+  if (blockIdx.x < blocks) gemm_tile<T, true, false, EPI_PLAIN, 0, BMX, BNX, WX, 4 / WX, NBX>(dx, blockIdx.x, lds);
+  else gemm_tile<T, false, false, EPI_PLAIN, 0, 128, BNW, 2, 2, NBW>(dw, blockIdx.x - blocks, lds);
+}
+
+// the parts' sums in order, and what becomes of them: the share `block` of `blocks`
 template <typename T, int EPI, int ACT>
-__global__ void __launch_bounds__(256) ffn_join_kernel(FfnArgs a) {
+__device__ __forceinline__ void join_parts(const FfnArgs& a, const i64 block, const i64 blocks) {
   constexpr bool PAIR = EPI != EPI_PLAIN;
   const i64 each = a.M * a.N;
-  for (i64 i = ((i64)blockIdx.x * 256 + threadIdx.x) * 4; i < each * a.items; i += (i64)gridDim.x * 1024) {
+  for (i64 i = (block * 256 + threadIdx.x) * 4; i < each * a.items; i += blocks * 1024) {
     const int item = (int)(i / each);
     const i64 e = i - item * each;
     float v[3][4];
@@ -442,6 +457,16 @@ __global__ void __launch_bounds__(256) ffn_join_kernel(FfnArgs a) {
         if constexpr (EPI == EPI_GLU) store4<T>(a.C[2], at, v[2]);
       }
   }
+}
+
+template <typename T, int EPI, int ACT>
+__global__ void __launch_bounds__(256) ffn_join_kernel(FfnArgs a) {
+  join_parts<T, EPI, ACT>(a, blockIdx.x, gridDim.x);
+}
+template <typename T>
+__global__ void __launch_bounds__(256) ffn_join_grads_kernel(FfnArgs dx, FfnArgs dw, unsigned blocks) {
+  if (blockIdx.x < blocks) join_parts<T, EPI_PLAIN, 0>(dx, blockIdx.x, blocks);
+  else join_parts<T, EPI_PLAIN, 0>(dw, blockIdx.x - blocks, gridDim.x - blocks);
 }
 
 // dgate, dup from the kept gate and up, 16 bytes a lane; n a multiple of 8
@@ -523,32 +548,73 @@ GemmPlan gemm_plan(i64 M, i64 N, i64 K, int segs, int items, bool pair, bool kc,
 }
 
 size_t part_bytes(const GemmPlan& g, i64 M, i64 N, int items, bool pair) {
-  return g.split > 1 ? (size_t)(items * g.split * M * N * (pair ? 8 : 4)) : 0;
+  return g.split > 1 ? (size_t)((items * g.split * M * N * (pair ? 8 : 4) + 255) / 256 * 256) : 0;
+}
+
+// bytes of LDS: the buffers, or the outputs on their way
+template <typename T, int EPI, int BM, int BN, int WM, int NB>
+constexpr int lds_bytes() {
+  constexpr int loop = NB * (BM + BN) * ROWB, rows = StoreOf<T, EPI != EPI_PLAIN, BM, EPI != EPI_PLAIN ? BN / 2 : BN, BM / WM / 16>::BYTES;
+  static_assert(loop <= LDS_BYTES, "");
+  return loop > rows ? loop : rows;
+}
+// a product's workgroups on tiles of bm x bn (PAIR: of both products)
+unsigned gemm_blocks(const FfnArgs& a, i64 bm, i64 bn) {
+  return (unsigned)(((a.N + bn - 1) / bn) * ((a.M + bm - 1) / bm) * a.items * a.split);
+}
+unsigned join_blocks(const FfnArgs& a) {
+  const i64 blocks = (a.items * a.M * a.N + 1023) / 1024;
+  return (unsigned)(blocks < 4096 ? blocks : 4096);
 }
 
 template <typename T, bool AKC, bool BKC, int EPI, int ACT, int BM, int BN, int WM, int WN, int NB>
 void launch_tile(const FfnArgs& a, hipStream_t s) {
-  constexpr int NOUT = EPI != EPI_PLAIN ? BN / 2 : BN, FM = BM / WM / 16;
-  constexpr int loop = NB * (BM + BN) * ROWB, rows = StoreOf<T, EPI != EPI_PLAIN, BM, NOUT, FM>::BYTES;
-  static_assert(loop <= LDS_BYTES, "");
-  const dim3 grid((unsigned)(((a.N + NOUT - 1) / NOUT) * ((a.M + BM - 1) / BM) * a.items * a.split));
-  hipLaunchKernelGGL((ffn_gemm_kernel<T, AKC, BKC, EPI, ACT, BM, BN, WM, WN, NB>), grid, dim3(64 * WM * WN),
-                     loop > rows ? loop : rows, s, a);
+  hipLaunchKernelGGL((ffn_gemm_kernel<T, AKC, BKC, EPI, ACT, BM, BN, WM, WN, NB>),
+                     dim3(gemm_blocks(a, BM, EPI != EPI_PLAIN ? BN / 2 : BN)), dim3(64 * WM * WN), (lds_bytes<T, EPI, BM, BN, WM, NB>()), s, a);
+}
+
+template <typename T, int EPI, bool KC>
+GemmPlan plan_of(const FfnArgs& a) {
+  return gemm_plan(a.M, a.N, a.K, a.segs, a.items, EPI != EPI_PLAIN, KC, sizeof(T));
 }
 
 template <typename T, bool AKC, bool BKC, int EPI, int ACT>
 void launch_gemm(FfnArgs a, float* part, hipStream_t s) {
-  const GemmPlan g = gemm_plan(a.M, a.N, a.K, a.segs, a.items, EPI != EPI_PLAIN, AKC, sizeof(T));
+  const GemmPlan g = plan_of<T, EPI, AKC>(a);
   a.split = g.split;
   a.part = part;
   if (g.tile == TILE_LARGE) launch_tile<T, AKC, BKC, EPI, ACT, 256, 256, 2, 4, 2>(a, s);
   else if (g.tile == TILE_MID) launch_tile<T, AKC, BKC, EPI, ACT, 128, 128, 2, 2, 2>(a, s);
   else if (g.tile == TILE_NARROW) launch_tile<T, AKC, BKC, EPI, ACT, 128, 64, 2, 2, 3>(a, s);
   else if constexpr (AKC) launch_tile<T, AKC, BKC, EPI, ACT, 32, 64, 2, 2, 6>(a, s);
-  if (g.split > 1) {
-    const i64 blocks = (a.items * a.M * a.N + 1023) / 1024;
-    hipLaunchKernelGGL((ffn_join_kernel<T, EPI, ACT>), dim3((unsigned)(blocks < 4096 ? blocks : 4096)), dim3(256), 0, s, a);
-  }
+  if (g.split > 1) hipLaunchKernelGGL((ffn_join_kernel<T, EPI, ACT>), dim3(join_blocks(a)), dim3(256), 0, s, a);
+}
+
+// dx and the weights' gradients, neither on the large tile
+template <typename T, int BMX, int BNX, int WX, int NBX, int BNW, int NBW>
+void launch_grads_tile(const FfnArgs& dx, const FfnArgs& dw, hipStream_t s) {
+  constexpr int lx = lds_bytes<T, EPI_PLAIN, BMX, BNX, WX, NBX>(), lw = lds_bytes<T, EPI_PLAIN, 128, BNW, 2, NBW>();
+  const unsigned first = gemm_blocks(dx, BMX, BNX);
+  hipLaunchKernelGGL((ffn_grads_kernel<T, BMX, BNX, WX, NBX, BNW, NBW>), dim3(first + gemm_blocks(dw, 128, BNW)), dim3(256),
+                     lx > lw ? lx : lw, s, dx, dw, first);
+}
+template <typename T, int BMX, int BNX, int WX, int NBX>
+void launch_grads_dx(const FfnArgs& dx, const FfnArgs& dw, bool mid, hipStream_t s) {
+  if (mid) launch_grads_tile<T, BMX, BNX, WX, NBX, 128, 2>(dx, dw, s);
+  else launch_grads_tile<T, BMX, BNX, WX, NBX, 64, 3>(dx, dw, s);
+}
+template <typename T>
+void launch_grads(FfnArgs dx, FfnArgs dw, const GemmPlan& px, const GemmPlan& pw, float* part, hipStream_t s) {
+  dx.split = px.split;
+  dx.part = part;
+  dw.split = pw.split;
+  dw.part = (float*)((char*)part + part_bytes(px, dx.M, dx.N, 1, false));
+  const bool mid = pw.tile == TILE_MID;
+  if (px.tile == TILE_MID) launch_grads_dx<T, 128, 128, 2, 2>(dx, dw, mid, s);
+  else if (px.tile == TILE_NARROW) launch_grads_dx<T, 128, 64, 2, 3>(dx, dw, mid, s);
+  else launch_grads_dx<T, 32, 64, 2, 6>(dx, dw, mid, s);
+  const unsigned first = px.split > 1 ? join_blocks(dx) : 0, rest = pw.split > 1 ? join_blocks(dw) : 0;
+  if (first + rest) hipLaunchKernelGGL((ffn_join_grads_kernel<T>), dim3(first + rest), dim3(256), 0, s, dx, dw, first);
 }
 
 template <typename T, int ACT>
@@ -576,16 +642,19 @@ void ffn_bwd(const ssmvjp_ffn_desc& d, const FfnBwdPointers& p, hipStream_t s) {
       FfnArgs a{d.rows, d.hidden, d.dim, {{p.x, d.dim}}, {{p.w_gate, d.dim}, {p.w_up, d.dim}}, 1, d.hidden, {dgate, dup}, p.dh, 1, 1, nullptr};
       launch_gemm<T, true, true, EPI_GLU_BACK, ACT>(a, part, s);
     }
-    if (p.dx) {
-      FfnArgs a{d.rows, d.dim, d.hidden, {{dgate, d.hidden}, {dup, d.hidden}}, {{p.w_gate, d.dim}, {p.w_up, d.dim}}, 2, d.dim, {p.dx}, nullptr, 1, 1, nullptr};
-      launch_gemm<T, true, false, EPI_PLAIN, 0>(a, part, s);
-    }
   }
-  // both weights' gradients in one launch
-  FfnArgs a{d.hidden, d.dim, d.rows, {}, {{p.x, d.dim}}, 1, d.dim, {}, nullptr, 0, 1, nullptr};
-  if (p.dw_gate) a.A[a.items] = {dgate, d.hidden}, a.C[a.items++] = p.dw_gate;
-  if (p.dw_up) a.A[a.items] = {dup, d.hidden}, a.C[a.items++] = p.dw_up;
-  if (a.items) launch_gemm<T, false, false, EPI_PLAIN, 0>(a, part, s);
+  const bool want_dx = p.dx && n > 0;
+  const FfnArgs x{d.rows, d.dim, d.hidden, {{dgate, d.hidden}, {dup, d.hidden}}, {{p.w_gate, d.dim}, {p.w_up, d.dim}}, 2, d.dim, {p.dx}, nullptr, 1, 1, nullptr};
+  // both weights' gradients are one product
+  FfnArgs w{d.hidden, d.dim, d.rows, {}, {{p.x, d.dim}}, 1, d.dim, {}, nullptr, 0, 1, nullptr};
+  if (p.dw_gate) w.A[w.items] = {dgate, d.hidden}, w.C[w.items++] = p.dw_gate;
+  if (p.dw_up) w.A[w.items] = {dup, d.hidden}, w.C[w.items++] = p.dw_up;
+  if (want_dx && w.items) {
+    const GemmPlan px = plan_of<T, EPI_PLAIN, true>(x), pw = plan_of<T, EPI_PLAIN, false>(w);
+    if (px.tile != TILE_LARGE && pw.tile != TILE_LARGE) return launch_grads<T>(x, w, px, pw, part, s);
+  }
+  if (want_dx) launch_gemm<T, true, false, EPI_PLAIN, 0>(x, part, s);
+  if (w.items) launch_gemm<T, false, false, EPI_PLAIN, 0>(w, part, s);
 }
 
 }  // namespace
@@ -594,17 +663,17 @@ size_t ffn_fwd_workspace_bytes(const ssmvjp_ffn_desc& d) {
   return part_bytes(gemm_plan(d.rows, d.hidden, d.dim, 1, 1, true, true, d.dtype == SSMVJP_BF16 ? 2 : 4), d.rows, d.hidden, 1, true);
 }
 
-// dgate and dup, then the largest of the products' parts
+// dgate and dup, then the parts: of the forward's products, and behind those of dx and the weights' gradients
 size_t ffn_bwd_workspace_bytes(const ssmvjp_ffn_desc& d) {
-  const size_t elem = d.dtype == SSMVJP_BF16 ? 2 : 4;
-  size_t part = ffn_fwd_workspace_bytes(d);
+  const size_t elem = d.dtype == SSMVJP_BF16 ? 2 : 4, fwd = ffn_fwd_workspace_bytes(d);
   const size_t dx = part_bytes(gemm_plan(d.rows, d.dim, d.hidden, 2, 1, false, true, elem), d.rows, d.dim, 1, false);
+  size_t dw = 0;
   // one weight's gradient may be asked for without the other
   for (int items = 1; items <= 2; ++items) {
-    const size_t dw = part_bytes(gemm_plan(d.hidden, d.dim, d.rows, 1, items, false, false, elem), d.hidden, d.dim, items, false);
-    part = part > dw ? part : dw;
+    const size_t some = part_bytes(gemm_plan(d.hidden, d.dim, d.rows, 1, items, false, false, elem), d.hidden, d.dim, items, false);
+    dw = dw > some ? dw : some;
   }
-  return grads_bytes(d) + (part > dx ? part : dx);
+  return grads_bytes(d) + (fwd > dx + dw ? fwd : dx + dw);
 }
 
 hipError_t launch_ffn_fwd(const ssmvjp_ffn_desc& d, const FfnFwdPointers& p, hipStream_t stream) {

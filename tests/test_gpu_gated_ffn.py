@@ -76,13 +76,10 @@ def test_large_tiles(M, D, F):
         near(got["dw_up"], torch.mm(du.T, X), 2.0**-7, "dw_up")
 
 
-# 256 x 256 of the forward and of what it forms again; of dx; of the weights' gradients; of dx with k in parts
-@pytest.mark.parametrize("M,D,F,dtype", [(2100, 72, 4104, F32), (4104, 4104, 72, F32), (264, 2056, 4360, F32),
-                                         (1024, 2048, 12296, F32), (1000, 4096, 12288, BF)])
-def test_large_tiles_of_both_types(M, D, F, dtype):
+def agrees(M, D, F, dtype):
     """Norms of the errors: bf16 as above.  float32: a sum of k products wanders off by about 2^-24 sqrt(k / 6) of its
     norm, what the activation adds is a few roundings, and the second product passes the first one's on."""
-    announce(f"gated ffn large {M} {D} {F} {dtype}")
+    announce(f"gated ffn tiles {M} {D} {F} {dtype}")
     x, wg, wu, dh = (v.to(DEV) for v in inputs(M, D, F, dtype, 6))
     out = bd.gated_ffn_fwd(x, wg, wu, want_saved=True)
     first, rows, cols = ((2.0**-8, 2.0**-7, 2.0**-7) if dtype is BF else
@@ -102,6 +99,31 @@ def test_large_tiles_of_both_types(M, D, F, dtype):
         near(got["dx"], torch.mm(dg, G) + torch.mm(du, Uw), rows, "dx")
         near(got["dw_gate"], torch.mm(dg.T, X), cols, "dw_gate")
         near(got["dw_up"], torch.mm(du.T, X), cols, "dw_up")
+    only = bd.gated_ffn_bwd(dh, x, wg, wu, saved=saved, want_dw=False)
+    assert only["dw_gate"] is None
+    near(only["dx"], torch.mm(dg, G) + torch.mm(du, Uw), rows, "dx alone")
+    only = bd.gated_ffn_bwd(dh, x, wg, wu, saved=saved, want_dx=False)
+    assert only["dx"] is None and torch.equal(only["dw_gate"], got["dw_gate"]) and torch.equal(only["dw_up"], got["dw_up"])
+
+
+# 256 x 256 of the forward and of what it forms again; of dx; of the weights' gradients; of dx with k in parts
+@pytest.mark.parametrize("M,D,F,dtype", [(2100, 72, 4104, F32), (4104, 4104, 72, F32), (264, 2056, 4360, F32),
+                                         (1024, 2048, 12296, F32), (1000, 4096, 12288, BF)])
+def test_large_tiles_of_both_types(M, D, F, dtype):
+    agrees(M, D, F, dtype)
+
+
+# The smaller tiles of dx (32 x 64, 128 x 64, 128 x 128) beside those of the weights' gradients (128 x 64, 128 x 128), each
+# whole and with k in parts, and the forward's
+@pytest.mark.parametrize("M,D,F,dtype", [
+    (177, 1912, 1088, BF), (1, 1904, 1248, BF), (891, 8, 472, BF), (31, 48, 8, BF), (2236, 1864, 264, BF), (2219, 1912, 352, BF),
+    (2331, 392, 2376, BF), (2356, 520, 1416, BF), (34, 1648, 1720, BF), (2474, 200, 2760, BF), (1345, 8, 1368, BF),
+    (2222, 1360, 408, BF), (2192, 1736, 8, BF), (133, 1728, 2760, BF),
+    (172, 1616, 520, F32), (1137, 72, 1320, F32), (562, 16, 8, F32), (31, 48, 8, F32), (1762, 1800, 648, F32),
+    (2065, 1584, 536, F32), (2438, 72, 936, F32), (2053, 72, 872, F32), (113, 1376, 1208, F32), (1510, 1064, 8, F32),
+    (2220, 664, 8, F32), (867, 1840, 368, F32), (2290, 1640, 40, F32)])
+def test_every_pair_of_tiles(M, D, F, dtype):
+    agrees(M, D, F, dtype)
 
 
 @pytest.mark.parametrize("dtype", [F32, BF], ids=["f32", "bf16"])
