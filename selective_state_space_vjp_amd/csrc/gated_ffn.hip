@@ -420,7 +420,7 @@ __global__ void __launch_bounds__(64 * WM * WN) ffn_gemm_kernel(FfnArgs a) {
 }
 
 // dx by the first workgroups, the weights' gradients by the others, which need nothing of each other: a launch less (the
-// backward of 20 x 512 -> 1024 takes 13.3 us, 16.2 with two; of 777 x 1000 -> 2712 65, 68).
+// backward of 20 x 512 -> 1024 takes 13.4 us, 16.2 with two; of 777 x 1000 -> 2712 60, 68).
 template <typename T, int BMX, int BNX, int WX, int NBX, int BNW, int NBW>
 __global__ void __launch_bounds__(256) ffn_grads_kernel(FfnArgs dx, FfnArgs dw, unsigned blocks) {
   extern __shared__ __align__(1024) char lds[];
@@ -498,46 +498,69 @@ struct GemmPlan {
   int tile, split;
 };
 
-// Which tile, and into how many parts k is cut (a second launch adds the parts).  The large one where it fills the 256 CUs
-// by itself (4096 x 2048 -> 8192 dw: 278 us, 327 with 128 x 128) or with k cut into long parts (dx of the same: 317, uncut
-// 446, 128 x 128 347; of 1024 x 4096 -> 12288: 215, 552, 270).
-//
-// Else the tile and parts of at least 4 steps (together at most 512 workgroups) by the time of the busiest CU in steps of
-// 128 x 128: a step of 128 x 64 takes 0.7 of one (0.6 in float32), of 32 x 64, which is for operands with k along the
-// rows, 0.35 (0.15).  bf16 waits for its loads, so that two workgroups of a CU take 1.2 of the time of one; with the small
-// tile and in float32 they take 2.  The sum of parts: a launch, 4 steps (1.5), and the parts' bytes, 2 MB a step (8 MB).
-// These come from a sweep of the tiles in 1 to 16 parts over 125 products of 1 to 8000 rows: the choice is 1.4 % above the
-// fastest on average.  Forward at 100 x 1024 -> 2048: 6.9 us with 32 x 64, 9.8 with 128 x 64, 12.7 with 128 x 128; at
-// 777 x 1000 -> 2712: 22.8 with 128 x 64, 19 with 128 x 128; dx of 512 x 1024 -> 4096 in 8 parts: 28, 31.  Up to 32 rows are
-// one tile of the small kind.
-GemmPlan gemm_plan(i64 M, i64 N, i64 K, int segs, int items, bool pair, bool kc, size_t elem) {
-  struct Kind {
-    int tile;
-    i64 bm, bn;
-    float step, crowd;  // bf16
-    float step32;
-  };
-  constexpr Kind kinds[] = {{TILE_MID, 128, 128, 1.0f, 0.6f, 1.0f}, {TILE_NARROW, 128, 64, 0.7f, 0.6f, 0.6f}, {TILE_FEW, 32, 64, 0.35f, 1.0f, 0.15f}};
-  const i64 steps = segs * ((K * (i64)elem + ROWB - 1) / ROWB);
-  const auto tiles = [&](i64 bm, i64 bn) { return items * ((M + bm - 1) / bm) * ((N * (pair ? 2 : 1) + bn - 1) / bn); };
-  const bool one = kc && M <= 32, two = elem == 2;
-  const i64 large = tiles(256, 256);
-  if (large == 0) return {TILE_MID, 1};
-  if (!one) {
-    if (large >= 256) return {TILE_LARGE, 1};
-    const i64 cut = 256 / large;
-    if (cut * large >= 232 && steps >= 96 * cut) return {TILE_LARGE, (int)cut};
-  }
-  GemmPlan best{one ? TILE_FEW : TILE_MID, 1};
+// A product's shape as the rules below see it.  kc: k along the rows of A.
+struct Shape {
+  i64 M, N, steps;
+  int items;
+  bool pair, kc, two;  // two: bf16
+};
+Shape shape_of(i64 M, i64 N, i64 K, int segs, int items, bool pair, bool kc, size_t elem) {
+  return {M, N, segs * ((K * (i64)elem + ROWB - 1) / ROWB), items, pair, kc, elem == 2};
+}
+i64 tiles_of(const Shape& p, i64 bm, i64 bn) {
+  return p.items * ((p.M + bm - 1) / bm) * ((p.N * (p.pair ? 2 : 1) + bn - 1) / bn);
+}
+
+// Parts of at least 4 steps, together at most 512 workgroups.
+constexpr int PARTS = 16, WORKGROUPS = 512;
+bool may_cut(const Shape& p, i64 tiles, int split) { return split == 1 || (p.steps >= 4 * split && tiles * split <= WORKGROUPS); }
+
+// The smaller tiles: the time of a step of bf16 and float32 in steps of 128 x 128, alone and beside another product.
+struct Kind {
+  int tile;
+  i64 bm, bn;
+  float step[2], beside[2];
+};
+constexpr Kind KINDS[] = {{TILE_MID, 128, 128, {1.0f, 1.0f}, {1.0f, 1.0f}},
+                          {TILE_NARROW, 128, 64, {0.7f, 0.6f}, {0.7f, 0.6f}},
+                          {TILE_FEW, 32, 64, {0.35f, 0.15f}, {0.45f, 0.25f}}};
+// Up to 32 rows are one tile of the small kind, which is for operands with k along the rows.
+bool single(const Shape& p) { return p.kc && p.M <= 32; }
+bool fits(const Shape& p, const Kind& k) { return k.tile == TILE_FEW ? p.kc : !single(p); }
+
+// what the second launch takes that adds the parts, in steps: a launch, and the parts' bytes
+float sum_time(const Shape& p, int split, float launch) {
+  return split > 1 ? launch + (float)(split * p.items * p.M * p.N * (p.pair ? 8 : 4)) / (p.two ? 2e6f : 4e6f) : 0.0f;
+}
+
+// Whether the large tile fills the 256 CUs by itself (4096 x 2048 -> 8192 dw: 278 us, 327 with 128 x 128) or with k cut into
+// long parts (dx of the same: 317, uncut 446, 128 x 128 347; of 1024 x 4096 -> 12288: 215, 552, 270).
+bool large_plan(const Shape& p, GemmPlan& g) {
+  const i64 large = tiles_of(p, 256, 256);
+  if (large == 0 || single(p)) return false;
+  const i64 cut = large >= 256 ? 1 : 256 / large;
+  g = {TILE_LARGE, (int)cut};
+  return large >= 256 || (cut * large >= 232 && p.steps >= 96 * cut);
+}
+
+// Which tile, and into how many parts k is cut, for a product by itself: by the time of the busiest CU.  bf16 waits for its
+// loads, so that two workgroups of a CU take 1.2 of the time of one; with the small tile and in float32 they take 2.  The
+// constants come from a sweep of the tiles in 1 to 16 parts over 125 products of 1 to 8000 rows: the choice is 1.4 % above
+// the fastest on average.  Forward at 100 x 1024 -> 2048: 6.9 us with 32 x 64, 9.8 with 128 x 64, 12.7 with 128 x 128; at
+// 777 x 1000 -> 2712: 22.8 with 128 x 64, 19 with 128 x 128; dx of 512 x 1024 -> 4096 in 8 parts: 28, 31.
+GemmPlan gemm_plan(const Shape& p) {
+  GemmPlan best;
+  if (large_plan(p, best)) return best;
+  best = {single(p) ? TILE_FEW : TILE_MID, 1};
   float least = INFINITY;
-  for (const Kind& k : kinds) {
-    if (k.tile == TILE_FEW ? !kc : one) continue;
-    for (int split = 1; split <= 16; ++split) {
-      const i64 n = split * tiles(k.bm, k.bn), per_cu = (n + 255) / 256;
-      if (split > 1 && (steps < 4 * split || n > 512)) break;
-      float time = (float)((steps + split - 1) / split) * (two ? k.step : k.step32);
-      if (per_cu > 1) time *= (two ? k.crowd : 1.0f) * (float)per_cu;
-      if (split > 1) time += (two ? 4.0f : 1.5f) + (float)(split * items * M * N * (pair ? 8 : 4)) / (two ? 2e6f : 8e6f);
+  for (const Kind& k : KINDS) {
+    if (!fits(p, k)) continue;
+    const i64 tiles = tiles_of(p, k.bm, k.bn);
+    for (int split = 1; split <= PARTS && may_cut(p, tiles, split); ++split) {
+      const i64 per_cu = (split * tiles + 255) / 256;
+      float time = (float)((p.steps + split - 1) / split) * k.step[p.two ? 0 : 1];
+      if (per_cu > 1) time *= (p.two && k.tile != TILE_FEW ? 0.6f : 1.0f) * (float)per_cu;
+      time += sum_time(p, split, p.two ? 4.0f : 1.5f);
       if (time < least) {
         least = time;
         best = {k.tile, split};
@@ -547,8 +570,60 @@ GemmPlan gemm_plan(i64 M, i64 N, i64 K, int segs, int items, bool pair, bool kc,
   return best;
 }
 
-size_t part_bytes(const GemmPlan& g, i64 M, i64 N, int items, bool pair) {
-  return g.split > 1 ? (size_t)((items * g.split * M * N * (pair ? 8 : 4) + 255) / 256 * 256) : 0;
+// The same for dx and the weights' gradients in one launch, neither on the large tile (else false): 512 workgroups run at
+// one time, those of dx begin first, and dx in few long parts leaves room beside it.  A workgroup takes its steps and 2 more
+// (float32: half of one), two on a CU 1.4 (1.6) of that.  From a sweep of both products' tiles and parts over 18 sizes: 3 % above
+// the fastest on average, the plans that are best alone 13 % (float32 16 %).  Both of 777 x 1000 -> 2712 from the kept gate and
+// up: 42 us with dx in 3 parts of 128 x 128, 50 in 4 of 128 x 64.
+bool grads_plan(const Shape& x, const Shape& w, GemmPlan& px, GemmPlan& pw) {
+  if (large_plan(x, px) || large_plan(w, pw)) return false;
+  const int dt = x.two ? 0 : 1;
+  const float more = x.two ? 2.0f : 0.5f, crowd = x.two ? 1.4f : 1.6f, launch = x.two ? 4.0f : 1.5f;
+  float least = INFINITY;
+  px = {single(x) ? TILE_FEW : TILE_MID, 1};
+  pw = {TILE_MID, 1};
+  for (const Kind& kw : KINDS) {
+    if (!fits(w, kw)) continue;
+    const i64 tw = tiles_of(w, kw.bm, kw.bn);
+    for (int sw = 1; sw <= PARTS && may_cut(w, tw, sw); sw *= 2) {
+      const float nw = (float)(tw * sw), lw = (float)((w.steps + sw - 1) / sw) * kw.beside[dt] + more, jw = sum_time(w, sw, launch);
+      for (const Kind& kx : KINDS) {
+        if (!fits(x, kx)) continue;
+        const i64 tx = tiles_of(x, kx.bm, kx.bn);
+        for (int sx = 1; sx <= PARTS && may_cut(x, tx, sx); ++sx) {
+          const float nx = (float)(tx * sx), lx = (float)((x.steps + sx - 1) / sx) * kx.beside[dt] + more;
+          float time = lx > lw ? lx : lw;
+          if (nx + nw > WORKGROUPS) {
+            const float even = (nx * lx + nw * lw) / WORKGROUPS + 0.7f * lw;
+            time = lx > even ? lx : even;
+          }
+          if (nx + nw > 256) time *= crowd;
+          time += sum_time(x, sx, launch) + jw - (sx > 1 && sw > 1 ? launch : 0.0f);
+          if (time < least) {
+            least = time;
+            px = {kx.tile, sx};
+            pw = {kw.tile, sw};
+          }
+        }
+      }
+    }
+  }
+  return true;
+}
+
+size_t part_bytes(const Shape& p, int split) {
+  return split > 1 ? (size_t)((p.items * split * p.M * p.N * (p.pair ? 8 : 4) + 255) / 256 * 256) : 0;
+}
+// at most, whatever the choice
+size_t most_part_bytes(const Shape& p) {
+  GemmPlan g{TILE_MID, 1};
+  if (large_plan(p, g)) return part_bytes(p, g.split);
+  int most = 1;
+  for (const Kind& k : KINDS)
+    if (fits(p, k))
+      for (int split = PARTS; split > most; --split)
+        if (may_cut(p, tiles_of(p, k.bm, k.bn), split)) most = split;
+  return part_bytes(p, most);
 }
 
 // bytes of LDS: the buffers, or the outputs on their way
@@ -574,13 +649,13 @@ void launch_tile(const FfnArgs& a, hipStream_t s) {
 }
 
 template <typename T, int EPI, bool KC>
-GemmPlan plan_of(const FfnArgs& a) {
-  return gemm_plan(a.M, a.N, a.K, a.segs, a.items, EPI != EPI_PLAIN, KC, sizeof(T));
+Shape shape_of(const FfnArgs& a) {
+  return shape_of(a.M, a.N, a.K, a.segs, a.items, EPI != EPI_PLAIN, KC, sizeof(T));
 }
 
 template <typename T, bool AKC, bool BKC, int EPI, int ACT>
 void launch_gemm(FfnArgs a, float* part, hipStream_t s) {
-  const GemmPlan g = plan_of<T, EPI, AKC>(a);
+  const GemmPlan g = gemm_plan(shape_of<T, EPI, AKC>(a));
   a.split = g.split;
   a.part = part;
   if (g.tile == TILE_LARGE) launch_tile<T, AKC, BKC, EPI, ACT, 256, 256, 2, 4, 2>(a, s);
@@ -608,7 +683,7 @@ void launch_grads(FfnArgs dx, FfnArgs dw, const GemmPlan& px, const GemmPlan& pw
   dx.split = px.split;
   dx.part = part;
   dw.split = pw.split;
-  dw.part = (float*)((char*)part + part_bytes(px, dx.M, dx.N, 1, false));
+  dw.part = (float*)((char*)part + part_bytes(shape_of<T, EPI_PLAIN, true>(dx), px.split));
   const bool mid = pw.tile == TILE_MID;
   if (px.tile == TILE_MID) launch_grads_dx<T, 128, 128, 2, 2>(dx, dw, mid, s);
   else if (px.tile == TILE_NARROW) launch_grads_dx<T, 128, 64, 2, 3>(dx, dw, mid, s);
@@ -650,8 +725,8 @@ void ffn_bwd(const ssmvjp_ffn_desc& d, const FfnBwdPointers& p, hipStream_t s) {
   if (p.dw_gate) w.A[w.items] = {dgate, d.hidden}, w.C[w.items++] = p.dw_gate;
   if (p.dw_up) w.A[w.items] = {dup, d.hidden}, w.C[w.items++] = p.dw_up;
   if (want_dx && w.items) {
-    const GemmPlan px = plan_of<T, EPI_PLAIN, true>(x), pw = plan_of<T, EPI_PLAIN, false>(w);
-    if (px.tile != TILE_LARGE && pw.tile != TILE_LARGE) return launch_grads<T>(x, w, px, pw, part, s);
+    GemmPlan px, pw;
+    if (grads_plan(shape_of<T, EPI_PLAIN, true>(x), shape_of<T, EPI_PLAIN, false>(w), px, pw)) return launch_grads<T>(x, w, px, pw, part, s);
   }
   if (want_dx) launch_gemm<T, true, false, EPI_PLAIN, 0>(x, part, s);
   if (w.items) launch_gemm<T, false, false, EPI_PLAIN, 0>(w, part, s);
@@ -660,20 +735,19 @@ void ffn_bwd(const ssmvjp_ffn_desc& d, const FfnBwdPointers& p, hipStream_t s) {
 }  // namespace
 
 size_t ffn_fwd_workspace_bytes(const ssmvjp_ffn_desc& d) {
-  return part_bytes(gemm_plan(d.rows, d.hidden, d.dim, 1, 1, true, true, d.dtype == SSMVJP_BF16 ? 2 : 4), d.rows, d.hidden, 1, true);
+  const Shape p = shape_of(d.rows, d.hidden, d.dim, 1, 1, true, true, d.dtype == SSMVJP_BF16 ? 2 : 4);
+  return part_bytes(p, gemm_plan(p).split);
 }
 
 // dgate and dup, then the parts: of the forward's products, and behind those of dx and the weights' gradients
 size_t ffn_bwd_workspace_bytes(const ssmvjp_ffn_desc& d) {
-  const size_t elem = d.dtype == SSMVJP_BF16 ? 2 : 4, fwd = ffn_fwd_workspace_bytes(d);
-  const size_t dx = part_bytes(gemm_plan(d.rows, d.dim, d.hidden, 2, 1, false, true, elem), d.rows, d.dim, 1, false);
-  size_t dw = 0;
+  const size_t elem = d.dtype == SSMVJP_BF16 ? 2 : 4, fwd = most_part_bytes(shape_of(d.rows, d.hidden, d.dim, 1, 1, true, true, elem));
+  const size_t dx = most_part_bytes(shape_of(d.rows, d.dim, d.hidden, 2, 1, false, true, elem));
   // one weight's gradient may be asked for without the other
-  for (int items = 1; items <= 2; ++items) {
-    const size_t some = part_bytes(gemm_plan(d.hidden, d.dim, d.rows, 1, items, false, false, elem), d.hidden, d.dim, items, false);
-    dw = dw > some ? dw : some;
-  }
-  return grads_bytes(d) + (fwd > dx + dw ? fwd : dx + dw);
+  const size_t one = most_part_bytes(shape_of(d.hidden, d.dim, d.rows, 1, 1, false, false, elem));
+  const size_t both = most_part_bytes(shape_of(d.hidden, d.dim, d.rows, 1, 2, false, false, elem));
+  const size_t grads = dx + (one > both ? one : both);
+  return grads_bytes(d) + (fwd > grads ? fwd : grads);
 }
 
 hipError_t launch_ffn_fwd(const ssmvjp_ffn_desc& d, const FfnFwdPointers& p, hipStream_t stream) {

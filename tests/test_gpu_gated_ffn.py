@@ -103,7 +103,9 @@ def agrees(M, D, F, dtype):
     assert only["dw_gate"] is None
     near(only["dx"], torch.mm(dg, G) + torch.mm(du, Uw), rows, "dx alone")
     only = bd.gated_ffn_bwd(dh, x, wg, wu, saved=saved, want_dx=False)
-    assert only["dx"] is None and torch.equal(only["dw_gate"], got["dw_gate"]) and torch.equal(only["dw_up"], got["dw_up"])
+    assert only["dx"] is None  # another call may cut k elsewhere
+    near(only["dw_gate"], torch.mm(dg.T, X), cols, "dw_gate without dx")
+    near(only["dw_up"], torch.mm(du.T, X), cols, "dw_up without dx")
 
 
 # 256 x 256 of the forward and of what it forms again; of dx; of the weights' gradients; of dx with k in parts
