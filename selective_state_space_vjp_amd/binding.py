@@ -187,8 +187,9 @@ def _on_gpu(device, *tensors):
     """Every tensor handed to the library lives on the same GPU (there is no CPU path)."""
     if not device.type == "cuda":
         raise ValueError("inputs must be GPU tensors (there is no CPU path)")
+    index = device.index
     for t in tensors:
-        if t is not None and t.device != device:
+        if t is not None and t.get_device() != index:
             raise ValueError(f"a tensor is on {t.device}, expected {device} (there is no CPU path)")
 
 
@@ -608,7 +609,7 @@ def _scope(dev, stream):
         if stream.device != dev:
             raise ValueError(f"the stream is on {stream.device}, the tensors on {dev}")
         return torch.cuda.stream(stream)
-    return _HERE if torch.cuda.current_device() == dev.index else torch.cuda.device(dev)
+    return _HERE if torch._C._cuda_getDevice() == dev.index else torch.cuda.device(dev)
 
 
 def _required(**tensors):
