@@ -10,8 +10,11 @@
 //
 // dgate and dup are rounded to the type between the products, as gate and up are
 // when they are kept: the gradients of bf16 come out at 2.3e-3 of the norm, the
-// two roundings of 1.7e-3 together; in two parts each they would take twice the
-// products.
+// two roundings of 1.7e-3 together.  In two parts each (the value's rounding and
+// what that leaves) they take twice the products, and the gradients come out at
+// 1.7e-3: that is done where a result has few values or few roundings in it,
+// whose errors do not average out (up to 2.6e-3 otherwise), and the time is the
+// launches' (TWO_PARTS).
 //
 // The matrix cores and what feeds them are the bound: bf16 at 8192 x 4096 ->
 // 12288 runs at 1.31 PFLOP/s without and 1.24 with gate and up (their 400 MB are
@@ -41,12 +44,12 @@ struct Operand {
 
 struct FfnArgs {
   i64 M, N, K;          // K: of one segment
-  Operand A[2], B[2];   // PAIR: A[0] with both B; else segments of k
+  Operand A[4], B[2];   // PAIR: A[0] with both B; else segments of k, segment s of A with B[s % 2]
   int segs;
   i64 ldc;
-  void* C[3];           // h, gate, up | dgate, dup | C
+  void* C[4];           // h, gate, up | dgate, dup and, in two parts, what their roundings leave | C
   const void *dh;       // BACK: [M, N]
-  int items;            // products of one shape in one launch: A[i], C[i] (EPI_PLAIN, segs = 1)
+  int items;            // products of one shape in one launch: A[i segs ..], C[i] (EPI_PLAIN)
   int split;            // parts of k, each a workgroup's; more than one: sums to part
   float* part;          // [items][split][PAIR ? 2 : 1][M][N]
 };
@@ -213,9 +216,16 @@ __device__ __forceinline__ void step_barrier() {
   asm volatile("" ::: "memory");
 }
 
-// What the sums v[0] (and v[1], PAIR) of four n of one m become: the values of the outputs 0, 1, 2.  e: where dh has them.
+// what the rounding of v leaves; nothing of a value that is rounded to an infinity or is none
+template <typename T>
+__device__ __forceinline__ float left_over(float v) {
+  const float r = (float)(T)v;
+  return fabsf(r) < INFINITY ? v - r : 0.0f;
+}
+
+// What the sums v[0] (and v[1], PAIR) of four n of one m become: the values of the outputs.  e: where dh has them.
 template <typename T, int EPI, int ACT>
-__device__ __forceinline__ void finish4(const FfnArgs& a, i64 e, float (&v)[3][4]) {
+__device__ __forceinline__ void finish4(const FfnArgs& a, i64 e, float (&v)[4][4]) {
   if constexpr (EPI == EPI_GLU) {
 #pragma unroll
     for (int r = 0; r < 4; ++r) {
@@ -232,17 +242,23 @@ __device__ __forceinline__ void finish4(const FfnArgs& a, i64 e, float (&v)[3][4
       v[0][r] = v[2][r] * v[1][r] * df;
       v[1][r] = v[2][r] * f;
     }
+    if (a.C[2])
+#pragma unroll
+      for (int r = 0; r < 4; ++r) {
+        v[2][r] = left_over<T>(v[0][r]);
+        v[3][r] = left_over<T>(v[1][r]);
+      }
   }
 }
 template <int EPI>
 __device__ __forceinline__ int outputs(const FfnArgs& a) {
-  return EPI == EPI_PLAIN ? 1 : EPI == EPI_GLU_BACK ? 2 : a.C[1] ? 3 : 1;
+  return EPI == EPI_PLAIN ? 1 : EPI == EPI_GLU_BACK ? (a.C[2] ? 4 : 2) : a.C[1] ? 3 : 1;
 }
 
 // The outputs on their way through LDS: ROWS of a wave's FM rows of 16 at a time, the most that fit, in 1, 2, 4 .. parts.
-template <typename T, bool PAIR, int BM, int NOUT, int FM>
+template <typename T, int EPI, int BM, int NOUT, int FM>
 struct StoreOf {
-  static constexpr int PITCH = NOUT * (int)sizeof(T) + 16, ALL = (PAIR ? 3 : 1) * BM * PITCH;
+  static constexpr int PITCH = NOUT * (int)sizeof(T) + 16, ALL = (EPI == EPI_PLAIN ? 1 : EPI == EPI_GLU ? 3 : 4) * BM * PITCH;
   static constexpr int PARTS = FM > 2 && ALL / 2 > LDS_BYTES ? 4 : FM > 1 ? 2 : 1;
   static constexpr int ROWS = FM / PARTS, BYTES = ALL / PARTS;
   static_assert(FM % PARTS == 0 && BYTES <= LDS_BYTES, "");
@@ -279,11 +295,11 @@ __device__ __forceinline__ void gemm_tile(const FfnArgs& a, const unsigned block
   for (int i = 0; i < IB; ++i) offB[i] = TB::source((wave * IB + i) * 64 + lane, (unsigned)(a.B[0].ld * sizeof(T)));
 
   auto load = [&](int at, int buf) {
-    const int step = first + at, s = !PAIR && step >= steps1;
+    const int step = first + at, s = PAIR ? 0 : (step >= steps1) + (step >= 2 * steps1) + (step >= 3 * steps1);
     const i64 k0 = (i64)(step - s * steps1) * KB;
     const bool part = k0 + KB > a.K;  // KC: chunks past the last k would be the next row's
     const unsigned to = base + buf * BUF;
-    const u32x4 ra = tile_rsrc<T, AKC>(a.A[s + item], m0, a.M, k0, a.K, BM);
+    const u32x4 ra = tile_rsrc<T, AKC>(a.A[s + item * a.segs], m0, a.M, k0, a.K, BM);
 #pragma unroll
     for (int i = 0; i < IA; ++i) {
       unsigned off = offA[i];
@@ -292,7 +308,7 @@ __device__ __forceinline__ void gemm_tile(const FfnArgs& a, const unsigned block
     }
 #pragma unroll
     for (int p = 0; p < (PAIR ? 2 : 1); ++p) {
-      const u32x4 rb = tile_rsrc<T, BKC>(a.B[PAIR ? p : s], n0, a.N, k0, a.K, NOUT);
+      const u32x4 rb = tile_rsrc<T, BKC>(a.B[PAIR ? p : s & 1], n0, a.N, k0, a.K, NOUT);
 #pragma unroll
       for (int i = 0; i < IB; ++i) {
         unsigned off = offB[i];
@@ -373,7 +389,7 @@ __device__ __forceinline__ void gemm_tile(const FfnArgs& a, const unsigned block
   // Through LDS, so that whole rows of the tile are stored by 16 bytes a lane: a part of every wave's rows at a time, all
   // outputs side by side (8192 x 4096 -> 12288 with gate and up: 1350 us; 1440 with stores of 32 bytes of a row from the
   // registers).
-  typedef StoreOf<T, PAIR, BM, NOUT, FM> SO;
+  typedef StoreOf<T, EPI, BM, NOUT, FM> SO;
   constexpr int ROWS = SO::ROWS, ER = WM * 16 * ROWS, PITCH = SO::PITCH, CHUNKS = NOUT * (int)sizeof(T) / 16;
   const int nout = outputs<EPI>(a);
 #pragma unroll
@@ -387,7 +403,7 @@ __device__ __forceinline__ void gemm_tile(const FfnArgs& a, const unsigned block
         const int col = wn + 16 * j + 4 * (lane >> 4);
         const i64 m = m0 + wm + 16 * (h * ROWS + i) + (lane & 15), n = n0 + col;
         const bool in = m < a.M && n < a.N;
-        float v[3][4];
+        float v[4][4];
 #pragma unroll
         for (int r = 0; r < 4; ++r) {
           v[0][r] = acc[h * ROWS + i][j][r];
@@ -399,7 +415,8 @@ __device__ __forceinline__ void gemm_tile(const FfnArgs& a, const unsigned block
         if constexpr (PAIR)
           if (nout > 1) {
             store4<T>(to + ER * PITCH, 0, v[1]);
-            if constexpr (EPI == EPI_GLU) store4<T>(to + 2 * ER * PITCH, 0, v[2]);
+            if (EPI == EPI_GLU || nout > 2) store4<T>(to + 2 * ER * PITCH, 0, v[2]);
+            if (EPI == EPI_GLU_BACK && nout > 2) store4<T>(to + 3 * ER * PITCH, 0, v[3]);
           }
       }
     step_wait<0>();
@@ -436,7 +453,7 @@ __device__ __forceinline__ void join_parts(const FfnArgs& a, const i64 block, co
   for (i64 i = (block * 256 + threadIdx.x) * 4; i < each * a.items; i += blocks * 1024) {
     const int item = (int)(i / each);
     const i64 e = i - item * each;
-    float v[3][4];
+    float v[4][4];
 #pragma unroll
     for (int p = 0; p < (PAIR ? 2 : 1); ++p) {
       const float* part = a.part + ((PAIR ? 2 : 1) * (i64)item * a.split + p) * each + e;
@@ -451,11 +468,12 @@ __device__ __forceinline__ void join_parts(const FfnArgs& a, const i64 block, co
     const i64 at = e / a.N * a.ldc + e % a.N;
     finish4<T, EPI, ACT>(a, at, v);
     store4<T>(a.C[EPI == EPI_PLAIN ? item : 0], at, v[0]);
-    if constexpr (PAIR)
-      if (outputs<EPI>(a) > 1) {
-        store4<T>(a.C[1], at, v[1]);
-        if constexpr (EPI == EPI_GLU) store4<T>(a.C[2], at, v[2]);
-      }
+    if constexpr (PAIR) {
+      const int nout = outputs<EPI>(a);
+      if (nout > 1) store4<T>(a.C[1], at, v[1]);
+      if (nout > 2) store4<T>(a.C[2], at, v[2]);
+      if (nout > 3) store4<T>(a.C[3], at, v[3]);
+    }
   }
 }
 
@@ -469,23 +487,33 @@ __global__ void __launch_bounds__(256) ffn_join_grads_kernel(FfnArgs dx, FfnArgs
   else join_parts<T, EPI_PLAIN, 0>(dw, blockIdx.x - blocks, gridDim.x - blocks);
 }
 
-// dgate, dup from the kept gate and up, 16 bytes a lane; n a multiple of 8
-template <typename T, int ACT>
+// dgate, dup (TWO: and what their roundings leave, n further on each) from the kept gate and up, 16 bytes a lane; n a
+// multiple of 8
+template <typename T, int ACT, bool TWO>
 __global__ void __launch_bounds__(256) ffn_grad_kernel(const T* dh, const T* gate, const T* up, T* dgate, T* dup, i64 n) {
   constexpr int W = 16 / sizeof(T);
   typedef T vec __attribute__((ext_vector_type(W)));
   for (i64 e = ((i64)blockIdx.x * 256 + threadIdx.x) * W; e < n; e += (i64)gridDim.x * 256 * W) {
     const vec d = *(const vec*)(dh + e), g = *(const vec*)(gate + e), u = *(const vec*)(up + e);
-    vec og, ou;
+    vec og, ou, og2, ou2;
 #pragma unroll
     for (int r = 0; r < W; ++r) {
       float f, df;
       act_pair<ACT>((float)g[r], f, df);
-      og[r] = (T)((float)d[r] * (float)u[r] * df);
-      ou[r] = (T)((float)d[r] * f);
+      const float vg = (float)d[r] * (float)u[r] * df, vu = (float)d[r] * f;
+      og[r] = (T)vg;
+      ou[r] = (T)vu;
+      if constexpr (TWO) {
+        og2[r] = (T)left_over<T>(vg);
+        ou2[r] = (T)left_over<T>(vu);
+      }
     }
     *(vec*)(dgate + e) = og;
     *(vec*)(dup + e) = ou;
+    if constexpr (TWO) {
+      *(vec*)(dgate + 2 * n + e) = og2;
+      *(vec*)(dup + 2 * n + e) = ou2;
+    }
   }
 }
 
@@ -629,7 +657,7 @@ size_t most_part_bytes(const Shape& p) {
 // bytes of LDS: the buffers, or the outputs on their way
 template <typename T, int EPI, int BM, int BN, int WM, int NB>
 constexpr int lds_bytes() {
-  constexpr int loop = NB * (BM + BN) * ROWB, rows = StoreOf<T, EPI != EPI_PLAIN, BM, EPI != EPI_PLAIN ? BN / 2 : BN, BM / WM / 16>::BYTES;
+  constexpr int loop = NB * (BM + BN) * ROWB, rows = StoreOf<T, EPI, BM, EPI != EPI_PLAIN ? BN / 2 : BN, BM / WM / 16>::BYTES;
   static_assert(loop <= LDS_BYTES, "");
   return loop > rows ? loop : rows;
 }
@@ -698,32 +726,48 @@ void ffn_fwd(const ssmvjp_ffn_desc& d, const FfnFwdPointers& p, hipStream_t s) {
   launch_gemm<T, true, true, EPI_GLU, ACT>(a, (float*)p.workspace, s);
 }
 
-// dgate and dup
+// Whether dgate and dup of bf16 are kept in two parts: where dx, a weight's gradient or dgate itself has fewer than
+// TWO_PARTS values.  The errors of 2048 values are their average within 2 %.
+constexpr i64 TWO_PARTS = 2048;
+int grads_parts(const ssmvjp_ffn_desc& d) {
+  const i64 dx = d.rows * d.dim, dw = d.hidden * d.dim, dgate = d.rows * d.hidden, some = dx < dw ? dx : dw;
+  return d.dtype == SSMVJP_BF16 && (some < dgate ? some : dgate) < TWO_PARTS ? 2 : 1;
+}
+// dgate, dup, and their second parts
 size_t grads_bytes(const ssmvjp_ffn_desc& d) {
-  return (size_t)((2 * d.rows * d.hidden * (d.dtype == SSMVJP_BF16 ? 2 : 4) + 255) / 256 * 256);
+  return (size_t)((grads_parts(d) * 2 * d.rows * d.hidden * (d.dtype == SSMVJP_BF16 ? 2 : 4) + 255) / 256 * 256);
 }
 
 template <typename T, int ACT>
 void ffn_bwd(const ssmvjp_ffn_desc& d, const FfnBwdPointers& p, hipStream_t s) {
   const i64 n = d.rows * d.hidden;
-  T *dgate = (T*)p.workspace, *dup = dgate + n;
+  const bool two = grads_parts(d) == 2;
+  T *dgate = (T*)p.workspace, *dup = dgate + n, *dgate2 = two ? dup + n : nullptr, *dup2 = two ? dgate2 + n : nullptr;
   float* part = (float*)((char*)p.workspace + grads_bytes(d));
   if (n > 0) {
     if (p.gate) {
       const i64 need = (n * (i64)sizeof(T) + 4095) / 4096, blocks = need < (1 << 22) ? need : 1 << 22;
-      hipLaunchKernelGGL((ffn_grad_kernel<T, ACT>), dim3((unsigned)blocks), dim3(256), 0, s, (const T*)p.dh, (const T*)p.gate,
-                         (const T*)p.up, dgate, dup, n);
+      const dim3 grid((unsigned)blocks);
+      const T *dh = (const T*)p.dh, *gate = (const T*)p.gate, *up = (const T*)p.up;
+      if (two) hipLaunchKernelGGL((ffn_grad_kernel<T, ACT, true>), grid, dim3(256), 0, s, dh, gate, up, dgate, dup, n);
+      else hipLaunchKernelGGL((ffn_grad_kernel<T, ACT, false>), grid, dim3(256), 0, s, dh, gate, up, dgate, dup, n);
     } else {
-      FfnArgs a{d.rows, d.hidden, d.dim, {{p.x, d.dim}}, {{p.w_gate, d.dim}, {p.w_up, d.dim}}, 1, d.hidden, {dgate, dup}, p.dh, 1, 1, nullptr};
+      FfnArgs a{d.rows, d.hidden, d.dim, {{p.x, d.dim}}, {{p.w_gate, d.dim}, {p.w_up, d.dim}}, 1, d.hidden, {dgate, dup, dgate2, dup2}, p.dh, 1, 1, nullptr};
       launch_gemm<T, true, true, EPI_GLU_BACK, ACT>(a, part, s);
     }
   }
   const bool want_dx = p.dx && n > 0;
-  const FfnArgs x{d.rows, d.dim, d.hidden, {{dgate, d.hidden}, {dup, d.hidden}}, {{p.w_gate, d.dim}, {p.w_up, d.dim}}, 2, d.dim, {p.dx}, nullptr, 1, 1, nullptr};
+  const FfnArgs x{d.rows, d.dim, d.hidden, {{dgate, d.hidden}, {dup, d.hidden}, {dgate2, d.hidden}, {dup2, d.hidden}},
+                  {{p.w_gate, d.dim}, {p.w_up, d.dim}}, two ? 4 : 2, d.dim, {p.dx}, nullptr, 1, 1, nullptr};
   // both weights' gradients are one product
-  FfnArgs w{d.hidden, d.dim, d.rows, {}, {{p.x, d.dim}}, 1, d.dim, {}, nullptr, 0, 1, nullptr};
-  if (p.dw_gate) w.A[w.items] = {dgate, d.hidden}, w.C[w.items++] = p.dw_gate;
-  if (p.dw_up) w.A[w.items] = {dup, d.hidden}, w.C[w.items++] = p.dw_up;
+  FfnArgs w{d.hidden, d.dim, d.rows, {}, {{p.x, d.dim}, {p.x, d.dim}}, two ? 2 : 1, d.dim, {}, nullptr, 0, 1, nullptr};
+  const auto weight = [&](const T* first, const T* second, void* out) {
+    w.A[w.items * w.segs] = {first, d.hidden};
+    if (two) w.A[w.items * w.segs + 1] = {second, d.hidden};
+    w.C[w.items++] = out;
+  };
+  if (p.dw_gate) weight(dgate, dgate2, p.dw_gate);
+  if (p.dw_up) weight(dup, dup2, p.dw_up);
   if (want_dx && w.items) {
     GemmPlan px, pw;
     if (grads_plan(shape_of<T, EPI_PLAIN, true>(x), shape_of<T, EPI_PLAIN, false>(w), px, pw)) return launch_grads<T>(x, w, px, pw, part, s);
@@ -742,10 +786,11 @@ size_t ffn_fwd_workspace_bytes(const ssmvjp_ffn_desc& d) {
 // dgate and dup, then the parts: of the forward's products, and behind those of dx and the weights' gradients
 size_t ffn_bwd_workspace_bytes(const ssmvjp_ffn_desc& d) {
   const size_t elem = d.dtype == SSMVJP_BF16 ? 2 : 4, fwd = most_part_bytes(shape_of(d.rows, d.hidden, d.dim, 1, 1, true, true, elem));
-  const size_t dx = most_part_bytes(shape_of(d.rows, d.dim, d.hidden, 2, 1, false, true, elem));
+  const int parts = grads_parts(d);
+  const size_t dx = most_part_bytes(shape_of(d.rows, d.dim, d.hidden, 2 * parts, 1, false, true, elem));
   // one weight's gradient may be asked for without the other
-  const size_t one = most_part_bytes(shape_of(d.hidden, d.dim, d.rows, 1, 1, false, false, elem));
-  const size_t both = most_part_bytes(shape_of(d.hidden, d.dim, d.rows, 1, 2, false, false, elem));
+  const size_t one = most_part_bytes(shape_of(d.hidden, d.dim, d.rows, parts, 1, false, false, elem));
+  const size_t both = most_part_bytes(shape_of(d.hidden, d.dim, d.rows, parts, 2, false, false, elem));
   const size_t grads = dx + (one > both ? one : both);
   return grads_bytes(d) + (fwd > grads ? fwd : grads);
 }

@@ -128,6 +128,41 @@ def test_every_pair_of_tiles(M, D, F, dtype):
     agrees(M, D, F, dtype)
 
 
+@pytest.mark.parametrize("M,D,F", [(48, 392, 8), (1, 64, 2584), (1, 3208, 16), (30, 16, 1232), (3, 8, 8), (2500, 8, 200),
+                                   (700, 128, 8), (1, 1000, 4104)])
+@pytest.mark.parametrize("act", ["silu", "gelu"])
+def test_few_values_are_formed_from_two_parts(M, D, F, act):
+    """A gradient is off by its own rounding, 2^-8 of it at most, and by what two parts of dgate and dup leave: 2^-16 of
+    every term, with the float32 errors of the products and the sums (a few 2^-22) 2^-15.  act' has a zero, near which its
+    error is not one of itself: with u = 2^-24 and |z| <= 5, s is off by (|z| + 4) s (1 - s) u <= 2 u, f = z s by 11 u,
+    f (1 - s) by 11 u + 5 * 2 u, act' by 24 u; in GELU's f (1 - s) <= 0.2 meets a factor of at most 1.6 (1 + 0.13 z^2) <= 7
+    and is off by (|2 v| + 6) <= 40 u of itself where that is more than u, so by 56 u: 2^-18 of dh up in dgate.
+    gate and up that are formed again are sums of D terms: each addition rounds a partial sum of at most 5 by 5 u to either
+    side, D of them wander off by 5 u sqrt(D / 3), six times that is below 2^-19 sqrt(D); |act'| and |act''| <= 1.2."""
+    announce(f"gated ffn two parts {act} {M} {D} {F}")
+    x, wg, wu, dh = (v.to(DEV) for v in inputs(M, D, F, BF, 8))
+    out = bd.gated_ffn_fwd(x, wg, wu, act=act, want_saved=True)
+    X, G, Uw, H = (v.double() for v in (x, wg, wu, dh))
+    for saved in (None, (out["gate"], out["up"])):
+        gate, up = (v.double() for v in saved) if saved else (torch.mm(X, G.T), torch.mm(X, Uw.T))
+        gate.requires_grad_(True)
+        f = gate * torch.sigmoid(gate) if act == "silu" else torch.nn.functional.gelu(gate, approximate="tanh")
+        df, = torch.autograd.grad(f.sum(), gate)
+        dg, du = H * up * df, H * f.detach()
+        eg = 2.0**-15 * dg.abs() + 2.0**-18 * (H * up).abs()
+        eu = 2.0**-15 * du.abs()
+        if not saved:
+            wander = 1.2 * 2.0**-19 * math.sqrt(D)
+            eg += wander * (H.abs() + (H * up).abs())
+            eu += wander * H.abs()
+        got = bd.gated_ffn_bwd(dh, x, wg, wu, act=act, saved=saved)
+        for k, want, left in (("dx", torch.mm(dg, G) + torch.mm(du, Uw), torch.mm(eg, G.abs()) + torch.mm(eu, Uw.abs())),
+                              ("dw_gate", torch.mm(dg.T, X), torch.mm(eg.T, X.abs())),
+                              ("dw_up", torch.mm(du.T, X), torch.mm(eu.T, X.abs()))):
+            over = (got[k].double() - want).abs() - 2.0**-8 * want.abs() - left
+            assert float(over.max()) <= 0, (k, float(over.max()))
+
+
 @pytest.mark.parametrize("dtype", [F32, BF], ids=["f32", "bf16"])
 def test_rows_are_independent(dtype):
     """A row's result does not depend on which rows stand beside it where the same kernel runs, a NaN row harms no other,
