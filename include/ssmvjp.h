@@ -576,8 +576,8 @@ ssmvjp_status gated_ffn_fwd(const ssmvjp_ffn_desc* desc, const void* x, const vo
  *   dgate = dh up act'(gate);  dup = dh act(gate);
  *   dx = dgate w_gate + dup w_up;  dw_gate = dgate^T x;  dw_up = dup^T x
  * Outputs like their inputs, each NULL = not computed; zeros when rows = 0.  dgate and dup
- * are kept in `dtype` between the products, in bf16 as the sum of two values where rows dim,
- * hidden dim or rows hidden is below 2048.  Constraints as for gated_ffn_fwd. */
+ * are kept in `dtype` between the products, in bf16 as the sum of two values where rows
+ * hidden or hidden dim is below 8192 or rows dim below 2048.  Constraints as for gated_ffn_fwd. */
 ssmvjp_status gated_ffn_bwd_workspace(const ssmvjp_ffn_desc* desc, size_t* bytes);
 ssmvjp_status gated_ffn_bwd(const ssmvjp_ffn_desc* desc, const void* dh, const void* x, const void* w_gate,
                             const void* w_up, const void* gate, const void* up, void* dx, void* dw_gate, void* dw_up,

@@ -726,12 +726,14 @@ void ffn_fwd(const ssmvjp_ffn_desc& d, const FfnFwdPointers& p, hipStream_t s) {
   launch_gemm<T, true, true, EPI_GLU, ACT>(a, (float*)p.workspace, s);
 }
 
-// Whether dgate and dup of bf16 are kept in two parts: where dx, a weight's gradient or dgate itself has fewer than
-// TWO_PARTS values.  The errors of 2048 values are their average within 2 %.
-constexpr i64 TWO_PARTS = 2048;
+// Whether dgate and dup of bf16 are kept in two parts: where dgate or a weight's gradient has fewer than TWO_PARTS values,
+// of products of normal ones, among which few large ones count, or dx, whose values are sums, fewer than a quarter of
+// that.  Over 400 drawn sizes the gradients are then at most 1.45 of the error that their own roundings would leave (1.55
+// without).  33 x 400 -> 96: 10.9 us instead of 9.6.
+constexpr i64 TWO_PARTS = 8192;
 int grads_parts(const ssmvjp_ffn_desc& d) {
-  const i64 dx = d.rows * d.dim, dw = d.hidden * d.dim, dgate = d.rows * d.hidden, some = dx < dw ? dx : dw;
-  return d.dtype == SSMVJP_BF16 && (some < dgate ? some : dgate) < TWO_PARTS ? 2 : 1;
+  const bool few = d.rows * d.hidden < TWO_PARTS || d.hidden * d.dim < TWO_PARTS || d.rows * d.dim < TWO_PARTS / 4;
+  return d.dtype == SSMVJP_BF16 && few ? 2 : 1;
 }
 // dgate, dup, and their second parts
 size_t grads_bytes(const ssmvjp_ffn_desc& d) {

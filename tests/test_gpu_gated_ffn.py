@@ -129,7 +129,7 @@ def test_every_pair_of_tiles(M, D, F, dtype):
 
 
 @pytest.mark.parametrize("M,D,F", [(48, 392, 8), (1, 64, 2584), (1, 3208, 16), (30, 16, 1232), (3, 8, 8), (2500, 8, 200),
-                                   (700, 128, 8), (1, 1000, 4104)])
+                                   (700, 128, 8), (1, 1000, 4104), (33, 400, 96), (1, 2000, 8200)])
 @pytest.mark.parametrize("act", ["silu", "gelu"])
 def test_few_values_are_formed_from_two_parts(M, D, F, act):
     """A gradient is off by its own rounding, 2^-8 of it at most, and by what two parts of dgate and dup leave: 2^-16 of
