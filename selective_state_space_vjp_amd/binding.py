@@ -955,7 +955,8 @@ def linear_scan_fwd(x, gate, h0=None, *, input_gate=None, decay=None, c=8.0, seq
     """
     desc = _linear_scan_inputs(x, gate, h0, input_gate, decay, c, seq_offsets)
     dev, f32 = x.device, torch.float32
-    final, kept = (desc.batch, desc.dim), linear_scan_ckpt_shape(desc)
+    final = (desc.batch, desc.dim)
+    kept = linear_scan_ckpt_shape(desc) if want_ckpt or out is not None else None
     if out is not None:
         if out.get("h") is None:
             raise ValueError("out is missing 'h'")
@@ -982,11 +983,12 @@ def linear_scan_bwd(x, gate, dh, h0=None, dh_final=None, *, input_gate=None, dec
     sequence of a packed call owns are left as they were.  dh0 must not be dh_final.
     """
     desc = _linear_scan_inputs(x, gate, h0, input_gate, decay, c, seq_offsets)
-    _required(dh=dh)
-    dev, f32 = x.device, torch.float32
+    dev, f32, xs, dtype = x.device, torch.float32, x.shape, x.dtype
     gated, final = decay is not None, (desc.batch, desc.dim)
-    _needs(dev, ("dh", dh, x.dtype, x.shape), ("dh_final", dh_final, f32, final),
-           ("ckpt", ckpt, f32, linear_scan_ckpt_shape(desc)))
+    if (dh is None or not _fits(dh, dtype, xs) or not (dh_final is None or _fits(dh_final, f32, final))
+            or not (ckpt is None or _fits(ckpt, f32, linear_scan_ckpt_shape(desc)))):
+        _required(dh=dh)
+        _needs(dev, ("dh", dh, dtype, xs), ("dh_final", dh_final, f32, final), ("ckpt", ckpt, f32, linear_scan_ckpt_shape(desc)))
     if out is not None:
         spec = {"dx": (x.dtype, x.shape), "dgate": (gate.dtype, x.shape)}
         if gated:
