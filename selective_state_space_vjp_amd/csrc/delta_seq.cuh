@@ -29,6 +29,21 @@ struct DeltaSeqs {
     const i64 o = off[s];
     return o < 0 ? 0 : o > T ? T : o;
   }
+  // the largest of borders 0 .. s, where a border below one before it counts as that one; called by whole waves
+  __device__ __forceinline__ i64 risen(i64 s, int lane) const {
+    int most = 0;
+#pragma unroll 4
+    for (i64 i = lane; i <= s; i += 64) {
+      const int o = (int)border(i);
+      most = o > most ? o : most;
+    }
+#pragma unroll
+    for (int d = 1; d < 64; d *= 2) {
+      const int o = __shfl_xor(most, d);
+      most = o > most ? o : most;
+    }
+    return most;
+  }
   __device__ __forceinline__ DeltaSpan span(i64 s) const {
     if (!off) return {s * T, T, s * per};
     const i64 o0 = border(s), o1 = border(s + 1);

@@ -654,21 +654,22 @@ __global__ void __launch_bounds__(64 * NW) scan_bwd_kernel(ScanArgs a) {
 }
 
 // Before a call whose tiles wait for each other: the filling of what they publish, and the counter.  Sequences without
-// tokens, which have no tile: their final state (`to`) is their first (`from`).  Rows of ckpt that no token has: zeros.
-__global__ void __launch_bounds__(256) scan_init_kernel(u64* pairs, i64 words, const int* off, i64 nseq, i64 T, i64 D,
-                                                        const float* from, float* to, float* clear, i64 nclear) {
+// tokens, which have no tile: their final state (`to`) is their first (`from`).  Which those are goes by the rule of the
+// tiles (of_slot): the end is not above any border before it.  Rows of ckpt that no token has: zeros.
+constexpr int INIT_CHANNELS = 256;  // of one sequence, a wave's at a time
+__global__ void __launch_bounds__(256) scan_init_kernel(u64* pairs, i64 words, DeltaSeqs seqs, i64 D, const float* from, float* to,
+                                                        float* clear, i64 nclear) {
   const i64 i0 = (i64)blockIdx.x * 256 + threadIdx.x, step = (i64)gridDim.x * 256;
   for (i64 i = i0; i < words; i += step) pairs[i] = NO_PAIR;
   for (i64 i = i0; i < nclear; i += step) clear[i] = 0.0f;
   if (!to) return;
-  for (i64 i = i0; i < nseq * D; i += step) {
-    const i64 s = i / D;
-    bool empty = T == 0;
-    if (off) {
-      const i64 o0 = off[s] < 0 ? 0 : off[s] > T ? T : off[s], o1 = off[s + 1] < 0 ? 0 : off[s + 1] > T ? T : off[s + 1];
-      empty = o1 <= o0;
-    }
-    if (empty) to[i] = from ? from[i] : 0.0f;
+  const int lane = threadIdx.x & 63;
+  const i64 per = (D + INIT_CHANNELS - 1) / INIT_CHANNELS;
+  for (i64 i = uniform(i0 / 64); i < seqs.nseq * per; i += step / 64) {
+    const i64 s = i / per;
+    if (seqs.off ? seqs.border(s + 1) > seqs.risen(s, lane) : seqs.T > 0) continue;
+    for (i64 ch = (i - s * per) * INIT_CHANNELS + lane, k = 0; k < INIT_CHANNELS && ch < D; k += 64, ch += 64)
+      to[s * D + ch] = from ? from[s * D + ch] : 0.0f;
   }
 }
 
@@ -775,10 +776,11 @@ void set_chain(const ssmvjp_linear_scan_desc& d, int n, void* workspace, ScanArg
 void launch_init(const ScanArgs& a, void* base, i64 words, const float* from, float* to, float* clear, i64 nclear, hipStream_t s) {
   if (words <= 0 && !to && nclear <= 0) return;
   i64 most = words > nclear ? words : nclear;
-  if (to && a.nseq * a.D > most) most = a.nseq * a.D;
+  const i64 shares = to ? a.nseq * ((a.D + INIT_CHANNELS - 1) / INIT_CHANNELS) * INIT_CHANNELS : 0;
+  if (shares > most) most = shares;
   const i64 blocks = (most + 1023) / 1024 < 2048 ? (most + 1023) / 1024 : 2048;
-  hipLaunchKernelGGL(scan_init_kernel, dim3((unsigned)(blocks > 0 ? blocks : 1)), dim3(256), 0, s, (u64*)base, words, a.off, a.nseq,
-                     a.T, a.D, from, to, clear, nclear);
+  hipLaunchKernelGGL(scan_init_kernel, dim3((unsigned)(blocks > 0 ? blocks : 1)), dim3(256), 0, s, (u64*)base, words,
+                     DeltaSeqs{a.off, a.nseq, a.T, a.per}, a.D, from, to, clear, nclear);
 }
 
 template <typename T, bool GATED, int V, bool BWD, bool STREAM>
