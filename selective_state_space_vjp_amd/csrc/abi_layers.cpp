@@ -42,7 +42,7 @@ ssmvjp_status finite_check_tokens(const ssmvjp_delta_chunk_desc& d, const int32_
                                   size_t plan_bytes, const OutSpan (&outs)[K], const OutSpan (&rows)[R], hipStream_t stream) {
   return finite_check(workspace, plan_bytes, outs, stream, [&](unsigned* flag) {
     for (const OutSpan& r : rows)
-      if (d.packed) launch_nonfinite_check_rows(r.p, r.n, r.bf16, seq_offsets, d.batch, d.seqlen, flag, stream);
+      if (d.packed) launch_nonfinite_check_rows(r.p, r.n, r.bf16, seq_offsets, d.batch, d.seqlen, false, flag, stream);
       else launch_nonfinite_check(r.p, r.n * chunk_tokens(d), r.bf16, flag, stream);
   });
 }

@@ -21,14 +21,17 @@ __global__ void __launch_bounds__(256) nonfinite_scan_kernel(const T* p, i64 n, 
 }
 
 // ---- outputs of which a call writes a part that only device memory knows ----
-// elements [lo, hi) of part i: the rows of a packed call's sequence ...
+// elements [lo, hi) of part i: the rows of a packed call's sequence (rising: a border below one before it counts as that
+// one, as in the linear recurrence; called by whole waves) ...
 struct OwnedRows {
   DeltaSeqs seq;
   i64 n;  // elements of a row
+  bool rising;
   __device__ __forceinline__ void part(i64 i, i64& lo, i64& hi) const {
     const DeltaSpan sp = seq.span(i);
-    lo = sp.start * n;
-    hi = lo + sp.len * n;
+    const i64 start = rising ? seq.risen(i, threadIdx.x & 63) : sp.start, end = sp.start + sp.len;
+    lo = start * n;
+    hi = end > start ? end * n : lo;
   }
 };
 // ... or the state that request i names (nothing where it names none)
@@ -74,9 +77,9 @@ void launch_nonfinite_check(const void* p, int64_t n, bool is_bf16, unsigned* fl
 }
 
 void launch_nonfinite_check_rows(const void* p, int64_t n, bool is_bf16, const int32_t* seq_offsets, int64_t nseq,
-                                 int64_t tokens, unsigned* flag, hipStream_t stream) {
+                                 int64_t tokens, bool rising, unsigned* flag, hipStream_t stream) {
   if (!p || n <= 0 || nseq <= 0) return;
-  const OwnedRows parts{{seq_offsets, nseq, tokens, 0}, n};
+  const OwnedRows parts{{seq_offsets, nseq, tokens, 0}, n, rising};
   if (is_bf16)
     hipLaunchKernelGGL((nonfinite_parts_kernel<bf16, OwnedRows>), parts_grid(nseq), dim3(256), 0, stream, (const bf16*)p,
                        parts, nseq, flag);

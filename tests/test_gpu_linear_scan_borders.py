@@ -76,3 +76,37 @@ def test_every_output_is_that_of_ascending_borders(form, dtype, D, state, border
             given = torch.zeros_like(got[k]) if given is None else given
             assert torch.equal(got[k][empty], given[empty]), (k, keep)
             assert torch.isfinite(got[k]).all(), (k, keep)
+
+
+@pytest.mark.parametrize("form", ["log", "gated"])
+@pytest.mark.parametrize("dtype", [F32, BF], ids=["f32", "bf16"])
+def test_finiteness_mode_scans_what_ascending_borders_own(monkeypatch, form, dtype):
+    """Rows that only the borders as they stand would give to a sequence say nothing; those that one owns do."""
+    announce(f"linear scan falling borders, finiteness mode {form} {dtype}")
+    monkeypatch.setenv("SSMVJP_CHECK_FINITE", "1")
+    borders = [5, 300, 0, 4, 800] + [k % 700 for k in range(90)] + [850]  # 0 .. 4 and 850 .. 899 are nobody's
+    t = scan(form, dtype, borders, 20, True, seed=3)
+    own = torch.zeros(900, dtype=torch.bool)
+    own[5:850] = True
+    for k in ("x", "gate", "dh", "input_gate"):
+        if t[k] is not None:
+            t[k][0, ~own] = math.nan
+    off = torch.tensor(borders, dtype=torch.int32, device=DEV)
+    kw = dict(input_gate=t["input_gate"], decay=t["decay"], c=C, seq_offsets=off)
+
+    def both(x, dh):
+        out = {"h": torch.full_like(x, math.nan), "h_final": torch.empty_like(t["h0"])}  # unowned rows are left as they are
+        bd.linear_scan_fwd(x, t["gate"], t["h0"], out=out, **kw)
+        g = {"dx": torch.full_like(x, math.nan), "dgate": torch.full_like(t["gate"], math.nan), "dh0": torch.empty_like(t["h0"])}
+        if form == "gated":
+            g.update(dinput_gate=torch.full_like(x, math.nan), ddecay=torch.empty_like(t["decay"]))
+        bd.linear_scan_bwd(t["x"], t["gate"], dh, t["h0"], t["dh_final"], out=g, **kw)
+
+    both(t["x"], t["dh"])
+    for at in (5, 299, 300, 799, 849):
+        for k in ("x", "dh"):
+            bad = t[k].clone()
+            bad[0, at, 19] = math.nan
+            with pytest.raises(bd.SsmVjpError) as e:
+                both(*((bad, t["dh"]) if k == "x" else (t["x"], bad)))
+            assert e.value.status == bd.ENONFINITE, (k, at)
