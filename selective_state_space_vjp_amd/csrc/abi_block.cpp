@@ -121,7 +121,8 @@ ssmvjp_status linear_scan_fwd(const ssmvjp_linear_scan_desc* desc, const void* x
   if (!aligned(h, big_elem(d.dtype)) || !all_aligned(p4, 4)) return SSMVJP_EINVAL;
   const size_t plan = linear_scan_fwd_workspace_bytes(d);
   s = workspace_check(with_flag(plan), workspace, workspace_bytes);
-  if (s != SSMVJP_OK || d.batch == 0) return s;
+  // without a sequence there may still be rows of ckpt, zeros then
+  if (s != SSMVJP_OK || (d.batch == 0 && !(ckpt && linear_scan_ckpt_rows(d) > 0))) return s;
   const LinearScanPointers ptr{x, gate, input_gate, decay, h0, seq_offsets, h, h_final, ckpt, workspace};
   s = hip_status(launch_linear_scan_fwd(d, ptr, (hipStream_t)stream));
   if (s != SSMVJP_OK || !check_finite_on()) return s;

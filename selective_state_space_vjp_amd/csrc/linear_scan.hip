@@ -826,7 +826,7 @@ void launch_step(StepArgs& a, i64 batch, hipStream_t s) {
 
 template <bool BWD>
 void launch_scan(const ssmvjp_linear_scan_desc& d, ScanArgs& a, hipStream_t s) {
-  if (a.ntiles == 0 || d.seqlen == 0) return;
+  if (a.ntiles == 0 || d.seqlen == 0 || d.batch == 0) return;
   const bool gated = d.form == SSMVJP_SCAN_GATED;
   if (d.dtype == SSMVJP_BF16) gated ? launch_wide<bf16, true, BWD>(a, s) : launch_wide<bf16, false, BWD>(a, s);
   else gated ? launch_wide<float, true, BWD>(a, s) : launch_wide<float, false, BWD>(a, s);

@@ -1,5 +1,5 @@
 """linear_scan_fwd and linear_scan_bwd on borders that are not ascending: a border below one before it counts as that
-one, so every output is that of the ascending borders, bit for bit."""
+one, so every output is that of the ascending borders, bit for bit; and on borders of no sequence at all."""
 import math
 
 import pytest
@@ -110,3 +110,23 @@ def test_finiteness_mode_scans_what_ascending_borders_own(monkeypatch, form, dty
             with pytest.raises(bd.SsmVjpError) as e:
                 both(*((bad, t["dh"]) if k == "x" else (t["x"], bad)))
             assert e.value.status == bd.ENONFINITE, (k, at)
+
+
+@pytest.mark.parametrize("form", ["log", "gated"])
+@pytest.mark.parametrize("T", [1, 64, 200, 5000])
+def test_kept_states_of_no_sequences(form, T):
+    """Packed tokens that no sequence owns, for there is none: rows of ckpt that no token has are zeros all the same."""
+    announce(f"linear scan no sequences {form} T={T}")
+    d = make_scan(form, 1, T, 70, BF, seed=T)
+    t = {k: (v.to(DEV) if isinstance(v, torch.Tensor) else v) for k, v in d.items()}
+    kw = dict(input_gate=t["input_gate"], decay=t["decay"], c=C, seq_offsets=torch.tensor([3], dtype=torch.int32, device=DEV))
+    none = torch.empty(0, 70, device=DEV)
+    out = {"h": torch.full_like(t["x"], 7.0), "h_final": none, "ckpt": torch.full((T // 64, 70), math.nan, device=DEV)}
+    bd.linear_scan_fwd(t["x"], t["gate"], none, out=out, **kw)
+    assert (out["h"] == 7.0).all() and (out["ckpt"] == 0).all()
+    for ckpt in (out["ckpt"], None):
+        g = {"dx": torch.full_like(t["x"], 7.0), "dgate": torch.full_like(t["gate"], 7.0), "dh0": none}
+        if form == "gated":
+            g.update(dinput_gate=torch.full_like(t["x"], 7.0), ddecay=torch.full((70,), math.nan, device=DEV))
+        bd.linear_scan_bwd(t["x"], t["gate"], t["dh"], none, none, ckpt=ckpt, out=g, **kw)
+        assert all((v == (0.0 if k == "ddecay" else 7.0)).all() for k, v in g.items())
