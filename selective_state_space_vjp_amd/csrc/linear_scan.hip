@@ -150,8 +150,13 @@ __device__ __forceinline__ bool find_tile(const ScanArgs& a, i64 o, int lane, Ti
 
 __device__ __forceinline__ float sigmoid_hw(float z) { return __builtin_amdgcn_rcpf(1.0f + exp_hw(-z)); }
 
-// per channel: c softplus(decay), and sigmoid(decay) / softplus(decay) (1 where both go to exp(decay))
-__device__ __forceinline__ float decay_rate(float c, float z) { return c * softplus_hw(z); }
+// per channel: c softplus(decay), and sigmoid(decay) / softplus(decay) (1 where both go to exp(decay)).  The rate stays
+// finite with its factor log2(e): it meets the 0 of a shut gate, and that of a = 0 in the gradients.
+constexpr float RATE_MAX = 2.3e38f;
+__device__ __forceinline__ float decay_rate(float c, float z) {
+  const float rate = c * softplus_hw(z);
+  return rate > RATE_MAX ? RATE_MAX : rate;
+}
 __device__ __forceinline__ float decay_slope(float z) { return z < -16.0f ? 1.0f : sigmoid_f(z) / softplus_f(z); }
 
 constexpr float LOG2E = 1.4426950408889634f, LN2 = 0.6931471805599453f;
