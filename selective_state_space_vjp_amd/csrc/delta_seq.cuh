@@ -29,17 +29,28 @@ struct DeltaSeqs {
     const i64 o = off[s];
     return o < 0 ? 0 : o > T ? T : o;
   }
-  // the largest of borders 0 .. s, where a border below one before it counts as that one; called by whole waves
+  // Where a border below one before it counts as that one (called by whole waves): where sequence s starts, the largest
+  // of borders 0 .. s ...
   __device__ __forceinline__ i64 risen(i64 s, int lane) const {
+    int most = most_of(s, lane);
+#pragma unroll
+    for (int d = 1; d < 64; d *= 2) {
+      const int o = __shfl_xor(most, d);
+      most = o > most ? o : most;
+    }
+    return most;
+  }
+  // ... and whether it has no tokens: its end is not above that
+  __device__ __forceinline__ bool risen_empty(i64 s, int lane) const {
+    const int end = (int)border(s + 1);
+    return __any(most_of(s, lane) >= end);
+  }
+  // a lane's share of that maximum
+  __device__ __forceinline__ int most_of(i64 s, int lane) const {
     int most = 0;
 #pragma unroll 4
     for (i64 i = lane; i <= s; i += 64) {
       const int o = (int)border(i);
-      most = o > most ? o : most;
-    }
-#pragma unroll
-    for (int d = 1; d < 64; d *= 2) {
-      const int o = __shfl_xor(most, d);
       most = o > most ? o : most;
     }
     return most;
