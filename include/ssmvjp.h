@@ -474,8 +474,9 @@ ssmvjp_status layer_norm_bwd(const ssmvjp_norm_desc* desc,
  * with h_{-1} = h0.  Sequences as for delta_chunk_fwd: packed = 0, `batch` sequences of
  * `seqlen` tokens (token tensors [batch, seqlen, dim]); packed = 1, `batch` sequences
  * behind one another in `seqlen` tokens ([seqlen, dim]) with their borders in seq_offsets,
- * clamped to [0, seqlen] (a border below one before it counts as that one); tokens that
- * no sequence owns are neither read nor written. */
+ * clamped to [0, seqlen] (a border below one before it counts as that one, and a sequence that
+ * ends where it then starts is an empty one); tokens that no sequence owns are neither read nor
+ * written. */
 enum { SSMVJP_SCAN_LOG = 0, SSMVJP_SCAN_GATED = 1 };
 typedef struct {
   int64_t batch, seqlen, dim;
@@ -515,7 +516,7 @@ ssmvjp_status linear_scan_fwd(const ssmvjp_linear_scan_desc* desc,
  *   (NULL = zeros)
  * Outputs: dx like x, dgate like gate, dinput_gate like input_gate (gated form),
  *   ddecay [dim] f32 (gated form; summed over all tokens in a fixed order; zeros where there
- *   are none), dh0 [batch, dim] f32 (NULL = not written).
+ *   are none), dh0 [batch, dim] f32 (NULL = not written; an empty sequence's is its dh_final).
  * Constraints as for linear_scan_fwd.  dh0 must not be dh_final (SSMVJP_EINVAL). */
 ssmvjp_status linear_scan_bwd_workspace(const ssmvjp_linear_scan_desc* desc, size_t* bytes);
 ssmvjp_status linear_scan_bwd(const ssmvjp_linear_scan_desc* desc,
@@ -577,7 +578,8 @@ ssmvjp_status gated_ffn_fwd(const ssmvjp_ffn_desc* desc, const void* x, const vo
  *   dx = dgate w_gate + dup w_up;  dw_gate = dgate^T x;  dw_up = dup^T x
  * Outputs like their inputs, each NULL = not computed; zeros when rows = 0.  dgate and dup
  * are kept in `dtype` between the products, in bf16 as the sum of two values where rows
- * hidden or hidden dim is below 8192 or rows dim below 2048.  Constraints as for gated_ffn_fwd. */
+ * hidden or hidden dim is below 8192 or rows dim below 2048: bf16 gradients are off by 2.4e-3 of
+ * their norm (their own rounding leaves 1.7e-3 of it), by 1.7e-3 there.  Constraints as for gated_ffn_fwd. */
 ssmvjp_status gated_ffn_bwd_workspace(const ssmvjp_ffn_desc* desc, size_t* bytes);
 ssmvjp_status gated_ffn_bwd(const ssmvjp_ffn_desc* desc, const void* dh, const void* x, const void* w_gate,
                             const void* w_up, const void* gate, const void* up, void* dx, void* dw_gate, void* dw_up,

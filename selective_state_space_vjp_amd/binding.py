@@ -1091,7 +1091,9 @@ def gated_ffn_bwd(dh, x, w_gate, w_up, *, act="silu", saved=None, want_dx=True, 
     for what want_dx=False or want_dw=False leaves out.
 
     dh [..., F]; saved=(gate, up) from a forward with want_saved=True, or None: they are then formed
-    again, in float32.
+    again, in float32.  The gradients of gate and up are bfloat16 between the products where the
+    tensors are (in two parts where a gradient has few values): what that leaves adds to the rounding
+    of the results, 2.4e-3 of their norm together.
     """
     desc, shape = _ffn_inputs(x, w_gate, w_up, act)
     _required(dh=dh)
